@@ -51,6 +51,12 @@ _SIGNATURES = {
                             _i, _vp]),
     "fa_get_device_error": (_i, [_vp]),
     "fa_status_string": (ctypes.c_char_p, [_i]),
+    "fa_rope": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _i, ctypes.POINTER(ctypes.c_int), ctypes.c_double, _i,
+                     _i, _i, _vp]),
+    "fa_cache_write": (_i, [_vp] * 6 + [_i] * 7 + [_vp] * 4),
+    "fa_cache_read": (_i, [_vp] * 6 + [_i] * 7 + [_vp] * 3),
+    "fa_fwd_paged_workspace_size": (_sz, [_i] * 7),
+    "fa_fwd_paged": (_i, [_vp] * 7 + [_i] * 9 + [_f] + [_vp] * 3 + [_i, _vp, _sz, _vp]),
     "fa_diag_exp2": (_i, [_vp, _vp, _vp, ctypes.c_longlong, _vp]),
     "fa_diag_wait_timeout": (_i, [ctypes.c_ulonglong, _vp]),
 }
@@ -234,6 +240,232 @@ def bwd(q, k, v, o, lse, do, causal=False, scale=None, deterministic=False, work
             st = lib.fa_bwd_ex(*args, ctypes.byref(t), _stream(stream))
     _check(st, "fa_bwd")
     return dq, dk, dv
+
+
+class _OnStream:
+    """The current stream and device for a call's launches and for what it
+    allocates: with `stream` given, outputs and workspace come from that
+    stream's pool, so the allocator reuses them in its order."""
+
+    def __init__(self, device, stream):
+        self.device, self.stream = device, stream
+
+    def __enter__(self):
+        if self.stream is not None and self.stream.device != self.device:
+            raise ValueError("stream is on %s, the tensors on %s" % (self.stream.device, self.device))
+        self.ctx = torch.cuda.stream(self.stream) if self.stream is not None else torch.cuda.device(self.device)
+        self.ctx.__enter__()
+        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+    def __exit__(self, *exc):
+        return self.ctx.__exit__(*exc)
+
+
+def _check_int32(name, t, device, dims):
+    if t.device != device or t.dtype != torch.int32 or not t.is_contiguous() or t.dim() != dims:
+        raise ValueError("%s must be a contiguous CUDA int32 tensor with %d dimension(s) on %s" % (name, dims, device))
+
+
+def _cache_args(x_heads, D, device, k_pages, v_pages, k_scale, v_scale, block_table):
+    """Checks the tensors of a cache; (num_pages, Hkv, page_size, max_pages)."""
+    fp8 = k_scale is not None or v_scale is not None
+    dtype = torch.float8_e4m3fn if fp8 else torch.bfloat16
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        if not t.is_cuda or t.device != device or t.dtype != dtype or not t.is_contiguous() or t.dim() != 4:
+            raise ValueError("%s must be a contiguous CUDA %s tensor [num_pages, Hkv, page_size, D] on %s"
+                             % (name, dtype, device))
+    if k_pages.shape != v_pages.shape:
+        raise ValueError("v_pages must have k_pages' shape %s" % (tuple(k_pages.shape),))
+    num_pages, Hkv, page_size, Dp = k_pages.shape
+    if Dp != D:
+        raise ValueError("the pages' head dimension is %d, not %d" % (Dp, D))
+    if x_heads is not None and x_heads != Hkv:
+        raise ValueError("the pages have %d heads, k and v %d" % (Hkv, x_heads))
+    if fp8:
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if (t is None or t.device != device or t.dtype != torch.uint8 or not t.is_contiguous()
+                    or tuple(t.shape) != (num_pages, Hkv, page_size)):
+                raise ValueError("%s must be a contiguous CUDA uint8 tensor of shape %s on %s"
+                                 % (name, (num_pages, Hkv, page_size), device))
+    _check_int32("block_table", block_table, device, 2)
+    return num_pages, Hkv, page_size, block_table.shape[1]
+
+
+def _new_tokens(name, x, B, cu_seqlens):
+    """Sn of the C ABI for new tokens x, dense [B, Sn, H, D] or packed [Sn, H, D]."""
+    _check_bf16(name, x)
+    if x.dim() != (4 if cu_seqlens is None else 3):
+        raise ValueError("%s is [B, Sn, H, D], or [total, H, D] with cu_seqlens" % name)
+    if cu_seqlens is None:
+        if x.shape[0] != B:
+            raise ValueError("%s has %d sequences, the block table %d" % (name, x.shape[0], B))
+        return x.shape[1]
+    _check_int32("cu_seqlens", cu_seqlens, x.device, 1)
+    if cu_seqlens.numel() != B + 1:
+        raise ValueError("cu_seqlens has %d offsets for %d sequences" % (cu_seqlens.numel(), B))
+    return x.shape[0]
+
+
+def _check_seq_lens(seq_lens, device, B):
+    _check_int32("seq_lens", seq_lens, device, 1)
+    if seq_lens.numel() != B:
+        raise ValueError("seq_lens has %d lengths for %d sequences" % (seq_lens.numel(), B))
+
+
+def rope(q, k, positions, sections=None, base=10000.0, restart=False, interleaved=False, inverse=False, q_out=None,
+         k_out=None, stream=None):
+    """q and k ([..., H, D], the same leading shape; k may be None) turned by
+    rotary positions.  positions: int32 [axes, ...] with that leading shape
+    (or without the first dimension for one axis).  sections: rotary pairs of
+    each axis (one axis: all D / 2 by default).  Frequencies base^(-i / pairs),
+    starting anew on each axis with restart=True.  Pairs are elements i and
+    i + pairs, or neighbours with interleaved=True.  inverse=True turns
+    backwards: the gradients of a call without it.  q_out and k_out may be q
+    and k.  Returns (q_out, k_out)."""
+    lib = load_library()
+    _check_bf16("q", q)
+    if q.dim() < 2:
+        raise ValueError("q is [..., H, D]")
+    lead, Hq, D = tuple(q.shape[:-2]), q.shape[-2], q.shape[-1]
+    Hkv = 0
+    if k is not None:
+        _check_bf16("k", k)
+        _check_same_device(q.device, k=k)
+        if tuple(k.shape[:-2]) != lead or k.shape[-1] != D:
+            raise ValueError("k is [..., H, D] with q's leading shape and D")
+        Hkv = k.shape[-2]
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    if positions.device != q.device or positions.dtype != torch.int32 or not positions.is_contiguous():
+        raise ValueError("positions must be a contiguous CUDA int32 tensor on %s" % q.device)
+    axes = 1 if tuple(positions.shape) == lead else positions.shape[0] if positions.dim() else 0
+    if tuple(positions.shape) not in (lead, (axes,) + lead):
+        raise ValueError("positions are %s, with a first dimension for the axes" % (lead,))
+    if sections is None:
+        if axes != 1:
+            raise ValueError("%d axes need sections" % axes)
+        sections = [D // 2]
+    sections = [int(x) for x in sections]
+    if len(sections) != axes:
+        raise ValueError("%d sections for %d axes" % (len(sections), axes))
+    for name, t, like in (("q_out", q_out, q), ("k_out", k_out, k)):
+        if t is not None:
+            _check_out(name, t, like.shape, torch.bfloat16, q.device)
+    tokens = 1
+    for n in lead:
+        tokens *= n
+    with _OnStream(q.device, stream) as s:
+        if q_out is None:
+            q_out = torch.empty_like(q)
+        if k is not None and k_out is None:
+            k_out = torch.empty_like(k)
+        st = lib.fa_rope(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), tokens, Hq, Hkv, D, _ptr(positions), axes,
+                         (ctypes.c_int * len(sections))(*sections), float(base), int(bool(restart)),
+                         int(bool(interleaved)), int(bool(inverse)), s)
+    _check(st, "fa_rope")
+    return q_out, k_out
+
+
+def cache_write(k, v, k_pages, v_pages, block_table, seq_lens, cu_seqlens=None, k_scale=None, v_scale=None,
+                stream=None):
+    """Writes new keys and values, dense [B, n, Hkv, D] or packed
+    [total, Hkv, D] with cu_seqlens, into the pages [num_pages, Hkv, page_size,
+    D]: the last tokens of sequences that are seq_lens long with them.  BF16
+    pages; or float8_e4m3fn pages with uint8 scales [num_pages, Hkv,
+    page_size], quantised on the way."""
+    lib = load_library()
+    B = block_table.shape[0]
+    Sn = _new_tokens("k", k, B, cu_seqlens)
+    _check_bf16("v", v)
+    _check_same_device(k.device, v=v)
+    if v.shape != k.shape:
+        raise ValueError("v must have k's shape %s" % (tuple(k.shape),))
+    D = k.shape[-1]
+    num_pages, Hkv, page_size, max_pages = _cache_args(k.shape[-2], D, k.device, k_pages, v_pages, k_scale, v_scale,
+                                                       block_table)
+    _check_seq_lens(seq_lens, k.device, B)
+    with _OnStream(k.device, stream) as s:
+        st = lib.fa_cache_write(_ptr(k), _ptr(v), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), B, Hkv,
+                                Sn, D, num_pages, page_size, max_pages, _ptr(block_table), _ptr(seq_lens),
+                                _ptr(cu_seqlens), s)
+    _check(st, "fa_cache_write")
+
+
+def cache_read(k_pages, v_pages, block_table, cu_seqlens, total, k_scale=None, v_scale=None, k_out=None, v_out=None,
+               stream=None):
+    """The first cu_seqlens[b + 1] - cu_seqlens[b] tokens of every sequence as
+    packed BF16 (k, v), each [total, Hkv, D]; rows from cu_seqlens[B] on are
+    left as they were."""
+    lib = load_library()
+    if k_pages.dim() != 4:
+        raise ValueError("k_pages is [num_pages, Hkv, page_size, D]")
+    device, D, B = k_pages.device, k_pages.shape[3], block_table.shape[0]
+    num_pages, Hkv, page_size, max_pages = _cache_args(None, D, device, k_pages, v_pages, k_scale, v_scale,
+                                                       block_table)
+    _check_int32("cu_seqlens", cu_seqlens, device, 1)
+    if cu_seqlens.numel() != B + 1:
+        raise ValueError("cu_seqlens has %d offsets for %d sequences" % (cu_seqlens.numel(), B))
+    shape = (int(total), Hkv, D)
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        if t is not None:
+            _check_out(name, t, shape, torch.bfloat16, device)
+    with _OnStream(device, stream) as s:
+        if k_out is None:
+            k_out = torch.empty(shape, dtype=torch.bfloat16, device=device)
+        if v_out is None:
+            v_out = torch.empty(shape, dtype=torch.bfloat16, device=device)
+        st = lib.fa_cache_read(_ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), _ptr(k_out), _ptr(v_out),
+                               B, Hkv, int(total), D, num_pages, page_size, max_pages, _ptr(block_table),
+                               _ptr(cu_seqlens), s)
+    _check(st, "fa_cache_read")
+    return k_out, v_out
+
+
+def fwd_paged_workspace_size(B, Hq, Hkv, Sn, D, packed=False, max_q=None):
+    """Workspace bytes of fa_fwd_paged; max_q (packed) as in fwd_paged."""
+    return int(load_library().fa_fwd_paged_workspace_size(B, Hq, Hkv, Sn, D, int(bool(packed)),
+                                                          int(Sn if max_q is None else max_q)))
+
+
+def fwd_paged(q, k_pages, v_pages, block_table, seq_lens, causal=True, scale=None, cu_seqlens=None, max_q=None,
+              k_scale=None, v_scale=None, out=None, lse=None, workspace=None, stream=None):
+    """O, LSE = attention of new tokens q, dense [B, n, Hq, D] or packed
+    [total, Hq, D] with cu_seqlens, over the seq_lens[b] keys that each
+    sequence has in the cache, the new tokens' own (written before by
+    cache_write) as the last.  max_q: an upper bound of the new tokens of any
+    one sequence (packed; `total` by default, which is right but may choose a
+    slower kernel)."""
+    lib = load_library()
+    B = block_table.shape[0]
+    Sn = _new_tokens("q", q, B, cu_seqlens)
+    Hq, D = q.shape[-2], q.shape[-1]
+    num_pages, Hkv, page_size, max_pages = _cache_args(None, D, q.device, k_pages, v_pages, k_scale, v_scale,
+                                                       block_table)
+    _check_seq_lens(seq_lens, q.device, B)
+    max_q = Sn if cu_seqlens is None or max_q is None else int(max_q)
+    if scale is None:
+        scale = D ** -0.5
+    lse_shape = (Hq, Sn) if cu_seqlens is not None else (B, Hq, Sn)
+    if out is not None:
+        _check_out("out", out, q.shape, torch.bfloat16, q.device)
+    if lse is not None:
+        _check_out("lse", lse, lse_shape, torch.float32, q.device)
+    if workspace is not None and (workspace.device != q.device or not workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous tensor on %s" % q.device)
+    with _OnStream(q.device, stream) as s:
+        if out is None:
+            out = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty(lse_shape, dtype=torch.float32, device=q.device)
+        if workspace is None:
+            need = fwd_paged_workspace_size(B, Hq, Hkv, Sn, D, cu_seqlens is not None, max_q)
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        st = lib.fa_fwd_paged(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), _ptr(out),
+                              _ptr(lse), B, Hq, Hkv, Sn, D, num_pages, page_size, max_pages, int(bool(causal)),
+                              float(scale), _ptr(block_table), _ptr(seq_lens), _ptr(cu_seqlens), max_q,
+                              _ptr(workspace), workspace.numel() * workspace.element_size(), s)
+    _check(st, "fa_fwd_paged")
+    return out, lse
 
 
 def get_device_error(stream=None):

@@ -14,6 +14,7 @@
 #include "fa.h"
 #include "fa_diag.h"
 #include "fa_internal.h"
+#include "paged_internal.h"
 
 namespace fa {
 namespace {
@@ -68,6 +69,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
+}  // namespace
+
 // Current device's SM count; FA_ERR_UNSUPPORTED unless it is compute 10.3.
 fa_status device_info(int* num_sms) {
   int dev = 0;
@@ -80,6 +83,8 @@ fa_status device_info(int* num_sms) {
   if (major != 10 || minor != 3) return FA_ERR_UNSUPPORTED;
   return FA_OK;
 }
+
+namespace {
 
 // Shape checks common to both passes.  Packed inputs: Sq == Sk == total.
 fa_status check_shapes(int B, int Hq, int Hkv, int Sq, int Sk, int D, float scale, const int* cu_seqlens) {
@@ -140,6 +145,23 @@ fa_status make_tmap_f32_rows_heads_d(CUtensorMap* map, const void* base, int row
   const cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void*>(base), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status make_tmap_pages(CUtensorMap* map, const void* base, long long page_heads, int page_size, int D, bool fp8,
+                          int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return FA_ERR_CUDA;
+  const cuuint64_t row = (cuuint64_t)D * (fp8 ? 1 : 2);   // bytes
+  const bool narrow = row < 128;                           // E4M3 at D = 64
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)page_size, (cuuint64_t)page_heads};
+  const cuuint64_t strides[2] = {row, row * (cuuint64_t)page_size};
+  const cuuint32_t box[3] = {(cuuint32_t)(fp8 ? D : 64), (cuuint32_t)box_rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                  const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  narrow ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
 }
@@ -433,8 +455,9 @@ fa_status fa_bwd(const void* q, const void* k, const void* v, const void* o, con
 fa_status fa_get_device_error(fa_stream_t stream) {
   if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return FA_ERR_CUDA;
   fa_status first = FA_OK;
-  const fa_status all[5] = {fwd_take_device_error(), bwd_take_device_error(), bwd_pair_take_device_error(),
-                            bwd_dq_take_device_error(), diag_take_device_error()};
+  const fa_status all[] = {fwd_take_device_error(),          bwd_take_device_error(), bwd_pair_take_device_error(),
+                           bwd_dq_take_device_error(),       diag_take_device_error(), cache_take_device_error(),
+                           paged_decode_take_device_error()};
   for (fa_status s : all)
     if (first == FA_OK && s != FA_OK) first = s;
   return first;

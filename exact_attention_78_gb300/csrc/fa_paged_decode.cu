@@ -1,0 +1,730 @@
+// Attention of a few new tokens over a paged cache (a decoding step).
+//
+//   O = softmax(scale q K^T [+ causal mask]) V, LSE, per row of q.
+//
+// A step reads every sequence's keys and values once and computes little with
+// them, so HBM bounds it: the design keeps loads in flight and splits the keys
+// evenly over the SMs.
+//
+//   * Rows.  The query heads of one key/value head, for up to 16 rows of
+//     (new token, head of the group), share the keys that a warp loads: they
+//     are the 16 rows of an mma.sync tile.  (tcgen05 tiles have at least 64
+//     rows; with 16 or fewer to fill, the warp-level instruction leaves the
+//     tensor cores no busier and needs no trip through tensor memory.)
+//   * Work.  The blocks of 16 keys of all (sequence, key/value head, row tile)
+//     units form one line, and thread block c takes the c-th of `grid` equal
+//     stretches of it.  A unit cut by a border leaves partial results in the
+//     workspace, at most two per thread block, and the combine kernel joins
+//     them.  Sequences of any mixture of lengths load all SMs alike.
+//   * Pipeline.  Each of the 8 warps walks every eighth key block of the
+//     stretch with a ring of its own in shared memory, which its lane 0 fills
+//     by TMA (the pages' rows, swizzled for ldmatrix); no warp waits for
+//     another until the unit's end, where the 8 softmax states are merged.
+//   * E4M3 pages are widened in registers on the way to the tensor cores; the
+//     rows' power-of-two scales go to the scores (keys) and to the weights
+//     (values), both exactly.
+#include <cuda_runtime.h>
+
+#include "paged.cuh"
+#include "softmax_math.cuh"
+
+namespace fa {
+namespace pdec {
+
+__device__ DeviceError g_err;
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kRows = 16;     // rows of a tile
+constexpr int kKeys = 16;     // keys of a block: one page or a part of one
+
+enum Site { kSiteSeqs = 1, kSitePage, kSiteRing };
+
+// Layout of the workspace: per slot the rows' unnormalised outputs, then per
+// slot and row the maximum (log2 units) and the two sums.
+template <int D>
+struct Part {
+  static constexpr int kSlotFloats = kRows * D;
+  static constexpr int kStat = 4;
+  FA_DEV static float* out(float* ws, int slot) { return ws + (size_t)slot * kSlotFloats; }
+  FA_DEV static float* stat(float* ws, int slot) {
+    return ws + (size_t)2 * kMaxCtas * kSlotFloats + (size_t)slot * kRows * kStat;
+  }
+  static constexpr size_t bytes() { return (size_t)2 * kMaxCtas * (kSlotFloats + kRows * kStat) * sizeof(float); }
+};
+
+template <int D, bool kFp8>
+struct Layout {
+  static constexpr int kTile = kKeys * D * (kFp8 ? 1 : 2);        // keys or values of a block
+  static constexpr int kStage = 2 * kTile;
+  static constexpr int kStages = kStage >= 8192 ? 3 : kStage >= 4096 ? 5 : 8;
+  static constexpr int kPitch = D + 8;                            // floats of a merge row
+  static constexpr int kMergeRows = 32;                           // rows of all merge slots
+  static constexpr int kRing = 0;
+  static constexpr int kScales = kRing + kWarps * kStages * kStage;   // E4M3: 16 + 16 scale bytes a stage
+  static constexpr int kMerge = kScales + (kFp8 ? kWarps * kStages * 2 * kKeys : 0);
+  static constexpr int kStats = kMerge + kMergeRows * kPitch * 4;     // m, l, lr of [warp][row]
+  static constexpr int kPre = kStats + 3 * kWarps * kRows * 4;        // prefix of blocks, [B + 1]
+  static constexpr int kBars = kPre + (kMaxPackedSeqs + 1) * 8 + 8;
+  static constexpr int kMisc = kBars + kWarps * kStages * 8;
+  static constexpr int kBytes = kMisc + 64 + kSmemAlignSlack;
+  static_assert(kBytes <= 232448, "dynamic shared memory above the 227 KB per-CTA limit");
+};
+
+// ------------------------------------------------------------ the work line --
+
+struct Seq {
+  int n, L, q0;     // new tokens, keys, first row of q
+};
+FA_DEV Seq seq_of(const PagedSeqs& s, int b) {
+  Seq r;
+  r.L = s.seq_lens[b];
+  if (s.cu) {
+    r.q0 = s.cu[b];
+    r.n = s.cu[b + 1] - r.q0;
+  } else {
+    r.q0 = b * s.Sn;
+    r.n = s.Sn;
+  }
+  return r;
+}
+FA_DEV int tiles_of(int n, int group) { return (n * group + kRows - 1) / kRows; }
+// Blocks of a unit: at least one, so that rows without a key are written too.
+FA_DEV int blocks_of(int L) { return max(1, (L + kKeys - 1) / kKeys); }
+
+// Prefix sums of the sequences' blocks into pre[0 .. B]; returns their total,
+// 0 when the sequences break the rules.  All threads of the block.
+template <int kN>
+FA_DEV long long build_line(const PagedAttnParams& p, long long* pre, long long* warp_sums) {
+  const bool ok = paged::sequences_ok(p.s, p.max_q);
+  if (!ok) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) paged::record_bad_input(&g_err, kSiteSeqs);
+    return 0;
+  }
+  constexpr int kEach = kMaxPackedSeqs / kN;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  long long v[kEach], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int b = threadIdx.x * kEach + i;
+    v[i] = 0;
+    if (b < p.s.B) {
+      const Seq q = seq_of(p.s, b);
+      if (q.n > 0) v[i] = (long long)p.s.Hkv * tiles_of(q.n, p.group) * blocks_of(q.L);
+    }
+    sum += v[i];
+  }
+  long long incl = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += o;
+  }
+  if (lane == 31) warp_sums[warp] = incl;
+  __syncthreads();
+  long long before = incl - sum;
+  for (int w = 0; w < warp; ++w) before += warp_sums[w];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int b = threadIdx.x * kEach + i;
+    before += v[i];
+    if (b < p.s.B) pre[b + 1] = before;
+  }
+  if (threadIdx.x == 0) pre[0] = 0;
+  __syncthreads();
+  return pre[p.s.B];
+}
+
+// Thread blocks that share the line: no more than leave each a block per warp.
+FA_DEV int active_ctas(long long total, int ctas) {
+  const long long most = (total + kWarps - 1) / kWarps;
+  return most < ctas ? (int)most : ctas;
+}
+// First block of stretch c of G.
+FA_DEV long long stretch(long long total, int c, int G) { return total * c / G; }
+
+// A walk over the segments (the stretch's share of one unit) of [t0, t1).
+struct Walk {
+  int b, head, tile, tiles;
+  Seq s;
+  int nblk;          // blocks of the unit
+  int kb, count;     // the segment: blocks [kb, kb + count)
+  long long left;    // blocks of the stretch from this segment on
+
+  FA_DEV void load(const PagedAttnParams& p) {
+    s = seq_of(p.s, b);
+    tiles = tiles_of(s.n, p.group);
+    nblk = blocks_of(s.L);
+  }
+  FA_DEV void begin(const PagedAttnParams& p, const long long* pre, long long t0, long long t1) {
+    int lo = 0, hi = p.s.B - 1;      // last b with pre[b] <= t0
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (pre[mid] <= t0) lo = mid; else hi = mid - 1;
+    }
+    b = lo;
+    load(p);
+    const long long r = t0 - pre[b];
+    const long long unit = r / nblk;
+    kb = (int)(r - unit * nblk);
+    head = (int)(unit / tiles);
+    tile = (int)(unit - (long long)head * tiles);
+    left = t1 - t0;
+    count = (int)(left < nblk - kb ? left : nblk - kb);
+  }
+  FA_DEV bool more() const { return left > 0; }
+  FA_DEV void next(const PagedAttnParams& p) {
+    left -= count;
+    if (left <= 0) return;
+    kb = 0;
+    if (++tile == tiles) {
+      tile = 0;
+      if (++head == p.s.Hkv) {
+        head = 0;
+        do ++b; while (b < p.s.B - 1 && seq_of(p.s, b).n == 0);
+        load(p);
+      }
+    }
+    count = (int)(left < nblk ? left : nblk);
+  }
+  FA_DEV int rows(const PagedAttnParams& p) const { return min(kRows, s.n * p.group - tile * kRows); }
+  // Keys that the tile's last row sees.
+  FA_DEV int seen(const PagedAttnParams& p) const {
+    if (!p.causal) return s.L;
+    const int t = min(s.n * p.group, (tile + 1) * kRows) - 1;
+    return min(s.L, max(0, s.L - s.n + t / p.group + 1));
+  }
+  // Blocks of the segment that any row sees: the leading ones.
+  FA_DEV int visible(const PagedAttnParams& p) const {
+    return min(count, max(0, (seen(p) + kKeys - 1) / kKeys - kb));
+  }
+};
+
+// ----------------------------------------------------------- instructions --
+
+FA_DEV void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+FA_DEV void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+FA_DEV void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Shared-memory address of 16-byte piece `c` of row `r` of a tile at `base`.
+// BF16: 64-column chunks of 128-byte rows, 128-byte swizzle.  E4M3: rows of D
+// bytes, swizzled by their width.
+template <int D, bool kFp8>
+FA_DEV uint32_t piece(uint32_t base, int r, int c) {
+  if (!kFp8) return base + (c >> 3) * (kKeys * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+  if (D == 128) return base + r * 128 + ((c ^ (r & 7)) << 4);
+  return base + r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
+// ---------------------------------------------------------------- kernel --
+
+template <int D, bool kFp8>
+__global__ void __launch_bounds__(kThreads, 1)
+    decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                  const PagedAttnParams p) {
+  using L = Layout<D, kFp8>;
+  constexpr int kSteps = D / 16;      // 16-wide steps along D
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int c = lane % 4, g = lane / 4;       // column pair and row of the fragments
+  long long* pre = reinterpret_cast<long long*>(smem + L::kPre);
+  float* merge = reinterpret_cast<float*>(smem + L::kMerge);
+  float* st_m = reinterpret_cast<float*>(smem + L::kStats);
+  float* st_l = st_m + kWarps * kRows;
+  float* st_lr = st_l + kWarps * kRows;
+  const uint32_t abort = sbase + L::kMisc;
+  const uint32_t ring = sbase + L::kRing + warp * L::kStages * L::kStage;
+  const uint32_t scales = sbase + L::kScales + warp * L::kStages * 2 * kKeys;
+  const uint32_t bars = sbase + L::kBars + warp * L::kStages * 8;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kWarps * L::kStages; ++i) mbar_init(sbase + L::kBars + 8 * i, 1);
+    st_shared(abort, 0);
+    fence_barrier_init();
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  const long long total = build_line<kThreads>(p, pre, reinterpret_cast<long long*>(merge));
+  __syncthreads();
+  const int G = active_ctas(total, gridDim.x);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if ((int)blockIdx.x >= G) return;
+  const long long t0 = stretch(total, blockIdx.x, G), t1 = stretch(total, blockIdx.x + 1, G);
+
+  // The walk that issues loads runs ahead of the one that consumes them.
+  Walk in, at;
+  in.begin(p, pre, t0, t1);
+  at = in;
+  int in_i = warp, in_vis = in.visible(p);       // next block of this warp in the segment
+  int in_page = 0, in_page_i = -1;               // page numbers, one per lane, of the warp's next 32 blocks
+  int in_stage = 0;
+  // Issues the warp's next block, if there is one.  The whole warp calls it.
+  auto issue = [&]() {
+    while (in_i >= in_vis) {
+      in.next(p);
+      if (!in.more()) {
+        in_vis = 0x7fffffff;                     // never again
+        in_i = in_vis;
+        break;
+      }
+      in_i = warp;
+      in_vis = in.visible(p);
+      in_page_i = -1;
+    }
+    if (in_vis == 0x7fffffff) return;
+    const int k = in_i / kWarps;                 // the warp's k-th block of the segment
+    if (in_page_i < 0 || k - in_page_i >= 32) {
+      in_page_i = k;
+      const int i = in_i + lane * kWarps;
+      in_page = -1;
+      if (i < in_vis) {
+        in_page = p.s.block_table[(size_t)in.b * p.s.max_pages + (((in.kb + i) * kKeys) >> p.s.page_shift)];
+        if (in_page < 0 || in_page >= p.s.num_pages) {
+          paged::record_bad_input(&g_err, kSitePage);
+          in_page = -1;                          // outside the tensor maps: reads as zeros
+        }
+      }
+    }
+    const int page = __shfl_sync(0xffffffffu, in_page, k - in_page_i);
+    if (lane == 0) {
+      const int off = ((in.kb + in_i) * kKeys) & ((1 << p.s.page_shift) - 1);
+      const int ph = page < 0 ? -1 : page * p.s.Hkv + in.head;
+      const uint32_t dst = ring + in_stage * L::kStage, bar = bars + 8 * in_stage;
+      mbar_arrive_expect_tx(bar, 2 * L::kTile + (kFp8 ? 2 * kKeys : 0));
+#pragma unroll
+      for (int h = 0; h < (kFp8 ? 1 : D / 64); ++h) {
+        tma_load_3d(dst + h * kKeys * 128, &tm_k, bar, h * 64, off, ph);
+        tma_load_3d(dst + L::kTile + h * kKeys * 128, &tm_v, bar, h * 64, off, ph);
+      }
+      if (kFp8) {
+        const size_t row = ((size_t)max(ph, 0) << p.s.page_shift) + off;
+        bulk_load(scales + in_stage * 2 * kKeys, p.k_scale + row, kKeys, bar);
+        bulk_load(scales + in_stage * 2 * kKeys + kKeys, p.v_scale + row, kKeys, bar);
+      }
+    }
+    in_i += kWarps;
+    in_stage = in_stage + 1 == L::kStages ? 0 : in_stage + 1;
+  };
+#pragma unroll 1
+  for (int i = 0; i < L::kStages; ++i) issue();
+
+  int stage = 0;
+  uint32_t phase = 0;
+  bool lost = false;      // a wait ran out: no more loads, no more results
+  while (at.more()) {
+    const int rows = at.rows(p), row0 = at.tile * kRows;
+    const int vis = at.visible(p);
+    // Q of the tile as A fragments, rows g and g + 8
+    uint32_t qf[kSteps][4];
+    int row_lim[2];       // keys that the two rows see
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = row0 + g + 8 * h;
+      const bool valid = g + 8 * h < rows;
+      const int t = r / p.group, j = r - t * p.group;
+      row_lim[h] = !valid ? 0 : p.causal ? at.s.L - at.s.n + t + 1 : at.s.L;
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) +
+                                 ((size_t)(at.s.q0 + t) * p.Hq + at.head * p.group + j) * D;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        uint2 w = make_uint2(0u, 0u);
+        if (kFp8) {
+          // four consecutive values of the row; an E4M3 word gives the pairs
+          // (0, 2) and (1, 3), so Q's pairs are taken likewise
+          if (valid) w = *reinterpret_cast<const uint2*>(src + 16 * s + 4 * c);
+          qf[s][h] = __byte_perm(w.x, w.y, 0x5410);
+          qf[s][2 + h] = __byte_perm(w.x, w.y, 0x7632);
+        } else {
+          if (valid) {
+            w.x = *reinterpret_cast<const uint32_t*>(src + 16 * s + 2 * c);
+            w.y = *reinterpret_cast<const uint32_t*>(src + 16 * s + 8 + 2 * c);
+          }
+          qf[s][h] = w.x;
+          qf[s][2 + h] = w.y;
+        }
+      }
+    }
+    float acc[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, lr[2] = {0.0f, 0.0f};
+
+#pragma unroll 1
+    for (int i = warp; i < vis && !lost; i += kWarps) {
+      if (!mbar_wait_bounded(bars + 8 * stage, phase, abort, &g_err, kSiteRing, p.wait_limit_ns)) {
+        lost = true;
+        break;
+      }
+      const uint32_t kt = ring + stage * L::kStage, vt = kt + L::kTile;
+      const int key0 = (at.kb + i) * kKeys;
+      // scores of 16 rows and 2 x 8 keys
+      float s0[4] = {0.0f, 0.0f, 0.0f, 0.0f}, s1[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (!kFp8) {
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+          uint32_t b[4];
+          ldsm4(piece<D, kFp8>(kt, (lane >> 4) * 8 + (lane & 7), 2 * s + ((lane >> 3) & 1)), b);
+          mma16816(s0, qf[s], b[0], b[1]);
+          mma16816(s1, qf[s], b[2], b[3]);
+        }
+      } else {
+#pragma unroll
+        for (int s = 0; s < kSteps; s += 2) {
+          // keys 0-7 and 8-15 of 16-byte pieces s and s + 1
+          uint32_t b[4];
+          ldsm4(piece<D, kFp8>(kt, (lane >> 4) * 8 + (lane & 7), s + ((lane >> 3) & 1)), b);
+          mma16816(s0, qf[s], paged::e4m3_even(b[0]), paged::e4m3_odd(b[0]));
+          mma16816(s0, qf[s + 1], paged::e4m3_even(b[1]), paged::e4m3_odd(b[1]));
+          mma16816(s1, qf[s], paged::e4m3_even(b[2]), paged::e4m3_odd(b[2]));
+          mma16816(s1, qf[s + 1], paged::e4m3_even(b[3]), paged::e4m3_odd(b[3]));
+        }
+      }
+      // x[h][e]: row g + 8 h, keys 2 c, 2 c + 1, 2 c + 8, 2 c + 9, in log2 units
+      float x[2][4] = {{s0[0], s0[1], s1[0], s1[1]}, {s0[2], s0[3], s1[2], s1[3]}};
+      float vs[4];
+      if (kFp8) {
+        const uint8_t* ks = smem + (scales - sbase) + stage * 2 * kKeys;
+        const uint32_t k0 = *reinterpret_cast<const uint16_t*>(ks + 2 * c);
+        const uint32_t k1 = *reinterpret_cast<const uint16_t*>(ks + 8 + 2 * c);
+        const uint32_t v0 = *reinterpret_cast<const uint16_t*>(ks + kKeys + 2 * c);
+        const uint32_t v1 = *reinterpret_cast<const uint16_t*>(ks + kKeys + 8 + 2 * c);
+        const float ksc[4] = {paged::scale_value(k0 & 255u), paged::scale_value(k0 >> 8),
+                              paged::scale_value(k1 & 255u), paged::scale_value(k1 >> 8)};
+        vs[0] = paged::scale_value(v0 & 255u);
+        vs[1] = paged::scale_value(v0 >> 8);
+        vs[2] = paged::scale_value(v1 & 255u);
+        vs[3] = paged::scale_value(v1 >> 8);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[0][e] *= ksc[e];
+          x[1][e] *= ksc[e];
+        }
+      }
+      // a block that every row sees whole needs no mask (rows of the tile see
+      // at least the first row's keys)
+      const bool tail = key0 + kKeys > (p.causal ? at.s.L - at.s.n + row0 / p.group + 1 : at.s.L);
+      uint32_t pk[2][2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[h][e] *= p.scale_log2;
+          if (tail && key0 + 2 * c + (e & 1) + 8 * (e >> 1) >= row_lim[h]) x[h][e] = -INFINITY;
+        }
+        float mx = fmaxf(fmaxf(x[h][0], x[h][1]), fmaxf(x[h][2], x[h][3]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float m_new = fmaxf(m[h], mx);
+        const float m_use = m_new == -INFINITY ? 0.0f : m_new;
+        if (__any_sync(0xffffffffu, m_new > m[h])) {
+          const float f = ex2_mufu(m[h] - m_use);      // 0 from a maximum of -inf
+          l[h] *= f;
+          lr[h] *= f;
+#pragma unroll
+          for (int j = 0; j < D / 8; ++j) {
+            acc[j][2 * h] *= f;
+            acc[j][2 * h + 1] *= f;
+          }
+          m[h] = m_new;
+        }
+        float e[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) e[k] = ex2_mufu(x[h][k] - m_use);
+        // Two sums: of the FP32 weights for LSE, and of the weights as the
+        // product with V takes them, rounded to BF16, for the division, so
+        // that the weights used add up to one.
+        l[h] += (e[0] + e[1]) + (e[2] + e[3]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint32_t w = pack_bf16x2(e[2 * k], e[2 * k + 1]);
+          const float w0 = __uint_as_float(w << 16), w1 = __uint_as_float(w & 0xFFFF0000u);
+          lr[h] += w0 + w1;
+          if (kFp8) {
+            // the value's scale goes with its weight (a power of two: exact);
+            // a masked key's scale may be anything
+            float y0 = w0 * vs[2 * k], y1 = w1 * vs[2 * k + 1];
+            if (tail) {
+              const int key = key0 + 2 * c + 8 * k;
+              if (key >= row_lim[h]) y0 = 0.0f;
+              if (key + 1 >= row_lim[h]) y1 = 0.0f;
+            }
+            w = pack_bf16x2(y0, y1);
+          }
+          pk[h][k] = w;
+        }
+      }
+      // O += P V.  Values behind the sequence's end may be NaN or infinite,
+      // which a weight of zero would not cancel: they are cleared.
+      const uint32_t pa[4] = {pk[0][0], pk[1][0], pk[0][1], pk[1][1]};
+      const bool ragged = key0 + kKeys > at.s.L;
+      uint32_t keep[2];
+      if (ragged) {
+        const int n = at.s.L - key0;
+        keep[0] = (2 * c < n ? 0x0000FFFFu : 0u) | (2 * c + 1 < n ? 0xFFFF0000u : 0u);
+        keep[1] = (2 * c + 8 < n ? 0x0000FFFFu : 0u) | (2 * c + 9 < n ? 0xFFFF0000u : 0u);
+      }
+      if (!kFp8) {
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+          uint32_t b[4];
+          ldsm4_t(piece<D, kFp8>(vt, lane & 15, 2 * j + (lane >> 4)), b);
+          if (ragged) {
+            b[0] &= keep[0];
+            b[1] &= keep[1];
+            b[2] &= keep[0];
+            b[3] &= keep[1];
+          }
+          mma16816(acc[2 * j], pa, b[0], b[1]);
+          mma16816(acc[2 * j + 1], pa, b[2], b[3]);
+        }
+      } else {
+        // a word holds D columns 2 n and 2 n + 1 of two keys: the even bytes
+        // are one column tile's operand, the odd bytes another's
+#pragma unroll
+        for (int j = 0; j < D / 16; j += 2) {
+          uint32_t b[4];
+          ldsm4_t(piece<D, kFp8>(vt, lane & 15, j + (lane >> 4)), b);
+          if (ragged) {
+            b[0] &= keep[0];
+            b[1] &= keep[1];
+            b[2] &= keep[0];
+            b[3] &= keep[1];
+          }
+          mma16816(acc[2 * j], pa, paged::e4m3_even(b[0]), paged::e4m3_even(b[1]));
+          mma16816(acc[2 * j + 1], pa, paged::e4m3_odd(b[0]), paged::e4m3_odd(b[1]));
+          mma16816(acc[2 * j + 2], pa, paged::e4m3_even(b[2]), paged::e4m3_even(b[3]));
+          mma16816(acc[2 * j + 3], pa, paged::e4m3_odd(b[2]), paged::e4m3_odd(b[3]));
+        }
+      }
+      __syncwarp();       // every lane is done with the stage
+      issue();
+      if (++stage == L::kStages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+
+    // Merge of the warps' states: row maxima and sums first, then the outputs,
+    // as many warps at a time as the merge rows hold.
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int d = 1; d < 4; d *= 2) {
+        l[h] += __shfl_xor_sync(0xffffffffu, l[h], d);
+        lr[h] += __shfl_xor_sync(0xffffffffu, lr[h], d);
+      }
+      if (c == 0) {
+        const int i = warp * kRows + g + 8 * h;
+        st_m[i] = m[h];
+        st_l[i] = l[h];
+        st_lr[i] = lr[h];
+      }
+    }
+    __syncthreads();
+    float top[2], f[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      top[h] = -INFINITY;
+      for (int w = 0; w < kWarps; ++w) top[h] = fmaxf(top[h], st_m[w * kRows + g + 8 * h]);
+      f[h] = top[h] == -INFINITY ? 1.0f : ex2_mufu(m[h] - top[h]);
+    }
+    const int pad = rows <= 4 ? 4 : rows <= 8 ? 8 : 16;
+    const int slots = L::kMergeRows / pad;       // warps that write at a time
+    for (int w0 = 0; w0 < kWarps; w0 += slots) {
+      if (warp >= w0 && warp < w0 + slots) {
+        float* to = merge + (warp - w0) * pad * L::kPitch;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (g + 8 * h >= rows) continue;
+          float* r = to + (g + 8 * h) * L::kPitch;
+#pragma unroll
+          for (int j = 0; j < D / 8; ++j) {
+            // BF16: columns 8 j + 2 c, + 1; E4M3: of tiles 2 i, 2 i + 1, columns 16 i + 4 c + {0, 2}, {1, 3}
+            const int d0 = kFp8 ? 16 * (j / 2) + 4 * c + (j & 1) : 8 * j + 2 * c;
+            const int d1 = kFp8 ? d0 + 2 : d0 + 1;
+            const float y0 = acc[j][2 * h] * f[h], y1 = acc[j][2 * h + 1] * f[h];
+            r[d0] = w0 ? r[d0] + y0 : y0;
+            r[d1] = w0 ? r[d1] + y1 : y1;
+          }
+        }
+      }
+      __syncthreads();
+    }
+    // The rows' results: final when the segment is the whole unit, else partial.
+    const bool whole = at.kb == 0 && at.count == at.nblk;
+    const bool first = at.left == t1 - t0;
+    const int slot = 2 * blockIdx.x + (first ? 0 : 1);
+    if (!lost && !ld_shared_volatile(abort)) {
+      for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
+        const int r = i / (D / 4), d = i % (D / 4) * 4;
+        float mt = -INFINITY;
+        for (int w = 0; w < kWarps; ++w) mt = fmaxf(mt, st_m[w * kRows + r]);
+        float lt = 0.0f, lrt = 0.0f;
+        for (int w = 0; w < kWarps; ++w) {
+          const float fw = mt == -INFINITY ? 1.0f : ex2_mufu(st_m[w * kRows + r] - mt);
+          lt += st_l[w * kRows + r] * fw;
+          lrt += st_lr[w * kRows + r] * fw;
+        }
+        float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int s = 0; s < min(slots, kWarps); ++s) {
+          const float* from = merge + (s * pad + r) * L::kPitch + d;
+          y.x += from[0];
+          y.y += from[1];
+          y.z += from[2];
+          y.w += from[3];
+        }
+        if (whole) {
+          const float inv = lrt == 0.0f ? 0.0f : 1.0f / lrt;
+          const int row = row0 + r, t = row / p.group, head = at.head * p.group + row - t * p.group;
+          const int tok = at.s.q0 + t;
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + ((size_t)tok * p.Hq + head) * D + d) =
+              make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
+          if (d == 0) {
+            const size_t li = p.s.cu ? (size_t)head * p.s.Sn + tok
+                                     : ((size_t)at.b * p.Hq + head) * p.s.Sn + t;
+            p.lse[li] = lt == 0.0f ? -INFINITY : (mt + log2f(lt)) * 0.693147180559945309f;
+          }
+        } else {
+          *reinterpret_cast<float4*>(Part<D>::out(p.part, slot) + r * D + d) = y;
+          if (d == 0) {
+            float* stat = Part<D>::stat(p.part, slot) + r * Part<D>::kStat;
+            stat[0] = mt;
+            stat[1] = lt;
+            stat[2] = lrt;
+          }
+        }
+      }
+    }
+    __syncthreads();       // the merge rows and the statistics are free again
+    at.next(p);
+  }
+
+  // After a give-up, loads already in flight land before the shared memory
+  // they target is released.
+  if (ld_shared_volatile(abort)) {
+    const uint64_t w0 = globaltimer_ns();
+    while (globaltimer_ns() - w0 < 2000000ull) __nanosleep(1000);
+  }
+}
+
+// Joins the partial results of the units that borders between thread blocks
+// cut: block x + 1 looks at border x + 1 and does the unit whose first cut that
+// border is.
+template <int D>
+__global__ void __launch_bounds__(kThreads) combine_kernel(const PagedAttnParams p, int ctas) {
+  __shared__ long long pre[kMaxPackedSeqs + 1];
+  __shared__ long long sums[kThreads / 32];
+  const long long total = build_line<kThreads>(p, pre, sums);
+  const int G = active_ctas(total, ctas);
+  const int c = blockIdx.x + 1;
+  // before any exit, so that this grid ends after the main one
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (c >= G) return;
+  const long long t = stretch(total, c, G);
+  Walk w;
+  w.begin(p, pre, t, total);
+  const long long start = t - w.kb, end = start + w.nblk;
+  const long long t_prev = stretch(total, c - 1, G);
+  if (w.kb == 0 || t_prev > start) return;      // no cut here, or not the unit's first
+  const int first = 2 * (c - 1) + (t_prev == start ? 0 : 1);
+  int last = c;                                  // parts: slot `first`, then slots 2 c .. 2 last
+  while (last + 1 < G && stretch(total, last + 1, G) < end) ++last;
+  const int rows = w.rows(p);
+  for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
+    const int r = i / (D / 4), d = i % (D / 4) * 4;
+    float mt = Part<D>::stat(p.part, first)[r * Part<D>::kStat];
+    for (int k = c; k <= last; ++k) mt = fmaxf(mt, Part<D>::stat(p.part, 2 * k)[r * Part<D>::kStat]);
+    float lt = 0.0f, lrt = 0.0f;
+    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int k = c - 1; k <= last; ++k) {
+      const int slot = k < c ? first : 2 * k;
+      const float* stat = Part<D>::stat(p.part, slot) + r * Part<D>::kStat;
+      const float f = mt == -INFINITY ? 1.0f : ex2_mufu(stat[0] - mt);
+      lt += stat[1] * f;
+      lrt += stat[2] * f;
+      const float4 x = *reinterpret_cast<const float4*>(Part<D>::out(p.part, slot) + r * D + d);
+      y.x += x.x * f;
+      y.y += x.y * f;
+      y.z += x.z * f;
+      y.w += x.w * f;
+    }
+    const float inv = lrt == 0.0f ? 0.0f : 1.0f / lrt;
+    const int row = w.tile * kRows + r, tk = row / p.group, head = w.head * p.group + row - tk * p.group;
+    const int tok = w.s.q0 + tk;
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + ((size_t)tok * p.Hq + head) * D + d) =
+        make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
+    if (d == 0) {
+      const size_t li = p.s.cu ? (size_t)head * p.s.Sn + tok : ((size_t)w.b * p.Hq + head) * p.s.Sn + tk;
+      p.lse[li] = lt == 0.0f ? -INFINITY : (mt + log2f(lt)) * 0.693147180559945309f;
+    }
+  }
+}
+
+template <int D, bool kFp8>
+fa_status launch_inst(const PagedAttnLaunch& L, cudaStream_t stream) {
+  using Lay = Layout<D, kFp8>;
+  const int page_size = 1 << L.p.s.page_shift;
+  const long long page_heads = (long long)L.p.s.num_pages * L.p.s.Hkv;
+  CUtensorMap tk, tv;
+  fa_status st;
+  if ((st = make_tmap_pages(&tk, L.k_pages, page_heads, page_size, D, kFp8, kKeys)) != FA_OK) return st;
+  if ((st = make_tmap_pages(&tv, L.v_pages, page_heads, page_size, D, kFp8, kKeys)) != FA_OK) return st;
+  auto kern = decode_kernel<D, kFp8>;
+  if ((st = prepare_kernel(reinterpret_cast<const void*>(kern), Lay::kBytes)) != FA_OK) return st;
+  const int ctas = L.p.num_ctas;
+  kern<<<ctas, kThreads, Lay::kBytes, stream>>>(tk, tv, L.p);
+  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  if (ctas > 1) {
+    // the joining kernel works out its borders while the main one still runs
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(ctas - 1);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, combine_kernel<D>, L.p, ctas) != cudaSuccess) return FA_ERR_CUDA;
+  }
+  return FA_OK;
+}
+
+}  // namespace pdec
+
+size_t paged_decode_workspace(int D) { return D == 128 ? pdec::Part<128>::bytes() : pdec::Part<64>::bytes(); }
+
+fa_status launch_paged_decode(const PagedAttnLaunch& L, cudaStream_t stream) {
+  if (L.D == 128) return L.fp8 ? pdec::launch_inst<128, true>(L, stream) : pdec::launch_inst<128, false>(L, stream);
+  return L.fp8 ? pdec::launch_inst<64, true>(L, stream) : pdec::launch_inst<64, false>(L, stream);
+}
+
+fa_status paged_decode_take_device_error() {
+  DeviceError e{0, 0};
+  if (cudaMemcpyFromSymbol(&e, pdec::g_err, sizeof(e)) != cudaSuccess) return FA_ERR_CUDA;
+  if (e.status != 0) {
+    const DeviceError z{0, 0};
+    if (cudaMemcpyToSymbol(pdec::g_err, &z, sizeof(z)) != cudaSuccess) return FA_ERR_CUDA;
+  }
+  return static_cast<fa_status>(e.status);
+}
+
+}  // namespace fa

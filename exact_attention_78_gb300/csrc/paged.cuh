@@ -1,0 +1,70 @@
+// Device code shared by the paged-cache kernels: which sequence and position a
+// new token has, E4M3 rows and their scales.
+#pragma once
+
+#include "paged_internal.h"
+#include "ptx.cuh"
+
+namespace fa {
+namespace paged {
+
+FA_DEV void record_bad_input(DeviceError* err, int site) {
+  if (atomicCAS(&err->status, 0, FA_ERR_INVALID_ARG) == 0) atomicExch(&err->site, site);
+}
+
+// The sequence that packed row i belongs to: the number of b in [1, B] with
+// cu[b] <= i (B where i lies behind the last sequence).  One warp searches for
+// one row, 32 offsets a step: two steps of independent loads for up to 1024
+// sequences, where a binary search takes ten dependent ones.
+FA_DEV int find_sequence(const int* __restrict__ cu, int B, int i, int lane) {
+  const int step = (B + 31) / 32;
+  // shares of `step` offsets whose last one is still <= i, then the rest one by one
+  const int last = (lane + 1) * step;
+  const int full = __popc(__ballot_sync(0xffffffffu, last <= B && cu[min(last, B)] <= i));
+  if (step == 1) return full;
+  const int b = full * step + 1 + lane;                     // step <= 32
+  return full * step + __popc(__ballot_sync(0xffffffffu, lane < step && b <= B && cu[min(b, B)] <= i));
+}
+
+// Whether the offsets and lengths of all sequences keep to the rules.  Every
+// thread of the block calls it; the answer is the same in all of them.
+// max_new: the most new tokens that a sequence may have (packed).
+FA_DEV bool sequences_ok(const PagedSeqs& s, int max_new) {
+  bool ok = true;
+  const int capacity = s.max_pages << s.page_shift;
+  for (int b = threadIdx.x; b < s.B; b += blockDim.x) {
+    if (s.seq_lens) ok = ok && s.seq_lens[b] >= 0 && s.seq_lens[b] <= capacity;
+    if (s.cu) {
+      const int a = s.cu[b], e = s.cu[b + 1];
+      ok = ok && a >= 0 && e >= a && e <= s.Sn && e - a <= max_new && (b > 0 || a == 0);
+      if (!s.seq_lens) ok = ok && e - a <= capacity;
+    }
+  }
+  return __syncthreads_and(ok);
+}
+
+// 2^e of a scale byte; NaN for the byte of a row without a finite scale.
+FA_DEV float scale_value(uint32_t byte) {
+  return byte == 255u ? __int_as_float(0x7FC00000) : __uint_as_float(byte << 23);
+}
+
+// E4M3 codes to BF16, exactly but for a factor of 2^-120: sign, exponent and
+// mantissa move to their places in a BF16, whose exponent then reads 120 too
+// low (subnormal codes become subnormal BF16, in the same proportion).  One
+// word of four codes gives two pairs, of codes 0 and 2 and of codes 1 and 3.
+// Three logic instructions a pair; there is no direct conversion, and the one
+// through FP16 and FP32 takes five.
+FA_DEV uint32_t e4m3_even_raw(uint32_t w) { return ((w << 4) & 0x07F007F0u) | ((w << 8) & 0x80008000u); }
+FA_DEV uint32_t e4m3_odd_raw(uint32_t w) { return ((w >> 4) & 0x07F007F0u) | (w & 0x80008000u); }
+// Product of BF16 pairs (subnormals kept).
+FA_DEV uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+constexpr uint32_t kTwo120 = 0x7B807B80u;   // 2^120 twice
+FA_DEV uint32_t e4m3_even(uint32_t w) { return mul_bf16x2(e4m3_even_raw(w), kTwo120); }
+FA_DEV uint32_t e4m3_odd(uint32_t w) { return mul_bf16x2(e4m3_odd_raw(w), kTwo120); }
+
+}  // namespace paged
+}  // namespace fa
