@@ -6,6 +6,7 @@ There is no fallback: if the shared library is missing, every call raises.
 """
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -242,23 +243,47 @@ def bwd(q, k, v, o, lse, do, causal=False, scale=None, deterministic=False, work
     return dq, dk, dv
 
 
+class _Here:
+    """The current stream of the current device, as a context like _OnStream."""
+
+    def __init__(self, raw):
+        self.raw = raw
+
+    def __enter__(self):
+        return self.raw
+
+    def __exit__(self, *exc):
+        return False
+
+
 class _OnStream:
-    """The current stream and device for a call's launches and for what it
-    allocates: with `stream` given, outputs and workspace come from that
+    """`stream` (or `device`'s current one) as the current stream for a call's
+    launches and for what it allocates: outputs and workspace come from that
     stream's pool, so the allocator reuses them in its order."""
 
     def __init__(self, device, stream):
-        self.device, self.stream = device, stream
+        if stream is not None and stream.device != device:
+            raise ValueError("stream is on %s, the tensors on %s" % (stream.device, device))
+        self.ctx = torch.cuda.stream(stream) if stream is not None else torch.cuda.device(device)
 
     def __enter__(self):
-        if self.stream is not None and self.stream.device != self.device:
-            raise ValueError("stream is on %s, the tensors on %s" % (self.stream.device, self.device))
-        self.ctx = torch.cuda.stream(self.stream) if self.stream is not None else torch.cuda.device(self.device)
         self.ctx.__enter__()
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        return torch.cuda.current_stream().cuda_stream
 
     def __exit__(self, *exc):
         return self.ctx.__exit__(*exc)
+
+
+def _on(device, stream):
+    # a small call takes a few microseconds on the GPU; entering a context
+    # costs as much again on the host, and mostly changes nothing
+    if stream is None and device.index == torch.cuda.current_device():
+        return _Here(torch._C._cuda_getCurrentRawStream(device.index))
+    return _OnStream(device, stream)
+
+
+def _adr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _check_int32(name, t, device, dims):
@@ -271,7 +296,7 @@ def _cache_args(x_heads, D, device, k_pages, v_pages, k_scale, v_scale, block_ta
     fp8 = k_scale is not None or v_scale is not None
     dtype = torch.float8_e4m3fn if fp8 else torch.bfloat16
     for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        if not t.is_cuda or t.device != device or t.dtype != dtype or not t.is_contiguous() or t.dim() != 4:
+        if not t.is_cuda or t.device != device or t.dtype is not dtype or not t.is_contiguous() or t.dim() != 4:
             raise ValueError("%s must be a contiguous CUDA %s tensor [num_pages, Hkv, page_size, D] on %s"
                              % (name, dtype, device))
     if k_pages.shape != v_pages.shape:
@@ -354,12 +379,12 @@ def rope(q, k, positions, sections=None, base=10000.0, restart=False, interleave
     tokens = 1
     for n in lead:
         tokens *= n
-    with _OnStream(q.device, stream) as s:
+    with _on(q.device, stream) as s:
         if q_out is None:
             q_out = torch.empty_like(q)
         if k is not None and k_out is None:
             k_out = torch.empty_like(k)
-        st = lib.fa_rope(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), tokens, Hq, Hkv, D, _ptr(positions), axes,
+        st = lib.fa_rope(_adr(q), _adr(k), _adr(q_out), _adr(k_out), tokens, Hq, Hkv, D, _adr(positions), axes,
                          (ctypes.c_int * len(sections))(*sections), float(base), int(bool(restart)),
                          int(bool(interleaved)), int(bool(inverse)), s)
     _check(st, "fa_rope")
@@ -384,10 +409,10 @@ def cache_write(k, v, k_pages, v_pages, block_table, seq_lens, cu_seqlens=None, 
     num_pages, Hkv, page_size, max_pages = _cache_args(k.shape[-2], D, k.device, k_pages, v_pages, k_scale, v_scale,
                                                        block_table)
     _check_seq_lens(seq_lens, k.device, B)
-    with _OnStream(k.device, stream) as s:
-        st = lib.fa_cache_write(_ptr(k), _ptr(v), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), B, Hkv,
-                                Sn, D, num_pages, page_size, max_pages, _ptr(block_table), _ptr(seq_lens),
-                                _ptr(cu_seqlens), s)
+    with _on(k.device, stream) as s:
+        st = lib.fa_cache_write(_adr(k), _adr(v), _adr(k_pages), _adr(v_pages), _adr(k_scale), _adr(v_scale), B, Hkv,
+                                Sn, D, num_pages, page_size, max_pages, _adr(block_table), _adr(seq_lens),
+                                _adr(cu_seqlens), s)
     _check(st, "fa_cache_write")
 
 
@@ -409,18 +434,19 @@ def cache_read(k_pages, v_pages, block_table, cu_seqlens, total, k_scale=None, v
     for name, t in (("k_out", k_out), ("v_out", v_out)):
         if t is not None:
             _check_out(name, t, shape, torch.bfloat16, device)
-    with _OnStream(device, stream) as s:
+    with _on(device, stream) as s:
         if k_out is None:
             k_out = torch.empty(shape, dtype=torch.bfloat16, device=device)
         if v_out is None:
             v_out = torch.empty(shape, dtype=torch.bfloat16, device=device)
-        st = lib.fa_cache_read(_ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), _ptr(k_out), _ptr(v_out),
-                               B, Hkv, int(total), D, num_pages, page_size, max_pages, _ptr(block_table),
-                               _ptr(cu_seqlens), s)
+        st = lib.fa_cache_read(_adr(k_pages), _adr(v_pages), _adr(k_scale), _adr(v_scale), _adr(k_out), _adr(v_out),
+                               B, Hkv, int(total), D, num_pages, page_size, max_pages, _adr(block_table),
+                               _adr(cu_seqlens), s)
     _check(st, "fa_cache_read")
     return k_out, v_out
 
 
+@functools.lru_cache(maxsize=1024)
 def fwd_paged_workspace_size(B, Hq, Hkv, Sn, D, packed=False, max_q=None):
     """Workspace bytes of fa_fwd_paged; max_q (packed) as in fwd_paged."""
     return int(load_library().fa_fwd_paged_workspace_size(B, Hq, Hkv, Sn, D, int(bool(packed)),
@@ -452,7 +478,7 @@ def fwd_paged(q, k_pages, v_pages, block_table, seq_lens, causal=True, scale=Non
         _check_out("lse", lse, lse_shape, torch.float32, q.device)
     if workspace is not None and (workspace.device != q.device or not workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous tensor on %s" % q.device)
-    with _OnStream(q.device, stream) as s:
+    with _on(q.device, stream) as s:
         if out is None:
             out = torch.empty_like(q)
         if lse is None:
@@ -460,10 +486,10 @@ def fwd_paged(q, k_pages, v_pages, block_table, seq_lens, causal=True, scale=Non
         if workspace is None:
             need = fwd_paged_workspace_size(B, Hq, Hkv, Sn, D, cu_seqlens is not None, max_q)
             workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
-        st = lib.fa_fwd_paged(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), _ptr(out),
-                              _ptr(lse), B, Hq, Hkv, Sn, D, num_pages, page_size, max_pages, int(bool(causal)),
-                              float(scale), _ptr(block_table), _ptr(seq_lens), _ptr(cu_seqlens), max_q,
-                              _ptr(workspace), workspace.numel() * workspace.element_size(), s)
+        st = lib.fa_fwd_paged(_adr(q), _adr(k_pages), _adr(v_pages), _adr(k_scale), _adr(v_scale), _adr(out),
+                              _adr(lse), B, Hq, Hkv, Sn, D, num_pages, page_size, max_pages, int(bool(causal)),
+                              float(scale), _adr(block_table), _adr(seq_lens), _adr(cu_seqlens), max_q,
+                              _adr(workspace), workspace.numel() * workspace.element_size(), s)
     _check(st, "fa_fwd_paged")
     return out, lse
 

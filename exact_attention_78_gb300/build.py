@@ -19,7 +19,8 @@ OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libfa_gb300.so")
 
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_bwd_dq.cu", "fa_bwd_pair.cu", "fa_diag.cu",
-           "fa_paged_api.cu", "fa_cache.cu", "fa_rope.cu", "fa_paged_decode.cu"]
+           "fa_paged_api.cu", "fa_cache.cu", "fa_rope.cu", "fa_paged_decode.cu",
+           "fa_paged_chunk.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "-I" + INCLUDE, "-I" + CSRC]

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -72,15 +73,25 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }  // namespace
 
 // Current device's SM count; FA_ERR_UNSUPPORTED unless it is compute 10.3.
+// Looked up once per device: three attribute queries are a good part of a
+// small call's time on the host.
 fa_status device_info(int* num_sms) {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices];   // 0: not asked yet; else the SM count, or -status
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return FA_ERR_CUDA;
-  int major = 0, minor = 0;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return FA_ERR_CUDA;
-  if (major != 10 || minor != 3) return FA_ERR_UNSUPPORTED;
+  int v = dev < kDevices ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (v == 0) {
+    int major = 0, minor = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return FA_ERR_CUDA;
+    if (major != 10 || minor != 3) v = -FA_ERR_UNSUPPORTED;
+    if (dev < kDevices) known[dev].store(v, std::memory_order_relaxed);
+  }
+  if (v < 0) return static_cast<fa_status>(-v);
+  *num_sms = v;
   return FA_OK;
 }
 
@@ -145,6 +156,20 @@ fa_status make_tmap_f32_rows_heads_d(CUtensorMap* map, const void* base, int row
   const cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void*>(base), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status make_tmap_rows_group(CUtensorMap* map, const void* base, int rows, int heads, int D, int group,
+                               int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return FA_ERR_CUDA;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)heads * D * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)box_rows};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
 }
@@ -457,7 +482,7 @@ fa_status fa_get_device_error(fa_stream_t stream) {
   fa_status first = FA_OK;
   const fa_status all[] = {fwd_take_device_error(),          bwd_take_device_error(), bwd_pair_take_device_error(),
                            bwd_dq_take_device_error(),       diag_take_device_error(), cache_take_device_error(),
-                           paged_decode_take_device_error()};
+                           paged_decode_take_device_error(), paged_chunk_take_device_error()};
   for (fa_status s : all)
     if (first == FA_OK && s != FA_OK) first = s;
   return first;

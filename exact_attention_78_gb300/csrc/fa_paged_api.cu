@@ -48,6 +48,13 @@ fa_status check_cache(const void* k_pages, const void* v_pages, const void* k_sc
   return FA_OK;
 }
 
+// Rows of one sequence and key/value head up to which a call takes the decode
+// kernel; above it the chunk kernel.
+constexpr int kDecodeRows = 16;
+bool takes_decode(int Hq, int Hkv, int Sn, bool packed, int max_q) {
+  return (long long)(packed ? max_q : Sn) * (Hq / Hkv) <= kDecodeRows;
+}
+
 bool attn_shape_ok(int B, int Hq, int Hkv, int Sn, int D, bool packed, int max_q, fa_status* why) {
   *why = FA_ERR_INVALID_ARG;
   if (B <= 0 || Hq <= 0 || Hkv <= 0 || Sn <= 0 || Hq % Hkv != 0) return false;
@@ -174,7 +181,7 @@ fa_status fa_cache_read(const void* k_pages, const void* v_pages, const void* k_
 size_t fa_fwd_paged_workspace_size(int B, int Hq, int Hkv, int Sn, int D, int packed, int max_q) {
   fa_status why;
   if ((packed != 0 && packed != 1) || !attn_shape_ok(B, Hq, Hkv, Sn, D, packed != 0, max_q, &why)) return 0;
-  return paged_decode_workspace(D);
+  return takes_decode(Hq, Hkv, Sn, packed != 0, max_q) ? paged_decode_workspace(D) : paged_chunk_workspace(D);
 }
 
 fa_status fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages, const void* k_scale,
@@ -213,7 +220,8 @@ fa_status fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages, 
     L.v_pages = v_pages;
     L.D = D;
     L.fp8 = k_scale != nullptr;
-    return launch_paged_decode(L, reinterpret_cast<cudaStream_t>(stream));
+    const bool decode = takes_decode(Hq, Hkv, Sn, cu_seqlens != nullptr, max_q);
+    return (decode ? launch_paged_decode : launch_paged_chunk)(L, reinterpret_cast<cudaStream_t>(stream));
   } catch (...) {
     return FA_ERR_CUDA;
   }

@@ -1,0 +1,1208 @@
+// Attention of chunks of new tokens over a paged cache, on tcgen05.
+//
+//   O = softmax(scale q K^T [+ causal mask]) V, LSE, per row of q.
+//
+// A tile is up to 128 rows of (new token, query head of one key/value head's
+// group), so grouped heads share the key and value tiles they read; a unit is
+// a pair of tiles of one (sequence, key/value head), worked on in turn: while
+// one tile's softmax runs, the tensor cores compute the other's products.
+//
+//   * Keys and values come in blocks of 128 from pages of 16 to 1024 tokens,
+//     one TMA box per page (or per 128 rows of it), into a ring of shared
+//     memory tiles.  Rows behind the sequence's end hold anything: as keys
+//     they are masked, as values they are cleared before the product, since a
+//     weight of zero would not cancel a NaN.
+//   * E4M3 pages go through a second ring: four warps widen each tile to BF16
+//     once per unit, with the rows' power-of-two scales, exactly, so the
+//     products are those of BF16 pages.
+//   * Work.  Whole rounds of units, one per thread block, run in lockstep
+//     from the first key on, so that the pairs of a head share its keys in L2.
+//     The units left over are a line of key blocks that is cut into equal
+//     stretches, one per thread block; parts of a cut unit are joined by the
+//     combine kernel.  A few long chunks thus load all SMs.  A scheduler warp
+//     works out each thread block's segments and hands them to the other
+//     warps through a small ring.
+//
+// Warps: 0-3 and 4-7 softmax of tile 0 and 1 (a thread per row), 8-11
+// correction and epilogue, 12 loads, 13 MMA issue, 14 clearing of values
+// behind the end (BF16 pages), 15 scheduler, 16-19 widening (E4M3 pages).
+// Registers: BF16 256 x 192 + 128 x 80 + 128 x 48 = 65,536 = 512 x 128;
+// E4M3 256 x 160 + 128 x 72 + 128 x 40 + 128 x 48 = 61,440 = 640 x 96.
+//
+// Tensor memory (512 columns): [0, 128) S of tile 0, its P as BF16 pairs in
+// the first 64; [128, 256) tile 1; [256, 256 + D) O of tile 0; the next D
+// columns O of tile 1.
+#include <cuda_runtime.h>
+
+#include "paged.cuh"
+#include "softmax_math.cuh"
+
+namespace fa {
+namespace pchunk {
+
+__device__ DeviceError g_err;
+
+constexpr int kBM = 128;      // rows of a tile
+constexpr int kBN = 128;      // keys of a block
+constexpr int kEmu = 2;       // exponentials of every 16 on the FMA pipe
+constexpr float kThreshold = 8.0f;   // lazy rescaling, log2 units
+constexpr int kMinStretch = 4;       // blocks
+
+enum Site {
+  kSiteSeqs = 1, kSitePage, kSiteSegFull, kSiteSegEmpty, kSiteQEmpty, kSiteKvEmpty, kSiteKvFull, kSiteQFull, kSiteS,
+  kSiteP, kSiteO, kSiteLanded, kSiteRaw
+};
+
+// Workspace: per slot (two per thread block) both tiles' unnormalised rows,
+// then per slot and row maximum and sums.
+template <int D>
+struct Part {
+  static constexpr int kRows = 2 * kBM;
+  static constexpr int kStat = 4;
+  FA_DEV static float* out(float* ws, int slot) { return ws + (size_t)slot * kRows * D; }
+  FA_DEV static float* stat(float* ws, int slot) {
+    return ws + (size_t)2 * kMaxCtas * kRows * D + (size_t)slot * kRows * kStat;
+  }
+  static constexpr size_t bytes() { return (size_t)2 * kMaxCtas * kRows * (D + kStat) * sizeof(float); }
+};
+
+// A segment: blocks [kb, kb + count) of a unit, as the roles get it.
+struct Seg {
+  int b, head, tok0;     // tok0: the pair's first new token; b < 0: no more work
+  int kb, count;
+  int n, L, q0;
+  int slot;              // partial results go here; -1: the unit is whole
+  int pad[3];
+};
+constexpr int kSegs = 4;
+
+template <int D, bool kFp8>
+struct Layout {
+  static constexpr int kThreads = kFp8 ? 640 : 512;
+  static constexpr int kChunks = D / 64;
+  static constexpr int kTileBytes = kBM * D * 2;
+  static constexpr int kChunkBytes = kBM * 128;
+  static constexpr int kStages = D == 128 ? (kFp8 ? 3 : 4) : 6;
+  static constexpr int kRawBytes = kBN * D;                  // an E4M3 tile
+  static constexpr int kRaws = kFp8 ? 3 : 0;
+  static constexpr int kReaders = kFp8 ? 18 : 15;            // warps that take segments
+  static constexpr int kQ = 0;
+  static constexpr int kKV = kQ + 2 * kTileBytes;
+  static constexpr int kRaw = kKV + kStages * kTileBytes;
+  static constexpr int kRawScale = kRaw + kRaws * kRawBytes;
+  static constexpr int kStats = kRawScale + kRaws * kBN;     // scale, l, lr, m of [2][128]
+  static constexpr int kBPre = kStats + 4 * 2 * kBM * 4;     // block prefix [B + 1], 64 bits
+  static constexpr int kUPre = kBPre + (kMaxPackedSeqs + 1) * 8;   // unit prefix [B + 1]
+  static constexpr int kSums = (kUPre + (kMaxPackedSeqs + 1) * 4 + 7) / 8 * 8;
+  static constexpr int kSegRing = (kSums + 32 * 16 + 15) / 16 * 16;
+  static constexpr int kBars = kSegRing + kSegs * (int)sizeof(Seg);
+  static constexpr int kNumBars = 2 + 2 * kStages + 10 + 2 * kSegs + (kFp8 ? 2 * kRaws : kStages);
+  static constexpr int kMisc = kBars + kNumBars * 8;
+  static constexpr int kBytes = kMisc + 64 + kSmemAlignSlack;
+  static_assert(kBytes <= 232448, "dynamic shared memory above the 227 KB per-CTA limit");
+};
+
+template <int D, bool kFp8>
+struct Shared {
+  using L = Layout<D, kFp8>;
+  uint8_t* base;
+  uint32_t sbase;
+  FA_DEV uint32_t bar(int i) const { return sbase + L::kBars + 8 * i; }
+  FA_DEV uint32_t q_full() const { return bar(0); }
+  FA_DEV uint32_t q_empty() const { return bar(1); }
+  FA_DEV uint32_t kv_full(int s) const { return bar(2 + s); }
+  FA_DEV uint32_t kv_empty(int s) const { return bar(2 + L::kStages + s); }
+  FA_DEV uint32_t s_full(int t) const { return bar(2 + 2 * L::kStages + t); }
+  FA_DEV uint32_t p_lo(int t) const { return bar(4 + 2 * L::kStages + t); }
+  FA_DEV uint32_t p_hi(int t) const { return bar(6 + 2 * L::kStages + t); }
+  FA_DEV uint32_t o_ready(int t) const { return bar(8 + 2 * L::kStages + t); }
+  FA_DEV uint32_t o_full(int t) const { return bar(10 + 2 * L::kStages + t); }
+  FA_DEV uint32_t seg_full(int s) const { return bar(12 + 2 * L::kStages + s); }
+  FA_DEV uint32_t seg_empty(int s) const { return bar(12 + 2 * L::kStages + kSegs + s); }
+  // BF16: a value tile with rows to clear has landed (the clearing warp then
+  // fills kv_full).  One per stage, so that it cannot run a phase ahead.
+  FA_DEV uint32_t v_landed(int s) const { return bar(12 + 2 * L::kStages + 2 * kSegs + s); }
+  FA_DEV uint32_t raw_full(int s) const { return bar(12 + 2 * L::kStages + 2 * kSegs + s); }
+  FA_DEV uint32_t raw_empty(int s) const { return bar(12 + 2 * L::kStages + 2 * kSegs + L::kRaws + s); }
+  FA_DEV uint32_t abort() const { return sbase + L::kMisc + 4; }
+  FA_DEV uint32_t* tmem_slot() const { return reinterpret_cast<uint32_t*>(base + L::kMisc); }
+  FA_DEV int* warp_flag() const { return reinterpret_cast<int*>(base + L::kMisc + 8); }
+  FA_DEV float* st_scale() const { return reinterpret_cast<float*>(base + L::kStats); }
+  FA_DEV float* st_l() const { return st_scale() + 2 * kBM; }
+  FA_DEV float* st_lr() const { return st_l() + 2 * kBM; }
+  FA_DEV float* st_m() const { return st_lr() + 2 * kBM; }
+  FA_DEV volatile Seg* segs() const { return reinterpret_cast<volatile Seg*>(base + L::kSegRing); }
+  FA_DEV bool wait(uint32_t b, uint32_t parity, int site, const PagedAttnParams& p) const {
+    return mbar_wait_bounded(b, parity, abort(), &g_err, site, p.wait_limit_ns);
+  }
+};
+
+// ------------------------------------------------------------- units, line --
+
+FA_DEV int tile_tokens(int group) { return kBM / group; }
+
+// sum of floor((a i + b) / m) for i in [0, n); a, b >= 0, a n + b < 2^31 once
+// a and b are below m (Euclid's algorithm on the slope).
+FA_DEV long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
+  long long s = 0;
+  while (n > 0) {
+    if (a >= m) {
+      s += (long long)n * (n - 1) / 2 * (a / m);
+      a %= m;
+    }
+    if (b >= m) {
+      s += (long long)n * (b / m);
+      b %= m;
+    }
+    const uint32_t top = a * n + b;
+    if (top < m) break;
+    n = top / m;
+    b = top % m;
+    const uint32_t t = m;
+    m = a;
+    a = t;
+  }
+  return s;
+}
+
+// A sequence's pairs of tiles and their key blocks.
+struct Seq {
+  int n, L, q0;
+  int pairs, t2;      // pairs of tiles, tokens of a pair
+  bool causal;
+  FA_DEV int blocks(int pair) const {      // at least one, so that rows without a key are written too
+    const int end = causal ? min(L, L - n + (pair + 1) * t2) : L;
+    return max(1, (end + kBN - 1) / kBN);
+  }
+  // Blocks of the pairs [0, p).
+  FA_DEV long long prefix(int p) const {
+    if (!causal) return (long long)p * max(1, (L + kBN - 1) / kBN);
+    const int last = p == pairs ? blocks(pairs - 1) : 0;      // the one whose end the sequence's end cuts
+    if (p == pairs) --p;
+    const int e0 = L - n + t2;                                // end of pair 0's keys
+    const int none = e0 <= 0 ? min(p, -e0 / t2 + 1) : 0;      // pairs that see no key
+    return last + none + (p > none ? floor_sum(p - none, kBN, t2, e0 + none * t2 + kBN - 1) : 0);
+  }
+  FA_DEV long long total() const { return prefix(pairs); }
+  // Pairs run from the last (the longest under a mask) to the first: blocks of
+  // the i units before unit i of a head.
+  FA_DEV long long before(int i) const { return total() - prefix(pairs - i); }
+};
+FA_DEV Seq seq_of(const PagedAttnParams& p, int b) {
+  Seq r;
+  r.L = p.s.seq_lens[b];
+  if (p.s.cu) {
+    r.q0 = p.s.cu[b];
+    r.n = p.s.cu[b + 1] - r.q0;
+  } else {
+    r.q0 = b * p.s.Sn;
+    r.n = p.s.Sn;
+  }
+  r.t2 = 2 * tile_tokens(p.group);
+  r.pairs = (r.n + r.t2 - 1) / r.t2;
+  r.causal = p.causal != 0;
+  return r;
+}
+
+// The work of a call: prefix tables over the sequences and where the whole
+// rounds end.
+struct Line {
+  const long long* bpre;
+  const int* upre;
+  int units;          // all units
+  int whole;          // units of the whole rounds
+  long long t0, t1;   // the blocks of the others
+  int G;              // stretches that they are cut into
+  FA_DEV long long stretch(int c) const { return t0 + (t1 - t0) * c / G; }
+};
+
+// Last b in [0, B) with table[b] <= x.
+template <class T>
+FA_DEV int last_at_most(const T* table, int B, T x) {
+  int lo = 0, hi = B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (table[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Builds the tables; all threads of the block.  No units when the sequences
+// break the rules.
+FA_DEV Line build_line(const PagedAttnParams& p, long long* bpre, int* upre, long long* sums, int ctas) {
+  Line line{bpre, upre, 0, 0, 0, 0, 0};
+  if (!paged::sequences_ok(p.s, p.max_q)) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) paged::record_bad_input(&g_err, kSiteSeqs);
+    return line;
+  }
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  long long carry_b = 0;
+  int carry_u = 0;
+  for (int b0 = 0; b0 < p.s.B; b0 += blockDim.x) {
+    const int b = b0 + threadIdx.x;
+    long long vb = 0;
+    int vu = 0;
+    if (b < p.s.B) {
+      const Seq s = seq_of(p, b);
+      if (s.n > 0) {
+        vu = s.pairs * p.s.Hkv;
+        vb = s.total() * p.s.Hkv;
+      }
+    }
+    long long ib = vb;
+    int iu = vu;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const long long ob = __shfl_up_sync(0xffffffffu, ib, d);
+      const int ou = __shfl_up_sync(0xffffffffu, iu, d);
+      if (lane >= d) {
+        ib += ob;
+        iu += ou;
+      }
+    }
+    if (lane == 31) {
+      sums[2 * warp] = ib;
+      sums[2 * warp + 1] = iu;
+    }
+    __syncthreads();
+    long long before_b = carry_b + ib - vb;
+    int before_u = carry_u + iu - vu;
+    const int warps = blockDim.x / 32;
+    for (int w = 0; w < warps; ++w) {
+      if (w < warp) {
+        before_b += sums[2 * w];
+        before_u += (int)sums[2 * w + 1];
+      }
+      carry_b += sums[2 * w];
+      carry_u += (int)sums[2 * w + 1];
+    }
+    if (b < p.s.B) {
+      bpre[b] = before_b;
+      upre[b] = before_u;
+    }
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    bpre[p.s.B] = carry_b;
+    upre[p.s.B] = carry_u;
+  }
+  __syncthreads();
+  line.units = carry_u;
+  line.t1 = carry_b;
+  // a last round that is nearly full is not worth cutting
+  const int rest = carry_u % ctas;
+  line.whole = rest * 10 >= ctas * 9 ? carry_u : carry_u - rest;
+  if (line.whole < carry_u) {
+    const int b = last_at_most(upre, p.s.B, line.whole);
+    const Seq s = seq_of(p, b);
+    const int r = line.whole - upre[b], head = r / s.pairs;
+    line.t0 = bpre[b] + head * s.total() + s.before(r - head * s.pairs);
+  } else {
+    line.t0 = line.t1;
+  }
+  const long long most = (line.t1 - line.t0 + kMinStretch - 1) / kMinStretch;
+  line.G = most < ctas ? (int)most : ctas;
+  return line;
+}
+
+// The unit that holds position t of the line.  One warp, converged.
+struct Place {
+  int b, head, i;     // i: the unit within its head, pair = pairs - 1 - i
+  long long start;    // its first position
+};
+FA_DEV Place find_place(const PagedAttnParams& p, const Line& line, long long t) {
+  Place w;
+  w.b = last_at_most(line.bpre, p.s.B, t);
+  const Seq s = seq_of(p, w.b);
+  const long long per_head = s.total();
+  long long r = t - line.bpre[w.b];
+  w.head = (int)(r / per_head);
+  r -= w.head * per_head;
+  const int lane = threadIdx.x % 32;
+  int lo = 0, size = s.pairs;       // the unit is in [lo, lo + size)
+  while (size > 1) {
+    const int step = (size + 31) / 32, at = lo + lane * step;
+    const bool in = at < lo + size && s.before(at) <= r;
+    const int k = __popc(__ballot_sync(0xffffffffu, in)) - 1;
+    size = min(step, size - k * step);
+    lo += k * step;
+  }
+  w.i = lo;
+  w.start = t - r + s.before(lo);
+  return w;
+}
+
+// ------------------------------------------------------------------ roles --
+
+// Takes the next segment out of the ring; false at the end of the work or
+// after a give-up.
+template <int D, bool kFp8>
+struct SegReader {
+  const Shared<D, kFp8>& sh;
+  const PagedAttnParams& p;
+  int i = 0;
+  uint32_t phase = 0;
+  FA_DEV SegReader(const Shared<D, kFp8>& s, const PagedAttnParams& q) : sh(s), p(q) {}
+  // The whole warp calls it.
+  FA_DEV bool next(Seg& w) {
+    if (!sh.wait(sh.seg_full(i), phase, kSiteSegFull, p)) return false;
+    const volatile Seg& r = sh.segs()[i];
+    w.b = r.b;
+    w.head = r.head;
+    w.tok0 = r.tok0;
+    w.kb = r.kb;
+    w.count = r.count;
+    w.n = r.n;
+    w.L = r.L;
+    w.q0 = r.q0;
+    w.slot = r.slot;
+    __syncwarp();
+    if (threadIdx.x % 32 == 0) mbar_arrive(sh.seg_empty(i));
+    if (++i == kSegs) {
+      i = 0;
+      phase ^= 1;
+    }
+    return w.b >= 0;
+  }
+};
+
+// Key blocks of the segment that tile t sees.
+FA_DEV int tile_blocks(const Seg& w, int t, int tt, bool causal) {
+  const int tok = w.tok0 + t * tt;
+  if (tok >= w.n) return 0;
+  const int end = causal ? min(w.L, w.L - w.n + min(tok + tt, w.n)) : w.L;
+  return min(w.count, max(0, (end + kBN - 1) / kBN - w.kb));
+}
+
+template <int D, bool kFp8>
+__device__ void scheduler_role(const Shared<D, kFp8>& sh, const PagedAttnParams& p, const Line& line) {
+  const int lane = threadIdx.x % 32;
+  const int G = gridDim.x, c = blockIdx.x;
+  int slot_i = 0;
+  uint32_t phase = 1;
+  auto put = [&](int b, int head, int pair, int kb, int count, const Seq& s, int slot) -> bool {
+    if (!sh.wait(sh.seg_empty(slot_i), phase, kSiteSegEmpty, p)) return false;
+    if (lane == 0) {
+      volatile Seg& r = sh.segs()[slot_i];
+      r.b = b;
+      r.head = head;
+      r.tok0 = pair * s.t2;
+      r.kb = kb;
+      r.count = count;
+      r.n = s.n;
+      r.L = s.L;
+      r.q0 = s.q0;
+      r.slot = slot;
+      mbar_arrive(sh.seg_full(slot_i));
+    }
+    __syncwarp();
+    if (++slot_i == kSegs) {
+      slot_i = 0;
+      phase ^= 1;
+    }
+    return true;
+  };
+  for (int u = c; u < line.whole; u += G) {
+    const int b = last_at_most(line.upre, p.s.B, u);
+    const Seq s = seq_of(p, b);
+    const int r = u - line.upre[b], head = r / s.pairs;
+    const int pair = s.pairs - 1 - (r - head * s.pairs);
+    if (!put(b, head, pair, 0, s.blocks(pair), s, -1)) return;
+  }
+  if (c < line.G) {
+    const long long t0 = line.stretch(c), t1 = line.stretch(c + 1);
+    Place w = find_place(p, line, t0);
+    Seq s = seq_of(p, w.b);
+    for (long long t = t0; t < t1;) {
+      const int pair = s.pairs - 1 - w.i, nblk = s.blocks(pair);
+      const int kb = (int)(t - w.start);
+      const int count = (int)(t1 - t < nblk - kb ? t1 - t : nblk - kb);
+      const bool whole = kb == 0 && count == nblk;
+      if (!put(w.b, w.head, pair, kb, count, s, whole ? -1 : 2 * c + (t == t0 ? 0 : 1))) return;
+      t += count;
+      w.start += nblk;
+      if (++w.i == s.pairs && t < t1) {
+        w.i = 0;
+        if (++w.head == p.s.Hkv) {
+          w.head = 0;
+          do {
+            ++w.b;
+            s = seq_of(p, w.b);
+          } while (s.n == 0 && w.b < p.s.B - 1);
+        }
+      }
+    }
+  }
+  Seq none{};
+  put(-1, 0, 0, 0, 0, none, -1);
+}
+
+// Loads: Q of both tiles once per segment, then the key and value blocks in
+// turn.  The whole warp runs along; lane 0 issues, the lanes hold the numbers
+// of the next 32 pages.
+template <int D, bool kFp8>
+__device__ void load_role(const Shared<D, kFp8>& sh, const CUtensorMap* tq, const CUtensorMap* tk,
+                          const CUtensorMap* tv, const PagedAttnParams& p) {
+  using L = Layout<D, kFp8>;
+  const int lane = threadIdx.x % 32;
+  const int tt = tile_tokens(p.group);
+  const int box = min(1 << p.s.page_shift, kBN);          // rows of a box
+  constexpr int kRing = kFp8 ? L::kRaws : L::kStages;
+  SegReader<D, kFp8> in(sh, p);
+  Seg w;
+  uint32_t uit = 0;
+  int stage = 0;
+  uint32_t phase = 1;
+  while (in.next(w)) {
+    const int n0 = tile_blocks(w, 0, tt, p.causal), n1 = tile_blocks(w, 1, tt, p.causal);
+    const int n = max(n0, n1);
+    if (n == 0) continue;
+    if (!sh.wait(sh.q_empty(), (uit & 1) ^ 1, kSiteQEmpty, p)) return;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(sh.q_full(), 2 * tt * p.group * D * 2);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int c = 0; c < L::kChunks; ++c)
+          tma_load_3d(sh.sbase + L::kQ + t * L::kTileBytes + c * L::kChunkBytes, tq, sh.q_full(), c * 64,
+                      w.head * p.group, w.q0 + w.tok0 + t * tt);
+    }
+    ++uit;
+    const int* table = p.s.block_table + (size_t)w.b * p.s.max_pages;
+    const int last_page = (w.L - 1) >> p.s.page_shift;
+    int held = -64, pages = -1;                            // pages[held .. held + 32) one per lane
+    for (int j = 0; j < n; ++j) {
+      const int key0 = (w.kb + j) * kBN;
+      const int boxes = (min(kBN, w.L - key0) + box - 1) / box;   // that hold a key of the sequence
+      const int page0 = key0 >> p.s.page_shift;
+      if (page0 < held || page0 + boxes > held + 32) {
+        held = page0;
+        pages = -1;
+        if (held + lane <= last_page) {
+          pages = table[held + lane];
+          if (pages < 0 || pages >= p.s.num_pages) {
+            if (held + lane <= (min(w.L, (w.kb + n) * kBN) - 1) >> p.s.page_shift)
+              paged::record_bad_input(&g_err, kSitePage);
+            pages = -1;
+          }
+        }
+      }
+#pragma unroll 1
+      for (int which = 0; which < 2; ++which) {
+        const bool clear = !kFp8 && which && w.L - key0 < kBN;
+        const uint32_t full = kFp8 ? sh.raw_full(stage) : clear ? sh.v_landed(stage) : sh.kv_full(stage);
+        if (!sh.wait(kFp8 ? sh.raw_empty(stage) : sh.kv_empty(stage), phase, kSiteKvEmpty, p)) return;
+        if (lane == 0) mbar_arrive_expect_tx(full, boxes * box * (kFp8 ? D + 1 : 2 * D));
+        __syncwarp();
+        const CUtensorMap* map = which ? tv : tk;
+        const uint32_t dst = sh.sbase + (kFp8 ? L::kRaw + stage * L::kRawBytes : L::kKV + stage * L::kTileBytes);
+        for (int i = 0; i < boxes; ++i) {
+          const int page = __shfl_sync(0xffffffffu, pages, page0 + i - held);
+          if (lane == 0) {
+            const int off = (key0 + i * box) & ((1 << p.s.page_shift) - 1);
+            const int ph = page < 0 ? -1 : page * p.s.Hkv + w.head;    // -1: reads as zeros
+            if (kFp8) {
+              tma_load_3d(dst + i * box * D, map, full, 0, off, ph);
+              bulk_load(sh.sbase + L::kRawScale + stage * kBN + i * box,
+                        (which ? p.v_scale : p.k_scale) + ((size_t)max(ph, 0) << p.s.page_shift) + off, box, full);
+            } else {
+#pragma unroll
+              for (int c = 0; c < L::kChunks; ++c)
+                tma_load_3d(dst + c * L::kChunkBytes + i * box * 128, map, full, c * 64, off, ph);
+            }
+          }
+        }
+        if (++stage == kRing) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    }
+  }
+}
+
+// BF16 pages: value rows behind the sequence's end, in its last block, are
+// cleared between the load and the product.
+template <int D>
+__device__ void clean_role(const Shared<D, false>& sh, const PagedAttnParams& p) {
+  using L = Layout<D, false>;
+  const int lane = threadIdx.x % 32;
+  const int tt = tile_tokens(p.group);
+  SegReader<D, false> in(sh, p);
+  Seg w;
+  uint32_t tiles = 0;      // tiles that went through the ring
+  uint32_t parity = 0;     // of each stage's v_landed
+  while (in.next(w)) {
+    const int n = max(tile_blocks(w, 0, tt, p.causal), tile_blocks(w, 1, tt, p.causal));
+    const int rows = w.L - (w.kb + n - 1) * kBN;
+    if (n > 0 && rows < kBN) {
+      const int stage = (tiles + 2 * n - 1) % L::kStages;
+      if (!sh.wait(sh.v_landed(stage), (parity >> stage) & 1, kSiteLanded, p)) return;
+      parity ^= 1u << stage;
+      uint8_t* tile = sh.base + L::kKV + stage * L::kTileBytes;
+      for (int c = 0; c < L::kChunks; ++c)
+        for (int i = rows * 8 + lane; i < kBN * 8; i += 32)
+          *reinterpret_cast<uint4*>(tile + c * L::kChunkBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sh.kv_full(stage));
+    }
+    tiles += 2 * n;
+  }
+}
+
+// E4M3 pages: four warps widen each tile, a piece of 16 codes at a time, into
+// the swizzled BF16 tile that the products read.  Rows behind the sequence's
+// end come out as zeros.
+template <int D>
+__device__ void widen_role(const Shared<D, true>& sh, const PagedAttnParams& p) {
+  using L = Layout<D, true>;
+  constexpr int kPieces = D / 16;                    // of a row
+  constexpr int kRowsPer = 32 / kPieces;             // rows of a warp's step
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32 - 16;
+  const int tt = tile_tokens(p.group);
+  const int piece = lane % kPieces;
+  SegReader<D, true> in(sh, p);
+  Seg w;
+  int raw = 0, stage = 0;
+  uint32_t raw_phase = 0, phase = 1;
+  while (in.next(w)) {
+    const int n = max(tile_blocks(w, 0, tt, p.causal), tile_blocks(w, 1, tt, p.causal));
+    for (int j = 0; j < 2 * n; ++j) {
+      const int rows = w.L - (w.kb + j / 2) * kBN;
+      if (!sh.wait(sh.raw_full(raw), raw_phase, kSiteRaw, p)) return;
+      if (!sh.wait(sh.kv_empty(stage), phase, kSiteKvEmpty, p)) return;
+      const uint8_t* src = sh.base + L::kRaw + raw * L::kRawBytes;
+      const uint8_t* scales = sh.base + L::kRawScale + raw * kBN;
+      uint8_t* dst = sh.base + L::kKV + stage * L::kTileBytes;
+#pragma unroll
+      for (int i = 0; i < 32 / kRowsPer; ++i) {
+        const int r = warp * 32 + i * kRowsPer + lane / kPieces;
+        // the TMA's swizzle of rows of D bytes
+        const int from = D == 128 ? r * 128 + ((piece ^ (r & 7)) << 4) : r * 64 + ((piece ^ ((r >> 1) & 3)) << 4);
+        const uint4 x = *reinterpret_cast<const uint4*>(src + from);
+        const uint32_t byte = scales[r];
+        // 2^(120 + e) does not exist for e > 7: the rest is a second factor
+        const uint32_t first = min(byte, 134u);       // e = 7
+        uint32_t f = (first + 120u) << 7;
+        f |= f << 16;
+        uint32_t g = byte == 255u ? 0x7FC0u : (byte - first + 127u) << 7;
+        g |= g << 16;
+        const bool big = __any_sync(0xffffffffu, byte > 134u);
+        const uint32_t words[4] = {x.x, x.y, x.z, x.w};
+        uint32_t y[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          // codes 2 k and 2 k + 1 to the upper bytes of the halves
+          const uint32_t t = __byte_perm(words[k / 2], 0u, k & 1 ? 0x3424 : 0x1404);
+          y[k] = paged::mul_bf16x2(((t >> 4) & 0x07F007F0u) | (t & 0x80008000u), f);
+          if (big) y[k] = paged::mul_bf16x2(y[k], g);
+          if (r >= rows) y[k] = 0u;
+        }
+        // 16 columns are two 16-byte pieces of a 64-column chunk's row; lanes
+        // of the second chunk write theirs in the other order, so that the
+        // eight lanes of a row touch all banks
+        uint8_t* to = dst + (piece / 4) * L::kChunkBytes + r * 128;
+        const int q = 2 * (piece % 4), flip = piece / 4;
+        const uint4 a = make_uint4(y[0], y[1], y[2], y[3]), b = make_uint4(y[4], y[5], y[6], y[7]);
+        *reinterpret_cast<uint4*>(to + (((q + flip) ^ (r & 7)) << 4)) = flip ? b : a;
+        *reinterpret_cast<uint4*>(to + (((q + 1 - flip) ^ (r & 7)) << 4)) = flip ? a : b;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(sh.kv_full(stage));
+        mbar_arrive(sh.raw_empty(raw));
+      }
+      if (++raw == L::kRaws) {
+        raw = 0;
+        raw_phase ^= 1;
+      }
+      if (++stage == L::kStages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+  }
+}
+
+// Maximum that keeps a NaN.
+FA_DEV float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// Softmax of tile t: one thread per row.  With 192 registers the block's 128
+// scores stay in registers; with 160 (E4M3) they are read from tensor memory
+// a second time for the exponentials.
+template <int D, bool kFp8>
+__device__ void softmax_role(const int t, const Shared<D, kFp8>& sh, const uint32_t tmem, const PagedAttnParams& p) {
+  constexpr bool kKeep = !kFp8;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int wq = warp & 3;
+  const int r_in_tile = wq * 32 + lane;
+  const uint32_t tm_s = tmem + (uint32_t(wq * 32) << 16) + uint32_t(t * kBN);
+  const float sl2 = p.scale_log2;
+  const int tt = tile_tokens(p.group);
+  const int my_tok = r_in_tile / p.group;
+  SegReader<D, kFp8> in(sh, p);
+  Seg w;
+  uint32_t sit = 0;
+  while (in.next(w)) {
+    const int nt = tile_blocks(w, t, tt, p.causal);
+    if (nt == 0) continue;
+    const int tok = w.tok0 + t * tt;
+    const int lim_first = p.causal ? w.L - w.n + tok + 1 : w.L;                  // of the tile's first row
+    const int lim_row = p.causal ? min(w.L, lim_first + my_tok) : w.L;
+    float m_run = -INFINITY, l_run = 0.0f, lr_run = 0.0f;
+    for (int j = 0; j < nt; ++j, ++sit) {
+      if (!sh.wait(sh.s_full(t), sit & 1, kSiteS, p)) return;
+      tc_fence_after();
+      const int kv0 = (w.kb + j) * kBN;
+      const bool need_mask = kv0 + kBN > lim_first;
+      const int lim = lim_row - kv0;            // columns >= lim are masked
+      uint32_t r[kKeep ? 4 : 1][32];
+      float mx[4];
+      if (kKeep) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(tm_s + c * 32, r[kKeep ? c : 0]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_fence(r[kKeep ? c : 0]);
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t(&x)[32] = r[kKeep ? c : 0];
+        if (!kKeep) {
+          tmem_ld32(tm_s + c * 32, x);
+          tmem_ld_wait();
+          tmem_ld_fence(x);
+        }
+        if (need_mask) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (c * 32 + i >= lim) x[i] = __float_as_uint(-INFINITY);
+        }
+        float m = __uint_as_float(x[0]);
+#pragma unroll
+        for (int i = 1; i < 31; i += 2) m = max3_nan(m, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+        mx[c] = max3_nan(m, __uint_as_float(x[31]), -INFINITY);
+      }
+      float m_blk = max3_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3], -INFINITY) * sl2;
+      // a NaN or +inf among the scores makes the row's sums NaN, whichever
+      // unit its exponential would go through
+      const bool lost = !(m_blk < INFINITY);
+      if (lost) m_blk = -INFINITY;
+      float factor = 1.0f;
+      bool rescaled = false;
+      if (j == 0) {
+        m_run = m_blk;
+      } else if (m_blk - m_run > kThreshold) {
+        factor = ex2_mufu(m_run - m_blk);
+        m_run = m_blk;
+        rescaled = true;
+      }
+      const float m_use = (m_run == -INFINITY) ? 0.0f : m_run;
+      const uint64_t sl2x2 = pk2(sl2, sl2), negm2 = pk2(-m_use, -m_use);
+      // sums of the FP32 weights (LSE) and of the weights rounded to BF16, as
+      // the product takes them (the division)
+      uint64_t se2[2] = {0ull, 0ull}, sr2[2] = {0ull, 0ull};
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int ch = 2 * half + q;
+          uint32_t(&x)[32] = r[kKeep ? ch : 0];
+          if (!kKeep) {
+            tmem_ld32(tm_s + ch * 32, x);
+            tmem_ld_wait();
+            tmem_ld_fence(x);
+            if (need_mask) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (ch * 32 + i >= lim) x[i] = __float_as_uint(-INFINITY);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const uint64_t x2 = fma2(pk2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), sl2x2, negm2);
+            float x0, x1, e0, e1;
+            up2(x2, x0, x1);
+            exp2_pair<kEmu>(x0, x1, i, e0, e1);
+            const uint32_t pp = pack_bf16x2(e0, e1);
+            pk[q * 16 + i / 2] = pp;
+            se2[(i / 2) & 1] = add2(se2[(i / 2) & 1], pk2(e0, e1));
+            sr2[(i / 2) & 1] = add2(sr2[(i / 2) & 1], pk2(__uint_as_float(pp << 16), __uint_as_float(pp & 0xFFFF0000u)));
+          }
+        }
+        // P lies over the first 64 columns of S: with the scores re-read, the
+        // second half's (columns 64-127) are still untouched
+        tmem_st32(tm_s + 32 * half, pk);
+        if (half == 0) {
+          sh.st_scale()[t * kBM + r_in_tile] = factor;
+          const unsigned any = __any_sync(0xffffffffu, rescaled);
+          if (lane == 0) sh.warp_flag()[t * 4 + wq] = any ? 1 : 0;
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(sh.p_lo(t));
+        }
+      }
+      float a0, a1, b0, b1;
+      up2(add2(se2[0], se2[1]), a0, a1);
+      up2(add2(sr2[0], sr2[1]), b0, b1);
+      l_run = l_run * factor + (a0 + a1);
+      lr_run = lr_run * factor + (b0 + b1);
+      if (lost) l_run = lr_run = __int_as_float(0x7FC00000);
+      tmem_st_wait();
+      if (j == nt - 1) {
+        sh.st_l()[t * kBM + r_in_tile] = l_run;
+        sh.st_lr()[t * kBM + r_in_tile] = lr_run;
+        sh.st_m()[t * kBM + r_in_tile] = m_run;
+      }
+      tc_fence_before();
+      mbar_arrive(sh.p_hi(t));
+    }
+  }
+}
+
+// Correction: rescales O in tensor memory when a row's maximum moved, and
+// writes the segment's rows: O / l in BF16 and LSE of a whole unit, else the
+// unnormalised row and its statistics.
+template <int D, bool kFp8>
+__device__ void correction_role(const Shared<D, kFp8>& sh, const uint32_t tmem, const PagedAttnParams& p) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int wq = warp & 3;
+  const int r_in_tile = wq * 32 + lane;
+  const uint32_t lane_off = uint32_t(wq * 32) << 16;
+  const int tt = tile_tokens(p.group);
+  const int my_tok = r_in_tile / p.group, my_head = r_in_tile - my_tok * p.group;
+  SegReader<D, kFp8> in(sh, p);
+  Seg w;
+  uint32_t sit[2] = {0u, 0u}, uit[2] = {0u, 0u};
+  while (in.next(w)) {
+    const int nts[2] = {tile_blocks(w, 0, tt, p.causal), tile_blocks(w, 1, tt, p.causal)};
+    const int n = max(nts[0], nts[1]);
+    float fin_l[2] = {0.0f, 0.0f}, fin_lr[2] = {0.0f, 0.0f}, fin_m[2] = {-INFINITY, -INFINITY};
+    for (int j = 0; j < n; ++j) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (j >= nts[t]) continue;
+        const uint32_t ph = sit[t] & 1;
+        ++sit[t];
+        if (!sh.wait(sh.p_lo(t), ph, kSiteP, p)) return;
+        tc_fence_after();
+        if (j > 0 && sh.warp_flag()[t * 4 + wq]) {
+          const float f = sh.st_scale()[t * kBM + r_in_tile];
+          const uint64_t f2 = pk2(f, f);
+          const uint32_t tm_o = tmem + lane_off + uint32_t(256 + t * D);
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t r[32];
+            tmem_ld32(tm_o + c * 32, r);
+            tmem_ld_wait();
+            tmem_ld_fence(r);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              float y0, y1;
+              up2(mul2(pk2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), f2), y0, y1);
+              r[i] = __float_as_uint(y0);
+              r[i + 1] = __float_as_uint(y1);
+            }
+            tmem_st32(tm_o + c * 32, r);
+          }
+          tmem_st_wait();
+        }
+        // the statistics come with the second half of the last block's P; they
+        // are taken before O is released, after which the next segment's
+        // softmax may overwrite them
+        if (j == nts[t] - 1) {
+          if (!sh.wait(sh.p_hi(t), ph, kSiteP, p)) return;
+          fin_l[t] = sh.st_l()[t * kBM + r_in_tile];
+          fin_lr[t] = sh.st_lr()[t * kBM + r_in_tile];
+          fin_m[t] = sh.st_m()[t * kBM + r_in_tile];
+        }
+        tc_fence_before();
+        mbar_arrive(sh.o_ready(t));
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int tok = w.tok0 + t * tt + my_tok;
+      const bool valid = my_tok < tt && tok < w.n;
+      const bool has = nts[t] > 0;
+      if (has) {
+        if (!sh.wait(sh.o_full(t), uit[t] & 1, kSiteO, p)) return;
+        ++uit[t];
+        tc_fence_after();
+      }
+      const float l = fin_l[t], lr = fin_lr[t], m = fin_m[t];
+      const float inv = w.slot >= 0 ? 1.0f : lr == 0.0f ? 0.0f : 1.0f / lr;
+      const int head = w.head * p.group + my_head;
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + ((size_t)(w.q0 + tok) * p.Hq + head) * D;
+      float* part = Part<D>::out(p.part, max(w.slot, 0)) + (t * kBM + r_in_tile) * D;
+      const uint32_t tm_o = tmem + lane_off + uint32_t(256 + t * D);
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t r[32];
+        if (has) {
+          tmem_ld32(tm_o + c * 32, r);
+          tmem_ld_wait();
+          tmem_ld_fence(r);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) r[i] = 0u;
+        }
+        if (valid && w.slot >= 0) {
+#pragma unroll
+          for (int v = 0; v < 4; ++v) st_global_v8(part + c * 32 + v * 8, r + v * 8);
+        } else if (valid) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            pk[e] = pack_bf16x2(__uint_as_float(r[2 * e]) * inv, __uint_as_float(r[2 * e + 1]) * inv);
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            reinterpret_cast<uint4*>(dst)[c * 4 + v] = make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
+        }
+      }
+      if (valid) {
+        if (w.slot >= 0) {
+          *reinterpret_cast<float4*>(Part<D>::stat(p.part, w.slot) + (t * kBM + r_in_tile) * Part<D>::kStat) =
+              make_float4(m, l, lr, 0.0f);
+        } else {
+          const size_t li = p.s.cu ? (size_t)head * p.s.Sn + w.q0 + tok : ((size_t)w.b * p.Hq + head) * p.s.Sn + tok;
+          p.lse[li] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
+        }
+      }
+      if (has) tc_fence_before();
+    }
+  }
+}
+
+// K steps of S = Q K^T, 16 wide: step kk reads 64-element chunk kk / 4 at byte
+// offset 32 (kk % 4) of its rows.
+template <int D, int CHUNK, int KK>
+FA_DEV void s_steps(uint32_t d_tmem, uint32_t alo, uint32_t ahi, uint32_t blo, uint32_t bhi, uint32_t idesc) {
+  if constexpr (KK < D / 16) {
+    constexpr uint32_t off = ((KK >> 2) * CHUNK + (KK & 3) * 32) >> 4;
+    mma_ss_w<off, off>(d_tmem, alo, ahi, blo, bhi, idesc, KK > 0 ? 1u : 0u);
+    s_steps<D, CHUNK, KK + 1>(d_tmem, alo, ahi, blo, bhi, idesc);
+  }
+}
+// K steps of O += P V: TMEM columns 8 kk.. of P, key rows 16 kk.. of V.
+template <int KK, int KEND>
+FA_DEV void pv_steps(uint32_t d_tmem, uint32_t a_tmem, uint32_t blo, uint32_t bhi, uint32_t idesc, uint32_t acc) {
+  if constexpr (KK < KEND) {
+    mma_ts_w<KK * 8, KK * 128>(d_tmem, a_tmem, blo, bhi, idesc, KK > 0 ? 1u : acc);
+    pv_steps<KK + 1, KEND>(d_tmem, a_tmem, blo, bhi, idesc, acc);
+  }
+}
+
+// MMA issue (a converged warp, one elected lane): S of both tiles for the first
+// block, then per block and tile PV(j), S(j + 1).  S(j + 1) overwrites the
+// columns of P(j) only after PV(j) was issued; MMAs of one thread run in order.
+template <int D, bool kFp8>
+__device__ void mma_role(const Shared<D, kFp8>& sh, const uint32_t tmem, const PagedAttnParams& p) {
+  using L = Layout<D, kFp8>;
+  constexpr uint32_t kIdS = idesc_bf16_f32(kBM, kBN, false, false);
+  constexpr uint32_t kIdPV = idesc_bf16_f32(kBM, D, false, true);
+  const int tt = tile_tokens(p.group);
+  uint32_t uit = 0;
+  uint32_t sit[2] = {0u, 0u};
+  int stage = 0;
+  uint32_t phase = 0;
+  auto issue_s = [&](int t, int st) {
+    const uint64_t da = sdesc_sw128(sh.sbase + L::kQ + t * L::kTileBytes, 16, 1024);
+    const uint64_t db = sdesc_sw128(sh.sbase + L::kKV + st * L::kTileBytes, 16, 1024);
+    s_steps<D, L::kChunkBytes, 0>(tmem + t * kBN, desc_lo(da), desc_hi(da), desc_lo(db), desc_hi(db), kIdS);
+  };
+  auto issue_pv = [&](int t, int st, bool acc, uint32_t ph) -> bool {
+    const uint64_t db = sdesc_sw128(sh.sbase + L::kKV + st * L::kTileBytes, L::kChunkBytes, 1024);
+    pv_steps<0, 4>(tmem + 256 + t * D, tmem + t * kBN, desc_lo(db), desc_hi(db), kIdPV, acc ? 1u : 0u);
+    if (!sh.wait(sh.p_hi(t), ph, kSiteP, p)) return false;
+    tc_fence_after();
+    pv_steps<4, 8>(tmem + 256 + t * D, tmem + t * kBN, desc_lo(db), desc_hi(db), kIdPV, 1u);
+    return true;
+  };
+  struct Pos {
+    int stage;
+    uint32_t phase;
+  };
+  auto take = [&]() {
+    const Pos r{stage, phase};
+    if (++stage == L::kStages) {
+      stage = 0;
+      phase ^= 1;
+    }
+    return r;
+  };
+  auto ready = [&](Pos r) -> bool {
+    if (!sh.wait(sh.kv_full(r.stage), r.phase, kSiteKvFull, p)) return false;
+    tc_fence_after();
+    return true;
+  };
+  SegReader<D, kFp8> in(sh, p);
+  Seg w;
+  while (in.next(w)) {
+    const int n0 = tile_blocks(w, 0, tt, p.causal), n1 = tile_blocks(w, 1, tt, p.causal);
+    const int n = max(n0, n1);
+    if (n == 0) continue;
+    if (!sh.wait(sh.q_full(), uit & 1, kSiteQFull, p)) return;
+    tc_fence_after();
+    Pos kp = take();
+    if (!ready(kp)) return;
+    if (n0 > 0) {
+      issue_s(0, kp.stage);
+      mma_commit_w(sh.s_full(0));
+    }
+    if (n1 > 0) {
+      issue_s(1, kp.stage);
+      mma_commit_w(sh.s_full(1));
+    }
+    mma_commit_w(sh.kv_empty(kp.stage));
+    if (n == 1) mma_commit_w(sh.q_empty());
+    for (int j = 0; j < n; ++j) {
+      const Pos vp = take();
+      if (!ready(vp)) return;
+      const bool more = j + 1 < n;
+      bool k_ready = false;
+      if (more) kp = take();
+      if (j < n0) {
+        const uint32_t ph = sit[0] & 1;
+        ++sit[0];
+        if (!sh.wait(sh.o_ready(0), ph, kSiteO, p)) return;
+        tc_fence_after();
+        if (!issue_pv(0, vp.stage, j > 0, ph)) return;
+        if (j + 1 < n0) {
+          if (!ready(kp)) return;
+          k_ready = true;
+          issue_s(0, kp.stage);
+          mma_commit_w(sh.s_full(0));
+        } else {
+          mma_commit_w(sh.o_full(0));
+        }
+      }
+      if (j < n1) {
+        const uint32_t ph = sit[1] & 1;
+        ++sit[1];
+        if (!sh.wait(sh.o_ready(1), ph, kSiteO, p)) return;
+        tc_fence_after();
+        if (!issue_pv(1, vp.stage, j > 0, ph)) return;
+        if (j + 1 == n1) mma_commit_w(sh.o_full(1));
+      }
+      mma_commit_w(sh.kv_empty(vp.stage));
+      if (more) {
+        if (j + 1 < n1) {
+          if (!k_ready && !ready(kp)) return;
+          issue_s(1, kp.stage);
+          mma_commit_w(sh.s_full(1));
+        }
+        mma_commit_w(sh.kv_empty(kp.stage));
+        if (j + 1 == n - 1) mma_commit_w(sh.q_empty());
+      }
+    }
+    ++uit;
+  }
+}
+
+template <int D, bool kFp8>
+__global__ void __launch_bounds__(Layout<D, kFp8>::kThreads, 1)
+    chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                 const __grid_constant__ CUtensorMap tm_v, const PagedAttnParams p) {
+  using L = Layout<D, kFp8>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x / 32;
+  Shared<D, kFp8> sh;
+  sh.base = smem;
+  sh.sbase = smem_u32(smem);
+
+  if (threadIdx.x == 0) {
+    mbar_init(sh.q_full(), 1);
+    mbar_init(sh.q_empty(), 1);
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(sh.kv_full(s), kFp8 ? 4 : 1);      // one arrival per widening warp
+      mbar_init(sh.kv_empty(s), 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(sh.s_full(t), 1);
+      mbar_init(sh.p_lo(t), kBM);
+      mbar_init(sh.p_hi(t), kBM);
+      mbar_init(sh.o_ready(t), kBM);
+      mbar_init(sh.o_full(t), 1);
+    }
+    for (int s = 0; s < kSegs; ++s) {
+      mbar_init(sh.seg_full(s), 1);
+      mbar_init(sh.seg_empty(s), L::kReaders);
+    }
+    for (int s = 0; s < (kFp8 ? 0 : L::kStages); ++s) mbar_init(sh.v_landed(s), 1);
+    for (int s = 0; s < L::kRaws; ++s) {
+      mbar_init(sh.raw_full(s), 1);
+      mbar_init(sh.raw_empty(s), 4);
+    }
+    st_shared(sh.abort(), 0);
+    fence_barrier_init();
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  if (warp == 13) {
+    tmem_alloc(sh.tmem_slot(), 512);
+    tmem_relinquish();
+  }
+  const Line line = build_line(p, reinterpret_cast<long long*>(smem + L::kBPre), reinterpret_cast<int*>(smem + L::kUPre),
+                               reinterpret_cast<long long*>(smem + L::kSums), gridDim.x);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *sh.tmem_slot();
+
+  if (warp < 8) {
+    reg_alloc<kFp8 ? 160 : 192>();
+    softmax_role<D, kFp8>(warp / 4, sh, tmem, p);
+  } else if (warp < 12) {
+    reg_dealloc<kFp8 ? 72 : 80>();
+    correction_role<D, kFp8>(sh, tmem, p);
+  } else if (warp < 16) {
+    reg_dealloc<kFp8 ? 40 : 48>();
+    if (warp == 12) {
+      load_role<D, kFp8>(sh, &tm_q, &tm_k, &tm_v, p);
+    } else if (warp == 13) {
+      mma_role<D, kFp8>(sh, tmem, p);
+    } else if (warp == 14) {
+      if constexpr (!kFp8) clean_role<D>(sh, p);
+    } else {
+      scheduler_role<D, kFp8>(sh, p, line);
+    }
+  } else {
+    if constexpr (kFp8) {
+      reg_dealloc<48>();
+      widen_role<D>(sh, p);
+    }
+  }
+
+  // After a give-up, copies and MMAs in flight land before the memory they
+  // target is released.
+  if (ld_shared_volatile(sh.abort())) {
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 2000000ull) __nanosleep(1000);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 13) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the parts of the units that borders between stretches cut: block
+// (x, y) does rows [32 y, 32 y + 32) of the unit whose first cut is border x + 1.
+constexpr int kJoinThreads = 256, kJoinRows = 32;
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) combine_kernel(const PagedAttnParams p, int ctas) {
+  __shared__ long long bpre[kMaxPackedSeqs + 1];
+  __shared__ int upre[kMaxPackedSeqs + 1];
+  __shared__ long long sums[2 * kJoinThreads / 32];
+  const Line line = build_line(p, bpre, upre, sums, ctas);
+  // before any exit, so that this grid ends after the main one
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = blockIdx.x + 1;
+  if (c >= line.G) return;
+  const long long t = line.stretch(c), prev = line.stretch(c - 1);
+  const Place w = find_place(p, line, t);
+  if (w.start == t || prev > w.start) return;      // no cut here, or not the unit's first
+  const Seq s = seq_of(p, w.b);
+  const int pair = s.pairs - 1 - w.i;
+  const long long end = w.start + s.blocks(pair);
+  const int first = 2 * (c - 1) + (prev == w.start ? 0 : 1);
+  int last = c;                                     // parts: slot `first`, then slots 2 c .. 2 last
+  while (last + 1 < line.G && line.stretch(last + 1) < end) ++last;
+  const int tt = tile_tokens(p.group);
+  for (int i = threadIdx.x; i < kJoinRows * (D / 4); i += kJoinThreads) {
+    const int r = blockIdx.y * kJoinRows + i / (D / 4), d = i % (D / 4) * 4;
+    const int in_tile = r % kBM, tk = in_tile / p.group;
+    const int tok = pair * s.t2 + r / kBM * tt + tk;
+    if (tk >= tt || tok >= s.n) continue;
+    float mt = Part<D>::stat(p.part, first)[r * Part<D>::kStat];
+    for (int k = c; k <= last; ++k) mt = fmaxf(mt, Part<D>::stat(p.part, 2 * k)[r * Part<D>::kStat]);
+    float lt = 0.0f, lrt = 0.0f;
+    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int k = c - 1; k <= last; ++k) {
+      const int slot = k < c ? first : 2 * k;
+      const float* stat = Part<D>::stat(p.part, slot) + r * Part<D>::kStat;
+      const float f = mt == -INFINITY ? 1.0f : ex2_mufu(stat[0] - mt);
+      lt += stat[1] * f;
+      lrt += stat[2] * f;
+      const float4 x = *reinterpret_cast<const float4*>(Part<D>::out(p.part, slot) + r * D + d);
+      y.x += x.x * f;
+      y.y += x.y * f;
+      y.z += x.z * f;
+      y.w += x.w * f;
+    }
+    const float inv = lrt == 0.0f ? 0.0f : 1.0f / lrt;
+    const int head = w.head * p.group + in_tile - tk * p.group;
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + ((size_t)(s.q0 + tok) * p.Hq + head) * D + d) =
+        make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
+    if (d == 0) {
+      const size_t li = p.s.cu ? (size_t)head * p.s.Sn + s.q0 + tok : ((size_t)w.b * p.Hq + head) * p.s.Sn + tok;
+      p.lse[li] = lt == 0.0f ? -INFINITY : (mt + log2f(lt)) * 0.693147180559945309f;
+    }
+  }
+}
+
+template <int D, bool kFp8>
+fa_status launch_inst(const PagedAttnLaunch& L, cudaStream_t stream) {
+  using Lay = Layout<D, kFp8>;
+  const PagedSeqs& s = L.p.s;
+  const int page_size = 1 << s.page_shift;
+  const long long page_heads = (long long)s.num_pages * s.Hkv;
+  const int box = page_size < kBN ? page_size : kBN;
+  CUtensorMap tq, tk, tv;
+  fa_status st;
+  const int rows = s.cu ? s.Sn : s.B * s.Sn;
+  if ((st = make_tmap_rows_group(&tq, L.p.q, rows, L.p.Hq, D, L.p.group, kBM / L.p.group)) != FA_OK) return st;
+  if ((st = make_tmap_pages(&tk, L.k_pages, page_heads, page_size, D, kFp8, box)) != FA_OK) return st;
+  if ((st = make_tmap_pages(&tv, L.v_pages, page_heads, page_size, D, kFp8, box)) != FA_OK) return st;
+  auto kern = chunk_kernel<D, kFp8>;
+  if ((st = prepare_kernel(reinterpret_cast<const void*>(kern), Lay::kBytes)) != FA_OK) return st;
+  const int ctas = L.p.num_ctas;
+  kern<<<ctas, Lay::kThreads, Lay::kBytes, stream>>>(tq, tk, tv, L.p);
+  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  if (ctas > 1) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(ctas - 1, 2 * kBM / kJoinRows);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, combine_kernel<D>, L.p, ctas) != cudaSuccess) return FA_ERR_CUDA;
+  }
+  return FA_OK;
+}
+
+}  // namespace pchunk
+
+size_t paged_chunk_workspace(int D) { return D == 128 ? pchunk::Part<128>::bytes() : pchunk::Part<64>::bytes(); }
+
+fa_status launch_paged_chunk(const PagedAttnLaunch& L, cudaStream_t stream) {
+  if (L.D == 128) return L.fp8 ? pchunk::launch_inst<128, true>(L, stream) : pchunk::launch_inst<128, false>(L, stream);
+  return L.fp8 ? pchunk::launch_inst<64, true>(L, stream) : pchunk::launch_inst<64, false>(L, stream);
+}
+
+fa_status paged_chunk_take_device_error() {
+  DeviceError e{0, 0};
+  if (cudaMemcpyFromSymbol(&e, pchunk::g_err, sizeof(e)) != cudaSuccess) return FA_ERR_CUDA;
+  if (e.status != 0) {
+    const DeviceError z{0, 0};
+    if (cudaMemcpyToSymbol(pchunk::g_err, &z, sizeof(z)) != cudaSuccess) return FA_ERR_CUDA;
+  }
+  return static_cast<fa_status>(e.status);
+}
+
+}  // namespace fa

@@ -81,6 +81,11 @@ struct PagedAttnLaunch {
 fa_status make_tmap_pages(CUtensorMap* map, const void* base, long long page_heads, int page_size, int D, bool fp8,
                           int box_rows);
 
+// 3-D tensor map over rows [rows, heads, D] of BF16: boxes of box_rows rows by
+// `group` heads by 64 columns, 128-byte swizzle.
+fa_status make_tmap_rows_group(CUtensorMap* map, const void* base, int rows, int heads, int D, int group,
+                               int box_rows);
+
 fa_status device_info(int* num_sms);
 
 // Persistent thread blocks of the attention kernels: one per SM, at most this
@@ -88,13 +93,16 @@ fa_status device_info(int* num_sms);
 constexpr int kMaxCtas = 160;
 
 size_t paged_decode_workspace(int D);
+size_t paged_chunk_workspace(int D);
 
 fa_status launch_rope(const RopeParams& p, int num_sms, cudaStream_t stream);
 fa_status launch_cache_write(const CacheParams& p, int num_sms, cudaStream_t stream);
 fa_status launch_cache_read(const CacheParams& p, int num_sms, cudaStream_t stream);
 fa_status launch_paged_decode(const PagedAttnLaunch& L, cudaStream_t stream);
+fa_status launch_paged_chunk(const PagedAttnLaunch& L, cudaStream_t stream);
 
 fa_status cache_take_device_error();
 fa_status paged_decode_take_device_error();
+fa_status paged_chunk_take_device_error();
 
 }  // namespace fa
