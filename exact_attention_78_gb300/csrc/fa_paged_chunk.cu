@@ -12,7 +12,7 @@
 //     memory tiles.  Rows behind the sequence's end hold anything: as keys
 //     they are masked, as values they are cleared before the product, since a
 //     weight of zero would not cancel a NaN.
-//   * E4M3 pages go through a second ring: four warps widen each tile to BF16
+//   * E4M3 pages go through a second ring: eight warps widen each tile to BF16
 //     once per unit, with the rows' power-of-two scales, exactly, so the
 //     products are those of BF16 pages.
 //   * Work.  Whole rounds of units, one per thread block, run in lockstep
@@ -25,9 +25,9 @@
 //
 // Warps: 0-3 and 4-7 softmax of tile 0 and 1 (a thread per row), 8-11
 // correction and epilogue, 12 loads, 13 MMA issue, 14 clearing of values
-// behind the end (BF16 pages), 15 scheduler, 16-19 widening (E4M3 pages).
+// behind the end (BF16 pages), 15 scheduler, 16-23 widening (E4M3 pages).
 // Registers: BF16 256 x 192 + 128 x 80 + 128 x 48 = 65,536 = 512 x 128;
-// E4M3 256 x 160 + 128 x 72 + 128 x 40 + 128 x 48 = 61,440 = 640 x 96.
+// E4M3 256 x 128 + 128 x 72 + 128 x 56 + 256 x 48 = 61,440 = 768 x 80.
 //
 // Tensor memory (512 columns): [0, 128) S of tile 0, its P as BF16 pairs in
 // the first 64; [128, 256) tile 1; [256, 256 + D) O of tile 0; the next D
@@ -44,7 +44,6 @@ __device__ DeviceError g_err;
 
 constexpr int kBM = 128;      // rows of a tile
 constexpr int kBN = 128;      // keys of a block
-constexpr int kEmu = 2;       // exponentials of every 16 on the FMA pipe
 constexpr float kThreshold = 8.0f;   // lazy rescaling, log2 units
 constexpr int kMinStretch = 4;       // blocks
 
@@ -78,14 +77,14 @@ constexpr int kSegs = 4;
 
 template <int D, bool kFp8>
 struct Layout {
-  static constexpr int kThreads = kFp8 ? 640 : 512;
+  static constexpr int kThreads = kFp8 ? 768 : 512;
   static constexpr int kChunks = D / 64;
   static constexpr int kTileBytes = kBM * D * 2;
   static constexpr int kChunkBytes = kBM * 128;
   static constexpr int kStages = D == 128 ? (kFp8 ? 3 : 4) : 6;
   static constexpr int kRawBytes = kBN * D;                  // an E4M3 tile
   static constexpr int kRaws = kFp8 ? 3 : 0;
-  static constexpr int kReaders = kFp8 ? 18 : 15;            // warps that take segments
+  static constexpr int kReaders = kFp8 ? 22 : 15;            // warps that take segments
   static constexpr int kQ = 0;
   static constexpr int kKV = kQ + 2 * kTileBytes;
   static constexpr int kRaw = kKV + kStages * kTileBytes;
@@ -134,6 +133,12 @@ struct Shared {
   FA_DEV volatile Seg* segs() const { return reinterpret_cast<volatile Seg*>(base + L::kSegRing); }
   FA_DEV bool wait(uint32_t b, uint32_t parity, int site, const PagedAttnParams& p) const {
     return mbar_wait_bounded(b, parity, abort(), &g_err, site, p.wait_limit_ns);
+  }
+  // For waits that last: sleeps between looks, off the issue slots.
+  FA_DEV bool wait_long(uint32_t b, uint32_t parity, int site, const PagedAttnParams& p) const {
+#pragma unroll 1
+    for (int i = 0; i < (1 << 23) && !mbar_try_wait(b, parity) && !ld_shared_volatile(abort()); ++i) __nanosleep(200);
+    return wait(b, parity, site, p);
   }
 };
 
@@ -334,6 +339,8 @@ FA_DEV Place find_place(const PagedAttnParams& p, const Line& line, long long t)
 
 // ------------------------------------------------------------------ roles --
 
+FA_DEV int all_same(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // Takes the next segment out of the ring; false at the end of the work or
 // after a give-up.
 template <int D, bool kFp8>
@@ -344,18 +351,23 @@ struct SegReader {
   uint32_t phase = 0;
   FA_DEV SegReader(const Shared<D, kFp8>& s, const PagedAttnParams& q) : sh(s), p(q) {}
   // The whole warp calls it.
-  FA_DEV bool next(Seg& w) {
-    if (!sh.wait(sh.seg_full(i), phase, kSiteSegFull, p)) return false;
+  FA_DEV bool next(Seg& w, bool may_sleep = false) {
+    if (!(may_sleep ? sh.wait_long(sh.seg_full(i), phase, kSiteSegFull, p) : sh.wait(sh.seg_full(i), phase, kSiteSegFull, p)))
+      return false;
     const volatile Seg& r = sh.segs()[i];
-    w.b = r.b;
-    w.head = r.head;
-    w.tok0 = r.tok0;
-    w.kb = r.kb;
-    w.count = r.count;
-    w.n = r.n;
-    w.L = r.L;
-    w.q0 = r.q0;
-    w.slot = r.slot;
+    // a value that comes out of a shuffle is known to be the same in all lanes,
+    // so that what depends on it (loops, ring positions, MMA descriptors) stays
+    // in uniform registers; with plain loads the MMA warp alone took half as
+    // long again
+    w.b = all_same(r.b);
+    w.head = all_same(r.head);
+    w.tok0 = all_same(r.tok0);
+    w.kb = all_same(r.kb);
+    w.count = all_same(r.count);
+    w.n = all_same(r.n);
+    w.L = all_same(r.L);
+    w.q0 = all_same(r.q0);
+    w.slot = all_same(r.slot);
     __syncwarp();
     if (threadIdx.x % 32 == 0) mbar_arrive(sh.seg_empty(i));
     if (++i == kSegs) {
@@ -381,7 +393,7 @@ __device__ void scheduler_role(const Shared<D, kFp8>& sh, const PagedAttnParams&
   int slot_i = 0;
   uint32_t phase = 1;
   auto put = [&](int b, int head, int pair, int kb, int count, const Seq& s, int slot) -> bool {
-    if (!sh.wait(sh.seg_empty(slot_i), phase, kSiteSegEmpty, p)) return false;
+    if (!sh.wait_long(sh.seg_empty(slot_i), phase, kSiteSegEmpty, p)) return false;
     if (lane == 0) {
       volatile Seg& r = sh.segs()[slot_i];
       r.b = b;
@@ -532,12 +544,12 @@ __device__ void clean_role(const Shared<D, false>& sh, const PagedAttnParams& p)
   Seg w;
   uint32_t tiles = 0;      // tiles that went through the ring
   uint32_t parity = 0;     // of each stage's v_landed
-  while (in.next(w)) {
+  while (in.next(w, true)) {
     const int n = max(tile_blocks(w, 0, tt, p.causal), tile_blocks(w, 1, tt, p.causal));
     const int rows = w.L - (w.kb + n - 1) * kBN;
     if (n > 0 && rows < kBN) {
       const int stage = (tiles + 2 * n - 1) % L::kStages;
-      if (!sh.wait(sh.v_landed(stage), (parity >> stage) & 1, kSiteLanded, p)) return;
+      if (!sh.wait_long(sh.v_landed(stage), (parity >> stage) & 1, kSiteLanded, p)) return;
       parity ^= 1u << stage;
       uint8_t* tile = sh.base + L::kKV + stage * L::kTileBytes;
       for (int c = 0; c < L::kChunks; ++c)
@@ -551,62 +563,81 @@ __device__ void clean_role(const Shared<D, false>& sh, const PagedAttnParams& p)
   }
 }
 
-// E4M3 pages: four warps widen each tile, a piece of 16 codes at a time, into
-// the swizzled BF16 tile that the products read.  Rows behind the sequence's
-// end come out as zeros.
+// E4M3 pages: eight warps widen the tiles, four the keys and four the values, a
+// piece of 16 codes at a time, into the swizzled BF16 tiles that the products
+// read.  Rows behind the sequence's end come out as zeros.  (Four warps for
+// both left the MMA warp waiting two thirds of the time: 749 us for a chunk of
+// 512 tokens over 32K keys, 76 heads.)
 template <int D>
 __device__ void widen_role(const Shared<D, true>& sh, const PagedAttnParams& p) {
   using L = Layout<D, true>;
-  constexpr int kPieces = D / 16;                    // of a row
-  constexpr int kRowsPer = 32 / kPieces;             // rows of a warp's step
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32 - 16;
+  // A step is a warp's 32 pieces of 16 codes.  The eight lanes that load and
+  // store together touch all banks: at D = 128 they are four pieces of rows r
+  // and r ^ 5 (the 128-byte swizzle puts the halves of a raw row apart by bit 2
+  // of its number, the even and odd pieces of a BF16 row by bit 0), a step
+  // rows {0, 5, 1, 4} or {2, 7, 3, 6} of eight; at D = 64 two neighbouring rows.
+  constexpr int kSteps = D / 16;
+  constexpr int kGroups = D == 128 ? 1 : 2;          // of eight rows, in two steps
+  constexpr int kDown = 8 * kGroups * D;             // raw bytes
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32 % 4;
   const int tt = tile_tokens(p.group);
-  const int piece = lane % kPieces;
+  int row[2], from[2], to[2][2];                     // in the warp's 32 rows; offsets of the tiles
+#pragma unroll
+  for (int odd = 0; odd < 2; ++odd) {
+    const int piece = D == 128 ? lane & 3 | lane >> 1 & 4 : lane & 3;
+    row[odd] = D == 128 ? (2 * odd + (lane >> 4)) ^ (lane & 4 ? 5 : 0) : 8 * odd + (lane >> 2);
+    const int r = warp * 32 + row[odd];
+    from[odd] = D == 128 ? r * 128 + ((piece ^ (r & 7)) << 4) : r * 64 + ((piece ^ ((r >> 1) & 3)) << 4);
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+      to[odd][s] = (piece / 4) * L::kChunkBytes + r * 128 + (((2 * (piece % 4) + s) ^ (r & 7)) << 4);
+  }
   SegReader<D, true> in(sh, p);
   Seg w;
-  int raw = 0, stage = 0;
-  uint32_t raw_phase = 0, phase = 1;
+  uint32_t at = threadIdx.x / 128 - 4;               // tile in the order of the loads: keys even, values odd
   while (in.next(w)) {
     const int n = max(tile_blocks(w, 0, tt, p.causal), tile_blocks(w, 1, tt, p.causal));
-    for (int j = 0; j < 2 * n; ++j) {
-      const int rows = w.L - (w.kb + j / 2) * kBN;
-      if (!sh.wait(sh.raw_full(raw), raw_phase, kSiteRaw, p)) return;
-      if (!sh.wait(sh.kv_empty(stage), phase, kSiteKvEmpty, p)) return;
+#pragma unroll 1
+    for (int j = 0; j < n; ++j, at += 2) {
+      const int rows = w.L - (w.kb + j) * kBN;
+      const int raw = at % L::kRaws, stage = at % L::kStages;
+      if (!sh.wait(sh.raw_full(raw), (at / L::kRaws) & 1, kSiteRaw, p)) return;
+      if (!sh.wait(sh.kv_empty(stage), (at / L::kStages & 1) ^ 1, kSiteKvEmpty, p)) return;
       const uint8_t* src = sh.base + L::kRaw + raw * L::kRawBytes;
-      const uint8_t* scales = sh.base + L::kRawScale + raw * kBN;
       uint8_t* dst = sh.base + L::kKV + stage * L::kTileBytes;
+      // Lane l holds the factors of row 32 warp + l: 2^(120 + e), which takes
+      // the raw codes' 2^-120 along.  That power does not exist for e > 7: the
+      // rest is a second factor, for the rare tile that needs one.  Rows behind
+      // the end are multiplied by zero (no raw code is a NaN or an infinity).
+      const int mine = warp * 32 + lane;
+      const uint32_t byte = sh.base[L::kRawScale + raw * kBN + mine];
+      const uint32_t first = min(byte, 134u);       // e = 7
+      uint32_t f = mine < rows ? (first + 120u) << 7 : 0u;
+      uint32_t g = byte == 255u ? 0x7FC0u : (byte - first + 127u) << 7;
+      f |= f << 16;
+      g = mine < rows ? g | g << 16 : 0u;
+      const bool big = __any_sync(0xffffffffu, byte > 134u && mine < rows);
 #pragma unroll
-      for (int i = 0; i < 32 / kRowsPer; ++i) {
-        const int r = warp * 32 + i * kRowsPer + lane / kPieces;
-        // the TMA's swizzle of rows of D bytes
-        const int from = D == 128 ? r * 128 + ((piece ^ (r & 7)) << 4) : r * 64 + ((piece ^ ((r >> 1) & 3)) << 4);
-        const uint4 x = *reinterpret_cast<const uint4*>(src + from);
-        const uint32_t byte = scales[r];
-        // 2^(120 + e) does not exist for e > 7: the rest is a second factor
-        const uint32_t first = min(byte, 134u);       // e = 7
-        uint32_t f = (first + 120u) << 7;
-        f |= f << 16;
-        uint32_t g = byte == 255u ? 0x7FC0u : (byte - first + 127u) << 7;
-        g |= g << 16;
-        const bool big = __any_sync(0xffffffffu, byte > 134u);
+      for (int i = 0; i < kSteps; ++i) {
+        // rows of a step repeat every two steps, 8 rows (1024 bytes) further
+        const int odd = i & 1, down = i >> 1;
+        const uint4 x = *reinterpret_cast<const uint4*>(src + from[odd] + down * kDown);
+        const uint32_t fr = __shfl_sync(0xffffffffu, f, row[odd] + down * 8 * kGroups);
         const uint32_t words[4] = {x.x, x.y, x.z, x.w};
         uint32_t y[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           // codes 2 k and 2 k + 1 to the upper bytes of the halves
-          const uint32_t t = __byte_perm(words[k / 2], 0u, k & 1 ? 0x3424 : 0x1404);
-          y[k] = paged::mul_bf16x2(((t >> 4) & 0x07F007F0u) | (t & 0x80008000u), f);
-          if (big) y[k] = paged::mul_bf16x2(y[k], g);
-          if (r >= rows) y[k] = 0u;
+          const uint32_t c = __byte_perm(words[k / 2], 0u, k & 1 ? 0x3424 : 0x1404);
+          y[k] = paged::mul_bf16x2(((c >> 4) & 0x07F007F0u) | (c & 0x80008000u), fr);
         }
-        // 16 columns are two 16-byte pieces of a 64-column chunk's row; lanes
-        // of the second chunk write theirs in the other order, so that the
-        // eight lanes of a row touch all banks
-        uint8_t* to = dst + (piece / 4) * L::kChunkBytes + r * 128;
-        const int q = 2 * (piece % 4), flip = piece / 4;
-        const uint4 a = make_uint4(y[0], y[1], y[2], y[3]), b = make_uint4(y[4], y[5], y[6], y[7]);
-        *reinterpret_cast<uint4*>(to + (((q + flip) ^ (r & 7)) << 4)) = flip ? b : a;
-        *reinterpret_cast<uint4*>(to + (((q + 1 - flip) ^ (r & 7)) << 4)) = flip ? a : b;
+        if (big) {
+          const uint32_t gr = __shfl_sync(0xffffffffu, g, row[odd] + down * 8 * kGroups);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) y[k] = paged::mul_bf16x2(y[k], gr);
+        }
+        *reinterpret_cast<uint4*>(dst + to[odd][0] + down * 1024 * kGroups) = make_uint4(y[0], y[1], y[2], y[3]);
+        *reinterpret_cast<uint4*>(dst + to[odd][1] + down * 1024 * kGroups) = make_uint4(y[4], y[5], y[6], y[7]);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -614,31 +645,74 @@ __device__ void widen_role(const Shared<D, true>& sh, const PagedAttnParams& p) 
         mbar_arrive(sh.kv_full(stage));
         mbar_arrive(sh.raw_empty(raw));
       }
-      if (++raw == L::kRaws) {
-        raw = 0;
-        raw_phase ^= 1;
-      }
-      if (++stage == L::kStages) {
-        stage = 0;
-        phase ^= 1;
-      }
     }
   }
 }
 
-// Maximum that keeps a NaN.
-FA_DEV float max3_nan(float a, float b, float c) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
+// Masks the columns >= lim of a row's scores, in tensor memory: only the blocks
+// at the edge of the mask come here, and a rolled loop over tensor memory costs
+// the others less (in code to fetch) than predicates on 128 registers.
+FA_DEV void mask_scores(uint32_t tm_s, int lim) {
+#pragma unroll 1
+  for (int c = 0; c < kBN; c += 32) {
+    uint32_t x[32];
+    tmem_ld32(tm_s + c, x);
+    tmem_ld_wait();
+    tmem_ld_fence(x);
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (c + i >= lim) x[i] = __float_as_uint(-INFINITY);
+    tmem_st32(tm_s + c, x);
+  }
+  tmem_st_wait();
+}
+FA_DEV float max32(const uint32_t (&x)[32]) {
+  float m = __uint_as_float(x[0]);
+#pragma unroll
+  for (int i = 1; i < 31; i += 2) m = max3(m, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+  return fmaxf(m, __uint_as_float(x[31]));
 }
 
-// Softmax of tile t: one thread per row.  With 192 registers the block's 128
-// scores stay in registers; with 160 (E4M3) they are read from tensor memory
-// a second time for the exponentials.
+// A row's weights and sums, 32 scores at a time.
+struct RowSums {
+  uint64_t scale2, negm2;      // pairs of scale, -maximum
+  uint64_t e2[2], r2[2];       // sums of the FP32 weights (LSE), and of those rounded to BF16, as the product
+                               // takes them (the division); a NaN among the scores passes into both
+  FA_DEV void begin(float scale, float m) {
+    scale2 = pk2(scale, scale);
+    negm2 = pk2(-m, -m);
+    e2[0] = e2[1] = r2[0] = r2[1] = 0ull;
+  }
+  FA_DEV void weights(const uint32_t (&x)[32], uint32_t* pk) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      const uint64_t x2 = fma2(pk2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), scale2, negm2);
+      float x0, x1;
+      up2(x2, x0, x1);
+      const float e0 = ex2_mufu(x0), e1 = ex2_mufu(x1);
+      const uint32_t pp = pack_bf16x2(e0, e1);
+      pk[i / 2] = pp;
+      e2[(i / 2) & 1] = add2(e2[(i / 2) & 1], pk2(e0, e1));
+      r2[(i / 2) & 1] = add2(r2[(i / 2) & 1], pk2(__uint_as_float(pp << 16), __uint_as_float(pp & 0xFFFF0000u)));
+    }
+  }
+  FA_DEV void totals(float& e, float& r) const {
+    float a, b;
+    up2(add2(e2[0], e2[1]), a, b);
+    e = a + b;
+    up2(add2(r2[0], r2[1]), a, b);
+    r = a + b;
+  }
+};
+
+// Softmax of tile t: one thread per row.  The scores are read from tensor memory
+// twice, for the maximum and for the exponentials, 32 columns at a time with
+// the next 32 on their way.  The rolled loops keep the code small: with a
+// block's 128 scores in registers and everything unrolled, the warps of the
+// other roles found their code pushed out of the instruction cache each time
+// (chunk of 512 tokens over 32K keys, 76 heads: 489 us, rolled 446 us).
 template <int D, bool kFp8>
 __device__ void softmax_role(const int t, const Shared<D, kFp8>& sh, const uint32_t tmem, const PagedAttnParams& p) {
-  constexpr bool kKeep = !kFp8;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int wq = warp & 3;
   const int r_in_tile = wq * 32 + lane;
@@ -656,105 +730,75 @@ __device__ void softmax_role(const int t, const Shared<D, kFp8>& sh, const uint3
     const int lim_first = p.causal ? w.L - w.n + tok + 1 : w.L;                  // of the tile's first row
     const int lim_row = p.causal ? min(w.L, lim_first + my_tok) : w.L;
     float m_run = -INFINITY, l_run = 0.0f, lr_run = 0.0f;
+    RowSums sums;
+    // The new running maximum from the block's; returns the factor for what
+    // was summed so far.  Lazy: a maximum that grew by less than the threshold
+    // stays.
+    auto move_max = [&](float m_blk, bool first, bool& rescaled) -> float {
+      rescaled = false;
+      if (first) {
+        m_run = m_blk;
+      } else if (m_blk - m_run > kThreshold) {
+        const float f = ex2_mufu(m_run - m_blk);
+        m_run = m_blk;
+        rescaled = true;
+        return f;
+      }
+      return 1.0f;
+    };
+    // The first half of P is in place: the factor goes along.
+    auto give_lo = [&](float factor, bool rescaled) {
+      sh.st_scale()[t * kBM + r_in_tile] = factor;
+      const unsigned any = __any_sync(0xffffffffu, rescaled);
+      if (lane == 0) sh.warp_flag()[t * 4 + wq] = any ? 1 : 0;
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(sh.p_lo(t));
+    };
     for (int j = 0; j < nt; ++j, ++sit) {
       if (!sh.wait(sh.s_full(t), sit & 1, kSiteS, p)) return;
       tc_fence_after();
       const int kv0 = (w.kb + j) * kBN;
       const bool need_mask = kv0 + kBN > lim_first;
       const int lim = lim_row - kv0;            // columns >= lim are masked
-      uint32_t r[kKeep ? 4 : 1][32];
-      float mx[4];
-      if (kKeep) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(tm_s + c * 32, r[kKeep ? c : 0]);
-        tmem_ld_wait();
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld_fence(r[kKeep ? c : 0]);
-      }
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t(&x)[32] = r[kKeep ? c : 0];
-        if (!kKeep) {
-          tmem_ld32(tm_s + c * 32, x);
-          tmem_ld_wait();
-          tmem_ld_fence(x);
-        }
-        if (need_mask) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (c * 32 + i >= lim) x[i] = __float_as_uint(-INFINITY);
-        }
-        float m = __uint_as_float(x[0]);
-#pragma unroll
-        for (int i = 1; i < 31; i += 2) m = max3_nan(m, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-        mx[c] = max3_nan(m, __uint_as_float(x[31]), -INFINITY);
-      }
-      float m_blk = max3_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3], -INFINITY) * sl2;
-      // a NaN or +inf among the scores makes the row's sums NaN, whichever
-      // unit its exponential would go through
-      const bool lost = !(m_blk < INFINITY);
-      if (lost) m_blk = -INFINITY;
-      float factor = 1.0f;
-      bool rescaled = false;
-      if (j == 0) {
-        m_run = m_blk;
-      } else if (m_blk - m_run > kThreshold) {
-        factor = ex2_mufu(m_run - m_blk);
-        m_run = m_blk;
-        rescaled = true;
-      }
-      const float m_use = (m_run == -INFINITY) ? 0.0f : m_run;
-      const uint64_t sl2x2 = pk2(sl2, sl2), negm2 = pk2(-m_use, -m_use);
-      // sums of the FP32 weights (LSE) and of the weights rounded to BF16, as
-      // the product takes them (the division)
-      uint64_t se2[2] = {0ull, 0ull}, sr2[2] = {0ull, 0ull};
-#pragma unroll
+      bool rescaled;
+      float factor, m_blk, e, r;
+      if (need_mask) mask_scores(tm_s, lim);
+      uint32_t xa[32], xb[32], pk[16];
+      m_blk = -INFINITY;
+      tmem_ld32(tm_s, xa);
+#pragma unroll 1
       for (int half = 0; half < 2; ++half) {
-        uint32_t pk[32];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int ch = 2 * half + q;
-          uint32_t(&x)[32] = r[kKeep ? ch : 0];
-          if (!kKeep) {
-            tmem_ld32(tm_s + ch * 32, x);
-            tmem_ld_wait();
-            tmem_ld_fence(x);
-            if (need_mask) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (ch * 32 + i >= lim) x[i] = __float_as_uint(-INFINITY);
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const uint64_t x2 = fma2(pk2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), sl2x2, negm2);
-            float x0, x1, e0, e1;
-            up2(x2, x0, x1);
-            exp2_pair<kEmu>(x0, x1, i, e0, e1);
-            const uint32_t pp = pack_bf16x2(e0, e1);
-            pk[q * 16 + i / 2] = pp;
-            se2[(i / 2) & 1] = add2(se2[(i / 2) & 1], pk2(e0, e1));
-            sr2[(i / 2) & 1] = add2(sr2[(i / 2) & 1], pk2(__uint_as_float(pp << 16), __uint_as_float(pp & 0xFFFF0000u)));
-          }
-        }
-        // P lies over the first 64 columns of S: with the scores re-read, the
-        // second half's (columns 64-127) are still untouched
-        tmem_st32(tm_s + 32 * half, pk);
-        if (half == 0) {
-          sh.st_scale()[t * kBM + r_in_tile] = factor;
-          const unsigned any = __any_sync(0xffffffffu, rescaled);
-          if (lane == 0) sh.warp_flag()[t * 4 + wq] = any ? 1 : 0;
-          tmem_st_wait();
-          tc_fence_before();
-          mbar_arrive(sh.p_lo(t));
-        }
+        tmem_ld_wait();
+        tmem_ld_fence(xa);
+        tmem_ld32(tm_s + 64 * half + 32, xb);
+        m_blk = fmaxf(m_blk, max32(xa));
+        tmem_ld_wait();
+        tmem_ld_fence(xb);
+        tmem_ld32(tm_s + (half ? 0 : 64), xa);       // at the end: the first columns again
+        m_blk = fmaxf(m_blk, max32(xb));
       }
-      float a0, a1, b0, b1;
-      up2(add2(se2[0], se2[1]), a0, a1);
-      up2(add2(sr2[0], sr2[1]), b0, b1);
-      l_run = l_run * factor + (a0 + a1);
-      lr_run = lr_run * factor + (b0 + b1);
-      if (lost) l_run = lr_run = __int_as_float(0x7FC00000);
+      m_blk *= sl2;
+      factor = move_max(m_blk, j == 0, rescaled);
+      sums.begin(sl2, m_run == -INFINITY ? 0.0f : m_run);
+      // P goes over columns of S whose scores have been read
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        tmem_ld_wait();
+        tmem_ld_fence(xa);
+        tmem_ld32(tm_s + 64 * half + 32, xb);
+        sums.weights(xa, pk);
+        tmem_st16(tm_s + 32 * half, pk);
+        tmem_ld_wait();
+        tmem_ld_fence(xb);
+        if (half == 0) tmem_ld32(tm_s + 64, xa);
+        sums.weights(xb, pk);
+        tmem_st16(tm_s + 32 * half + 16, pk);
+        if (half == 0) give_lo(factor, rescaled);
+      }
+      sums.totals(e, r);
+      l_run = l_run * factor + e;
+      lr_run = lr_run * factor + r;
       tmem_st_wait();
       if (j == nt - 1) {
         sh.st_l()[t * kBM + r_in_tile] = l_run;
@@ -780,17 +824,18 @@ __device__ void correction_role(const Shared<D, kFp8>& sh, const uint32_t tmem, 
   const int my_tok = r_in_tile / p.group, my_head = r_in_tile - my_tok * p.group;
   SegReader<D, kFp8> in(sh, p);
   Seg w;
-  uint32_t sit[2] = {0u, 0u}, uit[2] = {0u, 0u};
+  uint32_t sit = 0;      // phase bits of the two tiles
+  uint32_t uit[2] = {0u, 0u};
   while (in.next(w)) {
     const int nts[2] = {tile_blocks(w, 0, tt, p.causal), tile_blocks(w, 1, tt, p.causal)};
     const int n = max(nts[0], nts[1]);
     float fin_l[2] = {0.0f, 0.0f}, fin_lr[2] = {0.0f, 0.0f}, fin_m[2] = {-INFINITY, -INFINITY};
     for (int j = 0; j < n; ++j) {
-#pragma unroll
+#pragma unroll 1
       for (int t = 0; t < 2; ++t) {
-        if (j >= nts[t]) continue;
-        const uint32_t ph = sit[t] & 1;
-        ++sit[t];
+        if (j >= (t ? nts[1] : nts[0])) continue;
+        const uint32_t ph = (sit >> t) & 1;
+        sit ^= 1u << t;
         if (!sh.wait(sh.p_lo(t), ph, kSiteP, p)) return;
         tc_fence_after();
         if (j > 0 && sh.warp_flag()[t * 4 + wq]) {
@@ -817,11 +862,13 @@ __device__ void correction_role(const Shared<D, kFp8>& sh, const uint32_t tmem, 
         // the statistics come with the second half of the last block's P; they
         // are taken before O is released, after which the next segment's
         // softmax may overwrite them
-        if (j == nts[t] - 1) {
+        if (j == (t ? nts[1] : nts[0]) - 1) {
           if (!sh.wait(sh.p_hi(t), ph, kSiteP, p)) return;
-          fin_l[t] = sh.st_l()[t * kBM + r_in_tile];
-          fin_lr[t] = sh.st_lr()[t * kBM + r_in_tile];
-          fin_m[t] = sh.st_m()[t * kBM + r_in_tile];
+          const float a = sh.st_l()[t * kBM + r_in_tile], b = sh.st_lr()[t * kBM + r_in_tile];
+          const float c = sh.st_m()[t * kBM + r_in_tile];
+          (t ? fin_l[1] : fin_l[0]) = a;
+          (t ? fin_lr[1] : fin_lr[0]) = b;
+          (t ? fin_m[1] : fin_m[0]) = c;
         }
         tc_fence_before();
         mbar_arrive(sh.o_ready(t));
@@ -881,28 +928,54 @@ __device__ void correction_role(const Shared<D, kFp8>& sh, const uint32_t tmem, 
   }
 }
 
-// K steps of S = Q K^T, 16 wide: step kk reads 64-element chunk kk / 4 at byte
-// offset 32 (kk % 4) of its rows.
-template <int D, int CHUNK, int KK>
-FA_DEV void s_steps(uint32_t d_tmem, uint32_t alo, uint32_t ahi, uint32_t blo, uint32_t bhi, uint32_t idesc) {
-  if constexpr (KK < D / 16) {
-    constexpr uint32_t off = ((KK >> 2) * CHUNK + (KK & 3) * 32) >> 4;
-    mma_ss_w<off, off>(d_tmem, alo, ahi, blo, bhi, idesc, KK > 0 ? 1u : 0u);
-    s_steps<D, CHUNK, KK + 1>(d_tmem, alo, ahi, blo, bhi, idesc);
-  }
+// Four MMAs in one piece of PTX, issued by one elected lane of the (converged)
+// warp: one election instead of four, and only the operands' base words live
+// across it.  Offsets are in units of 16 bytes (descriptors) or TMEM columns.
+// The first MMA accumulates if acc != 0, the others always do.
+// D[tmem] (+)= A[smem] B[smem]: steps k at offset + 2 k in both operands.
+template <uint32_t OFF>
+FA_DEV void mma4_ss(uint32_t d, uint32_t alo, uint32_t ahi, uint32_t blo, uint32_t bhi, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred e, p;\n\t.reg .b32 al, bl;\n\t.reg .b64 ad, bd;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "add.u32 al, %1, %7;\n\tadd.u32 bl, %3, %7;\n\tmov.b64 ad, {al, %2};\n\tmov.b64 bd, {bl, %4};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %5, p;\n\t"
+      "add.u32 al, %1, %7 + 2;\n\tadd.u32 bl, %3, %7 + 2;\n\tmov.b64 ad, {al, %2};\n\tmov.b64 bd, {bl, %4};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %5, 1;\n\t"
+      "add.u32 al, %1, %7 + 4;\n\tadd.u32 bl, %3, %7 + 4;\n\tmov.b64 ad, {al, %2};\n\tmov.b64 bd, {bl, %4};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %5, 1;\n\t"
+      "add.u32 al, %1, %7 + 6;\n\tadd.u32 bl, %3, %7 + 6;\n\tmov.b64 ad, {al, %2};\n\tmov.b64 bd, {bl, %4};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %5, 1;\n\t}\n" ::"r"(d),
+      "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc), "r"(acc), "n"(OFF)
+      : "memory");
 }
-// K steps of O += P V: TMEM columns 8 kk.. of P, key rows 16 kk.. of V.
-template <int KK, int KEND>
-FA_DEV void pv_steps(uint32_t d_tmem, uint32_t a_tmem, uint32_t blo, uint32_t bhi, uint32_t idesc, uint32_t acc) {
-  if constexpr (KK < KEND) {
-    mma_ts_w<KK * 8, KK * 128>(d_tmem, a_tmem, blo, bhi, idesc, KK > 0 ? 1u : acc);
-    pv_steps<KK + 1, KEND>(d_tmem, a_tmem, blo, bhi, idesc, acc);
-  }
+// D[tmem] (+)= A[tmem] B[smem]: A at 8 columns, B at 128 units per step.
+template <uint32_t FIRST>
+FA_DEV void mma4_ts(uint32_t d, uint32_t a, uint32_t blo, uint32_t bhi, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred e, p;\n\t.reg .b32 at, bl;\n\t.reg .b64 bd;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "add.u32 at, %1, %6 * 8;\n\tadd.u32 bl, %2, %6 * 128;\n\tmov.b64 bd, {bl, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [at], bd, %4, p;\n\t"
+      "add.u32 at, %1, %6 * 8 + 8;\n\tadd.u32 bl, %2, %6 * 128 + 128;\n\tmov.b64 bd, {bl, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [at], bd, %4, 1;\n\t"
+      "add.u32 at, %1, %6 * 8 + 16;\n\tadd.u32 bl, %2, %6 * 128 + 256;\n\tmov.b64 bd, {bl, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [at], bd, %4, 1;\n\t"
+      "add.u32 at, %1, %6 * 8 + 24;\n\tadd.u32 bl, %2, %6 * 128 + 384;\n\tmov.b64 bd, {bl, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [at], bd, %4, 1;\n\t}\n" ::"r"(d),
+      "r"(a), "r"(blo), "r"(bhi), "r"(idesc), "r"(acc), "n"(FIRST)
+      : "memory");
 }
 
 // MMA issue (a converged warp, one elected lane): S of both tiles for the first
 // block, then per block and tile PV(j), S(j + 1).  S(j + 1) overwrites the
 // columns of P(j) only after PV(j) was issued; MMAs of one thread run in order.
+// One copy of each product's code serves both tiles and the first block: this
+// warp comes by once in some thousand cycles, in between the softmax warps'
+// long code has pushed its own out of the instruction cache, and with six
+// unrolled copies fetching it took longer than the products.
 template <int D, bool kFp8>
 __device__ void mma_role(const Shared<D, kFp8>& sh, const uint32_t tmem, const PagedAttnParams& p) {
   using L = Layout<D, kFp8>;
@@ -910,20 +983,27 @@ __device__ void mma_role(const Shared<D, kFp8>& sh, const uint32_t tmem, const P
   constexpr uint32_t kIdPV = idesc_bf16_f32(kBM, D, false, true);
   const int tt = tile_tokens(p.group);
   uint32_t uit = 0;
-  uint32_t sit[2] = {0u, 0u};
+  uint32_t sit = 0;      // phase bits of the two tiles
   int stage = 0;
   uint32_t phase = 0;
+  // S_t = Q_t K^T in K steps of 16: step k reads 64-element chunk k / 4 at byte
+  // offset 32 (k % 4) of its rows.
   auto issue_s = [&](int t, int st) {
     const uint64_t da = sdesc_sw128(sh.sbase + L::kQ + t * L::kTileBytes, 16, 1024);
     const uint64_t db = sdesc_sw128(sh.sbase + L::kKV + st * L::kTileBytes, 16, 1024);
-    s_steps<D, L::kChunkBytes, 0>(tmem + t * kBN, desc_lo(da), desc_hi(da), desc_lo(db), desc_hi(db), kIdS);
+    mma4_ss<0>(tmem + t * kBN, desc_lo(da), desc_hi(da), desc_lo(db), desc_hi(db), kIdS, 0u);
+    if (D == 128)
+      mma4_ss<L::kChunkBytes / 16>(tmem + t * kBN, desc_lo(da), desc_hi(da), desc_lo(db), desc_hi(db), kIdS, 1u);
+    mma_commit_w(sh.s_full(t));
   };
+  // O_t (+)= P_t V in K steps of 16 keys: TMEM columns 8 k.. of P, key rows
+  // 16 k.. (2048 bytes further) of V.
   auto issue_pv = [&](int t, int st, bool acc, uint32_t ph) -> bool {
     const uint64_t db = sdesc_sw128(sh.sbase + L::kKV + st * L::kTileBytes, L::kChunkBytes, 1024);
-    pv_steps<0, 4>(tmem + 256 + t * D, tmem + t * kBN, desc_lo(db), desc_hi(db), kIdPV, acc ? 1u : 0u);
+    mma4_ts<0>(tmem + 256 + t * D, tmem + t * kBN, desc_lo(db), desc_hi(db), kIdPV, acc ? 1u : 0u);
     if (!sh.wait(sh.p_hi(t), ph, kSiteP, p)) return false;
     tc_fence_after();
-    pv_steps<4, 8>(tmem + 256 + t * D, tmem + t * kBN, desc_lo(db), desc_hi(db), kIdPV, 1u);
+    mma4_ts<4>(tmem + 256 + t * D, tmem + t * kBN, desc_lo(db), desc_hi(db), kIdPV, 1u);
     return true;
   };
   struct Pos {
@@ -951,54 +1031,38 @@ __device__ void mma_role(const Shared<D, kFp8>& sh, const uint32_t tmem, const P
     if (n == 0) continue;
     if (!sh.wait(sh.q_full(), uit & 1, kSiteQFull, p)) return;
     tc_fence_after();
-    Pos kp = take();
+    Pos kp = take(), vp{0, 0u};
     if (!ready(kp)) return;
-    if (n0 > 0) {
-      issue_s(0, kp.stage);
-      mma_commit_w(sh.s_full(0));
-    }
-    if (n1 > 0) {
-      issue_s(1, kp.stage);
-      mma_commit_w(sh.s_full(1));
-    }
-    mma_commit_w(sh.kv_empty(kp.stage));
-    if (n == 1) mma_commit_w(sh.q_empty());
-    for (int j = 0; j < n; ++j) {
-      const Pos vp = take();
-      if (!ready(vp)) return;
+#pragma unroll 1
+    for (int j = -1; j < n; ++j) {
       const bool more = j + 1 < n;
-      bool k_ready = false;
-      if (more) kp = take();
-      if (j < n0) {
-        const uint32_t ph = sit[0] & 1;
-        ++sit[0];
-        if (!sh.wait(sh.o_ready(0), ph, kSiteO, p)) return;
-        tc_fence_after();
-        if (!issue_pv(0, vp.stage, j > 0, ph)) return;
-        if (j + 1 < n0) {
-          if (!ready(kp)) return;
-          k_ready = true;
-          issue_s(0, kp.stage);
-          mma_commit_w(sh.s_full(0));
-        } else {
-          mma_commit_w(sh.o_full(0));
+      bool k_ready = j < 0;
+      if (j >= 0) {
+        vp = take();
+        if (!ready(vp)) return;
+        if (more) kp = take();
+      }
+#pragma unroll 1
+      for (int t = 0; t < 2; ++t) {
+        const int nt = t ? n1 : n0;
+        if (j >= nt) continue;
+        if (j >= 0) {
+          const uint32_t ph = (sit >> t) & 1;
+          sit ^= 1u << t;
+          if (!sh.wait(sh.o_ready(t), ph, kSiteO, p)) return;
+          tc_fence_after();
+          if (!issue_pv(t, vp.stage, j > 0, ph)) return;
+          if (t == 1 || j >= n1) mma_commit_w(sh.kv_empty(vp.stage));
         }
-      }
-      if (j < n1) {
-        const uint32_t ph = sit[1] & 1;
-        ++sit[1];
-        if (!sh.wait(sh.o_ready(1), ph, kSiteO, p)) return;
-        tc_fence_after();
-        if (!issue_pv(1, vp.stage, j > 0, ph)) return;
-        if (j + 1 == n1) mma_commit_w(sh.o_full(1));
-      }
-      mma_commit_w(sh.kv_empty(vp.stage));
-      if (more) {
-        if (j + 1 < n1) {
+        if (j + 1 < nt) {
           if (!k_ready && !ready(kp)) return;
-          issue_s(1, kp.stage);
-          mma_commit_w(sh.s_full(1));
+          k_ready = true;
+          issue_s(t, kp.stage);
+        } else if (j >= 0) {
+          mma_commit_w(sh.o_full(t));
         }
+      }
+      if (more) {
         mma_commit_w(sh.kv_empty(kp.stage));
         if (j + 1 == n - 1) mma_commit_w(sh.q_empty());
       }
@@ -1061,13 +1125,13 @@ __global__ void __launch_bounds__(Layout<D, kFp8>::kThreads, 1)
   const uint32_t tmem = *sh.tmem_slot();
 
   if (warp < 8) {
-    reg_alloc<kFp8 ? 160 : 192>();
+    reg_alloc<kFp8 ? 128 : 192>();
     softmax_role<D, kFp8>(warp / 4, sh, tmem, p);
   } else if (warp < 12) {
     reg_dealloc<kFp8 ? 72 : 80>();
     correction_role<D, kFp8>(sh, tmem, p);
   } else if (warp < 16) {
-    reg_dealloc<kFp8 ? 40 : 48>();
+    reg_dealloc<kFp8 ? 56 : 48>();
     if (warp == 12) {
       load_role<D, kFp8>(sh, &tm_q, &tm_k, &tm_v, p);
     } else if (warp == 13) {
@@ -1106,6 +1170,8 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const PagedAttnPa
   __shared__ long long bpre[kMaxPackedSeqs + 1];
   __shared__ int upre[kMaxPackedSeqs + 1];
   __shared__ long long sums[2 * kJoinThreads / 32];
+  __shared__ float fac[kMaxCtas + 1][kJoinRows];
+  __shared__ float inv[kJoinRows];
   const Line line = build_line(p, bpre, upre, sums, ctas);
   // before any exit, so that this grid ends after the main one
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1116,40 +1182,71 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const PagedAttnPa
   if (w.start == t || prev > w.start) return;      // no cut here, or not the unit's first
   const Seq s = seq_of(p, w.b);
   const int pair = s.pairs - 1 - w.i;
+  if (pair * s.t2 + blockIdx.y * kJoinRows / kBM * tile_tokens(p.group) >= s.n) return;   // a tile without a token
   const long long end = w.start + s.blocks(pair);
   const int first = 2 * (c - 1) + (prev == w.start ? 0 : 1);
   int last = c;                                     // parts: slot `first`, then slots 2 c .. 2 last
   while (last + 1 < line.G && line.stretch(last + 1) < end) ++last;
+  // The parts' factors, one row a lane: 2^(maximum - the row's largest).
+  const int parts = last - c + 2;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  auto slot_of = [&](int k) { return k == 0 ? first : 2 * (c + k - 1); };
+  const int row0 = blockIdx.y * kJoinRows;
   const int tt = tile_tokens(p.group);
-  for (int i = threadIdx.x; i < kJoinRows * (D / 4); i += kJoinThreads) {
-    const int r = blockIdx.y * kJoinRows + i / (D / 4), d = i % (D / 4) * 4;
-    const int in_tile = r % kBM, tk = in_tile / p.group;
-    const int tok = pair * s.t2 + r / kBM * tt + tk;
-    if (tk >= tt || tok >= s.n) continue;
-    float mt = Part<D>::stat(p.part, first)[r * Part<D>::kStat];
-    for (int k = c; k <= last; ++k) mt = fmaxf(mt, Part<D>::stat(p.part, 2 * k)[r * Part<D>::kStat]);
-    float lt = 0.0f, lrt = 0.0f;
-    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int k = c - 1; k <= last; ++k) {
-      const int slot = k < c ? first : 2 * k;
-      const float* stat = Part<D>::stat(p.part, slot) + r * Part<D>::kStat;
-      const float f = mt == -INFINITY ? 1.0f : ex2_mufu(stat[0] - mt);
-      lt += stat[1] * f;
-      lrt += stat[2] * f;
-      const float4 x = *reinterpret_cast<const float4*>(Part<D>::out(p.part, slot) + r * D + d);
-      y.x += x.x * f;
-      y.y += x.y * f;
-      y.z += x.z * f;
-      y.w += x.w * f;
+  if (warp == 0) {
+    auto stat_of = [&](int k) {
+      return *reinterpret_cast<const float4*>(Part<D>::stat(p.part, slot_of(k)) + (row0 + lane) * Part<D>::kStat);
+    };
+    float mt = -INFINITY, lt = 0.0f, lrt = 0.0f;
+#pragma unroll 4
+    for (int k = 0; k < parts; ++k) mt = fmaxf(mt, stat_of(k).x);
+#pragma unroll 4
+    for (int k = 0; k < parts; ++k) {
+      const float4 st = stat_of(k);
+      const float f = mt == -INFINITY ? 1.0f : ex2_mufu(st.x - mt);
+      fac[k][lane] = f;
+      lt += st.y * f;
+      lrt += st.z * f;
     }
-    const float inv = lrt == 0.0f ? 0.0f : 1.0f / lrt;
-    const int head = w.head * p.group + in_tile - tk * p.group;
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + ((size_t)(s.q0 + tok) * p.Hq + head) * D + d) =
-        make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
-    if (d == 0) {
+    inv[lane] = lrt == 0.0f ? 0.0f : 1.0f / lrt;
+    const int in_tile = (row0 + lane) % kBM, tk = in_tile / p.group;
+    const int tok = pair * s.t2 + row0 / kBM * tt + tk;
+    if (tk < tt && tok < s.n) {
+      const int head = w.head * p.group + in_tile - tk * p.group;
       const size_t li = p.s.cu ? (size_t)head * p.s.Sn + s.q0 + tok : ((size_t)w.b * p.Hq + head) * p.s.Sn + tok;
       p.lse[li] = lt == 0.0f ? -INFINITY : (mt + log2f(lt)) * 0.693147180559945309f;
     }
+  }
+  __syncthreads();
+  constexpr int kEach = kJoinRows * (D / 4) / kJoinThreads;      // pieces of 4 columns per thread
+  float4 y[kEach];
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) y[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
+  for (int k = 0; k < parts; ++k) {
+    const float4* from = reinterpret_cast<const float4*>(Part<D>::out(p.part, slot_of(k)) + row0 * D);
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int i = threadIdx.x + e * kJoinThreads;
+      const float f = fac[k][i / (D / 4)];
+      const float4 x = from[i];
+      // (rows that no part wrote hold anything, and are not stored)
+      y[e].x += x.x * f;
+      y[e].y += x.y * f;
+      y[e].z += x.z * f;
+      y[e].w += x.w * f;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const int i = threadIdx.x + e * kJoinThreads;
+    const int r = i / (D / 4), d = i % (D / 4) * 4;
+    const int in_tile = (row0 + r) % kBM, tk = in_tile / p.group;
+    const int tok = pair * s.t2 + row0 / kBM * tt + tk;
+    if (tk >= tt || tok >= s.n) continue;
+    const int head = w.head * p.group + in_tile - tk * p.group;
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + ((size_t)(s.q0 + tok) * p.Hq + head) * D + d) =
+        make_uint2(pack_bf16x2(y[e].x * inv[r], y[e].y * inv[r]), pack_bf16x2(y[e].z * inv[r], y[e].w * inv[r]));
   }
 }
 
