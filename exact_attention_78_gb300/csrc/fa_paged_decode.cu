@@ -20,9 +20,12 @@
 //     stretch with a ring of its own in shared memory, which its lane 0 fills
 //     by TMA (the pages' rows, swizzled for ldmatrix); no warp waits for
 //     another until the unit's end, where the 8 softmax states are merged.
-//   * E4M3 pages are widened in registers on the way to the tensor cores; the
-//     rows' power-of-two scales go to the scores (keys) and to the weights
-//     (values), both exactly.
+//   * E4M3 pages are widened in registers on the way to the tensor cores, to
+//     FP16, which holds every code and which one instruction makes of a pair (to
+//     BF16 it takes five).  The queries become FP16 by a power of two of each
+//     row's own, which loses nothing of note: a row's largest value is below 2^14
+//     then, and what lies below 2^-38 of it is rounded.  The keys' scales go to
+//     the scores in FP32, the values' to the weights.
 #include <cuda_runtime.h>
 
 #include "paged.cuh"
@@ -36,7 +39,10 @@ __device__ DeviceError g_err;
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRows = 16;     // rows of a tile
-constexpr int kKeys = 16;     // keys of a block: one page or a part of one
+// Keys of a block, at most two pages: stages of 8 KB of keys and values keep
+// enough bytes in flight with few stages; E4M3 at D = 64 has stages of 4 KB.
+template <int D, bool kFp8>
+constexpr int keys_of() { return D == 128 && !kFp8 ? 16 : 32; }
 
 enum Site { kSiteSeqs = 1, kSitePage, kSiteRing };
 
@@ -55,14 +61,16 @@ struct Part {
 
 template <int D, bool kFp8>
 struct Layout {
+  static constexpr int kKeys = keys_of<D, kFp8>();
   static constexpr int kTile = kKeys * D * (kFp8 ? 1 : 2);        // keys or values of a block
   static constexpr int kStage = 2 * kTile;
   static constexpr int kStages = kStage >= 8192 ? 3 : kStage >= 4096 ? 5 : 8;
   static constexpr int kPitch = D + 8;                            // floats of a merge row
   static constexpr int kMergeRows = 32;                           // rows of all merge slots
   static constexpr int kRing = 0;
-  static constexpr int kScales = kRing + kWarps * kStages * kStage;   // E4M3: 16 + 16 scale bytes a stage
-  static constexpr int kMerge = kScales + (kFp8 ? kWarps * kStages * 2 * kKeys : 0);
+  static constexpr int kScales = kRing + kWarps * kStages * kStage;   // E4M3: scale bytes of a stage's keys, values
+  static constexpr int kFactors = kScales + (kFp8 ? kWarps * kStages * 2 * kKeys : 0);   // a block's, as floats
+  static constexpr int kMerge = kFactors + (kFp8 ? kWarps * 2 * kKeys * 4 : 0);
   static constexpr int kStats = kMerge + kMergeRows * kPitch * 4;     // m, l, lr of [warp][row]
   static constexpr int kPre = kStats + 3 * kWarps * kRows * 4;        // prefix of blocks, [B + 1]
   static constexpr int kBars = kPre + (kMaxPackedSeqs + 1) * 8 + 8;
@@ -90,11 +98,11 @@ FA_DEV Seq seq_of(const PagedSeqs& s, int b) {
 }
 FA_DEV int tiles_of(int n, int group) { return (n * group + kRows - 1) / kRows; }
 // Blocks of a unit: at least one, so that rows without a key are written too.
-FA_DEV int blocks_of(int L) { return max(1, (L + kKeys - 1) / kKeys); }
+FA_DEV int blocks_of(int L, int keys) { return max(1, (L + keys - 1) / keys); }
 
 // Prefix sums of the sequences' blocks into pre[0 .. B]; returns their total,
 // 0 when the sequences break the rules.  All threads of the block.
-template <int kN>
+template <int kN, int kKeys>
 FA_DEV long long build_line(const PagedAttnParams& p, long long* pre, long long* warp_sums) {
   const bool ok = paged::sequences_ok(p.s, p.max_q);
   if (!ok) {
@@ -110,7 +118,7 @@ FA_DEV long long build_line(const PagedAttnParams& p, long long* pre, long long*
     v[i] = 0;
     if (b < p.s.B) {
       const Seq q = seq_of(p.s, b);
-      if (q.n > 0) v[i] = (long long)p.s.Hkv * tiles_of(q.n, p.group) * blocks_of(q.L);
+      if (q.n > 0) v[i] = (long long)p.s.Hkv * tiles_of(q.n, p.group) * blocks_of(q.L, kKeys);
     }
     sum += v[i];
   }
@@ -144,6 +152,7 @@ FA_DEV int active_ctas(long long total, int ctas) {
 FA_DEV long long stretch(long long total, int c, int G) { return total * c / G; }
 
 // A walk over the segments (the stretch's share of one unit) of [t0, t1).
+template <int kKeys>
 struct Walk {
   int b, head, tile, tiles;
   Seq s;
@@ -154,7 +163,7 @@ struct Walk {
   FA_DEV void load(const PagedAttnParams& p) {
     s = seq_of(p.s, b);
     tiles = tiles_of(s.n, p.group);
-    nblk = blocks_of(s.L);
+    nblk = blocks_of(s.L, kKeys);
   }
   FA_DEV void begin(const PagedAttnParams& p, const long long* pre, long long t0, long long t1) {
     int lo = 0, hi = p.s.B - 1;      // last b with pre[b] <= t0
@@ -222,12 +231,31 @@ FA_DEV void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+FA_DEV void mma16816_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two E4M3 codes (the lower half of w) as FP16, exactly.
+FA_DEV uint32_t e4m3_f16x2(uint32_t w) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)w));
+  return r;
+}
+FA_DEV uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 // Shared-memory address of 16-byte piece `c` of row `r` of a tile at `base`.
 // BF16: 64-column chunks of 128-byte rows, 128-byte swizzle.  E4M3: rows of D
 // bytes, swizzled by their width.
 template <int D, bool kFp8>
 FA_DEV uint32_t piece(uint32_t base, int r, int c) {
-  if (!kFp8) return base + (c >> 3) * (kKeys * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+  if (!kFp8) return base + (c >> 3) * (Layout<D, kFp8>::kKeys * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
   if (D == 128) return base + r * 128 + ((c ^ (r & 7)) << 4);
   return base + r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
 }
@@ -239,6 +267,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const PagedAttnParams p) {
   using L = Layout<D, kFp8>;
+  constexpr int kKeys = L::kKeys;
+  constexpr int kGroups = kKeys / 16;
   constexpr int kSteps = D / 16;      // 16-wide steps along D
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -262,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
-  const long long total = build_line<kThreads>(p, pre, reinterpret_cast<long long*>(merge));
+  const long long total = build_line<kThreads, kKeys>(p, pre, reinterpret_cast<long long*>(merge));
   __syncthreads();
   const int G = active_ctas(total, gridDim.x);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -270,12 +300,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const long long t0 = stretch(total, blockIdx.x, G), t1 = stretch(total, blockIdx.x + 1, G);
 
   // The walk that issues loads runs ahead of the one that consumes them.
-  Walk in, at;
+  Walk<kKeys> in, at;
   in.begin(p, pre, t0, t1);
   at = in;
   int in_i = warp, in_vis = in.visible(p);       // next block of this warp in the segment
-  int in_page = 0, in_page_i = -1;               // page numbers, one per lane, of the warp's next 32 blocks
+  int in_page = 0, in_page_i = -1;               // page numbers, one per lane, of the warp's next blocks
   int in_stage = 0;
+  const int box_shift = min(p.s.page_shift, kKeys == 32 ? 5 : 4);    // rows of a box; one or two boxes a block
+  const int two = kKeys >> box_shift == 2 ? 1 : 0;
   // Issues the warp's next block, if there is one.  The whole warp calls it.
   auto issue = [&]() {
     while (in_i >= in_vis) {
@@ -291,33 +323,40 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (in_vis == 0x7fffffff) return;
     const int k = in_i / kWarps;                 // the warp's k-th block of the segment
-    if (in_page_i < 0 || k - in_page_i >= 32) {
+    if (in_page_i < 0 || k - in_page_i >= 32 >> two) {
       in_page_i = k;
-      const int i = in_i + lane * kWarps;
-      in_page = -1;
-      if (i < in_vis) {
-        in_page = p.s.block_table[(size_t)in.b * p.s.max_pages + (((in.kb + i) * kKeys) >> p.s.page_shift)];
+      const int i = in_i + (lane >> two) * kWarps;
+      const int key = (in.kb + i) * kKeys + ((lane & two) << box_shift);
+      in_page = -1;                              // outside the tensor maps: reads as zeros
+      if (i < in_vis && key < in.s.L) {
+        in_page = p.s.block_table[(size_t)in.b * p.s.max_pages + (key >> p.s.page_shift)];
         if (in_page < 0 || in_page >= p.s.num_pages) {
           paged::record_bad_input(&g_err, kSitePage);
-          in_page = -1;                          // outside the tensor maps: reads as zeros
+          in_page = -1;
         }
       }
     }
-    const int page = __shfl_sync(0xffffffffu, in_page, k - in_page_i);
+    const int from = (k - in_page_i) << two;
+    const int page0 = __shfl_sync(0xffffffffu, in_page, from), page1 = __shfl_sync(0xffffffffu, in_page, from + two);
     if (lane == 0) {
-      const int off = ((in.kb + in_i) * kKeys) & ((1 << p.s.page_shift) - 1);
-      const int ph = page < 0 ? -1 : page * p.s.Hkv + in.head;
-      const uint32_t dst = ring + in_stage * L::kStage, bar = bars + 8 * in_stage;
+      const uint32_t bar = bars + 8 * in_stage;
       mbar_arrive_expect_tx(bar, 2 * L::kTile + (kFp8 ? 2 * kKeys : 0));
+      for (int j = 0; j <= two; ++j) {
+        const int off = ((in.kb + in_i) * kKeys + (j << box_shift)) & ((1 << p.s.page_shift) - 1);
+        const int page = j ? page1 : page0;
+        const int ph = page < 0 ? -1 : page * p.s.Hkv + in.head;
+        const uint32_t dst = ring + in_stage * L::kStage + (j << box_shift) * (kFp8 ? D : 128);
 #pragma unroll
-      for (int h = 0; h < (kFp8 ? 1 : D / 64); ++h) {
-        tma_load_3d(dst + h * kKeys * 128, &tm_k, bar, h * 64, off, ph);
-        tma_load_3d(dst + L::kTile + h * kKeys * 128, &tm_v, bar, h * 64, off, ph);
-      }
-      if (kFp8) {
-        const size_t row = ((size_t)max(ph, 0) << p.s.page_shift) + off;
-        bulk_load(scales + in_stage * 2 * kKeys, p.k_scale + row, kKeys, bar);
-        bulk_load(scales + in_stage * 2 * kKeys + kKeys, p.v_scale + row, kKeys, bar);
+        for (int h = 0; h < (kFp8 ? 1 : D / 64); ++h) {
+          tma_load_3d(dst + h * kKeys * 128, &tm_k, bar, h * 64, off, ph);
+          tma_load_3d(dst + L::kTile + h * kKeys * 128, &tm_v, bar, h * 64, off, ph);
+        }
+        if (kFp8) {
+          const size_t row = ((size_t)max(ph, 0) << p.s.page_shift) + off;
+          const uint32_t sc = scales + in_stage * 2 * kKeys + (j << box_shift);
+          bulk_load(sc, p.k_scale + row, 1 << box_shift, bar);
+          bulk_load(sc + kKeys, p.v_scale + row, 1 << box_shift, bar);
+        }
       }
     }
     in_i += kWarps;
@@ -332,40 +371,62 @@ __global__ void __launch_bounds__(kThreads, 1)
   while (at.more()) {
     const int rows = at.rows(p), row0 = at.tile * kRows;
     const int vis = at.visible(p);
-    // Q of the tile as A fragments, rows g and g + 8
+    // Q of the tile as A fragments, rows g and g + 8.  E4M3: four consecutive
+    // values of a row are a lane's, for the k slots 2 c, 2 c + 1 and 2 c + 8,
+    // 2 c + 9, which is how a word of four codes of a key lies in it.
     uint32_t qf[kSteps][4];
-    int row_lim[2];       // keys that the two rows see
+    int row_lim[2];                  // keys that the two rows see
+    float row_scale[2];              // what the rows' scores are multiplied by, for log2 units
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int r = row0 + g + 8 * h;
       const bool valid = g + 8 * h < rows;
       const int t = r / p.group, j = r - t * p.group;
       row_lim[h] = !valid ? 0 : p.causal ? at.s.L - at.s.n + t + 1 : at.s.L;
+      row_scale[h] = p.scale_log2;
       const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) +
                                  ((size_t)(at.s.q0 + t) * p.Hq + at.head * p.group + j) * D;
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
         uint2 w = make_uint2(0u, 0u);
-        if (kFp8) {
-          // four consecutive values of the row; an E4M3 word gives the pairs
-          // (0, 2) and (1, 3), so Q's pairs are taken likewise
-          if (valid) w = *reinterpret_cast<const uint2*>(src + 16 * s + 4 * c);
-          qf[s][h] = __byte_perm(w.x, w.y, 0x5410);
-          qf[s][2 + h] = __byte_perm(w.x, w.y, 0x7632);
-        } else {
-          if (valid) {
+        if (valid) {
+          if (kFp8) {
+            w = *reinterpret_cast<const uint2*>(src + 16 * s + 4 * c);
+          } else {
             w.x = *reinterpret_cast<const uint32_t*>(src + 16 * s + 2 * c);
             w.y = *reinterpret_cast<const uint32_t*>(src + 16 * s + 8 + 2 * c);
           }
-          qf[s][h] = w.x;
-          qf[s][2 + h] = w.y;
         }
+        qf[s][h] = w.x;
+        qf[s][2 + h] = w.y;
+      }
+      if (kFp8) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            top = max(top, max(qf[s][2 * k + h] & 0x7FFFu, (qf[s][2 * k + h] >> 16) & 0x7FFFu));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int e = max((int)(top >> 7), 27) - 127;            // of the largest value, -100 at least
+        const float up = __uint_as_float((uint32_t)(127 + 13 - e) << 23);     // e <= 128
+        row_scale[h] *= __uint_as_float((uint32_t)(127 - 13 + e) << 23);
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t w = qf[s][2 * k + h];
+            qf[s][2 * k + h] = pack_f16x2(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xFFFF0000u) * up);
+          }
       }
     }
     float acc[D / 8][4];
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, lr[2] = {0.0f, 0.0f};
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    float ones[4] = {0.0f, 0.0f, 0.0f, 0.0f};      // BF16: sums of the weights as the product takes them
+    int v_top = 0;      // E4M3: the largest scale byte of a value so far; acc counts in 2^(v_top - 127 - 14)
 
 #pragma unroll 1
     for (int i = warp; i < vis && !lost; i += kWarps) {
@@ -375,143 +436,157 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const uint32_t kt = ring + stage * L::kStage, vt = kt + L::kTile;
       const int key0 = (at.kb + i) * kKeys;
-      // scores of 16 rows and 2 x 8 keys
-      float s0[4] = {0.0f, 0.0f, 0.0f, 0.0f}, s1[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      float2* factor = reinterpret_cast<float2*>(smem + L::kFactors) + warp * kKeys;     // of keys, then of values
+      if (kFp8) {
+        // lane i: the factors of key i.  Values' scales are taken relative to
+        // the largest so far and times 2^14, so that a weight has FP16's full
+        // precision down to 2^-28 of the largest there is.
+        const uint8_t* bytes = smem + (scales - sbase) + stage * 2 * kKeys;
+        const bool mine = key0 + lane < at.s.L;          // behind the end: anything
+        const uint32_t kb = bytes[lane], vb = mine ? bytes[kKeys + lane] : 0u;
+        const int block_top = __reduce_max_sync(0xffffffffu, vb == 255u ? 0u : vb);
+        if (block_top > v_top) {
+          if (v_top > 0) {
+            const float f = __uint_as_float((uint32_t)max(v_top - block_top + 127, 0) << 23);
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[j][e] *= f;
+          }
+          v_top = block_top;
+        }
+        float* to = reinterpret_cast<float*>(factor);
+        to[lane] = paged::scale_value(kb);
+        to[kKeys + lane] = vb == 255u ? __int_as_float(0x7FC00000)
+                                      : __uint_as_float((uint32_t)max((int)vb - v_top + 14 + 127, 0) << 23);
+        __syncwarp();
+      }
+      // scores of 16 rows and kGroups x 2 x 8 keys
+      float s[2 * kGroups][4];
+#pragma unroll
+      for (int j = 0; j < 2 * kGroups; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.0f;
       if (!kFp8) {
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-          uint32_t b[4];
-          ldsm4(piece<D, kFp8>(kt, (lane >> 4) * 8 + (lane & 7), 2 * s + ((lane >> 3) & 1)), b);
-          mma16816(s0, qf[s], b[0], b[1]);
-          mma16816(s1, qf[s], b[2], b[3]);
-        }
+        for (int st = 0; st < kSteps; ++st)
+#pragma unroll
+          for (int j = 0; j < kGroups; ++j) {
+            uint32_t b[4];
+            ldsm4(piece<D, kFp8>(kt, 16 * j + (lane >> 4) * 8 + (lane & 7), 2 * st + ((lane >> 3) & 1)), b);
+            mma16816(s[2 * j], qf[st], b[0], b[1]);
+            mma16816(s[2 * j + 1], qf[st], b[2], b[3]);
+          }
       } else {
 #pragma unroll
-        for (int s = 0; s < kSteps; s += 2) {
-          // keys 0-7 and 8-15 of 16-byte pieces s and s + 1
-          uint32_t b[4];
-          ldsm4(piece<D, kFp8>(kt, (lane >> 4) * 8 + (lane & 7), s + ((lane >> 3) & 1)), b);
-          mma16816(s0, qf[s], paged::e4m3_even(b[0]), paged::e4m3_odd(b[0]));
-          mma16816(s0, qf[s + 1], paged::e4m3_even(b[1]), paged::e4m3_odd(b[1]));
-          mma16816(s1, qf[s], paged::e4m3_even(b[2]), paged::e4m3_odd(b[2]));
-          mma16816(s1, qf[s + 1], paged::e4m3_even(b[3]), paged::e4m3_odd(b[3]));
-        }
-      }
-      // x[h][e]: row g + 8 h, keys 2 c, 2 c + 1, 2 c + 8, 2 c + 9, in log2 units
-      float x[2][4] = {{s0[0], s0[1], s1[0], s1[1]}, {s0[2], s0[3], s1[2], s1[3]}};
-      float vs[4];
-      if (kFp8) {
-        const uint8_t* ks = smem + (scales - sbase) + stage * 2 * kKeys;
-        const uint32_t k0 = *reinterpret_cast<const uint16_t*>(ks + 2 * c);
-        const uint32_t k1 = *reinterpret_cast<const uint16_t*>(ks + 8 + 2 * c);
-        const uint32_t v0 = *reinterpret_cast<const uint16_t*>(ks + kKeys + 2 * c);
-        const uint32_t v1 = *reinterpret_cast<const uint16_t*>(ks + kKeys + 8 + 2 * c);
-        const float ksc[4] = {paged::scale_value(k0 & 255u), paged::scale_value(k0 >> 8),
-                              paged::scale_value(k1 & 255u), paged::scale_value(k1 >> 8)};
-        vs[0] = paged::scale_value(v0 & 255u);
-        vs[1] = paged::scale_value(v0 >> 8);
-        vs[2] = paged::scale_value(v1 & 255u);
-        vs[3] = paged::scale_value(v1 >> 8);
+        for (int st = 0; st < kSteps; st += 2)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[0][e] *= ksc[e];
-          x[1][e] *= ksc[e];
+          for (int j = 0; j < kGroups; ++j) {
+            // keys 0-7 and 8-15 of the group, 16-byte pieces st and st + 1
+            uint32_t b[4];
+            ldsm4(piece<D, kFp8>(kt, 16 * j + (lane >> 4) * 8 + (lane & 7), st + ((lane >> 3) & 1)), b);
+            mma16816_f16(s[2 * j], qf[st], e4m3_f16x2(b[0]), e4m3_f16x2(b[0] >> 16));
+            mma16816_f16(s[2 * j + 1], qf[st], e4m3_f16x2(b[2]), e4m3_f16x2(b[2] >> 16));
+            mma16816_f16(s[2 * j], qf[st + 1], e4m3_f16x2(b[1]), e4m3_f16x2(b[1] >> 16));
+            mma16816_f16(s[2 * j + 1], qf[st + 1], e4m3_f16x2(b[3]), e4m3_f16x2(b[3] >> 16));
+          }
+      }
+      // s[j][2 h + e]: row g + 8 h, key 8 j + 2 c + e; in log2 units from here
+#pragma unroll
+      for (int j = 0; j < 2 * kGroups; ++j) {
+        const float2 kf = kFp8 ? factor[4 * j + c] : make_float2(1.0f, 1.0f);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          s[j][2 * h] *= kFp8 ? row_scale[h] * kf.x : row_scale[h];
+          s[j][2 * h + 1] *= kFp8 ? row_scale[h] * kf.y : row_scale[h];
         }
       }
       // a block that every row sees whole needs no mask (rows of the tile see
       // at least the first row's keys)
-      const bool tail = key0 + kKeys > (p.causal ? at.s.L - at.s.n + row0 / p.group + 1 : at.s.L);
-      uint32_t pk[2][2];
+      if (key0 + kKeys > (p.causal ? at.s.L - at.s.n + row0 / p.group + 1 : at.s.L)) {
+#pragma unroll
+        for (int j = 0; j < 2 * kGroups; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (key0 + 8 * j + 2 * c + (e & 1) >= row_lim[e >> 1]) s[j][e] = -INFINITY;
+      }
+      float m_use[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
+        float mx = m[h];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[h][e] *= p.scale_log2;
-          if (tail && key0 + 2 * c + (e & 1) + 8 * (e >> 1) >= row_lim[h]) x[h][e] = -INFINITY;
-        }
-        float mx = fmaxf(fmaxf(x[h][0], x[h][1]), fmaxf(x[h][2], x[h][3]));
+        for (int j = 0; j < 2 * kGroups; ++j) mx = max3(mx, s[j][2 * h], s[j][2 * h + 1]);
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float m_new = fmaxf(m[h], mx);
-        const float m_use = m_new == -INFINITY ? 0.0f : m_new;
-        if (__any_sync(0xffffffffu, m_new > m[h])) {
-          const float f = ex2_mufu(m[h] - m_use);      // 0 from a maximum of -inf
+        m_use[h] = mx == -INFINITY ? 0.0f : mx;
+        if (__any_sync(0xffffffffu, mx > m[h])) {
+          const float f = ex2_mufu(m[h] - m_use[h]);      // 0 from a maximum of -inf
           l[h] *= f;
-          lr[h] *= f;
+          ones[2 * h] *= f;
 #pragma unroll
           for (int j = 0; j < D / 8; ++j) {
             acc[j][2 * h] *= f;
             acc[j][2 * h + 1] *= f;
           }
-          m[h] = m_new;
+          m[h] = mx;
         }
-        float e[4];
+      }
+      // Values behind the sequence's end may be NaN or infinite, which a weight
+      // of zero would not cancel: they are cleared.
+      const int n_left = at.s.L - key0;
+      const bool ragged = n_left < kKeys;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) e[k] = ex2_mufu(x[h][k] - m_use);
-        // Two sums: of the FP32 weights for LSE, and of the weights as the
-        // product with V takes them, rounded to BF16, for the division, so
-        // that the weights used add up to one.
-        l[h] += (e[0] + e[1]) + (e[2] + e[3]);
+      for (int j = 0; j < kGroups; ++j) {
+        // weights of the group's 16 keys as an A fragment
+        uint32_t pa[4];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          uint32_t w = pack_bf16x2(e[2 * k], e[2 * k + 1]);
-          const float w0 = __uint_as_float(w << 16), w1 = __uint_as_float(w & 0xFFFF0000u);
-          lr[h] += w0 + w1;
-          if (kFp8) {
-            // the value's scale goes with its weight (a power of two: exact);
-            // a masked key's scale may be anything
-            float y0 = w0 * vs[2 * k], y1 = w1 * vs[2 * k + 1];
-            if (tail) {
-              const int key = key0 + 2 * c + 8 * k;
-              if (key >= row_lim[h]) y0 = 0.0f;
-              if (key + 1 >= row_lim[h]) y1 = 0.0f;
+          const float2 vf = kFp8 ? factor[kKeys / 2 + 8 * j + 4 * k + c] : make_float2(1.0f, 1.0f);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float e0 = ex2_mufu(s[2 * j + k][2 * h] - m_use[h]);
+            const float e1 = ex2_mufu(s[2 * j + k][2 * h + 1] - m_use[h]);
+            l[h] += e0 + e1;
+            pa[2 * k + h] = kFp8 ? pack_f16x2(e0 * vf.x, e1 * vf.y) : pack_bf16x2(e0, e1);
+          }
+        }
+        uint32_t keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+        if (ragged) {
+          const int n = n_left - 16 * j - 2 * c;
+          keep[0] = (n > 0 ? 0x0000FFFFu : 0u) | (n > 1 ? 0xFFFF0000u : 0u);
+          keep[1] = (n > 8 ? 0x0000FFFFu : 0u) | (n > 9 ? 0xFFFF0000u : 0u);
+        }
+        if (!kFp8) {
+          // the weights' sum as they are rounded, for the division, so that the
+          // weights used add up to one: a product with ones
+          mma16816(ones, pa, 0x3F803F80u, 0x3F803F80u);
+#pragma unroll
+          for (int d = 0; d < D / 16; ++d) {
+            uint32_t b[4];
+            ldsm4_t(piece<D, kFp8>(vt, 16 * j + (lane & 15), 2 * d + (lane >> 4)), b);
+            if (ragged) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) b[e] &= keep[e & 1];
             }
-            w = pack_bf16x2(y0, y1);
+            mma16816(acc[2 * d], pa, b[0], b[1]);
+            mma16816(acc[2 * d + 1], pa, b[2], b[3]);
           }
-          pk[h][k] = w;
-        }
-      }
-      // O += P V.  Values behind the sequence's end may be NaN or infinite,
-      // which a weight of zero would not cancel: they are cleared.
-      const uint32_t pa[4] = {pk[0][0], pk[1][0], pk[0][1], pk[1][1]};
-      const bool ragged = key0 + kKeys > at.s.L;
-      uint32_t keep[2];
-      if (ragged) {
-        const int n = at.s.L - key0;
-        keep[0] = (2 * c < n ? 0x0000FFFFu : 0u) | (2 * c + 1 < n ? 0xFFFF0000u : 0u);
-        keep[1] = (2 * c + 8 < n ? 0x0000FFFFu : 0u) | (2 * c + 9 < n ? 0xFFFF0000u : 0u);
-      }
-      if (!kFp8) {
+        } else {
+          // a word holds D columns 2 n and 2 n + 1 of two keys: the even bytes
+          // are one column tile's operand, the odd bytes another's
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-          uint32_t b[4];
-          ldsm4_t(piece<D, kFp8>(vt, lane & 15, 2 * j + (lane >> 4)), b);
-          if (ragged) {
-            b[0] &= keep[0];
-            b[1] &= keep[1];
-            b[2] &= keep[0];
-            b[3] &= keep[1];
-          }
-          mma16816(acc[2 * j], pa, b[0], b[1]);
-          mma16816(acc[2 * j + 1], pa, b[2], b[3]);
-        }
-      } else {
-        // a word holds D columns 2 n and 2 n + 1 of two keys: the even bytes
-        // are one column tile's operand, the odd bytes another's
+          for (int d = 0; d < D / 16; d += 2) {
+            uint32_t b[4];
+            ldsm4_t(piece<D, kFp8>(vt, 16 * j + (lane & 15), d + (lane >> 4)), b);
+            if (ragged) {
 #pragma unroll
-        for (int j = 0; j < D / 16; j += 2) {
-          uint32_t b[4];
-          ldsm4_t(piece<D, kFp8>(vt, lane & 15, j + (lane >> 4)), b);
-          if (ragged) {
-            b[0] &= keep[0];
-            b[1] &= keep[1];
-            b[2] &= keep[0];
-            b[3] &= keep[1];
+              for (int e = 0; e < 4; ++e) b[e] &= keep[e & 1];
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) b[e] = __byte_perm(b[e], 0u, 0x3120);     // even bytes, odd bytes
+            mma16816_f16(acc[2 * d], pa, e4m3_f16x2(b[0]), e4m3_f16x2(b[1]));
+            mma16816_f16(acc[2 * d + 1], pa, e4m3_f16x2(b[0] >> 16), e4m3_f16x2(b[1] >> 16));
+            mma16816_f16(acc[2 * d + 2], pa, e4m3_f16x2(b[2]), e4m3_f16x2(b[3]));
+            mma16816_f16(acc[2 * d + 3], pa, e4m3_f16x2(b[2] >> 16), e4m3_f16x2(b[3] >> 16));
           }
-          mma16816(acc[2 * j], pa, paged::e4m3_even(b[0]), paged::e4m3_even(b[1]));
-          mma16816(acc[2 * j + 1], pa, paged::e4m3_odd(b[0]), paged::e4m3_odd(b[1]));
-          mma16816(acc[2 * j + 2], pa, paged::e4m3_even(b[2]), paged::e4m3_even(b[3]));
-          mma16816(acc[2 * j + 3], pa, paged::e4m3_odd(b[2]), paged::e4m3_odd(b[3]));
         }
       }
       __syncwarp();       // every lane is done with the stage
@@ -527,19 +602,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
-      for (int d = 1; d < 4; d *= 2) {
-        l[h] += __shfl_xor_sync(0xffffffffu, l[h], d);
-        lr[h] += __shfl_xor_sync(0xffffffffu, lr[h], d);
-      }
+      for (int d = 1; d < 4; d *= 2) l[h] += __shfl_xor_sync(0xffffffffu, l[h], d);
       if (c == 0) {
         const int i = warp * kRows + g + 8 * h;
         st_m[i] = m[h];
         st_l[i] = l[h];
-        st_lr[i] = lr[h];
+        // FP16 weights (E4M3 pages) are off by 2^-12 at most: their own sum is
+        // not worth keeping
+        st_lr[i] = kFp8 ? l[h] : ones[2 * h];
       }
     }
     __syncthreads();
     float top[2], f[2];
+    // acc's unit; an empty share has none
+    const float unit = kFp8 && v_top > 0 ? __uint_as_float((uint32_t)max(v_top - 14, 0) << 23) : 1.0f;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       top[h] = -INFINITY;
@@ -560,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // BF16: columns 8 j + 2 c, + 1; E4M3: of tiles 2 i, 2 i + 1, columns 16 i + 4 c + {0, 2}, {1, 3}
             const int d0 = kFp8 ? 16 * (j / 2) + 4 * c + (j & 1) : 8 * j + 2 * c;
             const int d1 = kFp8 ? d0 + 2 : d0 + 1;
-            const float y0 = acc[j][2 * h] * f[h], y1 = acc[j][2 * h + 1] * f[h];
+            const float y0 = acc[j][2 * h] * f[h] * unit, y1 = acc[j][2 * h + 1] * f[h] * unit;
             r[d0] = w0 ? r[d0] + y0 : y0;
             r[d1] = w0 ? r[d1] + y1 : y1;
           }
@@ -628,18 +704,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Joins the partial results of the units that borders between thread blocks
 // cut: block x + 1 looks at border x + 1 and does the unit whose first cut that
 // border is.
-template <int D>
+template <int D, int kKeys>
 __global__ void __launch_bounds__(kThreads) combine_kernel(const PagedAttnParams p, int ctas) {
   __shared__ long long pre[kMaxPackedSeqs + 1];
   __shared__ long long sums[kThreads / 32];
-  const long long total = build_line<kThreads>(p, pre, sums);
+  const long long total = build_line<kThreads, kKeys>(p, pre, sums);
   const int G = active_ctas(total, ctas);
   const int c = blockIdx.x + 1;
   // before any exit, so that this grid ends after the main one
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (c >= G) return;
   const long long t = stretch(total, c, G);
-  Walk w;
+  Walk<kKeys> w;
   w.begin(p, pre, t, total);
   const long long start = t - w.kb, end = start + w.nblk;
   const long long t_prev = stretch(total, c - 1, G);
@@ -683,10 +759,11 @@ fa_status launch_inst(const PagedAttnLaunch& L, cudaStream_t stream) {
   using Lay = Layout<D, kFp8>;
   const int page_size = 1 << L.p.s.page_shift;
   const long long page_heads = (long long)L.p.s.num_pages * L.p.s.Hkv;
+  const int box = page_size < Lay::kKeys ? page_size : Lay::kKeys;
   CUtensorMap tk, tv;
   fa_status st;
-  if ((st = make_tmap_pages(&tk, L.k_pages, page_heads, page_size, D, kFp8, kKeys)) != FA_OK) return st;
-  if ((st = make_tmap_pages(&tv, L.v_pages, page_heads, page_size, D, kFp8, kKeys)) != FA_OK) return st;
+  if ((st = make_tmap_pages(&tk, L.k_pages, page_heads, page_size, D, kFp8, box)) != FA_OK) return st;
+  if ((st = make_tmap_pages(&tv, L.v_pages, page_heads, page_size, D, kFp8, box)) != FA_OK) return st;
   auto kern = decode_kernel<D, kFp8>;
   if ((st = prepare_kernel(reinterpret_cast<const void*>(kern), Lay::kBytes)) != FA_OK) return st;
   const int ctas = L.p.num_ctas;
@@ -703,7 +780,7 @@ fa_status launch_inst(const PagedAttnLaunch& L, cudaStream_t stream) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, combine_kernel<D>, L.p, ctas) != cudaSuccess) return FA_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, combine_kernel<D, Lay::kKeys>, L.p, ctas) != cudaSuccess) return FA_ERR_CUDA;
   }
   return FA_OK;
 }
