@@ -50,7 +50,7 @@ fa_status check_cache(const void* k_pages, const void* v_pages, const void* k_sc
 
 // Rows of one sequence and key/value head up to which a call takes the decode
 // kernel; above it the chunk kernel.
-constexpr int kDecodeRows = 16;
+constexpr int kDecodeRows = 32;
 bool takes_decode(int Hq, int Hkv, int Sn, bool packed, int max_q) {
   return (long long)(packed ? max_q : Sn) * (Hq / Hkv) <= kDecodeRows;
 }

@@ -6,26 +6,32 @@
 // them, so HBM bounds it: the design keeps loads in flight and splits the keys
 // evenly over the SMs.
 //
-//   * Rows.  The query heads of one key/value head, for up to 16 rows of
-//     (new token, head of the group), share the keys that a warp loads: they
-//     are the 16 rows of an mma.sync tile.  (tcgen05 tiles have at least 64
-//     rows; with 16 or fewer to fill, the warp-level instruction leaves the
-//     tensor cores no busier and needs no trip through tensor memory.)
-//   * Work.  The blocks of 16 keys of all (sequence, key/value head, row tile)
+//   * Rows.  The query heads of one key/value head, for up to 32 rows of
+//     (new token, head of the group), share the keys that a warp loads.  They
+//     are the N side of the products, 8 rows an mma.sync tile, and keys (for
+//     S^T = K Q^T) and columns of V (for O^T = V^T P^T) the M side: with 8 rows
+//     or fewer, the usual case, that halves the products and the softmax
+//     against rows on the M side, whose tiles are 16 high.  (tcgen05 tiles
+//     have at least 64 rows on M and their accumulators are a trip through
+//     tensor memory away; with so few rows the warp-level instruction leaves
+//     the tensor cores a quarter busy.)
+//   * Work.  The key blocks of all (sequence, key/value head, row tile)
 //     units form one line, and thread block c takes the c-th of `grid` equal
 //     stretches of it.  A unit cut by a border leaves partial results in the
 //     workspace, at most two per thread block, and the combine kernel joins
 //     them.  Sequences of any mixture of lengths load all SMs alike.
-//   * Pipeline.  Each of the 8 warps walks every eighth key block of the
-//     stretch with a ring of its own in shared memory, which its lane 0 fills
-//     by TMA (the pages' rows, swizzled for ldmatrix); no warp waits for
-//     another until the unit's end, where the 8 softmax states are merged.
+//   * Pipeline.  Each warp walks the key blocks of the stretch that are its
+//     turn, with a ring of its own in shared memory, which its lane 0 fills by
+//     TMA (the pages' rows, swizzled for ldmatrix); no warp waits for another
+//     until the unit's end, where the warps' softmax states are merged.
 //   * E4M3 pages are widened in registers on the way to the tensor cores, to
 //     FP16, which holds every code and which one instruction makes of a pair (to
 //     BF16 it takes five).  The queries become FP16 by a power of two of each
 //     row's own, which loses nothing of note: a row's largest value is below 2^14
 //     then, and what lies below 2^-38 of it is rounded.  The keys' scales go to
 //     the scores in FP32, the values' to the weights.
+//   * The running maximum is lazy: it moves, and the sums and O are rescaled,
+//     only when a row's scores pass it by more than 8 log2 units.
 #include <cuda_runtime.h>
 
 #include "paged.cuh"
@@ -36,19 +42,16 @@ namespace pdec {
 
 __device__ DeviceError g_err;
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-constexpr int kRows = 16;     // rows of a tile
-// Keys of a block, at most two pages: stages of 8 KB of keys and values keep
-// enough bytes in flight with few stages; E4M3 at D = 64 has stages of 4 KB.
-template <int D, bool kFp8>
-constexpr int keys_of() { return D == 128 && !kFp8 ? 16 : 32; }
+constexpr float kThreshold = 8.0f;   // lazy rescaling, log2 units
+// E4M3: weights are taken times 2^6 to FP16.  With the threshold they stay
+// below 2^14, and keep FP16's full precision down to 2^-20 of the maximum.
+constexpr int kWeightUp = 6;
 
 enum Site { kSiteSeqs = 1, kSitePage, kSiteRing };
 
 // Layout of the workspace: per slot the rows' unnormalised outputs, then per
 // slot and row the maximum (log2 units) and the two sums.
-template <int D>
+template <int D, int kRows>
 struct Part {
   static constexpr int kSlotFloats = kRows * D;
   static constexpr int kStat = 4;
@@ -59,13 +62,20 @@ struct Part {
   static constexpr size_t bytes() { return (size_t)2 * kMaxCtas * (kSlotFloats + kRows * kStat) * sizeof(float); }
 };
 
-template <int D, bool kFp8>
+// kTiles: tiles of 8 rows.  12 warps with up to 168 registers hide more latency
+// than 8; the 32-row kernel's accumulators leave room for 8.
+template <int D, bool kFp8, int kTiles>
 struct Layout {
-  static constexpr int kKeys = keys_of<D, kFp8>();
+  static constexpr int kWarps = kTiles == 4 ? 8 : 12;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kRows = 8 * kTiles;
+  // Keys of a block, at most two pages: stages of 8 KB of keys and values (4 KB
+  // for E4M3 at D = 64) keep enough bytes in flight with few stages.
+  static constexpr int kKeys = D == 128 && !kFp8 ? 16 : 32;
   static constexpr int kTile = kKeys * D * (kFp8 ? 1 : 2);        // keys or values of a block
   static constexpr int kStage = 2 * kTile;
-  static constexpr int kStages = kStage >= 8192 ? 3 : kStage >= 4096 ? 5 : 8;
-  static constexpr int kPitch = D + 8;                            // floats of a merge row
+  static constexpr int kStages = 196608 / (kWarps * kStage);
+  static constexpr int kPitch = D + 4;                            // floats of a merge row
   static constexpr int kMergeRows = 32;                           // rows of all merge slots
   static constexpr int kRing = 0;
   static constexpr int kScales = kRing + kWarps * kStages * kStage;   // E4M3: scale bytes of a stage's keys, values
@@ -96,20 +106,20 @@ FA_DEV Seq seq_of(const PagedSeqs& s, int b) {
   }
   return r;
 }
-FA_DEV int tiles_of(int n, int group) { return (n * group + kRows - 1) / kRows; }
+FA_DEV int tiles_of(int n, int group, int rows) { return (n * group + rows - 1) / rows; }
 // Blocks of a unit: at least one, so that rows without a key are written too.
 FA_DEV int blocks_of(int L, int keys) { return max(1, (L + keys - 1) / keys); }
 
 // Prefix sums of the sequences' blocks into pre[0 .. B]; returns their total,
 // 0 when the sequences break the rules.  All threads of the block.
-template <int kN, int kKeys>
+template <int kN, int kKeys, int kRows>
 FA_DEV long long build_line(const PagedAttnParams& p, long long* pre, long long* warp_sums) {
   const bool ok = paged::sequences_ok(p.s, p.max_q);
   if (!ok) {
     if (blockIdx.x == 0 && threadIdx.x == 0) paged::record_bad_input(&g_err, kSiteSeqs);
     return 0;
   }
-  constexpr int kEach = kMaxPackedSeqs / kN;
+  constexpr int kEach = (kMaxPackedSeqs + kN - 1) / kN;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   long long v[kEach], sum = 0;
 #pragma unroll
@@ -118,7 +128,7 @@ FA_DEV long long build_line(const PagedAttnParams& p, long long* pre, long long*
     v[i] = 0;
     if (b < p.s.B) {
       const Seq q = seq_of(p.s, b);
-      if (q.n > 0) v[i] = (long long)p.s.Hkv * tiles_of(q.n, p.group) * blocks_of(q.L, kKeys);
+      if (q.n > 0) v[i] = (long long)p.s.Hkv * tiles_of(q.n, p.group, kRows) * blocks_of(q.L, kKeys);
     }
     sum += v[i];
   }
@@ -143,16 +153,16 @@ FA_DEV long long build_line(const PagedAttnParams& p, long long* pre, long long*
   return pre[p.s.B];
 }
 
-// Thread blocks that share the line: no more than leave each a block per warp.
+// Thread blocks that share the line: no more than leave each 8 key blocks.
 FA_DEV int active_ctas(long long total, int ctas) {
-  const long long most = (total + kWarps - 1) / kWarps;
+  const long long most = (total + 7) / 8;
   return most < ctas ? (int)most : ctas;
 }
 // First block of stretch c of G.
 FA_DEV long long stretch(long long total, int c, int G) { return total * c / G; }
 
 // A walk over the segments (the stretch's share of one unit) of [t0, t1).
-template <int kKeys>
+template <int kKeys, int kRows>
 struct Walk {
   int b, head, tile, tiles;
   Seq s;
@@ -162,7 +172,7 @@ struct Walk {
 
   FA_DEV void load(const PagedAttnParams& p) {
     s = seq_of(p.s, b);
-    tiles = tiles_of(s.n, p.group);
+    tiles = tiles_of(s.n, p.group, kRows);
     nblk = blocks_of(s.L, kKeys);
   }
   FA_DEV void begin(const PagedAttnParams& p, const long long* pre, long long t0, long long t1) {
@@ -250,23 +260,33 @@ FA_DEV uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
+// Transposes an 8 x 8 matrix of 16-bit values over the warp: lane 4 r + c holds
+// row r, columns 2 c and 2 c + 1.
+FA_DEV uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
 // Shared-memory address of 16-byte piece `c` of row `r` of a tile at `base`.
 // BF16: 64-column chunks of 128-byte rows, 128-byte swizzle.  E4M3: rows of D
 // bytes, swizzled by their width.
-template <int D, bool kFp8>
+template <int D, bool kFp8, int kKeys>
 FA_DEV uint32_t piece(uint32_t base, int r, int c) {
-  if (!kFp8) return base + (c >> 3) * (Layout<D, kFp8>::kKeys * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+  if (!kFp8) return base + (c >> 3) * (kKeys * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
   if (D == 128) return base + r * 128 + ((c ^ (r & 7)) << 4);
   return base + r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
 // ---------------------------------------------------------------- kernel --
 
-template <int D, bool kFp8>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, bool kFp8, int kTiles>
+__global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
     decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const PagedAttnParams p) {
-  using L = Layout<D, kFp8>;
+  using L = Layout<D, kFp8, kTiles>;
+  using W = Part<D, L::kRows>;
+  constexpr int kWarps = L::kWarps, kThreads = L::kThreads, kRows = L::kRows;
   constexpr int kKeys = L::kKeys;
   constexpr int kGroups = kKeys / 16;
   constexpr int kSteps = D / 16;      // 16-wide steps along D
@@ -292,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
-  const long long total = build_line<kThreads, kKeys>(p, pre, reinterpret_cast<long long*>(merge));
+  const long long total = build_line<kThreads, kKeys, kRows>(p, pre, reinterpret_cast<long long*>(merge));
   __syncthreads();
   const int G = active_ctas(total, gridDim.x);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -300,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const long long t0 = stretch(total, blockIdx.x, G), t1 = stretch(total, blockIdx.x + 1, G);
 
   // The walk that issues loads runs ahead of the one that consumes them.
-  Walk<kKeys> in, at;
+  Walk<kKeys, kRows> in, at;
   in.begin(p, pre, t0, t1);
   at = in;
   int in_i = warp, in_vis = in.visible(p);       // next block of this warp in the segment
@@ -371,19 +391,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   while (at.more()) {
     const int rows = at.rows(p), row0 = at.tile * kRows;
     const int vis = at.visible(p);
-    // Q of the tile as A fragments, rows g and g + 8.  E4M3: four consecutive
-    // values of a row are a lane's, for the k slots 2 c, 2 c + 1 and 2 c + 8,
-    // 2 c + 9, which is how a word of four codes of a key lies in it.
-    uint32_t qf[kSteps][4];
-    int row_lim[2];                  // keys that the two rows see
-    float row_scale[2];              // what the rows' scores are multiplied by, for log2 units
+    // Q of the tile as B fragments: row 8 n + g of tile n, d = 16 s + 2 c, + 1 and
+    // + 8, + 9.  E4M3: four consecutive values at 16 s + 4 c instead, which is
+    // how a word of four codes of a key lies in its fragment.
+    uint32_t qf[kTiles][kSteps][2];
+    // rows 8 n + 2 c + e of the tile, whose scores this lane gets:
+    int row_lim[kTiles][2];          // keys that they see
+    float row_scale[kTiles][2];      // what their scores are multiplied by, for log2 units
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = row0 + g + 8 * h;
-      const bool valid = g + 8 * h < rows;
+    for (int n = 0; n < kTiles; ++n) {
+      const int r = row0 + 8 * n + g;
+      const bool valid = 8 * n + g < rows;
       const int t = r / p.group, j = r - t * p.group;
-      row_lim[h] = !valid ? 0 : p.causal ? at.s.L - at.s.n + t + 1 : at.s.L;
-      row_scale[h] = p.scale_log2;
       const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) +
                                  ((size_t)(at.s.q0 + t) * p.Hq + at.head * p.group + j) * D;
 #pragma unroll
@@ -397,36 +416,52 @@ __global__ void __launch_bounds__(kThreads, 1)
             w.y = *reinterpret_cast<const uint32_t*>(src + 16 * s + 8 + 2 * c);
           }
         }
-        qf[s][h] = w.x;
-        qf[s][2 + h] = w.y;
+        qf[n][s][0] = w.x;
+        qf[n][s][1] = w.y;
       }
+      float scale = p.scale_log2;
       if (kFp8) {
         uint32_t top = 0;
 #pragma unroll
         for (int s = 0; s < kSteps; ++s)
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
-            top = max(top, max(qf[s][2 * k + h] & 0x7FFFu, (qf[s][2 * k + h] >> 16) & 0x7FFFu));
+          for (int k = 0; k < 2; ++k) top = max(top, max(qf[n][s][k] & 0x7FFFu, (qf[n][s][k] >> 16) & 0x7FFFu));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const int e = max((int)(top >> 7), 27) - 127;            // of the largest value, -100 at least
         const float up = __uint_as_float((uint32_t)(127 + 13 - e) << 23);     // e <= 128
-        row_scale[h] *= __uint_as_float((uint32_t)(127 - 13 + e) << 23);
+        scale *= __uint_as_float((uint32_t)(127 - 13 + e) << 23);
 #pragma unroll
         for (int s = 0; s < kSteps; ++s)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const uint32_t w = qf[s][2 * k + h];
-            qf[s][2 * k + h] = pack_f16x2(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xFFFF0000u) * up);
+            const uint32_t w = qf[n][s][k];
+            qf[n][s][k] = pack_f16x2(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xFFFF0000u) * up);
           }
       }
-    }
-    float acc[D / 8][4];
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-    float ones[4] = {0.0f, 0.0f, 0.0f, 0.0f};      // BF16: sums of the weights as the product takes them
-    int v_top = 0;      // E4M3: the largest scale byte of a value so far; acc counts in 2^(v_top - 127 - 14)
+      for (int e = 0; e < 2; ++e) {
+        row_scale[n][e] = kFp8 ? __shfl_sync(0xffffffffu, scale, (2 * c + e) * 4) : scale;
+        const int in_tile = 8 * n + 2 * c + e;
+        row_lim[n][e] = in_tile >= rows ? 0 : p.causal ? at.s.L - at.s.n + (row0 + in_tile) / p.group + 1 : at.s.L;
+      }
+    }
+    // O^T: columns of V on the rows, tile rows on the columns (2 c, 2 c + 1 here)
+    float acc[kTiles][kSteps][4];
+    float m[kTiles][2], l[kTiles][2];
+    float ones[kTiles][4];      // BF16: sums of the weights as the product takes them
+#pragma unroll
+    for (int n = 0; n < kTiles; ++n) {
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        ones[n][e] = 0.0f;
+#pragma unroll
+        for (int d = 0; d < kSteps; ++d) acc[n][d][e] = 0.0f;
+      }
+    }
+    int v_top = 0;      // E4M3: the largest scale byte of a value so far; acc counts in 2^(v_top - 127 - kWeightUp)
 
 #pragma unroll 1
     for (int i = warp; i < vis && !lost; i += kWarps) {
@@ -436,11 +471,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const uint32_t kt = ring + stage * L::kStage, vt = kt + L::kTile;
       const int key0 = (at.kb + i) * kKeys;
-      float2* factor = reinterpret_cast<float2*>(smem + L::kFactors) + warp * kKeys;     // of keys, then of values
+      float2* factor = reinterpret_cast<float2*>(smem + L::kFactors) + warp * kKeys;     // of a key and its value
       if (kFp8) {
         // lane i: the factors of key i.  Values' scales are taken relative to
-        // the largest so far and times 2^14, so that a weight has FP16's full
-        // precision down to 2^-28 of the largest there is.
+        // the largest so far.
         const uint8_t* bytes = smem + (scales - sbase) + stage * 2 * kKeys;
         const bool mine = key0 + lane < at.s.L;          // behind the end: anything
         const uint32_t kb = bytes[lane], vb = mine ? bytes[kKeys + lane] : 0u;
@@ -449,143 +483,150 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (v_top > 0) {
             const float f = __uint_as_float((uint32_t)max(v_top - block_top + 127, 0) << 23);
 #pragma unroll
-            for (int j = 0; j < D / 8; ++j)
+            for (int n = 0; n < kTiles; ++n)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) acc[j][e] *= f;
+              for (int d = 0; d < kSteps; ++d)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[n][d][e] *= f;
           }
           v_top = block_top;
         }
-        float* to = reinterpret_cast<float*>(factor);
-        to[lane] = paged::scale_value(kb);
-        to[kKeys + lane] = vb == 255u ? __int_as_float(0x7FC00000)
-                                      : __uint_as_float((uint32_t)max((int)vb - v_top + 14 + 127, 0) << 23);
+        factor[lane] = make_float2(paged::scale_value(kb),
+                                   vb == 255u ? __int_as_float(0x7FC00000)
+                                              : __uint_as_float((uint32_t)max((int)vb - v_top + kWeightUp + 127, 0) << 23));
         __syncwarp();
       }
-      // scores of 16 rows and kGroups x 2 x 8 keys
-      float s[2 * kGroups][4];
+      // S^T of 16-key groups: s[n][j][2 h + e] is key 16 j + g + 8 h, row 8 n + 2 c + e
+      float s[kTiles][kGroups][4];
 #pragma unroll
-      for (int j = 0; j < 2 * kGroups; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.0f;
-      if (!kFp8) {
+      for (int n = 0; n < kTiles; ++n)
 #pragma unroll
-        for (int st = 0; st < kSteps; ++st)
+        for (int j = 0; j < kGroups; ++j) s[n][j][0] = s[n][j][1] = s[n][j][2] = s[n][j][3] = 0.0f;
 #pragma unroll
-          for (int j = 0; j < kGroups; ++j) {
-            uint32_t b[4];
-            ldsm4(piece<D, kFp8>(kt, 16 * j + (lane >> 4) * 8 + (lane & 7), 2 * st + ((lane >> 3) & 1)), b);
-            mma16816(s[2 * j], qf[st], b[0], b[1]);
-            mma16816(s[2 * j + 1], qf[st], b[2], b[3]);
+      for (int st = 0; st < kSteps; st += kFp8 ? 2 : 1)
+#pragma unroll
+        for (int j = 0; j < kGroups; ++j) {
+          uint32_t b[4];
+          if (!kFp8) {
+            // keys 0-7, 8-15 of the group at piece 2 st, then at 2 st + 1
+            ldsm4(piece<D, kFp8, kKeys>(kt, 16 * j + (lane & 15), 2 * st + (lane >> 4)), b);
+#pragma unroll
+            for (int n = 0; n < kTiles; ++n) mma16816(s[n][j], b, qf[n][st][0], qf[n][st][1]);
+          } else {
+            // keys 0-7, 8-15 of the group at piece st, then at st + 1
+            ldsm4(piece<D, kFp8, kKeys>(kt, 16 * j + (lane & 15), st + (lane >> 4)), b);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t a[4] = {e4m3_f16x2(b[2 * k]), e4m3_f16x2(b[2 * k + 1]), e4m3_f16x2(b[2 * k] >> 16),
+                                     e4m3_f16x2(b[2 * k + 1] >> 16)};
+#pragma unroll
+              for (int n = 0; n < kTiles; ++n) mma16816_f16(s[n][j], a, qf[n][st + k][0], qf[n][st + k][1]);
+            }
           }
-      } else {
-#pragma unroll
-        for (int st = 0; st < kSteps; st += 2)
-#pragma unroll
-          for (int j = 0; j < kGroups; ++j) {
-            // keys 0-7 and 8-15 of the group, 16-byte pieces st and st + 1
-            uint32_t b[4];
-            ldsm4(piece<D, kFp8>(kt, 16 * j + (lane >> 4) * 8 + (lane & 7), st + ((lane >> 3) & 1)), b);
-            mma16816_f16(s[2 * j], qf[st], e4m3_f16x2(b[0]), e4m3_f16x2(b[0] >> 16));
-            mma16816_f16(s[2 * j + 1], qf[st], e4m3_f16x2(b[2]), e4m3_f16x2(b[2] >> 16));
-            mma16816_f16(s[2 * j], qf[st + 1], e4m3_f16x2(b[1]), e4m3_f16x2(b[1] >> 16));
-            mma16816_f16(s[2 * j + 1], qf[st + 1], e4m3_f16x2(b[3]), e4m3_f16x2(b[3] >> 16));
-          }
-      }
-      // s[j][2 h + e]: row g + 8 h, key 8 j + 2 c + e; in log2 units from here
-#pragma unroll
-      for (int j = 0; j < 2 * kGroups; ++j) {
-        const float2 kf = kFp8 ? factor[4 * j + c] : make_float2(1.0f, 1.0f);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          s[j][2 * h] *= kFp8 ? row_scale[h] * kf.x : row_scale[h];
-          s[j][2 * h + 1] *= kFp8 ? row_scale[h] * kf.y : row_scale[h];
         }
-      }
-      // a block that every row sees whole needs no mask (rows of the tile see
-      // at least the first row's keys)
-      if (key0 + kKeys > (p.causal ? at.s.L - at.s.n + row0 / p.group + 1 : at.s.L)) {
+      float2 fac[kGroups][2];
 #pragma unroll
-        for (int j = 0; j < 2 * kGroups; ++j)
+      for (int j = 0; j < kGroups; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (key0 + 8 * j + 2 * c + (e & 1) >= row_lim[e >> 1]) s[j][e] = -INFINITY;
-      }
-      float m_use[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float mx = m[h];
-#pragma unroll
-        for (int j = 0; j < 2 * kGroups; ++j) mx = max3(mx, s[j][2 * h], s[j][2 * h + 1]);
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        m_use[h] = mx == -INFINITY ? 0.0f : mx;
-        if (__any_sync(0xffffffffu, mx > m[h])) {
-          const float f = ex2_mufu(m[h] - m_use[h]);      // 0 from a maximum of -inf
-          l[h] *= f;
-          ones[2 * h] *= f;
-#pragma unroll
-          for (int j = 0; j < D / 8; ++j) {
-            acc[j][2 * h] *= f;
-            acc[j][2 * h + 1] *= f;
-          }
-          m[h] = mx;
-        }
-      }
-      // Values behind the sequence's end may be NaN or infinite, which a weight
-      // of zero would not cancel: they are cleared.
+        for (int h = 0; h < 2; ++h) fac[j][h] = kFp8 ? factor[16 * j + 8 * h + g] : make_float2(1.0f, 1.0f);
+      // Behind the sequence's end values may be NaN or infinite, which a weight
+      // of zero would not cancel: they are cleared below.
       const int n_left = at.s.L - key0;
       const bool ragged = n_left < kKeys;
+      // a block that every row sees whole needs no mask (rows of the tile see
+      // at least the first row's keys)
+      const bool masked = key0 + kKeys > (p.causal ? at.s.L - at.s.n + row0 / p.group + 1 : at.s.L);
+      uint32_t pb[kTiles][kGroups][2];        // P^T as B fragments
 #pragma unroll
-      for (int j = 0; j < kGroups; ++j) {
-        // weights of the group's 16 keys as an A fragment
-        uint32_t pa[4];
+      for (int n = 0; n < kTiles; ++n) {
+        float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float2 vf = kFp8 ? factor[kKeys / 2 + 8 * j + 4 * k + c] : make_float2(1.0f, 1.0f);
+        for (int j = 0; j < kGroups; ++j) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float e0 = ex2_mufu(s[2 * j + k][2 * h] - m_use[h]);
-            const float e1 = ex2_mufu(s[2 * j + k][2 * h + 1] - m_use[h]);
-            l[h] += e0 + e1;
-            pa[2 * k + h] = kFp8 ? pack_f16x2(e0 * vf.x, e1 * vf.y) : pack_bf16x2(e0, e1);
+          for (int e = 0; e < 4; ++e) {
+            float x = s[n][j][e] * row_scale[n][e & 1];
+            if (kFp8) x *= fac[j][e >> 1].x;
+            if (masked && key0 + 16 * j + 8 * (e >> 1) + g >= row_lim[n][e & 1]) x = -INFINITY;
+            s[n][j][e] = x;
+          }
+          mx[0] = max3(mx[0], s[n][j][0], s[n][j][2]);
+          mx[1] = max3(mx[1], s[n][j][1], s[n][j][3]);
+        }
+        if (__any_sync(0xffffffffu, mx[0] > m[n][0] + kThreshold || mx[1] > m[n][1] + kThreshold)) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int d = 4; d < 32; d *= 2) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], d));
+            const float top = fmaxf(m[n][e], mx[e]);
+            const float f = top == -INFINITY ? 1.0f : ex2_mufu(m[n][e] - top);      // 0 from a maximum of -inf
+            m[n][e] = top;
+            l[n][e] *= f;
+            ones[n][e] *= f;
+#pragma unroll
+            for (int d = 0; d < kSteps; ++d) {
+              acc[n][d][e] *= f;
+              acc[n][d][2 + e] *= f;
+            }
           }
         }
-        uint32_t keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+        const float use[2] = {m[n][0] == -INFINITY ? 0.0f : m[n][0], m[n][1] == -INFINITY ? 0.0f : m[n][1]};
+#pragma unroll
+        for (int j = 0; j < kGroups; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float e0 = ex2_mufu(s[n][j][2 * h] - use[0]), e1 = ex2_mufu(s[n][j][2 * h + 1] - use[1]);
+            l[n][0] += e0;
+            l[n][1] += e1;
+            pb[n][j][h] = transpose8x8(kFp8 ? pack_f16x2(e0 * fac[j][h].y, e1 * fac[j][h].y) : pack_bf16x2(e0, e1));
+          }
+      }
+#pragma unroll
+      for (int j = 0; j < kGroups; ++j) {
+        uint32_t keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};      // keys 2 c, 2 c + 1 and 2 c + 8, 2 c + 9
         if (ragged) {
-          const int n = n_left - 16 * j - 2 * c;
-          keep[0] = (n > 0 ? 0x0000FFFFu : 0u) | (n > 1 ? 0xFFFF0000u : 0u);
-          keep[1] = (n > 8 ? 0x0000FFFFu : 0u) | (n > 9 ? 0xFFFF0000u : 0u);
+          const int k = n_left - 16 * j - 2 * c;
+          keep[0] = (k > 0 ? 0x0000FFFFu : 0u) | (k > 1 ? 0xFFFF0000u : 0u);
+          keep[1] = (k > 8 ? 0x0000FFFFu : 0u) | (k > 9 ? 0xFFFF0000u : 0u);
         }
         if (!kFp8) {
           // the weights' sum as they are rounded, for the division, so that the
           // weights used add up to one: a product with ones
-          mma16816(ones, pa, 0x3F803F80u, 0x3F803F80u);
+          const uint32_t one[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
 #pragma unroll
-          for (int d = 0; d < D / 16; ++d) {
+          for (int n = 0; n < kTiles; ++n) mma16816(ones[n], one, pb[n][j][0], pb[n][j][1]);
+#pragma unroll
+          for (int d = 0; d < kSteps; ++d) {
+            // keys 0-7 at pieces 2 d and 2 d + 1, then keys 8-15
             uint32_t b[4];
-            ldsm4_t(piece<D, kFp8>(vt, 16 * j + (lane & 15), 2 * d + (lane >> 4)), b);
+            ldsm4_t(piece<D, kFp8, kKeys>(vt, 16 * j + (lane & 7) + (lane >> 4) * 8, 2 * d + ((lane >> 3) & 1)), b);
             if (ragged) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) b[e] &= keep[e & 1];
+              for (int e = 0; e < 4; ++e) b[e] &= keep[e >> 1];
             }
-            mma16816(acc[2 * d], pa, b[0], b[1]);
-            mma16816(acc[2 * d + 1], pa, b[2], b[3]);
+#pragma unroll
+            for (int n = 0; n < kTiles; ++n) mma16816(acc[n][d], b, pb[n][j][0], pb[n][j][1]);
           }
         } else {
-          // a word holds D columns 2 n and 2 n + 1 of two keys: the even bytes
-          // are one column tile's operand, the odd bytes another's
+          // a word holds D columns 2 g and 2 g + 1 of two keys: the even bytes
+          // are row g of the tile, the odd bytes row g + 8
 #pragma unroll
-          for (int d = 0; d < D / 16; d += 2) {
+          for (int d = 0; d < kSteps; d += 2) {
+            // keys 0-7, 8-15 at piece d, then at d + 1
             uint32_t b[4];
-            ldsm4_t(piece<D, kFp8>(vt, 16 * j + (lane & 15), d + (lane >> 4)), b);
+            ldsm4_t(piece<D, kFp8, kKeys>(vt, 16 * j + (lane & 15), d + (lane >> 4)), b);
             if (ragged) {
 #pragma unroll
               for (int e = 0; e < 4; ++e) b[e] &= keep[e & 1];
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) b[e] = __byte_perm(b[e], 0u, 0x3120);     // even bytes, odd bytes
-            mma16816_f16(acc[2 * d], pa, e4m3_f16x2(b[0]), e4m3_f16x2(b[1]));
-            mma16816_f16(acc[2 * d + 1], pa, e4m3_f16x2(b[0] >> 16), e4m3_f16x2(b[1] >> 16));
-            mma16816_f16(acc[2 * d + 2], pa, e4m3_f16x2(b[2]), e4m3_f16x2(b[3]));
-            mma16816_f16(acc[2 * d + 3], pa, e4m3_f16x2(b[2] >> 16), e4m3_f16x2(b[3] >> 16));
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t a[4] = {e4m3_f16x2(b[2 * k]), e4m3_f16x2(b[2 * k] >> 16), e4m3_f16x2(b[2 * k + 1]),
+                                     e4m3_f16x2(b[2 * k + 1] >> 16)};
+#pragma unroll
+              for (int n = 0; n < kTiles; ++n) mma16816_f16(acc[n][d + k], a, pb[n][j][0], pb[n][j][1]);
+            }
           }
         }
       }
@@ -600,47 +641,47 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Merge of the warps' states: row maxima and sums first, then the outputs,
     // as many warps at a time as the merge rows hold.
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int n = 0; n < kTiles; ++n)
 #pragma unroll
-      for (int d = 1; d < 4; d *= 2) l[h] += __shfl_xor_sync(0xffffffffu, l[h], d);
-      if (c == 0) {
-        const int i = warp * kRows + g + 8 * h;
-        st_m[i] = m[h];
-        st_l[i] = l[h];
-        // FP16 weights (E4M3 pages) are off by 2^-12 at most: their own sum is
-        // not worth keeping
-        st_lr[i] = kFp8 ? l[h] : ones[2 * h];
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int d = 4; d < 32; d *= 2) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], d);
+        if (g == 0) {
+          const int i = warp * kRows + 8 * n + 2 * c + e;
+          st_m[i] = m[n][e];
+          st_l[i] = l[n][e];
+          // FP16 weights (E4M3 pages) are off by 2^-12 at most: their own sum
+          // is not worth keeping
+          st_lr[i] = kFp8 ? l[n][e] : ones[n][e];
+        }
       }
-    }
     __syncthreads();
-    float top[2], f[2];
     // acc's unit; an empty share has none
-    const float unit = kFp8 && v_top > 0 ? __uint_as_float((uint32_t)max(v_top - 14, 0) << 23) : 1.0f;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      top[h] = -INFINITY;
-      for (int w = 0; w < kWarps; ++w) top[h] = fmaxf(top[h], st_m[w * kRows + g + 8 * h]);
-      f[h] = top[h] == -INFINITY ? 1.0f : ex2_mufu(m[h] - top[h]);
-    }
-    const int pad = rows <= 4 ? 4 : rows <= 8 ? 8 : 16;
-    const int slots = L::kMergeRows / pad;       // warps that write at a time
+    const float unit = kFp8 && v_top > 0 ? __uint_as_float((uint32_t)max(v_top - kWeightUp, 0) << 23) : 1.0f;
+    const int pad = rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+    const int slots = min(kWarps, L::kMergeRows / pad);       // warps that write at a time
     for (int w0 = 0; w0 < kWarps; w0 += slots) {
       if (warp >= w0 && warp < w0 + slots) {
         float* to = merge + (warp - w0) * pad * L::kPitch;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (g + 8 * h >= rows) continue;
-          float* r = to + (g + 8 * h) * L::kPitch;
+        for (int n = 0; n < kTiles; ++n)
 #pragma unroll
-          for (int j = 0; j < D / 8; ++j) {
-            // BF16: columns 8 j + 2 c, + 1; E4M3: of tiles 2 i, 2 i + 1, columns 16 i + 4 c + {0, 2}, {1, 3}
-            const int d0 = kFp8 ? 16 * (j / 2) + 4 * c + (j & 1) : 8 * j + 2 * c;
-            const int d1 = kFp8 ? d0 + 2 : d0 + 1;
-            const float y0 = acc[j][2 * h] * f[h] * unit, y1 = acc[j][2 * h + 1] * f[h] * unit;
-            r[d0] = w0 ? r[d0] + y0 : y0;
-            r[d1] = w0 ? r[d1] + y1 : y1;
+          for (int e = 0; e < 2; ++e) {
+            const int row = 8 * n + 2 * c + e;
+            if (row >= rows) continue;
+            float top = -INFINITY;
+            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, st_m[w * kRows + row]);
+            const float f = (top == -INFINITY ? 1.0f : ex2_mufu(m[n][e] - top)) * unit;
+            float* r = to + row * L::kPitch;
+#pragma unroll
+            for (int d = 0; d < kSteps; ++d)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int col = 16 * d + (kFp8 ? 2 * g + h : 8 * h + g);
+                const float y = acc[n][d][2 * h + e] * f;
+                r[col] = w0 ? r[col] + y : y;
+              }
           }
-        }
       }
       __syncthreads();
     }
@@ -660,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           lrt += st_lr[w * kRows + r] * fw;
         }
         float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int s = 0; s < min(slots, kWarps); ++s) {
+        for (int s = 0; s < slots; ++s) {
           const float* from = merge + (s * pad + r) * L::kPitch + d;
           y.x += from[0];
           y.y += from[1];
@@ -679,9 +720,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             p.lse[li] = lt == 0.0f ? -INFINITY : (mt + log2f(lt)) * 0.693147180559945309f;
           }
         } else {
-          *reinterpret_cast<float4*>(Part<D>::out(p.part, slot) + r * D + d) = y;
+          *reinterpret_cast<float4*>(W::out(p.part, slot) + r * D + d) = y;
           if (d == 0) {
-            float* stat = Part<D>::stat(p.part, slot) + r * Part<D>::kStat;
+            float* stat = W::stat(p.part, slot) + r * W::kStat;
             stat[0] = mt;
             stat[1] = lt;
             stat[2] = lrt;
@@ -704,18 +745,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Joins the partial results of the units that borders between thread blocks
 // cut: block x + 1 looks at border x + 1 and does the unit whose first cut that
 // border is.
-template <int D, int kKeys>
-__global__ void __launch_bounds__(kThreads) combine_kernel(const PagedAttnParams p, int ctas) {
+constexpr int kJoinThreads = 256;
+template <int D, int kKeys, int kRows>
+__global__ void __launch_bounds__(kJoinThreads) combine_kernel(const PagedAttnParams p, int ctas) {
+  using W = Part<D, kRows>;
   __shared__ long long pre[kMaxPackedSeqs + 1];
-  __shared__ long long sums[kThreads / 32];
-  const long long total = build_line<kThreads, kKeys>(p, pre, sums);
+  __shared__ long long sums[kJoinThreads / 32];
+  const long long total = build_line<kJoinThreads, kKeys, kRows>(p, pre, sums);
   const int G = active_ctas(total, ctas);
   const int c = blockIdx.x + 1;
   // before any exit, so that this grid ends after the main one
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (c >= G) return;
   const long long t = stretch(total, c, G);
-  Walk<kKeys> w;
+  Walk<kKeys, kRows> w;
   w.begin(p, pre, t, total);
   const long long start = t - w.kb, end = start + w.nblk;
   const long long t_prev = stretch(total, c - 1, G);
@@ -724,19 +767,19 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const PagedAttnParams
   int last = c;                                  // parts: slot `first`, then slots 2 c .. 2 last
   while (last + 1 < G && stretch(total, last + 1, G) < end) ++last;
   const int rows = w.rows(p);
-  for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
+  for (int i = threadIdx.x; i < rows * (D / 4); i += kJoinThreads) {
     const int r = i / (D / 4), d = i % (D / 4) * 4;
-    float mt = Part<D>::stat(p.part, first)[r * Part<D>::kStat];
-    for (int k = c; k <= last; ++k) mt = fmaxf(mt, Part<D>::stat(p.part, 2 * k)[r * Part<D>::kStat]);
+    float mt = W::stat(p.part, first)[r * W::kStat];
+    for (int k = c; k <= last; ++k) mt = fmaxf(mt, W::stat(p.part, 2 * k)[r * W::kStat]);
     float lt = 0.0f, lrt = 0.0f;
     float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int k = c - 1; k <= last; ++k) {
       const int slot = k < c ? first : 2 * k;
-      const float* stat = Part<D>::stat(p.part, slot) + r * Part<D>::kStat;
+      const float* stat = W::stat(p.part, slot) + r * W::kStat;
       const float f = mt == -INFINITY ? 1.0f : ex2_mufu(stat[0] - mt);
       lt += stat[1] * f;
       lrt += stat[2] * f;
-      const float4 x = *reinterpret_cast<const float4*>(Part<D>::out(p.part, slot) + r * D + d);
+      const float4 x = *reinterpret_cast<const float4*>(W::out(p.part, slot) + r * D + d);
       y.x += x.x * f;
       y.y += x.y * f;
       y.z += x.z * f;
@@ -754,9 +797,9 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const PagedAttnParams
   }
 }
 
-template <int D, bool kFp8>
+template <int D, bool kFp8, int kTiles>
 fa_status launch_inst(const PagedAttnLaunch& L, cudaStream_t stream) {
-  using Lay = Layout<D, kFp8>;
+  using Lay = Layout<D, kFp8, kTiles>;
   const int page_size = 1 << L.p.s.page_shift;
   const long long page_heads = (long long)L.p.s.num_pages * L.p.s.Hkv;
   const int box = page_size < Lay::kKeys ? page_size : Lay::kKeys;
@@ -764,34 +807,45 @@ fa_status launch_inst(const PagedAttnLaunch& L, cudaStream_t stream) {
   fa_status st;
   if ((st = make_tmap_pages(&tk, L.k_pages, page_heads, page_size, D, kFp8, box)) != FA_OK) return st;
   if ((st = make_tmap_pages(&tv, L.v_pages, page_heads, page_size, D, kFp8, box)) != FA_OK) return st;
-  auto kern = decode_kernel<D, kFp8>;
+  auto kern = decode_kernel<D, kFp8, kTiles>;
   if ((st = prepare_kernel(reinterpret_cast<const void*>(kern), Lay::kBytes)) != FA_OK) return st;
   const int ctas = L.p.num_ctas;
-  kern<<<ctas, kThreads, Lay::kBytes, stream>>>(tk, tv, L.p);
+  kern<<<ctas, Lay::kThreads, Lay::kBytes, stream>>>(tk, tv, L.p);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
   if (ctas > 1) {
     // the joining kernel works out its borders while the main one still runs
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(ctas - 1);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, combine_kernel<D, Lay::kKeys>, L.p, ctas) != cudaSuccess) return FA_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, combine_kernel<D, Lay::kKeys, Lay::kRows>, L.p, ctas) != cudaSuccess) return FA_ERR_CUDA;
   }
   return FA_OK;
 }
 
+// As few tiles of 8 rows as hold a sequence's rows.
+template <int D, bool kFp8>
+fa_status launch_tiles(const PagedAttnLaunch& L, cudaStream_t stream) {
+  const long long rows = (long long)L.p.max_q * L.p.group;
+  if (rows <= 8) return launch_inst<D, kFp8, 1>(L, stream);
+  if (rows <= 16) return launch_inst<D, kFp8, 2>(L, stream);
+  return launch_inst<D, kFp8, 4>(L, stream);
+}
+
 }  // namespace pdec
 
-size_t paged_decode_workspace(int D) { return D == 128 ? pdec::Part<128>::bytes() : pdec::Part<64>::bytes(); }
+size_t paged_decode_workspace(int D) {
+  return D == 128 ? pdec::Part<128, 32>::bytes() : pdec::Part<64, 32>::bytes();
+}
 
 fa_status launch_paged_decode(const PagedAttnLaunch& L, cudaStream_t stream) {
-  if (L.D == 128) return L.fp8 ? pdec::launch_inst<128, true>(L, stream) : pdec::launch_inst<128, false>(L, stream);
-  return L.fp8 ? pdec::launch_inst<64, true>(L, stream) : pdec::launch_inst<64, false>(L, stream);
+  if (L.D == 128) return L.fp8 ? pdec::launch_tiles<128, true>(L, stream) : pdec::launch_tiles<128, false>(L, stream);
+  return L.fp8 ? pdec::launch_tiles<64, true>(L, stream) : pdec::launch_tiles<64, false>(L, stream);
 }
 
 fa_status paged_decode_take_device_error() {
