@@ -20,10 +20,13 @@
 //     stretches of it.  A unit cut by a border leaves partial results in the
 //     workspace, at most two per thread block, and the combine kernel joins
 //     them.  Sequences of any mixture of lengths load all SMs alike.
-//   * Pipeline.  Each warp walks the key blocks of the stretch that are its
-//     turn, with a ring of its own in shared memory, which its lane 0 fills by
-//     TMA (the pages' rows, swizzled for ldmatrix); no warp waits for another
-//     until the unit's end, where the warps' softmax states are merged.
+//   * Pipeline.  One warp looks up the pages of the stretch's blocks, 32 at a
+//     time and on into the next units.  The other warps take the blocks in turn
+//     and each refills by TMA the slots of the ring in shared memory that it
+//     empties (the pages' rows, swizzled for ldmatrix): one thread issues a TMA
+//     load in some 150 cycles, too slow to feed an SM alone (313 us for 64 x 4096
+//     BF16 keys, against 172).  No warp waits for another until the unit's end,
+//     where their softmax states are merged.
 //   * E4M3 pages are widened in registers on the way to the tensor cores, to
 //     FP16, which holds every code and which one instruction makes of a pair (to
 //     BF16 it takes five).  The queries become FP16 by a power of two of each
@@ -47,7 +50,7 @@ constexpr float kThreshold = 8.0f;   // lazy rescaling, log2 units
 // below 2^14, and keep FP16's full precision down to 2^-20 of the maximum.
 constexpr int kWeightUp = 6;
 
-enum Site { kSiteSeqs = 1, kSitePage, kSiteRing };
+enum Site { kSiteSeqs = 1, kSitePage, kSiteFull, kSitePlaced, kSiteTaken, kSiteMerged };
 
 // Layout of the workspace: per slot the rows' unnormalised outputs, then per
 // slot and row the maximum (log2 units) and the two sums.
@@ -62,29 +65,33 @@ struct Part {
   static constexpr size_t bytes() { return (size_t)2 * kMaxCtas * (kSlotFloats + kRows * kStat) * sizeof(float); }
 };
 
-// kTiles: tiles of 8 rows.  12 warps with up to 168 registers hide more latency
-// than 8; the 32-row kernel's accumulators leave room for 8.
+// kTiles: tiles of 8 rows.  11 computing warps with up to 168 registers hide
+// more latency than 7; with more than one tile they would spill.
 template <int D, bool kFp8, int kTiles>
 struct Layout {
-  static constexpr int kWarps = kTiles == 4 ? 8 : 12;
-  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kWarps = kTiles == 1 ? 11 : 7;       // with the looking-up one, a multiple of 4
+  static constexpr int kThreads = (kWarps + 1) * 32;         // and the warp that looks up pages
   static constexpr int kRows = 8 * kTiles;
   // Keys of a block, at most two pages: stages of 8 KB of keys and values (4 KB
   // for E4M3 at D = 64) keep enough bytes in flight with few stages.
   static constexpr int kKeys = D == 128 && !kFp8 ? 16 : 32;
   static constexpr int kTile = kKeys * D * (kFp8 ? 1 : 2);        // keys or values of a block
   static constexpr int kStage = 2 * kTile;
-  static constexpr int kStages = 196608 / (kWarps * kStage);
+  static constexpr int kRingBytes = 184320;
+  static constexpr int kSlots = kRingBytes / (kWarps * kStage) * kWarps;   // of the ring; warp w takes those = w mod kWarps
+  static constexpr int kBatches = 4;                              // of 32 looked-up blocks
   static constexpr int kPitch = D + 4;                            // floats of a merge row
-  static constexpr int kMergeRows = 32;                           // rows of all merge slots
+  static constexpr int kRound = kTiles == 1 ? 4 : 8;              // rows that are merged at a time
+  static constexpr int kMergeFloats = kWarps * kRound * kPitch;   // a round's outputs of all warps
   static constexpr int kRing = 0;
-  static constexpr int kScales = kRing + kWarps * kStages * kStage;   // E4M3: scale bytes of a stage's keys, values
-  static constexpr int kFactors = kScales + (kFp8 ? kWarps * kStages * 2 * kKeys : 0);   // a block's, as floats
+  static constexpr int kScales = kRing + kSlots * kStage;   // E4M3: scale bytes of a stage's keys, values
+  static constexpr int kFactors = kScales + (kFp8 ? kSlots * 2 * kKeys : 0);   // a block's, as floats
   static constexpr int kMerge = kFactors + (kFp8 ? kWarps * 2 * kKeys * 4 : 0);
-  static constexpr int kStats = kMerge + kMergeRows * kPitch * 4;     // m, l, lr of [warp][row]
-  static constexpr int kPre = kStats + 3 * kWarps * kRows * 4;        // prefix of blocks, [B + 1]
+  static constexpr int kStats = kMerge + kMergeFloats * 4;        // m, l, lr of [row in round][warp]
+  static constexpr int kPre = (kStats + 3 * kWarps * kRound * 4 + 7) / 8 * 8;   // prefix of blocks, [B + 1]
   static constexpr int kBars = kPre + (kMaxPackedSeqs + 1) * 8 + 8;
-  static constexpr int kMisc = kBars + kWarps * kStages * 8;
+  static constexpr int kPlaces = (kBars + kSlots * 8 + 2 * kBatches * 8 + 8 + 15) / 16 * 16;    // where blocks lie
+  static constexpr int kMisc = kPlaces + kBatches * 32 * 16;
   static constexpr int kBytes = kMisc + 64 + kSmemAlignSlack;
   static_assert(kBytes <= 232448, "dynamic shared memory above the 227 KB per-CTA limit");
 };
@@ -206,6 +213,11 @@ struct Walk {
     }
     count = (int)(left < nblk ? left : nblk);
   }
+  // Token and head of the tile's first row.
+  FA_DEV void first_row(const PagedAttnParams& p, int& t, int& j) const {
+    t = tile * kRows / p.group;
+    j = tile * kRows - t * p.group;
+  }
   FA_DEV int rows(const PagedAttnParams& p) const { return min(kRows, s.n * p.group - tile * kRows); }
   // Keys that the tile's last row sees.
   FA_DEV int seen(const PagedAttnParams& p) const {
@@ -297,16 +309,18 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
   const int c = lane % 4, g = lane / 4;       // column pair and row of the fragments
   long long* pre = reinterpret_cast<long long*>(smem + L::kPre);
   float* merge = reinterpret_cast<float*>(smem + L::kMerge);
-  float* st_m = reinterpret_cast<float*>(smem + L::kStats);
-  float* st_l = st_m + kWarps * kRows;
-  float* st_lr = st_l + kWarps * kRows;
+  float* stats = reinterpret_cast<float*>(smem + L::kStats);
   const uint32_t abort = sbase + L::kMisc;
-  const uint32_t ring = sbase + L::kRing + warp * L::kStages * L::kStage;
-  const uint32_t scales = sbase + L::kScales + warp * L::kStages * 2 * kKeys;
-  const uint32_t bars = sbase + L::kBars + warp * L::kStages * 8;
+  // barriers: a slot is loaded; a batch of places is looked up, is used up; the
+  // merge rows are free
+  const uint32_t full = sbase + L::kBars, placed = full + 8 * L::kSlots, taken = placed + 8 * L::kBatches;
+  const uint32_t merged = taken + 8 * L::kBatches;
+  int4* places = reinterpret_cast<int4*>(smem + L::kPlaces);
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kWarps * L::kStages; ++i) mbar_init(sbase + L::kBars + 8 * i, 1);
+    for (int i = 0; i < L::kSlots + L::kBatches; ++i) mbar_init(full + 8 * i, 1);
+    for (int i = 0; i < L::kBatches; ++i) mbar_init(taken + 8 * i, 32);
+    mbar_init(merged, kWarps);
     st_shared(abort, 0);
     fence_barrier_init();
     tma_prefetch_desc(&tm_k);
@@ -319,106 +333,138 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
   if ((int)blockIdx.x >= G) return;
   const long long t0 = stretch(total, blockIdx.x, G), t1 = stretch(total, blockIdx.x + 1, G);
 
-  // The walk that issues loads runs ahead of the one that consumes them.
-  Walk<kKeys, kRows> in, at;
-  in.begin(p, pre, t0, t1);
-  at = in;
-  int in_i = warp, in_vis = in.visible(p);       // next block of this warp in the segment
-  int in_page = 0, in_page_i = -1;               // page numbers, one per lane, of the warp's next blocks
-  int in_stage = 0;
-  const int box_shift = min(p.s.page_shift, kKeys == 32 ? 5 : 4);    // rows of a box; one or two boxes a block
-  const int two = kKeys >> box_shift == 2 ? 1 : 0;
-  // Issues the warp's next block, if there is one.  The whole warp calls it.
-  auto issue = [&]() {
-    while (in_i >= in_vis) {
-      in.next(p);
-      if (!in.more()) {
-        in_vis = 0x7fffffff;                     // never again
-        in_i = in_vis;
+  // The stretch's visible blocks are numbered through; block q goes through ring
+  // slot q mod kSlots.
+  Walk<kKeys, kRows> at;
+  at.begin(p, pre, t0, t1);
+
+  const int box_shift = min(p.s.page_shift, kKeys == 32 ? 5 : 4);    // rows of a box
+  const int two = kKeys >> box_shift == 2;                            // two boxes a block, else one
+  constexpr int kEnd = -2;                                             // in place of a page: no more blocks
+
+  if (warp == kWarps) {
+    // ---- looks up where blocks lie: (page, head) and row of the block's boxes
+    int i = 0, vis = at.visible(p), past = 0;
+    uint32_t batch = 0;
+    while (past < 2) {       // until a whole batch lies behind the end
+      int4 place = make_int4(kEnd, kEnd, 0, 0);
+      if (!at.more()) ++past;
+      for (int filled = 0; filled < 32 && at.more();) {
+        const int take = min(32 - filled, vis - i);
+        if (lane >= filled && lane < filled + take) {
+          int ph[2] = {-1, -1}, off[2] = {0, 0};      // -1: outside the tensor maps, reads as zeros
+          for (int j = 0; j <= two; ++j) {
+            const int key = (at.kb + i + lane - filled) * kKeys + (j << box_shift);
+            if (key >= at.s.L) break;
+            const int page = p.s.block_table[(size_t)at.b * p.s.max_pages + (key >> p.s.page_shift)];
+            if (page < 0 || page >= p.s.num_pages)
+              paged::record_bad_input(&g_err, kSitePage);
+            else
+              ph[j] = page * p.s.Hkv + at.head;
+            off[j] = key & ((1 << p.s.page_shift) - 1);
+          }
+          place = make_int4(ph[0], ph[1], off[0], off[1]);
+        }
+        filled += take;
+        i += take;
+        if (i == vis) {
+          at.next(p);
+          i = 0;
+          vis = at.more() ? at.visible(p) : 0;
+        }
+      }
+      const int b = batch % L::kBatches;
+      if (!mbar_wait_bounded(taken + 8 * b, (batch / L::kBatches & 1) ^ 1, abort, &g_err, kSiteTaken, p.wait_limit_ns))
         break;
-      }
-      in_i = warp;
-      in_vis = in.visible(p);
-      in_page_i = -1;
+      places[b * 32 + lane] = place;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(placed + 8 * b);
+      ++batch;
     }
-    if (in_vis == 0x7fffffff) return;
-    const int k = in_i / kWarps;                 // the warp's k-th block of the segment
-    if (in_page_i < 0 || k - in_page_i >= 32 >> two) {
-      in_page_i = k;
-      const int i = in_i + (lane >> two) * kWarps;
-      const int key = (in.kb + i) * kKeys + ((lane & two) << box_shift);
-      in_page = -1;                              // outside the tensor maps: reads as zeros
-      if (i < in_vis && key < in.s.L) {
-        in_page = p.s.block_table[(size_t)in.b * p.s.max_pages + (key >> p.s.page_shift)];
-        if (in_page < 0 || in_page >= p.s.num_pages) {
-          paged::record_bad_input(&g_err, kSitePage);
-          in_page = -1;
-        }
-      }
-    }
-    const int from = (k - in_page_i) << two;
-    const int page0 = __shfl_sync(0xffffffffu, in_page, from), page1 = __shfl_sync(0xffffffffu, in_page, from + two);
+    return;
+  }
+
+  // Loads block q into its slot.  The whole warp calls it.
+  auto load = [&](uint32_t q) {
+    const int b = q / 32 % L::kBatches;
+    if (!mbar_wait_bounded(placed + 8 * b, q / (32 * L::kBatches) & 1, abort, &g_err, kSitePlaced, p.wait_limit_ns)) return;
     if (lane == 0) {
-      const uint32_t bar = bars + 8 * in_stage;
-      mbar_arrive_expect_tx(bar, 2 * L::kTile + (kFp8 ? 2 * kKeys : 0));
-      for (int j = 0; j <= two; ++j) {
-        const int off = ((in.kb + in_i) * kKeys + (j << box_shift)) & ((1 << p.s.page_shift) - 1);
-        const int page = j ? page1 : page0;
-        const int ph = page < 0 ? -1 : page * p.s.Hkv + in.head;
-        const uint32_t dst = ring + in_stage * L::kStage + (j << box_shift) * (kFp8 ? D : 128);
+      const int4 place = places[q % (32 * L::kBatches)];
+      mbar_arrive(taken + 8 * b);
+      if (place.x != kEnd) {
+        const uint32_t slot = q % L::kSlots, bar = full + 8 * slot;
+        mbar_arrive_expect_tx(bar, 2 * L::kTile + (kFp8 ? 2 * kKeys : 0));
+        for (int j = 0; j <= two; ++j) {
+          const int ph = j ? place.y : place.x, off = j ? place.w : place.z;
+          const uint32_t dst = sbase + L::kRing + slot * L::kStage + (j << box_shift) * (kFp8 ? D : 128);
 #pragma unroll
-        for (int h = 0; h < (kFp8 ? 1 : D / 64); ++h) {
-          tma_load_3d(dst + h * kKeys * 128, &tm_k, bar, h * 64, off, ph);
-          tma_load_3d(dst + L::kTile + h * kKeys * 128, &tm_v, bar, h * 64, off, ph);
-        }
-        if (kFp8) {
-          const size_t row = ((size_t)max(ph, 0) << p.s.page_shift) + off;
-          const uint32_t sc = scales + in_stage * 2 * kKeys + (j << box_shift);
-          bulk_load(sc, p.k_scale + row, 1 << box_shift, bar);
-          bulk_load(sc + kKeys, p.v_scale + row, 1 << box_shift, bar);
+          for (int h = 0; h < (kFp8 ? 1 : D / 64); ++h) {
+            tma_load_3d(dst + h * kKeys * 128, &tm_k, bar, h * 64, off, ph);
+            tma_load_3d(dst + L::kTile + h * kKeys * 128, &tm_v, bar, h * 64, off, ph);
+          }
+          if (kFp8) {
+            const size_t row = ((size_t)max(ph, 0) << p.s.page_shift) + off;
+            const uint32_t sc = sbase + L::kScales + slot * 2 * kKeys + (j << box_shift);
+            bulk_load(sc, p.k_scale + row, 1 << box_shift, bar);
+            bulk_load(sc + kKeys, p.v_scale + row, 1 << box_shift, bar);
+          }
         }
       }
     }
-    in_i += kWarps;
-    in_stage = in_stage + 1 == L::kStages ? 0 : in_stage + 1;
+    __syncwarp();
   };
 #pragma unroll 1
-  for (int i = 0; i < L::kStages; ++i) issue();
+  for (int q = warp; q < L::kSlots; q += kWarps) load(q);
 
-  int stage = 0;
-  uint32_t phase = 0;
-  bool lost = false;      // a wait ran out: no more loads, no more results
+  // Q of a segment's tile as B fragments: row 8 n + g of tile n, d = 16 s + 2 c,
+  // + 1 and + 8, + 9.  E4M3: four consecutive values at 16 s + 4 c instead, which
+  // is how a word of four codes of a key lies in its fragment.
+  uint32_t qf[kTiles][kSteps][2];
+  const float inv_group = 1.0f / (float)p.group;
+  // (token, head) of row j0 + x of a token's group: exact for the small numbers here
+  auto tokens_on = [&](int j0_plus_x) { return (int)(((float)j0_plus_x + 0.5f) * inv_group); };
+  auto load_q = [&](const Walk<kKeys, kRows>& w) {
+    const int rows = w.rows(p);
+    int tok0, j0;
+    w.first_row(p, tok0, j0);
+#pragma unroll
+    for (int n = 0; n < kTiles; ++n) {
+      const int r = j0 + 8 * n + g;
+      const bool valid = 8 * n + g < rows;
+      const int t = tokens_on(r), j = r - t * p.group;
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) +
+                                 ((size_t)(w.s.q0 + tok0 + t) * p.Hq + w.head * p.group + j) * D;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        uint2 x = make_uint2(0u, 0u);
+        if (valid) {
+          if (kFp8) {
+            x = *reinterpret_cast<const uint2*>(src + 16 * s + 4 * c);
+          } else {
+            x.x = *reinterpret_cast<const uint32_t*>(src + 16 * s + 2 * c);
+            x.y = *reinterpret_cast<const uint32_t*>(src + 16 * s + 8 + 2 * c);
+          }
+        }
+        qf[n][s][0] = x.x;
+        qf[n][s][1] = x.y;
+      }
+    }
+  };
+  load_q(at);
+
+  uint32_t q0 = 0;        // number of the segment's first block
+  uint32_t round = 0;     // of merging
+  bool lost = false;      // a wait ran out: no more results
   while (at.more()) {
     const int rows = at.rows(p), row0 = at.tile * kRows;
+    int tok0, j0;
+    at.first_row(p, tok0, j0);
     const int vis = at.visible(p);
-    // Q of the tile as B fragments: row 8 n + g of tile n, d = 16 s + 2 c, + 1 and
-    // + 8, + 9.  E4M3: four consecutive values at 16 s + 4 c instead, which is
-    // how a word of four codes of a key lies in its fragment.
-    uint32_t qf[kTiles][kSteps][2];
     // rows 8 n + 2 c + e of the tile, whose scores this lane gets:
     int row_lim[kTiles][2];          // keys that they see
     float row_scale[kTiles][2];      // what their scores are multiplied by, for log2 units
 #pragma unroll
     for (int n = 0; n < kTiles; ++n) {
-      const int r = row0 + 8 * n + g;
-      const bool valid = 8 * n + g < rows;
-      const int t = r / p.group, j = r - t * p.group;
-      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) +
-                                 ((size_t)(at.s.q0 + t) * p.Hq + at.head * p.group + j) * D;
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        uint2 w = make_uint2(0u, 0u);
-        if (valid) {
-          if (kFp8) {
-            w = *reinterpret_cast<const uint2*>(src + 16 * s + 4 * c);
-          } else {
-            w.x = *reinterpret_cast<const uint32_t*>(src + 16 * s + 2 * c);
-            w.y = *reinterpret_cast<const uint32_t*>(src + 16 * s + 8 + 2 * c);
-          }
-        }
-        qf[n][s][0] = w.x;
-        qf[n][s][1] = w.y;
-      }
       float scale = p.scale_log2;
       if (kFp8) {
         uint32_t top = 0;
@@ -443,7 +489,7 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
       for (int e = 0; e < 2; ++e) {
         row_scale[n][e] = kFp8 ? __shfl_sync(0xffffffffu, scale, (2 * c + e) * 4) : scale;
         const int in_tile = 8 * n + 2 * c + e;
-        row_lim[n][e] = in_tile >= rows ? 0 : p.causal ? at.s.L - at.s.n + (row0 + in_tile) / p.group + 1 : at.s.L;
+        row_lim[n][e] = in_tile >= rows ? 0 : p.causal ? at.s.L - at.s.n + tok0 + tokens_on(j0 + in_tile) + 1 : at.s.L;
       }
     }
     // O^T: columns of V on the rows, tile rows on the columns (2 c, 2 c + 1 here)
@@ -464,18 +510,19 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
     int v_top = 0;      // E4M3: the largest scale byte of a value so far; acc counts in 2^(v_top - 127 - kWeightUp)
 
 #pragma unroll 1
-    for (int i = warp; i < vis && !lost; i += kWarps) {
-      if (!mbar_wait_bounded(bars + 8 * stage, phase, abort, &g_err, kSiteRing, p.wait_limit_ns)) {
+    for (int i = (warp + kWarps - q0 % kWarps) % kWarps; i < vis && !lost; i += kWarps) {
+      const uint32_t slot = (q0 + i) % L::kSlots;
+      if (!mbar_wait_bounded(full + 8 * slot, (q0 + i) / L::kSlots & 1, abort, &g_err, kSiteFull, p.wait_limit_ns)) {
         lost = true;
         break;
       }
-      const uint32_t kt = ring + stage * L::kStage, vt = kt + L::kTile;
+      const uint32_t kt = sbase + L::kRing + slot * L::kStage, vt = kt + L::kTile;
       const int key0 = (at.kb + i) * kKeys;
       float2* factor = reinterpret_cast<float2*>(smem + L::kFactors) + warp * kKeys;     // of a key and its value
       if (kFp8) {
         // lane i: the factors of key i.  Values' scales are taken relative to
         // the largest so far.
-        const uint8_t* bytes = smem + (scales - sbase) + stage * 2 * kKeys;
+        const uint8_t* bytes = smem + L::kScales + slot * 2 * kKeys;
         const bool mine = key0 + lane < at.s.L;          // behind the end: anything
         const uint32_t kb = bytes[lane], vb = mine ? bytes[kKeys + lane] : 0u;
         const int block_top = __reduce_max_sync(0xffffffffu, vb == 255u ? 0u : vb);
@@ -535,7 +582,7 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
       const bool ragged = n_left < kKeys;
       // a block that every row sees whole needs no mask (rows of the tile see
       // at least the first row's keys)
-      const bool masked = key0 + kKeys > (p.causal ? at.s.L - at.s.n + row0 / p.group + 1 : at.s.L);
+      const bool masked = key0 + kKeys > (p.causal ? at.s.L - at.s.n + tok0 + 1 : at.s.L);
       uint32_t pb[kTiles][kGroups][2];        // P^T as B fragments
 #pragma unroll
       for (int n = 0; n < kTiles; ++n) {
@@ -630,112 +677,107 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
           }
         }
       }
-      __syncwarp();       // every lane is done with the stage
-      issue();
-      if (++stage == L::kStages) {
-        stage = 0;
-        phase ^= 1;
-      }
+      __syncwarp();       // every lane is done with the slot
+      load(q0 + i + L::kSlots);
     }
+    q0 += vis;
 
-    // Merge of the warps' states: row maxima and sums first, then the outputs,
-    // as many warps at a time as the merge rows hold.
-#pragma unroll
-    for (int n = 0; n < kTiles; ++n)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-#pragma unroll
-        for (int d = 4; d < 32; d *= 2) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], d);
-        if (g == 0) {
-          const int i = warp * kRows + 8 * n + 2 * c + e;
-          st_m[i] = m[n][e];
-          st_l[i] = l[n][e];
-          // FP16 weights (E4M3 pages) are off by 2^-12 at most: their own sum
-          // is not worth keeping
-          st_lr[i] = kFp8 ? l[n][e] : ones[n][e];
-        }
-      }
-    __syncthreads();
-    // acc's unit; an empty share has none
-    const float unit = kFp8 && v_top > 0 ? __uint_as_float((uint32_t)max(v_top - kWeightUp, 0) << 23) : 1.0f;
-    const int pad = rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
-    const int slots = min(kWarps, L::kMergeRows / pad);       // warps that write at a time
-    for (int w0 = 0; w0 < kWarps; w0 += slots) {
-      if (warp >= w0 && warp < w0 + slots) {
-        float* to = merge + (warp - w0) * pad * L::kPitch;
-#pragma unroll
-        for (int n = 0; n < kTiles; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int row = 8 * n + 2 * c + e;
-            if (row >= rows) continue;
-            float top = -INFINITY;
-            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, st_m[w * kRows + row]);
-            const float f = (top == -INFINITY ? 1.0f : ex2_mufu(m[n][e] - top)) * unit;
-            float* r = to + row * L::kPitch;
-#pragma unroll
-            for (int d = 0; d < kSteps; ++d)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const int col = 16 * d + (kFp8 ? 2 * g + h : 8 * h + g);
-                const float y = acc[n][d][2 * h + e] * f;
-                r[col] = w0 ? r[col] + y : y;
-              }
-          }
-      }
-      __syncthreads();
-    }
-    // The rows' results: final when the segment is the whole unit, else partial.
+    // the next segment's queries come while this one is finished
+    Walk<kKeys, kRows> after = at;
+    after.next(p);
+    if (after.more()) load_q(after);
+
+    // Merge of the warps' states, kRound rows at a time: every warp writes its
+    // rows and their statistics, and after a barrier the rows are summed up and
+    // written out.  The next round's writes wait for the last reader, mostly
+    // long gone by then.
     const bool whole = at.kb == 0 && at.count == at.nblk;
     const bool first = at.left == t1 - t0;
     const int slot = 2 * blockIdx.x + (first ? 0 : 1);
-    if (!lost && !ld_shared_volatile(abort)) {
-      for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
-        const int r = i / (D / 4), d = i % (D / 4) * 4;
-        float mt = -INFINITY;
-        for (int w = 0; w < kWarps; ++w) mt = fmaxf(mt, st_m[w * kRows + r]);
-        float lt = 0.0f, lrt = 0.0f;
-        for (int w = 0; w < kWarps; ++w) {
-          const float fw = mt == -INFINITY ? 1.0f : ex2_mufu(st_m[w * kRows + r] - mt);
-          lt += st_l[w * kRows + r] * fw;
-          lrt += st_lr[w * kRows + r] * fw;
+    // acc's unit; an empty share has none
+    const float unit = kFp8 && v_top > 0 ? __uint_as_float((uint32_t)max(v_top - kWeightUp, 0) << 23) : 1.0f;
+#pragma unroll
+    for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int d = 4; d < 32; d *= 2) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], d);
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += L::kRound, ++round) {
+      if (!mbar_wait_bounded(merged, round & 1 ^ 1, abort, &g_err, kSiteMerged, p.wait_limit_ns)) lost = true;
+      float* buf = merge;
+      float* st_m = stats;
+      float* st_l = st_m + kWarps * L::kRound;
+      float* st_lr = st_l + kWarps * L::kRound;
+#pragma unroll
+      for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int row = 8 * n + 2 * c + e - r0;
+          if (row < 0 || row >= min(L::kRound, rows - r0)) continue;
+          if (g == 0) {
+            st_m[row * kWarps + warp] = m[n][e];
+            st_l[row * kWarps + warp] = l[n][e];
+            // FP16 weights (E4M3 pages) are off by 2^-12 at most: their own sum
+            // is not worth keeping
+            st_lr[row * kWarps + warp] = kFp8 ? l[n][e] : ones[n][e];
+          }
+          float* to = buf + (warp * L::kRound + row) * L::kPitch;
+#pragma unroll
+          for (int d = 0; d < kSteps; ++d)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) to[16 * d + (kFp8 ? 2 * g + h : 8 * h + g)] = acc[n][d][2 * h + e] * unit;
         }
-        float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int s = 0; s < slots; ++s) {
-          const float* from = merge + (s * pad + r) * L::kPitch + d;
-          y.x += from[0];
-          y.y += from[1];
-          y.z += from[2];
-          y.w += from[3];
+      named_barrier(1, kWarps * 32);
+      if (ld_shared_volatile(abort)) lost = true;
+      // final when the segment is the whole unit, else partial
+      for (int i = threadIdx.x; i < min(L::kRound, rows - r0) * (D / 2) && !lost; i += kWarps * 32) {
+        const int r = i / (D / 2), d = i % (D / 2) * 2;
+        float fw[kWarps], mt = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          fw[w] = st_m[r * kWarps + w];
+          mt = fmaxf(mt, fw[w]);
+        }
+        float lt = 0.0f, lrt = 0.0f;
+        float2 y = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float f = mt == -INFINITY ? 1.0f : ex2_mufu(fw[w] - mt);
+          lt += st_l[r * kWarps + w] * f;
+          lrt += st_lr[r * kWarps + w] * f;
+          const float2 x = *reinterpret_cast<const float2*>(buf + (w * L::kRound + r) * L::kPitch + d);
+          y.x += x.x * f;
+          y.y += x.y * f;
         }
         if (whole) {
           const float inv = lrt == 0.0f ? 0.0f : 1.0f / lrt;
-          const int row = row0 + r, t = row / p.group, head = at.head * p.group + row - t * p.group;
+          const int row = row0 + r0 + r, t = row / p.group, head = at.head * p.group + row - t * p.group;
           const int tok = at.s.q0 + t;
-          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + ((size_t)tok * p.Hq + head) * D + d) =
-              make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
+          *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + ((size_t)tok * p.Hq + head) * D + d) =
+              pack_bf16x2(y.x * inv, y.y * inv);
           if (d == 0) {
-            const size_t li = p.s.cu ? (size_t)head * p.s.Sn + tok
-                                     : ((size_t)at.b * p.Hq + head) * p.s.Sn + t;
+            const size_t li = p.s.cu ? (size_t)head * p.s.Sn + tok : ((size_t)at.b * p.Hq + head) * p.s.Sn + t;
             p.lse[li] = lt == 0.0f ? -INFINITY : (mt + log2f(lt)) * 0.693147180559945309f;
           }
         } else {
-          *reinterpret_cast<float4*>(W::out(p.part, slot) + r * D + d) = y;
+          *reinterpret_cast<float2*>(W::out(p.part, slot) + (r0 + r) * D + d) = y;
           if (d == 0) {
-            float* stat = W::stat(p.part, slot) + r * W::kStat;
+            float* stat = W::stat(p.part, slot) + (r0 + r) * W::kStat;
             stat[0] = mt;
             stat[1] = lt;
             stat[2] = lrt;
           }
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(merged);
     }
-    __syncthreads();       // the merge rows and the statistics are free again
-    at.next(p);
+    at = after;
   }
 
-  // After a give-up, loads already in flight land before the shared memory
-  // they target is released.
+  // After a give-up, loads already in flight land before the shared memory they
+  // target is released.
   if (ld_shared_volatile(abort)) {
     const uint64_t w0 = globaltimer_ns();
     while (globaltimer_ns() - w0 < 2000000ull) __nanosleep(1000);
