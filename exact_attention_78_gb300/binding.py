@@ -105,7 +105,7 @@ def _stream(stream):
 
 
 def _check_bf16(name, t):
-    if not t.is_cuda or t.dtype != torch.bfloat16 or not t.is_contiguous():
+    if not t.is_cuda or t.dtype is not torch.bfloat16 or not t.is_contiguous():
         raise ValueError("%s must be a contiguous CUDA bfloat16 tensor" % name)
 
 
@@ -286,32 +286,40 @@ def _adr(t):
     return None if t is None else t.data_ptr()
 
 
+# A small call spends a few microseconds on the GPU, and as many on the host for
+# every twenty or so attributes that are looked at.  So the checks below test
+# everything in one expression and say what was wrong only when it is.
+
+def _bad(name, what, device=None):
+    raise ValueError("%s must be %s%s" % (name, what, "" if device is None else " on %s" % device))
+
+
 def _check_int32(name, t, device, dims):
-    if t.device != device or t.dtype != torch.int32 or not t.is_contiguous() or t.dim() != dims:
-        raise ValueError("%s must be a contiguous CUDA int32 tensor with %d dimension(s) on %s" % (name, dims, device))
+    if not (t.dtype is torch.int32 and t.is_cuda and t.device == device and t.is_contiguous() and t.dim() == dims):
+        _bad(name, "a contiguous CUDA int32 tensor with %d dimension(s)" % dims, device)
 
 
-def _cache_args(x_heads, D, device, k_pages, v_pages, k_scale, v_scale, block_table):
+def _cache_args(heads, D, device, k_pages, v_pages, k_scale, v_scale, block_table):
     """Checks the tensors of a cache; (num_pages, Hkv, page_size, max_pages)."""
-    fp8 = k_scale is not None or v_scale is not None
-    dtype = torch.float8_e4m3fn if fp8 else torch.bfloat16
-    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        if not t.is_cuda or t.device != device or t.dtype is not dtype or not t.is_contiguous() or t.dim() != 4:
-            raise ValueError("%s must be a contiguous CUDA %s tensor [num_pages, Hkv, page_size, D] on %s"
-                             % (name, dtype, device))
-    if k_pages.shape != v_pages.shape:
-        raise ValueError("v_pages must have k_pages' shape %s" % (tuple(k_pages.shape),))
-    num_pages, Hkv, page_size, Dp = k_pages.shape
+    dtype = torch.bfloat16 if k_scale is None and v_scale is None else torch.float8_e4m3fn
+    shape = k_pages.shape
+    if not (k_pages.dtype is dtype and v_pages.dtype is dtype and k_pages.is_cuda and k_pages.device == device
+            and v_pages.device == device and len(shape) == 4 and v_pages.shape == shape and k_pages.is_contiguous()
+            and v_pages.is_contiguous()):
+        _bad("k_pages and v_pages", "contiguous CUDA %s tensors of one shape [num_pages, Hkv, page_size, D]" % dtype,
+             device)
+    num_pages, Hkv, page_size, Dp = shape
     if Dp != D:
         raise ValueError("the pages' head dimension is %d, not %d" % (Dp, D))
-    if x_heads is not None and x_heads != Hkv:
-        raise ValueError("the pages have %d heads, k and v %d" % (Hkv, x_heads))
-    if fp8:
-        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-            if (t is None or t.device != device or t.dtype != torch.uint8 or not t.is_contiguous()
-                    or tuple(t.shape) != (num_pages, Hkv, page_size)):
-                raise ValueError("%s must be a contiguous CUDA uint8 tensor of shape %s on %s"
-                                 % (name, (num_pages, Hkv, page_size), device))
+    if heads is not None and heads != Hkv:
+        raise ValueError("the pages have %d heads, k and v %d" % (Hkv, heads))
+    if dtype is not torch.bfloat16:
+        want = shape[:3]
+        if not (k_scale is not None and v_scale is not None and k_scale.dtype is torch.uint8
+                and v_scale.dtype is torch.uint8 and k_scale.device == device and v_scale.device == device
+                and k_scale.shape == want and v_scale.shape == want and k_scale.is_contiguous()
+                and v_scale.is_contiguous()):
+            _bad("k_scale and v_scale", "contiguous CUDA uint8 tensors of shape %s" % (tuple(want),), device)
     _check_int32("block_table", block_table, device, 2)
     return num_pages, Hkv, page_size, block_table.shape[1]
 
@@ -319,22 +327,33 @@ def _cache_args(x_heads, D, device, k_pages, v_pages, k_scale, v_scale, block_ta
 def _new_tokens(name, x, B, cu_seqlens):
     """Sn of the C ABI for new tokens x, dense [B, Sn, H, D] or packed [Sn, H, D]."""
     _check_bf16(name, x)
-    if x.dim() != (4 if cu_seqlens is None else 3):
+    shape = x.shape
+    if len(shape) != (4 if cu_seqlens is None else 3):
         raise ValueError("%s is [B, Sn, H, D], or [total, H, D] with cu_seqlens" % name)
     if cu_seqlens is None:
-        if x.shape[0] != B:
-            raise ValueError("%s has %d sequences, the block table %d" % (name, x.shape[0], B))
-        return x.shape[1]
-    _check_int32("cu_seqlens", cu_seqlens, x.device, 1)
+        if shape[0] != B:
+            raise ValueError("%s has %d sequences, the block table %d" % (name, shape[0], B))
+        return shape[1]
+    _check_offsets(cu_seqlens, x.device, B)
+    return shape[0]
+
+
+def _check_offsets(cu_seqlens, device, B):
+    _check_int32("cu_seqlens", cu_seqlens, device, 1)
     if cu_seqlens.numel() != B + 1:
         raise ValueError("cu_seqlens has %d offsets for %d sequences" % (cu_seqlens.numel(), B))
-    return x.shape[0]
 
 
 def _check_seq_lens(seq_lens, device, B):
     _check_int32("seq_lens", seq_lens, device, 1)
     if seq_lens.numel() != B:
         raise ValueError("seq_lens has %d lengths for %d sequences" % (seq_lens.numel(), B))
+
+
+@functools.lru_cache(maxsize=256)
+def _c_ints(values):
+    """A C array of ints; the library reads it before its call returns."""
+    return (ctypes.c_int * len(values))(*values)
 
 
 def rope(q, k, positions, sections=None, base=10000.0, restart=False, interleaved=False, inverse=False, q_out=None,
@@ -349,45 +368,45 @@ def rope(q, k, positions, sections=None, base=10000.0, restart=False, interleave
     and k.  Returns (q_out, k_out)."""
     lib = load_library()
     _check_bf16("q", q)
-    if q.dim() < 2:
+    shape, device = q.shape, q.device
+    if len(shape) < 2:
         raise ValueError("q is [..., H, D]")
-    lead, Hq, D = tuple(q.shape[:-2]), q.shape[-2], q.shape[-1]
+    lead, Hq, D = shape[:-2], shape[-2], shape[-1]
     Hkv = 0
     if k is not None:
         _check_bf16("k", k)
-        _check_same_device(q.device, k=k)
-        if tuple(k.shape[:-2]) != lead or k.shape[-1] != D:
-            raise ValueError("k is [..., H, D] with q's leading shape and D")
+        if k.device != device or k.shape[:-2] != lead or k.shape[-1] != D:
+            raise ValueError("k is [..., H, D] with q's leading shape, D and device")
         Hkv = k.shape[-2]
     elif k_out is not None:
         raise ValueError("k_out without k")
-    if positions.device != q.device or positions.dtype != torch.int32 or not positions.is_contiguous():
-        raise ValueError("positions must be a contiguous CUDA int32 tensor on %s" % q.device)
-    axes = 1 if tuple(positions.shape) == lead else positions.shape[0] if positions.dim() else 0
-    if tuple(positions.shape) not in (lead, (axes,) + lead):
-        raise ValueError("positions are %s, with a first dimension for the axes" % (lead,))
+    if not (positions.dtype is torch.int32 and positions.device == device and positions.is_contiguous()):
+        _bad("positions", "a contiguous CUDA int32 tensor", device)
+    axes = 1
+    if positions.shape != lead:
+        if positions.shape[1:] != lead or positions.dim() == 0:
+            raise ValueError("positions are %s, with a first dimension for the axes" % (tuple(lead),))
+        axes = positions.shape[0]
     if sections is None:
         if axes != 1:
             raise ValueError("%d axes need sections" % axes)
-        sections = [D // 2]
-    sections = [int(x) for x in sections]
+        sections = (D // 2,)
     if len(sections) != axes:
         raise ValueError("%d sections for %d axes" % (len(sections), axes))
-    for name, t, like in (("q_out", q_out, q), ("k_out", k_out, k)):
-        if t is not None:
-            _check_out(name, t, like.shape, torch.bfloat16, q.device)
-    tokens = 1
-    for n in lead:
-        tokens *= n
-    with _on(q.device, stream) as s:
+    if q_out is not None:
+        _check_out("q_out", q_out, shape, torch.bfloat16, device)
+    if k_out is not None:
+        _check_out("k_out", k_out, k.shape, torch.bfloat16, device)
+    with _on(device, stream) as s:
         if q_out is None:
             q_out = torch.empty_like(q)
         if k is not None and k_out is None:
             k_out = torch.empty_like(k)
-        st = lib.fa_rope(_adr(q), _adr(k), _adr(q_out), _adr(k_out), tokens, Hq, Hkv, D, _adr(positions), axes,
-                         (ctypes.c_int * len(sections))(*sections), float(base), int(bool(restart)),
-                         int(bool(interleaved)), int(bool(inverse)), s)
-    _check(st, "fa_rope")
+        st = lib.fa_rope(q.data_ptr(), _adr(k), q_out.data_ptr(), _adr(k_out), lead.numel(), Hq, Hkv, D,
+                         positions.data_ptr(), axes, _c_ints(tuple(sections)), base, bool(restart),
+                         bool(interleaved), bool(inverse), s)
+    if st:
+        raise FAError(st, "fa_rope")
     return q_out, k_out
 
 
@@ -399,21 +418,20 @@ def cache_write(k, v, k_pages, v_pages, block_table, seq_lens, cu_seqlens=None, 
     pages; or float8_e4m3fn pages with uint8 scales [num_pages, Hkv,
     page_size], quantised on the way."""
     lib = load_library()
-    B = block_table.shape[0]
+    B, device, shape = block_table.shape[0], k.device, k.shape
     Sn = _new_tokens("k", k, B, cu_seqlens)
     _check_bf16("v", v)
-    _check_same_device(k.device, v=v)
-    if v.shape != k.shape:
-        raise ValueError("v must have k's shape %s" % (tuple(k.shape),))
-    D = k.shape[-1]
-    num_pages, Hkv, page_size, max_pages = _cache_args(k.shape[-2], D, k.device, k_pages, v_pages, k_scale, v_scale,
-                                                       block_table)
-    _check_seq_lens(seq_lens, k.device, B)
-    with _on(k.device, stream) as s:
-        st = lib.fa_cache_write(_adr(k), _adr(v), _adr(k_pages), _adr(v_pages), _adr(k_scale), _adr(v_scale), B, Hkv,
-                                Sn, D, num_pages, page_size, max_pages, _adr(block_table), _adr(seq_lens),
-                                _adr(cu_seqlens), s)
-    _check(st, "fa_cache_write")
+    if v.shape != shape or v.device != device:
+        raise ValueError("v must have k's shape %s and device" % (tuple(shape),))
+    num_pages, Hkv, page_size, max_pages = _cache_args(shape[-2], shape[-1], device, k_pages, v_pages, k_scale,
+                                                       v_scale, block_table)
+    _check_seq_lens(seq_lens, device, B)
+    with _on(device, stream) as s:
+        st = lib.fa_cache_write(k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _adr(k_scale),
+                                _adr(v_scale), B, Hkv, Sn, shape[-1], num_pages, page_size, max_pages,
+                                block_table.data_ptr(), seq_lens.data_ptr(), _adr(cu_seqlens), s)
+    if st:
+        raise FAError(st, "fa_cache_write")
 
 
 def cache_read(k_pages, v_pages, block_table, cu_seqlens, total, k_scale=None, v_scale=None, k_out=None, v_out=None,
@@ -427,22 +445,22 @@ def cache_read(k_pages, v_pages, block_table, cu_seqlens, total, k_scale=None, v
     device, D, B = k_pages.device, k_pages.shape[3], block_table.shape[0]
     num_pages, Hkv, page_size, max_pages = _cache_args(None, D, device, k_pages, v_pages, k_scale, v_scale,
                                                        block_table)
-    _check_int32("cu_seqlens", cu_seqlens, device, 1)
-    if cu_seqlens.numel() != B + 1:
-        raise ValueError("cu_seqlens has %d offsets for %d sequences" % (cu_seqlens.numel(), B))
-    shape = (int(total), Hkv, D)
-    for name, t in (("k_out", k_out), ("v_out", v_out)):
-        if t is not None:
-            _check_out(name, t, shape, torch.bfloat16, device)
+    _check_offsets(cu_seqlens, device, B)
+    shape = (total, Hkv, D)
+    if k_out is not None:
+        _check_out("k_out", k_out, shape, torch.bfloat16, device)
+    if v_out is not None:
+        _check_out("v_out", v_out, shape, torch.bfloat16, device)
     with _on(device, stream) as s:
         if k_out is None:
             k_out = torch.empty(shape, dtype=torch.bfloat16, device=device)
         if v_out is None:
             v_out = torch.empty(shape, dtype=torch.bfloat16, device=device)
-        st = lib.fa_cache_read(_adr(k_pages), _adr(v_pages), _adr(k_scale), _adr(v_scale), _adr(k_out), _adr(v_out),
-                               B, Hkv, int(total), D, num_pages, page_size, max_pages, _adr(block_table),
-                               _adr(cu_seqlens), s)
-    _check(st, "fa_cache_read")
+        st = lib.fa_cache_read(k_pages.data_ptr(), v_pages.data_ptr(), _adr(k_scale), _adr(v_scale), k_out.data_ptr(),
+                               v_out.data_ptr(), B, Hkv, total, D, num_pages, page_size, max_pages,
+                               block_table.data_ptr(), cu_seqlens.data_ptr(), s)
+    if st:
+        raise FAError(st, "fa_cache_read")
     return k_out, v_out
 
 
@@ -462,35 +480,37 @@ def fwd_paged(q, k_pages, v_pages, block_table, seq_lens, causal=True, scale=Non
     one sequence (packed; `total` by default, which is right but may choose a
     slower kernel)."""
     lib = load_library()
-    B = block_table.shape[0]
+    B, device = block_table.shape[0], q.device
     Sn = _new_tokens("q", q, B, cu_seqlens)
-    Hq, D = q.shape[-2], q.shape[-1]
-    num_pages, Hkv, page_size, max_pages = _cache_args(None, D, q.device, k_pages, v_pages, k_scale, v_scale,
+    Hq, D = q.shape[-2:]
+    num_pages, Hkv, page_size, max_pages = _cache_args(None, D, device, k_pages, v_pages, k_scale, v_scale,
                                                        block_table)
-    _check_seq_lens(seq_lens, q.device, B)
-    max_q = Sn if cu_seqlens is None or max_q is None else int(max_q)
-    if scale is None:
-        scale = D ** -0.5
-    lse_shape = (Hq, Sn) if cu_seqlens is not None else (B, Hq, Sn)
+    _check_seq_lens(seq_lens, device, B)
+    if cu_seqlens is None:
+        max_q, lse_shape = Sn, (B, Hq, Sn)
+    else:
+        max_q, lse_shape = Sn if max_q is None else max_q, (Hq, Sn)
     if out is not None:
-        _check_out("out", out, q.shape, torch.bfloat16, q.device)
+        _check_out("out", out, q.shape, torch.bfloat16, device)
     if lse is not None:
-        _check_out("lse", lse, lse_shape, torch.float32, q.device)
-    if workspace is not None and (workspace.device != q.device or not workspace.is_contiguous()):
-        raise ValueError("workspace must be a contiguous tensor on %s" % q.device)
-    with _on(q.device, stream) as s:
+        _check_out("lse", lse, lse_shape, torch.float32, device)
+    if workspace is not None and (workspace.device != device or not workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous tensor on %s" % device)
+    with _on(device, stream) as s:
         if out is None:
             out = torch.empty_like(q)
         if lse is None:
-            lse = torch.empty(lse_shape, dtype=torch.float32, device=q.device)
+            lse = torch.empty(lse_shape, dtype=torch.float32, device=device)
         if workspace is None:
             need = fwd_paged_workspace_size(B, Hq, Hkv, Sn, D, cu_seqlens is not None, max_q)
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
-        st = lib.fa_fwd_paged(_adr(q), _adr(k_pages), _adr(v_pages), _adr(k_scale), _adr(v_scale), _adr(out),
-                              _adr(lse), B, Hq, Hkv, Sn, D, num_pages, page_size, max_pages, int(bool(causal)),
-                              float(scale), _adr(block_table), _adr(seq_lens), _adr(cu_seqlens), max_q,
-                              _adr(workspace), workspace.numel() * workspace.element_size(), s)
-    _check(st, "fa_fwd_paged")
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+        st = lib.fa_fwd_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _adr(k_scale), _adr(v_scale),
+                              out.data_ptr(), lse.data_ptr(), B, Hq, Hkv, Sn, D, num_pages, page_size, max_pages,
+                              bool(causal), D ** -0.5 if scale is None else scale, block_table.data_ptr(),
+                              seq_lens.data_ptr(), _adr(cu_seqlens), max_q, workspace.data_ptr(),
+                              workspace.numel() * workspace.element_size(), s)
+    if st:
+        raise FAError(st, "fa_fwd_paged")
     return out, lse
 
 

@@ -785,58 +785,81 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
 }
 
 // Joins the partial results of the units that borders between thread blocks
-// cut: block x + 1 looks at border x + 1 and does the unit whose first cut that
-// border is.
-constexpr int kJoinThreads = 256;
+// cut: block (x, y) looks at border x + 1 and does rows [8 y, 8 y + 8) of the
+// unit whose first cut that border is.  One long sequence has parts of every
+// thread block: their statistics and rows are loaded together, not one after
+// the other.
+constexpr int kJoinThreads = 256, kJoinRows = 8;
 template <int D, int kKeys, int kRows>
 __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const PagedAttnParams p, int ctas) {
   using W = Part<D, kRows>;
   __shared__ long long pre[kMaxPackedSeqs + 1];
   __shared__ long long sums[kJoinThreads / 32];
+  __shared__ float st_m[kMaxCtas + 1][kJoinRows], st_l[kMaxCtas + 1][kJoinRows], st_lr[kMaxCtas + 1][kJoinRows];
+  __shared__ float inv[kJoinRows];
   const long long total = build_line<kJoinThreads, kKeys, kRows>(p, pre, sums);
   const int G = active_ctas(total, ctas);
   const int c = blockIdx.x + 1;
+  Walk<kKeys, kRows> w;
+  long long start = 0, end = 0;
+  int first = -1;
+  if (c < G) {
+    const long long t = stretch(total, c, G), t_prev = stretch(total, c - 1, G);
+    w.begin(p, pre, t, total);
+    start = t - w.kb;
+    end = start + w.nblk;
+    // no cut here, or not the unit's first: nothing to do
+    if (w.kb > 0 && t_prev <= start) first = 2 * (c - 1) + (t_prev == start ? 0 : 1);
+  }
   // before any exit, so that this grid ends after the main one
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (c >= G) return;
-  const long long t = stretch(total, c, G);
-  Walk<kKeys, kRows> w;
-  w.begin(p, pre, t, total);
-  const long long start = t - w.kb, end = start + w.nblk;
-  const long long t_prev = stretch(total, c - 1, G);
-  if (w.kb == 0 || t_prev > start) return;      // no cut here, or not the unit's first
-  const int first = 2 * (c - 1) + (t_prev == start ? 0 : 1);
-  int last = c;                                  // parts: slot `first`, then slots 2 c .. 2 last
-  while (last + 1 < G && stretch(total, last + 1, G) < end) ++last;
-  const int rows = w.rows(p);
-  for (int i = threadIdx.x; i < rows * (D / 4); i += kJoinThreads) {
-    const int r = i / (D / 4), d = i % (D / 4) * 4;
-    float mt = W::stat(p.part, first)[r * W::kStat];
-    for (int k = c; k <= last; ++k) mt = fmaxf(mt, W::stat(p.part, 2 * k)[r * W::kStat]);
-    float lt = 0.0f, lrt = 0.0f;
-    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int k = c - 1; k <= last; ++k) {
-      const int slot = k < c ? first : 2 * k;
-      const float* stat = W::stat(p.part, slot) + r * W::kStat;
-      const float f = mt == -INFINITY ? 1.0f : ex2_mufu(stat[0] - mt);
-      lt += stat[1] * f;
-      lrt += stat[2] * f;
-      const float4 x = *reinterpret_cast<const float4*>(W::out(p.part, slot) + r * D + d);
-      y.x += x.x * f;
-      y.y += x.y * f;
-      y.z += x.z * f;
-      y.w += x.w * f;
-    }
-    const float inv = lrt == 0.0f ? 0.0f : 1.0f / lrt;
-    const int row = w.tile * kRows + r, tk = row / p.group, head = w.head * p.group + row - tk * p.group;
-    const int tok = w.s.q0 + tk;
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + ((size_t)tok * p.Hq + head) * D + d) =
-        make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
-    if (d == 0) {
-      const size_t li = p.s.cu ? (size_t)head * p.s.Sn + tok : ((size_t)w.b * p.Hq + head) * p.s.Sn + tk;
-      p.lse[li] = lt == 0.0f ? -INFINITY : (mt + log2f(lt)) * 0.693147180559945309f;
-    }
+  const int row0 = blockIdx.y * kJoinRows;
+  const int rows = first < 0 ? 0 : min(kJoinRows, w.rows(p) - row0);
+  if (rows <= 0) return;
+  int parts = 2;                                 // slot `first`, then slots 2 c, 2 (c + 1), ...
+  while (c + parts - 1 < G && stretch(total, c + parts - 1, G) < end) ++parts;
+  auto slot_of = [&](int k) { return k == 0 ? first : 2 * (c + k - 1); };
+  for (int i = threadIdx.x; i < parts * kJoinRows; i += kJoinThreads) {
+    const int k = i / kJoinRows, r = i % kJoinRows;
+    if (r >= rows) continue;
+    const float4 st = *reinterpret_cast<const float4*>(W::stat(p.part, slot_of(k)) + (row0 + r) * W::kStat);
+    st_m[k][r] = st.x;
+    st_l[k][r] = st.y;
+    st_lr[k][r] = st.z;
   }
+  __syncthreads();
+  const int tile_row = w.tile * kRows + row0;
+  if ((int)threadIdx.x < rows) {
+    const int r = threadIdx.x;
+    float mt = -INFINITY, lt = 0.0f, lrt = 0.0f;
+    for (int k = 0; k < parts; ++k) mt = fmaxf(mt, st_m[k][r]);
+    for (int k = 0; k < parts; ++k) {
+      const float f = mt == -INFINITY ? 1.0f : ex2_mufu(st_m[k][r] - mt);
+      st_m[k][r] = f;                            // from here on the part's factor
+      lt += st_l[k][r] * f;
+      lrt += st_lr[k][r] * f;
+    }
+    inv[r] = lrt == 0.0f ? 0.0f : 1.0f / lrt;
+    const int tk = (tile_row + r) / p.group, head = w.head * p.group + tile_row + r - tk * p.group;
+    const size_t li = p.s.cu ? (size_t)head * p.s.Sn + w.s.q0 + tk : ((size_t)w.b * p.Hq + head) * p.s.Sn + tk;
+    p.lse[li] = lt == 0.0f ? -INFINITY : (mt + log2f(lt)) * 0.693147180559945309f;
+  }
+  __syncthreads();
+  const int r = threadIdx.x / (D / 4), d = threadIdx.x % (D / 4) * 4;
+  if (r >= rows) return;
+  float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+  for (int k = 0; k < parts; ++k) {
+    const float4 x = *reinterpret_cast<const float4*>(W::out(p.part, slot_of(k)) + (row0 + r) * D + d);
+    const float f = st_m[k][r];
+    y.x += x.x * f;
+    y.y += x.y * f;
+    y.z += x.z * f;
+    y.w += x.w * f;
+  }
+  const int tk = (tile_row + r) / p.group, head = w.head * p.group + tile_row + r - tk * p.group;
+  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + ((size_t)(w.s.q0 + tk) * p.Hq + head) * D + d) =
+      make_uint2(pack_bf16x2(y.x * inv[r], y.y * inv[r]), pack_bf16x2(y.z * inv[r], y.w * inv[r]));
 }
 
 template <int D, bool kFp8, int kTiles>
@@ -857,7 +880,7 @@ fa_status launch_inst(const PagedAttnLaunch& L, cudaStream_t stream) {
   if (ctas > 1) {
     // the joining kernel works out its borders while the main one still runs
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(ctas - 1);
+    cfg.gridDim = dim3(ctas - 1, Lay::kRows / kJoinRows);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr{};
