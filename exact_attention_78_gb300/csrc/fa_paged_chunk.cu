@@ -45,7 +45,7 @@ __device__ DeviceError g_err;
 constexpr int kBM = 128;      // rows of a tile
 constexpr int kBN = 128;      // keys of a block
 constexpr float kThreshold = 8.0f;   // lazy rescaling, log2 units
-constexpr int kMinStretch = 4;       // blocks
+constexpr int kMinStretch = 2;       // blocks: shorter ones cost more to join than they save
 
 enum Site {
   kSiteSeqs = 1, kSitePage, kSiteSegFull, kSiteSegEmpty, kSiteQEmpty, kSiteKvEmpty, kSiteKvFull, kSiteQFull, kSiteS,
@@ -146,10 +146,20 @@ struct Shared {
 
 FA_DEV int tile_tokens(int group) { return kBM / group; }
 
-// sum of floor((a i + b) / m) for i in [0, n); a, b >= 0, a n + b < 2^31 once
-// a and b are below m (Euclid's algorithm on the slope).
-FA_DEV long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
-  long long s = 0;
+// sum of floor((a i + b) / 128) for i in [0, n), n > 0; a, b >= 0, 128 n + 128 <
+// 2^32 (Euclid's algorithm on the slope).
+FA_DEV long long floor_sum_128(uint32_t n, uint32_t a, uint32_t b) {
+  // the first step, m = 128, without divisions; most tiles' slopes end there or
+  // one step later
+  long long s = (long long)n * (n - 1) / 2 * (a >> 7) + (long long)n * (b >> 7);
+  a &= 127u;
+  b &= 127u;
+  uint32_t m = a;
+  const uint32_t top0 = a * n + b;
+  if (top0 < 128u) return s;
+  n = top0 >> 7;
+  b = top0 & 127u;
+  a = 128u;
   while (n > 0) {
     if (a >= m) {
       s += (long long)n * (n - 1) / 2 * (a / m);
@@ -186,28 +196,24 @@ struct Seq {
     if (p == pairs) --p;
     const int e0 = L - n + t2;                                // end of pair 0's keys
     const int none = e0 <= 0 ? min(p, -e0 / t2 + 1) : 0;      // pairs that see no key
-    return last + none + (p > none ? floor_sum(p - none, kBN, t2, e0 + none * t2 + kBN - 1) : 0);
+    return last + none + (p > none ? floor_sum_128(p - none, t2, e0 + none * t2 + kBN - 1) : 0);
   }
   FA_DEV long long total() const { return prefix(pairs); }
   // Pairs run from the last (the longest under a mask) to the first: blocks of
-  // the i units before unit i of a head.
-  FA_DEV long long before(int i) const { return total() - prefix(pairs - i); }
+  // the i units before unit i of a head, all of which have `total`.
+  FA_DEV long long before(int i, long long total) const { return total - prefix(pairs - i); }
 };
-FA_DEV Seq seq_of(const PagedAttnParams& p, int b) {
+FA_DEV Seq seq_from(const PagedAttnParams& p, const paged::SeqRows& rows) {
   Seq r;
-  r.L = p.s.seq_lens[b];
-  if (p.s.cu) {
-    r.q0 = p.s.cu[b];
-    r.n = p.s.cu[b + 1] - r.q0;
-  } else {
-    r.q0 = b * p.s.Sn;
-    r.n = p.s.Sn;
-  }
+  r.L = rows.L;
+  r.n = rows.n;
+  r.q0 = rows.q0;
   r.t2 = 2 * tile_tokens(p.group);
   r.pairs = (r.n + r.t2 - 1) / r.t2;
   r.causal = p.causal != 0;
   return r;
 }
+FA_DEV Seq seq_of(const PagedAttnParams& p, int b) { return seq_from(p, paged::rows_of(p.s, b)); }
 
 // The work of a call: prefix tables over the sequences and where the whole
 // rounds end.
@@ -218,7 +224,7 @@ struct Line {
   int whole;          // units of the whole rounds
   long long t0, t1;   // the blocks of the others
   int G;              // stretches that they are cut into
-  FA_DEV long long stretch(int c) const { return t0 + (t1 - t0) * c / G; }
+  FA_DEV long long stretch(int c) const { return t0 + paged::div64((t1 - t0) * c, G); }
 };
 
 // Last b in [0, B) with table[b] <= x.
@@ -236,72 +242,31 @@ FA_DEV int last_at_most(const T* table, int B, T x) {
 // break the rules.
 FA_DEV Line build_line(const PagedAttnParams& p, long long* bpre, int* upre, long long* sums, int ctas) {
   Line line{bpre, upre, 0, 0, 0, 0, 0};
-  if (!paged::sequences_ok(p.s, p.max_q)) {
+  const bool ok = paged::prefix_sequences(
+      p.s, p.max_q,
+      [&](const paged::SeqRows& rows) {
+        const Seq s = seq_from(p, rows);
+        return paged::Work{s.total() * p.s.Hkv, s.pairs * p.s.Hkv};
+      },
+      bpre, upre, sums);
+  if (!ok) {
     if (blockIdx.x == 0 && threadIdx.x == 0) paged::record_bad_input(&g_err, kSiteSeqs);
     return line;
   }
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  long long carry_b = 0;
-  int carry_u = 0;
-  for (int b0 = 0; b0 < p.s.B; b0 += blockDim.x) {
-    const int b = b0 + threadIdx.x;
-    long long vb = 0;
-    int vu = 0;
-    if (b < p.s.B) {
-      const Seq s = seq_of(p, b);
-      if (s.n > 0) {
-        vu = s.pairs * p.s.Hkv;
-        vb = s.total() * p.s.Hkv;
-      }
-    }
-    long long ib = vb;
-    int iu = vu;
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-      const long long ob = __shfl_up_sync(0xffffffffu, ib, d);
-      const int ou = __shfl_up_sync(0xffffffffu, iu, d);
-      if (lane >= d) {
-        ib += ob;
-        iu += ou;
-      }
-    }
-    if (lane == 31) {
-      sums[2 * warp] = ib;
-      sums[2 * warp + 1] = iu;
-    }
-    __syncthreads();
-    long long before_b = carry_b + ib - vb;
-    int before_u = carry_u + iu - vu;
-    const int warps = blockDim.x / 32;
-    for (int w = 0; w < warps; ++w) {
-      if (w < warp) {
-        before_b += sums[2 * w];
-        before_u += (int)sums[2 * w + 1];
-      }
-      carry_b += sums[2 * w];
-      carry_u += (int)sums[2 * w + 1];
-    }
-    if (b < p.s.B) {
-      bpre[b] = before_b;
-      upre[b] = before_u;
-    }
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) {
-    bpre[p.s.B] = carry_b;
-    upre[p.s.B] = carry_u;
-  }
-  __syncthreads();
+  const int carry_u = upre[p.s.B];
   line.units = carry_u;
-  line.t1 = carry_b;
+  line.t1 = bpre[p.s.B];
   // a last round that is nearly full is not worth cutting
-  const int rest = carry_u % ctas;
+  const int rest = carry_u < ctas ? carry_u : carry_u % ctas;
   line.whole = rest * 10 >= ctas * 9 ? carry_u : carry_u - rest;
-  if (line.whole < carry_u) {
+  if (line.whole == 0) {
+    line.t0 = 0;
+  } else if (line.whole < carry_u) {
     const int b = last_at_most(upre, p.s.B, line.whole);
     const Seq s = seq_of(p, b);
     const int r = line.whole - upre[b], head = r / s.pairs;
-    line.t0 = bpre[b] + head * s.total() + s.before(r - head * s.pairs);
+    const long long total = s.total();
+    line.t0 = bpre[b] + head * total + s.before(r - head * s.pairs, total);
   } else {
     line.t0 = line.t1;
   }
@@ -321,19 +286,19 @@ FA_DEV Place find_place(const PagedAttnParams& p, const Line& line, long long t)
   const Seq s = seq_of(p, w.b);
   const long long per_head = s.total();
   long long r = t - line.bpre[w.b];
-  w.head = (int)(r / per_head);
+  w.head = (int)paged::div64(r, per_head);
   r -= w.head * per_head;
   const int lane = threadIdx.x % 32;
   int lo = 0, size = s.pairs;       // the unit is in [lo, lo + size)
   while (size > 1) {
     const int step = (size + 31) / 32, at = lo + lane * step;
-    const bool in = at < lo + size && s.before(at) <= r;
+    const bool in = at < lo + size && s.before(at, per_head) <= r;
     const int k = __popc(__ballot_sync(0xffffffffu, in)) - 1;
     size = min(step, size - k * step);
     lo += k * step;
   }
   w.i = lo;
-  w.start = t - r + s.before(lo);
+  w.start = t - r + s.before(lo, per_head);
   return w;
 }
 

@@ -98,66 +98,26 @@ struct Layout {
 
 // ------------------------------------------------------------ the work line --
 
-struct Seq {
-  int n, L, q0;     // new tokens, keys, first row of q
-};
-FA_DEV Seq seq_of(const PagedSeqs& s, int b) {
-  Seq r;
-  r.L = s.seq_lens[b];
-  if (s.cu) {
-    r.q0 = s.cu[b];
-    r.n = s.cu[b + 1] - r.q0;
-  } else {
-    r.q0 = b * s.Sn;
-    r.n = s.Sn;
-  }
-  return r;
-}
+using Seq = paged::SeqRows;
+FA_DEV Seq seq_of(const PagedSeqs& s, int b) { return paged::rows_of(s, b); }
 FA_DEV int tiles_of(int n, int group, int rows) { return (n * group + rows - 1) / rows; }
 // Blocks of a unit: at least one, so that rows without a key are written too.
 FA_DEV int blocks_of(int L, int keys) { return max(1, (L + keys - 1) / keys); }
 
 // Prefix sums of the sequences' blocks into pre[0 .. B]; returns their total,
 // 0 when the sequences break the rules.  All threads of the block.
-template <int kN, int kKeys, int kRows>
+template <int kKeys, int kRows>
 FA_DEV long long build_line(const PagedAttnParams& p, long long* pre, long long* warp_sums) {
-  const bool ok = paged::sequences_ok(p.s, p.max_q);
-  if (!ok) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) paged::record_bad_input(&g_err, kSiteSeqs);
-    return 0;
-  }
-  constexpr int kEach = (kMaxPackedSeqs + kN - 1) / kN;
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  long long v[kEach], sum = 0;
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int b = threadIdx.x * kEach + i;
-    v[i] = 0;
-    if (b < p.s.B) {
-      const Seq q = seq_of(p.s, b);
-      if (q.n > 0) v[i] = (long long)p.s.Hkv * tiles_of(q.n, p.group, kRows) * blocks_of(q.L, kKeys);
-    }
-    sum += v[i];
-  }
-  long long incl = sum;
-#pragma unroll
-  for (int d = 1; d < 32; d *= 2) {
-    const long long o = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += o;
-  }
-  if (lane == 31) warp_sums[warp] = incl;
-  __syncthreads();
-  long long before = incl - sum;
-  for (int w = 0; w < warp; ++w) before += warp_sums[w];
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int b = threadIdx.x * kEach + i;
-    before += v[i];
-    if (b < p.s.B) pre[b + 1] = before;
-  }
-  if (threadIdx.x == 0) pre[0] = 0;
-  __syncthreads();
-  return pre[p.s.B];
+  const bool ok = paged::prefix_sequences(
+      p.s, p.max_q,
+      [&](const Seq& q) {
+        const int tiles = tiles_of(q.n, p.group, kRows);
+        return paged::Work{(long long)p.s.Hkv * tiles * blocks_of(q.L, kKeys), 0};
+      },
+      pre, nullptr, warp_sums);
+  if (ok) return pre[p.s.B];
+  if (blockIdx.x == 0 && threadIdx.x == 0) paged::record_bad_input(&g_err, kSiteSeqs);
+  return 0;
 }
 
 // Thread blocks that share the line: no more than leave each 8 key blocks.
@@ -166,7 +126,7 @@ FA_DEV int active_ctas(long long total, int ctas) {
   return most < ctas ? (int)most : ctas;
 }
 // First block of stretch c of G.
-FA_DEV long long stretch(long long total, int c, int G) { return total * c / G; }
+FA_DEV long long stretch(long long total, int c, int G) { return paged::div64(total * c, G); }
 
 // A walk over the segments (the stretch's share of one unit) of [t0, t1).
 template <int kKeys, int kRows>
@@ -191,9 +151,9 @@ struct Walk {
     b = lo;
     load(p);
     const long long r = t0 - pre[b];
-    const long long unit = r / nblk;
+    const long long unit = paged::div64(r, nblk);
     kb = (int)(r - unit * nblk);
-    head = (int)(unit / tiles);
+    head = (int)paged::div64(unit, tiles);
     tile = (int)(unit - (long long)head * tiles);
     left = t1 - t0;
     count = (int)(left < nblk - kb ? left : nblk - kb);
@@ -326,7 +286,7 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
-  const long long total = build_line<kThreads, kKeys, kRows>(p, pre, reinterpret_cast<long long*>(merge));
+  const long long total = build_line<kKeys, kRows>(p, pre, reinterpret_cast<long long*>(merge));
   __syncthreads();
   const int G = active_ctas(total, gridDim.x);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -794,10 +754,10 @@ template <int D, int kKeys, int kRows>
 __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const PagedAttnParams p, int ctas) {
   using W = Part<D, kRows>;
   __shared__ long long pre[kMaxPackedSeqs + 1];
-  __shared__ long long sums[kJoinThreads / 32];
+  __shared__ long long sums[2 * kJoinThreads / 32];
   __shared__ float st_m[kMaxCtas + 1][kJoinRows], st_l[kMaxCtas + 1][kJoinRows], st_lr[kMaxCtas + 1][kJoinRows];
   __shared__ float inv[kJoinRows];
-  const long long total = build_line<kJoinThreads, kKeys, kRows>(p, pre, sums);
+  const long long total = build_line<kKeys, kRows>(p, pre, sums);
   const int G = active_ctas(total, ctas);
   const int c = blockIdx.x + 1;
   Walk<kKeys, kRows> w;

@@ -43,6 +43,98 @@ FA_DEV bool sequences_ok(const PagedSeqs& s, int max_new) {
   return __syncthreads_and(ok);
 }
 
+// New tokens, keys and first row of sequence b.
+struct SeqRows {
+  int n, L, q0;
+};
+FA_DEV SeqRows rows_of(const PagedSeqs& s, int b) {
+  SeqRows r;
+  r.L = s.seq_lens[b];
+  if (s.cu) {
+    r.q0 = s.cu[b];
+    r.n = s.cu[b + 1] - r.q0;
+  } else {
+    r.q0 = b * s.Sn;
+    r.n = s.Sn;
+  }
+  return r;
+}
+
+// Checks the sequences' offsets and lengths, and sums up their work: `work`
+// gives a sequence's {key blocks, units}, whose prefix sums go to bpre and (if
+// given) upre, [B + 1].  All threads of the block; false, in all of them, when
+// the rules are broken.  Every attention kernel starts with this, so that one
+// pass and two barriers have to do: the loads, the sums within warps and the
+// check share the first.  `sums`: two values per warp.
+struct Work {
+  long long blocks;
+  int units;
+};
+template <class F>
+FA_DEV bool prefix_sequences(const PagedSeqs& s, int max_new, F work, long long* bpre, int* upre, long long* sums) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int capacity = s.max_pages << s.page_shift;
+  Work carry{0, 0};
+  int ok = 1;
+  for (int b0 = 0; b0 < s.B; b0 += blockDim.x) {
+    const int b = b0 + threadIdx.x;
+    const int warps = (min(s.B - b0, (int)blockDim.x) + 31) / 32;      // with a sequence
+    Work own{0, 0}, incl;
+    if (b < s.B) {
+      const SeqRows r = rows_of(s, b);
+      bool fine = r.L >= 0 && r.L <= capacity;
+      if (s.cu) fine = fine && r.q0 >= 0 && r.n >= 0 && r.n <= max_new && r.q0 <= s.Sn - r.n && (b > 0 || r.q0 == 0);
+      if (fine && r.n > 0) own = work(r);
+      ok = ok && fine;
+    }
+    incl = own;
+    if (warp < warps) {
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const long long ob = __shfl_up_sync(0xffffffffu, incl.blocks, d);
+        const int ou = __shfl_up_sync(0xffffffffu, incl.units, d);
+        if (lane >= d) {
+          incl.blocks += ob;
+          incl.units += ou;
+        }
+      }
+      if (lane == 31) {
+        sums[2 * warp] = incl.blocks;
+        sums[2 * warp + 1] = incl.units;
+      }
+    }
+    ok = __syncthreads_and(ok);
+    Work before = carry;
+    for (int w = 0; w < warps; ++w) {
+      const long long sb = sums[2 * w];
+      const int su = (int)sums[2 * w + 1];
+      if (w < warp) {
+        before.blocks += sb;
+        before.units += su;
+      }
+      carry.blocks += sb;
+      carry.units += su;
+    }
+    if (b < s.B) {
+      bpre[b] = before.blocks + incl.blocks - own.blocks;
+      if (upre) upre[b] = before.units + incl.units - own.units;
+    }
+    if (b0 + (int)blockDim.x >= s.B && threadIdx.x == 0) {
+      bpre[s.B] = carry.blocks;
+      if (upre) upre[s.B] = carry.units;
+    }
+    __syncthreads();
+  }
+  return ok;
+}
+
+// a / b for a >= 0, b > 0: 64-bit division takes some hundred instructions, and
+// the numbers here mostly fit 32 bits.
+FA_DEV long long div64(long long a, long long b) {
+  if ((unsigned long long)(a | b) >> 32 == 0) return (unsigned)a / (unsigned)b;
+  return a / b;
+}
+
 // 2^e of a scale byte; NaN for the byte of a row without a finite scale.
 FA_DEV float scale_value(uint32_t byte) {
   return byte == 255u ? __int_as_float(0x7FC00000) : __uint_as_float(byte << 23);
