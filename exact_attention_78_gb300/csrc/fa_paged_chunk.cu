@@ -17,9 +17,9 @@
 //     products are those of BF16 pages.
 //   * Work.  Whole rounds of units, one per thread block, run in lockstep
 //     from the first key on, so that the pairs of a head share its keys in L2.
-//     The units left over are a line of key blocks that is cut into equal
-//     stretches, one per thread block; parts of a cut unit are joined by the
-//     combine kernel.  A few long chunks thus load all SMs.  A scheduler warp
+//     The units left over are a line of keys that is cut into equal stretches
+//     (at the key block before each border), one per thread block; parts of a
+//     cut unit are joined by the combine kernel.  A few long chunks thus load all SMs.  A scheduler warp
 //     works out each thread block's segments and hands them to the other
 //     warps through a small ring.
 //
@@ -45,7 +45,7 @@ __device__ DeviceError g_err;
 constexpr int kBM = 128;      // rows of a tile
 constexpr int kBN = 128;      // keys of a block
 constexpr float kThreshold = 8.0f;   // lazy rescaling, log2 units
-constexpr int kMinStretch = 2;       // blocks: shorter ones cost more to join than they save
+constexpr int kMinStretch = 2 * kBN;  // keys: shorter stretches cost more to join than they save
 
 enum Site {
   kSiteSeqs = 1, kSitePage, kSiteSegFull, kSiteSegEmpty, kSiteQEmpty, kSiteKvEmpty, kSiteKvFull, kSiteQFull, kSiteS,
@@ -62,7 +62,12 @@ struct Part {
   FA_DEV static float* stat(float* ws, int slot) {
     return ws + (size_t)2 * kMaxCtas * kRows * D + (size_t)slot * kRows * kStat;
   }
-  static constexpr size_t bytes() { return (size_t)2 * kMaxCtas * kRows * (D + kStat) * sizeof(float); }
+  FA_DEV static paged::Join* join(float* ws, int c) {
+    return reinterpret_cast<paged::Join*>(stat(ws, 2 * kMaxCtas)) + c;
+  }
+  static constexpr size_t bytes() {
+    return (size_t)2 * kMaxCtas * kRows * (D + kStat) * sizeof(float) + kMaxCtas * sizeof(paged::Join);
+  }
 };
 
 // A segment: blocks [kb, kb + count) of a unit, as the roles get it.
@@ -90,8 +95,8 @@ struct Layout {
   static constexpr int kRaw = kKV + kStages * kTileBytes;
   static constexpr int kRawScale = kRaw + kRaws * kRawBytes;
   static constexpr int kStats = kRawScale + kRaws * kBN;     // scale, l, lr, m of [2][128]
-  static constexpr int kBPre = kStats + 4 * 2 * kBM * 4;     // block prefix [B + 1], 64 bits
-  static constexpr int kUPre = kBPre + (kMaxPackedSeqs + 1) * 8;   // unit prefix [B + 1]
+  static constexpr int kKPre = kStats + 4 * 2 * kBM * 4;     // key prefix [B + 1], 64 bits
+  static constexpr int kUPre = kKPre + (kMaxPackedSeqs + 1) * 8;   // unit prefix [B + 1]
   static constexpr int kSums = (kUPre + (kMaxPackedSeqs + 1) * 4 + 7) / 8 * 8;
   static constexpr int kSegRing = (kSums + 32 * 16 + 15) / 16 * 16;
   static constexpr int kBars = kSegRing + kSegs * (int)sizeof(Seg);
@@ -146,60 +151,26 @@ struct Shared {
 
 FA_DEV int tile_tokens(int group) { return kBM / group; }
 
-// sum of floor((a i + b) / 128) for i in [0, n), n > 0; a, b >= 0, 128 n + 128 <
-// 2^32 (Euclid's algorithm on the slope).
-FA_DEV long long floor_sum_128(uint32_t n, uint32_t a, uint32_t b) {
-  // the first step, m = 128, without divisions; most tiles' slopes end there or
-  // one step later
-  long long s = (long long)n * (n - 1) / 2 * (a >> 7) + (long long)n * (b >> 7);
-  a &= 127u;
-  b &= 127u;
-  uint32_t m = a;
-  const uint32_t top0 = a * n + b;
-  if (top0 < 128u) return s;
-  n = top0 >> 7;
-  b = top0 & 127u;
-  a = 128u;
-  while (n > 0) {
-    if (a >= m) {
-      s += (long long)n * (n - 1) / 2 * (a / m);
-      a %= m;
-    }
-    if (b >= m) {
-      s += (long long)n * (b / m);
-      b %= m;
-    }
-    const uint32_t top = a * n + b;
-    if (top < m) break;
-    n = top / m;
-    b = top % m;
-    const uint32_t t = m;
-    m = a;
-    a = t;
-  }
-  return s;
-}
-
-// A sequence's pairs of tiles and their key blocks.
+// A sequence's pairs of tiles and the keys that they see.
 struct Seq {
   int n, L, q0;
   int pairs, t2;      // pairs of tiles, tokens of a pair
   bool causal;
-  FA_DEV int blocks(int pair) const {      // at least one, so that rows without a key are written too
-    const int end = causal ? min(L, L - n + (pair + 1) * t2) : L;
-    return max(1, (end + kBN - 1) / kBN);
-  }
-  // Blocks of the pairs [0, p).
+  // Keys of a pair: at least one, so that rows without a key are written too.
+  FA_DEV int keys(int pair) const { return max(1, causal ? min(L, L - n + (pair + 1) * t2) : L); }
+  FA_DEV int blocks(int pair) const { return (keys(pair) + kBN - 1) / kBN; }
+  // Keys of the pairs [0, p).
   FA_DEV long long prefix(int p) const {
-    if (!causal) return (long long)p * max(1, (L + kBN - 1) / kBN);
-    const int last = p == pairs ? blocks(pairs - 1) : 0;      // the one whose end the sequence's end cuts
+    if (!causal) return (long long)p * max(1, L);
+    const long long last = p == pairs ? keys(pairs - 1) : 0;  // the one whose end the sequence's end cuts
     if (p == pairs) --p;
-    const int e0 = L - n + t2;                                // end of pair 0's keys
+    const int e0 = L - n + t2;                                // of pair 0
     const int none = e0 <= 0 ? min(p, -e0 / t2 + 1) : 0;      // pairs that see no key
-    return last + none + (p > none ? floor_sum_128(p - none, t2, e0 + none * t2 + kBN - 1) : 0);
+    return last + none + (long long)(p - none) * e0 +
+           ((long long)p * (p - 1) - (long long)none * (none - 1)) / 2 * t2;
   }
   FA_DEV long long total() const { return prefix(pairs); }
-  // Pairs run from the last (the longest under a mask) to the first: blocks of
+  // Pairs run from the last (the longest under a mask) to the first: keys of
   // the i units before unit i of a head, all of which have `total`.
   FA_DEV long long before(int i, long long total) const { return total - prefix(pairs - i); }
 };
@@ -218,11 +189,11 @@ FA_DEV Seq seq_of(const PagedAttnParams& p, int b) { return seq_from(p, paged::r
 // The work of a call: prefix tables over the sequences and where the whole
 // rounds end.
 struct Line {
-  const long long* bpre;
+  const long long* kpre;
   const int* upre;
   int units;          // all units
   int whole;          // units of the whole rounds
-  long long t0, t1;   // the blocks of the others
+  long long t0, t1;   // the keys of the others
   int G;              // stretches that they are cut into
   FA_DEV long long stretch(int c) const { return t0 + paged::div64((t1 - t0) * c, G); }
 };
@@ -240,22 +211,22 @@ FA_DEV int last_at_most(const T* table, int B, T x) {
 
 // Builds the tables; all threads of the block.  No units when the sequences
 // break the rules.
-FA_DEV Line build_line(const PagedAttnParams& p, long long* bpre, int* upre, long long* sums, int ctas) {
-  Line line{bpre, upre, 0, 0, 0, 0, 0};
+FA_DEV Line build_line(const PagedAttnParams& p, long long* kpre, int* upre, long long* sums, int ctas) {
+  Line line{kpre, upre, 0, 0, 0, 0, 0};
   const bool ok = paged::prefix_sequences(
       p.s, p.max_q,
       [&](const paged::SeqRows& rows) {
         const Seq s = seq_from(p, rows);
         return paged::Work{s.total() * p.s.Hkv, s.pairs * p.s.Hkv};
       },
-      bpre, upre, sums);
+      kpre, upre, sums);
   if (!ok) {
     if (blockIdx.x == 0 && threadIdx.x == 0) paged::record_bad_input(&g_err, kSiteSeqs);
     return line;
   }
   const int carry_u = upre[p.s.B];
   line.units = carry_u;
-  line.t1 = bpre[p.s.B];
+  line.t1 = kpre[p.s.B];
   // a last round that is nearly full is not worth cutting
   const int rest = carry_u < ctas ? carry_u : carry_u % ctas;
   line.whole = rest * 10 >= ctas * 9 ? carry_u : carry_u - rest;
@@ -266,7 +237,7 @@ FA_DEV Line build_line(const PagedAttnParams& p, long long* bpre, int* upre, lon
     const Seq s = seq_of(p, b);
     const int r = line.whole - upre[b], head = r / s.pairs;
     const long long total = s.total();
-    line.t0 = bpre[b] + head * total + s.before(r - head * s.pairs, total);
+    line.t0 = kpre[b] + head * total + s.before(r - head * s.pairs, total);
   } else {
     line.t0 = line.t1;
   }
@@ -275,17 +246,19 @@ FA_DEV Line build_line(const PagedAttnParams& p, long long* bpre, int* upre, lon
   return line;
 }
 
-// The unit that holds position t of the line.  One warp, converged.
+// A place on the line, at a key block: block kb of unit i of a head (pair
+// pairs - 1 - i).
 struct Place {
-  int b, head, i;     // i: the unit within its head, pair = pairs - 1 - i
-  long long start;    // its first position
+  int b, head, i, kb;
+  long long start;    // the unit's first position
 };
+// The last one at or before position t < t1.  One warp, converged.
 FA_DEV Place find_place(const PagedAttnParams& p, const Line& line, long long t) {
   Place w;
-  w.b = last_at_most(line.bpre, p.s.B, t);
+  w.b = last_at_most(line.kpre, p.s.B, t);
   const Seq s = seq_of(p, w.b);
   const long long per_head = s.total();
-  long long r = t - line.bpre[w.b];
+  long long r = t - line.kpre[w.b];
   w.head = (int)paged::div64(r, per_head);
   r -= w.head * per_head;
   const int lane = threadIdx.x % 32;
@@ -299,6 +272,7 @@ FA_DEV Place find_place(const PagedAttnParams& p, const Line& line, long long t)
   }
   w.i = lo;
   w.start = t - r + s.before(lo, per_head);
+  w.kb = (int)((t - w.start) / kBN);
   return w;
 }
 
@@ -386,30 +360,46 @@ __device__ void scheduler_role(const Shared<D, kFp8>& sh, const PagedAttnParams&
     const int pair = s.pairs - 1 - (r - head * s.pairs);
     if (!put(b, head, pair, 0, s.blocks(pair), s, -1)) return;
   }
+  paged::Join join{};
   if (c < line.G) {
-    const long long t0 = line.stretch(c), t1 = line.stretch(c + 1);
-    Place w = find_place(p, line, t0);
+    Place w = find_place(p, line, line.stretch(c));
+    const bool to_end = c + 1 == line.G;
+    const Place z = to_end ? Place{} : find_place(p, line, line.stretch(c + 1));
     Seq s = seq_of(p, w.b);
-    for (long long t = t0; t < t1;) {
+    if (w.kb > 0) {
+      // the unit is cut here: if for the first time, its parts are joined
+      const int pair = s.pairs - 1 - w.i;
+      if (line.stretch(c - 1) < w.start + kBN) {
+        const long long end = w.start + s.keys(pair);
+        join = paged::Join{2, 2 * (c - 1) + 1, w.b, w.head, pair * s.t2, s.n, s.q0, 0};
+        while (c + join.parts - 1 < line.G && line.stretch(c + join.parts - 1) < end) ++join.parts;
+      }
+    }
+    // from place w to place z
+    for (;;) {
       const int pair = s.pairs - 1 - w.i, nblk = s.blocks(pair);
-      const int kb = (int)(t - w.start);
-      const int count = (int)(t1 - t < nblk - kb ? t1 - t : nblk - kb);
-      const bool whole = kb == 0 && count == nblk;
-      if (!put(w.b, w.head, pair, kb, count, s, whole ? -1 : 2 * c + (t == t0 ? 0 : 1))) return;
-      t += count;
-      w.start += nblk;
-      if (++w.i == s.pairs && t < t1) {
+      const bool last = !to_end && w.b == z.b && w.head == z.head && w.i == z.i;
+      const int end = last ? z.kb : nblk;
+      if (end > w.kb) {
+        const int slot = w.kb > 0 ? 2 * c : end < nblk ? 2 * c + 1 : -1;
+        if (!put(w.b, w.head, pair, w.kb, end - w.kb, s, slot)) return;
+      }
+      if (last) break;
+      w.kb = 0;
+      if (++w.i == s.pairs) {
         w.i = 0;
         if (++w.head == p.s.Hkv) {
           w.head = 0;
           do {
-            ++w.b;
+            if (++w.b == p.s.B) break;
             s = seq_of(p, w.b);
-          } while (s.n == 0 && w.b < p.s.B - 1);
+          } while (s.n == 0);
+          if (w.b == p.s.B) break;
         }
       }
     }
   }
+  if (lane == 0) *Part<D>::join(p.part, c) = join;
   Seq none{};
   put(-1, 0, 0, 0, 0, none, -1);
 }
@@ -1081,7 +1071,7 @@ __global__ void __launch_bounds__(Layout<D, kFp8>::kThreads, 1)
     tmem_alloc(sh.tmem_slot(), 512);
     tmem_relinquish();
   }
-  const Line line = build_line(p, reinterpret_cast<long long*>(smem + L::kBPre), reinterpret_cast<int*>(smem + L::kUPre),
+  const Line line = build_line(p, reinterpret_cast<long long*>(smem + L::kKPre), reinterpret_cast<int*>(smem + L::kUPre),
                                reinterpret_cast<long long*>(smem + L::kSums), gridDim.x);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before();
@@ -1131,42 +1121,27 @@ __global__ void __launch_bounds__(Layout<D, kFp8>::kThreads, 1)
 // (x, y) does rows [32 y, 32 y + 32) of the unit whose first cut is border x + 1.
 constexpr int kJoinThreads = 256, kJoinRows = 32;
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) combine_kernel(const PagedAttnParams p, int ctas) {
-  __shared__ long long bpre[kMaxPackedSeqs + 1];
-  __shared__ int upre[kMaxPackedSeqs + 1];
-  __shared__ long long sums[2 * kJoinThreads / 32];
+__global__ void __launch_bounds__(kJoinThreads) combine_kernel(const PagedAttnParams p) {
   __shared__ float fac[kMaxCtas + 1][kJoinRows];
   __shared__ float inv[kJoinRows];
-  const Line line = build_line(p, bpre, upre, sums, ctas);
-  // before any exit, so that this grid ends after the main one
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x + 1;
-  if (c >= line.G) return;
-  const long long t = line.stretch(c), prev = line.stretch(c - 1);
-  const Place w = find_place(p, line, t);
-  if (w.start == t || prev > w.start) return;      // no cut here, or not the unit's first
-  const Seq s = seq_of(p, w.b);
-  const int pair = s.pairs - 1 - w.i;
-  if (pair * s.t2 + blockIdx.y * kJoinRows / kBM * tile_tokens(p.group) >= s.n) return;   // a tile without a token
-  const long long end = w.start + s.blocks(pair);
-  const int first = 2 * (c - 1) + (prev == w.start ? 0 : 1);
-  int last = c;                                     // parts: slot `first`, then slots 2 c .. 2 last
-  while (last + 1 < line.G && line.stretch(last + 1) < end) ++last;
-  // The parts' factors, one row a lane: 2^(maximum - the row's largest).
-  const int parts = last - c + 2;
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  auto slot_of = [&](int k) { return k == 0 ? first : 2 * (c + k - 1); };
-  const int row0 = blockIdx.y * kJoinRows;
+  const paged::Join j = *Part<D>::join(p.part, c);
   const int tt = tile_tokens(p.group);
+  const int row0 = blockIdx.y * kJoinRows;
+  const int tok0 = j.row0 + row0 / kBM * tt;                // of the rows' tile
+  if (j.parts == 0 || tok0 >= j.n) return;
+  // The parts' factors, one row a lane: 2^(maximum - the row's largest).
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   if (warp == 0) {
     auto stat_of = [&](int k) {
-      return *reinterpret_cast<const float4*>(Part<D>::stat(p.part, slot_of(k)) + (row0 + lane) * Part<D>::kStat);
+      return *reinterpret_cast<const float4*>(Part<D>::stat(p.part, paged::join_slot(j, c, k)) + (row0 + lane) * Part<D>::kStat);
     };
     float mt = -INFINITY, lt = 0.0f, lrt = 0.0f;
 #pragma unroll 4
-    for (int k = 0; k < parts; ++k) mt = fmaxf(mt, stat_of(k).x);
+    for (int k = 0; k < j.parts; ++k) mt = fmaxf(mt, stat_of(k).x);
 #pragma unroll 4
-    for (int k = 0; k < parts; ++k) {
+    for (int k = 0; k < j.parts; ++k) {
       const float4 st = stat_of(k);
       const float f = mt == -INFINITY ? 1.0f : ex2_mufu(st.x - mt);
       fac[k][lane] = f;
@@ -1175,10 +1150,10 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const PagedAttnPa
     }
     inv[lane] = lrt == 0.0f ? 0.0f : 1.0f / lrt;
     const int in_tile = (row0 + lane) % kBM, tk = in_tile / p.group;
-    const int tok = pair * s.t2 + row0 / kBM * tt + tk;
-    if (tk < tt && tok < s.n) {
-      const int head = w.head * p.group + in_tile - tk * p.group;
-      const size_t li = p.s.cu ? (size_t)head * p.s.Sn + s.q0 + tok : ((size_t)w.b * p.Hq + head) * p.s.Sn + tok;
+    const int tok = tok0 + tk;
+    if (tk < tt && tok < j.n) {
+      const int head = j.head * p.group + in_tile - tk * p.group;
+      const size_t li = p.s.cu ? (size_t)head * p.s.Sn + j.q0 + tok : ((size_t)j.b * p.Hq + head) * p.s.Sn + tok;
       p.lse[li] = lt == 0.0f ? -INFINITY : (mt + log2f(lt)) * 0.693147180559945309f;
     }
   }
@@ -1188,8 +1163,8 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const PagedAttnPa
 #pragma unroll
   for (int e = 0; e < kEach; ++e) y[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 2
-  for (int k = 0; k < parts; ++k) {
-    const float4* from = reinterpret_cast<const float4*>(Part<D>::out(p.part, slot_of(k)) + row0 * D);
+  for (int k = 0; k < j.parts; ++k) {
+    const float4* from = reinterpret_cast<const float4*>(Part<D>::out(p.part, paged::join_slot(j, c, k)) + row0 * D);
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
       const int i = threadIdx.x + e * kJoinThreads;
@@ -1207,10 +1182,10 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const PagedAttnPa
     const int i = threadIdx.x + e * kJoinThreads;
     const int r = i / (D / 4), d = i % (D / 4) * 4;
     const int in_tile = (row0 + r) % kBM, tk = in_tile / p.group;
-    const int tok = pair * s.t2 + row0 / kBM * tt + tk;
-    if (tk >= tt || tok >= s.n) continue;
-    const int head = w.head * p.group + in_tile - tk * p.group;
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + ((size_t)(s.q0 + tok) * p.Hq + head) * D + d) =
+    const int tok = tok0 + tk;
+    if (tk >= tt || tok >= j.n) continue;
+    const int head = j.head * p.group + in_tile - tk * p.group;
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + ((size_t)(j.q0 + tok) * p.Hq + head) * D + d) =
         make_uint2(pack_bf16x2(y[e].x * inv[r], y[e].y * inv[r]), pack_bf16x2(y[e].z * inv[r], y[e].w * inv[r]));
   }
 }
@@ -1243,7 +1218,7 @@ fa_status launch_inst(const PagedAttnLaunch& L, cudaStream_t stream) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, combine_kernel<D>, L.p, ctas) != cudaSuccess) return FA_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, combine_kernel<D>, L.p) != cudaSuccess) return FA_ERR_CUDA;
   }
   return FA_OK;
 }

@@ -62,7 +62,12 @@ struct Part {
   FA_DEV static float* stat(float* ws, int slot) {
     return ws + (size_t)2 * kMaxCtas * kSlotFloats + (size_t)slot * kRows * kStat;
   }
-  static constexpr size_t bytes() { return (size_t)2 * kMaxCtas * (kSlotFloats + kRows * kStat) * sizeof(float); }
+  FA_DEV static paged::Join* join(float* ws, int c) {
+    return reinterpret_cast<paged::Join*>(stat(ws, 2 * kMaxCtas)) + c;
+  }
+  static constexpr size_t bytes() {
+    return (size_t)2 * kMaxCtas * (kSlotFloats + kRows * kStat) * sizeof(float) + kMaxCtas * sizeof(paged::Join);
+  }
 };
 
 // kTiles: tiles of 8 rows.  11 computing warps with up to 168 registers hide
@@ -258,7 +263,7 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
                   const PagedAttnParams p) {
   using L = Layout<D, kFp8, kTiles>;
   using W = Part<D, L::kRows>;
-  constexpr int kWarps = L::kWarps, kThreads = L::kThreads, kRows = L::kRows;
+  constexpr int kWarps = L::kWarps, kRows = L::kRows;
   constexpr int kKeys = L::kKeys;
   constexpr int kGroups = kKeys / 16;
   constexpr int kSteps = D / 16;      // 16-wide steps along D
@@ -290,7 +295,10 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
   __syncthreads();
   const int G = active_ctas(total, gridDim.x);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if ((int)blockIdx.x >= G) return;
+  if ((int)blockIdx.x >= G) {
+    if (threadIdx.x == 0) W::join(p.part, blockIdx.x)->parts = 0;
+    return;
+  }
   const long long t0 = stretch(total, blockIdx.x, G), t1 = stretch(total, blockIdx.x + 1, G);
 
   // The stretch's visible blocks are numbered through; block q goes through ring
@@ -303,6 +311,21 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
   constexpr int kEnd = -2;                                             // in place of a page: no more blocks
 
   if (warp == kWarps) {
+    // ---- says what there is to join at the border before this stretch
+    if (lane == 0) {
+      const int c = blockIdx.x;
+      paged::Join j{0, 0, at.b, at.head, at.tile * kRows, at.s.n, at.s.q0, 0};
+      const long long start = t0 - at.kb, end = start + at.nblk;
+      if (at.kb > 0) {
+        const long long prev = stretch(total, c - 1, G);
+        if (prev <= start) {       // the unit's first cut
+          j.first = 2 * (c - 1) + (prev == start ? 0 : 1);
+          j.parts = 2;
+          while (c + j.parts - 1 < G && stretch(total, c + j.parts - 1, G) < end) ++j.parts;
+        }
+      }
+      *W::join(p.part, c) = j;
+    }
     // ---- looks up where blocks lie: (page, head) and row of the block's boxes
     int i = 0, vis = at.visible(p), past = 0;
     uint32_t batch = 0;
@@ -750,58 +773,40 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
 // thread block: their statistics and rows are loaded together, not one after
 // the other.
 constexpr int kJoinThreads = 256, kJoinRows = 8;
-template <int D, int kKeys, int kRows>
-__global__ void __launch_bounds__(kJoinThreads) combine_kernel(const PagedAttnParams p, int ctas) {
+template <int D, int kRows>
+__global__ void __launch_bounds__(kJoinThreads) combine_kernel(const PagedAttnParams p) {
   using W = Part<D, kRows>;
-  __shared__ long long pre[kMaxPackedSeqs + 1];
-  __shared__ long long sums[2 * kJoinThreads / 32];
   __shared__ float st_m[kMaxCtas + 1][kJoinRows], st_l[kMaxCtas + 1][kJoinRows], st_lr[kMaxCtas + 1][kJoinRows];
   __shared__ float inv[kJoinRows];
-  const long long total = build_line<kKeys, kRows>(p, pre, sums);
-  const int G = active_ctas(total, ctas);
-  const int c = blockIdx.x + 1;
-  Walk<kKeys, kRows> w;
-  long long start = 0, end = 0;
-  int first = -1;
-  if (c < G) {
-    const long long t = stretch(total, c, G), t_prev = stretch(total, c - 1, G);
-    w.begin(p, pre, t, total);
-    start = t - w.kb;
-    end = start + w.nblk;
-    // no cut here, or not the unit's first: nothing to do
-    if (w.kb > 0 && t_prev <= start) first = 2 * (c - 1) + (t_prev == start ? 0 : 1);
-  }
-  // before any exit, so that this grid ends after the main one
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = blockIdx.x + 1;
+  const paged::Join j = *W::join(p.part, c);
   const int row0 = blockIdx.y * kJoinRows;
-  const int rows = first < 0 ? 0 : min(kJoinRows, w.rows(p) - row0);
+  const int rows = j.parts == 0 ? 0 : min(kJoinRows, min(kRows, j.n * p.group - j.row0) - row0);
   if (rows <= 0) return;
-  int parts = 2;                                 // slot `first`, then slots 2 c, 2 (c + 1), ...
-  while (c + parts - 1 < G && stretch(total, c + parts - 1, G) < end) ++parts;
-  auto slot_of = [&](int k) { return k == 0 ? first : 2 * (c + k - 1); };
-  for (int i = threadIdx.x; i < parts * kJoinRows; i += kJoinThreads) {
+  for (int i = threadIdx.x; i < j.parts * kJoinRows; i += kJoinThreads) {
     const int k = i / kJoinRows, r = i % kJoinRows;
     if (r >= rows) continue;
-    const float4 st = *reinterpret_cast<const float4*>(W::stat(p.part, slot_of(k)) + (row0 + r) * W::kStat);
+    const float4 st = *reinterpret_cast<const float4*>(W::stat(p.part, paged::join_slot(j, c, k)) + (row0 + r) * W::kStat);
     st_m[k][r] = st.x;
     st_l[k][r] = st.y;
     st_lr[k][r] = st.z;
   }
   __syncthreads();
-  const int tile_row = w.tile * kRows + row0;
+  const int unit_row = j.row0 + row0;
   if ((int)threadIdx.x < rows) {
     const int r = threadIdx.x;
     float mt = -INFINITY, lt = 0.0f, lrt = 0.0f;
-    for (int k = 0; k < parts; ++k) mt = fmaxf(mt, st_m[k][r]);
-    for (int k = 0; k < parts; ++k) {
+    for (int k = 0; k < j.parts; ++k) mt = fmaxf(mt, st_m[k][r]);
+    for (int k = 0; k < j.parts; ++k) {
       const float f = mt == -INFINITY ? 1.0f : ex2_mufu(st_m[k][r] - mt);
       st_m[k][r] = f;                            // from here on the part's factor
       lt += st_l[k][r] * f;
       lrt += st_lr[k][r] * f;
     }
     inv[r] = lrt == 0.0f ? 0.0f : 1.0f / lrt;
-    const int tk = (tile_row + r) / p.group, head = w.head * p.group + tile_row + r - tk * p.group;
-    const size_t li = p.s.cu ? (size_t)head * p.s.Sn + w.s.q0 + tk : ((size_t)w.b * p.Hq + head) * p.s.Sn + tk;
+    const int tk = (unit_row + r) / p.group, head = j.head * p.group + unit_row + r - tk * p.group;
+    const size_t li = p.s.cu ? (size_t)head * p.s.Sn + j.q0 + tk : ((size_t)j.b * p.Hq + head) * p.s.Sn + tk;
     p.lse[li] = lt == 0.0f ? -INFINITY : (mt + log2f(lt)) * 0.693147180559945309f;
   }
   __syncthreads();
@@ -809,16 +814,16 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const PagedAttnPa
   if (r >= rows) return;
   float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
-  for (int k = 0; k < parts; ++k) {
-    const float4 x = *reinterpret_cast<const float4*>(W::out(p.part, slot_of(k)) + (row0 + r) * D + d);
+  for (int k = 0; k < j.parts; ++k) {
+    const float4 x = *reinterpret_cast<const float4*>(W::out(p.part, paged::join_slot(j, c, k)) + (row0 + r) * D + d);
     const float f = st_m[k][r];
     y.x += x.x * f;
     y.y += x.y * f;
     y.z += x.z * f;
     y.w += x.w * f;
   }
-  const int tk = (tile_row + r) / p.group, head = w.head * p.group + tile_row + r - tk * p.group;
-  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + ((size_t)(w.s.q0 + tk) * p.Hq + head) * D + d) =
+  const int tk = (unit_row + r) / p.group, head = j.head * p.group + unit_row + r - tk * p.group;
+  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + ((size_t)(j.q0 + tk) * p.Hq + head) * D + d) =
       make_uint2(pack_bf16x2(y.x * inv[r], y.y * inv[r]), pack_bf16x2(y.z * inv[r], y.w * inv[r]));
 }
 
@@ -838,7 +843,7 @@ fa_status launch_inst(const PagedAttnLaunch& L, cudaStream_t stream) {
   kern<<<ctas, Lay::kThreads, Lay::kBytes, stream>>>(tk, tv, L.p);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
   if (ctas > 1) {
-    // the joining kernel works out its borders while the main one still runs
+    // the joining kernel is on its way while the main one still runs
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(ctas - 1, Lay::kRows / kJoinRows);
     cfg.blockDim = dim3(kJoinThreads);
@@ -848,7 +853,7 @@ fa_status launch_inst(const PagedAttnLaunch& L, cudaStream_t stream) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, combine_kernel<D, Lay::kKeys, Lay::kRows>, L.p, ctas) != cudaSuccess) return FA_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, combine_kernel<D, Lay::kRows>, L.p) != cudaSuccess) return FA_ERR_CUDA;
   }
   return FA_OK;
 }

@@ -135,6 +135,20 @@ FA_DEV long long div64(long long a, long long b) {
   return a / b;
 }
 
+// What the kernels that join partial results need to know of border c between
+// thread blocks c - 1 and c.  Thread block c of the main kernel, which knows the
+// place, leaves it behind for them: working it out again took as long as the
+// joining.
+struct Join {
+  int parts;       // of the unit whose first cut this border is: slot `first`, then slots 2 c, 2 (c + 1), ...; 0: none
+  int first;
+  int b, head;
+  int row0;        // the unit's first row: decode kernel (token, head) rows, chunk kernel tokens
+  int n, q0;       // the sequence's new tokens and their first row
+  int pad;
+};
+FA_DEV int join_slot(const Join& j, int c, int k) { return k == 0 ? j.first : 2 * (c + k - 1); }
+
 // 2^e of a scale byte; NaN for the byte of a row without a finite scale.
 FA_DEV float scale_value(uint32_t byte) {
   return byte == 255u ? __int_as_float(0x7FC00000) : __uint_as_float(byte << 23);
