@@ -14,6 +14,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxGroup = 128;      // query heads per key/value head
+constexpr int kMaxHkv = 4096;       // (the cache kernels' row arithmetic)
 constexpr int kMinPage = 16, kMaxPage = 1024;
 
 bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1u)) == 0; }
@@ -31,6 +32,7 @@ fa_status check_cache(const void* k_pages, const void* v_pages, const void* k_sc
   if (page_size <= 0 || (page_size & (page_size - 1)) != 0) return FA_ERR_INVALID_ARG;
   if (page_size < kMinPage || page_size > kMaxPage) return FA_ERR_UNSUPPORTED;
   if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
+  if (Hkv > kMaxHkv) return FA_ERR_UNSUPPORTED;
   if (B > kMaxPackedSeqs || (long long)max_pages * page_size > (1ll << 30)) return FA_ERR_UNSUPPORTED;
   // (page, head) pairs and rows of the new tokens fit 32-bit indices
   if ((long long)num_pages * Hkv > INT32_MAX) return FA_ERR_UNSUPPORTED;
@@ -60,7 +62,7 @@ bool attn_shape_ok(int B, int Hq, int Hkv, int Sn, int D, bool packed, int max_q
   if (B <= 0 || Hq <= 0 || Hkv <= 0 || Sn <= 0 || Hq % Hkv != 0) return false;
   if (packed && (max_q <= 0 || max_q > Sn)) return false;
   *why = FA_ERR_UNSUPPORTED;
-  if (Hq / Hkv > kMaxGroup || (D != 64 && D != 128) || B > kMaxPackedSeqs) return false;
+  if (Hkv > kMaxHkv || Hq / Hkv > kMaxGroup || (D != 64 && D != 128) || B > kMaxPackedSeqs) return false;
   if ((packed ? (long long)Sn : (long long)B * Sn) > INT32_MAX - 512) return false;
   if ((long long)(packed ? max_q : Sn) * (Hq / Hkv) > INT32_MAX - 512) return false;
   return true;

@@ -117,7 +117,7 @@ FA_DEV long long build_line(const PagedAttnParams& p, long long* pre, long long*
       p.s, p.max_q,
       [&](const Seq& q) {
         const int tiles = tiles_of(q.n, p.group, kRows);
-        return paged::Work{(long long)p.s.Hkv * tiles * blocks_of(q.L, kKeys), 0};
+        return paged::Work{(long long)p.s.Hkv * tiles * blocks_of(q.L, kKeys), 0, 0};
       },
       pre, nullptr, warp_sums);
   if (ok) return pre[p.s.B];

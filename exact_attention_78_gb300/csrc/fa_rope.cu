@@ -10,7 +10,8 @@
 //
 // HBM bounds the kernel at training sizes (a row is read once and written
 // once), so each angle is computed once per token, into shared memory, for all
-// heads of q and k, and rows move in 16-byte pieces.
+// heads of q and k, and rows move in 16-byte pieces, several in flight per
+// thread; the first ones are on their way while the angles are computed.
 #include <cuda_runtime.h>
 
 #include "paged.cuh"
@@ -27,114 +28,132 @@ FA_DEV float hi_of(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 // kHalf: pairs (i, i + R), R a multiple of 8, so that a 16-byte piece of
 // first elements has its partners in one other aligned piece and a thread
 // turns both.  kAdjacent: pairs (2 i, 2 i + 1), inside one piece.  kAny: pairs
-// (i, i + R) at any R: a thread's piece meets its partners one by one.
+// (i, i + R) at any R: a thread's piece meets its partners one by one, in the
+// row's copy in shared memory.  16,384 tokens x 32 heads, D = 128, R = 64: kHalf
+// 42.7 us (6.3 TB/s), kAny 82.3 us.
 enum Layout { kHalf, kAdjacent, kAny };
+
+// 16-byte pieces that one thread loads and stores at a time.
+struct Piece {
+  uint4 a, b;      // b: the partners' (kHalf)
+};
 
 template <int D, Layout kLayout>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
-  __shared__ float2 cs[kMaxTb * (D / 2)];      // cos, sin of each token's pairs
+  constexpr int kPieces = D / 8;                // of a row
+  constexpr int kPer = kLayout == kAdjacent ? 4 : 8;        // pairs of a piece
+  constexpr int kUnroll = kLayout == kHalf ? 2 : 4;
+  // cos, sin of each token's pairs, pair i at (i mod kPer) (pairs / kPer) +
+  // i / kPer: lanes with neighbouring pieces read neighbouring entries
+  constexpr int kStride = D / 2 / kPer;
+  __shared__ float2 cs[kMaxTb][D / 2];
+  __shared__ uint4 copy[kLayout == kAny ? kThreads : 1];
   const int R = p.pairs;
   const int tok0 = blockIdx.x * p.tb;
   const int ntok = min(p.tb, p.tokens - tok0);
+
+  // A thread does one piece of every step's row: piece j (kHalf: and j + R / 8;
+  // the pieces from 2 R / 8 on are copied).
+  const int half = R / 8;
+  const int work = kLayout == kHalf ? kPieces - half : kPieces;
+  const int step = kThreads / work;             // rows a step
+  const int first = threadIdx.x / work;
+  int j = threadIdx.x - first * work;
+  const bool turns = kLayout != kHalf || j < half;
+  if (!turns) j += half;
+  const int nq = ntok * p.Hq, n = nq + ntok * p.Hkv;        // rows of q, of both
+  const uint4* q = static_cast<const uint4*>(p.q) + (size_t)tok0 * p.Hq * kPieces;
+  const uint4* k = static_cast<const uint4*>(p.k) + (size_t)tok0 * p.Hkv * kPieces;
+  uint4* q_out = static_cast<uint4*>(p.q_out) + (size_t)tok0 * p.Hq * kPieces;
+  uint4* k_out = static_cast<uint4*>(p.k_out) + (size_t)tok0 * p.Hkv * kPieces;
+
+  auto load = [&](int r0, Piece (&x)[kUnroll]) {
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int r = r0 + first + u * step;
+      if (first >= step || r >= n) continue;
+      const uint4* src = (r < nq ? q + (size_t)r * kPieces : k + (size_t)(r - nq) * kPieces) + j;
+      x[u].a = src[0];
+      if (kLayout == kHalf && turns) x[u].b = src[half];
+    }
+  };
+  Piece x[kUnroll];
+  load(0, x);
+
   for (int i = threadIdx.x; i < ntok * R; i += kThreads) {
     const int t = i / R, pair = i - t * R;
     const long long pos = p.positions[(size_t)p.axis[pair] * p.tokens + tok0 + t];
     const unsigned long long frac = (unsigned long long)pos * p.turn[pair];
     float s, c;
     sincospif((float)(int)(frac >> 32) * 4.656612873077393e-10f, &s, &c);   // 2^-31: half turns
-    cs[t * (D / 2) + pair] = make_float2(c, p.inverse ? -s : s);
+    cs[t][pair % kPer * kStride + pair / kPer] = make_float2(c, p.inverse ? -s : s);
   }
   __syncthreads();
 
-  const int heads = p.Hq + p.Hkv;
-  // 16-byte pieces of a row; kHalf: the thread of piece j < R / 8 also does
-  // piece j + R / 8, and the pieces from 2 R / 8 on are copied
-  constexpr int kPieces = D / 8;
-  const int half = R / 8;
-  const int work = kLayout == kHalf ? kPieces - half : kPieces;
-  for (int i = threadIdx.x; i < ntok * heads * work; i += kThreads) {
-    const int row = i / work;
-    int j = i - row * work;
-    const int t = row / heads, h = row - t * heads;
-    const bool is_k = h >= p.Hq;
-    const size_t at = ((size_t)(tok0 + t) * (is_k ? p.Hkv : p.Hq) + (is_k ? h - p.Hq : h)) * D;
-    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(is_k ? p.k : p.q) + at;
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(is_k ? p.k_out : p.q_out) + at;
-    const float2* c = cs + t * (D / 2);
-    if constexpr (kLayout == kHalf) {
-      if (j >= half) {
-        j += half;
-        reinterpret_cast<uint4*>(dst)[j] = reinterpret_cast<const uint4*>(src)[j];
-        continue;
-      }
-      const uint4 a4 = reinterpret_cast<const uint4*>(src)[j], b4 = reinterpret_cast<const uint4*>(src)[j + half];
-      const uint32_t a[4] = {a4.x, a4.y, a4.z, a4.w}, b[4] = {b4.x, b4.y, b4.z, b4.w};
-      uint32_t ya[4], yb[4];
+  for (int r0 = 0; r0 < n; r0 += kUnroll * step) {
+    if (r0 > 0) load(r0, x);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 c0 = c[8 * j + 2 * e], c1 = c[8 * j + 2 * e + 1];
-        const float a0 = lo_of(a[e]), a1 = hi_of(a[e]), b0 = lo_of(b[e]), b1 = hi_of(b[e]);
-        ya[e] = pack_bf16x2(a0 * c0.x - b0 * c0.y, a1 * c1.x - b1 * c1.y);
-        yb[e] = pack_bf16x2(b0 * c0.x + a0 * c0.y, b1 * c1.x + a1 * c1.y);
+    for (int u = 0; u < kUnroll; ++u) {
+      const int r = r0 + first + u * step;
+      const bool on = first < step && r < n;
+      if (kLayout == kAny) {
+        // (a row's lanes may sit in two warps; in place, its stores below must
+        // not overtake these loads)
+        __syncthreads();
+        if (on) copy[threadIdx.x] = x[u].a;
+        __syncthreads();
       }
-      reinterpret_cast<uint4*>(dst)[j] = make_uint4(ya[0], ya[1], ya[2], ya[3]);
-      reinterpret_cast<uint4*>(dst)[j + half] = make_uint4(yb[0], yb[1], yb[2], yb[3]);
-    } else if constexpr (kLayout == kAdjacent) {
-      const uint4 x4 = reinterpret_cast<const uint4*>(src)[j];
-      const uint32_t x[4] = {x4.x, x4.y, x4.z, x4.w};
-      uint32_t y[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int pair = 4 * j + e;
-        y[e] = x[e];
-        if (pair < R) {
-          const float2 cc = c[pair];
-          const float a0 = lo_of(x[e]), b0 = hi_of(x[e]);
-          y[e] = pack_bf16x2(a0 * cc.x - b0 * cc.y, b0 * cc.x + a0 * cc.y);
+      if (!on) continue;
+      const int in = r < nq ? r : r - nq, heads = r < nq ? p.Hq : p.Hkv;
+      const int t = (in >= heads) + (in >= 2 * heads) + (in >= 3 * heads);       // kMaxTb is 4
+      uint4* dst = (r < nq ? q_out + (size_t)r * kPieces : k_out + (size_t)in * kPieces) + j;
+      const uint32_t a[4] = {x[u].a.x, x[u].a.y, x[u].a.z, x[u].a.w};
+      if constexpr (kLayout == kHalf) {
+        if (!turns) {
+          *dst = x[u].a;
+          continue;
         }
-      }
-      reinterpret_cast<uint4*>(dst)[j] = make_uint4(y[0], y[1], y[2], y[3]);
-    }
-  }
-  if constexpr (kLayout == kAny) {
-    // A row's D / 8 lanes take a piece each; partners come from the row's copy
-    // in shared memory, so that the rows may be turned in place.
-    __shared__ float rows[kThreads * 8];
-    const int lane = threadIdx.x % kPieces, group = threadIdx.x / kPieces;
-    constexpr int kGroups = kThreads / kPieces;
-    float* mine = rows + group * D;
-    for (int r0 = 0; r0 < ntok * heads; r0 += kGroups) {
-      const int row = r0 + group;
-      const bool on = row < ntok * heads;
-      const int t = row / heads, h = row - t * heads;
-      const bool is_k = h >= p.Hq;
-      const size_t at = ((size_t)(tok0 + t) * (is_k ? p.Hkv : p.Hq) + (is_k ? h - p.Hq : h)) * D;
-      if (on) {
-        const uint4 x4 = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(is_k ? p.k : p.q) + at)[lane];
-        const uint32_t x[4] = {x4.x, x4.y, x4.z, x4.w};
+        const uint32_t b[4] = {x[u].b.x, x[u].b.y, x[u].b.z, x[u].b.w};
+        uint32_t ya[4], yb[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          mine[8 * lane + 2 * e] = lo_of(x[e]);
-          mine[8 * lane + 2 * e + 1] = hi_of(x[e]);
+          const float2 c0 = cs[t][2 * e * kStride + j], c1 = cs[t][(2 * e + 1) * kStride + j];
+          const float a0 = lo_of(a[e]), a1 = hi_of(a[e]), b0 = lo_of(b[e]), b1 = hi_of(b[e]);
+          ya[e] = pack_bf16x2(a0 * c0.x - b0 * c0.y, a1 * c1.x - b1 * c1.y);
+          yb[e] = pack_bf16x2(b0 * c0.x + a0 * c0.y, b1 * c1.x + a1 * c1.y);
         }
-      }
-      __syncwarp();
-      if (on) {
+        dst[0] = make_uint4(ya[0], ya[1], ya[2], ya[3]);
+        dst[half] = make_uint4(yb[0], yb[1], yb[2], yb[3]);
+      } else if constexpr (kLayout == kAdjacent) {
+        uint32_t y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          y[e] = a[e];
+          if (4 * j + e < R) {
+            const float2 cc = cs[t][e * kStride + j];
+            const float a0 = lo_of(a[e]), b0 = hi_of(a[e]);
+            y[e] = pack_bf16x2(a0 * cc.x - b0 * cc.y, b0 * cc.x + a0 * cc.y);
+          }
+        }
+        *dst = make_uint4(y[0], y[1], y[2], y[3]);
+      } else {
+        const __nv_bfloat16* row = reinterpret_cast<const __nv_bfloat16*>(copy + first * kPieces);
         float y[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const int i = 8 * lane + e;
-          y[e] = mine[i];
+          const int i = 8 * j + e;
+          const float own = e & 1 ? hi_of(a[e / 2]) : lo_of(a[e / 2]);
+          y[e] = own;
           if (i < 2 * R) {
-            const float2 cc = cs[t * (D / 2) + (i < R ? i : i - R)];
-            y[e] = i < R ? mine[i] * cc.x - mine[i + R] * cc.y : mine[i] * cc.x + mine[i - R] * cc.y;
+            const int pair = i < R ? i : i - R;
+            const float other = __bfloat162float(row[i < R ? i + R : pair]);
+            const float2 cc = cs[t][pair % kPer * kStride + pair / kPer];
+            y[e] = own * cc.x + (i < R ? -other : other) * cc.y;
           }
         }
-        reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(is_k ? p.k_out : p.q_out) + at)[lane] =
-            make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
-                       pack_bf16x2(y[6], y[7]));
+        *dst = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                          pack_bf16x2(y[6], y[7]));
       }
-      __syncwarp();
     }
   }
 }

@@ -62,24 +62,25 @@ FA_DEV SeqRows rows_of(const PagedSeqs& s, int b) {
 
 // Checks the sequences' offsets and lengths, and sums up their work: `work`
 // gives a sequence's {key blocks, units}, whose prefix sums go to bpre and (if
-// given) upre, [B + 1].  All threads of the block; false, in all of them, when
+// given) upre, [B + 1], and the longest unit of all to upre[B + 1].  All threads of the block; false, in all of them, when
 // the rules are broken.  Every attention kernel starts with this, so that one
 // pass and two barriers have to do: the loads, the sums within warps and the
 // check share the first.  `sums`: two values per warp.
 struct Work {
   long long blocks;
   int units;
+  int longest;      // unit
 };
 template <class F>
 FA_DEV bool prefix_sequences(const PagedSeqs& s, int max_new, F work, long long* bpre, int* upre, long long* sums) {
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int capacity = s.max_pages << s.page_shift;
-  Work carry{0, 0};
+  Work carry{0, 0, 0};
   int ok = 1;
   for (int b0 = 0; b0 < s.B; b0 += blockDim.x) {
     const int b = b0 + threadIdx.x;
     const int warps = (min(s.B - b0, (int)blockDim.x) + 31) / 32;      // with a sequence
-    Work own{0, 0}, incl;
+    Work own{0, 0, 0}, incl;
     if (b < s.B) {
       const SeqRows r = rows_of(s, b);
       bool fine = r.L >= 0 && r.L <= capacity;
@@ -98,9 +99,10 @@ FA_DEV bool prefix_sequences(const PagedSeqs& s, int max_new, F work, long long*
           incl.units += ou;
         }
       }
+      const int longest = __reduce_max_sync(0xffffffffu, own.longest);
       if (lane == 31) {
         sums[2 * warp] = incl.blocks;
-        sums[2 * warp + 1] = incl.units;
+        sums[2 * warp + 1] = (long long)longest << 32 | (unsigned)incl.units;
       }
     }
     ok = __syncthreads_and(ok);
@@ -114,6 +116,7 @@ FA_DEV bool prefix_sequences(const PagedSeqs& s, int max_new, F work, long long*
       }
       carry.blocks += sb;
       carry.units += su;
+      carry.longest = max(carry.longest, (int)(sums[2 * w + 1] >> 32));
     }
     if (b < s.B) {
       bpre[b] = before.blocks + incl.blocks - own.blocks;
@@ -121,7 +124,10 @@ FA_DEV bool prefix_sequences(const PagedSeqs& s, int max_new, F work, long long*
     }
     if (b0 + (int)blockDim.x >= s.B && threadIdx.x == 0) {
       bpre[s.B] = carry.blocks;
-      if (upre) upre[s.B] = carry.units;
+      if (upre) {
+        upre[s.B] = carry.units;
+        upre[s.B + 1] = carry.longest;
+      }
     }
     __syncthreads();
   }
