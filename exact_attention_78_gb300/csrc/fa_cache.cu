@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const CacheParams p, in
       const uint32_t v[8] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w, x[u][1].x, x[u][1].y, x[u][1].z, x[u][1].w};
       uint32_t m2 = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m2 = __vmaxu2(m2, v[i] & 0x7FFF7FFFu);
+      for (int i = 0; i < 8; ++i) m2 = paged::max_bf16x2(m2, v[i] & 0x7FFF7FFFu);
       uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
       const uint32_t mask = ((1u << kLanes) - 1) << (threadIdx.x % 32 / kLanes * kLanes);
 #pragma unroll

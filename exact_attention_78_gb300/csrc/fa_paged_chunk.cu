@@ -12,9 +12,15 @@
 //     memory tiles.  Rows behind the sequence's end hold anything: as keys
 //     they are masked, as values they are cleared before the product, since a
 //     weight of zero would not cancel a NaN.
-//   * E4M3 pages go through a second ring: eight warps widen each tile to BF16
-//     once per unit, with the rows' power-of-two scales, exactly, so the
-//     products are those of BF16 pages.
+//   * E4M3 pages go through a second ring: eight warps widen each tile once per
+//     unit, to FP16, which one conversion per pair of codes makes (BF16 takes
+//     five instructions: 668 us for 512 tokens over 32K keys, 76/19 heads).  A
+//     segment's largest key scale and largest value scale are taken out of the
+//     tiles; what that leaves is a power of two of at most 1 per row, exact down
+//     to 2^-15 (FP16's subnormals: below, bits of a code are rounded off, 2^-25 of
+//     what the largest scale stands for).  The queries become FP16 by a power of
+//     two of each row's own, which with the keys' scale goes to the scores in
+//     FP32; the values' goes to O at the end.
 //   * Work.  Whole rounds of units, one per thread block, run in lockstep
 //     from the first key on, so that the pairs of a head share its keys in L2.
 //     The units left over are a line of keys that is cut into equal stretches
@@ -45,11 +51,14 @@ __device__ DeviceError g_err;
 constexpr int kBM = 128;      // rows of a tile
 constexpr int kBN = 128;      // keys of a block
 constexpr float kThreshold = 8.0f;   // lazy rescaling, log2 units
+// E4M3: weights are taken times 2^7 to FP16.  With the threshold they stay at
+// most 2^15, and keep FP16's full precision down to 2^-21 of the maximum.
+constexpr float kWeightUp = 7.0f;
 constexpr int kMinStretch = 2 * kBN;  // keys: shorter stretches cost more to join than they save
 
 enum Site {
   kSiteSeqs = 1, kSitePage, kSiteSegFull, kSiteSegEmpty, kSiteQEmpty, kSiteKvEmpty, kSiteKvFull, kSiteQFull, kSiteS,
-  kSiteP, kSiteO, kSiteLanded, kSiteRaw
+  kSiteP, kSiteO, kSiteLanded, kSiteRaw, kSiteQReady
 };
 
 // Workspace: per slot (two per thread block) both tiles' unnormalised rows,
@@ -94,13 +103,17 @@ struct Layout {
   static constexpr int kKV = kQ + 2 * kTileBytes;
   static constexpr int kRaw = kKV + kStages * kTileBytes;
   static constexpr int kRawScale = kRaw + kRaws * kRawBytes;
-  static constexpr int kStats = kRawScale + kRaws * kBN;     // scale, l, lr, m of [2][128]
-  static constexpr int kKPre = kStats + 4 * 2 * kBM * 4;     // key prefix [B + 1], 64 bits
+  static constexpr int kStats = kRawScale + kRaws * kBN;     // scale, l, m (and lr) of [2][128]
+  // E4M3.  Of four segments in turn: the warps' largest scale bytes of keys and
+  // values (the widening warps are up to two segments ahead of the products, and
+  // those one ahead of the epilogue).
+  static constexpr int kTops = kStats + (kFp8 ? 3 : 4) * 2 * kBM * 4;
+  static constexpr int kKPre = kTops + (kFp8 ? 4 * 8 * 2 * 4 : 0);     // key prefix [B + 1], 64 bits
   static constexpr int kUPre = kKPre + (kMaxPackedSeqs + 1) * 8;   // unit prefix [B + 1], longest unit
   static constexpr int kSums = (kUPre + (kMaxPackedSeqs + 2) * 4 + 7) / 8 * 8;
   static constexpr int kSegRing = (kSums + 32 * 16 + 15) / 16 * 16;
   static constexpr int kBars = kSegRing + kSegs * (int)sizeof(Seg);
-  static constexpr int kNumBars = 2 + 2 * kStages + 10 + 2 * kSegs + (kFp8 ? 2 * kRaws : kStages);
+  static constexpr int kNumBars = 2 + 2 * kStages + 10 + 2 * kSegs + (kFp8 ? 2 * kRaws + 1 : kStages);
   static constexpr int kMisc = kBars + kNumBars * 8;
   static constexpr int kBytes = kMisc + 64 + kSmemAlignSlack;
   static_assert(kBytes <= 232448, "dynamic shared memory above the 227 KB per-CTA limit");
@@ -128,13 +141,23 @@ struct Shared {
   FA_DEV uint32_t v_landed(int s) const { return bar(12 + 2 * L::kStages + 2 * kSegs + s); }
   FA_DEV uint32_t raw_full(int s) const { return bar(12 + 2 * L::kStages + 2 * kSegs + s); }
   FA_DEV uint32_t raw_empty(int s) const { return bar(12 + 2 * L::kStages + 2 * kSegs + L::kRaws + s); }
+  FA_DEV uint32_t q_ready() const { return bar(12 + 2 * L::kStages + 2 * kSegs + 2 * L::kRaws); }   // E4M3: Q is FP16
+  // E4M3, of segment number seg: largest scale bytes (all widening warps have
+  // written theirs).
+  FA_DEV int* tops(uint32_t seg) const { return reinterpret_cast<int*>(base + L::kTops) + (seg & 3) * 16; }
+  FA_DEV int key_top(uint32_t seg) const { return top_of(tops(seg)); }
+  FA_DEV int value_top(uint32_t seg) const { return top_of(tops(seg) + 8); }
+  FA_DEV static int top_of(const int* t) {
+    const int4 a = *reinterpret_cast<const int4*>(t), b = *reinterpret_cast<const int4*>(t + 4);
+    return max(max(max(a.x, a.y), max(a.z, a.w)), max(max(b.x, b.y), max(b.z, b.w)));
+  }
   FA_DEV uint32_t abort() const { return sbase + L::kMisc + 4; }
   FA_DEV uint32_t* tmem_slot() const { return reinterpret_cast<uint32_t*>(base + L::kMisc); }
   FA_DEV int* warp_flag() const { return reinterpret_cast<int*>(base + L::kMisc + 8); }
   FA_DEV float* st_scale() const { return reinterpret_cast<float*>(base + L::kStats); }
   FA_DEV float* st_l() const { return st_scale() + 2 * kBM; }
-  FA_DEV float* st_lr() const { return st_l() + 2 * kBM; }
-  FA_DEV float* st_m() const { return st_lr() + 2 * kBM; }
+  FA_DEV float* st_m() const { return st_l() + 2 * kBM; }
+  FA_DEV float* st_lr() const { return kFp8 ? st_l() : st_m() + 2 * kBM; }      // E4M3: one sum for both
   FA_DEV volatile Seg* segs() const { return reinterpret_cast<volatile Seg*>(base + L::kSegRing); }
   FA_DEV bool wait(uint32_t b, uint32_t parity, int site, const PagedAttnParams& p) const {
     return mbar_wait_bounded(b, parity, abort(), &g_err, site, p.wait_limit_ns);
@@ -522,23 +545,74 @@ __device__ void clean_role(const Shared<D, false>& sh, const PagedAttnParams& p)
   }
 }
 
+FA_DEV uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Two E4M3 codes (the lower half of w) as FP16, exactly, times f.
+FA_DEV uint32_t widened(uint32_t w, uint32_t f) {
+  uint32_t r;
+  asm("{\n\t.reg .b32 h;\n\tcvt.rn.f16x2.e4m3x2 h, %1;\n\tmul.rn.f16x2 %0, h, %2;\n\t}"
+      : "=r"(r)
+      : "h"((uint16_t)w), "r"(f));
+  return r;
+}
+// 2^d, d <= 0, as FP16 twice; zero below its range.
+FA_DEV uint32_t power_f16x2(int d) {
+  const uint32_t h = d >= -14 ? (uint32_t)(15 + d) << 10 : d >= -24 ? 1u << (24 + d) : 0u;
+  return h | h << 16;
+}
+
+// The largest scale bytes (of finite rows) among the segment's keys and values,
+// left in `tops`; the eight widening warps, 16 keys a thread at a time.
+template <int D>
+FA_DEV void find_tops(const PagedAttnParams& p, const Seg& w, int blocks, int* tops) {
+  const int lane = threadIdx.x % 32, thread = threadIdx.x - 512;
+  const int first = w.kb * kBN, end = min(w.L, (w.kb + blocks) * kBN);
+  const int* table = p.s.block_table + (size_t)w.b * p.s.max_pages;
+  uint32_t top[2] = {0u, 0u};                        // per byte
+#pragma unroll 4
+  for (int key = first + 16 * thread; key < end; key += 16 * 256) {
+    const int page = table[key >> p.s.page_shift];
+    if (page < 0 || page >= p.s.num_pages) continue;
+    const size_t row = ((size_t)page * p.s.Hkv + w.head << p.s.page_shift) + (key & ((1 << p.s.page_shift) - 1));
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      const uint4 x = *reinterpret_cast<const uint4*>((which ? p.v_scale : p.k_scale) + row);
+      const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int left = end - key - 4 * i;          // bytes of the word that count
+        const uint32_t on = left >= 4 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+        top[which] = __vmaxu4(top[which], v[i] & on & ~__vcmpeq4(v[i], 0xFFFFFFFFu));
+      }
+    }
+  }
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    const uint32_t m = max(max(top[which] & 255u, (top[which] >> 8) & 255u), max((top[which] >> 16) & 255u, top[which] >> 24));
+    const int all = __reduce_max_sync(0xffffffffu, (int)m);
+    if (lane == 0) tops[8 * which + thread / 32] = all;
+  }
+}
+
 // E4M3 pages: eight warps widen the tiles, four the keys and four the values, a
-// piece of 16 codes at a time, into the swizzled BF16 tiles that the products
-// read.  Rows behind the sequence's end come out as zeros.  (Four warps for
-// both left the MMA warp waiting two thirds of the time: 749 us for a chunk of
-// 512 tokens over 32K keys, 76 heads.)
+// piece of 16 codes at a time, into the swizzled FP16 tiles that the products
+// read.  Rows behind the sequence's end come out as zeros.
 template <int D>
 __device__ void widen_role(const Shared<D, true>& sh, const PagedAttnParams& p) {
   using L = Layout<D, true>;
   // A step is a warp's 32 pieces of 16 codes.  The eight lanes that load and
   // store together touch all banks: at D = 128 they are four pieces of rows r
   // and r ^ 5 (the 128-byte swizzle puts the halves of a raw row apart by bit 2
-  // of its number, the even and odd pieces of a BF16 row by bit 0), a step
+  // of its number, the even and odd pieces of a wide row by bit 0), a step
   // rows {0, 5, 1, 4} or {2, 7, 3, 6} of eight; at D = 64 two neighbouring rows.
   constexpr int kSteps = D / 16;
   constexpr int kGroups = D == 128 ? 1 : 2;          // of eight rows, in two steps
   constexpr int kDown = 8 * kGroups * D;             // raw bytes
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32 % 4;
+  const bool values = threadIdx.x >= 640;
   const int tt = tile_tokens(p.group);
   int row[2], from[2], to[2][2];                     // in the warp's 32 rows; offsets of the tiles
 #pragma unroll
@@ -553,9 +627,15 @@ __device__ void widen_role(const Shared<D, true>& sh, const PagedAttnParams& p) 
   }
   SegReader<D, true> in(sh, p);
   Seg w;
-  uint32_t at = threadIdx.x / 128 - 4;               // tile in the order of the loads: keys even, values odd
+  uint32_t at = values ? 1 : 0;                      // tile in the order of the loads: keys even, values odd
+  uint32_t seg = 0;
   while (in.next(w)) {
     const int n = max(tile_blocks(w, 0, tt, p.causal), tile_blocks(w, 1, tt, p.causal));
+    if (n == 0) continue;
+    find_tops<D>(p, w, n, sh.tops(seg));
+    named_barrier(1, 256);
+    const int top = values ? sh.value_top(seg) : sh.key_top(seg);
+    ++seg;
 #pragma unroll 1
     for (int j = 0; j < n; ++j, at += 2) {
       const int rows = w.L - (w.kb + j) * kBN;
@@ -564,39 +644,23 @@ __device__ void widen_role(const Shared<D, true>& sh, const PagedAttnParams& p) 
       if (!sh.wait(sh.kv_empty(stage), (at / L::kStages & 1) ^ 1, kSiteKvEmpty, p)) return;
       const uint8_t* src = sh.base + L::kRaw + raw * L::kRawBytes;
       uint8_t* dst = sh.base + L::kKV + stage * L::kTileBytes;
-      // Lane l holds the factors of row 32 warp + l: 2^(120 + e), which takes
-      // the raw codes' 2^-120 along.  That power does not exist for e > 7: the
-      // rest is a second factor, for the rare tile that needs one.  Rows behind
-      // the end are multiplied by zero (no raw code is a NaN or an infinity).
-      const int mine = warp * 32 + lane;
-      const uint32_t byte = sh.base[L::kRawScale + raw * kBN + mine];
-      const uint32_t first = min(byte, 134u);       // e = 7
-      uint32_t f = mine < rows ? (first + 120u) << 7 : 0u;
-      uint32_t g = byte == 255u ? 0x7FC0u : (byte - first + 127u) << 7;
-      f |= f << 16;
-      g = mine < rows ? g | g << 16 : 0u;
-      const bool big = __any_sync(0xffffffffu, byte > 134u && mine < rows);
-#pragma unroll
+      // lane l holds the factor of row 32 warp + l
+      const int byte = sh.base[L::kRawScale + raw * kBN + warp * 32 + lane];
+      const uint32_t f = byte == 255 ? 0x7E007E00u : power_f16x2(byte - top);
+      const bool ragged = rows < kBN;
+#pragma unroll 4
       for (int i = 0; i < kSteps; ++i) {
         // rows of a step repeat every two steps, 8 rows (1024 bytes) further
         const int odd = i & 1, down = i >> 1;
-        const uint4 x = *reinterpret_cast<const uint4*>(src + from[odd] + down * kDown);
-        const uint32_t fr = __shfl_sync(0xffffffffu, f, row[odd] + down * 8 * kGroups);
-        const uint32_t words[4] = {x.x, x.y, x.z, x.w};
-        uint32_t y[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          // codes 2 k and 2 k + 1 to the upper bytes of the halves
-          const uint32_t c = __byte_perm(words[k / 2], 0u, k & 1 ? 0x3424 : 0x1404);
-          y[k] = paged::mul_bf16x2(((c >> 4) & 0x07F007F0u) | (c & 0x80008000u), fr);
-        }
-        if (big) {
-          const uint32_t gr = __shfl_sync(0xffffffffu, g, row[odd] + down * 8 * kGroups);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) y[k] = paged::mul_bf16x2(y[k], gr);
-        }
-        *reinterpret_cast<uint4*>(dst + to[odd][0] + down * 1024 * kGroups) = make_uint4(y[0], y[1], y[2], y[3]);
-        *reinterpret_cast<uint4*>(dst + to[odd][1] + down * 1024 * kGroups) = make_uint4(y[4], y[5], y[6], y[7]);
+        const int r = row[odd] + down * 8 * kGroups;
+        uint4 x = *reinterpret_cast<const uint4*>(src + from[odd] + down * kDown);
+        const uint32_t fr = __shfl_sync(0xffffffffu, f, r);
+        if (ragged && warp * 32 + r >= rows) x = make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t fz = ragged && warp * 32 + r >= rows ? 0u : fr;
+        *reinterpret_cast<uint4*>(dst + to[odd][0] + down * 1024 * kGroups) =
+            make_uint4(widened(x.x, fz), widened(x.x >> 16, fz), widened(x.y, fz), widened(x.y >> 16, fz));
+        *reinterpret_cast<uint4*>(dst + to[odd][1] + down * 1024 * kGroups) =
+            make_uint4(widened(x.z, fz), widened(x.z >> 16, fz), widened(x.w, fz), widened(x.w >> 16, fz));
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -633,13 +697,16 @@ FA_DEV float max32(const uint32_t (&x)[32]) {
 }
 
 // A row's weights and sums, 32 scores at a time.
+template <bool kFp16>
 struct RowSums {
-  uint64_t scale2, negm2;      // pairs of scale, -maximum
-  uint64_t e2[2], r2[2];       // sums of the FP32 weights (LSE), and of those rounded to BF16, as the product
-                               // takes them (the division); a NaN among the scores passes into both
+  uint64_t scale2, negm2;      // pairs of scale, -maximum (FP16: + kWeightUp)
+  uint64_t e2[2];              // sums of the FP32 weights (LSE); a NaN among the scores passes into them
+  uint64_t r2[2];              // BF16: and of the weights as they are rounded for the product, for the division.
+                               // FP16 weights are off by 2^-12 at most: not worth a sum of their own
   FA_DEV void begin(float scale, float m) {
     scale2 = pk2(scale, scale);
-    negm2 = pk2(-m, -m);
+    const float b = kFp16 ? kWeightUp - m : -m;
+    negm2 = pk2(b, b);
     e2[0] = e2[1] = r2[0] = r2[1] = 0ull;
   }
   FA_DEV void weights(const uint32_t (&x)[32], uint32_t* pk) {
@@ -649,20 +716,58 @@ struct RowSums {
       float x0, x1;
       up2(x2, x0, x1);
       const float e0 = ex2_mufu(x0), e1 = ex2_mufu(x1);
-      const uint32_t pp = pack_bf16x2(e0, e1);
+      const uint32_t pp = kFp16 ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
       pk[i / 2] = pp;
       e2[(i / 2) & 1] = add2(e2[(i / 2) & 1], pk2(e0, e1));
-      r2[(i / 2) & 1] = add2(r2[(i / 2) & 1], pk2(__uint_as_float(pp << 16), __uint_as_float(pp & 0xFFFF0000u)));
+      if (!kFp16)
+        r2[(i / 2) & 1] = add2(r2[(i / 2) & 1], pk2(__uint_as_float(pp << 16), __uint_as_float(pp & 0xFFFF0000u)));
     }
   }
   FA_DEV void totals(float& e, float& r) const {
     float a, b;
     up2(add2(e2[0], e2[1]), a, b);
     e = a + b;
-    up2(add2(r2[0], r2[1]), a, b);
-    r = a + b;
+    if (kFp16) {
+      r = e;
+    } else {
+      up2(add2(r2[0], r2[1]), a, b);
+      r = a + b;
+    }
   }
 };
+
+// Row r of tile t of Q, in place, to FP16 by a power of two of its own: 2^(13 - e),
+// below 2^14 then; returns e.
+template <int D>
+FA_DEV int narrow_row(const Shared<D, true>& sh, int t, int r) {
+  using L = Layout<D, true>;
+  uint8_t* row = sh.base + L::kQ + t * L::kTileBytes + r * 128;
+  uint4 x[D / 8];
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i)     // (in an order in which eight neighbouring rows touch all banks)
+    x[i] = *reinterpret_cast<const uint4*>(row + (i / 8) * L::kChunkBytes + (((i ^ r) & 7) << 4));
+  uint32_t m[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) {
+    m[0] = paged::max_bf16x2(m[0], x[i].x & 0x7FFF7FFFu);
+    m[1] = paged::max_bf16x2(m[1], x[i].y & 0x7FFF7FFFu);
+    m[2] = paged::max_bf16x2(m[2], x[i].z & 0x7FFF7FFFu);
+    m[3] = paged::max_bf16x2(m[3], x[i].w & 0x7FFF7FFFu);
+  }
+  m[0] = paged::max_bf16x2(paged::max_bf16x2(m[0], m[1]), paged::max_bf16x2(m[2], m[3]));
+  const int e = max((int)(max(m[0] & 0xFFFFu, m[0] >> 16) >> 7), 27) - 127;       // of the largest value, -100 at least
+  const float up = __uint_as_float((uint32_t)(127 + 13 - e) << 23);
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) {
+    const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    uint32_t y[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      y[k] = pack_f16x2(__uint_as_float(v[k] << 16) * up, __uint_as_float(v[k] & 0xFFFF0000u) * up);
+    *reinterpret_cast<uint4*>(row + (i / 8) * L::kChunkBytes + (((i ^ r) & 7) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+  }
+  return e;
+}
 
 // Softmax of tile t: one thread per row.  The scores are read from tensor memory
 // twice, for the maximum and for the exponentials, 32 columns at a time with
@@ -676,20 +781,36 @@ __device__ void softmax_role(const int t, const Shared<D, kFp8>& sh, const uint3
   const int wq = warp & 3;
   const int r_in_tile = wq * 32 + lane;
   const uint32_t tm_s = tmem + (uint32_t(wq * 32) << 16) + uint32_t(t * kBN);
-  const float sl2 = p.scale_log2;
+  float sl2 = p.scale_log2;
   const int tt = tile_tokens(p.group);
   const int my_tok = r_in_tile / p.group;
   SegReader<D, kFp8> in(sh, p);
   Seg w;
-  uint32_t sit = 0;
+  uint32_t sit = 0, seg = 0;
   while (in.next(w)) {
     const int nt = tile_blocks(w, t, tt, p.causal);
+    int q_exp = 0;
+    if constexpr (kFp8) {
+      // Both tiles' warps take every segment's Q, also when theirs has no block,
+      // so that neither falls two phases behind.
+      if (max(nt, tile_blocks(w, t ^ 1, tt, p.causal)) > 0) {
+        if (!sh.wait(sh.q_full(), seg & 1, kSiteQFull, p)) return;
+        if (nt > 0) q_exp = narrow_row<D>(sh, t, r_in_tile);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sh.q_ready());
+        ++seg;
+      }
+    }
     if (nt == 0) continue;
     const int tok = w.tok0 + t * tt;
     const int lim_first = p.causal ? w.L - w.n + tok + 1 : w.L;                  // of the tile's first row
     const int lim_row = p.causal ? min(w.L, lim_first + my_tok) : w.L;
+    // rows of the tile that are no token's hold anything: they must not cause
+    // rescaling
+    const bool live = my_tok < tt && tok + my_tok < w.n;
     float m_run = -INFINITY, l_run = 0.0f, lr_run = 0.0f;
-    RowSums sums;
+    RowSums<kFp8> sums;
     // The new running maximum from the block's; returns the factor for what
     // was summed so far.  Lazy: a maximum that grew by less than the threshold
     // stays.
@@ -708,7 +829,7 @@ __device__ void softmax_role(const int t, const Shared<D, kFp8>& sh, const uint3
     // The first half of P is in place: the factor goes along.
     auto give_lo = [&](float factor, bool rescaled) {
       sh.st_scale()[t * kBM + r_in_tile] = factor;
-      const unsigned any = __any_sync(0xffffffffu, rescaled);
+      const unsigned any = __any_sync(0xffffffffu, rescaled && live);
       if (lane == 0) sh.warp_flag()[t * 4 + wq] = any ? 1 : 0;
       tmem_st_wait();
       tc_fence_before();
@@ -717,6 +838,13 @@ __device__ void softmax_role(const int t, const Shared<D, kFp8>& sh, const uint3
     for (int j = 0; j < nt; ++j, ++sit) {
       if (!sh.wait(sh.s_full(t), sit & 1, kSiteS, p)) return;
       tc_fence_after();
+      if (kFp8 && j == 0) {
+        // the scores' unit: of the row of Q, and of the segment's keys.  2^-100 at
+        // least: a masked score is -inf times this, which zero would make NaN
+        const int top = sh.key_top(seg - 1);
+        const int unit = min(max(q_exp - 13 + (top > 0 ? top - 127 : 0), -100), 127);
+        sl2 = p.scale_log2 * __uint_as_float((uint32_t)(unit + 127) << 23);
+      }
       const int kv0 = (w.kb + j) * kBN;
       const bool need_mask = kv0 + kBN > lim_first;
       const int lim = lim_row - kv0;            // columns >= lim are masked
@@ -760,8 +888,8 @@ __device__ void softmax_role(const int t, const Shared<D, kFp8>& sh, const uint3
       lr_run = lr_run * factor + r;
       tmem_st_wait();
       if (j == nt - 1) {
-        sh.st_l()[t * kBM + r_in_tile] = l_run;
-        sh.st_lr()[t * kBM + r_in_tile] = lr_run;
+        sh.st_l()[t * kBM + r_in_tile] = kFp8 ? l_run * 0.0078125f : l_run;        // 2^-kWeightUp
+        sh.st_lr()[t * kBM + r_in_tile] = kFp8 ? lr_run * 0.0078125f : lr_run;
         sh.st_m()[t * kBM + r_in_tile] = m_run;
       }
       tc_fence_before();
@@ -784,10 +912,12 @@ __device__ void correction_role(const Shared<D, kFp8>& sh, const uint32_t tmem, 
   SegReader<D, kFp8> in(sh, p);
   Seg w;
   uint32_t sit = 0;      // phase bits of the two tiles
-  uint32_t uit[2] = {0u, 0u};
+  uint32_t uit[2] = {0u, 0u}, seg = 0;
   while (in.next(w)) {
     const int nts[2] = {tile_blocks(w, 0, tt, p.causal), tile_blocks(w, 1, tt, p.causal)};
     const int n = max(nts[0], nts[1]);
+    if (kFp8 && n > 0) ++seg;
+    float unit = 1.0f;       // of O
     float fin_l[2] = {0.0f, 0.0f}, fin_lr[2] = {0.0f, 0.0f}, fin_m[2] = {-INFINITY, -INFINITY};
     for (int j = 0; j < n; ++j) {
 #pragma unroll 1
@@ -844,7 +974,11 @@ __device__ void correction_role(const Shared<D, kFp8>& sh, const uint32_t tmem, 
         tc_fence_after();
       }
       const float l = fin_l[t], lr = fin_lr[t], m = fin_m[t];
-      const float inv = w.slot >= 0 ? 1.0f : lr == 0.0f ? 0.0f : 1.0f / lr;
+      if (kFp8 && has) {
+        const int top = sh.value_top(seg - 1);
+        unit = top > 0 ? __uint_as_float((uint32_t)max(top - (int)kWeightUp, 0) << 23) : 1.0f;   // 2^(top - 127 - kWeightUp)
+      }
+      const float inv = w.slot >= 0 ? unit : lr == 0.0f ? 0.0f : unit / lr;
       const int head = w.head * p.group + my_head;
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + ((size_t)(w.q0 + tok) * p.Hq + head) * D;
       float* part = Part<D>::out(p.part, max(w.slot, 0)) + (t * kBM + r_in_tile) * D;
@@ -861,6 +995,10 @@ __device__ void correction_role(const Shared<D, kFp8>& sh, const uint32_t tmem, 
           for (int i = 0; i < 32; ++i) r[i] = 0u;
         }
         if (valid && w.slot >= 0) {
+          if (kFp8) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * inv);
+          }
 #pragma unroll
           for (int v = 0; v < 4; ++v) st_global_v8(part + c * 32 + v * 8, r + v * 8);
         } else if (valid) {
@@ -938,8 +1076,10 @@ FA_DEV void mma4_ts(uint32_t d, uint32_t a, uint32_t blo, uint32_t bhi, uint32_t
 template <int D, bool kFp8>
 __device__ void mma_role(const Shared<D, kFp8>& sh, const uint32_t tmem, const PagedAttnParams& p) {
   using L = Layout<D, kFp8>;
-  constexpr uint32_t kIdS = idesc_bf16_f32(kBM, kBN, false, false);
-  constexpr uint32_t kIdPV = idesc_bf16_f32(kBM, D, false, true);
+  // E4M3: both operands of both products are FP16 (format 0 in place of BF16's 1)
+  constexpr uint32_t kFormats = kFp8 ? (1u << 7) | (1u << 10) : 0u;
+  constexpr uint32_t kIdS = idesc_bf16_f32(kBM, kBN, false, false) & ~kFormats;
+  constexpr uint32_t kIdPV = idesc_bf16_f32(kBM, D, false, true) & ~kFormats;
   const int tt = tile_tokens(p.group);
   uint32_t uit = 0;
   uint32_t sit = 0;      // phase bits of the two tiles
@@ -988,7 +1128,7 @@ __device__ void mma_role(const Shared<D, kFp8>& sh, const uint32_t tmem, const P
     const int n0 = tile_blocks(w, 0, tt, p.causal), n1 = tile_blocks(w, 1, tt, p.causal);
     const int n = max(n0, n1);
     if (n == 0) continue;
-    if (!sh.wait(sh.q_full(), uit & 1, kSiteQFull, p)) return;
+    if (!sh.wait(kFp8 ? sh.q_ready() : sh.q_full(), uit & 1, kSiteQFull, p)) return;
     tc_fence_after();
     Pos kp = take(), vp{0, 0u};
     if (!ready(kp)) return;
@@ -1061,6 +1201,7 @@ __global__ void __launch_bounds__(Layout<D, kFp8>::kThreads, 1)
       mbar_init(sh.seg_empty(s), L::kReaders);
     }
     for (int s = 0; s < (kFp8 ? 0 : L::kStages); ++s) mbar_init(sh.v_landed(s), 1);
+    if (kFp8) mbar_init(sh.q_ready(), 8);
     for (int s = 0; s < L::kRaws; ++s) {
       mbar_init(sh.raw_full(s), 1);
       mbar_init(sh.raw_empty(s), 4);

@@ -174,6 +174,12 @@ FA_DEV uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+// Larger of two BF16 pairs, element by element; NaN if either is.
+FA_DEV uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 constexpr uint32_t kTwo120 = 0x7B807B80u;   // 2^120 twice
 FA_DEV uint32_t e4m3_even(uint32_t w) { return mul_bf16x2(e4m3_even_raw(w), kTwo120); }
 FA_DEV uint32_t e4m3_odd(uint32_t w) { return mul_bf16x2(e4m3_odd_raw(w), kTwo120); }
