@@ -490,22 +490,22 @@ __device__ void load_role(const Shared<D, kFp8>& sh, const CUtensorMap* tq, cons
         __syncwarp();
         const CUtensorMap* map = which ? tv : tk;
         const uint32_t dst = sh.sbase + (kFp8 ? L::kRaw + stage * L::kRawBytes : L::kKV + stage * L::kTileBytes);
-        for (int i = 0; i < boxes; ++i) {
-          const int page = __shfl_sync(0xffffffffu, pages, page0 + i - held);
-          if (lane == 0) {
-            const int off = (key0 + i * box) & ((1 << p.s.page_shift) - 1);
-            const int ph = page < 0 ? -1 : page * p.s.Hkv + w.head;    // -1: reads as zeros
-            if (kFp8) {
-              tma_load_3d(dst + i * box * D, map, full, 0, off, ph);
-              bulk_load(sh.sbase + L::kRawScale + stage * kBN + i * box,
-                        (which ? p.v_scale : p.k_scale) + ((size_t)max(ph, 0) << p.s.page_shift) + off, box, full);
-            } else {
-#pragma unroll
-              for (int c = 0; c < L::kChunks; ++c)
-                tma_load_3d(dst + c * L::kChunkBytes + i * box * 128, map, full, c * 64, off, ph);
-            }
+        // each lane issues its own box
+        constexpr int kParts = kFp8 ? 1 : L::kChunks;
+        const int i = lane / kParts, c = lane % kParts;
+        const int page = __shfl_sync(0xffffffffu, pages, (page0 + i - held) & 31);
+        if (i < boxes) {
+          const int off = (key0 + i * box) & ((1 << p.s.page_shift) - 1);
+          const int ph = page < 0 ? -1 : page * p.s.Hkv + w.head;    // -1: reads as zeros
+          if (kFp8) {
+            tma_load_3d(dst + i * box * D, map, full, 0, off, ph);
+            bulk_load(sh.sbase + L::kRawScale + stage * kBN + i * box,
+                      (which ? p.v_scale : p.k_scale) + ((size_t)max(ph, 0) << p.s.page_shift) + off, box, full);
+          } else {
+            tma_load_3d(dst + c * L::kChunkBytes + i * box * 128, map, full, c * 64, off, ph);
           }
         }
+        __syncwarp();
         if (++stage == kRing) {
           stage = 0;
           phase ^= 1;
