@@ -23,9 +23,9 @@
 //   * Pipeline.  One warp looks up the pages of the stretch's blocks, 32 at a
 //     time and on into the next units.  The other warps take the blocks in turn
 //     and each refills by TMA the slots of the ring in shared memory that it
-//     empties (the pages' rows, swizzled for ldmatrix): one thread issues a TMA
-//     load in some 150 cycles, too slow to feed an SM alone (313 us for 64 x 4096
-//     BF16 keys, against 172).  No warp waits for another until the unit's end,
+//     empties (the pages' rows, swizzled for ldmatrix), every lane with a load of
+//     its own: a single thread issues one in some 150 cycles, too slow to feed an
+//     SM alone (313 us for 64 x 4096 BF16 keys).  No warp waits for another until the unit's end,
 //     where their softmax states are merged.
 //   * E4M3 pages are widened in registers on the way to the tensor cores, to
 //     FP16, which holds every code and which one instruction makes of a pair (to
@@ -371,28 +371,24 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
   auto load = [&](uint32_t q) {
     const int b = q / 32 % L::kBatches;
     if (!mbar_wait_bounded(placed + 8 * b, q / (32 * L::kBatches) & 1, abort, &g_err, kSitePlaced, p.wait_limit_ns)) return;
-    if (lane == 0) {
-      const int4 place = places[q % (32 * L::kBatches)];
-      mbar_arrive(taken + 8 * b);
-      if (place.x != kEnd) {
-        const uint32_t slot = q % L::kSlots, bar = full + 8 * slot;
-        mbar_arrive_expect_tx(bar, 2 * L::kTile + (kFp8 ? 2 * kKeys : 0));
-        for (int j = 0; j <= two; ++j) {
-          const int ph = j ? place.y : place.x, off = j ? place.w : place.z;
-          const uint32_t dst = sbase + L::kRing + slot * L::kStage + (j << box_shift) * (kFp8 ? D : 128);
-#pragma unroll
-          for (int h = 0; h < (kFp8 ? 1 : D / 64); ++h) {
-            tma_load_3d(dst + h * kKeys * 128, &tm_k, bar, h * 64, off, ph);
-            tma_load_3d(dst + L::kTile + h * kKeys * 128, &tm_v, bar, h * 64, off, ph);
-          }
-          if (kFp8) {
-            const size_t row = ((size_t)max(ph, 0) << p.s.page_shift) + off;
-            const uint32_t sc = sbase + L::kScales + slot * 2 * kKeys + (j << box_shift);
-            bulk_load(sc, p.k_scale + row, 1 << box_shift, bar);
-            bulk_load(sc + kKeys, p.v_scale + row, 1 << box_shift, bar);
-          }
-        }
-      }
+    const int4 place = places[q % (32 * L::kBatches)];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(taken + 8 * b);
+    if (place.x == kEnd) return;
+    const uint32_t slot = q % L::kSlots, bar = full + 8 * slot;
+    if (lane == 0) mbar_arrive_expect_tx(bar, 2 * L::kTile + (kFp8 ? 2 * kKeys : 0));
+    __syncwarp();
+    // each lane issues its own load: keys or values, 64-column chunk, box
+    constexpr int kParts = kFp8 ? 2 : D / 32;
+    const int j = lane / kParts, which = lane & 1, h = lane % kParts / 2;
+    if (j <= two) {
+      const int ph = j ? place.y : place.x, off = j ? place.w : place.z;
+      tma_load_3d(sbase + L::kRing + slot * L::kStage + which * L::kTile + h * kKeys * 128 +
+                      (j << box_shift) * (kFp8 ? D : 128),
+                  which ? &tm_v : &tm_k, bar, h * 64, off, ph);
+      if (kFp8)
+        bulk_load(sbase + L::kScales + slot * 2 * kKeys + which * kKeys + (j << box_shift),
+                  (which ? p.v_scale : p.k_scale) + ((size_t)max(ph, 0) << p.s.page_shift) + off, 1 << box_shift, bar);
     }
     __syncwarp();
   };
