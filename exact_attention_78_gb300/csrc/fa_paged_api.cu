@@ -50,11 +50,14 @@ fa_status check_cache(const void* k_pages, const void* v_pages, const void* k_sc
   return FA_OK;
 }
 
-// Rows of one sequence and key/value head up to which a call takes the decode
-// kernel; above it the chunk kernel.
-constexpr int kDecodeRows = 32;
-bool takes_decode(int Hq, int Hkv, int Sn, bool packed, int max_q) {
-  return (long long)(packed ? max_q : Sn) * (Hq / Hkv) <= kDecodeRows;
+// Whether a call takes the decode kernel: up to kDecodeRows rows of one sequence
+// and key/value head; else the chunk kernel.  64 sequences of 4096 keys, 32/8
+// heads, decode against chunk kernel: 16 rows 177 / 186 us (D = 128 BF16), 127 /
+// 222 (E4M3), 97 / 167 and 103 / 185 (D = 64); 32 rows, whose accumulators do not fit
+// the registers at D = 128, 412 / 186 and 370 / 222, but 128 / 168 and 145 / 186
+// (D = 64).
+bool takes_decode(int Hq, int Hkv, int Sn, int D, bool packed, int max_q) {
+  return (long long)(packed ? max_q : Sn) * (Hq / Hkv) <= kDecodeRows(D);
 }
 
 bool attn_shape_ok(int B, int Hq, int Hkv, int Sn, int D, bool packed, int max_q, fa_status* why) {
@@ -183,7 +186,7 @@ fa_status fa_cache_read(const void* k_pages, const void* v_pages, const void* k_
 size_t fa_fwd_paged_workspace_size(int B, int Hq, int Hkv, int Sn, int D, int packed, int max_q) {
   fa_status why;
   if ((packed != 0 && packed != 1) || !attn_shape_ok(B, Hq, Hkv, Sn, D, packed != 0, max_q, &why)) return 0;
-  return takes_decode(Hq, Hkv, Sn, packed != 0, max_q) ? paged_decode_workspace(D) : paged_chunk_workspace(D);
+  return takes_decode(Hq, Hkv, Sn, D, packed != 0, max_q) ? paged_decode_workspace(D) : paged_chunk_workspace(D);
 }
 
 fa_status fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages, const void* k_scale,
@@ -222,7 +225,7 @@ fa_status fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages, 
     L.v_pages = v_pages;
     L.D = D;
     L.fp8 = k_scale != nullptr;
-    const bool decode = takes_decode(Hq, Hkv, Sn, cu_seqlens != nullptr, max_q);
+    const bool decode = takes_decode(Hq, Hkv, Sn, D, cu_seqlens != nullptr, max_q);
     return (decode ? launch_paged_decode : launch_paged_chunk)(L, reinterpret_cast<cudaStream_t>(stream));
   } catch (...) {
     return FA_ERR_CUDA;

@@ -6,15 +6,15 @@
 // them, so HBM bounds it: the design keeps loads in flight and splits the keys
 // evenly over the SMs.
 //
-//   * Rows.  The query heads of one key/value head, for up to 32 rows of
-//     (new token, head of the group), share the keys that a warp loads.  They
-//     are the N side of the products, 8 rows an mma.sync tile, and keys (for
-//     S^T = K Q^T) and columns of V (for O^T = V^T P^T) the M side: with 8 rows
-//     or fewer, the usual case, that halves the products and the softmax
-//     against rows on the M side, whose tiles are 16 high.  (tcgen05 tiles
-//     have at least 64 rows on M and their accumulators are a trip through
-//     tensor memory away; with so few rows the warp-level instruction leaves
-//     the tensor cores a quarter busy.)
+//   * Rows.  The query heads of one key/value head, for up to 16 rows (32 at
+//     D = 64) of (new token, head of the group), share the keys that a warp
+//     loads.  They are the N side of the products, 8 rows an mma.sync tile, and
+//     keys (for S^T = K Q^T) and columns of V (for O^T = V^T P^T) the M side:
+//     with 8 rows or fewer, the usual case, that halves the products and the
+//     softmax against rows on the M side, whose tiles are 16 high.  (tcgen05
+//     tiles have at least 64 rows on M and their accumulators are a trip through
+//     tensor memory away; with so few rows the warp-level instruction leaves the
+//     tensor cores a quarter busy.)
 //   * Work.  The key blocks of all (sequence, key/value head, row tile)
 //     units form one line, and thread block c takes the c-th of `grid` equal
 //     stretches of it.  A unit cut by a border leaves partial results in the
@@ -25,8 +25,8 @@
 //     and each refills by TMA the slots of the ring in shared memory that it
 //     empties (the pages' rows, swizzled for ldmatrix), every lane with a load of
 //     its own: a single thread issues one in some 150 cycles, too slow to feed an
-//     SM alone (313 us for 64 x 4096 BF16 keys).  No warp waits for another until the unit's end,
-//     where their softmax states are merged.
+//     SM alone (313 us for 64 x 4096 BF16 keys).  No warp waits for another until
+//     the unit's end, where their softmax states are merged.
 //   * E4M3 pages are widened in registers on the way to the tensor cores, to
 //     FP16, which holds every code and which one instruction makes of a pair (to
 //     BF16 it takes five).  The queries become FP16 by a power of two of each
@@ -859,14 +859,16 @@ template <int D, bool kFp8>
 fa_status launch_tiles(const PagedAttnLaunch& L, cudaStream_t stream) {
   const long long rows = (long long)L.p.max_q * L.p.group;
   if (rows <= 8) return launch_inst<D, kFp8, 1>(L, stream);
-  if (rows <= 16) return launch_inst<D, kFp8, 2>(L, stream);
-  return launch_inst<D, kFp8, 4>(L, stream);
+  if constexpr (kDecodeRows(D) > 16) {
+    if (rows > 16) return launch_inst<D, kFp8, 4>(L, stream);
+  }
+  return launch_inst<D, kFp8, 2>(L, stream);
 }
 
 }  // namespace pdec
 
 size_t paged_decode_workspace(int D) {
-  return D == 128 ? pdec::Part<128, 32>::bytes() : pdec::Part<64, 32>::bytes();
+  return D == 128 ? pdec::Part<128, kDecodeRows(128)>::bytes() : pdec::Part<64, kDecodeRows(64)>::bytes();
 }
 
 fa_status launch_paged_decode(const PagedAttnLaunch& L, cudaStream_t stream) {

@@ -92,6 +92,8 @@ fa_status device_info(int* num_sms);
 // many, so that the workspace's size is known without a device.
 constexpr int kMaxCtas = 160;
 
+// Most rows of one sequence and key/value head that the decode kernel takes.
+constexpr int kDecodeRows(int D) { return D == 64 ? 32 : 16; }
 size_t paged_decode_workspace(int D);
 size_t paged_chunk_workspace(int D);
 
