@@ -199,7 +199,8 @@ fa_status fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages, 
     if (!q || !o || !lse || !seq_lens || !aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 16))
       return FA_ERR_INVALID_ARG;
     if (causal != 0 && causal != 1) return FA_ERR_INVALID_ARG;
-    if (!(scale > 0.0f) || !std::isfinite(scale)) return FA_ERR_INVALID_ARG;
+    // (a factor of -inf, masked scores, has to be a normal number)
+    if (!(scale > 0.0f) || !std::isnormal(scale * kLog2e)) return FA_ERR_INVALID_ARG;
     fa_status st;
     if (!attn_shape_ok(B, Hq, Hkv, Sn, D, cu_seqlens != nullptr, max_q, &st)) return st;
     st = check_cache(k_pages, v_pages, k_scale, v_scale, B, Hkv, Sn, D, num_pages, page_size, max_pages, block_table,

@@ -160,12 +160,14 @@ struct Shared {
   FA_DEV float* st_lr() const { return kFp8 ? st_l() : st_m() + 2 * kBM; }      // E4M3: one sum for both
   FA_DEV volatile Seg* segs() const { return reinterpret_cast<volatile Seg*>(base + L::kSegRing); }
   FA_DEV bool wait(uint32_t b, uint32_t parity, int site, const PagedAttnParams& p) const {
-    return mbar_wait_bounded(b, parity, abort(), &g_err, site, p.wait_limit_ns);
+    return paged::wait_warp(b, parity, abort(), &g_err, site, p.wait_limit_ns);
   }
-  // For waits that last: sleeps between looks, off the issue slots.
+  // For waits that last as long as a segment (some seconds over 2^30 keys; the
+  // other roles wait for a block at a time, and give up first if nothing moves):
+  // sleeps between looks, off the issue slots.
   FA_DEV bool wait_long(uint32_t b, uint32_t parity, int site, const PagedAttnParams& p) const {
 #pragma unroll 1
-    for (int i = 0; i < (1 << 23) && !mbar_try_wait(b, parity) && !ld_shared_volatile(abort()); ++i) __nanosleep(200);
+    for (int i = 0; i < (1 << 27) && !mbar_try_wait(b, parity) && !ld_shared_volatile(abort()); ++i) __nanosleep(200);
     return wait(b, parity, site, p);
   }
 };
@@ -500,7 +502,8 @@ __device__ void load_role(const Shared<D, kFp8>& sh, const CUtensorMap* tq, cons
           if (kFp8) {
             tma_load_3d(dst + i * box * D, map, full, 0, off, ph);
             bulk_load(sh.sbase + L::kRawScale + stage * kBN + i * box,
-                      (which ? p.v_scale : p.k_scale) + ((size_t)max(ph, 0) << p.s.page_shift) + off, box, full);
+                      ph < 0 ? paged::g_no_scales : (which ? p.v_scale : p.k_scale) + ((size_t)ph << p.s.page_shift) + off,
+                      box, full);
           } else {
             tma_load_3d(dst + c * L::kChunkBytes + i * box * 128, map, full, c * 64, off, ph);
           }
@@ -839,11 +842,11 @@ __device__ void softmax_role(const int t, const Shared<D, kFp8>& sh, const uint3
       if (!sh.wait(sh.s_full(t), sit & 1, kSiteS, p)) return;
       tc_fence_after();
       if (kFp8 && j == 0) {
-        // the scores' unit: of the row of Q, and of the segment's keys.  2^-100 at
-        // least: a masked score is -inf times this, which zero would make NaN
+        // the scores' unit: of the row of Q, and of the segment's keys.  Normal
+        // at least: a masked score is -inf times this, which zero would make NaN
         const int top = sh.key_top(seg - 1);
         const int unit = min(max(q_exp - 13 + (top > 0 ? top - 127 : 0), -100), 127);
-        sl2 = p.scale_log2 * __uint_as_float((uint32_t)(unit + 127) << 23);
+        sl2 = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)(unit + 127) << 23), 1.17549435e-38f);
       }
       const int kv0 = (w.kb + j) * kBN;
       const bool need_mask = kv0 + kBN > lim_first;
@@ -1207,6 +1210,7 @@ __global__ void __launch_bounds__(Layout<D, kFp8>::kThreads, 1)
       mbar_init(sh.raw_empty(s), 4);
     }
     st_shared(sh.abort(), 0);
+    Part<D>::join(p.part, blockIdx.x)->parts = 0;      // the scheduler's to fill; after a give-up it stays
     fence_barrier_init();
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);

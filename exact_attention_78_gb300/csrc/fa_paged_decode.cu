@@ -99,6 +99,8 @@ struct Layout {
   static constexpr int kMisc = kPlaces + kBatches * 32 * 16;
   static constexpr int kBytes = kMisc + 64 + kSmemAlignSlack;
   static_assert(kBytes <= 232448, "dynamic shared memory above the 227 KB per-CTA limit");
+  // places are looked up to 64 behind the last block, and asked for up to kSlots
+  static_assert(kSlots <= 64, "slots whose places nobody looks up");
 };
 
 // ------------------------------------------------------------ the work line --
@@ -357,7 +359,7 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
         }
       }
       const int b = batch % L::kBatches;
-      if (!mbar_wait_bounded(taken + 8 * b, (batch / L::kBatches & 1) ^ 1, abort, &g_err, kSiteTaken, p.wait_limit_ns))
+      if (!paged::wait_warp(taken + 8 * b, (batch / L::kBatches & 1) ^ 1, abort, &g_err, kSiteTaken, p.wait_limit_ns))
         break;
       places[b * 32 + lane] = place;
       __syncwarp();
@@ -370,7 +372,7 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
   // Loads block q into its slot.  The whole warp calls it.
   auto load = [&](uint32_t q) {
     const int b = q / 32 % L::kBatches;
-    if (!mbar_wait_bounded(placed + 8 * b, q / (32 * L::kBatches) & 1, abort, &g_err, kSitePlaced, p.wait_limit_ns)) return;
+    if (!paged::wait_warp(placed + 8 * b, q / (32 * L::kBatches) & 1, abort, &g_err, kSitePlaced, p.wait_limit_ns)) return;
     const int4 place = places[q % (32 * L::kBatches)];
     __syncwarp();
     if (lane == 0) mbar_arrive(taken + 8 * b);
@@ -388,7 +390,8 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
                   which ? &tm_v : &tm_k, bar, h * 64, off, ph);
       if (kFp8)
         bulk_load(sbase + L::kScales + slot * 2 * kKeys + which * kKeys + (j << box_shift),
-                  (which ? p.v_scale : p.k_scale) + ((size_t)max(ph, 0) << p.s.page_shift) + off, 1 << box_shift, bar);
+                  ph < 0 ? paged::g_no_scales : (which ? p.v_scale : p.k_scale) + ((size_t)ph << p.s.page_shift) + off,
+                  1 << box_shift, bar);
     }
     __syncwarp();
   };
@@ -491,7 +494,7 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
 #pragma unroll 1
     for (int i = (warp + kWarps - q0 % kWarps) % kWarps; i < vis && !lost; i += kWarps) {
       const uint32_t slot = (q0 + i) % L::kSlots;
-      if (!mbar_wait_bounded(full + 8 * slot, (q0 + i) / L::kSlots & 1, abort, &g_err, kSiteFull, p.wait_limit_ns)) {
+      if (!paged::wait_warp(full + 8 * slot, (q0 + i) / L::kSlots & 1, abort, &g_err, kSiteFull, p.wait_limit_ns)) {
         lost = true;
         break;
       }
@@ -683,7 +686,7 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
         for (int d = 4; d < 32; d *= 2) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], d);
 #pragma unroll 1
     for (int r0 = 0; r0 < rows; r0 += L::kRound, ++round) {
-      if (!mbar_wait_bounded(merged, round & 1 ^ 1, abort, &g_err, kSiteMerged, p.wait_limit_ns)) lost = true;
+      if (!paged::wait_warp(merged, round & 1 ^ 1, abort, &g_err, kSiteMerged, p.wait_limit_ns)) lost = true;
       float* buf = merge;
       float* st_m = stats;
       float* st_l = st_m + kWarps * L::kRound;

@@ -12,6 +12,15 @@ FA_DEV void record_bad_input(DeviceError* err, int site) {
   if (atomicCAS(&err->status, 0, FA_ERR_INVALID_ARG) == 0) atomicExch(&err->site, site);
 }
 
+// A bounded wait of a whole warp, whose lanes all get one answer: a lane that
+// gave up alone would leave the others waiting for it at the next __syncwarp.
+FA_DEV bool wait_warp(uint32_t bar, uint32_t parity, uint32_t abort, DeviceError* err, int site, uint64_t limit_ns) {
+  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort, err, site, limit_ns));
+}
+
+// Scale bytes of the rows of a bad page, which reads as zeros (one box at most).
+static __device__ const __align__(128) uint8_t g_no_scales[128] = {};
+
 // The sequence that packed row i belongs to: the number of b in [1, B] with
 // cu[b] <= i (B where i lies behind the last sequence).  One warp searches for
 // one row, 32 offsets a step: two steps of independent loads for up to 1024
@@ -61,15 +70,15 @@ FA_DEV SeqRows rows_of(const PagedSeqs& s, int b) {
 }
 
 // Checks the sequences' offsets and lengths, and sums up their work: `work`
-// gives a sequence's {key blocks, units}, whose prefix sums go to bpre and (if
-// given) upre, [B + 1], and the longest unit of all to upre[B + 1].  All threads of the block; false, in all of them, when
-// the rules are broken.  Every attention kernel starts with this, so that one
-// pass and two barriers have to do: the loads, the sums within warps and the
-// check share the first.  `sums`: two values per warp.
+// gives a sequence's, whose prefix sums go to bpre and (if given) upre, [B + 1],
+// and the longest unit of all to upre[B + 1].  All threads of the block; false,
+// in all of them, when the rules are broken.  Both attention kernels start with
+// this, so one pass and two barriers have to do: the loads, the sums within
+// warps and the check share the first.  `sums`: two values per warp.
 struct Work {
-  long long blocks;
+  long long blocks;      // of keys (decode kernel), or keys (chunk kernel)
   int units;
-  int longest;      // unit
+  int longest;           // unit
 };
 template <class F>
 FA_DEV bool prefix_sequences(const PagedSeqs& s, int max_new, F work, long long* bpre, int* upre, long long* sums) {
