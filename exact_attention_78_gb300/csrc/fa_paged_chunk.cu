@@ -23,10 +23,11 @@
 //     FP32; the values' goes to O at the end.
 //   * Work.  Whole rounds of units, one per thread block, run in lockstep
 //     from the first key on, so that the pairs of a head share its keys in L2.
-//     The units left over are a line of keys that is cut into equal stretches
-//     (at the key block before each border), one per thread block; parts of a
-//     cut unit are joined by the combine kernel.  A few long chunks thus load all SMs.  A scheduler warp
-//     works out each thread block's segments and hands them to the other
+//     The units left over are a line, of their keys and a constant for each
+//     one's start and end, that is cut into equal stretches (at the key block
+//     before each border), one per thread block; parts of a cut unit are joined
+//     by the combine kernel.  A few long chunks thus load all SMs.  A scheduler
+//     warp works out each thread block's segments and hands them to the other
 //     warps through a small ring.
 //
 // Warps: 0-3 and 4-7 softmax of tile 0 and 1 (a thread per row), 8-11
@@ -55,6 +56,11 @@ constexpr float kThreshold = 8.0f;   // lazy rescaling, log2 units
 // most 2^15, and keep FP16's full precision down to 2^-21 of the maximum.
 constexpr float kWeightUp = 7.0f;
 constexpr int kMinStretch = 2 * kBN;  // keys: shorter stretches cost more to join than they save
+// What a unit takes on the line besides its keys: its start (queries, the first
+// scores) and its epilogue, when the tensor cores wait.  (12 ragged E4M3
+// sequences, 1 to 500 tokens over up to 9000 keys: as nothing 123 us, as one block
+// 119, 4 110, 8 115; others 138 -> 99, 119 -> 72.)
+constexpr int kUnitCost = 4 * kBN;
 
 enum Site {
   kSiteSeqs = 1, kSitePage, kSiteSegFull, kSiteSegEmpty, kSiteQEmpty, kSiteKvEmpty, kSiteKvFull, kSiteQFull, kSiteS,
@@ -184,8 +190,9 @@ struct Seq {
   // Keys of a pair: at least one, so that rows without a key are written too.
   FA_DEV int keys(int pair) const { return max(1, causal ? min(L, L - n + (pair + 1) * t2) : L); }
   FA_DEV int blocks(int pair) const { return (keys(pair) + kBN - 1) / kBN; }
-  // Keys of the pairs [0, p).
-  FA_DEV long long prefix(int p) const {
+  // What the pairs [0, p) take on the line: their keys, and kUnitCost each.
+  FA_DEV long long prefix(int p) const { return keys_before(p) + (long long)p * kUnitCost; }
+  FA_DEV long long keys_before(int p) const {
     if (!causal) return (long long)p * max(1, L);
     const long long last = p == pairs ? keys(pairs - 1) : 0;  // the one whose end the sequence's end cuts
     if (p == pairs) --p;
@@ -242,7 +249,7 @@ FA_DEV Line build_line(const PagedAttnParams& p, long long* kpre, int* upre, lon
       p.s, p.max_q,
       [&](const paged::SeqRows& rows) {
         const Seq s = seq_from(p, rows);
-        return paged::Work{s.total() * p.s.Hkv, s.pairs * p.s.Hkv, s.keys(s.pairs - 1)};
+        return paged::Work{s.total() * p.s.Hkv, s.pairs * p.s.Hkv, s.keys(s.pairs - 1) + kUnitCost};
       },
       kpre, upre, sums);
   if (!ok) {
@@ -281,7 +288,8 @@ struct Place {
   int b, head, i, kb;
   long long start;    // the unit's first position
 };
-// The last one at or before position t < t1.  One warp, converged.
+// The last one at or before position t < t1; kb may be the unit's blocks (t lies
+// in its cost: the unit stays whole).  One warp, converged.
 FA_DEV Place find_place(const PagedAttnParams& p, const Line& line, long long t) {
   Place w;
   w.b = last_at_most(line.kpre, p.s.B, t);
@@ -301,7 +309,7 @@ FA_DEV Place find_place(const PagedAttnParams& p, const Line& line, long long t)
   }
   w.i = lo;
   w.start = t - r + s.before(lo, per_head);
-  w.kb = (int)((t - w.start) / kBN);
+  w.kb = min((int)((t - w.start) / kBN), s.blocks(s.pairs - 1 - lo));
   return w;
 }
 
@@ -395,11 +403,11 @@ __device__ void scheduler_role(const Shared<D, kFp8>& sh, const PagedAttnParams&
     const bool to_end = c + 1 == line.G;
     const Place z = to_end ? Place{} : find_place(p, line, line.stretch(c + 1));
     Seq s = seq_of(p, w.b);
-    if (w.kb > 0) {
+    const int pair = s.pairs - 1 - w.i, nblk = s.blocks(pair);
+    if (w.kb > 0 && w.kb < nblk) {
       // the unit is cut here: if for the first time, its parts are joined
-      const int pair = s.pairs - 1 - w.i;
       if (line.stretch(c - 1) < w.start + kBN) {
-        const long long end = w.start + s.keys(pair);
+        const long long end = w.start + (long long)nblk * kBN;
         join = paged::Join{2, 2 * (c - 1) + 1, w.b, w.head, pair * s.t2, s.n, s.q0, 0};
         while (c + join.parts - 1 < line.G && line.stretch(c + join.parts - 1) < end) ++join.parts;
       }

@@ -16,10 +16,11 @@
 //     tensor memory away; with so few rows the warp-level instruction leaves the
 //     tensor cores a quarter busy.)
 //   * Work.  The key blocks of all (sequence, key/value head, row tile)
-//     units form one line, and thread block c takes the c-th of `grid` equal
-//     stretches of it.  A unit cut by a border leaves partial results in the
-//     workspace, at most two per thread block, and the combine kernel joins
-//     them.  Sequences of any mixture of lengths load all SMs alike.
+//     units, and a constant for each unit's start and end, form one line, and
+//     thread block c takes the c-th of `grid` equal stretches of it.  A unit cut
+//     by a border leaves partial results in the workspace, at most two per
+//     thread block, and the combine kernel joins them.  Sequences of any mixture
+//     of lengths load all SMs alike.
 //   * Pipeline.  One warp looks up the pages of the stretch's blocks, 32 at a
 //     time and on into the next units.  The other warps take the blocks in turn
 //     and each refills by TMA the slots of the ring in shared memory that it
@@ -110,6 +111,11 @@ FA_DEV Seq seq_of(const PagedSeqs& s, int b) { return paged::rows_of(s, b); }
 FA_DEV int tiles_of(int n, int group, int rows) { return (n * group + rows - 1) / rows; }
 // Blocks of a unit: at least one, so that rows without a key are written too.
 FA_DEV int blocks_of(int L, int keys) { return max(1, (L + keys - 1) / keys); }
+// What a unit takes on the line besides its blocks: starting and merging it.  (64
+// ragged sequences up to 8192 E4M3 keys, 8 heads: counted as nothing, 115 us, since
+// a stretch of short sequences has up to 16 units, the average 4; as 6 blocks
+// 106, 18 98, 32 101.)
+constexpr int kUnitCost = 18;
 
 // Prefix sums of the sequences' blocks into pre[0 .. B]; returns their total,
 // 0 when the sequences break the rules.  All threads of the block.
@@ -119,7 +125,7 @@ FA_DEV long long build_line(const PagedAttnParams& p, long long* pre, long long*
       p.s, p.max_q,
       [&](const Seq& q) {
         const int tiles = tiles_of(q.n, p.group, kRows);
-        return paged::Work{(long long)p.s.Hkv * tiles * blocks_of(q.L, kKeys), 0, 0};
+        return paged::Work{(long long)p.s.Hkv * tiles * (blocks_of(q.L, kKeys) + kUnitCost), 0, 0};
       },
       pre, nullptr, warp_sums);
   if (ok) return pre[p.s.B];
@@ -135,41 +141,47 @@ FA_DEV int active_ctas(long long total, int ctas) {
 // First block of stretch c of G.
 FA_DEV long long stretch(long long total, int c, int G) { return paged::div64(total * c, G); }
 
-// A walk over the segments (the stretch's share of one unit) of [t0, t1).
+// A walk over the segments (the stretch's share of one unit) of [t0, t1).  A
+// border behind a unit's blocks, in what starting and merging it counts, leaves
+// the unit whole.
 template <int kKeys, int kRows>
 struct Walk {
   int b, head, tile, tiles;
   Seq s;
   int nblk;          // blocks of the unit
   int kb, count;     // the segment: blocks [kb, kb + count)
-  long long left;    // blocks of the stretch from this segment on
+  long long start;   // the unit's first place on the line
+  long long t1;
 
   FA_DEV void load(const PagedAttnParams& p) {
     s = seq_of(p.s, b);
     tiles = tiles_of(s.n, p.group, kRows);
     nblk = blocks_of(s.L, kKeys);
   }
-  FA_DEV void begin(const PagedAttnParams& p, const long long* pre, long long t0, long long t1) {
+  FA_DEV void begin(const PagedAttnParams& p, const long long* pre, long long t0, long long end) {
     int lo = 0, hi = p.s.B - 1;      // last b with pre[b] <= t0
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (pre[mid] <= t0) lo = mid; else hi = mid - 1;
     }
     b = lo;
+    t1 = end;
     load(p);
     const long long r = t0 - pre[b];
-    const long long unit = paged::div64(r, nblk);
-    kb = (int)(r - unit * nblk);
+    const long long unit = paged::div64(r, nblk + kUnitCost);
+    kb = (int)(r - unit * (nblk + kUnitCost));
+    start = t0 - kb;
     head = (int)paged::div64(unit, tiles);
     tile = (int)(unit - (long long)head * tiles);
-    left = t1 - t0;
-    count = (int)(left < nblk - kb ? left : nblk - kb);
+    cut();
+    if (kb >= nblk) next(p);
   }
-  FA_DEV bool more() const { return left > 0; }
+  FA_DEV void cut() { count = (int)min((long long)(nblk - kb), t1 - start - kb); }
+  FA_DEV bool more() const { return start + kb < t1; }
   FA_DEV void next(const PagedAttnParams& p) {
-    left -= count;
-    if (left <= 0) return;
+    start += nblk + kUnitCost;
     kb = 0;
+    if (start >= t1) return;
     if (++tile == tiles) {
       tile = 0;
       if (++head == p.s.Hkv) {
@@ -178,7 +190,7 @@ struct Walk {
         load(p);
       }
     }
-    count = (int)(left < nblk ? left : nblk);
+    cut();
   }
   // Token and head of the tile's first row.
   FA_DEV void first_row(const PagedAttnParams& p, int& t, int& j) const {
@@ -317,14 +329,10 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
     if (lane == 0) {
       const int c = blockIdx.x;
       paged::Join j{0, 0, at.b, at.head, at.tile * kRows, at.s.n, at.s.q0, 0};
-      const long long start = t0 - at.kb, end = start + at.nblk;
-      if (at.kb > 0) {
-        const long long prev = stretch(total, c - 1, G);
-        if (prev <= start) {       // the unit's first cut
-          j.first = 2 * (c - 1) + (prev == start ? 0 : 1);
-          j.parts = 2;
-          while (c + j.parts - 1 < G && stretch(total, c + j.parts - 1, G) < end) ++j.parts;
-        }
+      if (at.kb > 0 && stretch(total, c - 1, G) <= at.start) {       // the unit's first cut
+        j.first = 2 * (c - 1) + 1;
+        j.parts = 2;
+        while (c + j.parts - 1 < G && stretch(total, c + j.parts - 1, G) < at.start + at.nblk) ++j.parts;
       }
       *W::join(p.part, c) = j;
     }
@@ -674,8 +682,7 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
     // written out.  The next round's writes wait for the last reader, mostly
     // long gone by then.
     const bool whole = at.kb == 0 && at.count == at.nblk;
-    const bool first = at.left == t1 - t0;
-    const int slot = 2 * blockIdx.x + (first ? 0 : 1);
+    const int slot = 2 * blockIdx.x + (at.kb > 0 ? 0 : 1);      // a stretch begins and ends in a cut unit at most once each
     // acc's unit; an empty share has none
     const float unit = kFp8 && v_top > 0 ? __uint_as_float((uint32_t)max(v_top - kWeightUp, 0) << 23) : 1.0f;
 #pragma unroll
