@@ -26,8 +26,9 @@
 //     and each refills by TMA the slots of the ring in shared memory that it
 //     empties (the pages' rows, swizzled for ldmatrix), every lane with a load of
 //     its own: a single thread issues one in some 150 cycles, too slow to feed an
-//     SM alone (313 us for 64 x 4096 BF16 keys).  No warp waits for another until
-//     the unit's end, where their softmax states are merged.
+//     SM alone (313 us for 64 x 4096 BF16 keys).  At a unit's end they leave
+//     their softmax states in shared memory and go on; the warp that looks pages
+//     up merges them in between.
 //   * E4M3 pages are widened in registers on the way to the tensor cores, to
 //     FP16, which holds every code and which one instruction makes of a pair (to
 //     BF16 it takes five).  The queries become FP16 by a power of two of each
@@ -96,7 +97,7 @@ struct Layout {
   static constexpr int kStats = kMerge + kMergeFloats * 4;        // m, l, lr of [row in round][warp]
   static constexpr int kPre = (kStats + 3 * kWarps * kRound * 4 + 7) / 8 * 8;   // prefix of blocks, [B + 1]
   static constexpr int kBars = kPre + (kMaxPackedSeqs + 1) * 8 + 8;
-  static constexpr int kPlaces = (kBars + kSlots * 8 + 2 * kBatches * 8 + 8 + 15) / 16 * 16;    // where blocks lie
+  static constexpr int kPlaces = (kBars + kSlots * 8 + 2 * kBatches * 8 + 16 + 15) / 16 * 16;   // where blocks lie
   static constexpr int kMisc = kPlaces + kBatches * 32 * 16;
   static constexpr int kBytes = kMisc + 64 + kSmemAlignSlack;
   static_assert(kBytes <= 232448, "dynamic shared memory above the 227 KB per-CTA limit");
@@ -112,10 +113,10 @@ FA_DEV int tiles_of(int n, int group, int rows) { return (n * group + rows - 1) 
 // Blocks of a unit: at least one, so that rows without a key are written too.
 FA_DEV int blocks_of(int L, int keys) { return max(1, (L + keys - 1) / keys); }
 // What a unit takes on the line besides its blocks: starting and merging it.  (64
-// ragged sequences up to 8192 E4M3 keys, 8 heads: counted as nothing, 115 us, since
-// a stretch of short sequences has up to 16 units, the average 4; as 6 blocks
-// 106, 18 98, 32 101.)
-constexpr int kUnitCost = 18;
+// ragged sequences up to 8192 E4M3 keys, 8 heads: counted as nothing, 111 us, since
+// a stretch of short sequences has up to 16 units, the average 4; as 14 blocks 99,
+// 20 100.)
+constexpr int kUnitCost = 14;
 
 // Prefix sums of the sequences' blocks into pre[0 .. B]; returns their total,
 // 0 when the sequences break the rules.  All threads of the block.
@@ -271,6 +272,81 @@ FA_DEV uint32_t piece(uint32_t base, int r, int c) {
 
 // ---------------------------------------------------------------- kernel --
 
+// Whether a phase is complete, without waiting; one answer for the whole warp.
+FA_DEV bool test_warp(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return __all_sync(0xffffffffu, done != 0);
+}
+
+// Joins the states that the computing warps left of rows [r0, r0 + kRound) of a
+// segment: final when it is the whole unit, else into the workspace.  One warp.
+template <int D, bool kFp8, int kTiles>
+FA_DEV void merge_rows(const PagedAttnParams& p, const Walk<Layout<D, kFp8, kTiles>::kKeys, 8 * kTiles>& at, int r0,
+                       const float* buf, float* stats) {
+  using L = Layout<D, kFp8, kTiles>;
+  using W = Part<D, L::kRows>;
+  constexpr int kWarps = L::kWarps;
+  const int lane = threadIdx.x % 32;
+  const int rows = min(L::kRound, at.rows(p) - r0), row0 = at.tile * L::kRows + r0;
+  const bool whole = at.kb == 0 && at.count == at.nblk;
+  // a stretch begins in a cut unit at most once, and ends in one at most once
+  const int slot = 2 * blockIdx.x + (at.kb > 0 ? 0 : 1);
+  float* st_m = stats;
+  const float* st_l = st_m + kWarps * L::kRound;
+  float* st_lr = stats + 2 * kWarps * L::kRound;
+  if (lane < rows) {
+    float f[kWarps], mt = -INFINITY, lt = 0.0f, lrt = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      f[w] = st_m[lane * kWarps + w];
+      mt = fmaxf(mt, f[w]);
+    }
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      f[w] = mt == -INFINITY ? 1.0f : ex2_mufu(f[w] - mt);
+      lt += st_l[lane * kWarps + w] * f[w];
+      lrt += st_lr[lane * kWarps + w] * f[w];
+    }
+    const float inv = !whole ? 1.0f : lrt == 0.0f ? 0.0f : 1.0f / lrt;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) st_m[lane * kWarps + w] = f[w] * inv;       // from here on the warps' factors
+    if (whole) {
+      const int row = row0 + lane, t = row / p.group, head = at.head * p.group + row - t * p.group;
+      const size_t li = p.s.cu ? (size_t)head * p.s.Sn + at.s.q0 + t : ((size_t)at.b * p.Hq + head) * p.s.Sn + t;
+      p.lse[li] = lt == 0.0f ? -INFINITY : (mt + log2f(lt)) * 0.693147180559945309f;
+    } else {
+      *reinterpret_cast<float4*>(W::stat(p.part, slot) + (r0 + lane) * W::kStat) = make_float4(mt, lt, lrt, 0.0f);
+    }
+  }
+  __syncwarp();
+#pragma unroll 1
+  for (int i = lane; i < rows * (D / 4); i += 32) {
+    const int r = i / (D / 4), d = i % (D / 4) * 4;
+    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float4 x = *reinterpret_cast<const float4*>(buf + (w * L::kRound + r) * L::kPitch + d);
+      const float f = st_m[r * kWarps + w];
+      y.x += x.x * f;
+      y.y += x.y * f;
+      y.z += x.z * f;
+      y.w += x.w * f;
+    }
+    if (whole) {
+      const int row = row0 + r, t = row / p.group, head = at.head * p.group + row - t * p.group;
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + ((size_t)(at.s.q0 + t) * p.Hq + head) * D + d) =
+          make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+    } else {
+      *reinterpret_cast<float4*>(W::out(p.part, slot) + (r0 + r) * D + d) = y;
+    }
+  }
+}
+
 template <int D, bool kFp8, int kTiles>
 __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
     decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -291,15 +367,16 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
   float* stats = reinterpret_cast<float*>(smem + L::kStats);
   const uint32_t abort = sbase + L::kMisc;
   // barriers: a slot is loaded; a batch of places is looked up, is used up; the
-  // merge rows are free
+  // merge rows are written, are free
   const uint32_t full = sbase + L::kBars, placed = full + 8 * L::kSlots, taken = placed + 8 * L::kBatches;
-  const uint32_t merged = taken + 8 * L::kBatches;
+  const uint32_t written = taken + 8 * L::kBatches, merged = written + 8;
   int4* places = reinterpret_cast<int4*>(smem + L::kPlaces);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kSlots + L::kBatches; ++i) mbar_init(full + 8 * i, 1);
     for (int i = 0; i < L::kBatches; ++i) mbar_init(taken + 8 * i, 32);
-    mbar_init(merged, kWarps);
+    mbar_init(written, kWarps);
+    mbar_init(merged, 1);
     st_shared(abort, 0);
     fence_barrier_init();
     tma_prefetch_desc(&tm_k);
@@ -336,43 +413,92 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
       }
       *W::join(p.part, c) = j;
     }
-    // ---- looks up where blocks lie: (page, head) and row of the block's boxes
+    // ---- looks up where blocks lie, (page, head) and row of the block's boxes,
+    // and merges the states that the other warps leave at a unit's end, whichever
+    // can be done
+    Walk<kKeys, kRows> mine = at;
+    int r0 = 0;                        // of the rows to merge next
+    uint32_t round = 0, batch = 0;
     int i = 0, vis = at.visible(p), past = 0;
-    uint32_t batch = 0;
-    while (past < 2) {       // until a whole batch lies behind the end
-      int4 place = make_int4(kEnd, kEnd, 0, 0);
-      if (!at.more()) ++past;
-      for (int filled = 0; filled < 32 && at.more();) {
-        const int take = min(32 - filled, vis - i);
-        if (lane >= filled && lane < filled + take) {
-          int ph[2] = {-1, -1}, off[2] = {0, 0};      // -1: outside the tensor maps, reads as zeros
-          for (int j = 0; j <= two; ++j) {
-            const int key = (at.kb + i + lane - filled) * kKeys + (j << box_shift);
-            if (key >= at.s.L) break;
-            const int page = p.s.block_table[(size_t)at.b * p.s.max_pages + (key >> p.s.page_shift)];
-            if (page < 0 || page >= p.s.num_pages)
-              paged::record_bad_input(&g_err, kSitePage);
-            else
-              ph[j] = page * p.s.Hkv + at.head;
-            off[j] = key & ((1 << p.s.page_shift) - 1);
+    bool have = false;                 // a batch that waits for its place
+    int4 place;
+    uint64_t idle = 0;                 // since when nothing could be done
+    for (uint32_t it = 1;; ++it) {
+      bool did = false;
+      if (past < 2 || have) {          // until a whole batch lies behind the end
+        if (!have) {
+          place = make_int4(kEnd, kEnd, 0, 0);
+          if (!at.more()) ++past;
+          for (int filled = 0; filled < 32 && at.more();) {
+            const int take = min(32 - filled, vis - i);
+            if (lane >= filled && lane < filled + take) {
+              int ph[2] = {-1, -1}, off[2] = {0, 0};      // -1: outside the tensor maps, reads as zeros
+              for (int j = 0; j <= two; ++j) {
+                const int key = (at.kb + i + lane - filled) * kKeys + (j << box_shift);
+                if (key >= at.s.L) break;
+                const int page = p.s.block_table[(size_t)at.b * p.s.max_pages + (key >> p.s.page_shift)];
+                if (page < 0 || page >= p.s.num_pages)
+                  paged::record_bad_input(&g_err, kSitePage);
+                else
+                  ph[j] = page * p.s.Hkv + at.head;
+                off[j] = key & ((1 << p.s.page_shift) - 1);
+              }
+              place = make_int4(ph[0], ph[1], off[0], off[1]);
+            }
+            filled += take;
+            i += take;
+            if (i == vis) {
+              at.next(p);
+              i = 0;
+              vis = at.more() ? at.visible(p) : 0;
+            }
           }
-          place = make_int4(ph[0], ph[1], off[0], off[1]);
+          have = true;
         }
-        filled += take;
-        i += take;
-        if (i == vis) {
-          at.next(p);
-          i = 0;
-          vis = at.more() ? at.visible(p) : 0;
+        const int b = batch % L::kBatches;
+        if (test_warp(taken + 8 * b, (batch / L::kBatches & 1) ^ 1)) {
+          places[b * 32 + lane] = place;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(placed + 8 * b);
+          ++batch;
+          have = false;
+          did = true;
         }
       }
-      const int b = batch % L::kBatches;
-      if (!paged::wait_warp(taken + 8 * b, (batch / L::kBatches & 1) ^ 1, abort, &g_err, kSiteTaken, p.wait_limit_ns))
+      if (mine.more()) {
+        if (test_warp(written, round & 1)) {
+          merge_rows<D, kFp8, kTiles>(p, mine, r0, merge, stats);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(merged);
+          ++round;
+          r0 += L::kRound;
+          if (r0 >= mine.rows(p)) {
+            r0 = 0;
+            mine.next(p);
+          }
+          did = true;
+        }
+      } else if (past == 2 && !have) {
         break;
-      places[b * 32 + lane] = place;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(placed + 8 * b);
-      ++batch;
+      }
+      if (did) {
+        idle = 0;
+        continue;
+      }
+      __nanosleep(40);
+      if ((it & 15u) == 0u) {
+        const uint64_t now = globaltimer_ns();
+        if (idle == 0) idle = now;
+        const bool late = now - idle > p.wait_limit_ns;
+        if (__any_sync(0xffffffffu, late)) {
+          if (lane == 0) {
+            if (atomicCAS(&g_err.status, 0, FA_ERR_TIMEOUT) == 0) atomicExch(&g_err.site, kSiteTaken);
+            st_shared(abort, 1);
+          }
+          break;
+        }
+        if (__any_sync(0xffffffffu, ld_shared_volatile(abort) != 0)) break;
+      }
     }
     return;
   }
@@ -446,7 +572,7 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
   uint32_t round = 0;     // of merging
   bool lost = false;      // a wait ran out: no more results
   while (at.more()) {
-    const int rows = at.rows(p), row0 = at.tile * kRows;
+    const int rows = at.rows(p);
     int tok0, j0;
     at.first_row(p, tok0, j0);
     const int vis = at.visible(p);
@@ -676,13 +802,15 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
     Walk<kKeys, kRows> after = at;
     after.next(p);
     if (after.more()) load_q(after);
+    // Long units end together: warps that drift apart refill the ring out of turn.
+    // (64 ragged E4M3 sequences up to 8192 keys: 97.6 us, without 101; 256 of 300
+    // keys 61.7, without 58.)  A warp that has given up still walks along to here.
+    if (vis >= 4 * kWarps) named_barrier(1, kWarps * 32);
 
-    // Merge of the warps' states, kRound rows at a time: every warp writes its
-    // rows and their statistics, and after a barrier the rows are summed up and
-    // written out.  The next round's writes wait for the last reader, mostly
-    // long gone by then.
-    const bool whole = at.kb == 0 && at.count == at.nblk;
-    const int slot = 2 * blockIdx.x + (at.kb > 0 ? 0 : 1);      // a stretch begins and ends in a cut unit at most once each
+    // Every warp leaves its rows and their statistics, kRound rows at a time, for
+    // the merging warp, and goes on with the next unit.  (With the merging done by
+    // all of them behind a barrier they waited for one another at every unit's end:
+    // 256 sequences of 300 keys, 8 heads, E4M3 67 us.)
     // acc's unit; an empty share has none
     const float unit = kFp8 && v_top > 0 ? __uint_as_float((uint32_t)max(v_top - kWeightUp, 0) << 23) : 1.0f;
 #pragma unroll
@@ -692,9 +820,11 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
 #pragma unroll
         for (int d = 4; d < 32; d *= 2) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], d);
 #pragma unroll 1
-    for (int r0 = 0; r0 < rows; r0 += L::kRound, ++round) {
-      if (!paged::wait_warp(merged, round & 1 ^ 1, abort, &g_err, kSiteMerged, p.wait_limit_ns)) lost = true;
-      float* buf = merge;
+    for (int r0 = 0; r0 < rows && !lost; r0 += L::kRound, ++round) {
+      if (!paged::wait_warp(merged, round & 1 ^ 1, abort, &g_err, kSiteMerged, p.wait_limit_ns)) {
+        lost = true;
+        break;
+      }
       float* st_m = stats;
       float* st_l = st_m + kWarps * L::kRound;
       float* st_lr = st_l + kWarps * L::kRound;
@@ -711,56 +841,14 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
             // is not worth keeping
             st_lr[row * kWarps + warp] = kFp8 ? l[n][e] : ones[n][e];
           }
-          float* to = buf + (warp * L::kRound + row) * L::kPitch;
+          float* to = merge + (warp * L::kRound + row) * L::kPitch;
 #pragma unroll
           for (int d = 0; d < kSteps; ++d)
 #pragma unroll
             for (int h = 0; h < 2; ++h) to[16 * d + (kFp8 ? 2 * g + h : 8 * h + g)] = acc[n][d][2 * h + e] * unit;
         }
-      named_barrier(1, kWarps * 32);
-      if (ld_shared_volatile(abort)) lost = true;
-      // final when the segment is the whole unit, else partial
-      for (int i = threadIdx.x; i < min(L::kRound, rows - r0) * (D / 2) && !lost; i += kWarps * 32) {
-        const int r = i / (D / 2), d = i % (D / 2) * 2;
-        float fw[kWarps], mt = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          fw[w] = st_m[r * kWarps + w];
-          mt = fmaxf(mt, fw[w]);
-        }
-        float lt = 0.0f, lrt = 0.0f;
-        float2 y = make_float2(0.0f, 0.0f);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float f = mt == -INFINITY ? 1.0f : ex2_mufu(fw[w] - mt);
-          lt += st_l[r * kWarps + w] * f;
-          lrt += st_lr[r * kWarps + w] * f;
-          const float2 x = *reinterpret_cast<const float2*>(buf + (w * L::kRound + r) * L::kPitch + d);
-          y.x += x.x * f;
-          y.y += x.y * f;
-        }
-        if (whole) {
-          const float inv = lrt == 0.0f ? 0.0f : 1.0f / lrt;
-          const int row = row0 + r0 + r, t = row / p.group, head = at.head * p.group + row - t * p.group;
-          const int tok = at.s.q0 + t;
-          *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + ((size_t)tok * p.Hq + head) * D + d) =
-              pack_bf16x2(y.x * inv, y.y * inv);
-          if (d == 0) {
-            const size_t li = p.s.cu ? (size_t)head * p.s.Sn + tok : ((size_t)at.b * p.Hq + head) * p.s.Sn + t;
-            p.lse[li] = lt == 0.0f ? -INFINITY : (mt + log2f(lt)) * 0.693147180559945309f;
-          }
-        } else {
-          *reinterpret_cast<float2*>(W::out(p.part, slot) + (r0 + r) * D + d) = y;
-          if (d == 0) {
-            float* stat = W::stat(p.part, slot) + (r0 + r) * W::kStat;
-            stat[0] = mt;
-            stat[1] = lt;
-            stat[2] = lrt;
-          }
-        }
-      }
       __syncwarp();
-      if (lane == 0) mbar_arrive(merged);
+      if (lane == 0) mbar_arrive(written);
     }
     at = after;
   }
