@@ -1017,9 +1017,15 @@ __device__ void correction_role(const Shared<D, kFp8>& sh, const uint32_t tmem, 
 #pragma unroll
           for (int e = 0; e < 16; ++e)
             pk[e] = pack_bf16x2(__uint_as_float(r[2 * e]) * inv, __uint_as_float(r[2 * e + 1]) * inv);
+          // 32 bytes a store where O is aligned so
+          if ((reinterpret_cast<uintptr_t>(p.o) & 31) == 0) {
+            st_global_v8(dst + c * 32, pk);
+            st_global_v8(dst + c * 32 + 16, pk + 8);
+          } else {
 #pragma unroll
-          for (int v = 0; v < 4; ++v)
-            reinterpret_cast<uint4*>(dst)[c * 4 + v] = make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
+            for (int v = 0; v < 4; ++v)
+              reinterpret_cast<uint4*>(dst)[c * 4 + v] = make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
+          }
         }
       }
       if (valid) {
