@@ -67,13 +67,15 @@ enum Site {
   kSiteP, kSiteO, kSiteLanded, kSiteRaw, kSiteQReady
 };
 
-// Workspace: per slot (two per thread block) both tiles' unnormalised rows,
-// then per slot and row maximum and sums.
+// Workspace: per slot (two per thread block) both tiles' unnormalised rows, then
+// per slot and row maximum and sums.  The rows lie in pieces of 8 columns,
+// [D / 8][row][8], so that a warp, which holds a row a lane, stores whole lines.
 template <int D>
 struct Part {
   static constexpr int kRows = 2 * kBM;
   static constexpr int kStat = 4;
   FA_DEV static float* out(float* ws, int slot) { return ws + (size_t)slot * kRows * D; }
+  FA_DEV static int piece(int i, int row) { return (i * kRows + row) * 8; }
   FA_DEV static float* stat(float* ws, int slot) {
     return ws + (size_t)2 * kMaxCtas * kRows * D + (size_t)slot * kRows * kStat;
   }
@@ -992,7 +994,7 @@ __device__ void correction_role(const Shared<D, kFp8>& sh, const uint32_t tmem, 
       const float inv = w.slot >= 0 ? unit : lr == 0.0f ? 0.0f : unit / lr;
       const int head = w.head * p.group + my_head;
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + ((size_t)(w.q0 + tok) * p.Hq + head) * D;
-      float* part = Part<D>::out(p.part, max(w.slot, 0)) + (t * kBM + r_in_tile) * D;
+      float* part = Part<D>::out(p.part, max(w.slot, 0));
       const uint32_t tm_o = tmem + lane_off + uint32_t(256 + t * D);
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
@@ -1011,7 +1013,7 @@ __device__ void correction_role(const Shared<D, kFp8>& sh, const uint32_t tmem, 
             for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * inv);
           }
 #pragma unroll
-          for (int v = 0; v < 4; ++v) st_global_v8(part + c * 32 + v * 8, r + v * 8);
+          for (int v = 0; v < 4; ++v) st_global_v8(part + Part<D>::piece(4 * c + v, t * kBM + r_in_tile), r + v * 8);
         } else if (valid) {
           uint32_t pk[16];
 #pragma unroll
@@ -1321,18 +1323,22 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const PagedAttnPa
     }
   }
   __syncthreads();
-  constexpr int kEach = kJoinRows * (D / 4) / kJoinThreads;      // pieces of 4 columns per thread
+  // 16 bytes a thread at a time, as they lie in the workspace; the rows are put
+  // together in shared memory
+  constexpr int kEach = kJoinRows * (D / 4) / kJoinThreads;
   float4 y[kEach];
 #pragma unroll
   for (int e = 0; e < kEach; ++e) y[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const int r = threadIdx.x / 2 % kJoinRows, half = threadIdx.x % 2;
+  const int piece0 = threadIdx.x / (2 * kJoinRows);
+  constexpr int kPieces = kJoinThreads / (2 * kJoinRows);        // at a time
 #pragma unroll 2
   for (int k = 0; k < j.parts; ++k) {
-    const float4* from = reinterpret_cast<const float4*>(Part<D>::out(p.part, paged::join_slot(j, c, k)) + row0 * D);
+    const float* from = Part<D>::out(p.part, paged::join_slot(j, c, k)) + half * 4;
+    const float f = fac[k][r];
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
-      const int i = threadIdx.x + e * kJoinThreads;
-      const float f = fac[k][i / (D / 4)];
-      const float4 x = from[i];
+      const float4 x = *reinterpret_cast<const float4*>(from + Part<D>::piece(piece0 + e * kPieces, row0 + r));
       // (rows that no part wrote hold anything, and are not stored)
       y[e].x += x.x * f;
       y[e].y += x.y * f;
@@ -1340,16 +1346,19 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const PagedAttnPa
       y[e].w += x.w * f;
     }
   }
+  __shared__ uint2 rows[kJoinRows][D / 4 + 1];
 #pragma unroll
-  for (int e = 0; e < kEach; ++e) {
-    const int i = threadIdx.x + e * kJoinThreads;
-    const int r = i / (D / 4), d = i % (D / 4) * 4;
-    const int in_tile = (row0 + r) % kBM, tk = in_tile / p.group;
+  for (int e = 0; e < kEach; ++e)
+    rows[r][2 * (piece0 + e * kPieces) + half] =
+        make_uint2(pack_bf16x2(y[e].x * inv[r], y[e].y * inv[r]), pack_bf16x2(y[e].z * inv[r], y[e].w * inv[r]));
+  __syncthreads();
+  for (int i = threadIdx.x; i < kJoinRows * (D / 4); i += kJoinThreads) {
+    const int row = i / (D / 4), d = i % (D / 4);
+    const int in_tile = (row0 + row) % kBM, tk = in_tile / p.group;
     const int tok = tok0 + tk;
     if (tk >= tt || tok >= j.n) continue;
     const int head = j.head * p.group + in_tile - tk * p.group;
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + ((size_t)(j.q0 + tok) * p.Hq + head) * D + d) =
-        make_uint2(pack_bf16x2(y[e].x * inv[r], y[e].y * inv[r]), pack_bf16x2(y[e].z * inv[r], y[e].w * inv[r]));
+    reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + ((size_t)(j.q0 + tok) * p.Hq + head) * D)[d] = rows[row][d];
   }
 }
 
