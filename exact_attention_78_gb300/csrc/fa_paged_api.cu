@@ -114,16 +114,21 @@ fa_status fa_rope(const void* q, const void* k, void* q_out, void* k_out, int to
     p.pairs = (int)pairs;
     p.interleaved = interleaved;
     p.inverse = inverse;
+    // Frequencies base^-x as 2^-y, y = x log2 base.  y is rounded by 2^-52 of
+    // itself, which moves 2^-y by less than 2^-53; against 60 digits the turns
+    // are off by 2^-55 at most.
+    const double log2_base = std::log2(base);
     int i = 0;
     for (int a = 0; a < axes; ++a)
       for (int j = 0; j < sections[a]; ++j, ++i) {
-        const double f = std::pow(base, restart ? -(double)j / sections[a] : -(double)i / (double)pairs);
+        const double f = std::exp2(-log2_base * (restart ? (double)j / sections[a] : (double)i / (double)pairs));
         // turns per position, its whole turns dropped, as a fraction of 2^64.
         // The division by two pi in double is good to 2^-53 of the frequency;
         // a long double would not be the same on both host architectures.
+        constexpr double kTwo32 = 4294967296.0;
         double t = f / 6.283185307179586476925;
         t -= std::floor(t);
-        const double hi = std::floor(std::ldexp(t, 32)), lo = std::ldexp(t, 64) - std::ldexp(hi, 32);
+        const double hi = std::floor(t * kTwo32), lo = (t * kTwo32 - hi) * kTwo32;
         p.turn[i] = ((unsigned long long)hi << 32) + (unsigned long long)lo;
         p.axis[i] = (unsigned char)a;
       }
