@@ -39,7 +39,8 @@
  *     larger saturate), stored as the byte e + 127; each code is the row's
  *     value * 2^-e rounded to nearest even.  What a code stands for is exact
  *     in BF16.  A row that holds a NaN or an infinity gets the byte 255 and
- *     zero codes and stands for NaN.
+ *     zero codes and stands for NaN.  The two NaN codes, 0x7F and 0xFF, and
+ *     bytes outside 17 ... 246 and 255 are made by no write and mean nothing.
  *   - Offsets, lengths and page numbers live on the device, so their rules are
  *     checked there.  Offsets or lengths that break them make fa_fwd_paged()
  *     compute nothing, and fa_cache_write() and fa_cache_read() skip the rows
@@ -100,10 +101,10 @@ FA_API fa_status fa_cache_read(const void* k_pages, const void* v_pages, const v
                                int max_pages, const int* block_table, const int* cu_seqlens, fa_stream_t stream);
 
 /*
- * Bytes of device workspace fa_fwd_paged() needs: the
- * partial results of queries whose keys are split over thread blocks.  It
- * depends on these arguments alone, not on the sequences' lengths.  Returns 0
- * for arguments fa_fwd_paged() would reject.
+ * Bytes of device workspace fa_fwd_paged() needs: the partial results of
+ * queries whose keys are split over thread blocks.  It depends on these
+ * arguments alone, not on the sequences' lengths.  Returns 0 for arguments
+ * fa_fwd_paged() would reject.
  */
 FA_API size_t fa_fwd_paged_workspace_size(int B, int Hq, int Hkv, int Sn, int D, int packed, int max_q);
 
@@ -122,10 +123,23 @@ FA_API size_t fa_fwd_paged_workspace_size(int B, int Hq, int Hkv, int Sn, int D,
  *                fa_fwd_paged_workspace_size(...) bytes; contents on entry are
  *                ignored and clobbered.  Calls whose work overlaps on the GPU
  *                need one each.
+ *   scale        > 0; scale * log2(e) a normal FP32 number
+ * o and lse overlap none of the inputs.  Hq is a multiple of Hkv, Hq / Hkv at
+ * most 128, Hkv at most 4096.
  * A row that sees no key gets O = 0 and LSE = -inf.  Slots behind a sequence's
- * last token may hold anything (NaN and infinities too); a NaN or an infinity
- * among a sequence's own values may reach any row of its new tokens.
- * Hq / Hkv is at most 128.
+ * last token may hold anything (NaN and infinities too).  A NaN or an infinity
+ * in a key reaches the rows that see it; one in a value may reach any row of
+ * the same sequence and key/value head.
+ * Roundings, besides O's to BF16 (scores, sums and O are FP32):
+ *   - BF16 pages: weights to BF16 (2^-8 of each at most); O is divided by the
+ *     sum of the weights as rounded.
+ *   - E4M3 pages: the products take FP16.  Queries are exact but for elements
+ *     below 2^-30 of their row's largest (off by 2^-38 of it at most).  Codes
+ *     are exact where a row's scale is at least 2^-15 of the largest among the
+ *     sequence's keys (values); codes of a row further below may be off by
+ *     2^-25 of that largest scale.  A weight times its value's scale is off by
+ *     2^-11 of itself, or by 2^-31 of the largest weight times the largest
+ *     scale.
  * Results are bitwise repeatable.
  */
 FA_API fa_status fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages, const void* k_scale,
