@@ -410,7 +410,7 @@ __device__ void scheduler_role(const Shared<D, kFp8>& sh, const PagedAttnParams&
       // the unit is cut here: if for the first time, its parts are joined
       if (line.stretch(c - 1) < w.start + kBN) {
         const long long end = w.start + (long long)nblk * kBN;
-        join = paged::Join{2, 2 * (c - 1) + 1, w.b, w.head, pair * s.t2, s.n, s.q0, 0};
+        join = paged::Join{2, w.b, w.head, pair * s.t2, s.n, s.q0, {0, 0}};
         while (c + join.parts - 1 < line.G && line.stretch(c + join.parts - 1) < end) ++join.parts;
       }
     }
@@ -1291,28 +1291,50 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const PagedAttnPa
   __shared__ float inv[kJoinRows];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x + 1;
-  const paged::Join j = *Part<D>::join(p.part, c);
-  const int tt = tile_tokens(p.group);
   const int row0 = blockIdx.y * kJoinRows;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  // 16 bytes a thread at a time, as they lie in the workspace; the rows are put
+  // together in shared memory
+  constexpr int kEach = kJoinRows * (D / 4) / kJoinThreads;
+  const int r = threadIdx.x / 2 % kJoinRows, half = threadIdx.x % 2;
+  const int piece0 = threadIdx.x / (2 * kJoinRows);
+  constexpr int kPieces = kJoinThreads / (2 * kJoinRows);        // at a time
+  auto stat_of = [&](int k) {
+    return *reinterpret_cast<const float4*>(Part<D>::stat(p.part, paged::join_slot(c, k)) + (row0 + lane) * Part<D>::kStat);
+  };
+  auto part_of = [&](int k, int e) {
+    return *reinterpret_cast<const float4*>(Part<D>::out(p.part, paged::join_slot(c, k)) +
+                                            Part<D>::piece(piece0 + e * kPieces, row0 + r) + half * 4);
+  };
+  // Which slots the parts are in is known before how many there are; the first two
+  // are loaded along with that (they hold anything where nothing is joined).
+  constexpr int kAhead = 2;
+  const paged::Join j = *Part<D>::join(p.part, c);
+  float4 st0[kAhead], x0[kAhead][kEach];
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) {
+    st0[k] = stat_of(k);
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) x0[k][e] = part_of(k, e);
+  }
+  const int tt = tile_tokens(p.group);
   const int tok0 = j.row0 + row0 / kBM * tt;                // of the rows' tile
   if (j.parts == 0 || tok0 >= j.n) return;
   // The parts' factors, one row a lane: 2^(maximum - the row's largest).
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   if (warp == 0) {
-    auto stat_of = [&](int k) {
-      return *reinterpret_cast<const float4*>(Part<D>::stat(p.part, paged::join_slot(j, c, k)) + (row0 + lane) * Part<D>::kStat);
-    };
-    float mt = -INFINITY, lt = 0.0f, lrt = 0.0f;
+    float mt = fmaxf(st0[0].x, st0[1].x), lt = 0.0f, lrt = 0.0f;
 #pragma unroll 4
-    for (int k = 0; k < j.parts; ++k) mt = fmaxf(mt, stat_of(k).x);
-#pragma unroll 4
-    for (int k = 0; k < j.parts; ++k) {
-      const float4 st = stat_of(k);
+    for (int k = kAhead; k < j.parts; ++k) mt = fmaxf(mt, stat_of(k).x);
+    auto take = [&](int k, const float4& st) {
       const float f = mt == -INFINITY ? 1.0f : ex2_mufu(st.x - mt);
       fac[k][lane] = f;
       lt += st.y * f;
       lrt += st.z * f;
-    }
+    };
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) take(k, st0[k]);
+#pragma unroll 4
+    for (int k = kAhead; k < j.parts; ++k) take(k, stat_of(k));
     inv[lane] = lrt == 0.0f ? 0.0f : 1.0f / lrt;
     const int in_tile = (row0 + lane) % kBM, tk = in_tile / p.group;
     const int tok = tok0 + tk;
@@ -1323,28 +1345,25 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const PagedAttnPa
     }
   }
   __syncthreads();
-  // 16 bytes a thread at a time, as they lie in the workspace; the rows are put
-  // together in shared memory
-  constexpr int kEach = kJoinRows * (D / 4) / kJoinThreads;
+  // (rows that no part wrote hold anything, and are not stored)
   float4 y[kEach];
 #pragma unroll
   for (int e = 0; e < kEach; ++e) y[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  const int r = threadIdx.x / 2 % kJoinRows, half = threadIdx.x % 2;
-  const int piece0 = threadIdx.x / (2 * kJoinRows);
-  constexpr int kPieces = kJoinThreads / (2 * kJoinRows);        // at a time
+  auto add = [&](int e, const float4& x, float f) {
+    y[e].x += x.x * f;
+    y[e].y += x.y * f;
+    y[e].z += x.z * f;
+    y[e].w += x.w * f;
+  };
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) add(e, x0[k][e], fac[k][r]);
 #pragma unroll 2
-  for (int k = 0; k < j.parts; ++k) {
-    const float* from = Part<D>::out(p.part, paged::join_slot(j, c, k)) + half * 4;
+  for (int k = kAhead; k < j.parts; ++k) {
     const float f = fac[k][r];
 #pragma unroll
-    for (int e = 0; e < kEach; ++e) {
-      const float4 x = *reinterpret_cast<const float4*>(from + Part<D>::piece(piece0 + e * kPieces, row0 + r));
-      // (rows that no part wrote hold anything, and are not stored)
-      y[e].x += x.x * f;
-      y[e].y += x.y * f;
-      y[e].z += x.z * f;
-      y[e].w += x.w * f;
-    }
+    for (int e = 0; e < kEach; ++e) add(e, part_of(k, e), f);
   }
   __shared__ uint2 rows[kJoinRows][D / 4 + 1];
 #pragma unroll

@@ -405,9 +405,8 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
     // ---- says what there is to join at the border before this stretch
     if (lane == 0) {
       const int c = blockIdx.x;
-      paged::Join j{0, 0, at.b, at.head, at.tile * kRows, at.s.n, at.s.q0, 0};
+      paged::Join j{0, at.b, at.head, at.tile * kRows, at.s.n, at.s.q0, {0, 0}};
       if (at.kb > 0 && stretch(total, c - 1, G) <= at.start) {       // the unit's first cut
-        j.first = 2 * (c - 1) + 1;
         j.parts = 2;
         while (c + j.parts - 1 < G && stretch(total, c + j.parts - 1, G) < at.start + at.nblk) ++j.parts;
       }
@@ -874,48 +873,64 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const PagedAttnPa
   __shared__ float inv[kJoinRows];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x + 1;
-  const paged::Join j = *W::join(p.part, c);
   const int row0 = blockIdx.y * kJoinRows;
+  const int r = threadIdx.x / (D / 4), d = threadIdx.x % (D / 4) * 4;
+  // Which slots the parts are in is known before how many there are; the first two
+  // are loaded along with that (they hold anything where nothing is joined).
+  constexpr int kAhead = 2;
+  auto stat_of = [&](int k, int row) {
+    return *reinterpret_cast<const float4*>(W::stat(p.part, paged::join_slot(c, k)) + (row0 + row) * W::kStat);
+  };
+  auto part_of = [&](int k) {
+    return *reinterpret_cast<const float4*>(W::out(p.part, paged::join_slot(c, k)) + (row0 + r) * D + d);
+  };
+  const paged::Join j = *W::join(p.part, c);
+  float4 st0, x0[kAhead];
+  if (threadIdx.x < kAhead * kJoinRows) st0 = stat_of(threadIdx.x / kJoinRows, threadIdx.x % kJoinRows);
+  if (r < kJoinRows) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) x0[k] = part_of(k);
+  }
   const int rows = j.parts == 0 ? 0 : min(kJoinRows, min(kRows, j.n * p.group - j.row0) - row0);
   if (rows <= 0) return;
   for (int i = threadIdx.x; i < j.parts * kJoinRows; i += kJoinThreads) {
-    const int k = i / kJoinRows, r = i % kJoinRows;
-    if (r >= rows) continue;
-    const float4 st = *reinterpret_cast<const float4*>(W::stat(p.part, paged::join_slot(j, c, k)) + (row0 + r) * W::kStat);
-    st_m[k][r] = st.x;
-    st_l[k][r] = st.y;
-    st_lr[k][r] = st.z;
+    const int k = i / kJoinRows, row = i % kJoinRows;
+    if (row >= rows) continue;
+    const float4 st = k < kAhead ? st0 : stat_of(k, row);
+    st_m[k][row] = st.x;
+    st_l[k][row] = st.y;
+    st_lr[k][row] = st.z;
   }
   __syncthreads();
   const int unit_row = j.row0 + row0;
   if ((int)threadIdx.x < rows) {
-    const int r = threadIdx.x;
+    const int row = threadIdx.x;
     float mt = -INFINITY, lt = 0.0f, lrt = 0.0f;
-    for (int k = 0; k < j.parts; ++k) mt = fmaxf(mt, st_m[k][r]);
+    for (int k = 0; k < j.parts; ++k) mt = fmaxf(mt, st_m[k][row]);
     for (int k = 0; k < j.parts; ++k) {
-      const float f = mt == -INFINITY ? 1.0f : ex2_mufu(st_m[k][r] - mt);
-      st_m[k][r] = f;                            // from here on the part's factor
-      lt += st_l[k][r] * f;
-      lrt += st_lr[k][r] * f;
+      const float f = mt == -INFINITY ? 1.0f : ex2_mufu(st_m[k][row] - mt);
+      st_m[k][row] = f;                            // from here on the part's factor
+      lt += st_l[k][row] * f;
+      lrt += st_lr[k][row] * f;
     }
-    inv[r] = lrt == 0.0f ? 0.0f : 1.0f / lrt;
-    const int tk = (unit_row + r) / p.group, head = j.head * p.group + unit_row + r - tk * p.group;
+    inv[row] = lrt == 0.0f ? 0.0f : 1.0f / lrt;
+    const int tk = (unit_row + row) / p.group, head = j.head * p.group + unit_row + row - tk * p.group;
     const size_t li = p.s.cu ? (size_t)head * p.s.Sn + j.q0 + tk : ((size_t)j.b * p.Hq + head) * p.s.Sn + tk;
     p.lse[li] = lt == 0.0f ? -INFINITY : (mt + log2f(lt)) * 0.693147180559945309f;
   }
   __syncthreads();
-  const int r = threadIdx.x / (D / 4), d = threadIdx.x % (D / 4) * 4;
   if (r >= rows) return;
   float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-  for (int k = 0; k < j.parts; ++k) {
-    const float4 x = *reinterpret_cast<const float4*>(W::out(p.part, paged::join_slot(j, c, k)) + (row0 + r) * D + d);
-    const float f = st_m[k][r];
+  auto add = [&](const float4& x, float f) {
     y.x += x.x * f;
     y.y += x.y * f;
     y.z += x.z * f;
     y.w += x.w * f;
-  }
+  };
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) add(x0[k], st_m[k][r]);      // (a join has two parts or more)
+#pragma unroll 8
+  for (int k = kAhead; k < j.parts; ++k) add(part_of(k), st_m[k][r]);
   const int tk = (unit_row + r) / p.group, head = j.head * p.group + unit_row + r - tk * p.group;
   *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + ((size_t)(j.q0 + tk) * p.Hq + head) * D + d) =
       make_uint2(pack_bf16x2(y.x * inv[r], y.y * inv[r]), pack_bf16x2(y.z * inv[r], y.w * inv[r]));

@@ -155,14 +155,16 @@ FA_DEV long long div64(long long a, long long b) {
 // place, leaves it behind for them: working it out again took as long as the
 // joining.
 struct Join {
-  int parts;       // of the unit whose first cut this border is: slot `first`, then slots 2 c, 2 (c + 1), ...; 0: none
-  int first;
+  int parts;       // of the unit whose first cut this border is (two or more); 0: none
   int b, head;
   int row0;        // the unit's first row: decode kernel (token, head) rows, chunk kernel tokens
   int n, q0;       // the sequence's new tokens and their first row
-  int pad;
+  int pad[2];
 };
-FA_DEV int join_slot(const Join& j, int c, int k) { return k == 0 ? j.first : 2 * (c + k - 1); }
+// A thread block's slots: 2 c for the part that begins at the border before it,
+// 2 c + 1 for the one that ends at the border behind it (and began at its unit's
+// start).  The slot of part k:
+FA_DEV int join_slot(int c, int k) { return k == 0 ? 2 * c - 1 : 2 * (c + k - 1); }
 
 // 2^e of a scale byte; NaN for the byte of a row without a finite scale.
 FA_DEV float scale_value(uint32_t byte) {
