@@ -393,6 +393,8 @@ def rope(q, k, positions, sections=None, base=10000.0, restart=False, interleave
         sections = (D // 2,)
     if len(sections) != axes:
         raise ValueError("%d sections for %d axes" % (len(sections), axes))
+    if min(sections) < 1 or sum(sections) > D // 2:      # (the C interface's ints would wrap)
+        raise ValueError("sections %s of at most %d pairs" % (tuple(sections), D // 2))
     if q_out is not None:
         _check_out("q_out", q_out, shape, torch.bfloat16, device)
     if k_out is not None:
@@ -490,6 +492,8 @@ def fwd_paged(q, k_pages, v_pages, block_table, seq_lens, causal=True, scale=Non
         max_q, lse_shape = Sn, (B, Hq, Sn)
     else:
         max_q, lse_shape = Sn if max_q is None else max_q, (Hq, Sn)
+        if not 0 < max_q <= Sn:      # (the C interface's ints would wrap)
+            raise ValueError("max_q is %d for %d rows" % (max_q, Sn))
     if out is not None:
         _check_out("out", out, q.shape, torch.bfloat16, device)
     if lse is not None:

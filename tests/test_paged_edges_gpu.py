@@ -307,3 +307,15 @@ def test_rope_write_attend_on_another_stream_in_place(fa, interleaved, sections)
             c.value[name][end - n:end] = P.dequantise(*P.quantise(f64(x[first:first + n])))
         first += n
     check_attention(o, lse, q, c, new, True, 128 ** -0.5)
+
+
+def test_numbers_that_no_int_holds_are_refused(fa):
+    c = Cache([20], 1, 64, 16, False)
+    q = randn((4, 2, 64), 1).cuda()
+    for max_q in (0, -1, 5, 2 ** 32 + 1):
+        with pytest.raises(ValueError):
+            run(fa, c, q, [4], max_q=max_q)
+    pos = torch.arange(4, dtype=torch.int32, device="cuda")
+    for sections in ([0], [33], [2 ** 32 + 16]):
+        with pytest.raises(ValueError):
+            fa.rope(q, None, pos, sections=sections)
