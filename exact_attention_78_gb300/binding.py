@@ -506,13 +506,20 @@ def fwd_paged(q, k_pages, v_pages, block_table, seq_lens, causal=True, scale=Non
         if lse is None:
             lse = torch.empty(lse_shape, dtype=torch.float32, device=device)
         if workspace is None:
-            need = fwd_paged_workspace_size(B, Hq, Hkv, Sn, D, cu_seqlens is not None, max_q)
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
-        st = lib.fa_fwd_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _adr(k_scale), _adr(v_scale),
-                              out.data_ptr(), lse.data_ptr(), B, Hq, Hkv, Sn, D, num_pages, page_size, max_pages,
-                              bool(causal), D ** -0.5 if scale is None else scale, block_table.data_ptr(),
-                              seq_lens.data_ptr(), _adr(cu_seqlens), max_q, workspace.data_ptr(),
-                              workspace.numel() * workspace.element_size(), s)
+            # from torch's allocator and back to it in the stream's order, as a
+            # tensor would be, whose making takes 2 us more
+            size = max(fwd_paged_workspace_size(B, Hq, Hkv, Sn, D, cu_seqlens is not None, max_q), 256)
+            ws = torch._C._cuda_cudaCachingAllocator_raw_alloc(size, s)
+        else:
+            size, ws = workspace.numel() * workspace.element_size(), workspace.data_ptr()
+        try:
+            st = lib.fa_fwd_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _adr(k_scale), _adr(v_scale),
+                                  out.data_ptr(), lse.data_ptr(), B, Hq, Hkv, Sn, D, num_pages, page_size, max_pages,
+                                  bool(causal), D ** -0.5 if scale is None else scale, block_table.data_ptr(),
+                                  seq_lens.data_ptr(), _adr(cu_seqlens), max_q, ws, size, s)
+        finally:
+            if workspace is None:
+                torch._C._cuda_cudaCachingAllocator_raw_delete(ws)
     if st:
         raise FAError(st, "fa_fwd_paged")
     return out, lse
