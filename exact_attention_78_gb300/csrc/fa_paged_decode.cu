@@ -35,6 +35,9 @@
 //     row's own, which loses nothing of note: a row's largest value is below 2^14
 //     then, and what lies below 2^-38 of it is rounded.  The keys' scales go to
 //     the scores in FP32, the values' to the weights.
+//   * The launch overlaps the end of the kernel before it in the stream: barriers
+//     are set up before griddepcontrol.wait (a call over a few keys, behind another:
+//     13.3 -> 11.0 us on the GPU).
 //   * The running maximum is lazy: it moves, and the sums and O are rescaled,
 //     only when a row's scores pass it by more than 8 log2 units.
 #include <cuda_runtime.h>
@@ -382,6 +385,7 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");      // nothing global before this
   const long long total = build_line<kKeys, kRows>(p, pre, reinterpret_cast<long long*>(merge));
   __syncthreads();
   const int G = active_ctas(total, gridDim.x);
@@ -872,6 +876,7 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const PagedAttnPa
   __shared__ float st_m[kMaxCtas + 1][kJoinRows], st_l[kMaxCtas + 1][kJoinRows], st_lr[kMaxCtas + 1][kJoinRows];
   __shared__ float inv[kJoinRows];
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int c = blockIdx.x + 1;
   const int row0 = blockIdx.y * kJoinRows;
   const int r = threadIdx.x / (D / 4), d = threadIdx.x % (D / 4) * 4;
@@ -949,22 +954,10 @@ fa_status launch_inst(const PagedAttnLaunch& L, cudaStream_t stream) {
   auto kern = decode_kernel<D, kFp8, kTiles>;
   if ((st = prepare_kernel(reinterpret_cast<const void*>(kern), Lay::kBytes)) != FA_OK) return st;
   const int ctas = L.p.num_ctas;
-  kern<<<ctas, Lay::kThreads, Lay::kBytes, stream>>>(tk, tv, L.p);
-  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-  if (ctas > 1) {
-    // the joining kernel is on its way while the main one still runs
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(ctas - 1, Lay::kRows / kJoinRows);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, combine_kernel<D, Lay::kRows>, L.p) != cudaSuccess) return FA_ERR_CUDA;
-  }
-  return FA_OK;
+  if ((st = launch_overlapped(kern, dim3(ctas), Lay::kThreads, Lay::kBytes, stream, tk, tv, L.p)) != FA_OK) return st;
+  if (ctas == 1) return FA_OK;
+  return launch_overlapped(combine_kernel<D, Lay::kRows>, dim3(ctas - 1, Lay::kRows / kJoinRows), kJoinThreads, 0, stream,
+                           L.p);
 }
 
 // As few tiles of 8 rows as hold a sequence's rows.

@@ -97,6 +97,24 @@ constexpr int kDecodeRows(int D) { return D == 64 ? 32 : 16; }
 size_t paged_decode_workspace(int D);
 size_t paged_chunk_workspace(int D);
 
+// Launches a kernel that may start while the one before it in the stream still
+// runs; it executes griddepcontrol.wait before its first access to global memory.
+template <class... P, class... A>
+fa_status launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t stream,
+                            const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
 fa_status launch_rope(const RopeParams& p, int num_sms, cudaStream_t stream);
 fa_status launch_cache_write(const CacheParams& p, int num_sms, cudaStream_t stream);
 fa_status launch_cache_read(const CacheParams& p, int num_sms, cudaStream_t stream);

@@ -319,3 +319,57 @@ def test_numbers_that_no_int_holds_are_refused(fa):
     for sections in ([0], [33], [2 ** 32 + 16]):
         with pytest.raises(ValueError):
             fa.rope(q, None, pos, sections=sections)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("new", [[1, 1, 1], [90, 1, 200]])
+def test_calls_behind_one_another(fa, new, fp8):
+    """Copies, writes, attention calls and what reads their outputs, queued
+    without a pause (a call may start while the one before still runs) and as a
+    graph that begins with a copy: the bits of calls that wait for each other."""
+    c = Cache([700, 64, 1500], 2, 128, 16, fp8, seed=9)
+    T, cu = sum(new), cu_of(new)
+    src = [[randn((T, h, 128), 10 * i + h).cuda() for h in (8, 2, 2)] for i in range(6)]
+    q, k, v = (torch.empty_like(x) for x in src[0])
+
+    def attention(x):
+        return fa.fwd_paged(x, c.k_pages, c.v_pages, c.block_table, c.seq_lens, cu_seqlens=cu, max_q=max(new),
+                            **c.scales)
+
+    def step(pause):
+        fa.cache_write(k, v, c.k_pages, c.v_pages, c.block_table, c.seq_lens, cu_seqlens=cu, **c.scales)
+        pause()
+        o, lse = attention(q)
+        pause()
+        o2, lse2 = attention(o)                # the outputs as the next call's queries
+        pause()
+        return o, lse, o2, lse2
+
+    def series(pause):
+        out = []
+        for x in src:
+            for to, y in zip((q, k, v), x):
+                to.copy_(y)
+            pause()
+            out.append([t.clone() for t in step(pause)])
+        torch.cuda.synchronize()
+        return out
+
+    want = series(torch.cuda.synchronize)
+    for _ in range(5):
+        for got, w in zip(series(lambda: None), want):
+            assert all(torch.equal(a, b) for a, b in zip(got, w))
+    source = [torch.empty_like(x) for x in src[0]]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for to, y in zip((k, v, q), (source[1], source[2], source[0])):
+            to.copy_(y)
+        got = attention(q)                     # right behind a copy
+        got2 = step(lambda: None)
+    for x, w in zip(src, want):
+        for to, y in zip(source, x):
+            to.copy_(y)
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(got2, w))
+    assert fa.get_device_error() == 0
+    assert torch.isfinite(got[0].float()).all()
