@@ -118,6 +118,7 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const CacheParams p, in
   const int tok0 = blockIdx.x * tb;
   const int n = min(tb, p.rows - tok0) * 2 * Hkv;    // rows of this block
 
+  overlap_launches();
   // (n >= 2 Hkv > 0, and every thread makes the same number of steps)
   for (int r0 = 0; r0 < n; r0 += kUnroll * kGroups) {
     uint4 x[kUnroll][2];
@@ -187,6 +188,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const CacheParams p, int
   const float inv = 1.0f / (float)(2 * Hkv);
   const int tok0 = blockIdx.x * tb;
   const int n = min(tb, p.rows - tok0) * 2 * Hkv;
+  overlap_launches();
   find_slots<false>(p.s, p.rows, tb, slots);
   __syncthreads();
   for (int r0 = 0; r0 < n; r0 += kUnroll * kGroups) {
@@ -250,22 +252,16 @@ template <int D>
 fa_status launch_write_d(const CacheParams& p, int num_sms, cudaStream_t stream) {
   const int tb = tokens_per_block(p.rows, p.s.Hkv, num_sms);
   const int grid = (p.rows + tb - 1) / tb;
-  if (p.k_scale)
-    write_kernel<D, true><<<grid, kThreads, 0, stream>>>(p, tb);
-  else
-    write_kernel<D, false><<<grid, kThreads, 0, stream>>>(p, tb);
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  auto kernel = p.k_scale ? write_kernel<D, true> : write_kernel<D, false>;
+  return launch_overlapped(kernel, dim3(grid), kThreads, 0, stream, p, tb);
 }
 
 template <int D>
 fa_status launch_read_d(const CacheParams& p, int num_sms, cudaStream_t stream) {
   const int tb = tokens_per_block(p.rows, p.s.Hkv, num_sms);
   const int grid = (p.rows + tb - 1) / tb;
-  if (p.k_scale)
-    read_kernel<D, true><<<grid, kThreads, 0, stream>>>(p, tb);
-  else
-    read_kernel<D, false><<<grid, kThreads, 0, stream>>>(p, tb);
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  auto kernel = p.k_scale ? read_kernel<D, true> : read_kernel<D, false>;
+  return launch_overlapped(kernel, dim3(grid), kThreads, 0, stream, p, tb);
 }
 
 }  // namespace cache

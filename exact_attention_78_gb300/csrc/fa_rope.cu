@@ -77,6 +77,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
       if (kLayout == kHalf && turns) x[u].b = src[half];
     }
   };
+  overlap_launches();
   Piece x[kUnroll];
   load(0, x);
 
@@ -164,13 +165,8 @@ fa_status launch_d(RopeParams p, int num_sms, cudaStream_t stream) {
   p.tb = 1;
   while (p.tb < kMaxTb && (long long)p.tokens >= (long long)num_sms * 4 * p.tb) p.tb *= 2;
   const int grid = (p.tokens + p.tb - 1) / p.tb;
-  if (p.interleaved)
-    rope_kernel<D, kAdjacent><<<grid, kThreads, 0, stream>>>(p);
-  else if (p.pairs % 8 == 0)
-    rope_kernel<D, kHalf><<<grid, kThreads, 0, stream>>>(p);
-  else
-    rope_kernel<D, kAny><<<grid, kThreads, 0, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  auto kernel = p.interleaved ? rope_kernel<D, kAdjacent> : p.pairs % 8 == 0 ? rope_kernel<D, kHalf> : rope_kernel<D, kAny>;
+  return launch_overlapped(kernel, dim3(grid), kThreads, 0, stream, p);
 }
 
 }  // namespace rope

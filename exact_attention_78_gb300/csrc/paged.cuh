@@ -6,6 +6,15 @@
 #include "ptx.cuh"
 
 namespace fa {
+
+// In a kernel started by launch_overlapped(), ahead of its first access to global
+// memory: lets the next such launch start once all blocks are here, and waits for
+// the end of the kernel before.
+FA_DEV void overlap_launches() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 namespace paged {
 
 FA_DEV void record_bad_input(DeviceError* err, int site) {
