@@ -30,7 +30,7 @@ FA_DEV float hi_of(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 // turns both.  kAdjacent: pairs (2 i, 2 i + 1), inside one piece.  kAny: pairs
 // (i, i + R) at any R: a thread's piece meets its partners one by one, in the
 // row's copy in shared memory.  16,384 tokens x 32 heads, D = 128, R = 64: kHalf
-// 42.7 us (6.3 TB/s), kAny 82.3 us.
+// 40.9 us (6.6 TB/s), kAny 82 us.
 enum Layout { kHalf, kAdjacent, kAny };
 
 // 16-byte pieces that one thread loads and stores at a time.
