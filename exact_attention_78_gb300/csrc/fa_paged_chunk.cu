@@ -64,7 +64,7 @@ constexpr int kUnitCost = 4 * kBN;
 
 enum Site {
   kSiteSeqs = 1, kSitePage, kSiteSegFull, kSiteSegEmpty, kSiteQEmpty, kSiteKvEmpty, kSiteKvFull, kSiteQFull, kSiteS,
-  kSiteP, kSiteO, kSiteLanded, kSiteRaw, kSiteQReady
+  kSiteP, kSiteO, kSiteLanded, kSiteRaw, kSiteQReady, kSiteTops
 };
 
 // Workspace: per slot (two per thread block) both tiles' unnormalised rows, then
@@ -121,7 +121,7 @@ struct Layout {
   static constexpr int kSums = (kUPre + (kMaxPackedSeqs + 2) * 4 + 7) / 8 * 8;
   static constexpr int kSegRing = (kSums + 32 * 16 + 15) / 16 * 16;
   static constexpr int kBars = kSegRing + kSegs * (int)sizeof(Seg);
-  static constexpr int kNumBars = 2 + 2 * kStages + 10 + 2 * kSegs + (kFp8 ? 2 * kRaws + 1 : kStages);
+  static constexpr int kNumBars = 2 + 2 * kStages + 10 + 2 * kSegs + (kFp8 ? 2 * kRaws + 2 : kStages);
   static constexpr int kMisc = kBars + kNumBars * 8;
   static constexpr int kBytes = kMisc + 64 + kSmemAlignSlack;
   static_assert(kBytes <= 232448, "dynamic shared memory above the 227 KB per-CTA limit");
@@ -150,6 +150,7 @@ struct Shared {
   FA_DEV uint32_t raw_full(int s) const { return bar(12 + 2 * L::kStages + 2 * kSegs + s); }
   FA_DEV uint32_t raw_empty(int s) const { return bar(12 + 2 * L::kStages + 2 * kSegs + L::kRaws + s); }
   FA_DEV uint32_t q_ready() const { return bar(12 + 2 * L::kStages + 2 * kSegs + 2 * L::kRaws); }   // E4M3: Q is FP16
+  FA_DEV uint32_t tops_full() const { return bar(13 + 2 * L::kStages + 2 * kSegs + 2 * L::kRaws); }
   // E4M3, of segment number seg: largest scale bytes (all widening warps have
   // written theirs).
   FA_DEV int* tops(uint32_t seg) const { return reinterpret_cast<int*>(base + L::kTops) + (seg & 3) * 16; }
@@ -645,8 +646,12 @@ __device__ void widen_role(const Shared<D, true>& sh, const PagedAttnParams& p) 
   while (in.next(w)) {
     const int n = max(tile_blocks(w, 0, tt, p.causal), tile_blocks(w, 1, tt, p.causal));
     if (n == 0) continue;
+    // The eight warps wait for one another's largest scales on an mbarrier, which
+    // gives up with the rest of the block: a barrier of the hardware's would hold
+    // the ones that come to it after the others have given up and left.
     find_tops<D>(p, w, n, sh.tops(seg));
-    named_barrier(1, 256);
+    if (lane == 0) mbar_arrive(sh.tops_full());
+    if (!sh.wait(sh.tops_full(), seg & 1, kSiteTops, p)) return;
     const int top = values ? sh.value_top(seg) : sh.key_top(seg);
     ++seg;
 #pragma unroll 1
@@ -1220,7 +1225,10 @@ __global__ void __launch_bounds__(Layout<D, kFp8>::kThreads, 1)
       mbar_init(sh.seg_empty(s), L::kReaders);
     }
     for (int s = 0; s < (kFp8 ? 0 : L::kStages); ++s) mbar_init(sh.v_landed(s), 1);
-    if (kFp8) mbar_init(sh.q_ready(), 8);
+    if (kFp8) {
+      mbar_init(sh.q_ready(), 8);
+      mbar_init(sh.tops_full(), 8);
+    }
     for (int s = 0; s < L::kRaws; ++s) {
       mbar_init(sh.raw_full(s), 1);
       mbar_init(sh.raw_empty(s), 4);
