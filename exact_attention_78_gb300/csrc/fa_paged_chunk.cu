@@ -755,7 +755,7 @@ struct RowSums {
 };
 
 // Row r of tile t of Q, in place, to FP16 by a power of two of its own: 2^(13 - e),
-// below 2^14 then; returns e.
+// below 2^14 then; returns e.  At 2^126, the most, every BF16 number is exact in FP16.
 template <int D>
 FA_DEV int narrow_row(const Shared<D, true>& sh, int t, int r) {
   using L = Layout<D, true>;
@@ -773,7 +773,7 @@ FA_DEV int narrow_row(const Shared<D, true>& sh, int t, int r) {
     m[3] = paged::max_bf16x2(m[3], x[i].w & 0x7FFF7FFFu);
   }
   m[0] = paged::max_bf16x2(paged::max_bf16x2(m[0], m[1]), paged::max_bf16x2(m[2], m[3]));
-  const int e = max((int)(max(m[0] & 0xFFFFu, m[0] >> 16) >> 7), 27) - 127;       // of the largest value, -100 at least
+  const int e = max((int)(max(m[0] & 0xFFFFu, m[0] >> 16) >> 7), 14) - 127;       // of the largest value, -113 at least
   const float up = __uint_as_float((uint32_t)(127 + 13 - e) << 23);
 #pragma unroll
   for (int i = 0; i < D / 8; ++i) {
@@ -857,11 +857,17 @@ __device__ void softmax_role(const int t, const Shared<D, kFp8>& sh, const uint3
       if (!sh.wait(sh.s_full(t), sit & 1, kSiteS, p)) return;
       tc_fence_after();
       if (kFp8 && j == 0) {
-        // the scores' unit: of the row of Q, and of the segment's keys.  Normal
-        // at least: a masked score is -inf times this, which zero would make NaN
+        // the scores' unit, 2^-236 to 2^234: of the row of Q, and of the segment's
+        // keys.  Its halves are floats, and both move the scale the same way, so
+        // that only the product's own size counts.  That is normal and finite at
+        // least: a masked score is -inf times this, which zero would make NaN, and a
+        // score of zero stays one (below 2^-126 every score, 2^31 at most, is zero
+        // to the exponentials).
         const int top = sh.key_top(seg - 1);
-        const int unit = min(max(q_exp - 13 + (top > 0 ? top - 127 : 0), -100), 127);
-        sl2 = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)(unit + 127) << 23), 1.17549435e-38f);
+        const int unit = q_exp - 13 + (top > 0 ? top - 127 : 0), half = unit / 2;
+        sl2 = p.scale_log2 * __uint_as_float((uint32_t)(half + 127) << 23) *
+              __uint_as_float((uint32_t)(unit - half + 127) << 23);
+        sl2 = fminf(fmaxf(sl2, 1.17549435e-38f), 3.40282347e38f);
       }
       const int kv0 = (w.kb + j) * kBN;
       const bool need_mask = kv0 + kBN > lim_first;
