@@ -571,6 +571,11 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
   };
   load_q(at);
 
+  // E4M3: a row of Q is taken times 2^(13 - e), and its scores times 2^(e - 13)
+  // and the scale.  e is -113 at least, where every BF16 number is exact in FP16,
+  // and large enough to keep that product normal: a small scale leaves fewer bits to
+  // rows of small queries, which moves no score by more than 2^-15.
+  const int least_exp = 14 + max(0, 127 - (int)(__float_as_uint(p.scale_log2) >> 23));
   uint32_t q0 = 0;        // number of the segment's first block
   uint32_t round = 0;     // of merging
   bool lost = false;      // a wait ran out: no more results
@@ -593,9 +598,9 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
           for (int k = 0; k < 2; ++k) top = max(top, max(qf[n][s][k] & 0x7FFFu, (qf[n][s][k] >> 16) & 0x7FFFu));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int e = max((int)(top >> 7), 27) - 127;            // of the largest value, -100 at least
+        const int e = max((int)(top >> 7), least_exp) - 127;     // of the largest value
         const float up = __uint_as_float((uint32_t)(127 + 13 - e) << 23);     // e <= 128
-        scale *= __uint_as_float((uint32_t)(127 - 13 + e) << 23);
+        scale *= __uint_as_float((uint32_t)(127 - 13 + e) << 23);            // normal
 #pragma unroll
         for (int s = 0; s < kSteps; ++s)
 #pragma unroll

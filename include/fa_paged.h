@@ -134,7 +134,10 @@ FA_API size_t fa_fwd_paged_workspace_size(int B, int Hq, int Hkv, int Sn, int D,
  *   - BF16 pages: weights to BF16 (2^-8 of each at most); O is divided by the
  *     sum of the weights as rounded.
  *   - E4M3 pages: the products take FP16.  Queries are exact but for elements
- *     below 2^-30 of their row's largest (off by 2^-38 of it at most).  Codes
+ *     below 2^-30 of their row's largest (off by 2^-38 of it at most), and but
+ *     for what moves no score by more than 2^-15.  A score may overflow FP32 on
+ *     its way, and come out NaN, where `scale` times a query's largest element
+ *     is above 2^100.  Codes
  *     are exact where a row's scale is at least 2^-15 of the largest among the
  *     sequence's keys (values); codes of a row further below may be off by
  *     2^-25 of that largest scale.  A weight times its value's scale is off by

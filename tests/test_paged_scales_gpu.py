@@ -68,3 +68,35 @@ def test_chunk_rows_of_unlike_size(fa, D):
                           scale=2.0 ** -74, **c.scales)
     assert fa.get_device_error() == 0
     check_attention(o, lse, q, c, [50], True, 2.0 ** -74)
+
+
+@pytest.mark.parametrize("q_exp,k_exp", PAIRS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new", [1, 4])
+def test_single_tokens_scores_of_ordinary_size(fa, new, D, q_exp, k_exp):
+    lse = attend(fa, D, new, 4, q_exp, k_exp, 2.0 ** (-q_exp - k_exp - 4))
+    assert torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("new", [1, 4, 50])
+@pytest.mark.parametrize("D,scale", [(128, 2.0 ** -113), (64, 2.0 ** -112), (128, 1.3 * 2.0 ** -126)])
+def test_the_largest_keys_with_a_small_scale(fa, new, D, scale):
+    """Keys of all of BF16's range, alike along D, so that the scores of an FP16
+    row and a row of codes are the largest there are, and the factor that brings
+    them back is below the normal numbers."""
+    c = Cache([90], 1, D, 16, True, seed=1)
+    g = torch.Generator().manual_seed(2)
+    own = c.scale_host["k"] != 255
+    c.host["k"][:] = 0x7E                                              # 448
+    e = torch.randint(112, 120, own.shape, generator=g)
+    c.scale_host["k"] = torch.where(own, e + 127, torch.full_like(e, 255)).to(torch.uint8)
+    for t in range(90):
+        c.value["k"][t] = 448 * 2.0 ** float(e[c.table[0, t // 16], 0, t % 16])
+    c.upload()
+    size = 3.5 / (D * 448 * 2.0 ** 119 * scale)                        # the largest score is about 3.5
+    q = (torch.rand(new, 4, 1, generator=g) + 0.5).expand(new, 4, D).double() * size
+    q = q.to(torch.bfloat16).contiguous().cuda()
+    o, lse = fa.fwd_paged(q, c.k_pages, c.v_pages, c.block_table, c.seq_lens, cu_seqlens=cu_of([new]), max_q=new,
+                          scale=scale, **c.scales)
+    assert fa.get_device_error() == 0
+    check_attention(o, lse, q, c, [new], True, scale)
