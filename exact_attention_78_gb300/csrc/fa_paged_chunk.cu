@@ -1018,6 +1018,10 @@ __device__ void correction_role(const Shared<D, kFp8>& sh, const uint32_t tmem, 
 #pragma unroll
           for (int i = 0; i < 32; ++i) r[i] = 0u;
         }
+        if (l == 0.0f) {     // sees none of the keys: zero, whatever their values made of its zeros
+#pragma unroll
+          for (int i = 0; i < 32; ++i) r[i] = 0u;
+        }
         if (valid && w.slot >= 0) {
           if (kFp8) {
 #pragma unroll

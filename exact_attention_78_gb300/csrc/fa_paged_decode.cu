@@ -318,6 +318,7 @@ FA_DEV void merge_rows(const PagedAttnParams& p, const Walk<Layout<D, kFp8, kTil
     const float inv = !whole ? 1.0f : lrt == 0.0f ? 0.0f : 1.0f / lrt;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) st_m[lane * kWarps + w] = f[w] * inv;       // from here on the warps' factors
+    st_lr[lane * kWarps] = lt;                                                   // and the row's sum
     if (whole) {
       const int row = row0 + lane, t = row / p.group, head = at.head * p.group + row - t * p.group;
       const size_t li = p.s.cu ? (size_t)head * p.s.Sn + at.s.q0 + t : ((size_t)at.b * p.Hq + head) * p.s.Sn + t;
@@ -340,6 +341,8 @@ FA_DEV void merge_rows(const PagedAttnParams& p, const Walk<Layout<D, kFp8, kTil
       y.z += x.z * f;
       y.w += x.w * f;
     }
+    // a row that sees none of the keys is zero, whatever their values made of its zeros
+    if (st_lr[r * kWarps] == 0.0f) y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (whole) {
       const int row = row0 + r, t = row / p.group, head = at.head * p.group + row - t * p.group;
       *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + ((size_t)(at.s.q0 + t) * p.Hq + head) * D + d) =

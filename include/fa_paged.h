@@ -126,10 +126,10 @@ FA_API size_t fa_fwd_paged_workspace_size(int B, int Hq, int Hkv, int Sn, int D,
  *   scale        > 0; scale * log2(e) a normal FP32 number
  * o and lse overlap none of the inputs.  Hq is a multiple of Hkv, Hq / Hkv at
  * most 128, Hkv at most 4096.
- * A row that sees no key gets O = 0 and LSE = -inf.  Slots behind a sequence's
+ * A row that sees no key gets O = 0 and LSE = -inf, always.  Slots behind a sequence's
  * last token may hold anything (NaN and infinities too).  A NaN or an infinity
  * in a key reaches the rows that see it; one in a value may reach any row of
- * the same sequence and key/value head.
+ * the same sequence and key/value head that sees a key.
  * Roundings, besides O's to BF16 (scores, sums and O are FP32):
  *   - BF16 pages: weights to BF16 (2^-8 of each at most); O is divided by the
  *     sum of the weights as rounded.
