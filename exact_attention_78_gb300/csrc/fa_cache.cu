@@ -42,8 +42,9 @@ FA_DEV void find_slots(const PagedSeqs& s, int rows, int tb, Slots& out) {
   const int tok0 = blockIdx.x * tb;
   if (warp * 32 >= tb || tok0 + warp * 32 >= rows) return;
   const int i = tok0 + threadIdx.x;
+  const int capacity = s.max_pages << s.page_shift;
   int b, pos = -1;
-  bool mine = true, good = true;      // the row belongs to a sequence; its offsets keep to the rules
+  bool mine = true, good;             // the row belongs to a sequence; its offsets and length keep to the rules
   if (s.cu) {
     b = find_sequence(s.cu, s.B, tok0 + warp * 32, lane);
     if ((int)threadIdx.x >= tb || i >= rows) return;
@@ -51,19 +52,19 @@ FA_DEV void find_slots(const PagedSeqs& s, int rows, int tb, Slots& out) {
     mine = b < s.B;
     if (mine) {
       const int first = s.cu[b], end = s.cu[b + 1];
-      good = first >= 0 && i >= first && i < end;
-      pos = kWrite ? s.seq_lens[b] - (end - i) : i - first;
-      good = good && (!kWrite || s.seq_lens[b] >= 0);
+      const int len = kWrite ? s.seq_lens[b] : end - first;
+      good = first >= 0 && i >= first && end <= rows && (b > 0 || first == 0) && len >= 0 && len <= capacity;
+      if (good) pos = kWrite ? len - (end - i) : i - first;
     }
   } else {
     if ((int)threadIdx.x >= tb || i >= rows) return;
     b = i / s.Sn;
-    pos = s.seq_lens[b] - (s.Sn - (i - b * s.Sn));
-    good = s.seq_lens[b] >= 0;
+    const int len = s.seq_lens[b];
+    good = len >= 0 && len <= capacity;
+    if (good) pos = len - (s.Sn - (i - b * s.Sn));
   }
-  good = good && (pos >> s.page_shift) < s.max_pages;
   int page = -1;
-  if (mine && good && pos >= 0) {
+  if (pos >= 0) {                     // below the capacity: a token lies before its sequence's end
     page = s.block_table[(size_t)b * s.max_pages + (pos >> s.page_shift)];
     if (page < 0 || page >= s.num_pages) {
       record_bad_input(&g_err, kSitePage);
