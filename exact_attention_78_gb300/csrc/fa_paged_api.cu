@@ -6,6 +6,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "fa_diag.h"
 #include "fa_paged.h"
 #include "paged_internal.h"
 
@@ -69,6 +70,54 @@ bool attn_shape_ok(int B, int Hq, int Hkv, int Sn, int D, bool packed, int max_q
   if ((packed ? (long long)Sn : (long long)B * Sn) > INT32_MAX - 512) return false;
   if ((long long)(packed ? max_q : Sn) * (Hq / Hkv) > INT32_MAX - 512) return false;
   return true;
+}
+
+size_t workspace_size(int B, int Hq, int Hkv, int Sn, int D, bool packed, int max_q) {
+  return takes_decode(Hq, Hkv, Sn, D, packed, max_q) ? paged_decode_workspace(D) : paged_chunk_workspace(D);
+}
+
+fa_status fwd_paged(const void* q, const void* k_pages, const void* v_pages, const void* k_scale,
+                    const void* v_scale, void* o, float* lse, int B, int Hq, int Hkv, int Sn, int D, int num_pages,
+                    int page_size, int max_pages, int causal, float scale, const int* block_table,
+                    const int* seq_lens, const int* cu_seqlens, int max_q, void* workspace, size_t workspace_bytes,
+                    unsigned long long wait_limit_ns, fa_stream_t stream) {
+  try {
+    PagedAttnLaunch L{};
+    if (!q || !o || !lse || !seq_lens || !aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 16))
+      return FA_ERR_INVALID_ARG;
+    if (causal != 0 && causal != 1) return FA_ERR_INVALID_ARG;
+    // (a factor of -inf, masked scores, has to be a normal number)
+    if (!(scale > 0.0f) || !std::isnormal(scale * kLog2e)) return FA_ERR_INVALID_ARG;
+    fa_status st;
+    if (!attn_shape_ok(B, Hq, Hkv, Sn, D, cu_seqlens != nullptr, max_q, &st)) return st;
+    st = check_cache(k_pages, v_pages, k_scale, v_scale, B, Hkv, Sn, D, num_pages, page_size, max_pages, block_table,
+                     seq_lens, cu_seqlens, &L.p.s);
+    if (st != FA_OK) return st;
+    const size_t need = workspace_size(B, Hq, Hkv, Sn, D, cu_seqlens != nullptr, max_q);
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return FA_ERR_WORKSPACE;
+    if ((st = device_info(&L.num_sms)) != FA_OK) return st;
+    L.p.q = q;
+    L.p.o = o;
+    L.p.lse = lse;
+    L.p.k_scale = static_cast<const uint8_t*>(k_scale);
+    L.p.v_scale = static_cast<const uint8_t*>(v_scale);
+    L.p.Hq = Hq;
+    L.p.group = Hq / Hkv;
+    L.p.causal = causal;
+    L.p.max_q = cu_seqlens ? max_q : Sn;
+    L.p.scale_log2 = scale * kLog2e;
+    L.p.part = static_cast<float*>(workspace);
+    L.p.num_ctas = L.num_sms < kMaxCtas ? L.num_sms : kMaxCtas;
+    L.p.wait_limit_ns = wait_limit_ns;
+    L.k_pages = k_pages;
+    L.v_pages = v_pages;
+    L.D = D;
+    L.fp8 = k_scale != nullptr;
+    const bool decode = takes_decode(Hq, Hkv, Sn, D, cu_seqlens != nullptr, max_q);
+    return (decode ? launch_paged_decode : launch_paged_chunk)(L, reinterpret_cast<cudaStream_t>(stream));
+  } catch (...) {
+    return FA_ERR_CUDA;
+  }
 }
 
 }  // namespace
@@ -191,7 +240,7 @@ fa_status fa_cache_read(const void* k_pages, const void* v_pages, const void* k_
 size_t fa_fwd_paged_workspace_size(int B, int Hq, int Hkv, int Sn, int D, int packed, int max_q) {
   fa_status why;
   if ((packed != 0 && packed != 1) || !attn_shape_ok(B, Hq, Hkv, Sn, D, packed != 0, max_q, &why)) return 0;
-  return takes_decode(Hq, Hkv, Sn, D, packed != 0, max_q) ? paged_decode_workspace(D) : paged_chunk_workspace(D);
+  return workspace_size(B, Hq, Hkv, Sn, D, packed != 0, max_q);
 }
 
 fa_status fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages, const void* k_scale,
@@ -199,43 +248,21 @@ fa_status fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages, 
                        int page_size, int max_pages, int causal, float scale, const int* block_table,
                        const int* seq_lens, const int* cu_seqlens, int max_q, void* workspace, size_t workspace_bytes,
                        fa_stream_t stream) {
-  try {
-    PagedAttnLaunch L{};
-    if (!q || !o || !lse || !seq_lens || !aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 16))
-      return FA_ERR_INVALID_ARG;
-    if (causal != 0 && causal != 1) return FA_ERR_INVALID_ARG;
-    // (a factor of -inf, masked scores, has to be a normal number)
-    if (!(scale > 0.0f) || !std::isnormal(scale * kLog2e)) return FA_ERR_INVALID_ARG;
-    fa_status st;
-    if (!attn_shape_ok(B, Hq, Hkv, Sn, D, cu_seqlens != nullptr, max_q, &st)) return st;
-    st = check_cache(k_pages, v_pages, k_scale, v_scale, B, Hkv, Sn, D, num_pages, page_size, max_pages, block_table,
-                     seq_lens, cu_seqlens, &L.p.s);
-    if (st != FA_OK) return st;
-    const size_t need = fa_fwd_paged_workspace_size(B, Hq, Hkv, Sn, D, cu_seqlens != nullptr, max_q);
-    if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return FA_ERR_WORKSPACE;
-    if ((st = device_info(&L.num_sms)) != FA_OK) return st;
-    L.p.q = q;
-    L.p.o = o;
-    L.p.lse = lse;
-    L.p.k_scale = static_cast<const uint8_t*>(k_scale);
-    L.p.v_scale = static_cast<const uint8_t*>(v_scale);
-    L.p.Hq = Hq;
-    L.p.group = Hq / Hkv;
-    L.p.causal = causal;
-    L.p.max_q = cu_seqlens ? max_q : Sn;
-    L.p.scale_log2 = scale * kLog2e;
-    L.p.part = static_cast<float*>(workspace);
-    L.p.num_ctas = L.num_sms < kMaxCtas ? L.num_sms : kMaxCtas;
-    L.p.wait_limit_ns = kDefaultWaitLimitNs;
-    L.k_pages = k_pages;
-    L.v_pages = v_pages;
-    L.D = D;
-    L.fp8 = k_scale != nullptr;
-    const bool decode = takes_decode(Hq, Hkv, Sn, D, cu_seqlens != nullptr, max_q);
-    return (decode ? launch_paged_decode : launch_paged_chunk)(L, reinterpret_cast<cudaStream_t>(stream));
-  } catch (...) {
-    return FA_ERR_CUDA;
-  }
+  return fwd_paged(q, k_pages, v_pages, k_scale, v_scale, o, lse, B, Hq, Hkv, Sn, D, num_pages, page_size, max_pages,
+                   causal, scale, block_table, seq_lens, cu_seqlens, max_q, workspace, workspace_bytes,
+                   kDefaultWaitLimitNs, stream);
+}
+
+fa_status fa_diag_fwd_paged(const void* q, const void* k_pages, const void* v_pages, const void* k_scale,
+                            const void* v_scale, void* o, float* lse, int B, int Hq, int Hkv, int Sn, int D,
+                            int num_pages, int page_size, int max_pages, int causal, float scale,
+                            const int* block_table, const int* seq_lens, const int* cu_seqlens, int max_q,
+                            void* workspace, size_t workspace_bytes, unsigned long long wait_limit_ns,
+                            fa_stream_t stream) {
+  if (wait_limit_ns == 0 || wait_limit_ns > 10000000000ull) return FA_ERR_INVALID_ARG;
+  return fwd_paged(q, k_pages, v_pages, k_scale, v_scale, o, lse, B, Hq, Hkv, Sn, D, num_pages, page_size, max_pages,
+                   causal, scale, block_table, seq_lens, cu_seqlens, max_q, workspace, workspace_bytes, wait_limit_ns,
+                   stream);
 }
 
 }  // extern "C"

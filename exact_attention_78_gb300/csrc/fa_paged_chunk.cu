@@ -1286,16 +1286,20 @@ __global__ void __launch_bounds__(Layout<D, kFp8>::kThreads, 1)
     }
   }
 
-  // After a give-up, copies and MMAs in flight land before the memory they
-  // target is released.
-  if (ld_shared_volatile(sh.abort())) {
-    const uint64_t t0 = globaltimer_ns();
-    while (globaltimer_ns() - t0 < 2000000ull) __nanosleep(1000);
-  }
+  // After a give-up, copies and MMAs in flight land before the memory they target is
+  // released: one warp stays for that, when all roles have ended.  (With every warp
+  // staying, ahead of the barrier, those of 48 registers among them, a give-up over
+  // E4M3 pages ended in a launch failure.)
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == 13) {
     tc_fence_after();
+    if (ld_shared_volatile(sh.abort())) {
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 2000000ull) __nanosleep(1000);
+      __syncwarp();
+    }
     tmem_dealloc(tmem, 512);
   }
 }

@@ -151,6 +151,18 @@ FA_API fa_status fa_diag_exp2(const float* x, float* y_emu, float* y_hw, long lo
  */
 FA_API fa_status fa_diag_wait_timeout(unsigned long long limit_ns, fa_stream_t stream);
 
+/*
+ * fa_fwd_paged() (fa_paged.h) whose kernels' waits give up after
+ * wait_limit_ns, 1 to 10^10, in place of the library's bound.  For the test
+ * that waits last a key block or so, however long a sequence is.
+ */
+FA_API fa_status fa_diag_fwd_paged(const void* q, const void* k_pages, const void* v_pages, const void* k_scale,
+                                   const void* v_scale, void* o, float* lse, int B, int Hq, int Hkv, int Sn, int D,
+                                   int num_pages, int page_size, int max_pages, int causal, float scale,
+                                   const int* block_table, const int* seq_lens, const int* cu_seqlens, int max_q,
+                                   void* workspace, size_t workspace_bytes, unsigned long long wait_limit_ns,
+                                   fa_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
