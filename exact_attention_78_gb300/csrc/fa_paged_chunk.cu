@@ -172,11 +172,12 @@ struct Shared {
     return paged::wait_warp(b, parity, abort(), &g_err, site, p.wait_limit_ns);
   }
   // For waits that last as long as a segment (some seconds over 2^30 keys; the
-  // other roles wait for a block at a time, and give up first if nothing moves):
-  // sleeps between looks, off the issue slots.
-  FA_DEV bool wait_long(uint32_t b, uint32_t parity, int site, const PagedAttnParams& p) const {
+  // other roles wait for a block at a time, and give up first if nothing moves).
+  // Roles that are not in a hurry sleep between looks, off the issue slots.
+  FA_DEV bool wait_long(uint32_t b, uint32_t parity, int site, const PagedAttnParams& p, bool sleeps = true) const {
 #pragma unroll 1
-    for (int i = 0; i < (1 << 27) && !mbar_try_wait(b, parity) && !ld_shared_volatile(abort()); ++i) __nanosleep(200);
+    for (int i = 0; i < (1 << 27) && !mbar_try_wait(b, parity) && !ld_shared_volatile(abort()); ++i)
+      if (sleeps) __nanosleep(200);
     return wait(b, parity, site, p);
   }
 };
@@ -329,9 +330,11 @@ struct SegReader {
   int i = 0;
   uint32_t phase = 0;
   FA_DEV SegReader(const Shared<D, kFp8>& s, const PagedAttnParams& q) : sh(s), p(q) {}
-  // The whole warp calls it.
-  FA_DEV bool next(Seg& w, bool may_sleep = false) {
-    if (!(may_sleep ? sh.wait_long(sh.seg_full(i), phase, kSiteSegFull, p) : sh.wait(sh.seg_full(i), phase, kSiteSegFull, p)))
+  // The whole warp calls it.  `idle`: had nothing to do with the segments before, and
+  // may be here as long before the next as one lasts.
+  FA_DEV bool next(Seg& w, bool idle = false, bool sleeps = true) {
+    if (!(idle ? sh.wait_long(sh.seg_full(i), phase, kSiteSegFull, p, sleeps)
+               : sh.wait(sh.seg_full(i), phase, kSiteSegFull, p)))
       return false;
     const volatile Seg& r = sh.segs()[i];
     // a value that comes out of a shuffle is known to be the same in all lanes,
@@ -805,14 +808,17 @@ __device__ void softmax_role(const int t, const Shared<D, kFp8>& sh, const uint3
   SegReader<D, kFp8> in(sh, p);
   Seg w;
   uint32_t sit = 0, seg = 0;
-  while (in.next(w)) {
+  bool idle = false;       // the segment before had no block of this tile
+  while (in.next(w, idle, false)) {
     const int nt = tile_blocks(w, t, tt, p.causal);
     int q_exp = 0;
     if constexpr (kFp8) {
       // Both tiles' warps take every segment's Q, also when theirs has no block,
       // so that neither falls two phases behind.
       if (max(nt, tile_blocks(w, t ^ 1, tt, p.causal)) > 0) {
-        if (!sh.wait(sh.q_full(), seg & 1, kSiteQFull, p)) return;
+        if (!(idle ? sh.wait_long(sh.q_full(), seg & 1, kSiteQFull, p, false)
+                   : sh.wait(sh.q_full(), seg & 1, kSiteQFull, p)))
+          return;
         if (nt > 0) q_exp = narrow_row<D>(sh, t, r_in_tile);
         fence_proxy_async_smem();
         __syncwarp();
@@ -820,7 +826,8 @@ __device__ void softmax_role(const int t, const Shared<D, kFp8>& sh, const uint3
         ++seg;
       }
     }
-    if (nt == 0) continue;
+    idle = nt == 0;
+    if (idle) continue;
     const int tok = w.tok0 + t * tt;
     const int lim_first = p.causal ? w.L - w.n + tok + 1 : w.L;                  // of the tile's first row
     const int lim_row = p.causal ? min(w.L, lim_first + my_tok) : w.L;
