@@ -396,6 +396,9 @@ def rope(q, k, positions, sections=None, base=10000.0, restart=False, interleave
         raise ValueError("%d sections for %d axes" % (len(sections), axes))
     if min(sections) < 1 or sum(sections) > D // 2:      # (the C interface's ints would wrap)
         raise ValueError("sections %s of at most %d pairs" % (tuple(sections), D // 2))
+    tokens = lead.numel()
+    if tokens >= 2 ** 31:
+        raise ValueError("%d tokens in one call" % tokens)
     if q_out is not None:
         _check_out("q_out", q_out, shape, torch.bfloat16, device)
     if k_out is not None:
@@ -405,7 +408,7 @@ def rope(q, k, positions, sections=None, base=10000.0, restart=False, interleave
             q_out = torch.empty_like(q)
         if k is not None and k_out is None:
             k_out = torch.empty_like(k)
-        st = lib.fa_rope(q.data_ptr(), _adr(k), q_out.data_ptr(), _adr(k_out), lead.numel(), Hq, Hkv, D,
+        st = lib.fa_rope(q.data_ptr(), _adr(k), q_out.data_ptr(), _adr(k_out), tokens, Hq, Hkv, D,
                          positions.data_ptr(), axes, _c_ints(tuple(sections)), base, bool(restart),
                          bool(interleaved), bool(inverse), s)
     if st:

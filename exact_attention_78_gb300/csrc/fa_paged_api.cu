@@ -146,6 +146,7 @@ fa_status fa_rope(const void* q, const void* k, void* q_out, void* k_out, int to
     if (pairs > D / 2) return FA_ERR_INVALID_ARG;
     // the largest loop index of a thread block: 4 tokens of 16 pieces per head
     if ((long long)Hq + (k ? Hkv : 0) > (1 << 20)) return FA_ERR_UNSUPPORTED;
+    if (tokens > INT32_MAX - 512) return FA_ERR_UNSUPPORTED;      // (the grid's size and the last block's tokens)
     int num_sms = 0;
     fa_status st = device_info(&num_sms);
     if (st != FA_OK) return st;

@@ -59,8 +59,8 @@ extern "C" {
 
 /*
  * Rotary positions with one to four axes, on queries and keys in one launch.
- *   q, k         [tokens, Hq, D] and [tokens, Hkv, D]; k may be NULL (Hkv is
- *                then ignored)
+ *   q, k         [tokens, Hq, D] and [tokens, Hkv, D], at most 2^31 - 513
+ *                tokens; k may be NULL (Hkv is then ignored)
  *   q_out, k_out where the turned rows go; may be q and k themselves, and
  *                must not overlap them in any other way
  *   positions    device int32 [axes, tokens]; any int32 value
