@@ -29,8 +29,8 @@ FA_DEV float hi_of(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 // first elements has its partners in one other aligned piece and a thread
 // turns both.  kAdjacent: pairs (2 i, 2 i + 1), inside one piece.  kAny: pairs
 // (i, i + R) at any R: a thread's piece meets its partners one by one, in the
-// row's copy in shared memory.  16,384 tokens x 32 heads, D = 128, R = 64: kHalf
-// 40.9 us (6.6 TB/s), kAny 82 us.
+// row's copy in shared memory.  16,384 tokens x 32 heads, D = 128: kHalf 41.1 us at
+// R = 64 (6.5 TB/s), kAny 70, 92, 88 and 73 us at R = 63, 60, 44 and 20, kAdjacent 48.
 enum Layout { kHalf, kAdjacent, kAny };
 
 // 16-byte pieces that one thread loads and stores at a time.
@@ -98,11 +98,11 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
       const int r = r0 + first + u * step;
       const bool on = first < step && r < n;
       if (kLayout == kAny) {
-        // (a row's lanes may sit in two warps; in place, its stores below must
-        // not overtake these loads)
-        __syncthreads();
+        // (a row's lanes, 8 or 16 from a multiple of that on, sit in one warp; in
+        // place, a thread stores over no piece but its own, which it has loaded)
+        __syncwarp();
         if (on) copy[threadIdx.x] = x[u].a;
-        __syncthreads();
+        __syncwarp();
       }
       if (!on) continue;
       const int in = r < nq ? r : r - nq, heads = r < nq ? p.Hq : p.Hkv;
