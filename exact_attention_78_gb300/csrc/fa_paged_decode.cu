@@ -15,9 +15,9 @@
 //     tiles have at least 64 rows on M and their accumulators are a trip through
 //     tensor memory away; with so few rows the warp-level instruction leaves the
 //     tensor cores a quarter busy.)
-//   * Work.  The key blocks of all (sequence, key/value head, row tile)
-//     units, and a constant for each unit's start and end, form one line, and
-//     thread block c takes the c-th of `grid` equal stretches of it.  A unit cut
+//   * Work.  The key blocks of all (sequence, key/value head) units, and a
+//     constant for each unit's start and end, form one line, and thread block c
+//     takes the c-th of `grid` equal stretches of it.  A unit cut
 //     by a border leaves partial results in the workspace, at most two per
 //     thread block, and the combine kernel joins them.  Sequences of any mixture
 //     of lengths load all SMs alike.
@@ -112,7 +112,6 @@ struct Layout {
 
 using Seq = paged::SeqRows;
 FA_DEV Seq seq_of(const PagedSeqs& s, int b) { return paged::rows_of(s, b); }
-FA_DEV int tiles_of(int n, int group, int rows) { return (n * group + rows - 1) / rows; }
 // Blocks of a unit: at least one, so that rows without a key are written too.
 FA_DEV int blocks_of(int L, int keys) { return max(1, (L + keys - 1) / keys); }
 // What a unit takes on the line besides its blocks: starting and merging it.  (64
@@ -123,14 +122,11 @@ constexpr int kUnitCost = 14;
 
 // Prefix sums of the sequences' blocks into pre[0 .. B]; returns their total,
 // 0 when the sequences break the rules.  All threads of the block.
-template <int kKeys, int kRows>
+template <int kKeys>
 FA_DEV long long build_line(const PagedAttnParams& p, long long* pre, long long* warp_sums) {
   const bool ok = paged::prefix_sequences(
       p.s, p.max_q,
-      [&](const Seq& q) {
-        const int tiles = tiles_of(q.n, p.group, kRows);
-        return paged::Work{(long long)p.s.Hkv * tiles * (blocks_of(q.L, kKeys) + kUnitCost), 0, 0};
-      },
+      [&](const Seq& q) { return paged::Work{(long long)p.s.Hkv * (blocks_of(q.L, kKeys) + kUnitCost), 0, 0}; },
       pre, nullptr, warp_sums);
   if (ok) return pre[p.s.B];
   if (blockIdx.x == 0 && threadIdx.x == 0) paged::record_bad_input(&g_err, kSiteSeqs);
@@ -148,9 +144,9 @@ FA_DEV long long stretch(long long total, int c, int G) { return paged::div64(to
 // A walk over the segments (the stretch's share of one unit) of [t0, t1).  A
 // border behind a unit's blocks, in what starting and merging it counts, leaves
 // the unit whole.
-template <int kKeys, int kRows>
+template <int kKeys>
 struct Walk {
-  int b, head, tile, tiles;
+  int b, head;
   Seq s;
   int nblk;          // blocks of the unit
   int kb, count;     // the segment: blocks [kb, kb + count)
@@ -159,7 +155,6 @@ struct Walk {
 
   FA_DEV void load(const PagedAttnParams& p) {
     s = seq_of(p.s, b);
-    tiles = tiles_of(s.n, p.group, kRows);
     nblk = blocks_of(s.L, kKeys);
   }
   FA_DEV void begin(const PagedAttnParams& p, const long long* pre, long long t0, long long end) {
@@ -175,8 +170,7 @@ struct Walk {
     const long long unit = paged::div64(r, nblk + kUnitCost);
     kb = (int)(r - unit * (nblk + kUnitCost));
     start = t0 - kb;
-    head = (int)paged::div64(unit, tiles);
-    tile = (int)(unit - (long long)head * tiles);
+    head = (int)unit;
     cut();
     if (kb >= nblk) next(p);
   }
@@ -186,32 +180,17 @@ struct Walk {
     start += nblk + kUnitCost;
     kb = 0;
     if (start >= t1) return;
-    if (++tile == tiles) {
-      tile = 0;
-      if (++head == p.s.Hkv) {
-        head = 0;
-        do ++b; while (b < p.s.B - 1 && seq_of(p.s, b).n == 0);
-        load(p);
-      }
+    if (++head == p.s.Hkv) {
+      head = 0;
+      do ++b; while (b < p.s.B - 1 && seq_of(p.s, b).n == 0);
+      load(p);
     }
     cut();
   }
-  // Token and head of the tile's first row.
-  FA_DEV void first_row(const PagedAttnParams& p, int& t, int& j) const {
-    t = tile * kRows / p.group;
-    j = tile * kRows - t * p.group;
-  }
-  FA_DEV int rows(const PagedAttnParams& p) const { return min(kRows, s.n * p.group - tile * kRows); }
-  // Keys that the tile's last row sees.
-  FA_DEV int seen(const PagedAttnParams& p) const {
-    if (!p.causal) return s.L;
-    const int t = min(s.n * p.group, (tile + 1) * kRows) - 1;
-    return min(s.L, max(0, s.L - s.n + t / p.group + 1));
-  }
-  // Blocks of the segment that any row sees: the leading ones.
-  FA_DEV int visible(const PagedAttnParams& p) const {
-    return min(count, max(0, (seen(p) + kKeys - 1) / kKeys - kb));
-  }
+  // Rows (token, head of the group) of the unit.
+  FA_DEV int rows(const PagedAttnParams& p) const { return s.n * p.group; }
+  // Blocks of the segment with keys, all of which the last token sees.
+  FA_DEV int visible() const { return min(count, max(0, (s.L + kKeys - 1) / kKeys - kb)); }
 };
 
 // ----------------------------------------------------------- instructions --
@@ -289,13 +268,13 @@ FA_DEV bool test_warp(uint32_t bar, uint32_t parity) {
 // Joins the states that the computing warps left of rows [r0, r0 + kRound) of a
 // segment: final when it is the whole unit, else into the workspace.  One warp.
 template <int D, bool kFp8, int kTiles>
-FA_DEV void merge_rows(const PagedAttnParams& p, const Walk<Layout<D, kFp8, kTiles>::kKeys, 8 * kTiles>& at, int r0,
+FA_DEV void merge_rows(const PagedAttnParams& p, const Walk<Layout<D, kFp8, kTiles>::kKeys>& at, int r0,
                        const float* buf, float* stats) {
   using L = Layout<D, kFp8, kTiles>;
   using W = Part<D, L::kRows>;
   constexpr int kWarps = L::kWarps;
   const int lane = threadIdx.x % 32;
-  const int rows = min(L::kRound, at.rows(p) - r0), row0 = at.tile * L::kRows + r0;
+  const int rows = min(L::kRound, at.rows(p) - r0);
   const bool whole = at.kb == 0 && at.count == at.nblk;
   // a stretch begins in a cut unit at most once, and ends in one at most once
   const int slot = 2 * blockIdx.x + (at.kb > 0 ? 0 : 1);
@@ -320,7 +299,7 @@ FA_DEV void merge_rows(const PagedAttnParams& p, const Walk<Layout<D, kFp8, kTil
     for (int w = 0; w < kWarps; ++w) st_m[lane * kWarps + w] = f[w] * inv;       // from here on the warps' factors
     st_lr[lane * kWarps] = lt;                                                   // and the row's sum
     if (whole) {
-      const int row = row0 + lane, t = row / p.group, head = at.head * p.group + row - t * p.group;
+      const int row = r0 + lane, t = row / p.group, head = at.head * p.group + row - t * p.group;
       const size_t li = p.s.cu ? (size_t)head * p.s.Sn + at.s.q0 + t : ((size_t)at.b * p.Hq + head) * p.s.Sn + t;
       p.lse[li] = lt == 0.0f ? -INFINITY : (mt + log2f(lt)) * 0.693147180559945309f;
     } else {
@@ -344,7 +323,7 @@ FA_DEV void merge_rows(const PagedAttnParams& p, const Walk<Layout<D, kFp8, kTil
     // a row that sees none of the keys is zero, whatever their values made of its zeros
     if (st_lr[r * kWarps] == 0.0f) y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (whole) {
-      const int row = row0 + r, t = row / p.group, head = at.head * p.group + row - t * p.group;
+      const int row = r0 + r, t = row / p.group, head = at.head * p.group + row - t * p.group;
       *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + ((size_t)(at.s.q0 + t) * p.Hq + head) * D + d) =
           make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
     } else {
@@ -359,7 +338,7 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
                   const PagedAttnParams p) {
   using L = Layout<D, kFp8, kTiles>;
   using W = Part<D, L::kRows>;
-  constexpr int kWarps = L::kWarps, kRows = L::kRows;
+  constexpr int kWarps = L::kWarps;
   constexpr int kKeys = L::kKeys;
   constexpr int kGroups = kKeys / 16;
   constexpr int kSteps = D / 16;      // 16-wide steps along D
@@ -389,7 +368,7 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
     tma_prefetch_desc(&tm_v);
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");      // nothing global before this
-  const long long total = build_line<kKeys, kRows>(p, pre, reinterpret_cast<long long*>(merge));
+  const long long total = build_line<kKeys>(p, pre, reinterpret_cast<long long*>(merge));
   __syncthreads();
   const int G = active_ctas(total, gridDim.x);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -401,7 +380,7 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
 
   // The stretch's visible blocks are numbered through; block q goes through ring
   // slot q mod kSlots.
-  Walk<kKeys, kRows> at;
+  Walk<kKeys> at;
   at.begin(p, pre, t0, t1);
 
   const int box_shift = min(p.s.page_shift, kKeys == 32 ? 5 : 4);    // rows of a box
@@ -412,7 +391,7 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
     // ---- says what there is to join at the border before this stretch
     if (lane == 0) {
       const int c = blockIdx.x;
-      paged::Join j{0, at.b, at.head, at.tile * kRows, at.s.n, at.s.q0, {0, 0}};
+      paged::Join j{0, at.b, at.head, 0, at.s.n, at.s.q0, {0, 0}};
       if (at.kb > 0 && stretch(total, c - 1, G) <= at.start) {       // the unit's first cut
         j.parts = 2;
         while (c + j.parts - 1 < G && stretch(total, c + j.parts - 1, G) < at.start + at.nblk) ++j.parts;
@@ -422,10 +401,10 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
     // ---- looks up where blocks lie, (page, head) and row of the block's boxes,
     // and merges the states that the other warps leave at a unit's end, whichever
     // can be done
-    Walk<kKeys, kRows> mine = at;
+    Walk<kKeys> mine = at;
     int r0 = 0;                        // of the rows to merge next
     uint32_t round = 0, batch = 0;
-    int i = 0, vis = at.visible(p), past = 0;
+    int i = 0, vis = at.visible(), past = 0;
     bool have = false;                 // a batch that waits for its place
     int4 place;
     uint64_t idle = 0;                 // since when nothing could be done
@@ -456,7 +435,7 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
             if (i == vis) {
               at.next(p);
               i = 0;
-              vis = at.more() ? at.visible(p) : 0;
+              vis = at.more() ? at.visible() : 0;
             }
           }
           have = true;
@@ -538,24 +517,22 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
 #pragma unroll 1
   for (int q = warp; q < L::kSlots; q += kWarps) load(q);
 
-  // Q of a segment's tile as B fragments: row 8 n + g of tile n, d = 16 s + 2 c,
+  // Q of a segment as B fragments: row 8 n + g in tile n, d = 16 s + 2 c,
   // + 1 and + 8, + 9.  E4M3: four consecutive values at 16 s + 4 c instead, which
   // is how a word of four codes of a key lies in its fragment.
   uint32_t qf[kTiles][kSteps][2];
   const float inv_group = 1.0f / (float)p.group;
-  // (token, head) of row j0 + x of a token's group: exact for the small numbers here
-  auto tokens_on = [&](int j0_plus_x) { return (int)(((float)j0_plus_x + 0.5f) * inv_group); };
-  auto load_q = [&](const Walk<kKeys, kRows>& w) {
+  // token of a row: exact for the small numbers here
+  auto token_of = [&](int row) { return (int)(((float)row + 0.5f) * inv_group); };
+  auto load_q = [&](const Walk<kKeys>& w) {
     const int rows = w.rows(p);
-    int tok0, j0;
-    w.first_row(p, tok0, j0);
 #pragma unroll
     for (int n = 0; n < kTiles; ++n) {
-      const int r = j0 + 8 * n + g;
-      const bool valid = 8 * n + g < rows;
-      const int t = tokens_on(r), j = r - t * p.group;
+      const int r = 8 * n + g;
+      const bool valid = r < rows;
+      const int t = token_of(r), j = r - t * p.group;
       const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) +
-                                 ((size_t)(w.s.q0 + tok0 + t) * p.Hq + w.head * p.group + j) * D;
+                                 ((size_t)(w.s.q0 + t) * p.Hq + w.head * p.group + j) * D;
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
         uint2 x = make_uint2(0u, 0u);
@@ -584,10 +561,8 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
   bool lost = false;      // a wait ran out: no more results
   while (at.more()) {
     const int rows = at.rows(p);
-    int tok0, j0;
-    at.first_row(p, tok0, j0);
-    const int vis = at.visible(p);
-    // rows 8 n + 2 c + e of the tile, whose scores this lane gets:
+    const int vis = at.visible();
+    // rows 8 n + 2 c + e, whose scores this lane gets:
     int row_lim[kTiles][2];          // keys that they see
     float row_scale[kTiles][2];      // what their scores are multiplied by, for log2 units
 #pragma unroll
@@ -615,11 +590,11 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         row_scale[n][e] = kFp8 ? __shfl_sync(0xffffffffu, scale, (2 * c + e) * 4) : scale;
-        const int in_tile = 8 * n + 2 * c + e;
-        row_lim[n][e] = in_tile >= rows ? 0 : p.causal ? at.s.L - at.s.n + tok0 + tokens_on(j0 + in_tile) + 1 : at.s.L;
+        const int row = 8 * n + 2 * c + e;
+        row_lim[n][e] = row >= rows ? 0 : p.causal ? at.s.L - at.s.n + token_of(row) + 1 : at.s.L;
       }
     }
-    // O^T: columns of V on the rows, tile rows on the columns (2 c, 2 c + 1 here)
+    // O^T: columns of V on the rows, rows of Q on the columns (2 c, 2 c + 1 here)
     float acc[kTiles][kSteps][4];
     float m[kTiles][2], l[kTiles][2];
     float ones[kTiles][4];      // BF16: sums of the weights as the product takes them
@@ -707,9 +682,8 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
       // of zero would not cancel: they are cleared below.
       const int n_left = at.s.L - key0;
       const bool ragged = n_left < kKeys;
-      // a block that every row sees whole needs no mask (rows of the tile see
-      // at least the first row's keys)
-      const bool masked = key0 + kKeys > (p.causal ? at.s.L - at.s.n + tok0 + 1 : at.s.L);
+      // a block that the first token sees whole needs no mask
+      const bool masked = key0 + kKeys > (p.causal ? at.s.L - at.s.n + 1 : at.s.L);
       uint32_t pb[kTiles][kGroups][2];        // P^T as B fragments
 #pragma unroll
       for (int n = 0; n < kTiles; ++n) {
@@ -810,7 +784,7 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
     q0 += vis;
 
     // the next segment's queries come while this one is finished
-    Walk<kKeys, kRows> after = at;
+    Walk<kKeys> after = at;
     after.next(p);
     if (after.more()) load_q(after);
     // Long units end together: warps that drift apart refill the ring out of turn.
@@ -904,7 +878,7 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const PagedAttnPa
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) x0[k] = part_of(k);
   }
-  const int rows = j.parts == 0 ? 0 : min(kJoinRows, min(kRows, j.n * p.group - j.row0) - row0);
+  const int rows = j.parts == 0 ? 0 : min(kJoinRows, j.n * p.group - row0);
   if (rows <= 0) return;
   for (int i = threadIdx.x; i < j.parts * kJoinRows; i += kJoinThreads) {
     const int k = i / kJoinRows, row = i % kJoinRows;
@@ -915,7 +889,6 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const PagedAttnPa
     st_lr[k][row] = st.z;
   }
   __syncthreads();
-  const int unit_row = j.row0 + row0;
   if ((int)threadIdx.x < rows) {
     const int row = threadIdx.x;
     float mt = -INFINITY, lt = 0.0f, lrt = 0.0f;
@@ -927,7 +900,7 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const PagedAttnPa
       lrt += st_lr[k][row] * f;
     }
     inv[row] = lrt == 0.0f ? 0.0f : 1.0f / lrt;
-    const int tk = (unit_row + row) / p.group, head = j.head * p.group + unit_row + row - tk * p.group;
+    const int tk = (row0 + row) / p.group, head = j.head * p.group + row0 + row - tk * p.group;
     const size_t li = p.s.cu ? (size_t)head * p.s.Sn + j.q0 + tk : ((size_t)j.b * p.Hq + head) * p.s.Sn + tk;
     p.lse[li] = lt == 0.0f ? -INFINITY : (mt + log2f(lt)) * 0.693147180559945309f;
   }
@@ -944,7 +917,7 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const PagedAttnPa
   for (int k = 0; k < kAhead; ++k) add(x0[k], st_m[k][r]);      // (a join has two parts or more)
 #pragma unroll 8
   for (int k = kAhead; k < j.parts; ++k) add(part_of(k), st_m[k][r]);
-  const int tk = (unit_row + r) / p.group, head = j.head * p.group + unit_row + r - tk * p.group;
+  const int tk = (row0 + r) / p.group, head = j.head * p.group + row0 + r - tk * p.group;
   *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + ((size_t)(j.q0 + tk) * p.Hq + head) * D + d) =
       make_uint2(pack_bf16x2(y.x * inv[r], y.y * inv[r]), pack_bf16x2(y.z * inv[r], y.w * inv[r]));
 }

@@ -166,7 +166,7 @@ FA_DEV long long div64(long long a, long long b) {
 struct Join {
   int parts;       // of the unit whose first cut this border is (two or more); 0: none
   int b, head;
-  int row0;        // the unit's first row: decode kernel (token, head) rows, chunk kernel tokens
+  int row0;        // chunk kernel: the unit's first token; decode kernel: 0
   int n, q0;       // the sequence's new tokens and their first row
   int pad[2];
 };
