@@ -723,7 +723,8 @@ struct RowSums {
   uint64_t scale2, negm2;      // pairs of scale, -maximum (FP16: + kWeightUp)
   uint64_t e2[2];              // sums of the FP32 weights (LSE); a NaN among the scores passes into them
   uint64_t r2[2];              // BF16: and of the weights as they are rounded for the product, for the division.
-                               // FP16 weights are off by 2^-12 at most: not worth a sum of their own
+                               // FP16 weights are off by 2^-11 of themselves at most, an eighth of O's own
+                               // rounding: with a sum of their own O's bound would be no smaller
   FA_DEV void begin(float scale, float m) {
     scale2 = pk2(scale, scale);
     const float b = kFp16 ? kWeightUp - m : -m;

@@ -13,14 +13,14 @@
 //     with 8 rows or fewer, the usual case, that halves the products and the
 //     softmax against rows on the M side, whose tiles are 16 high.  (tcgen05
 //     tiles have at least 64 rows on M and their accumulators are a trip through
-//     tensor memory away; with so few rows the warp-level instruction leaves the
-//     tensor cores a quarter busy.)
+//     tensor memory away; with so few rows the warp-level instruction leaves
+//     the tensor cores 8 to 14% busy.)
 //   * Work.  The key blocks of all (sequence, key/value head) units, and a
 //     constant for each unit's start and end, form one line, and thread block c
-//     takes the c-th of `grid` equal stretches of it.  A unit cut
-//     by a border leaves partial results in the workspace, at most two per
-//     thread block, and the combine kernel joins them.  Sequences of any mixture
-//     of lengths load all SMs alike.
+//     takes the c-th of `grid` equal stretches of it.  A unit cut by a border
+//     leaves partial results in the workspace, at most two per thread block, and
+//     the combine kernel joins them.  Sequences of any mixture of lengths load all
+//     SMs alike.
 //   * Pipeline.  One warp looks up the pages of the stretch's blocks, 32 at a
 //     time and on into the next units.  The other warps take the blocks in turn
 //     and each refills by TMA the slots of the ring in shared memory that it
@@ -33,8 +33,8 @@
 //     FP16, which holds every code and which one instruction makes of a pair (to
 //     BF16 it takes five).  The queries become FP16 by a power of two of each
 //     row's own, which loses nothing of note: a row's largest value is below 2^14
-//     then, and what lies below 2^-38 of it is rounded.  The keys' scales go to
-//     the scores in FP32, the values' to the weights.
+//     then, and what lies below 2^-30 of it is rounded, by 2^-38 of it at most.
+//     The keys' scales go to the scores in FP32, the values' to the weights.
 //   * The launch overlaps the end of the kernel before it in the stream: barriers
 //     are set up before griddepcontrol.wait (a call over a few keys, behind another:
 //     13.3 -> 11.0 us on the GPU).
@@ -822,8 +822,10 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
           if (g == 0) {
             st_m[row * kWarps + warp] = m[n][e];
             st_l[row * kWarps + warp] = l[n][e];
-            // FP16 weights (E4M3 pages) are off by 2^-12 at most: their own sum
-            // is not worth keeping
+            // FP16 weights (E4M3 pages) are off by 2^-11 of themselves at most, an
+            // eighth of O's own rounding, and O divided by the sum of the FP32 ones by
+            // 2^-11 of the weighted mean of |v|; with their own sum that bound would
+            // be no smaller (only values all alike would come out as they are)
             st_lr[row * kWarps + warp] = kFp8 ? l[n][e] : ones[n][e];
           }
           float* to = merge + (warp * L::kRound + row) * L::kPitch;
