@@ -26,8 +26,8 @@
  *     arrays are [B, Sn, H, D].  Otherwise (packed): arrays are [Sn, H, D],
  *     sequence b owns rows [cu_seqlens[b], cu_seqlens[b + 1]); cu_seqlens is a
  *     device int32 [B + 1] of non-decreasing offsets, cu_seqlens[0] = 0 and
- *     cu_seqlens[B] <= Sn.  Rows from cu_seqlens[B] on are neither read nor
- *     written.  At most 1024 sequences.
+ *     cu_seqlens[B] <= Sn.  Rows from cu_seqlens[B] on are not written, and what
+ *     they hold has no effect (kernels may load it).  At most 1024 sequences.
  *   - The n new tokens of a sequence are its last ones: token i of them is at
  *     position seq_lens[b] - n + i.  A token whose position is negative (a
  *     padded entry of a batch: seq_lens[b] < n) is not written to the cache
