@@ -244,6 +244,21 @@ def bwd(q, k, v, o, lse, do, causal=False, scale=None, deterministic=False, work
     return dq, dk, dv
 
 
+def _torch_forms(c):
+    """(current stream of a device, allocation and release on the current device
+    in a stream's order), as numbers: torch's own short forms where this release
+    has them in `c`, which save a small call 3 us on the host (1.9 the stream, 1 the
+    allocation), else the public ones."""
+    return (getattr(c, "_cuda_getCurrentRawStream", None)
+            or (lambda device: torch.cuda.current_stream(device).cuda_stream),
+            getattr(c, "_cuda_cudaCachingAllocator_raw_alloc", None)
+            or (lambda size, stream: torch.cuda.caching_allocator_alloc(size, stream=stream)),
+            getattr(c, "_cuda_cudaCachingAllocator_raw_delete", None) or torch.cuda.caching_allocator_delete)
+
+
+_current_stream, _alloc, _free = _torch_forms(torch._C)
+
+
 class _Here:
     """The current stream of the current device, as a context like _OnStream."""
 
@@ -279,7 +294,7 @@ def _on(device, stream):
     # a small call takes a few microseconds on the GPU; entering a context
     # costs as much again on the host, and mostly changes nothing
     if stream is None and device.index == torch.cuda.current_device():
-        return _Here(torch._C._cuda_getCurrentRawStream(device.index))
+        return _Here(_current_stream(device.index))
     return _OnStream(device, stream)
 
 
@@ -513,7 +528,7 @@ def fwd_paged(q, k_pages, v_pages, block_table, seq_lens, causal=True, scale=Non
             # from torch's allocator and back to it in the stream's order, as a
             # tensor would be, whose making takes 2 us more
             size = max(fwd_paged_workspace_size(B, Hq, Hkv, Sn, D, cu_seqlens is not None, max_q), 256)
-            ws = torch._C._cuda_cudaCachingAllocator_raw_alloc(size, s)
+            ws = _alloc(size, s)
         else:
             size, ws = workspace.numel() * workspace.element_size(), workspace.data_ptr()
         try:
@@ -523,7 +538,7 @@ def fwd_paged(q, k_pages, v_pages, block_table, seq_lens, causal=True, scale=Non
                                   seq_lens.data_ptr(), _adr(cu_seqlens), max_q, ws, size, s)
         finally:
             if workspace is None:
-                torch._C._cuda_cudaCachingAllocator_raw_delete(ws)
+                _free(ws)
     if st:
         raise FAError(st, "fa_fwd_paged")
     return out, lse
