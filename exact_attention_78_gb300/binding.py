@@ -498,8 +498,12 @@ def fwd_paged(q, k_pages, v_pages, block_table, seq_lens, causal=True, scale=Non
     [total, Hq, D] with cu_seqlens, over the seq_lens[b] keys that each
     sequence has in the cache, the new tokens' own (written before by
     cache_write) as the last.  max_q: an upper bound of the new tokens of any
-    one sequence (packed; `total` by default, which is right but may choose a
-    slower kernel)."""
+    one sequence (packed).  It chooses the kernel and the workspace, and the
+    lengths themselves are on the device: a packed decoding step should give it
+    (max_q=1).  Its default, `total`, is right for every call, but takes single
+    tokens to the kernel of chunks, with 43 MB of workspace at D = 128 instead
+    of 2.7 (64 tokens over 4096 keys each, 32/8 heads: BF16 192 us instead of
+    163, E4M3 222 instead of 92)."""
     lib = load_library()
     B, device = block_table.shape[0], q.device
     Sn = _new_tokens("q", q, B, cu_seqlens)
