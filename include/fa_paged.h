@@ -43,8 +43,8 @@
  *     bytes outside 17 ... 246 and 255 are made by no write and mean nothing.
  *   - Offsets, lengths and page numbers live on the device, so their rules are
  *     checked there.  Offsets or lengths that break them make fa_fwd_paged()
- *     compute nothing, and fa_cache_write() and fa_cache_read() skip the rows
- *     they concern; a page number outside [0, num_pages) that is needed reads
+ *     compute nothing, and fa_cache_write() and fa_cache_read() skip all rows of
+ *     the sequences they concern; a page number outside [0, num_pages) that is needed reads
  *     as zeros (fa_cache_write() skips the token).  fa_get_device_error()
  *     reports each as FA_ERR_INVALID_ARG.
  */
