@@ -21,5 +21,6 @@ from .binding import (  # noqa: F401
     load_library,
     rope,
     status_string,
+    tree_mask,
     wait_timeout_probe,
 )

@@ -58,6 +58,8 @@ _SIGNATURES = {
     "fa_cache_read": (_i, [_vp] * 6 + [_i] * 7 + [_vp] * 3),
     "fa_fwd_paged_workspace_size": (_sz, [_i] * 7),
     "fa_fwd_paged": (_i, [_vp] * 7 + [_i] * 9 + [_f] + [_vp] * 3 + [_i, _vp, _sz, _vp]),
+    "fa_fwd_paged_tree": (_i, [_vp] * 7 + [_i] * 8 + [_vp, _f] + [_vp] * 3 + [_i, _vp, _sz, _vp]),
+    "fa_tree_mask": (_i, [_vp] * 3 + [_i] * 2 + [_vp, _i, _vp]),
     "fa_diag_exp2": (_i, [_vp, _vp, _vp, ctypes.c_longlong, _vp]),
     "fa_diag_wait_timeout": (_i, [ctypes.c_ulonglong, _vp]),
     "fa_diag_fwd_paged": (_i, [_vp] * 7 + [_i] * 9 + [_f] + [_vp] * 3 + [_i, _vp, _sz, ctypes.c_ulonglong, _vp]),
@@ -492,8 +494,51 @@ def fwd_paged_workspace_size(B, Hq, Hkv, Sn, D, packed=False, max_q=None):
                                                           int(Sn if max_q is None else max_q)))
 
 
+def _most_new(cu_seqlens, rows, max_q):
+    """max_q of the C ABI: dense, the new tokens of every sequence; packed, an upper bound, `rows` by default."""
+    if cu_seqlens is None or max_q is None:
+        max_q = rows
+    if cu_seqlens is not None and not 0 < max_q <= rows:      # (the C interface's ints would wrap)
+        raise ValueError("max_q is %d for %d rows" % (max_q, rows))
+    return max_q
+
+
+def tree_mask(parents, cu_seqlens=None, max_q=None, mask=None, depth=None, stream=None):
+    """Masks and depths of trees of drafted tokens: parents int32 [B, n], or
+    packed [total] with cu_seqlens, a token's parent by its number in its own tree,
+    smaller than the token's own, or -1 where it follows the last token of the cache.
+    Returns (mask, depth): mask int32 [B, n, W] or [total, W], W = ceil(max_q / 32)
+    words of 32 tokens (max_q: an upper bound of a tree's tokens, packed; `total` by
+    default), with the bits of the token itself and its ancestors; depth int32, the
+    number of its ancestors, so that a token's position is that of its tree's first
+    token + depth.  At most 1024 tokens a tree."""
+    lib = load_library()
+    device = parents.device
+    _check_int32("parents", parents, device, 2 if cu_seqlens is None else 1)
+    if cu_seqlens is None:
+        B, Sn = parents.shape
+    else:
+        B, Sn = cu_seqlens.numel() - 1, parents.numel()
+        _check_offsets(cu_seqlens, device, B)
+    most = _most_new(cu_seqlens, Sn, max_q)
+    shape = (*parents.shape, (most + 31) // 32)
+    if mask is not None:
+        _check_out("mask", mask, shape, torch.int32, device)
+    if depth is not None:
+        _check_out("depth", depth, parents.shape, torch.int32, device)
+    with _on(device, stream) as s:
+        if mask is None:
+            mask = torch.empty(shape, dtype=torch.int32, device=device)
+        if depth is None:
+            depth = torch.empty_like(parents)
+        st = lib.fa_tree_mask(parents.data_ptr(), mask.data_ptr(), depth.data_ptr(), B, Sn, _adr(cu_seqlens), most, s)
+    if st:
+        raise FAError(st, "fa_tree_mask")
+    return mask, depth
+
+
 def fwd_paged(q, k_pages, v_pages, block_table, seq_lens, causal=True, scale=None, cu_seqlens=None, max_q=None,
-              k_scale=None, v_scale=None, out=None, lse=None, workspace=None, stream=None):
+              k_scale=None, v_scale=None, out=None, lse=None, workspace=None, stream=None, tree=None):
     """O, LSE = attention of new tokens q, dense [B, n, Hq, D] or packed
     [total, Hq, D] with cu_seqlens, over the seq_lens[b] keys that each
     sequence has in the cache, the new tokens' own (written before by
@@ -503,7 +548,10 @@ def fwd_paged(q, k_pages, v_pages, block_table, seq_lens, causal=True, scale=Non
     (max_q=1).  Its default, `total`, is right for every call, but takes single
     tokens to the kernel of chunks, with 43 MB of workspace at D = 128 instead
     of 2.7 (64 tokens over 4096 keys each, 32/8 heads: BF16 192 us instead of
-    163, E4M3 222 instead of 92)."""
+    163, E4M3 222 instead of 92).  tree: the new
+    tokens are a tree of drafts, and these are their masks (tree_mask's, for the same
+    max_q): each sees the keys before the tree, and those of the tree whose bits are
+    set (in place of the causal mask)."""
     lib = load_library()
     B, device = block_table.shape[0], q.device
     Sn = _new_tokens("q", q, B, cu_seqlens)
@@ -514,9 +562,11 @@ def fwd_paged(q, k_pages, v_pages, block_table, seq_lens, causal=True, scale=Non
     if cu_seqlens is None:
         max_q, lse_shape = Sn, (B, Hq, Sn)
     else:
-        max_q, lse_shape = Sn if max_q is None else max_q, (Hq, Sn)
-        if not 0 < max_q <= Sn:      # (the C interface's ints would wrap)
-            raise ValueError("max_q is %d for %d rows" % (max_q, Sn))
+        max_q, lse_shape = _most_new(cu_seqlens, Sn, max_q), (Hq, Sn)
+    if tree is not None:
+        if not causal:
+            raise ValueError("tree is in place of the causal mask")
+        _check_out("tree", tree, (*q.shape[:-2], (max_q + 31) // 32), torch.int32, device)
     if out is not None:
         _check_out("out", out, q.shape, torch.bfloat16, device)
     if lse is not None:
@@ -536,15 +586,16 @@ def fwd_paged(q, k_pages, v_pages, block_table, seq_lens, causal=True, scale=Non
         else:
             size, ws = workspace.numel() * workspace.element_size(), workspace.data_ptr()
         try:
-            st = lib.fa_fwd_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _adr(k_scale), _adr(v_scale),
-                                  out.data_ptr(), lse.data_ptr(), B, Hq, Hkv, Sn, D, num_pages, page_size, max_pages,
-                                  bool(causal), D ** -0.5 if scale is None else scale, block_table.data_ptr(),
-                                  seq_lens.data_ptr(), _adr(cu_seqlens), max_q, ws, size, s)
+            f, mask = (lib.fa_fwd_paged, bool(causal)) if tree is None else (lib.fa_fwd_paged_tree, tree.data_ptr())
+            st = f(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _adr(k_scale), _adr(v_scale), out.data_ptr(),
+                   lse.data_ptr(), B, Hq, Hkv, Sn, D, num_pages, page_size, max_pages, mask,
+                   D ** -0.5 if scale is None else scale, block_table.data_ptr(), seq_lens.data_ptr(),
+                   _adr(cu_seqlens), max_q, ws, size, s)
         finally:
             if workspace is None:
                 _free(ws)
     if st:
-        raise FAError(st, "fa_fwd_paged")
+        raise FAError(st, "fa_fwd_paged" if tree is None else "fa_fwd_paged_tree")
     return out, lse
 
 

@@ -76,11 +76,12 @@ size_t workspace_size(int B, int Hq, int Hkv, int Sn, int D, bool packed, int ma
   return takes_decode(Hq, Hkv, Sn, D, packed, max_q) ? paged_decode_workspace(D) : paged_chunk_workspace(D);
 }
 
+// `tree`: masks of drafted tokens, or nullptr.
 fa_status fwd_paged(const void* q, const void* k_pages, const void* v_pages, const void* k_scale,
                     const void* v_scale, void* o, float* lse, int B, int Hq, int Hkv, int Sn, int D, int num_pages,
-                    int page_size, int max_pages, int causal, float scale, const int* block_table,
-                    const int* seq_lens, const int* cu_seqlens, int max_q, void* workspace, size_t workspace_bytes,
-                    unsigned long long wait_limit_ns, fa_stream_t stream) {
+                    int page_size, int max_pages, int causal, const uint32_t* tree, float scale,
+                    const int* block_table, const int* seq_lens, const int* cu_seqlens, int max_q, void* workspace,
+                    size_t workspace_bytes, unsigned long long wait_limit_ns, fa_stream_t stream) {
   try {
     PagedAttnLaunch L{};
     if (!q || !o || !lse || !seq_lens || !aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 16))
@@ -90,6 +91,7 @@ fa_status fwd_paged(const void* q, const void* k_pages, const void* v_pages, con
     if (!(scale > 0.0f) || !std::isnormal(scale * kLog2e)) return FA_ERR_INVALID_ARG;
     fa_status st;
     if (!attn_shape_ok(B, Hq, Hkv, Sn, D, cu_seqlens != nullptr, max_q, &st)) return st;
+    if (tree && (cu_seqlens ? max_q : Sn) > kMaxTree) return FA_ERR_UNSUPPORTED;
     st = check_cache(k_pages, v_pages, k_scale, v_scale, B, Hkv, Sn, D, num_pages, page_size, max_pages, block_table,
                      seq_lens, cu_seqlens, &L.p.s);
     if (st != FA_OK) return st;
@@ -105,6 +107,8 @@ fa_status fwd_paged(const void* q, const void* k_pages, const void* v_pages, con
     L.p.group = Hq / Hkv;
     L.p.causal = causal;
     L.p.max_q = cu_seqlens ? max_q : Sn;
+    L.p.tree = tree;
+    L.p.tree_words = tree ? (L.p.max_q + 31) / 32 : 0;
     L.p.scale_log2 = scale * kLog2e;
     L.p.part = static_cast<float*>(workspace);
     L.p.num_ctas = L.num_sms < kMaxCtas ? L.num_sms : kMaxCtas;
@@ -250,8 +254,45 @@ fa_status fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages, 
                        const int* seq_lens, const int* cu_seqlens, int max_q, void* workspace, size_t workspace_bytes,
                        fa_stream_t stream) {
   return fwd_paged(q, k_pages, v_pages, k_scale, v_scale, o, lse, B, Hq, Hkv, Sn, D, num_pages, page_size, max_pages,
-                   causal, scale, block_table, seq_lens, cu_seqlens, max_q, workspace, workspace_bytes,
+                   causal, nullptr, scale, block_table, seq_lens, cu_seqlens, max_q, workspace, workspace_bytes,
                    kDefaultWaitLimitNs, stream);
+}
+
+fa_status fa_fwd_paged_tree(const void* q, const void* k_pages, const void* v_pages, const void* k_scale,
+                            const void* v_scale, void* o, float* lse, int B, int Hq, int Hkv, int Sn, int D,
+                            int num_pages, int page_size, int max_pages, const unsigned* tree, float scale,
+                            const int* block_table, const int* seq_lens, const int* cu_seqlens, int max_q,
+                            void* workspace, size_t workspace_bytes, fa_stream_t stream) {
+  if (!tree || !aligned(tree, 4)) return FA_ERR_INVALID_ARG;
+  return fwd_paged(q, k_pages, v_pages, k_scale, v_scale, o, lse, B, Hq, Hkv, Sn, D, num_pages, page_size, max_pages,
+                   0, tree, scale, block_table, seq_lens, cu_seqlens, max_q, workspace, workspace_bytes,
+                   kDefaultWaitLimitNs, stream);
+}
+
+fa_status fa_tree_mask(const int* parents, unsigned* mask, int* depth, int B, int Sn, const int* cu_seqlens, int max_q,
+                       fa_stream_t stream) {
+  try {
+    if (!parents || !mask || !depth || !aligned(parents, 4) || !aligned(mask, 4) || !aligned(depth, 4) ||
+        !aligned(cu_seqlens, 4))
+      return FA_ERR_INVALID_ARG;
+    if (B <= 0 || Sn <= 0 || (cu_seqlens && (max_q <= 0 || max_q > Sn))) return FA_ERR_INVALID_ARG;
+    TreeParams p{};
+    p.max_q = cu_seqlens ? max_q : Sn;
+    if (p.max_q > kMaxTree || B > kMaxPackedSeqs || Sn > INT32_MAX - 512) return FA_ERR_UNSUPPORTED;
+    int num_sms = 0;
+    fa_status st = device_info(&num_sms);
+    if (st != FA_OK) return st;
+    p.parents = parents;
+    p.mask = mask;
+    p.depth = depth;
+    p.cu = cu_seqlens;
+    p.B = B;
+    p.Sn = Sn;
+    p.words = (p.max_q + 31) / 32;
+    return launch_tree_mask(p, reinterpret_cast<cudaStream_t>(stream));
+  } catch (...) {
+    return FA_ERR_CUDA;
+  }
 }
 
 fa_status fa_diag_fwd_paged(const void* q, const void* k_pages, const void* v_pages, const void* k_scale,
@@ -262,8 +303,8 @@ fa_status fa_diag_fwd_paged(const void* q, const void* k_pages, const void* v_pa
                             fa_stream_t stream) {
   if (wait_limit_ns == 0 || wait_limit_ns > 10000000000ull) return FA_ERR_INVALID_ARG;
   return fwd_paged(q, k_pages, v_pages, k_scale, v_scale, o, lse, B, Hq, Hkv, Sn, D, num_pages, page_size, max_pages,
-                   causal, scale, block_table, seq_lens, cu_seqlens, max_q, workspace, workspace_bytes, wait_limit_ns,
-                   stream);
+                   causal, nullptr, scale, block_table, seq_lens, cu_seqlens, max_q, workspace, workspace_bytes,
+                   wait_limit_ns, stream);
 }
 
 }  // extern "C"

@@ -1,6 +1,6 @@
 // Attention of chunks of new tokens over a paged cache, on tcgen05.
 //
-//   O = softmax(scale q K^T [+ causal mask]) V, LSE, per row of q.
+//   O = softmax(scale q K^T [+ causal or tree mask]) V, LSE, per row of q.
 //
 // A tile is up to 128 rows of (new token, query head of one key/value head's
 // group), so grouped heads share the key and value tiles they read; a unit is
@@ -710,6 +710,24 @@ FA_DEV void mask_scores(uint32_t tm_s, int lim) {
   }
   tmem_st_wait();
 }
+// The same for a drafted token: the columns whose bits in its mask `row` are zero;
+// column 0 is number `first` of the n of its tree.
+FA_DEV void mask_tree(uint32_t tm_s, const uint32_t* row, int first, int n) {
+#pragma unroll 1
+  for (int c = max(0, -first) / 32 * 32; c < kBN; c += 32) {
+    const uint32_t bits = paged::tree_bits(row, first + c, n);
+    __syncwarp();
+    uint32_t x[32];
+    tmem_ld32(tm_s + c, x);
+    tmem_ld_wait();
+    tmem_ld_fence(x);
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (!(bits >> i & 1)) x[i] = __float_as_uint(-INFINITY);
+    tmem_st32(tm_s + c, x);
+  }
+  tmem_st_wait();
+}
 FA_DEV float max32(const uint32_t (&x)[32]) {
   float m = __uint_as_float(x[0]);
 #pragma unroll
@@ -797,7 +815,7 @@ FA_DEV int narrow_row(const Shared<D, true>& sh, int t, int r) {
 // block's 128 scores in registers and everything unrolled, the warps of the
 // other roles found their code pushed out of the instruction cache each time
 // (chunk of 512 tokens over 32K keys, 76 heads: 489 us, rolled 446 us).
-template <int D, bool kFp8>
+template <int D, bool kFp8, bool kTree>
 __device__ void softmax_role(const int t, const Shared<D, kFp8>& sh, const uint32_t tmem, const PagedAttnParams& p) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int wq = warp & 3;
@@ -830,11 +848,14 @@ __device__ void softmax_role(const int t, const Shared<D, kFp8>& sh, const uint3
     idle = nt == 0;
     if (idle) continue;
     const int tok = w.tok0 + t * tt;
-    const int lim_first = p.causal ? w.L - w.n + tok + 1 : w.L;                  // of the tile's first row
+    const int past = w.L - w.n;
+    const int lim_first = kTree ? past : p.causal ? past + tok + 1 : w.L;        // of the tile's first row
     const int lim_row = p.causal ? min(w.L, lim_first + my_tok) : w.L;
     // rows of the tile that are no token's hold anything: they must not cause
     // rescaling
     const bool live = my_tok < tt && tok + my_tok < w.n;
+    const uint32_t* drafted = nullptr;       // a padded token sees nothing
+    if (kTree && live && past + tok + my_tok >= 0) drafted = p.tree + (size_t)(w.q0 + tok + my_tok) * p.tree_words;
     float m_run = -INFINITY, l_run = 0.0f, lr_run = 0.0f;
     RowSums<kFp8> sums;
     // The new running maximum from the block's; returns the factor for what
@@ -882,7 +903,12 @@ __device__ void softmax_role(const int t, const Shared<D, kFp8>& sh, const uint3
       const int lim = lim_row - kv0;            // columns >= lim are masked
       bool rescaled;
       float factor, m_blk, e, r;
-      if (need_mask) mask_scores(tm_s, lim);
+      if (need_mask) {
+        if (kTree)
+          mask_tree(tm_s, drafted, kv0 - past, w.n);
+        else
+          mask_scores(tm_s, lim);
+      }
       uint32_t xa[32], xb[32], pk[16];
       m_blk = -INFINITY;
       tmem_ld32(tm_s, xa);
@@ -1212,7 +1238,7 @@ __device__ void mma_role(const Shared<D, kFp8>& sh, const uint32_t tmem, const P
   }
 }
 
-template <int D, bool kFp8>
+template <int D, bool kFp8, bool kTree>
 __global__ void __launch_bounds__(Layout<D, kFp8>::kThreads, 1)
     chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const PagedAttnParams p) {
@@ -1272,7 +1298,7 @@ __global__ void __launch_bounds__(Layout<D, kFp8>::kThreads, 1)
 
   if (warp < 8) {
     reg_alloc<kFp8 ? 128 : 192>();
-    softmax_role<D, kFp8>(warp / 4, sh, tmem, p);
+    softmax_role<D, kFp8, kTree>(warp / 4, sh, tmem, p);
   } else if (warp < 12) {
     reg_dealloc<kFp8 ? 72 : 80>();
     correction_role<D, kFp8>(sh, tmem, p);
@@ -1412,7 +1438,7 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const PagedAttnPa
   }
 }
 
-template <int D, bool kFp8>
+template <int D, bool kFp8, bool kTree>
 fa_status launch_inst(const PagedAttnLaunch& L, cudaStream_t stream) {
   using Lay = Layout<D, kFp8>;
   const PagedSeqs& s = L.p.s;
@@ -1425,7 +1451,7 @@ fa_status launch_inst(const PagedAttnLaunch& L, cudaStream_t stream) {
   if ((st = make_tmap_rows_group(&tq, L.p.q, rows, L.p.Hq, D, L.p.group, kBM / L.p.group)) != FA_OK) return st;
   if ((st = make_tmap_pages(&tk, L.k_pages, page_heads, page_size, D, kFp8, box)) != FA_OK) return st;
   if ((st = make_tmap_pages(&tv, L.v_pages, page_heads, page_size, D, kFp8, box)) != FA_OK) return st;
-  auto kern = chunk_kernel<D, kFp8>;
+  auto kern = chunk_kernel<D, kFp8, kTree>;
   if ((st = prepare_kernel(reinterpret_cast<const void*>(kern), Lay::kBytes)) != FA_OK) return st;
   // (Not overlapped with the kernel before it, unlike the decode kernel: small calls
   // would gain 2 us, but blocks then land on whichever SMs are free, away from
@@ -1437,13 +1463,18 @@ fa_status launch_inst(const PagedAttnLaunch& L, cudaStream_t stream) {
   return launch_overlapped(combine_kernel<D>, dim3(ctas - 1, 2 * kBM / kJoinRows), kJoinThreads, 0, stream, L.p);
 }
 
+template <bool kTree>
+fa_status launch_pages(const PagedAttnLaunch& L, cudaStream_t stream) {
+  if (L.D == 128) return L.fp8 ? launch_inst<128, true, kTree>(L, stream) : launch_inst<128, false, kTree>(L, stream);
+  return L.fp8 ? launch_inst<64, true, kTree>(L, stream) : launch_inst<64, false, kTree>(L, stream);
+}
+
 }  // namespace pchunk
 
 size_t paged_chunk_workspace(int D) { return D == 128 ? pchunk::Part<128>::bytes() : pchunk::Part<64>::bytes(); }
 
 fa_status launch_paged_chunk(const PagedAttnLaunch& L, cudaStream_t stream) {
-  if (L.D == 128) return L.fp8 ? pchunk::launch_inst<128, true>(L, stream) : pchunk::launch_inst<128, false>(L, stream);
-  return L.fp8 ? pchunk::launch_inst<64, true>(L, stream) : pchunk::launch_inst<64, false>(L, stream);
+  return L.p.tree ? pchunk::launch_pages<true>(L, stream) : pchunk::launch_pages<false>(L, stream);
 }
 
 fa_status paged_chunk_take_device_error() {

@@ -1,6 +1,6 @@
 // Attention of a few new tokens over a paged cache (a decoding step).
 //
-//   O = softmax(scale q K^T [+ causal mask]) V, LSE, per row of q.
+//   O = softmax(scale q K^T [+ causal or tree mask]) V, LSE, per row of q.
 //
 // A step reads every sequence's keys and values once and computes little with
 // them, so HBM bounds it: the design keeps loads in flight and splits the keys
@@ -332,7 +332,10 @@ FA_DEV void merge_rows(const PagedAttnParams& p, const Walk<Layout<D, kFp8, kTil
   }
 }
 
-template <int D, bool kFp8, int kTiles>
+// kTree: the new tokens are drafted ones, each of which sees the keys before them and
+// those of them that its mask names.  A mask is one word: a sequence has no more
+// than 32 rows here.
+template <int D, bool kFp8, int kTiles, bool kTree>
 __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
     decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const PagedAttnParams p) {
@@ -568,7 +571,8 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
     const int rows = at.rows(p);
     const int vis = at.visible();
     // rows 8 n + 2 c + e, whose scores this lane gets:
-    int row_lim[kTiles][2];          // keys that they see
+    int row_lim[kTiles][2];          // keys that they see (a tree's: the keys before it)
+    uint32_t row_bits[kTiles][2];    // and of the tree
     float row_scale[kTiles][2];      // what their scores are multiplied by, for log2 units
 #pragma unroll
     for (int n = 0; n < kTiles; ++n) {
@@ -596,7 +600,13 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
       for (int e = 0; e < 2; ++e) {
         row_scale[n][e] = kFp8 ? __shfl_sync(0xffffffffu, scale, (2 * c + e) * 4) : scale;
         const int row = 8 * n + 2 * c + e;
-        row_lim[n][e] = row >= rows ? 0 : p.causal ? at.s.L - at.s.n + token_of(row) + 1 : at.s.L;
+        if (kTree) {
+          const int past = at.s.L - at.s.n, t = token_of(row);
+          row_lim[n][e] = past;
+          row_bits[n][e] = row >= rows || past + t < 0 ? 0u : paged::tree_bits(p.tree + at.s.q0 + t, 0, at.s.n);
+        } else {
+          row_lim[n][e] = row >= rows ? 0 : p.causal ? at.s.L - at.s.n + token_of(row) + 1 : at.s.L;
+        }
       }
     }
     // O^T: columns of V on the rows, rows of Q on the columns (2 c, 2 c + 1 here)
@@ -688,7 +698,7 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
       const int n_left = at.s.L - key0;
       const bool ragged = n_left < kKeys;
       // a block that the first token sees whole needs no mask
-      const bool masked = key0 + kKeys > (p.causal ? at.s.L - at.s.n + 1 : at.s.L);
+      const bool masked = key0 + kKeys > (kTree ? at.s.L - at.s.n : p.causal ? at.s.L - at.s.n + 1 : at.s.L);
       uint32_t pb[kTiles][kGroups][2];        // P^T as B fragments
 #pragma unroll
       for (int n = 0; n < kTiles; ++n) {
@@ -699,7 +709,8 @@ __global__ void __launch_bounds__(Layout<D, kFp8, kTiles>::kThreads, 1)
           for (int e = 0; e < 4; ++e) {
             float x = s[n][j][e] * row_scale[n][e & 1];
             if (kFp8) x *= fac[j][e >> 1].x;
-            if (masked && key0 + 16 * j + 8 * (e >> 1) + g >= row_lim[n][e & 1]) x = -INFINITY;
+            const int behind = key0 + 16 * j + 8 * (e >> 1) + g - row_lim[n][e & 1];
+            if (masked && behind >= 0 && !(kTree && behind < 32 && (row_bits[n][e & 1] >> behind & 1))) x = -INFINITY;
             s[n][j][e] = x;
           }
           mx[0] = max3(mx[0], s[n][j][0], s[n][j][2]);
@@ -929,7 +940,7 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const PagedAttnPa
       make_uint2(pack_bf16x2(y.x * inv[r], y.y * inv[r]), pack_bf16x2(y.z * inv[r], y.w * inv[r]));
 }
 
-template <int D, bool kFp8, int kTiles>
+template <int D, bool kFp8, int kTiles, bool kTree>
 fa_status launch_inst(const PagedAttnLaunch& L, cudaStream_t stream) {
   using Lay = Layout<D, kFp8, kTiles>;
   const int page_size = 1 << L.p.s.page_shift;
@@ -939,7 +950,7 @@ fa_status launch_inst(const PagedAttnLaunch& L, cudaStream_t stream) {
   fa_status st;
   if ((st = make_tmap_pages(&tk, L.k_pages, page_heads, page_size, D, kFp8, box)) != FA_OK) return st;
   if ((st = make_tmap_pages(&tv, L.v_pages, page_heads, page_size, D, kFp8, box)) != FA_OK) return st;
-  auto kern = decode_kernel<D, kFp8, kTiles>;
+  auto kern = decode_kernel<D, kFp8, kTiles, kTree>;
   if ((st = prepare_kernel(reinterpret_cast<const void*>(kern), Lay::kBytes)) != FA_OK) return st;
   const int ctas = L.p.num_ctas;
   if ((st = launch_overlapped(kern, dim3(ctas), Lay::kThreads, Lay::kBytes, stream, tk, tv, L.p)) != FA_OK) return st;
@@ -949,14 +960,20 @@ fa_status launch_inst(const PagedAttnLaunch& L, cudaStream_t stream) {
 }
 
 // As few tiles of 8 rows as hold a sequence's rows.
-template <int D, bool kFp8>
+template <int D, bool kFp8, bool kTree>
 fa_status launch_tiles(const PagedAttnLaunch& L, cudaStream_t stream) {
   const long long rows = (long long)L.p.max_q * L.p.group;
-  if (rows <= 8) return launch_inst<D, kFp8, 1>(L, stream);
+  if (rows <= 8) return launch_inst<D, kFp8, 1, kTree>(L, stream);
   if constexpr (kDecodeRows(D) > 16) {
-    if (rows > 16) return launch_inst<D, kFp8, 4>(L, stream);
+    if (rows > 16) return launch_inst<D, kFp8, 4, kTree>(L, stream);
   }
-  return launch_inst<D, kFp8, 2>(L, stream);
+  return launch_inst<D, kFp8, 2, kTree>(L, stream);
+}
+
+template <bool kTree>
+fa_status launch_pages(const PagedAttnLaunch& L, cudaStream_t stream) {
+  if (L.D == 128) return L.fp8 ? launch_tiles<128, true, kTree>(L, stream) : launch_tiles<128, false, kTree>(L, stream);
+  return L.fp8 ? launch_tiles<64, true, kTree>(L, stream) : launch_tiles<64, false, kTree>(L, stream);
 }
 
 }  // namespace pdec
@@ -966,8 +983,7 @@ size_t paged_decode_workspace(int D) {
 }
 
 fa_status launch_paged_decode(const PagedAttnLaunch& L, cudaStream_t stream) {
-  if (L.D == 128) return L.fp8 ? pdec::launch_tiles<128, true>(L, stream) : pdec::launch_tiles<128, false>(L, stream);
-  return L.fp8 ? pdec::launch_tiles<64, true>(L, stream) : pdec::launch_tiles<64, false>(L, stream);
+  return L.p.tree ? pdec::launch_pages<true>(L, stream) : pdec::launch_pages<false>(L, stream);
 }
 
 fa_status paged_decode_take_device_error() {

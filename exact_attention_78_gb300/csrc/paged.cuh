@@ -152,6 +152,17 @@ FA_DEV bool prefix_sequences(const PagedSeqs& s, int max_new, F work, long long*
   return ok;
 }
 
+// Bits o ... o + 31 of a drafted token's mask `row` in a tree of n (nullptr: sees
+// none of the tree), the keys before the tree, o < 0, as ones.
+FA_DEV uint32_t tree_bits(const uint32_t* __restrict__ row, int o, int n) {
+  const int q = o >> 5, r = o & 31;
+  const uint32_t lo = q < 0 ? 0xFFFFFFFFu : row && 32 * q < n ? row[q] : 0u;
+  const uint32_t hi = r && row && 32 * (q + 1) < n ? row[q + 1] : 0u;      // (o > -32: q + 1 >= 0)
+  const uint32_t bits = __funnelshift_r(lo, hi, r);
+  const int left = n - o;                                                  // a row's last bits mean nothing
+  return left >= 32 ? bits : left <= 0 ? 0u : bits & ((1u << left) - 1u);
+}
+
 // a / b for a >= 0, b > 0: 64-bit division takes some hundred instructions, and
 // the numbers here mostly fit 32 bits.
 FA_DEV long long div64(long long a, long long b) {

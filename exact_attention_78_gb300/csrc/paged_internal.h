@@ -50,6 +50,17 @@ struct RopeParams {
   unsigned char axis[64];
 };
 
+// Most drafted tokens of a sequence.
+constexpr int kMaxTree = FA_MAX_TREE;
+
+struct TreeParams {
+  const int* parents;
+  uint32_t* mask;           // `words` of each token
+  int* depth;
+  const int* cu;            // [B + 1] or nullptr: Sn tokens each
+  int B, Sn, max_q, words;  // packed: Sn = rows of the packed arrays
+};
+
 struct PagedAttnParams {
   PagedSeqs s;
   const void* q;
@@ -59,6 +70,8 @@ struct PagedAttnParams {
   const uint8_t* v_scale;
   int Hq, group;            // group = Hq / Hkv
   int causal;
+  const uint32_t* tree;     // masks of drafted tokens, tree_words of each new token; or nullptr
+  int tree_words;
   int max_q;
   float scale_log2;         // scale * log2(e)
   float* part;              // workspace: partial results
@@ -117,12 +130,14 @@ fa_status launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, int sm
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
+fa_status launch_tree_mask(const TreeParams& p, cudaStream_t stream);
 fa_status launch_rope(const RopeParams& p, int num_sms, cudaStream_t stream);
 fa_status launch_cache_write(const CacheParams& p, int num_sms, cudaStream_t stream);
 fa_status launch_cache_read(const CacheParams& p, int num_sms, cudaStream_t stream);
 fa_status launch_paged_decode(const PagedAttnLaunch& L, cudaStream_t stream);
 fa_status launch_paged_chunk(const PagedAttnLaunch& L, cudaStream_t stream);
 
+fa_status tree_take_device_error();
 fa_status cache_take_device_error();
 fa_status paged_decode_take_device_error();
 fa_status paged_chunk_take_device_error();

@@ -4,7 +4,9 @@
  *
  * The serving path: fa_rope() turns the new queries and keys, fa_cache_write()
  * puts the new keys and values into the pages of a cache, fa_fwd_paged()
- * attends from the new queries to everything a sequence has in its pages, and
+ * attends from the new queries to everything a sequence has in its pages
+ * (fa_fwd_paged_tree() where the new tokens are a tree of drafts, whose masks
+ * fa_tree_mask() makes), and
  * fa_cache_read() copies pages back into packed rows (the layout of fa_fwd()
  * and fa_bwd() with cu_seqlens).  For training, fa_rope() with `inverse` is
  * the gradient of fa_rope().
@@ -150,6 +152,46 @@ FA_API fa_status fa_fwd_paged(const void* q, const void* k_pages, const void* v_
                               int num_pages, int page_size, int max_pages, int causal, float scale,
                               const int* block_table, const int* seq_lens, const int* cu_seqlens, int max_q,
                               void* workspace, size_t workspace_bytes, fa_stream_t stream);
+
+/* Most drafted tokens of one sequence. */
+#define FA_MAX_TREE 1024
+
+/*
+ * Masks and depths of trees of drafted tokens (speculative decoding), dense
+ * (cu_seqlens == NULL: B trees of Sn tokens) or packed (Sn rows, offsets and
+ * max_q as fa_fwd_paged() has them).  At most FA_MAX_TREE tokens a tree.
+ *   parents      device int32 [B, Sn] or [Sn]: the number, in its own tree, of
+ *                the token that a token follows, or -1 where it follows the last
+ *                token of the cache; smaller than its own number.  A parent that
+ *                is not is reported on the device, and counts as -1.
+ *   mask         device [B, Sn, W] or [Sn, W], W = ceil(max_q / 32) (dense: of
+ *                Sn): bit j % 32 of word j / 32 of token i is set where j is i or
+ *                an ancestor of i
+ *   depth        device int32 [B, Sn] or [Sn]: how many ancestors a token has; its
+ *                position is that of the last token of the cache + 1 + depth
+ * Rows from cu_seqlens[B] on, and those of a sequence whose offsets break the
+ * rules, are not written.
+ */
+FA_API fa_status fa_tree_mask(const int* parents, unsigned* mask, int* depth, int B, int Sn, const int* cu_seqlens,
+                              int max_q, fa_stream_t stream);
+
+/*
+ * fa_fwd_paged() where the new tokens of a sequence are a tree of drafts, whose
+ * keys and values fa_cache_write() has put behind the sequence's others, in the
+ * tokens' order.  New token i of n sees the seq_lens[b] - n keys before the tree,
+ * and new token j of the tree where bit j of its mask is set.  Arguments are those
+ * of fa_fwd_paged(), but
+ *   tree         device, W words for each new token as fa_tree_mask() lays them
+ *                out (any bits will do: a row may be empty; bits from n on mean
+ *                nothing), in place of the causal mask
+ *   max_q        (dense: Sn) at most FA_MAX_TREE
+ * A padded token (its position seq_lens[b] - n + i is negative) sees no key.
+ */
+FA_API fa_status fa_fwd_paged_tree(const void* q, const void* k_pages, const void* v_pages, const void* k_scale,
+                                   const void* v_scale, void* o, float* lse, int B, int Hq, int Hkv, int Sn, int D,
+                                   int num_pages, int page_size, int max_pages, const unsigned* tree, float scale,
+                                   const int* block_table, const int* seq_lens, const int* cu_seqlens, int max_q,
+                                   void* workspace, size_t workspace_bytes, fa_stream_t stream);
 
 #ifdef __cplusplus
 }

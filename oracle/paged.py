@@ -112,3 +112,65 @@ def rope(x, positions, sections, base, restart=False, interleaved=False, inverse
             y[..., q] = x[..., q] * c + x[..., p] * s
             i += 1
     return y
+
+
+# ------------------------------------------- drafted trees, sums, eviction --
+
+def tree_ancestors(parents):
+    """[n, n] truth values, token i's own and its ancestors', and the depths."""
+    n = len(parents)
+    sees = np.zeros((n, n), dtype=bool)
+    for i in range(n):
+        j = i
+        while j >= 0:
+            sees[i, j] = True
+            j = int(parents[j])
+    return sees, sees.sum(1) - 1
+
+
+def pack_bits(sees, words):
+    """Rows of truth values as int32 words of 32."""
+    n, m = sees.shape
+    out = np.zeros((n, words), dtype=np.uint32)
+    for j in range(m):
+        out[:, j // 32] |= sees[:, j].astype(np.uint32) << np.uint32(j % 32)
+    return out.view(np.int32)
+
+
+def tree_sees(bits, L):
+    """[n, L]: which keys a sequence's n drafted tokens see, by their masks' truth values [n, >= n]."""
+    n = bits.shape[0]
+    sees = np.zeros((n, L), dtype=bool)
+    past = L - n
+    for i in range(n):
+        if past + i < 0:                # padded
+            continue
+        sees[i, :max(0, past)] = True
+        for j in range(n):
+            if past + j >= 0:
+                sees[i, past + j] = bits[i, j]
+    return sees
+
+
+def causal_sees(n, L, causal):
+    """[n, L]: which keys the last n tokens of a sequence of L see."""
+    i, j = np.arange(n)[:, None], np.arange(L)[None, :]
+    return (j <= L - n + i) if causal else np.ones((n, L), dtype=bool)
+
+
+def attention_of(q, k, v, sees, scale):
+    """attention() with a mask [n, L] of truth values."""
+    n, Hq, D = q.shape
+    o, a = np.zeros((n, Hq, D)), np.zeros((n, Hq, D))
+    lse = np.full((Hq, n), -np.inf)
+    for h in range(Hq):
+        kh, vh = k[:, h // (Hq // k.shape[1])], v[:, h // (Hq // v.shape[1])]
+        for i in range(n):
+            if not sees[i].any():
+                continue
+            s = kh[sees[i]] @ q[i, h] * scale
+            p = np.exp(s - s.max())
+            o[i, h] = p @ vh[sees[i]] / p.sum()
+            a[i, h] = p @ np.abs(vh[sees[i]]) / p.sum()
+            lse[h, i] = s.max() + np.log(p.sum())
+    return o, lse, a
