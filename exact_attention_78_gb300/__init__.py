@@ -10,7 +10,9 @@ from .binding import (  # noqa: F401
     FAError,
     bwd,
     bwd_workspace_size,
+    cache_keep,
     cache_read,
+    cache_select,
     cache_write,
     exp2_probe,
     fwd,

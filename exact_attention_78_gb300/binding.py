@@ -59,6 +59,8 @@ _SIGNATURES = {
     "fa_fwd_paged_workspace_size": (_sz, [_i] * 7),
     "fa_fwd_paged": (_i, [_vp] * 7 + [_i] * 9 + [_f] + [_vp] * 3 + [_i, _vp, _sz, _vp]),
     "fa_fwd_paged_tree": (_i, [_vp] * 7 + [_i] * 8 + [_vp, _f] + [_vp] * 3 + [_i, _vp, _sz, _vp]),
+    "fa_cache_select": (_i, [_vp] * 3 + [_i] * 8 + [_vp] * 3),
+    "fa_cache_keep": (_i, [_vp] * 5 + [_i] * 6 + [_vp] * 2 + [_i] * 2 + [_vp] * 3),
     "fa_tree_mask": (_i, [_vp] * 3 + [_i] * 2 + [_vp, _i, _vp]),
     "fa_diag_exp2": (_i, [_vp, _vp, _vp, ctypes.c_longlong, _vp]),
     "fa_diag_wait_timeout": (_i, [ctypes.c_ulonglong, _vp]),
@@ -597,6 +599,78 @@ def fwd_paged(q, k_pages, v_pages, block_table, seq_lens, causal=True, scale=Non
     if st:
         raise FAError(st, "fa_fwd_paged" if tree is None else "fa_fwd_paged_tree")
     return out, lse
+
+
+def _check_sums(sums, device, shape=None):
+    """Sums of attention weights, beside pages [num_pages, Hkv, page_size, D] where there are some."""
+    if not (sums.dtype is torch.float32 and sums.is_cuda and sums.device == device and sums.is_contiguous()
+            and (len(sums.shape) == 3 if shape is None else sums.shape == shape[:3])):
+        _bad("sums", "a contiguous CUDA float32 tensor of shape %s" % (
+            "[num_pages, Hkv, page_size]" if shape is None else (tuple(shape[:3]),)), device)
+
+
+def cache_select(sums, block_table, seq_lens, keep, first=0, recent=0, index=None, kept=None, stream=None):
+    """Which tokens of its sequence each head keeps: the first `first`, the last
+    `recent`, and the others with the largest sums (float32 [num_pages, Hkv,
+    page_size], as cache_weights adds them up), `keep` in all.  Returns (index int32
+    [B, Hkv, keep], ascending, -1 behind the last; kept int32 [B] = min(seq_lens,
+    keep)): what cache_keep takes, after which `kept` are the sequences' lengths."""
+    lib = load_library()
+    device, B = sums.device, block_table.shape[0]
+    _check_sums(sums, device)
+    _check_int32("block_table", block_table, device, 2)
+    _check_seq_lens(seq_lens, device, B)
+    num_pages, Hkv, page_size = sums.shape
+    if not (0 < keep <= 2 ** 30 and first >= 0 and recent >= 0 and first + recent <= keep):
+        raise ValueError("keep %d tokens, %d first and %d last ones" % (keep, first, recent))
+    if index is not None:
+        _check_out("index", index, (B, Hkv, keep), torch.int32, device)
+    if kept is not None:
+        _check_out("kept", kept, (B,), torch.int32, device)
+    with _on(device, stream) as s:
+        if index is None:
+            index = torch.empty((B, Hkv, keep), dtype=torch.int32, device=device)
+        if kept is None:
+            kept = torch.empty((B,), dtype=torch.int32, device=device)
+        st = lib.fa_cache_select(sums.data_ptr(), index.data_ptr(), kept.data_ptr(), B, Hkv, num_pages, page_size,
+                                 block_table.shape[1], keep, first, recent, block_table.data_ptr(),
+                                 seq_lens.data_ptr(), s)
+    if st:
+        raise FAError(st, "fa_cache_select")
+    return index, kept
+
+
+def cache_keep(k_pages, v_pages, block_table, index, counts, start=None, k_scale=None, v_scale=None, sums=None,
+               stream=None):
+    """Moves rows of the cache together, in place: token index[b, h, i] of sequence b
+    and head h goes to slot start[b] + i (start: int32 [B], 0 by default), for i <
+    counts[b], its key, its value, their scales and, where `sums` are given, its sum
+    alike.  index: int32 [B, Hkv, n], or [B, 1, n] for all heads alike, each list
+    ascending; cache_select's after an eviction, the accepted drafts' tokens after a
+    tree, with `start` the number of tokens before it."""
+    lib = load_library()
+    device, B = k_pages.device, block_table.shape[0]
+    if k_pages.dim() != 4:
+        raise ValueError("k_pages is [num_pages, Hkv, page_size, D]")
+    D = k_pages.shape[3]
+    num_pages, Hkv, page_size, max_pages = _cache_args(None, D, device, k_pages, v_pages, k_scale, v_scale, block_table)
+    _check_int32("index", index, device, 3)
+    _, heads, most = index.shape
+    if index.shape[0] != B or heads not in (1, Hkv):
+        raise ValueError("index is %s for %d sequences and %d heads" % (tuple(index.shape), B, Hkv))
+    _check_int32("counts", counts, device, 1)
+    if start is not None:
+        _check_int32("start", start, device, 1)
+    if counts.numel() != B or (start is not None and start.numel() != B):
+        raise ValueError("counts and start have one entry for each of %d sequences" % B)
+    if sums is not None:
+        _check_sums(sums, device, k_pages.shape)
+    with _on(device, stream) as s:
+        st = lib.fa_cache_keep(k_pages.data_ptr(), v_pages.data_ptr(), _adr(k_scale), _adr(v_scale), _adr(sums), B, Hkv,
+                               D, num_pages, page_size, max_pages, block_table.data_ptr(), index.data_ptr(), heads, most,
+                               counts.data_ptr(), _adr(start), s)
+    if st:
+        raise FAError(st, "fa_cache_keep")
 
 
 def get_device_error(stream=None):

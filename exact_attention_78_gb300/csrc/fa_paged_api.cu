@@ -295,6 +295,64 @@ fa_status fa_tree_mask(const int* parents, unsigned* mask, int* depth, int B, in
   }
 }
 
+fa_status fa_cache_select(const float* sums, int* index, int* kept, int B, int Hkv, int num_pages, int page_size,
+                          int max_pages, int keep, int first, int recent, const int* block_table, const int* seq_lens,
+                          fa_stream_t stream) {
+  try {
+    SelectParams p{};
+    if (!sums || !index || !kept || !seq_lens || !aligned(sums, 16) || !aligned(index, 4) || !aligned(kept, 4))
+      return FA_ERR_INVALID_ARG;
+    if (keep <= 0 || first < 0 || recent < 0 || first > keep || recent > keep - first) return FA_ERR_INVALID_ARG;
+    // (sums have no pages of their own: the checks of the table and the sizes are the pages')
+    fa_status st = check_cache(sums, sums, nullptr, nullptr, B, Hkv, 1, 64, num_pages, page_size, max_pages, block_table,
+                               seq_lens, nullptr, &p.s);
+    if (st != FA_OK) return st;
+    if (keep > 1 << 30) return FA_ERR_UNSUPPORTED;
+    int num_sms = 0;
+    if ((st = device_info(&num_sms)) != FA_OK) return st;
+    p.sums = sums;
+    p.index = index;
+    p.kept = kept;
+    p.keep = keep;
+    p.first = first;
+    p.recent = recent;
+    return launch_cache_select(p, num_sms, reinterpret_cast<cudaStream_t>(stream));
+  } catch (...) {
+    return FA_ERR_CUDA;
+  }
+}
+
+fa_status fa_cache_keep(void* k_pages, void* v_pages, void* k_scale, void* v_scale, float* sums, int B, int Hkv, int D,
+                        int num_pages, int page_size, int max_pages, const int* block_table, const int* index,
+                        int heads, int most, const int* counts, const int* start, fa_stream_t stream) {
+  try {
+    KeepParams p{};
+    if (!index || !counts || !aligned(sums, 16) || !aligned(index, 4) || !aligned(counts, 4) || !aligned(start, 4))
+      return FA_ERR_INVALID_ARG;
+    if (most <= 0 || (heads != 1 && heads != Hkv)) return FA_ERR_INVALID_ARG;
+    fa_status st = check_cache(k_pages, v_pages, k_scale, v_scale, B, Hkv, 1, D, num_pages, page_size, max_pages,
+                               block_table, nullptr, nullptr, &p.s);
+    if (st != FA_OK) return st;
+    if (most > 1 << 30) return FA_ERR_UNSUPPORTED;
+    int num_sms = 0;
+    if ((st = device_info(&num_sms)) != FA_OK) return st;
+    p.k_pages = k_pages;
+    p.v_pages = v_pages;
+    p.k_scale = static_cast<uint8_t*>(k_scale);
+    p.v_scale = static_cast<uint8_t*>(v_scale);
+    p.sums = sums;
+    p.index = index;
+    p.counts = counts;
+    p.start = start;
+    p.D = D;
+    p.heads = heads;
+    p.most = most;
+    return launch_cache_keep(p, num_sms, reinterpret_cast<cudaStream_t>(stream));
+  } catch (...) {
+    return FA_ERR_CUDA;
+  }
+}
+
 fa_status fa_diag_fwd_paged(const void* q, const void* k_pages, const void* v_pages, const void* k_scale,
                             const void* v_scale, void* o, float* lse, int B, int Hq, int Hkv, int Sn, int D,
                             int num_pages, int page_size, int max_pages, int causal, float scale,

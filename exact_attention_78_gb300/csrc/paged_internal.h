@@ -61,6 +61,28 @@ struct TreeParams {
   int B, Sn, max_q, words;  // packed: Sn = rows of the packed arrays
 };
 
+struct SelectParams {
+  PagedSeqs s;              // cu = nullptr
+  const float* sums;        // [num_pages, Hkv, page_size]
+  int* index;               // [B, Hkv, keep]
+  int* kept;                // [B]
+  int keep, first, recent;
+  int cached;               // tokens of a thread block in shared memory
+};
+
+struct KeepParams {
+  PagedSeqs s;              // seq_lens = cu = nullptr
+  void* k_pages;
+  void* v_pages;
+  uint8_t* k_scale;         // nullptr: BF16 pages
+  uint8_t* v_scale;
+  float* sums;              // or nullptr
+  const int* index;         // [B, heads, most]
+  const int* counts;        // [B]
+  const int* start;         // [B] or nullptr: 0
+  int D, heads, most;       // heads: Hkv or 1
+};
+
 struct PagedAttnParams {
   PagedSeqs s;
   const void* q;
@@ -130,6 +152,8 @@ fa_status launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, int sm
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
+fa_status launch_cache_select(const SelectParams& p, int num_sms, cudaStream_t stream);
+fa_status launch_cache_keep(const KeepParams& p, int num_sms, cudaStream_t stream);
 fa_status launch_tree_mask(const TreeParams& p, cudaStream_t stream);
 fa_status launch_rope(const RopeParams& p, int num_sms, cudaStream_t stream);
 fa_status launch_cache_write(const CacheParams& p, int num_sms, cudaStream_t stream);
@@ -137,6 +161,7 @@ fa_status launch_cache_read(const CacheParams& p, int num_sms, cudaStream_t stre
 fa_status launch_paged_decode(const PagedAttnLaunch& L, cudaStream_t stream);
 fa_status launch_paged_chunk(const PagedAttnLaunch& L, cudaStream_t stream);
 
+fa_status evict_take_device_error();
 fa_status tree_take_device_error();
 fa_status cache_take_device_error();
 fa_status paged_decode_take_device_error();

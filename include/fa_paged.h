@@ -193,6 +193,46 @@ FA_API fa_status fa_fwd_paged_tree(const void* q, const void* k_pages, const voi
                                    const int* block_table, const int* seq_lens, const int* cu_seqlens, int max_q,
                                    void* workspace, size_t workspace_bytes, fa_stream_t stream);
 
+/*
+ * Eviction: which tokens each key/value head keeps of a sequence that is over its
+ * budget.  Of the seq_lens[b] tokens of sequence b, kept[b] = min(seq_lens[b],
+ * keep) stay: the first `first` and the last `recent` ones, and of the others those
+ * with the largest sums.  Of equal sums (-0 and 0 are) the lowest token stays first;
+ * a NaN counts as larger than every number.
+ *   sums         FP32 [num_pages, Hkv, page_size], laid out like the pages' scales
+ *   keep         >= 1, first + recent <= keep <= 2^30
+ *   index        device int32 [B, Hkv, keep]: the tokens that stay, in ascending
+ *                order; -1 behind the kept[b]-th
+ *   kept         device int32 [B]
+ * The sum of a token in a bad page reads as zero; a sequence whose length breaks the
+ * rules keeps no token.
+ */
+FA_API fa_status fa_cache_select(const float* sums, int* index, int* kept, int B, int Hkv, int num_pages, int page_size,
+                                 int max_pages, int keep, int first, int recent, const int* block_table,
+                                 const int* seq_lens, fa_stream_t stream);
+
+/*
+ * Moves rows of the cache together, in place: for i < counts[b] token index[b][h][i]
+ * of sequence b and head h goes to slot start[b] + i, its key, its value, their
+ * scales and its sum alike.  Slots that no token goes to keep what they hold.  After
+ * an eviction the sequence is counts[b] tokens long; after drafts were accepted (their
+ * tokens' numbers in the sequence in `index`, the number of tokens before the tree in
+ * `start`) start[b] + counts[b].
+ *   index        device int32 [B, heads, most], heads = Hkv, or 1: the same tokens for
+ *                all heads.  The first counts[b] of a list are ascending, none twice,
+ *                start[b] or more, and within the block table; a list that is not so is
+ *                reported, and nothing of it moves.
+ *   counts       device int32 [B], 0 ... most
+ *   start        device int32 [B], >= 0, or NULL: 0
+ *   sums         as fa_cache_select() has them, or NULL
+ * A token whose old or new page is bad is not moved.  No page that a row is written
+ * to may be in the table twice.
+ */
+FA_API fa_status fa_cache_keep(void* k_pages, void* v_pages, void* k_scale, void* v_scale, float* sums, int B, int Hkv,
+                               int D, int num_pages, int page_size, int max_pages, const int* block_table,
+                               const int* index, int heads, int most, const int* counts, const int* start,
+                               fa_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -174,3 +174,16 @@ def attention_of(q, k, v, sees, scale):
             a[i, h] = p @ np.abs(vh[sees[i]]) / p.sum()
             lse[h, i] = s.max() + np.log(p.sum())
     return o, lse, a
+
+
+def select(sums, keep, first, recent):
+    """Ascending tokens that stay of one head's sums [L]."""
+    L = len(sums)
+    if L <= keep:
+        return np.arange(L)
+    x = np.where(np.isnan(sums), np.inf, sums.astype(np.float64))
+    above = np.isnan(sums).astype(int)                  # a NaN is above an infinity
+    at = np.arange(L)
+    above[(at < first) | (at >= L - recent)] = 2
+    order = np.lexsort((at, -x, -above))                # by class, then by size, then the lowest token
+    return np.sort(order[:keep])
