@@ -13,6 +13,7 @@ from .binding import (  # noqa: F401
     cache_keep,
     cache_read,
     cache_select,
+    cache_weights,
     cache_write,
     exp2_probe,
     fwd,

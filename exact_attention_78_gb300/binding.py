@@ -59,6 +59,7 @@ _SIGNATURES = {
     "fa_fwd_paged_workspace_size": (_sz, [_i] * 7),
     "fa_fwd_paged": (_i, [_vp] * 7 + [_i] * 9 + [_f] + [_vp] * 3 + [_i, _vp, _sz, _vp]),
     "fa_fwd_paged_tree": (_i, [_vp] * 7 + [_i] * 8 + [_vp, _f] + [_vp] * 3 + [_i, _vp, _sz, _vp]),
+    "fa_cache_weights": (_i, [_vp] * 5 + [_i] * 9 + [_f] * 2 + [_vp] * 3 + [_i, _vp]),
     "fa_cache_select": (_i, [_vp] * 3 + [_i] * 8 + [_vp] * 3),
     "fa_cache_keep": (_i, [_vp] * 5 + [_i] * 6 + [_vp] * 2 + [_i] * 2 + [_vp] * 3),
     "fa_tree_mask": (_i, [_vp] * 3 + [_i] * 2 + [_vp, _i, _vp]),
@@ -607,6 +608,30 @@ def _check_sums(sums, device, shape=None):
             and (len(sums.shape) == 3 if shape is None else sums.shape == shape[:3])):
         _bad("sums", "a contiguous CUDA float32 tensor of shape %s" % (
             "[num_pages, Hkv, page_size]" if shape is None else (tuple(shape[:3]),)), device)
+
+
+def cache_weights(q, lse, k_pages, sums, block_table, seq_lens, causal=True, scale=None, decay=1.0, cu_seqlens=None,
+                  max_q=None, k_scale=None, stream=None):
+    """Adds up the attention weights that the keys of the cache get from new tokens q,
+    whose fwd_paged call gave `lse`: sums (float32 [num_pages, Hkv, page_size], a slot
+    for each key) become decay * sums + the weights of the group's rows; those of the new
+    tokens start at zero.  q, lse and the other arguments as fwd_paged has them."""
+    lib = load_library()
+    B, device = block_table.shape[0], q.device
+    Sn = _new_tokens("q", q, B, cu_seqlens)
+    Hq, D = q.shape[-2:]
+    num_pages, Hkv, page_size, max_pages = _cache_args(None, D, device, k_pages, k_pages, k_scale, k_scale, block_table)
+    _check_seq_lens(seq_lens, device, B)
+    _check_out("lse", lse, (B, Hq, Sn) if cu_seqlens is None else (Hq, Sn), torch.float32, device)
+    _check_sums(sums, device, k_pages.shape)
+    most = _most_new(cu_seqlens, Sn, max_q)
+    with _on(device, stream) as s:
+        st = lib.fa_cache_weights(q.data_ptr(), lse.data_ptr(), k_pages.data_ptr(), _adr(k_scale), sums.data_ptr(), B, Hq,
+                                  Hkv, Sn, D, num_pages, page_size, max_pages, bool(causal),
+                                  D ** -0.5 if scale is None else scale, decay, block_table.data_ptr(),
+                                  seq_lens.data_ptr(), _adr(cu_seqlens), most, s)
+    if st:
+        raise FAError(st, "fa_cache_weights")
 
 
 def cache_select(sums, block_table, seq_lens, keep, first=0, recent=0, index=None, kept=None, stream=None):

@@ -483,7 +483,7 @@ fa_status fa_get_device_error(fa_stream_t stream) {
   const fa_status all[] = {fwd_take_device_error(),          bwd_take_device_error(), bwd_pair_take_device_error(),
                            bwd_dq_take_device_error(),       diag_take_device_error(), cache_take_device_error(),
                            paged_decode_take_device_error(), paged_chunk_take_device_error(), tree_take_device_error(),
-                           evict_take_device_error()};
+                           evict_take_device_error(),        weigh_take_device_error()};
   for (fa_status s : all)
     if (first == FA_OK && s != FA_OK) first = s;
   return first;

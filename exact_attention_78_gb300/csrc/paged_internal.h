@@ -61,6 +61,20 @@ struct TreeParams {
   int B, Sn, max_q, words;  // packed: Sn = rows of the packed arrays
 };
 
+struct WeighParams {
+  PagedSeqs s;
+  const void* q;
+  const float* lse;
+  const void* k_pages;
+  const uint8_t* k_scale;   // nullptr: BF16 pages
+  float* sums;              // [num_pages, Hkv, page_size]
+  int Hq, group, D;         // group = Hq / Hkv
+  int causal;
+  int max_q;
+  float scale, decay;
+  unsigned long long wait_limit_ns;
+};
+
 struct SelectParams {
   PagedSeqs s;              // cu = nullptr
   const float* sums;        // [num_pages, Hkv, page_size]
@@ -152,6 +166,7 @@ fa_status launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, int sm
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
+fa_status launch_cache_weights(const WeighParams& p, int num_sms, cudaStream_t stream);
 fa_status launch_cache_select(const SelectParams& p, int num_sms, cudaStream_t stream);
 fa_status launch_cache_keep(const KeepParams& p, int num_sms, cudaStream_t stream);
 fa_status launch_tree_mask(const TreeParams& p, cudaStream_t stream);
@@ -161,6 +176,7 @@ fa_status launch_cache_read(const CacheParams& p, int num_sms, cudaStream_t stre
 fa_status launch_paged_decode(const PagedAttnLaunch& L, cudaStream_t stream);
 fa_status launch_paged_chunk(const PagedAttnLaunch& L, cudaStream_t stream);
 
+fa_status weigh_take_device_error();
 fa_status evict_take_device_error();
 fa_status tree_take_device_error();
 fa_status cache_take_device_error();

@@ -194,6 +194,30 @@ FA_API fa_status fa_fwd_paged_tree(const void* q, const void* k_pages, const voi
                                    void* workspace, size_t workspace_bytes, fa_stream_t stream);
 
 /*
+ * Sums of the attention weights that the keys of the cache get: for every head h of
+ * every sequence b that has new tokens, and each of its tokens t,
+ *   sums[t] = decay * sums[t] + sum over rows r that see t of exp(scale * q_r k_t - lse_r)
+ * where the rows are the new tokens' query heads of the group, a token's slot in `sums`
+ * is that of its key, and a new token's sum starts at zero (so does every sum with
+ * decay 0, whatever it holds).
+ *   q, causal, scale, block_table, seq_lens, cu_seqlens, max_q, and the pages
+ *                as fa_fwd_paged() had them
+ *   lse          as fa_fwd_paged() wrote it; a row with -inf gives no weight
+ *   sums         FP32 [num_pages, Hkv, page_size], laid out like the pages' scales;
+ *                slots that are no token's stay as they are
+ *   scale        > 0, a normal FP32 number
+ *   decay        >= 0, finite
+ * Weights and sums are FP32.  Over E4M3 pages, with up to 16 rows of a sequence and
+ * head, queries are FP16 as fa_fwd_paged() has them; else keys are BF16, exactly.  A
+ * token in a bad page gets no sum.  Sequences that share pages must not share the slots
+ * of tokens of theirs in one call.  Results are bitwise repeatable.
+ */
+FA_API fa_status fa_cache_weights(const void* q, const float* lse, const void* k_pages, const void* k_scale,
+                                  float* sums, int B, int Hq, int Hkv, int Sn, int D, int num_pages, int page_size,
+                                  int max_pages, int causal, float scale, float decay, const int* block_table,
+                                  const int* seq_lens, const int* cu_seqlens, int max_q, fa_stream_t stream);
+
+/*
  * Eviction: which tokens each key/value head keeps of a sequence that is over its
  * budget.  Of the seq_lens[b] tokens of sequence b, kept[b] = min(seq_lens[b],
  * keep) stay: the first `first` and the last `recent` ones, and of the others those

@@ -187,3 +187,21 @@ def select(sums, keep, first, recent):
     above[(at < first) | (at >= L - recent)] = 2
     order = np.lexsort((at, -x, -above))                # by class, then by size, then the lowest token
     return np.sort(order[:keep])
+
+
+def weights(q, lse, k, sees, scale):
+    """What one sequence's keys get: q [n, Hq, D], lse [Hq, n], k [L, Hkv, D], mask
+    [n, L].  Returns ([Hkv, L], the same with each weight times its |score - lse|)."""
+    n, Hq, D = q.shape
+    L, Hkv = k.shape[0], k.shape[1]
+    out, slack = np.zeros((Hkv, L)), np.zeros((Hkv, L))
+    for h in range(Hq):
+        x = q[:, h] @ k[:, h // (Hq // Hkv)].T * scale
+        for i in range(n):
+            if np.isneginf(lse[h, i]):
+                continue
+            d = np.where(sees[i], x[i] - lse[h, i], -np.inf)
+            w = np.exp(d)
+            out[h // (Hq // Hkv)] += w
+            slack[h // (Hq // Hkv)] += np.where(w > 0, w * np.abs(np.where(sees[i], d, 0.0)), 0.0)
+    return out, slack
