@@ -61,7 +61,7 @@ constexpr int kThreads = 512;
 constexpr int kBins = 2048;
 FA_DEV int bits_of(int round) { return round == 2 ? 10 : 11; }
 FA_DEV int shift_of(int round) { return round == 0 ? 21 : round == 1 ? 10 : 0; }
-constexpr int kMostCached = 16384;         // tokens of a block in shared memory; the others are read again
+constexpr int kMostCached = 49152;         // tokens of a block in shared memory; the others are read again
 
 // Floats in an order that unsigned integers have; a NaN is above all numbers.
 FA_DEV uint32_t ordered(float x) {
@@ -100,19 +100,30 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
 
   const int each = ((L + C - 1) / C + 3) / 4 * 4;     // tokens of a block
   const int t0 = min(L, rank * each), n = min(L, t0 + each) - t0;
-  auto load = [&](int i) -> uint32_t {
+  // tokens go four at a time, which lie in one page (i a multiple of 4)
+  auto load = [&](int i) -> uint4 {
     const int t = t0 + i;
-    if (t < p.first || t >= L - p.recent) return kProtected;
     const long long row = row_of(p.s, b, head, t);
-    return ordered(row < 0 ? 0.0f : p.sums[row]);
+    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (row >= 0) x = *reinterpret_cast<const float4*>(p.sums + row);
+    const int end = L - p.recent;
+    return make_uint4(t < p.first || t >= end ? kProtected : ordered(x.x),
+                      t + 1 < p.first || t + 1 >= end ? kProtected : ordered(x.y),
+                      t + 2 < p.first || t + 2 >= end ? kProtected : ordered(x.z),
+                      t + 3 < p.first || t + 3 >= end ? kProtected : ordered(x.w));
   };
-  auto key_at = [&](int i) -> uint32_t { return i < p.cached ? cached[i] : load(i); };
+  auto keys_at = [&](int i) -> uint4 {
+    return i < p.cached ? *reinterpret_cast<const uint4*>(cached + i) : load(i);
+  };
   __syncthreads();
 #pragma unroll 4
-  for (int i = tid; i < n; i += kThreads) {
-    const uint32_t key = load(i);
-    if (i < p.cached) cached[i] = key;
-    atomicAdd(&hist[key >> shift_of(0)], 1u);
+  for (int i = 4 * tid; i < n; i += 4 * kThreads) {
+    const uint4 x = load(i);
+    if (i < p.cached) *reinterpret_cast<uint4*>(cached + i) = x;
+    atomicAdd(&hist[x.x >> shift_of(0)], 1u);
+    if (i + 1 < n) atomicAdd(&hist[x.y >> shift_of(0)], 1u);
+    if (i + 2 < n) atomicAdd(&hist[x.z >> shift_of(0)], 1u);
+    if (i + 3 < n) atomicAdd(&hist[x.w >> shift_of(0)], 1u);
   }
 
   uint32_t prefix = 0u, need = (uint32_t)p.keep;      // of the candidates, whose bits so far are `prefix`
@@ -122,9 +133,12 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
     uint32_t* h = hist + round * kBins;
     if (round > 0) {
       const int shift = shift_of(round), bits = bits_of(round);
-      for (int i = tid; i < n; i += kThreads) {
-        const uint32_t key = key_at(i);
-        if (key >> shift >> bits == prefix) atomicAdd(&h[key >> shift & ((1u << bits) - 1u)], 1u);
+      for (int i = 4 * tid; i < n; i += 4 * kThreads) {
+        const uint4 x = keys_at(i);
+        const uint32_t key[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (i + k < n && key[k] >> shift >> bits == prefix) atomicAdd(&h[key[k] >> shift & ((1u << bits) - 1u)], 1u);
       }
     }
     cluster_sync();
@@ -183,15 +197,15 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
     over += ld_cluster_u32(mapa_shared(smem_u32(&counts[0]), r));
     equal += ld_cluster_u32(mapa_shared(smem_u32(&counts[1]), r));
   }
-  constexpr int kEach = 4;                            // tokens of a thread
-  for (int i0 = 0; i0 < n; i0 += kThreads * kEach) {
-    uint32_t key[kEach], own = 0u;                    // above: low half, equal: high half
+  for (int i0 = 0; i0 < n; i0 += 4 * kThreads) {
+    const int i = i0 + 4 * tid;
+    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+    if (i < n) x = keys_at(i);
+    const uint32_t key[4] = {x.x, x.y, x.z, x.w};
+    uint32_t own = 0u;                                // above: low half, equal: high half
 #pragma unroll
-    for (int k = 0; k < kEach; ++k) {
-      const int i = i0 + kEach * tid + k;
-      key[k] = i < n ? key_at(i) : 0u;
-      if (i < n) own += key[k] > threshold ? 1u : key[k] == threshold ? 0x10000u : 0u;
-    }
+    for (int k = 0; k < 4; ++k)
+      if (i + k < n) own += key[k] > threshold ? 1u : key[k] == threshold ? 0x10000u : 0u;
     uint32_t incl = own;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
@@ -208,14 +222,12 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
     }
     uint32_t a = over + (before & 0xFFFFu), e = equal + (before >> 16);
 #pragma unroll
-    for (int k = 0; k < kEach; ++k) {
-      const int i = i0 + kEach * tid + k;
-      if (i >= n) break;
-      if (key[k] < threshold) continue;
+    for (int k = 0; k < 4; ++k) {
+      if (i + k >= n || key[k] < threshold) continue;
       const uint32_t at = a + min(e, need);
       const bool more = key[k] > threshold;
       // (below `keep`, unless the sums change meanwhile)
-      if ((more || e < need) && at < (uint32_t)p.keep) out[at] = t0 + i;
+      if ((more || e < need) && at < (uint32_t)p.keep) out[at] = t0 + i + k;
       a += more;
       e += !more;
     }
@@ -236,10 +248,10 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
 // list, its blocks the parts of a tile.  Keys and values go apart.
 
 constexpr int kMoveThreads = 256;
-constexpr int kUnroll = 8;
+constexpr int kUnroll = 4;
 
 template <int D, bool kFp8>
-__global__ void __launch_bounds__(kMoveThreads) keep_kernel(const KeepParams p) {
+__global__ void __launch_bounds__(kMoveThreads, 4) keep_kernel(const KeepParams p) {
   constexpr int kLanes = D * (kFp8 ? 1 : 2) / 16;                    // of a row
   constexpr int kGroups = kMoveThreads / kLanes;
   constexpr int kRows = kUnroll * kGroups;                           // of a block's part of a tile
