@@ -15,6 +15,7 @@ using paged::record_bad_input;
 enum Site { kSiteLength = 1, kSitePage, kSiteCount, kSiteList };
 
 constexpr int kMaxCluster = 8;       // the largest portable one
+constexpr int kMaxSelect = 16;       // blocks of a selection's cluster
 
 FA_DEV uint32_t ld_cluster_u32(uint32_t addr) {
   uint32_t v;
@@ -48,35 +49,51 @@ FA_DEV long long row_of(const PagedSeqs& s, int b, int head, int tok) {
 // ------------------------------------------------------------------ select --
 // The k-th largest of a head's sums by their bits, 11, 11 and 10 at a time: a
 // histogram of the candidates, and from its top down the bin in which the k-th
-// lies.  A cluster takes a (sequence, head), each of its blocks a stretch of the
-// tokens, which stay in shared memory, and every block adds up the histograms of all
-// (reading the others' shared memory), so that all know the bin with one barrier a
-// round and nothing goes through global memory.  Then each block counts what
-// it keeps, and writes it in order.
+// lies.  A thread block takes a (sequence, head), whose tokens stay in shared memory;
+// where there are fewer of those than SMs, a cluster does, each of its blocks a stretch
+// of the tokens, and its blocks add up their histograms by reading one another's shared
+// memory.  They share the bins out: reading all of every histogram, 8 KB, in each block
+// took 20,000 cycles a round with 16 blocks.  Then each block counts what it keeps, and
+// writes it in order.
 //
 // It reads four bytes a key, little: what takes the time is the chain of loads and
-// barriers.
+// barriers, and the instructions for each token of the few SMs that take part.
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kGroups = kBins / 32;        // of bins that a warp adds up
+static_assert(kGroups == 64, "two groups a lane");
 FA_DEV int bits_of(int round) { return round == 2 ? 10 : 11; }
 FA_DEV int shift_of(int round) { return round == 0 ? 21 : round == 1 ? 10 : 0; }
 constexpr int kMostCached = 49152;         // tokens of a block in shared memory; the others are read again
 
-// Floats in an order that unsigned integers have; a NaN is above all numbers.
+// Floats in an order that unsigned integers have; a NaN is above all numbers.  Nothing
+// comes out below 0x007FFFFF, which is -inf.
 FA_DEV uint32_t ordered(float x) {
   const uint32_t u = __float_as_uint(x + 0.0f);       // (-0 is 0)
-  if ((u & 0x7FFFFFFFu) > 0x7F800000u) return 0xFFFFFFFEu;
-  return u >> 31 ? ~u : u | 0x80000000u;
+  const uint32_t key = u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
+  return (u & 0x7FFFFFFFu) > 0x7F800000u ? 0xFFFFFFFEu : key;
 }
-constexpr uint32_t kProtected = 0xFFFFFFFFu;
+constexpr uint32_t kProtected = 0xFFFFFFFFu, kNoToken = 0u;
+
+// Inclusive sums over the lanes.
+FA_DEV uint32_t scan(uint32_t v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const uint32_t o = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
 
 __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) {
   extern __shared__ __align__(16) uint32_t smem[];
   uint32_t* hist = smem;                              // [3][kBins]
   uint32_t* cached = smem + 3 * kBins;
-  __shared__ uint32_t warp_sum[kThreads / 32];
-  __shared__ uint32_t found[3];                       // bin, how many candidates lie above it
+  __shared__ uint32_t total[kBins], group_total[kGroups];      // of this block's share of the bins, over all blocks
+  __shared__ uint32_t warp_over[kWarps], warp_equal[kWarps];   // above the threshold, equal to it
+  __shared__ uint32_t found[2];                       // bin, how many candidates lie above it
   __shared__ uint32_t counts[2];                      // this block's: above the threshold, equal to it
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int C = (int)cluster_size(), rank = (int)cluster_ctarank();
@@ -90,9 +107,8 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
     if (tid == 0) record_bad_input(&g_err, kSiteLength);
     L = 0;
   }
-  const int kept = min(L, p.keep);
   int* out = p.index + (size_t)unit * p.keep;
-  if (head == 0 && rank == 0 && tid == 0) p.kept[b] = kept;
+  if (head == 0 && rank == 0 && tid == 0) p.kept[b] = min(L, p.keep);
   if (L <= p.keep) {                                  // all of them (the whole cluster comes here)
     for (int i = rank * kThreads + tid; i < p.keep; i += C * kThreads) out[i] = i < L ? i : -1;
     return;
@@ -100,142 +116,195 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
 
   const int each = ((L + C - 1) / C + 3) / 4 * 4;     // tokens of a block
   const int t0 = min(L, rank * each), n = min(L, t0 + each) - t0;
-  // tokens go four at a time, which lie in one page (i a multiple of 4)
+  // A warp has a stretch of the block's tokens, 128 at a time, four a lane, which lie
+  // in one page.
+  const int stretch = (each + 128 * kWarps - 1) / (128 * kWarps) * 128;
+  const int i0 = min(n, warp * stretch), i1 = min(n, i0 + stretch);
+  const int last = L - p.recent;                      // the first protected one at the end
   auto load = [&](int i) -> uint4 {
     const int t = t0 + i;
     const long long row = row_of(p.s, b, head, t);
     float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (row >= 0) x = *reinterpret_cast<const float4*>(p.sums + row);
-    const int end = L - p.recent;
-    return make_uint4(t < p.first || t >= end ? kProtected : ordered(x.x),
-                      t + 1 < p.first || t + 1 >= end ? kProtected : ordered(x.y),
-                      t + 2 < p.first || t + 2 >= end ? kProtected : ordered(x.z),
-                      t + 3 < p.first || t + 3 >= end ? kProtected : ordered(x.w));
+    uint4 y = make_uint4(ordered(x.x), ordered(x.y), ordered(x.z), ordered(x.w));
+    if (t < p.first || t + 3 >= last || i + 3 >= n) {
+      auto key = [&](int k, uint32_t v) {
+        return i + k >= n ? kNoToken : t + k < p.first || t + k >= last ? kProtected : v;
+      };
+      y = make_uint4(key(0, y.x), key(1, y.y), key(2, y.z), key(3, y.w));
+    }
+    return y;
+  };
+  auto sync_all = [&]() {
+    if (C > 1) cluster_sync(); else __syncthreads();
   };
   auto keys_at = [&](int i) -> uint4 {
     return i < p.cached ? *reinterpret_cast<const uint4*>(cached + i) : load(i);
   };
   __syncthreads();
-#pragma unroll 4
-  for (int i = 4 * tid; i < n; i += 4 * kThreads) {
-    const uint4 x = load(i);
-    if (i < p.cached) *reinterpret_cast<uint4*>(cached + i) = x;
-    atomicAdd(&hist[x.x >> shift_of(0)], 1u);
-    if (i + 1 < n) atomicAdd(&hist[x.y >> shift_of(0)], 1u);
-    if (i + 2 < n) atomicAdd(&hist[x.z >> shift_of(0)], 1u);
-    if (i + 3 < n) atomicAdd(&hist[x.w >> shift_of(0)], 1u);
+#pragma unroll 1
+  for (int j = i0; j < i1; j += 512) {
+    uint4 x[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = j + 128 * u + 4 * lane;
+      x[u] = make_uint4(kNoToken, kNoToken, kNoToken, kNoToken);
+      if (i < i1) x[u] = load(i);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = j + 128 * u + 4 * lane;
+      if (j + 128 * u >= i1) break;                   // (the whole warp)
+      if (i < i1 && i < p.cached) *reinterpret_cast<uint4*>(cached + i) = x[u];
+      const uint32_t bin[4] = {x[u].x >> shift_of(0), x[u].y >> shift_of(0), x[u].z >> shift_of(0), x[u].w >> shift_of(0)};
+      // tokens that are all alike (protected ones, zeros) would be counted one by one
+      const uint32_t lead = __shfl_sync(0xffffffffu, bin[0], 0);
+      if (__all_sync(0xffffffffu, bin[0] == lead && bin[1] == lead && bin[2] == lead && bin[3] == lead)) {
+        if (lane == 0) atomicAdd(&hist[lead], 128u);
+      } else {      // (what is no token goes to bin 0, where no token is)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) atomicAdd(&hist[bin[k]], 1u);
+      }
+    }
   }
-
   uint32_t prefix = 0u, need = (uint32_t)p.keep;      // of the candidates, whose bits so far are `prefix`
-  uint32_t above = 0u;                                // of this block, over the threshold
 #pragma unroll 1
   for (int round = 0; round < 3; ++round) {
     uint32_t* h = hist + round * kBins;
     if (round > 0) {
       const int shift = shift_of(round), bits = bits_of(round);
-      for (int i = 4 * tid; i < n; i += 4 * kThreads) {
-        const uint4 x = keys_at(i);
+      const uint32_t low = (1u << bits) - 1u;
+#pragma unroll 4
+      for (int j = i0 + 4 * lane; j < i1; j += 128) {
+        const uint4 x = keys_at(j);
         const uint32_t key[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          if (i + k < n && key[k] >> shift >> bits == prefix) atomicAdd(&h[key[k] >> shift & ((1u << bits) - 1u)], 1u);
+          if (key[k] >> shift >> bits == prefix) atomicAdd(&h[key[k] >> shift & low], 1u);
       }
     }
-    cluster_sync();
-    // thread t adds up bins 4 t ... 4 t + 3 of all blocks; bins run from the top down
-    const int bin0 = kBins - 4 - 4 * tid;
-    uint4 sum = make_uint4(0u, 0u, 0u, 0u);
-    for (int r = 0; r < C; ++r) {
-      const uint4 x = ld_cluster_v4(mapa_shared(smem_u32(h + bin0), r));
-      sum.x += x.x;
-      sum.y += x.y;
-      sum.z += x.z;
-      sum.w += x.w;
-    }
-    const uint32_t own = sum.x + sum.y + sum.z + sum.w;
-    uint32_t incl = own;
+    sync_all();
+    // this block's share: bins [rank * share, + share), 32 a warp
+    const int share = kBins / C;
+    for (int g = warp; g < share / 32; g += kWarps) {
+      uint32_t sum = 0u;
+      if (C == 1) {
+        sum = h[g * 32 + lane];
+      } else {
+        const uint32_t from = smem_u32(h + rank * share + g * 32 + lane);
+        uint32_t x[kMaxSelect];
 #pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-      const uint32_t o = __shfl_up_sync(0xffffffffu, incl, d);
-      if (lane >= d) incl += o;
+        for (int r = 0; r < kMaxSelect; ++r) x[r] = r < C ? ld_cluster_u32(mapa_shared(from, r)) : 0u;
+#pragma unroll
+        for (int r = 0; r < kMaxSelect; ++r) sum += x[r];
+      }
+      total[g * 32 + lane] = sum;
+      sum = __reduce_add_sync(0xffffffffu, sum);
+      if (lane == 0) group_total[g] = sum;
     }
-    if (lane == 31) warp_sum[warp] = incl;
-    __syncthreads();
-    uint32_t before = incl - own;
-    for (int w = 0; w < warp; ++w) before += warp_sum[w];
-    if (before < need && before + own >= need) {      // one thread
-      const uint32_t v[4] = {sum.w, sum.z, sum.y, sum.x};
-      int k = 0;
-      while (before + v[k] < need) before += v[k++];
-      found[0] = (uint32_t)(bin0 + 3 - k);
-      found[1] = before;
+    sync_all();
+    if (warp == 0) {
+      // the group, then the bin in it, from the top down
+      const int per = share / 32;
+      auto group_of = [&](int g) { return ld_cluster_u32(mapa_shared(smem_u32(group_total + g % per), g / per)); };
+      const uint32_t v0 = group_of(63 - 2 * lane), v1 = group_of(62 - 2 * lane);
+      uint32_t above = scan(v0 + v1, lane) - v0 - v1;
+      uint32_t mine = __ballot_sync(0xffffffffu, above < need && above + v0 + v1 >= need);
+      int at = mine ? __ffs(mine) - 1 : 0;
+      const bool second = above + v0 < need;
+      const int group = __shfl_sync(0xffffffffu, second ? 62 - 2 * lane : 63 - 2 * lane, at);
+      const uint32_t base = __shfl_sync(0xffffffffu, second ? above + v0 : above, at);
+      const uint32_t v = ld_cluster_u32(mapa_shared(smem_u32(total + group % per * 32 + 31 - lane), group / per));
+      above = base + scan(v, lane) - v;
+      mine = __ballot_sync(0xffffffffu, above < need && above + v >= need);
+      at = mine ? __ffs(mine) - 1 : 0;
+      if (lane == at) {
+        found[0] = (uint32_t)(group * 32 + 31 - lane);
+        found[1] = above;
+      }
     }
     __syncthreads();
-    const uint32_t bin = found[0];
     need -= found[1];
-    // this block's own candidates above the bin
-    uint32_t mine = 0u;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) mine += bin0 + k > (int)bin ? h[bin0 + k] : 0u;
-    mine = __reduce_add_sync(0xffffffffu, mine);
-    if (lane == 0) warp_sum[warp] = mine;             // (read above ahead of the barrier)
-    prefix = round == 0 ? bin : prefix << bits_of(round) | bin;
-    __syncthreads();
-    for (int w = 0; w < kThreads / 32; ++w) above += warp_sum[w];
-    __syncthreads();
+    prefix = round == 0 ? found[0] : prefix << bits_of(round) | found[0];
   }
 
   // Kept: the tokens above the threshold, and the first `need` of those at it.
   const uint32_t threshold = prefix;
-  if (tid == 0) {
-    counts[0] = above;
-    counts[1] = hist[2 * kBins + (threshold & (kBins / 2 - 1))];
+  uint32_t over = 0u, equal = 0u;                     // in the blocks and warps before, and on the way
+#pragma unroll 2
+  for (int i = i0 + 4 * lane; i < i1; i += 128) {
+    const uint4 x = keys_at(i);
+    over += (x.x > threshold) + (x.y > threshold) + (x.z > threshold) + (x.w > threshold);
+    equal += (x.x == threshold) + (x.y == threshold) + (x.z == threshold) + (x.w == threshold);
   }
-  cluster_sync();
-  uint32_t over = 0u, equal = 0u;                     // in the blocks before this one, and on the way
+  over = __reduce_add_sync(0xffffffffu, over);
+  equal = __reduce_add_sync(0xffffffffu, equal);
+  if (lane == 0) {
+    warp_over[warp] = over;
+    warp_equal[warp] = equal;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    const uint32_t o = lane < kWarps ? warp_over[lane] : 0u, e = lane < kWarps ? warp_equal[lane] : 0u;
+    const uint32_t so = scan(o, lane), se = scan(e, lane);
+    if (lane < kWarps) {
+      warp_over[lane] = so - o;
+      warp_equal[lane] = se - e;
+    }
+    if (lane == 31) {
+      counts[0] = so;
+      counts[1] = se;
+    }
+  }
+  sync_all();
+  over = warp_over[warp];
+  equal = warp_equal[warp];
   for (int r = 0; r < rank; ++r) {
     over += ld_cluster_u32(mapa_shared(smem_u32(&counts[0]), r));
     equal += ld_cluster_u32(mapa_shared(smem_u32(&counts[1]), r));
   }
-  for (int i0 = 0; i0 < n; i0 += 4 * kThreads) {
-    const int i = i0 + 4 * tid;
-    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-    if (i < n) x = keys_at(i);
+  const uint32_t below = (1u << lane) - 1u;
+  // (places are below `keep`, unless the sums change meanwhile)
+#pragma unroll 2
+  for (int j = i0; j < i1; j += 128) {
+    const int i = j + 4 * lane;
+    uint4 x = make_uint4(kNoToken, kNoToken, kNoToken, kNoToken);
+    if (i < i1) x = keys_at(i);
     const uint32_t key[4] = {x.x, x.y, x.z, x.w};
-    uint32_t own = 0u;                                // above: low half, equal: high half
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (i + k < n) own += key[k] > threshold ? 1u : key[k] == threshold ? 0x10000u : 0u;
-    uint32_t incl = own;
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-      const uint32_t o = __shfl_up_sync(0xffffffffu, incl, d);
-      if (lane >= d) incl += o;
-    }
-    if (lane == 31) warp_sum[warp] = incl;
-    __syncthreads();
-    uint32_t before = incl - own, all = 0u;
-    for (int w = 0; w < kThreads / 32; ++w) {
-      const uint32_t x = warp_sum[w];
-      before += w < warp ? x : 0u;
-      all += x;
-    }
-    uint32_t a = over + (before & 0xFFFFu), e = equal + (before >> 16);
+    uint32_t a = over;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      if (i + k >= n || key[k] < threshold) continue;
-      const uint32_t at = a + min(e, need);
-      const bool more = key[k] > threshold;
-      // (below `keep`, unless the sums change meanwhile)
-      if ((more || e < need) && at < (uint32_t)p.keep) out[at] = t0 + i + k;
-      a += more;
-      e += !more;
+      const uint32_t more = __ballot_sync(0xffffffffu, key[k] > threshold);
+      a += __popc(more & below);
+      over += __popc(more);
     }
-    over += all & 0xFFFFu;
-    equal += all >> 16;
-    __syncthreads();
+    if (!__any_sync(0xffffffffu, key[0] == threshold || key[1] == threshold || key[2] == threshold || key[3] == threshold)) {
+      uint32_t to = a + min(equal, need);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (key[k] <= threshold) continue;
+        if (to < (uint32_t)p.keep) out[to] = t0 + i + k;
+        ++to;
+      }
+      continue;
+    }
+    uint32_t e = equal;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t same = __ballot_sync(0xffffffffu, key[k] == threshold);
+      e += __popc(same & below);
+      equal += __popc(same);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const bool up = key[k] > threshold, at = key[k] == threshold;
+      const uint32_t to = a + min(e, need);
+      if ((up || (at && e < need)) && to < (uint32_t)p.keep) out[to] = t0 + i + k;
+      a += up;
+      e += at;
+    }
   }
-  cluster_sync();                                     // the others may still read this block's counts
+  sync_all();                                         // the others may still read this block's counts
 }
 
 // -------------------------------------------------------------------- keep --
@@ -408,11 +477,11 @@ fa_status launch_cache_select(const SelectParams& in, int num_sms, cudaStream_t 
   const int capacity = p.s.max_pages << p.s.page_shift;
   const long long units = (long long)p.s.B * p.s.Hkv;
   int C = 1;
-  while (C < evict::kMaxCluster && units * C * 2 <= 4ll * num_sms && 1024 * C < capacity) C *= 2;
+  while (C < evict::kMaxSelect && units * C * 2 <= num_sms && 4096 * C < capacity) C *= 2;
   const int each = ((capacity + C - 1) / C + 3) / 4 * 4;
   p.cached = each < evict::kMostCached ? each : evict::kMostCached;
   const int most = (3 * evict::kBins + evict::kMostCached) * 4;
-  const fa_status st = prepare_kernel(reinterpret_cast<const void*>(evict::select_kernel), most);
+  const fa_status st = prepare_kernel(reinterpret_cast<const void*>(evict::select_kernel), most, true);
   if (st != FA_OK) return st;
   return evict::launch_clusters(evict::select_kernel, (int)units, C, evict::kThreads,
                                 (3 * evict::kBins + p.cached) * 4, stream, p);
