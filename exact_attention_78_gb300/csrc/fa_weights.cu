@@ -40,10 +40,12 @@ FA_DEV long long slot_of(const WeighParams& p, int b, int head, int key) {
 // ---------------------------------------------------------------- few rows --
 // A step of single tokens reads every key once and computes little with it, so HBM
 // bounds it.  The keys are the M side of mma.sync products, 16 a tile, the rows the N
-// side, 8 a tile.  A product's sum may take its elements in any order, so that each
-// lane's share of a key is whole pieces of 16 bytes, straight from global memory:
-// no shared memory, no barriers, and a warp is on its own.  All tiles of all (sequence,
-// head) units form one line, of which every warp takes an equal stretch.
+// side, 8 a tile.  A product's sum may take its elements in any order, so each
+// lane's share of a key is whole pieces of 16 bytes, which the lane itself copies from
+// global memory ahead of their use, into its own places of a ring in shared memory:
+// a warp is on its own, with no barrier but its own lanes', and some 150 KB an SM are
+// under way.  All tiles of all (sequence, head) units form one line, of which every
+// warp takes an equal stretch.  (STEP_FIGURES)
 //
 // E4M3 codes become FP16, and the queries too, by a power of two of each row's own
 // (as in the decode kernel of the attention); keys' scales go to the scores in FP32.
@@ -51,7 +53,7 @@ FA_DEV long long slot_of(const WeighParams& p, int b, int head, int key) {
 constexpr int kStepThreads = 512;
 constexpr int kStepWarps = kStepThreads / 32;
 constexpr int kStepKeys = 16;
-constexpr int kStepRows = 16;        // most rows of a sequence and key/value head here
+constexpr int kStepRows = 32;        // most rows of a sequence and key/value head here
 
 FA_DEV void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -79,11 +81,57 @@ FA_DEV uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
+// 16 bytes from global to shared memory, past the L1 cache.
+FA_DEV void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(reinterpret_cast<uint64_t>(from)) : "memory");
+}
+FA_DEV void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+FA_DEV void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <int D, bool kFp8>
+struct StepLayout {
+  static constexpr int kPieces = D * (kFp8 ? 1 : 2) / 64;     // of 16 bytes of a key that a lane has
+  static constexpr int kTile = kStepKeys * kPieces * 64;
+  // behind a stage's keys: their scales, their sums so far, their row
+  static constexpr int kScales = kTile, kOld = kTile + 16, kRow = kTile + 80;
+  static constexpr int kStage = kTile + 128;
+  static constexpr int kRing = 212992;
+  static constexpr int kFit = kRing / (kStepWarps * kStage);
+  static constexpr int kDepth = kFit < 8 ? kFit : 8;
+  static constexpr int kBytes = kStepWarps * kDepth * kStage;
+};
+
+// A walk over a warp's stretch of the line, tile by tile.
+struct Walk {
+  paged::SeqRows q;
+  int b, head, k, tiles;      // tile k of `tiles` of a unit
+  long long left;             // tiles from here on
+  // To the next tile; whether it is another unit's.
+  FA_DEV bool next(const WeighParams& p) {
+    --left;
+    if (++k < tiles || left == 0) return false;
+    k = 0;
+    if (++head == p.s.Hkv) {
+      head = 0;
+      do {
+        ++b;                  // (one with tiles follows)
+        q = paged::rows_of(p.s, b);
+        tiles = q.n > 0 ? (q.L + kStepKeys - 1) / kStepKeys : 0;
+      } while (tiles == 0);
+    }
+    return true;
+  }
+};
+
 template <int D, bool kFp8, int kTiles>
 __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const WeighParams p) {
-  // pieces of 16 bytes of a key that a lane has: piece 4 i + c of the row
-  constexpr int kPieces = D * (kFp8 ? 1 : 2) / 64;
-  constexpr int kAhead = 2;            // tiles whose keys are loaded together
+  using Lay = StepLayout<D, kFp8>;
+  constexpr int kPieces = Lay::kPieces;
+  constexpr int kWords = kFp8 ? 2 * kPieces : kPieces;        // of 16 bytes of a row of Q
+  extern __shared__ __align__(128) uint8_t ring_raw[];
   __shared__ long long pre[kMaxPackedSeqs + 1];
   __shared__ long long work_sums[2 * kStepWarps];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -102,175 +150,191 @@ __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const WeighParams
   }
   const long long total = pre[p.s.B];
   const int warps = gridDim.x * kStepWarps, id = warp * gridDim.x + blockIdx.x;
-  long long t = paged::div64(total * id, warps);
-  const long long t1 = paged::div64(total * (id + 1), warps);
-  if (t >= t1) return;
-  int b;
+  const long long t0 = paged::div64(total * id, warps);
+  Walk at;
+  at.left = paged::div64(total * (id + 1), warps) - t0;
+  if (at.left == 0) return;
   {
-    int lo = 0, hi = p.s.B - 1;      // last b with pre[b] <= t
+    int lo = 0, hi = p.s.B - 1;      // last b with pre[b] <= t0
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (pre[mid] <= t) lo = mid; else hi = mid - 1;
+      if (pre[mid] <= t0) lo = mid; else hi = mid - 1;
     }
-    b = lo;
+    at.b = lo;
+    at.q = paged::rows_of(p.s, lo);
+    at.tiles = (at.q.L + kStepKeys - 1) / kStepKeys;
+    at.head = (int)paged::div64(t0 - pre[lo], at.tiles);
+    at.k = (int)(t0 - pre[lo] - (long long)at.head * at.tiles);
   }
-  paged::SeqRows q = paged::rows_of(p.s, b);
-  int tiles = (q.L + kStepKeys - 1) / kStepKeys;
-  int head = (int)paged::div64(t - pre[b], tiles);
-  int k = (int)(t - pre[b] - (long long)head * tiles);
-  const int least_exp = 14 + max(0, 127 - (int)(__float_as_uint(p.scale) >> 23));
 
-  for (;;) {
-    // ---- a segment: tiles [k, end) of (b, head)
-    const int end = (int)min((long long)tiles, k + (t1 - t));
-    const int rows = q.n * p.group, past = q.L - q.n;
-    uint4 qf[kTiles][kFp8 ? 2 * kPieces : kPieces];      // row 8 n + g, as the keys' pieces lie
-    float row_scale[kTiles][2], lse[kTiles][2];          // of rows 8 n + 2 c + e
-    int lim[kTiles][2];                                  // keys that they see
-#pragma unroll
-    for (int n = 0; n < kTiles; ++n) {
-      const int r = 8 * n + g, tok = r / p.group;
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                                        ((size_t)(q.q0 + tok) * p.Hq + head * p.group + r - tok * p.group) * D);
-      constexpr int kWords = kFp8 ? 2 * kPieces : kPieces;
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) {
-        qf[n][i] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < rows) qf[n][i] = src[kFp8 ? 8 * (i / 2) + 2 * c + i % 2 : 4 * i + c];
+  uint8_t* ring = ring_raw + warp * Lay::kDepth * Lay::kStage;
+  Walk ahead = at;                                     // the tile that is copied next
+  int held = -64, pages = -1;                          // its unit's pages [held, held + 32), one a lane
+  auto copy = [&](int stage) {
+    if (ahead.left > 0) {
+      const int key0 = ahead.k * kStepKeys, page_at = key0 >> p.s.page_shift;
+      if (page_at >= held + 32 || page_at < held) {
+        held = page_at;
+        pages = held + lane <= (ahead.q.L - 1) >> p.s.page_shift
+                    ? p.s.block_table[(size_t)ahead.b * p.s.max_pages + held + lane]
+                    : -1;
       }
-      float scale = p.scale;
-      if (kFp8) {
-        uint32_t top = 0u;
-#pragma unroll
-        for (int i = 0; i < kWords; ++i) {
-          const uint32_t v[4] = {qf[n][i].x, qf[n][i].y, qf[n][i].z, qf[n][i].w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) top = max(top, max(v[j] & 0x7FFFu, (v[j] >> 16) & 0x7FFFu));
-        }
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int e = max((int)(top >> 7), least_exp) - 127;
-        const float up = __uint_as_float((uint32_t)(127 + 13 - e) << 23);
-        scale *= __uint_as_float((uint32_t)(127 - 13 + e) << 23);
-#pragma unroll
-        for (int i = 0; i < kWords; ++i) {
-          uint32_t v[4] = {qf[n][i].x, qf[n][i].y, qf[n][i].z, qf[n][i].w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            v[j] = pack_f16x2(__uint_as_float(v[j] << 16) * up, __uint_as_float(v[j] & 0xFFFF0000u) * up);
-          qf[n][i] = make_uint4(v[0], v[1], v[2], v[3]);
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int row = 8 * n + 2 * c + e, tk = row / p.group;
-        row_scale[n][e] = kFp8 ? __shfl_sync(0xffffffffu, scale, (2 * c + e) * 4) : scale;
-        lim[n][e] = row >= rows ? 0 : p.causal ? past + tk + 1 : q.L;
-        lse[n][e] = row >= rows ? 0.0f : lse_of(p.lse[lse_at(p, b, q.q0, head * p.group + row - tk * p.group, tk)]);
-      }
-    }
-    const int* table = p.s.block_table + (size_t)b * p.s.max_pages;
-    const int last_page = (q.L - 1) >> p.s.page_shift;
-    int held = -64, pages = -1;                          // pages [held, held + 32), one a lane
-#pragma unroll 1
-    for (int k0 = k; k0 < end; k0 += kAhead) {
-      uint4 kf[kAhead][2][kPieces];                      // keys 16 tile + g, + 8
-      uint32_t byte[kAhead][2];
-      float old[kAhead];
-      long long slot[kAhead];                            // of the sum that this lane writes: key g + 8 c, c < 2
-#pragma unroll
-      for (int a = 0; a < kAhead; ++a) {
-        const int key0 = (k0 + a) * kStepKeys, at = key0 >> p.s.page_shift;
-        slot[a] = -1;
-        if (k0 + a >= end) continue;                     // (the whole warp)
-        if (at >= held + 32 || at < held) {
-          held = at;
-          pages = held + lane <= last_page ? table[held + lane] : -1;
-        }
-        int page = __shfl_sync(0xffffffffu, pages, at - held);
-        if (page < 0 || page >= p.s.num_pages) {
-          paged::record_bad_input(&g_err, kSitePage);
-          continue;
-        }
-        const long long row = ((long long)page * p.s.Hkv + head << p.s.page_shift) + (key0 & ((1 << p.s.page_shift) - 1));
+      const int page = __shfl_sync(0xffffffffu, pages, page_at - held);
+      uint8_t* to = ring + stage * Lay::kStage;
+      long long row = -1;
+      if (page < 0 || page >= p.s.num_pages) {
+        paged::record_bad_input(&g_err, kSitePage);
+      } else {
+        row = ((long long)page * p.s.Hkv + ahead.head << p.s.page_shift) + (key0 & ((1 << p.s.page_shift) - 1));
+        const uint32_t mine = smem_u32(to) + lane * 16;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint4* src = static_cast<const uint4*>(p.k_pages) + (row + g + 8 * h) * (4 * kPieces) + c;
 #pragma unroll
-          for (int i = 0; i < kPieces; ++i) kf[a][h][i] = src[4 * i];
-          if (kFp8) byte[a][h] = p.k_scale[row + g + 8 * h];
+          for (int i = 0; i < kPieces; ++i) copy16(mine + (h * kPieces + i) * 512, src + 4 * i);
         }
-        const int key = key0 + g + 8 * c;
-        if (c < 2 && key < q.L) {
-          slot[a] = row + g + 8 * c;
-          old[a] = p.decay != 0.0f && key < past ? p.sums[slot[a]] : 0.0f;
+        if (lane < 4) copy16(smem_u32(to) + Lay::kOld + lane * 16, p.sums + row + 4 * lane);
+        if (kFp8 && lane == 4) copy16(smem_u32(to) + Lay::kScales, p.k_scale + row);
+      }
+      if (lane == 0) *reinterpret_cast<long long*>(to + Lay::kRow) = row;
+      if (ahead.next(p)) held = -64;
+    }
+    copy_commit();
+  };
+#pragma unroll 1
+  for (int i = 0; i < Lay::kDepth; ++i) copy(i);
+
+  const int least_exp = 14 + max(0, 127 - (int)(__float_as_uint(p.scale) >> 23));
+  int stage = 0;
+  bool fresh = true;                                   // a unit begins
+  uint4 qf[kTiles][kWords];                            // row 8 n + g, as the keys' pieces lie
+  float row_scale[kTiles][2], lse[kTiles][2];          // of rows 8 n + 2 c + e
+  int lim[kTiles][2];                                  // keys that they see
+#pragma unroll 1
+  while (at.left > 0) {
+    const int past = at.q.L - at.q.n;
+    if (fresh) {
+      const int rows = at.q.n * p.group;
+#pragma unroll
+      for (int n = 0; n < kTiles; ++n) {
+        const int r = 8 * n + g, tok = r / p.group;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            static_cast<const __nv_bfloat16*>(p.q) +
+            ((size_t)(at.q.q0 + tok) * p.Hq + at.head * p.group + r - tok * p.group) * D);
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+          qf[n][i] = make_uint4(0u, 0u, 0u, 0u);
+          if (r < rows) qf[n][i] = src[kFp8 ? 8 * (i / 2) + 2 * c + i % 2 : 4 * i + c];
         }
       }
 #pragma unroll
-      for (int a = 0; a < kAhead; ++a) {
-        const int key0 = (k0 + a) * kStepKeys;
-        float w[2] = {0.0f, 0.0f};                       // of keys g, g + 8
-        float fac[2] = {1.0f, 1.0f};
+      for (int n = 0; n < kTiles; ++n) {
+        float scale = p.scale;
         if (kFp8) {
-          fac[0] = paged::scale_value(byte[a][0]);
-          fac[1] = paged::scale_value(byte[a][1]);
+          uint32_t top = 0u;
+#pragma unroll
+          for (int i = 0; i < kWords; ++i) {
+            const uint32_t v[4] = {qf[n][i].x, qf[n][i].y, qf[n][i].z, qf[n][i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) top = max(top, max(v[j] & 0x7FFFu, (v[j] >> 16) & 0x7FFFu));
+          }
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const int e = max((int)(top >> 7), least_exp) - 127;
+          const float up = __uint_as_float((uint32_t)(127 + 13 - e) << 23);
+          scale *= __uint_as_float((uint32_t)(127 - 13 + e) << 23);
+#pragma unroll
+          for (int i = 0; i < kWords; ++i) {
+            uint32_t v[4] = {qf[n][i].x, qf[n][i].y, qf[n][i].z, qf[n][i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              v[j] = pack_f16x2(__uint_as_float(v[j] << 16) * up, __uint_as_float(v[j] & 0xFFFF0000u) * up);
+            qf[n][i] = make_uint4(v[0], v[1], v[2], v[3]);
+          }
         }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int row = 8 * n + 2 * c + e, tk = row / p.group;
+          row_scale[n][e] = kFp8 ? __shfl_sync(0xffffffffu, scale, (2 * c + e) * 4) : scale;
+          lim[n][e] = row >= rows ? 0 : p.causal ? past + tk + 1 : at.q.L;
+          lse[n][e] =
+              row >= rows ? 0.0f : lse_of(p.lse[lse_at(p, at.b, at.q.q0, at.head * p.group + row - tk * p.group, tk)]);
+        }
+      }
+    }
+    copy_wait<Lay::kDepth - 1>();
+    __syncwarp();                                      // the other lanes' copies are here too
+    const uint8_t* from = ring + stage * Lay::kStage;
+    const int key0 = at.k * kStepKeys;
+    float fac[2] = {1.0f, 1.0f};
+    if (kFp8) {
+      fac[0] = paged::scale_value(from[Lay::kScales + g]);
+      fac[1] = paged::scale_value(from[Lay::kScales + g + 8]);
+    }
+    float s[kTiles][4];                                // [2 h + e]: key g + 8 h, row 8 n + 2 c + e
+#pragma unroll
+    for (int n = 0; n < kTiles; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const uint4 x = *reinterpret_cast<const uint4*>(from + i * 512 + lane * 16);
+      const uint4 y = *reinterpret_cast<const uint4*>(from + (kPieces + i) * 512 + lane * 16);
+      if (!kFp8) {
 #pragma unroll
         for (int n = 0; n < kTiles; ++n) {
-          float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};         // [2 h + e]: key g + 8 h, row 8 n + 2 c + e
+          mma16816(s[n], x.x, y.x, x.y, y.y, qf[n][i].x, qf[n][i].y);
+          mma16816(s[n], x.z, y.z, x.w, y.w, qf[n][i].z, qf[n][i].w);
+        }
+      } else {
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-          for (int i = 0; i < kPieces; ++i) {
-            const uint4 x = kf[a][0][i], y = kf[a][1][i];
-            if (!kFp8) {
-              mma16816(s, x.x, y.x, x.y, y.y, qf[n][i].x, qf[n][i].y);
-              mma16816(s, x.z, y.z, x.w, y.w, qf[n][i].z, qf[n][i].w);
-            } else {
-              const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-              const uint4 q0 = qf[n][2 * i], q1 = qf[n][2 * i + 1];
-              const uint32_t qs[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t a0 = e4m3_f16x2(xs[j]), a1 = e4m3_f16x2(ys[j]);
+          const uint32_t a2 = e4m3_f16x2(xs[j] >> 16), a3 = e4m3_f16x2(ys[j] >> 16);
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                mma16816_f16(s, e4m3_f16x2(xs[j]), e4m3_f16x2(ys[j]), e4m3_f16x2(xs[j] >> 16), e4m3_f16x2(ys[j] >> 16),
-                             qs[2 * j], qs[2 * j + 1]);
-            }
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            // taken from the LSE before it goes to log2 units: the difference is small
-            // where the weight is large, and so is its rounding
-            float x = kFp8 ? s[e] * fac[e >> 1] : s[e];
-            x = fmaf(x, row_scale[n][e & 1], -lse[n][e & 1]) * kLog2e;
-            w[e >> 1] += key0 + g + 8 * (e >> 1) < lim[n][e & 1] ? ex2_mufu(x) : 0.0f;
+          for (int n = 0; n < kTiles; ++n) {
+            const uint4 qw = qf[n][kFp8 ? 2 * i + j / 2 : 0];
+            mma16816_f16(s[n], a0, a1, a2, a3, j % 2 ? qw.z : qw.x, j % 2 ? qw.w : qw.y);
           }
         }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          w[h] += __shfl_xor_sync(0xffffffffu, w[h], 1);
-          w[h] += __shfl_xor_sync(0xffffffffu, w[h], 2);
-        }
-        if (slot[a] >= 0) p.sums[slot[a]] = p.decay * old[a] + (c ? w[1] : w[0]);
       }
     }
-    // ---- the next unit
-    t += end - k;
-    if (t >= t1) return;
-    k = 0;
-    if (++head == p.s.Hkv) {
-      head = 0;
-      do {
-        ++b;                                             // (one with tiles follows: t < t1)
-        q = paged::rows_of(p.s, b);
-        tiles = q.n > 0 ? (q.L + kStepKeys - 1) / kStepKeys : 0;
-      } while (tiles == 0);
+    float w[2] = {0.0f, 0.0f};                         // of keys g, g + 8
+#pragma unroll
+    for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        // taken from the LSE before it goes to log2 units: the difference is small
+        // where the weight is large, and so is its rounding
+        float x = kFp8 ? s[n][e] * fac[e >> 1] : s[n][e];
+        x = fmaf(x, row_scale[n][e & 1], -lse[n][e & 1]) * kLog2e;
+        w[e >> 1] += key0 + g + 8 * (e >> 1) < lim[n][e & 1] ? ex2_mufu(x) : 0.0f;
+      }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      w[h] += __shfl_xor_sync(0xffffffffu, w[h], 1);
+      w[h] += __shfl_xor_sync(0xffffffffu, w[h], 2);
     }
+    const long long row = *reinterpret_cast<const long long*>(from + Lay::kRow);
+    const int in = g + 8 * c;                          // lanes with c < 2 write a key's sum
+    if (c < 2 && key0 + in < at.q.L && row >= 0) {
+      const float old = *reinterpret_cast<const float*>(from + Lay::kOld + 4 * in);
+      p.sums[row + in] = (p.decay != 0.0f && key0 + in < past ? p.decay * old : 0.0f) + (c ? w[1] : w[0]);
+    }
+    __syncwarp();                                      // every lane is done with the stage
+    copy(stage);
+    stage = stage + 1 == Lay::kDepth ? 0 : stage + 1;
+    fresh = at.next(p);
   }
 }
 
 template <int D, bool kFp8>
 fa_status launch_step(const WeighParams& p, int num_sms, cudaStream_t stream) {
   const long long rows = (long long)p.max_q * p.group;
-  auto kernel = rows <= 8 ? step_kernel<D, kFp8, 1> : step_kernel<D, kFp8, 2>;
-  return launch_overlapped(kernel, dim3(num_sms), kStepThreads, 0, stream, p);
+  auto kernel = rows <= 8 ? step_kernel<D, kFp8, 1> : rows <= 16 ? step_kernel<D, kFp8, 2> : step_kernel<D, kFp8, 4>;
+  constexpr int kBytes = StepLayout<D, kFp8>::kBytes;
+  const fa_status st = prepare_kernel(reinterpret_cast<const void*>(kernel), kBytes);
+  if (st != FA_OK) return st;
+  return launch_overlapped(kernel, dim3(num_sms), kStepThreads, kBytes, stream, p);
 }
 
 // --------------------------------------------------------------- many rows --
