@@ -19,7 +19,7 @@ __device__ DeviceError g_err;
 constexpr float kLog2e = 1.4426950408889634f;
 
 enum Site { kSiteSeqs = 1, kSitePage, kSiteKEmpty, kSiteKFull, kSiteQEmpty, kSiteQFull, kSiteSEmpty, kSiteSFull,
-            kSiteLseEmpty, kSiteLseFull };
+            kSiteLseEmpty, kSiteLseFull, kSiteStep, kSiteUnitEmpty, kSiteUnitFull };
 
 FA_DEV size_t lse_at(const WeighParams& p, int b, int q0, int head, int tok) {
   return p.s.cu ? (size_t)head * p.s.Sn + q0 + tok : ((size_t)b * p.Hq + head) * p.s.Sn + tok;
@@ -40,19 +40,18 @@ FA_DEV long long slot_of(const WeighParams& p, int b, int head, int key) {
 // ---------------------------------------------------------------- few rows --
 // A step of single tokens reads every key once and computes little with it, so HBM
 // bounds it.  The keys are the M side of mma.sync products, 16 a tile, the rows the N
-// side, 8 a tile.  A product's sum may take its elements in any order, so each
-// lane's share of a key is whole pieces of 16 bytes, which the lane itself copies from
-// global memory ahead of their use, into its own places of a ring in shared memory:
-// a warp is on its own, with no barrier but its own lanes', and some 150 KB an SM are
-// under way.  All tiles of all (sequence, head) units form one line, of which every
-// warp takes an equal stretch.  (STEP_FIGURES)
+// side, 8 a tile.  A product's sum may take its elements in any order, so each lane's
+// share of a key is whole pieces of 16 bytes.  A head's rows of a page lie in one
+// piece, so that one bulk copy brings a tile of keys; each warp has a ring of its
+// own in shared memory and is on its own, and some 150 KB an SM are under way.  All
+// tiles of all (sequence, head) units form one line, of which every warp takes an equal
+// stretch.  (64 x 4096 keys, 8 heads, D = 128: E4M3 32 us of the bytes' 24, BF16 52 of 45.
+// Every lane loading its own pieces into registers, 64 ragged sequences up to 8192
+// E4M3 keys took 73 us; copying them to shared memory 60; so 57.)
 //
 // E4M3 codes become FP16, and the queries too, by a power of two of each row's own
 // (as in the decode kernel of the attention); keys' scales go to the scores in FP32.
 
-constexpr int kStepThreads = 512;
-constexpr int kStepWarps = kStepThreads / 32;
-constexpr int kStepKeys = 16;
 constexpr int kStepRows = 32;        // most rows of a sequence and key/value head here
 
 FA_DEV void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -81,27 +80,26 @@ FA_DEV uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
-// 16 bytes from global to shared memory, past the L1 cache.
-FA_DEV void copy16(uint32_t to, const void* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(reinterpret_cast<uint64_t>(from)) : "memory");
-}
-FA_DEV void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-FA_DEV void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-template <int D, bool kFp8>
+template <int D, bool kFp8, int kTiles>
 struct StepLayout {
+  static constexpr int kWarps = kTiles == 4 && D == 128 ? 8 : 16;      // (32 rows of Q in registers)
+  static constexpr int kThreads = 32 * kWarps;
   static constexpr int kPieces = D * (kFp8 ? 1 : 2) / 64;     // of 16 bytes of a key that a lane has
-  static constexpr int kTile = kStepKeys * kPieces * 64;
-  // behind a stage's keys: their scales, their sums so far, their row
-  static constexpr int kScales = kTile, kOld = kTile + 16, kRow = kTile + 80;
-  static constexpr int kStage = kTile + 128;
+  static constexpr int kRowBytes = 64 * kPieces;
+  static constexpr int kTile = 16 * kRowBytes;
+  // Tiles of a stage: two where they are small, which halves what goes with a stage.
+  static constexpr int kHalves = D == 128 && !kFp8 ? 1 : 2;
+  static constexpr int kKeys = 16 * kHalves;
+  // behind the keys: their sums so far, their scales, the halves' rows
+  static constexpr int kOld = kHalves * kTile, kScales = kOld + kHalves * 64, kRows = kScales + kHalves * 16;
+  static constexpr int kStage = (kRows + kHalves * 8 + 127) / 128 * 128;
   static constexpr int kRing = 212992;
-  static constexpr int kFit = kRing / (kStepWarps * kStage);
-  static constexpr int kDepth = kFit < 8 ? kFit : 8;
-  static constexpr int kBytes = kStepWarps * kDepth * kStage;
+  static constexpr int kFit = kRing / (kWarps * kStage);
+  static constexpr int kDepth = kFit < 6 ? kFit : 6;
+  static constexpr int kBars = kWarps * kDepth * kStage;  // [warp][stage]
+  static constexpr int kMisc = kBars + kWarps * kDepth * 8;
+  static constexpr int kBytes = kMisc + 16;
+  static constexpr int kHalfBytes = kTile + 64 + (kFp8 ? 16 : 0);
 };
 
 // A walk over a warp's stretch of the line, tile by tile.
@@ -110,6 +108,7 @@ struct Walk {
   int b, head, k, tiles;      // tile k of `tiles` of a unit
   long long left;             // tiles from here on
   // To the next tile; whether it is another unit's.
+  template <int kKeys>
   FA_DEV bool next(const WeighParams& p) {
     --left;
     if (++k < tiles || left == 0) return false;
@@ -119,7 +118,7 @@ struct Walk {
       do {
         ++b;                  // (one with tiles follows)
         q = paged::rows_of(p.s, b);
-        tiles = q.n > 0 ? (q.L + kStepKeys - 1) / kStepKeys : 0;
+        tiles = q.n > 0 ? (q.L + kKeys - 1) / kKeys : 0;
       } while (tiles == 0);
     }
     return true;
@@ -127,20 +126,24 @@ struct Walk {
 };
 
 template <int D, bool kFp8, int kTiles>
-__global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const WeighParams p) {
-  using Lay = StepLayout<D, kFp8>;
-  constexpr int kPieces = Lay::kPieces;
+__global__ void __launch_bounds__(StepLayout<D, kFp8, kTiles>::kThreads, 1) step_kernel(const WeighParams p) {
+  using Lay = StepLayout<D, kFp8, kTiles>;
+  constexpr int kPieces = Lay::kPieces, kHalves = Lay::kHalves, kKeys = Lay::kKeys;
   constexpr int kWords = kFp8 ? 2 * kPieces : kPieces;        // of 16 bytes of a row of Q
   extern __shared__ __align__(128) uint8_t ring_raw[];
   __shared__ long long pre[kMaxPackedSeqs + 1];
-  __shared__ long long work_sums[2 * kStepWarps];
+  __shared__ long long work_sums[2 * Lay::kWarps];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int c = lane % 4, g = lane / 4;
+  const uint32_t bars = smem_u32(ring_raw) + Lay::kBars + warp * Lay::kDepth * 8, abort = smem_u32(ring_raw) + Lay::kMisc;
+  if (lane < Lay::kDepth) mbar_init(bars + 8 * lane, 1);
+  if (threadIdx.x == 0) st_shared(abort, 0);
+  fence_barrier_init();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const bool ok = paged::prefix_sequences(
       p.s, p.max_q,
       [&](const paged::SeqRows& r) {
-        return paged::Work{(long long)p.s.Hkv * ((r.L + kStepKeys - 1) / kStepKeys), 0, 0};
+        return paged::Work{(long long)p.s.Hkv * ((r.L + kKeys - 1) / kKeys), 0, 0};
       },
       pre, nullptr, work_sums);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -149,7 +152,7 @@ __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const WeighParams
     return;
   }
   const long long total = pre[p.s.B];
-  const int warps = gridDim.x * kStepWarps, id = warp * gridDim.x + blockIdx.x;
+  const int warps = gridDim.x * Lay::kWarps, id = warp * gridDim.x + blockIdx.x;
   const long long t0 = paged::div64(total * id, warps);
   Walk at;
   at.left = paged::div64(total * (id + 1), warps) - t0;
@@ -162,7 +165,7 @@ __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const WeighParams
     }
     at.b = lo;
     at.q = paged::rows_of(p.s, lo);
-    at.tiles = (at.q.L + kStepKeys - 1) / kStepKeys;
+    at.tiles = (at.q.L + kKeys - 1) / kKeys;
     at.head = (int)paged::div64(t0 - pre[lo], at.tiles);
     at.k = (int)(t0 - pre[lo] - (long long)at.head * at.tiles);
   }
@@ -170,45 +173,46 @@ __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const WeighParams
   uint8_t* ring = ring_raw + warp * Lay::kDepth * Lay::kStage;
   Walk ahead = at;                                     // the tile that is copied next
   int held = -64, pages = -1;                          // its unit's pages [held, held + 32), one a lane
+  // what a lane copies of a stage: a half's keys, sums or scales
+  const int half = lane / 3, what = lane % 3;
+  const uint32_t copy_to = what == 0 ? half * Lay::kTile : what == 1 ? Lay::kOld + half * 64 : Lay::kScales + half * 16;
+  const char* copy_from = what == 0 ? static_cast<const char*>(p.k_pages)
+                          : what == 1 ? reinterpret_cast<const char*>(p.sums)
+                                      : reinterpret_cast<const char*>(p.k_scale);
+  const uint32_t copy_row = what == 0 ? Lay::kRowBytes : what == 1 ? 4 : 1;      // bytes of a key
+  const bool copies = lane < 3 * kHalves && (kFp8 || what != 2);
   auto copy = [&](int stage) {
-    if (ahead.left > 0) {
-      const int key0 = ahead.k * kStepKeys, page_at = key0 >> p.s.page_shift;
-      if (page_at >= held + 32 || page_at < held) {
-        held = page_at;
-        pages = held + lane <= (ahead.q.L - 1) >> p.s.page_shift
-                    ? p.s.block_table[(size_t)ahead.b * p.s.max_pages + held + lane]
-                    : -1;
-      }
-      const int page = __shfl_sync(0xffffffffu, pages, page_at - held);
-      uint8_t* to = ring + stage * Lay::kStage;
-      long long row = -1;
-      if (page < 0 || page >= p.s.num_pages) {
-        paged::record_bad_input(&g_err, kSitePage);
-      } else {
-        row = ((long long)page * p.s.Hkv + ahead.head << p.s.page_shift) + (key0 & ((1 << p.s.page_shift) - 1));
-        const uint32_t mine = smem_u32(to) + lane * 16;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint4* src = static_cast<const uint4*>(p.k_pages) + (row + g + 8 * h) * (4 * kPieces) + c;
-#pragma unroll
-          for (int i = 0; i < kPieces; ++i) copy16(mine + (h * kPieces + i) * 512, src + 4 * i);
-        }
-        if (lane < 4) copy16(smem_u32(to) + Lay::kOld + lane * 16, p.sums + row + 4 * lane);
-        if (kFp8 && lane == 4) copy16(smem_u32(to) + Lay::kScales, p.k_scale + row);
-      }
-      if (lane == 0) *reinterpret_cast<long long*>(to + Lay::kRow) = row;
-      if (ahead.next(p)) held = -64;
+    if (ahead.left == 0) return;
+    const int key0 = ahead.k * kKeys, page_at = key0 >> p.s.page_shift;
+    if (page_at >= held + 31 || page_at < held) {      // (two pages at most)
+      held = page_at;
+      pages = held + lane <= (ahead.q.L - 1) >> p.s.page_shift
+                  ? p.s.block_table[(size_t)ahead.b * p.s.max_pages + held + lane]
+                  : -1;
     }
-    copy_commit();
+    const int key = key0 + 16 * half;
+    const int page = __shfl_sync(0xffffffffu, pages, (key >> p.s.page_shift) - held);
+    const bool mine = copies && key < ahead.q.L;
+    const bool good = mine && (unsigned)page < (unsigned)p.s.num_pages;
+    if (mine && !good) paged::record_bad_input(&g_err, kSitePage);
+    const long long row = ((long long)page * p.s.Hkv + ahead.head << p.s.page_shift) + (key & ((1 << p.s.page_shift) - 1));
+    uint8_t* to = ring + stage * Lay::kStage;
+    if (copies && what == 0) *reinterpret_cast<long long*>(to + Lay::kRows + 8 * half) = good ? row : -1;
+    const int halves = __popc(__ballot_sync(0xffffffffu, good && what == 0));
+    if (lane == 0) mbar_arrive_expect_tx(bars + 8 * stage, halves * Lay::kHalfBytes);
+    __syncwarp();
+    if (good) bulk_load(smem_u32(to) + copy_to, copy_from + row * copy_row, 16 * copy_row, bars + 8 * stage);
+    if (ahead.next<kKeys>(p)) held = -64;
   };
 #pragma unroll 1
   for (int i = 0; i < Lay::kDepth; ++i) copy(i);
 
   const int least_exp = 14 + max(0, 127 - (int)(__float_as_uint(p.scale) >> 23));
   int stage = 0;
+  uint32_t phase = 0;
   bool fresh = true;                                   // a unit begins
   uint4 qf[kTiles][kWords];                            // row 8 n + g, as the keys' pieces lie
-  float row_scale[kTiles][2], lse[kTiles][2];          // of rows 8 n + 2 c + e
+  float row_scale[kTiles][2], nlse[kTiles][2];         // of rows 8 n + 2 c + e
   int lim[kTiles][2];                                  // keys that they see
 #pragma unroll 1
   while (at.left > 0) {
@@ -257,84 +261,109 @@ __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const WeighParams
           const int row = 8 * n + 2 * c + e, tk = row / p.group;
           row_scale[n][e] = kFp8 ? __shfl_sync(0xffffffffu, scale, (2 * c + e) * 4) : scale;
           lim[n][e] = row >= rows ? 0 : p.causal ? past + tk + 1 : at.q.L;
-          lse[n][e] =
-              row >= rows ? 0.0f : lse_of(p.lse[lse_at(p, at.b, at.q.q0, at.head * p.group + row - tk * p.group, tk)]);
+          nlse[n][e] =
+              row >= rows ? 0.0f : -lse_of(p.lse[lse_at(p, at.b, at.q.q0, at.head * p.group + row - tk * p.group, tk)]);
         }
       }
     }
-    copy_wait<Lay::kDepth - 1>();
-    __syncwarp();                                      // the other lanes' copies are here too
-    const uint8_t* from = ring + stage * Lay::kStage;
-    const int key0 = at.k * kStepKeys;
-    float fac[2] = {1.0f, 1.0f};
-    if (kFp8) {
-      fac[0] = paged::scale_value(from[Lay::kScales + g]);
-      fac[1] = paged::scale_value(from[Lay::kScales + g + 8]);
+    if (!paged::wait_warp(bars + 8 * stage, phase, abort, &g_err, kSiteStep, p.wait_limit_ns)) {
+      // what is under way lands before the memory that it targets is released
+      const uint64_t w0 = globaltimer_ns();
+      while (globaltimer_ns() - w0 < 2000000ull) __nanosleep(1000);
+      return;
     }
-    float s[kTiles][4];                                // [2 h + e]: key g + 8 h, row 8 n + 2 c + e
 #pragma unroll
-    for (int n = 0; n < kTiles; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+    for (int half = 0; half < kHalves; ++half) {
+      const uint8_t* from = ring + stage * Lay::kStage + half * Lay::kTile + g * Lay::kRowBytes + c * 16;
+      const uint8_t* stats = ring + stage * Lay::kStage;
+      const int key0 = at.k * kKeys + 16 * half;
+      float s[kTiles][4];                              // [2 h + e]: key g + 8 h, row 8 n + 2 c + e
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const uint4 x = *reinterpret_cast<const uint4*>(from + i * 512 + lane * 16);
-      const uint4 y = *reinterpret_cast<const uint4*>(from + (kPieces + i) * 512 + lane * 16);
-      if (!kFp8) {
+      for (int n = 0; n < kTiles; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
 #pragma unroll
-        for (int n = 0; n < kTiles; ++n) {
-          mma16816(s[n], x.x, y.x, x.y, y.y, qf[n][i].x, qf[n][i].y);
-          mma16816(s[n], x.z, y.z, x.w, y.w, qf[n][i].z, qf[n][i].w);
-        }
-      } else {
-        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t a0 = e4m3_f16x2(xs[j]), a1 = e4m3_f16x2(ys[j]);
-          const uint32_t a2 = e4m3_f16x2(xs[j] >> 16), a3 = e4m3_f16x2(ys[j] >> 16);
+      for (int i = 0; i < kPieces; ++i) {
+        const uint4 x = *reinterpret_cast<const uint4*>(from + i * 64);
+        const uint4 y = *reinterpret_cast<const uint4*>(from + 8 * Lay::kRowBytes + i * 64);
+        if (!kFp8) {
 #pragma unroll
           for (int n = 0; n < kTiles; ++n) {
-            const uint4 qw = qf[n][kFp8 ? 2 * i + j / 2 : 0];
-            mma16816_f16(s[n], a0, a1, a2, a3, j % 2 ? qw.z : qw.x, j % 2 ? qw.w : qw.y);
+            mma16816(s[n], x.x, y.x, x.y, y.y, qf[n][i].x, qf[n][i].y);
+            mma16816(s[n], x.z, y.z, x.w, y.w, qf[n][i].z, qf[n][i].w);
+          }
+        } else {
+          const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t a0 = e4m3_f16x2(xs[j]), a1 = e4m3_f16x2(ys[j]);
+            const uint32_t a2 = e4m3_f16x2(xs[j] >> 16), a3 = e4m3_f16x2(ys[j] >> 16);
+#pragma unroll
+            for (int n = 0; n < kTiles; ++n) {
+              const uint4 qw = qf[n][kFp8 ? 2 * i + j / 2 : 0];
+              mma16816_f16(s[n], a0, a1, a2, a3, j % 2 ? qw.z : qw.x, j % 2 ? qw.w : qw.y);
+            }
           }
         }
       }
-    }
-    float w[2] = {0.0f, 0.0f};                         // of keys g, g + 8
+      float w[2];                                      // of keys g, g + 8
 #pragma unroll
-    for (int n = 0; n < kTiles; ++n)
+      for (int h = 0; h < 2; ++h) {
+        // (a row that stands for NaN has codes of zero and the byte 255, which is
+        // infinity here: its scores are NaN)
+        const float fac = kFp8 ? __uint_as_float((uint32_t)stats[Lay::kScales + 16 * half + g + 8 * h] << 23) : 1.0f;
+        uint64_t sum2 = 0ull;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        // taken from the LSE before it goes to log2 units: the difference is small
-        // where the weight is large, and so is its rounding
-        float x = kFp8 ? s[n][e] * fac[e >> 1] : s[n][e];
-        x = fmaf(x, row_scale[n][e & 1], -lse[n][e & 1]) * kLog2e;
-        w[e >> 1] += key0 + g + 8 * (e >> 1) < lim[n][e & 1] ? ex2_mufu(x) : 0.0f;
+        for (int n = 0; n < kTiles; ++n) {
+          // taken from the LSE before it goes to log2 units: the difference is small
+          // where the weight is large, and so is its rounding
+          uint64_t x2 = pk2(s[n][2 * h], s[n][2 * h + 1]);
+          if (kFp8) x2 = mul2(x2, pk2(fac, fac));
+          x2 = mul2(fma2(x2, pk2(row_scale[n][0], row_scale[n][1]), pk2(nlse[n][0], nlse[n][1])), pk2(kLog2e, kLog2e));
+          float x0, x1;
+          up2(x2, x0, x1);
+          const int key = key0 + g + 8 * h;
+          sum2 = add2(sum2, pk2(key < lim[n][0] ? ex2_mufu(x0) : 0.0f, key < lim[n][1] ? ex2_mufu(x1) : 0.0f));
+        }
+        float a, b;
+        up2(sum2, a, b);
+        w[h] = a + b;
       }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      w[h] += __shfl_xor_sync(0xffffffffu, w[h], 1);
-      w[h] += __shfl_xor_sync(0xffffffffu, w[h], 2);
-    }
-    const long long row = *reinterpret_cast<const long long*>(from + Lay::kRow);
-    const int in = g + 8 * c;                          // lanes with c < 2 write a key's sum
-    if (c < 2 && key0 + in < at.q.L && row >= 0) {
-      const float old = *reinterpret_cast<const float*>(from + Lay::kOld + 4 * in);
-      p.sums[row + in] = (p.decay != 0.0f && key0 + in < past ? p.decay * old : 0.0f) + (c ? w[1] : w[0]);
+      // over the four lanes of a key; lanes with an odd c end up with key g + 8, the
+      // others with key g
+      float sum = c & 1 ? w[1] : w[0];
+      sum += __shfl_xor_sync(0xffffffffu, c & 1 ? w[0] : w[1], 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      const long long row = *reinterpret_cast<const long long*>(stats + Lay::kRows + 8 * half);
+      const int in = g + 8 * c;                        // lanes with c < 2 write a key's sum
+      if (c < 2 && key0 + in < at.q.L && row >= 0) {
+        const float old = *reinterpret_cast<const float*>(stats + Lay::kOld + 64 * half + 4 * in);
+        p.sums[row + in] = fmaf(p.decay, p.decay != 0.0f && key0 + in < past ? old : 0.0f, sum);
+      }
     }
     __syncwarp();                                      // every lane is done with the stage
     copy(stage);
-    stage = stage + 1 == Lay::kDepth ? 0 : stage + 1;
-    fresh = at.next(p);
+    if (++stage == Lay::kDepth) {
+      stage = 0;
+      phase ^= 1;
+    }
+    fresh = at.next<kKeys>(p);
   }
+}
+
+template <int D, bool kFp8, int kTiles>
+fa_status launch_tiles(const WeighParams& p, int num_sms, cudaStream_t stream) {
+  using Lay = StepLayout<D, kFp8, kTiles>;
+  auto kernel = step_kernel<D, kFp8, kTiles>;
+  const fa_status st = prepare_kernel(reinterpret_cast<const void*>(kernel), Lay::kBytes);
+  if (st != FA_OK) return st;
+  return launch_overlapped(kernel, dim3(num_sms), Lay::kThreads, Lay::kBytes, stream, p);
 }
 
 template <int D, bool kFp8>
 fa_status launch_step(const WeighParams& p, int num_sms, cudaStream_t stream) {
   const long long rows = (long long)p.max_q * p.group;
-  auto kernel = rows <= 8 ? step_kernel<D, kFp8, 1> : rows <= 16 ? step_kernel<D, kFp8, 2> : step_kernel<D, kFp8, 4>;
-  constexpr int kBytes = StepLayout<D, kFp8>::kBytes;
-  const fa_status st = prepare_kernel(reinterpret_cast<const void*>(kernel), kBytes);
-  if (st != FA_OK) return st;
-  return launch_overlapped(kernel, dim3(num_sms), kStepThreads, kBytes, stream, p);
+  return rows <= 8    ? launch_tiles<D, kFp8, 1>(p, num_sms, stream)
+         : rows <= 16 ? launch_tiles<D, kFp8, 2>(p, num_sms, stream)
+                      : launch_tiles<D, kFp8, 4>(p, num_sms, stream);
 }
 
 // --------------------------------------------------------------- many rows --
@@ -346,19 +375,33 @@ fa_status launch_step(const WeighParams& p, int num_sms, cudaStream_t stream) {
 // exponential, 16 a clock and SM.
 //
 // Warps: 0-3 and 4-7 exponentials of the first and second 128 keys, 8 loads (Q; K of
-// BF16 pages), 9 MMA issue, 10 the rows' LSE, 11-14 widening (E4M3 pages: codes and
-// scale to BF16, exactly, once per unit).
+// BF16 pages), 9 MMA issue, 10 the rows' LSE, 11 units (works out the next ones, looks
+// their pages up and has their old sums copied, ahead of the others), 12-15 widening
+// (E4M3 pages: codes and scale to BF16, exactly, once per unit).
 //
 // Tensor memory: scores of the first keys at columns 0 and 128, of the second at 256
 // and 384.
 
 constexpr int kBM = 128, kBN = 128;
 constexpr int kUnitKeys = 2 * kBM;
-constexpr int kLses = 4;
+constexpr int kLses = 4, kUnits = 4;
+
+// 256 keys of a (sequence, head), and the tiles of rows that see some of them, as the
+// roles get them.
+struct Unit {
+  int b, head, key0;     // b < 0: no more work
+  int n, past, q0, L;
+  int tile0, tiles;      // of tt tokens each
+  int pad[3];
+  long long row[kUnitKeys / 16];      // of every 16 keys' first; -1: behind the end, or in a bad page
+  float old[kUnitKeys];
+  FA_DEV bool two() const { return key0 + kBM < L; }
+};
 
 template <int D, bool kFp8>
 struct Layout {
-  static constexpr int kThreads = kFp8 ? 480 : 352;
+  static constexpr int kThreads = kFp8 ? 512 : 384;
+  static constexpr int kReaders = kFp8 ? 15 : 11;           // warps that take units
   static constexpr int kChunks = D / 64;
   static constexpr int kChunkBytes = 128 * 128;             // 128 rows by 64 columns
   static constexpr int kTileBytes = kChunks * kChunkBytes;
@@ -366,10 +409,11 @@ struct Layout {
   static constexpr int kK = 0;                              // [2][two tiles]
   static constexpr int kQ = kK + 4 * kTileBytes;
   static constexpr int kLse = kQ + kQStages * kTileBytes;   // [kLses][kBN]
-  static constexpr int kPre = kLse + kLses * kBN * 4;       // prefix of units, [B + 1], 64 bits
+  static constexpr int kUnitRing = kLse + kLses * kBN * 4;
+  static constexpr int kPre = kUnitRing + kUnits * (int)sizeof(Unit);      // prefix of units, [B + 1], 64 bits
   static constexpr int kSums = kPre + (kMaxPackedSeqs + 1) * 8;
   static constexpr int kBars = kSums + 32 * 16;
-  static constexpr int kNumBars = 4 + 2 * kQStages + 8 + 2 * kLses;
+  static constexpr int kNumBars = 4 + 2 * kQStages + 8 + 2 * kLses + 2 * kUnits;
   static constexpr int kMisc = kBars + kNumBars * 8;
   static constexpr int kBytes = kMisc + 64 + kSmemAlignSlack;
   static_assert(kBytes <= 232448, "dynamic shared memory above the 227 KB per-CTA limit");
@@ -389,6 +433,9 @@ struct Shared {
   FA_DEV uint32_t s_empty(int m, int i) const { return bar(8 + 2 * L::kQStages + 2 * m + i); }
   FA_DEV uint32_t lse_full(int i) const { return bar(12 + 2 * L::kQStages + i); }
   FA_DEV uint32_t lse_empty(int i) const { return bar(12 + 2 * L::kQStages + kLses + i); }
+  FA_DEV uint32_t unit_full(int i) const { return bar(12 + 2 * L::kQStages + 2 * kLses + i); }
+  FA_DEV uint32_t unit_empty(int i) const { return bar(12 + 2 * L::kQStages + 2 * kLses + kUnits + i); }
+  FA_DEV Unit* unit(int i) const { return reinterpret_cast<Unit*>(base + L::kUnitRing) + i; }
   FA_DEV const long long* pre() const { return reinterpret_cast<const long long*>(base + L::kPre); }
   FA_DEV float* lse(int i) const { return reinterpret_cast<float*>(base + L::kLse) + i * kBN; }
   FA_DEV uint32_t abort() const { return sbase + L::kMisc + 4; }
@@ -400,7 +447,7 @@ struct Shared {
   // wait for a tile at a time, and give up first if nothing moves).
   FA_DEV bool wait_long(uint32_t b, uint32_t parity, int site, const WeighParams& p) const {
 #pragma unroll 1
-    for (int i = 0; i < (1 << 27) && !mbar_try_wait(b, parity) && !ld_shared_volatile(abort()); ++i) __nanosleep(100);
+    for (int i = 0; i < (1 << 27) && !mbar_try_wait(b, parity) && !ld_shared_volatile(abort()); ++i) __nanosleep(50);
     return wait(b, parity, site, p);
   }
 };
@@ -418,75 +465,118 @@ struct Ring {
   }
 };
 
-// 256 keys of a (sequence, head), and the tiles of rows that see some of them.
-struct Unit {
-  int b, head, key0;
-  int n, past, q0, L;
-  int tile0, tiles;      // of tt tokens each
-  FA_DEV bool two() const { return key0 + kBM < L; }
-};
 FA_DEV int units_of(int L) { return (L + kUnitKeys - 1) / kUnitKeys; }
-FA_DEV Unit unit_at(const WeighParams& p, const long long* pre, long long u) {
-  int lo = 0, hi = p.s.B - 1;      // last b with pre[b] <= u
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (pre[mid] <= u) lo = mid; else hi = mid - 1;
-  }
-  const paged::SeqRows r = paged::rows_of(p.s, lo);
-  Unit w;
-  w.b = lo;
-  const int block = (int)paged::div64(u - pre[lo], p.s.Hkv);      // the first keys, which most rows see, come first
-  w.head = (int)(u - pre[lo] - (long long)block * p.s.Hkv);
-  w.key0 = block * kUnitKeys;
-  w.n = r.n;
-  w.L = r.L;
-  w.past = r.L - r.n;
-  w.q0 = r.q0;
+
+// Works out this thread block's units, every gridDim.x-th.
+template <int D, bool kFp8>
+__device__ void unit_role(const Shared<D, kFp8>& sh, const WeighParams& p, long long units) {
+  const int lane = threadIdx.x % 32;
   const int tt = kBN / p.group;
-  w.tile0 = p.causal ? max(0, w.key0 - w.past) / tt : 0;          // (the first key is seen by the last row at least)
-  w.tiles = (w.n + tt - 1) / tt - w.tile0;
-  return w;
+  const long long* pre = sh.pre();
+  Ring<kUnits> r;
+  for (long long u = blockIdx.x;; u += gridDim.x) {
+    if (!sh.wait_long(sh.unit_empty(r.i), r.phase ^ 1, kSiteUnitEmpty, p)) return;
+    Unit* to = sh.unit(r.i);
+    if (u >= units) {
+      if (lane == 0) {
+        to->b = -1;
+        mbar_arrive(sh.unit_full(r.i));
+      }
+      return;
+    }
+    int lo = 0, hi = p.s.B - 1;      // last b with pre[b] <= u
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (pre[mid] <= u) lo = mid; else hi = mid - 1;
+    }
+    const paged::SeqRows q = paged::rows_of(p.s, lo);
+    const int block = (int)paged::div64(u - pre[lo], p.s.Hkv);      // the first keys, which most rows see, come first
+    const int head = (int)(u - pre[lo] - (long long)block * p.s.Hkv);
+    const int key = block * kUnitKeys + 16 * lane, past = q.L - q.n;
+    const bool some = lane < kUnitKeys / 16 && key < q.L;
+    const long long row = some ? slot_of(p, lo, head, key) : -1;
+    if (lane < kUnitKeys / 16) to->row[lane] = row;
+    const int copies = __popc(__ballot_sync(0xffffffffu, row >= 0));
+    __syncwarp();                    // the rows are written
+    if (lane == 0) {
+      to->b = lo;
+      to->head = head;
+      to->key0 = block * kUnitKeys;
+      to->n = q.n;
+      to->past = past;
+      to->q0 = q.q0;
+      to->L = q.L;
+      const int tile0 = p.causal ? max(0, block * kUnitKeys - past) / tt : 0;      // (the last row at least sees the first key)
+      to->tile0 = tile0;
+      to->tiles = (q.n + tt - 1) / tt - tile0;
+      mbar_arrive_expect_tx(sh.unit_full(r.i), copies * 64);
+    }
+    __syncwarp();
+    if (row >= 0) bulk_load(smem_u32(to->old + 16 * lane), p.sums + row, 64, sh.unit_full(r.i));
+    r.next();
+  }
 }
+
+// Takes units out of the ring.
+template <int D, bool kFp8>
+struct UnitReader {
+  const Shared<D, kFp8>& sh;
+  const WeighParams& p;
+  Ring<kUnits> r;
+  FA_DEV UnitReader(const Shared<D, kFp8>& s, const WeighParams& q) : sh(s), p(q) {}
+  // The next one; nullptr at the end of the work or after a give-up.  The whole warp
+  // calls it, and done() when it no longer needs the unit.
+  FA_DEV const Unit* next() {
+    if (!sh.wait_long(sh.unit_full(r.i), r.phase, kSiteUnitFull, p)) return nullptr;
+    const Unit* w = sh.unit(r.i);
+    return w->b < 0 ? nullptr : w;
+  }
+  FA_DEV void done() {
+    __syncwarp();
+    if (threadIdx.x % 32 == 0) mbar_arrive(sh.unit_empty(r.i));
+    r.next();
+  }
+};
+FA_DEV int all_same(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // Q tiles, and the keys of BF16 pages.
 template <int D, bool kFp8>
-__device__ void load_role(const Shared<D, kFp8>& sh, const CUtensorMap* tq, const CUtensorMap* tk, const WeighParams& p,
-                          long long units) {
+__device__ void load_role(const Shared<D, kFp8>& sh, const CUtensorMap* tq, const CUtensorMap* tk, const WeighParams& p) {
   using L = Layout<D, kFp8>;
   const int lane = threadIdx.x % 32;
   const int tt = kBN / p.group;
   const int box = min(1 << p.s.page_shift, kBM);
   Ring<2> kr;
   Ring<L::kQStages> qr;
-  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-    const Unit w = unit_at(p, sh.pre(), u);
+  UnitReader<D, kFp8> in(sh, p);
+  while (const Unit* w = in.next()) {
+    const int tiles = all_same(w->tiles), head = all_same(w->head), q0 = all_same(w->q0 + w->tile0 * tt);
     if (!kFp8) {
       if (!sh.wait(sh.k_empty(kr.i), kr.phase ^ 1, kSiteKEmpty, p)) return;
-      const int keys = min(kUnitKeys, w.L - w.key0), boxes = (keys + box - 1) / box;
+      const int keys = min(kUnitKeys, w->L - w->key0), boxes = (keys + box - 1) / box;
       if (lane == 0) mbar_arrive_expect_tx(sh.k_full(kr.i), boxes * box * 2 * D);
       __syncwarp();
       // each lane issues its own box of 64 columns
-      const int i = lane / L::kChunks, c = lane % L::kChunks;
-      for (int x = i; x < boxes; x += 32 / L::kChunks) {
-        const int key = w.key0 + x * box;
-        const int page = p.s.block_table[(size_t)w.b * p.s.max_pages + (key >> p.s.page_shift)];
-        const bool bad = page < 0 || page >= p.s.num_pages;
-        if (bad) paged::record_bad_input(&g_err, kSitePage);
-        tma_load_3d(sh.sbase + L::kK + (2 * kr.i + x * box / kBM) * L::kTileBytes + c * L::kChunkBytes + x * box % kBM * 128,
-                    tk, sh.k_full(kr.i), c * 64, key & ((1 << p.s.page_shift) - 1),
-                    bad ? -1 : page * p.s.Hkv + w.head);          // -1: reads as zeros
+      const int c = lane % L::kChunks;
+      for (int x = lane / L::kChunks; x < boxes; x += 32 / L::kChunks) {
+        const int row0 = x * box;
+        const long long row = w->row[row0 / 16];
+        tma_load_3d(sh.sbase + L::kK + (2 * kr.i + row0 / kBM) * L::kTileBytes + c * L::kChunkBytes + row0 % kBM * 128, tk,
+                    sh.k_full(kr.i), c * 64, row < 0 ? 0 : (int)(row & ((1 << p.s.page_shift) - 1)),
+                    row < 0 ? -1 : (int)(row >> p.s.page_shift));          // -1: reads as zeros
       }
       __syncwarp();
       kr.next();
     }
-    for (int t = 0; t < w.tiles; ++t) {
+    in.done();
+    for (int t = 0; t < tiles; ++t) {
       if (!sh.wait(sh.q_empty(qr.i), qr.phase ^ 1, kSiteQEmpty, p)) return;
       if (lane == 0) {
         mbar_arrive_expect_tx(sh.q_full(qr.i), tt * p.group * D * 2);
 #pragma unroll
         for (int c = 0; c < L::kChunks; ++c)
           tma_load_3d(sh.sbase + L::kQ + qr.i * L::kTileBytes + c * L::kChunkBytes, tq, sh.q_full(qr.i), c * 64,
-                      w.head * p.group, w.q0 + (w.tile0 + t) * tt);
+                      head * p.group, q0 + t * tt);
       }
       __syncwarp();
       qr.next();
@@ -494,9 +584,9 @@ __device__ void load_role(const Shared<D, kFp8>& sh, const CUtensorMap* tq, cons
   }
 }
 
-// The rows' LSE, 128 floats a tile.
+// The rows' LSE, negative, 128 floats a tile.
 template <int D, bool kFp8>
-__device__ void lse_role(const Shared<D, kFp8>& sh, const WeighParams& p, long long units) {
+__device__ void lse_role(const Shared<D, kFp8>& sh, const WeighParams& p) {
   const int lane = threadIdx.x % 32;
   const int tt = kBN / p.group;
   Ring<kLses> r;
@@ -506,16 +596,17 @@ __device__ void lse_role(const Shared<D, kFp8>& sh, const WeighParams& p, long l
     tok[i] = (lane + 32 * i) / p.group;
     head[i] = lane + 32 * i - tok[i] * p.group;
   }
-  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-    const Unit w = unit_at(p, sh.pre(), u);
-    for (int t = 0; t < w.tiles; ++t) {
+  UnitReader<D, kFp8> in(sh, p);
+  while (const Unit* u = in.next()) {
+    const int b = u->b, q0 = u->q0, head0 = u->head * p.group, n = u->n, tiles = all_same(u->tiles);
+    int tok0 = u->tile0 * tt;
+    in.done();
+    for (int t = 0; t < tiles; ++t, tok0 += tt) {
       float x[kBN / 32];
-      const int tok0 = (w.tile0 + t) * tt;
 #pragma unroll
       for (int i = 0; i < kBN / 32; ++i) {
         x[i] = 0.0f;
-        if (tok[i] < tt && tok0 + tok[i] < w.n)
-          x[i] = lse_of(p.lse[lse_at(p, w.b, w.q0, w.head * p.group + head[i], tok0 + tok[i])]);
+        if (tok[i] < tt && tok0 + tok[i] < n) x[i] = lse_of(p.lse[lse_at(p, b, q0, head0 + head[i], tok0 + tok[i])]);
       }
       if (!sh.wait(sh.lse_empty(r.i), r.phase ^ 1, kSiteLseEmpty, p)) return;
 #pragma unroll
@@ -531,20 +622,21 @@ __device__ void lse_role(const Shared<D, kFp8>& sh, const WeighParams& p, long l
 // power of two exactly.  Rows behind the sequence's end are left as they were: each
 // is a lane of the product of its own.
 template <int D>
-__device__ void widen_role(const Shared<D, true>& sh, const WeighParams& p, long long units) {
+__device__ void widen_role(const Shared<D, true>& sh, const WeighParams& p) {
   using L = Layout<D, true>;
   constexpr int kLanes = D / 16;                  // of a row
   constexpr int kRows = 128 / kLanes;             // at a time
-  constexpr int kUnroll = 4;
-  const int thread = threadIdx.x - 352;
+  constexpr int kUnroll = 8;
+  const int thread = threadIdx.x - 384;
   const int piece = thread % kLanes, row0 = thread / kLanes;
   Ring<2> r;
-  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-    const Unit w = unit_at(p, sh.pre(), u);
-    const int keys = min(kUnitKeys, w.L - w.key0);
-    if (!sh.wait_long(sh.k_empty(r.i), r.phase ^ 1, kSiteKEmpty, p)) return;
+  UnitReader<D, true> in(sh, p);
+  while (const Unit* w = in.next()) {
+    const int keys = min(kUnitKeys, w->L - w->key0);
+    // the codes are on their way while the products still read what was there before
+    bool empty = false;
 #pragma unroll 1
-    for (int i0 = row0; i0 < keys; i0 += kRows * kUnroll) {
+    for (int i0 = row0; i0 - row0 < keys; i0 += kRows * kUnroll) {
       uint4 x[kUnroll];
       uint32_t byte[kUnroll];
 #pragma unroll
@@ -552,12 +644,13 @@ __device__ void widen_role(const Shared<D, true>& sh, const WeighParams& p, long
         const int i = i0 + k * kRows;
         x[k] = make_uint4(0u, 0u, 0u, 0u);
         byte[k] = 127u;
-        if (i >= keys) continue;
-        const long long row = slot_of(p, w.b, w.head, w.key0 + i);
+        const long long row = i < keys ? w->row[i / 16] : -1;
         if (row < 0) continue;
-        x[k] = static_cast<const uint4*>(p.k_pages)[row * kLanes + piece];
-        byte[k] = p.k_scale[row];
+        x[k] = static_cast<const uint4*>(p.k_pages)[(row + i % 16) * kLanes + piece];
+        byte[k] = p.k_scale[row + i % 16];
       }
+      if (!empty && !sh.wait_long(sh.k_empty(r.i), r.phase ^ 1, kSiteKEmpty, p)) return;
+      empty = true;
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k) {
         const int i = i0 + k * kRows;
@@ -582,24 +675,24 @@ __device__ void widen_role(const Shared<D, true>& sh, const WeighParams& p, long
     fence_proxy_async_smem();
     __syncwarp();
     if (threadIdx.x % 32 == 0) mbar_arrive(sh.k_full(r.i));
+    in.done();
     r.next();
   }
 }
 
 // MMA issue (a converged warp, one elected lane).
 template <int D, bool kFp8>
-__device__ void mma_role(const Shared<D, kFp8>& sh, const uint32_t tmem, const WeighParams& p, long long units) {
+__device__ void mma_role(const Shared<D, kFp8>& sh, const uint32_t tmem, const WeighParams& p) {
   using L = Layout<D, kFp8>;
   constexpr uint32_t kId = idesc_bf16_f32(kBM, kBN, false, false);
   Ring<2> kr, sr[2];
   Ring<L::kQStages> qr;
-  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-    const Unit w = unit_at(p, sh.pre(), u);
-    const int tiles = __shfl_sync(0xffffffffu, w.tiles, 0);
-    const bool two = __shfl_sync(0xffffffffu, (int)w.two(), 0) != 0;
-    // (the keys of a unit are on their way while the one before is worked on, but E4M3's
-    // may be waited for as long as a unit takes)
-    if (!sh.wait_long(sh.k_full(kr.i), kr.phase, kSiteKFull, p)) return;
+  UnitReader<D, kFp8> in(sh, p);
+  while (const Unit* w = in.next()) {
+    const int tiles = all_same(w->tiles);
+    const bool two = all_same((int)w->two()) != 0;
+    in.done();
+    if (!sh.wait(sh.k_full(kr.i), kr.phase, kSiteKFull, p)) return;
     tc_fence_after();
     for (int t = 0; t < tiles; ++t) {
       if (!sh.wait(sh.q_full(qr.i), qr.phase, kSiteQFull, p)) return;
@@ -660,28 +753,27 @@ FA_DEV void add_weights(const uint32_t (&x)[32], const float* nlse, float scale,
 
 // Exponentials and sums of 128 keys of each unit, a thread a key.
 template <int D, bool kFp8>
-__device__ void sum_role(const int m, const Shared<D, kFp8>& sh, const uint32_t tmem, const WeighParams& p,
-                         long long units) {
+__device__ void sum_role(const int m, const Shared<D, kFp8>& sh, const uint32_t tmem, const WeighParams& p) {
   const int lane = threadIdx.x % 32, wq = threadIdx.x / 32 % 4;
   const int tt = kBN / p.group;
+  const int in_unit = m * kBM + wq * 32 + lane;
   Ring<2> sr;
   Ring<kLses> lr;
-  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-    const Unit w = unit_at(p, sh.pre(), u);
-    const int key = w.key0 + m * kBM + wq * 32 + lane;
-    const bool active = m == 0 || w.two();
-    long long slot = -1;
-    float old = 0.0f;
-    if (key < w.L) {
-      slot = slot_of(p, w.b, w.head, key);
-      if (slot >= 0 && p.decay != 0.0f && key < w.past) old = p.sums[slot];
-    }
+  UnitReader<D, kFp8> in(sh, p);
+  while (const Unit* w = in.next()) {
+    const int tiles = all_same(w->tiles);
+    const bool active = m == 0 || all_same((int)w->two()) != 0;
+    const int past_key = w->key0 + in_unit - w->past;      // the first token that sees the key
+    int tok0 = w->tile0 * tt;
+    const int n = w->n;
     uint64_t total2[2] = {0ull, 0ull};
-    for (int t = 0; t < w.tiles; ++t) {
-      const int tok0 = (w.tile0 + t) * tt;
-      const int hi = min(tt, w.n - tok0) * p.group;                                   // columns with a row
-      const int lo = p.causal ? max(0, key - w.past - tok0) * p.group : 0;            // first one that sees the key
-      if (!sh.wait_long(sh.lse_full(lr.i), lr.phase, kSiteLseFull, p)) return;
+    for (int t = 0; t < tiles; ++t, tok0 += tt) {
+      const int hi = min(tt, n - tok0) * p.group;                             // columns with a row
+      const int lo = p.causal ? max(0, past_key - tok0) * p.group : 0;        // first one that sees the key
+      // (a half without keys is here long before the other is done with a unit)
+      if (!(active ? sh.wait(sh.lse_full(lr.i), lr.phase, kSiteLseFull, p)
+                   : sh.wait_long(sh.lse_full(lr.i), lr.phase, kSiteLseFull, p)))
+        return;
       if (active) {
         if (!sh.wait(sh.s_full(m, sr.i), sr.phase, kSiteSFull, p)) return;
         tc_fence_after();
@@ -691,9 +783,8 @@ __device__ void sum_role(const int m, const Shared<D, kFp8>& sh, const uint32_t 
         uint64_t sum2[2] = {0ull, 0ull};
         uint32_t xa[32], xb[32];
         tmem_ld32(tm, xa);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int c = 64 * half;
+#pragma unroll 1
+        for (int c = 0; c < hi; c += 64) {
           tmem_ld_wait();
           tmem_ld_fence(xa);
           tmem_ld32(tm + c + 32, xb);
@@ -703,8 +794,8 @@ __device__ void sum_role(const int m, const Shared<D, kFp8>& sh, const uint32_t 
             add_weights<true>(xa, nlse + c, p.scale, lo - c, hi - c, sum2);
           tmem_ld_wait();
           tmem_ld_fence(xb);
-          if (half == 0) {
-            tmem_ld32(tm + 64, xa);
+          if (c + 64 < hi) {
+            tmem_ld32(tm + c + 64, xa);
           } else {
             tc_fence_before();
             __syncwarp();
@@ -712,7 +803,7 @@ __device__ void sum_role(const int m, const Shared<D, kFp8>& sh, const uint32_t 
           }
           if (plain)
             add_weights<false>(xb, nlse + c + 32, p.scale, 0, 0, sum2);
-          else
+          else if (c + 32 < hi)
             add_weights<true>(xb, nlse + c + 32, p.scale, lo - c - 32, hi - c - 32, sum2);
         }
         total2[0] = add2(total2[0], sum2[0]);
@@ -723,11 +814,13 @@ __device__ void sum_role(const int m, const Shared<D, kFp8>& sh, const uint32_t 
       if (lane == 0) mbar_arrive(sh.lse_empty(lr.i));
       lr.next();
     }
-    if (slot >= 0) {
+    const long long row = w->row[in_unit / 16];
+    if (row >= 0 && w->key0 + in_unit < w->L) {
       float a, b;
       up2(add2(total2[0], total2[1]), a, b);
-      p.sums[slot] = p.decay * old + (a + b);
+      p.sums[row + in_unit % 16] = fmaf(p.decay, p.decay != 0.0f && past_key < 0 ? w->old[in_unit] : 0.0f, a + b);
     }
+    in.done();
   }
 }
 
@@ -758,6 +851,10 @@ __global__ void __launch_bounds__(Layout<D, kFp8>::kThreads, 1)
       mbar_init(sh.lse_full(i), 1);
       mbar_init(sh.lse_empty(i), 8);
     }
+    for (int i = 0; i < kUnits; ++i) {
+      mbar_init(sh.unit_full(i), 1);
+      mbar_init(sh.unit_empty(i), L::kReaders);
+    }
     st_shared(sh.abort(), 0);
     fence_barrier_init();
     tma_prefetch_desc(&tm_q);
@@ -779,15 +876,17 @@ __global__ void __launch_bounds__(Layout<D, kFp8>::kThreads, 1)
   const long long units = ok ? sh.pre()[p.s.B] : 0;
 
   if (warp < 8) {
-    sum_role<D, kFp8>(warp / 4, sh, tmem, p, units);
+    sum_role<D, kFp8>(warp / 4, sh, tmem, p);
   } else if (warp == 8) {
-    load_role<D, kFp8>(sh, &tm_q, &tm_k, p, units);
+    load_role<D, kFp8>(sh, &tm_q, &tm_k, p);
   } else if (warp == 9) {
-    mma_role<D, kFp8>(sh, tmem, p, units);
+    mma_role<D, kFp8>(sh, tmem, p);
   } else if (warp == 10) {
-    lse_role<D, kFp8>(sh, p, units);
+    lse_role<D, kFp8>(sh, p);
+  } else if (warp == 11) {
+    unit_role<D, kFp8>(sh, p, units);
   } else {
-    if constexpr (kFp8) widen_role<D>(sh, p, units);
+    if constexpr (kFp8) widen_role<D>(sh, p);
   }
 
   // after a give-up, copies and MMAs in flight land before the memory they target is

@@ -72,7 +72,7 @@ def check(fa, c, new, Hq, causal=True, decay=1.0, seed=3, dense=False, scale=Non
         at = (c.table[b, t // c.page], slice(None), t % c.page)
         qb, k = f64(q[i:i + n]), c.rows("k", b)
         want, slack = P.weights(qb, lse[:, i:i + n].numpy().astype(np.float64), k, P.causal_sees(n, L, causal), scale)
-        old = before[at].astype(np.float64).T * decay
+        old = before[at].astype(np.float64).T * float(np.float32(decay))       # (an FP32 argument)
         old[:, max(0, L - n):] = 0
         if decay == 0:
             old[:] = 0
