@@ -119,7 +119,7 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 }  // namespace
 
-fa_status prepare_kernel(const void* func, int bytes, bool wide_clusters) {
+fa_status prepare_kernel(const void* func, int bytes) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return FA_ERR_CUDA;
   static std::mutex mu;
@@ -128,9 +128,6 @@ fa_status prepare_kernel(const void* func, int bytes, bool wide_clusters) {
   for (const auto& e : done)
     if (e.first == func && e.second == dev) return FA_OK;
   if (cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
-    return FA_ERR_CUDA;
-  if (wide_clusters &&
-      cudaFuncSetAttribute(func, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
     return FA_ERR_CUDA;
   done.emplace_back(func, dev);
   return FA_OK;

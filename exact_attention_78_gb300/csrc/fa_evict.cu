@@ -481,8 +481,13 @@ fa_status launch_cache_select(const SelectParams& in, int num_sms, cudaStream_t 
   const int each = ((capacity + C - 1) / C + 3) / 4 * 4;
   p.cached = each < evict::kMostCached ? each : evict::kMostCached;
   const int most = (3 * evict::kBins + evict::kMostCached) * 4;
-  const fa_status st = prepare_kernel(reinterpret_cast<const void*>(evict::select_kernel), most, true);
+  const void* kernel = reinterpret_cast<const void*>(evict::select_kernel);
+  const fa_status st = prepare_kernel(kernel, most);
   if (st != FA_OK) return st;
+  // clusters of more than 8 blocks have to be asked for (on each device)
+  if (C > evict::kMaxCluster &&
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+    return FA_ERR_CUDA;
   return evict::launch_clusters(evict::select_kernel, (int)units, C, evict::kThreads,
                                 (3 * evict::kBins + p.cached) * 4, stream, p);
 }

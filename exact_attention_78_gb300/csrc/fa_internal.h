@@ -102,9 +102,8 @@ fa_status make_tmap_f32_rows_heads_d(CUtensorMap* map, const void* base, int row
 
 // Raises the dynamic shared-memory limit of kernel `func` to `bytes` the
 // first time it is launched on the current device (the attribute is per
-// device); thread-safe.  wide_clusters: it may also be launched in clusters of up
-// to 16 blocks.
-fa_status prepare_kernel(const void* func, int bytes, bool wide_clusters = false);
+// device); thread-safe.
+fa_status prepare_kernel(const void* func, int bytes);
 
 // Kernel launchers (defined in their translation units).
 fa_status launch_fwd(const FwdLaunch& L, cudaStream_t stream);

@@ -1093,28 +1093,7 @@ __device__ void correction_role(const Shared<D, kFp8>& sh, const uint32_t tmem, 
   }
 }
 
-// Four MMAs in one piece of PTX, issued by one elected lane of the (converged)
-// warp: one election instead of four, and only the operands' base words live
-// across it.  Offsets are in units of 16 bytes (descriptors) or TMEM columns.
-// The first MMA accumulates if acc != 0, the others always do.
-// D[tmem] (+)= A[smem] B[smem]: steps k at offset + 2 k in both operands.
-template <uint32_t OFF>
-FA_DEV void mma4_ss(uint32_t d, uint32_t alo, uint32_t ahi, uint32_t blo, uint32_t bhi, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred e, p;\n\t.reg .b32 al, bl;\n\t.reg .b64 ad, bd;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %6, 0;\n\t"
-      "add.u32 al, %1, %7;\n\tadd.u32 bl, %3, %7;\n\tmov.b64 ad, {al, %2};\n\tmov.b64 bd, {bl, %4};\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %5, p;\n\t"
-      "add.u32 al, %1, %7 + 2;\n\tadd.u32 bl, %3, %7 + 2;\n\tmov.b64 ad, {al, %2};\n\tmov.b64 bd, {bl, %4};\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %5, 1;\n\t"
-      "add.u32 al, %1, %7 + 4;\n\tadd.u32 bl, %3, %7 + 4;\n\tmov.b64 ad, {al, %2};\n\tmov.b64 bd, {bl, %4};\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %5, 1;\n\t"
-      "add.u32 al, %1, %7 + 6;\n\tadd.u32 bl, %3, %7 + 6;\n\tmov.b64 ad, {al, %2};\n\tmov.b64 bd, {bl, %4};\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %5, 1;\n\t}\n" ::"r"(d),
-      "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc), "r"(acc), "n"(OFF)
-      : "memory");
-}
+// Four MMAs in one piece of PTX, as paged::mma4_ss.
 // D[tmem] (+)= A[tmem] B[smem]: A at 8 columns, B at 128 units per step.
 template <uint32_t FIRST>
 FA_DEV void mma4_ts(uint32_t d, uint32_t a, uint32_t blo, uint32_t bhi, uint32_t idesc, uint32_t acc) {
@@ -1158,9 +1137,9 @@ __device__ void mma_role(const Shared<D, kFp8>& sh, const uint32_t tmem, const P
   auto issue_s = [&](int t, int st) {
     const uint64_t da = sdesc_sw128(sh.sbase + L::kQ + t * L::kTileBytes, 16, 1024);
     const uint64_t db = sdesc_sw128(sh.sbase + L::kKV + st * L::kTileBytes, 16, 1024);
-    mma4_ss<0>(tmem + t * kBN, desc_lo(da), desc_hi(da), desc_lo(db), desc_hi(db), kIdS, 0u);
+    paged::mma4_ss<0>(tmem + t * kBN, desc_lo(da), desc_hi(da), desc_lo(db), desc_hi(db), kIdS, 0u);
     if (D == 128)
-      mma4_ss<L::kChunkBytes / 16>(tmem + t * kBN, desc_lo(da), desc_hi(da), desc_lo(db), desc_hi(db), kIdS, 1u);
+      paged::mma4_ss<L::kChunkBytes / 16>(tmem + t * kBN, desc_lo(da), desc_hi(da), desc_lo(db), desc_hi(db), kIdS, 1u);
     mma_commit_w(sh.s_full(t));
   };
   // O_t (+)= P_t V in K steps of 16 keys: TMEM columns 8 k.. of P, key rows

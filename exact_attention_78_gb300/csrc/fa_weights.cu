@@ -19,7 +19,8 @@ __device__ DeviceError g_err;
 constexpr float kLog2e = 1.4426950408889634f;
 
 enum Site { kSiteSeqs = 1, kSitePage, kSiteKEmpty, kSiteKFull, kSiteQEmpty, kSiteQFull, kSiteSEmpty, kSiteSFull,
-            kSiteLseEmpty, kSiteLseFull, kSiteStep, kSiteUnitEmpty, kSiteUnitFull };
+            kSiteLseEmpty, kSiteStep, kSiteUnitEmpty, kSiteUnitFull,
+            kSitePart };
 
 FA_DEV size_t lse_at(const WeighParams& p, int b, int q0, int head, int tok) {
   return p.s.cu ? (size_t)head * p.s.Sn + q0 + tok : ((size_t)b * p.Hq + head) * p.s.Sn + tok;
@@ -368,23 +369,22 @@ fa_status launch_step(const WeighParams& p, int num_sms, cudaStream_t stream) {
 
 // --------------------------------------------------------------- many rows --
 // S^T = K Q^T on tcgen05: 256 keys of a unit (two tiles of 128, the M side, one key a
-// lane of tensor memory), the rows 128 at a time (N).  A thread has a key, reads its
-// scores out of tensor memory and adds their exponentials up: no row statistics, no
-// second product, nothing between the threads.  Both operands' tiles are read by all
-// units of a head (Q) or tiles of rows (K), from L2.  What bounds it is the
-// exponential, 16 a clock and SM.
+// lane of tensor memory), the rows 128 at a time (N).  A thread has a key and half of a
+// tile's rows, reads their scores out of tensor memory and adds their exponentials up:
+// no row statistics, no second product.  Both operands' tiles are read by all units
+// of a head (Q) or tiles of rows (K), from L2.  (BLOCK_FIGURES)
 //
-// Warps: 0-3 and 4-7 exponentials of the first and second 128 keys, 8 loads (Q; K of
-// BF16 pages), 9 MMA issue, 10 the rows' LSE, 11 units (works out the next ones, looks
-// their pages up and has their old sums copied, ahead of the others), 12-15 widening
+// Warps: 0-15 exponentials (8 m + 4 j on: keys m, rows j of a tile), 16 loads (Q; K of
+// BF16 pages), 17 MMA issue, 18 the rows' LSE, 19 units (works out the next ones, looks
+// their pages up and has their old sums copied, ahead of the others), 20-27 widening
 // (E4M3 pages: codes and scale to BF16, exactly, once per unit).
 //
-// Tensor memory: scores of the first keys at columns 0 and 128, of the second at 256
-// and 384.
+// Tensor memory: scores of the first keys at columns 0 and 128, tile by tile in turn, of
+// the second at 256 and 384.
 
 constexpr int kBM = 128, kBN = 128;
 constexpr int kUnitKeys = 2 * kBM;
-constexpr int kLses = 4, kUnits = 4;
+constexpr int kUnits = 6;
 
 // 256 keys of a (sequence, head), and the tiles of rows that see some of them, as the
 // roles get them.
@@ -395,25 +395,27 @@ struct Unit {
   int pad[3];
   long long row[kUnitKeys / 16];      // of every 16 keys' first; -1: behind the end, or in a bad page
   float old[kUnitKeys];
+  float part[kUnitKeys];              // what the second set of warps has added up
   FA_DEV bool two() const { return key0 + kBM < L; }
 };
 
 template <int D, bool kFp8>
 struct Layout {
-  static constexpr int kThreads = kFp8 ? 512 : 384;
-  static constexpr int kReaders = kFp8 ? 15 : 11;           // warps that take units
+  static constexpr int kWideners = kFp8 ? 8 : 0;
+  static constexpr int kThreads = 640 + 32 * kWideners;
+  static constexpr int kReaders = 19 + kWideners;           // warps that take units
   static constexpr int kChunks = D / 64;
   static constexpr int kChunkBytes = 128 * 128;             // 128 rows by 64 columns
   static constexpr int kTileBytes = kChunks * kChunkBytes;
   static constexpr int kQStages = D == 128 ? 2 : 4;
   static constexpr int kK = 0;                              // [2][two tiles]
   static constexpr int kQ = kK + 4 * kTileBytes;
-  static constexpr int kLse = kQ + kQStages * kTileBytes;   // [kLses][kBN]
-  static constexpr int kUnitRing = kLse + kLses * kBN * 4;
+  static constexpr int kLse = kQ + kQStages * kTileBytes;   // [2][kBN]
+  static constexpr int kUnitRing = kLse + 2 * kBN * 4;
   static constexpr int kPre = kUnitRing + kUnits * (int)sizeof(Unit);      // prefix of units, [B + 1], 64 bits
   static constexpr int kSums = kPre + (kMaxPackedSeqs + 1) * 8;
   static constexpr int kBars = kSums + 32 * 16;
-  static constexpr int kNumBars = 4 + 2 * kQStages + 8 + 2 * kLses + 2 * kUnits;
+  static constexpr int kNumBars = 4 + 2 * kQStages + 8 + 2 + 4 * kUnits;
   static constexpr int kMisc = kBars + kNumBars * 8;
   static constexpr int kBytes = kMisc + 64 + kSmemAlignSlack;
   static_assert(kBytes <= 232448, "dynamic shared memory above the 227 KB per-CTA limit");
@@ -429,12 +431,13 @@ struct Shared {
   FA_DEV uint32_t k_empty(int i) const { return bar(2 + i); }
   FA_DEV uint32_t q_full(int i) const { return bar(4 + i); }
   FA_DEV uint32_t q_empty(int i) const { return bar(4 + L::kQStages + i); }
+  // scores are complete, and the rows' LSE is here
   FA_DEV uint32_t s_full(int m, int i) const { return bar(4 + 2 * L::kQStages + 2 * m + i); }
   FA_DEV uint32_t s_empty(int m, int i) const { return bar(8 + 2 * L::kQStages + 2 * m + i); }
-  FA_DEV uint32_t lse_full(int i) const { return bar(12 + 2 * L::kQStages + i); }
-  FA_DEV uint32_t lse_empty(int i) const { return bar(12 + 2 * L::kQStages + kLses + i); }
-  FA_DEV uint32_t unit_full(int i) const { return bar(12 + 2 * L::kQStages + 2 * kLses + i); }
-  FA_DEV uint32_t unit_empty(int i) const { return bar(12 + 2 * L::kQStages + 2 * kLses + kUnits + i); }
+  FA_DEV uint32_t lse_empty(int i) const { return bar(12 + 2 * L::kQStages + i); }
+  FA_DEV uint32_t unit_full(int i) const { return bar(14 + 2 * L::kQStages + i); }
+  FA_DEV uint32_t unit_empty(int i) const { return bar(14 + 2 * L::kQStages + kUnits + i); }
+  FA_DEV uint32_t part_full(int i, int m) const { return bar(14 + 2 * L::kQStages + 2 * kUnits + 2 * i + m); }
   FA_DEV Unit* unit(int i) const { return reinterpret_cast<Unit*>(base + L::kUnitRing) + i; }
   FA_DEV const long long* pre() const { return reinterpret_cast<const long long*>(base + L::kPre); }
   FA_DEV float* lse(int i) const { return reinterpret_cast<float*>(base + L::kLse) + i * kBN; }
@@ -445,9 +448,10 @@ struct Shared {
   }
   // For waits that last as long as a unit, whose rows may be many (the other roles
   // wait for a tile at a time, and give up first if nothing moves).
-  FA_DEV bool wait_long(uint32_t b, uint32_t parity, int site, const WeighParams& p) const {
+  FA_DEV bool wait_long(uint32_t b, uint32_t parity, int site, const WeighParams& p, bool sleeps = true) const {
 #pragma unroll 1
-    for (int i = 0; i < (1 << 27) && !mbar_try_wait(b, parity) && !ld_shared_volatile(abort()); ++i) __nanosleep(50);
+    for (int i = 0; i < (1 << 27) && !mbar_try_wait(b, parity) && !ld_shared_volatile(abort()); ++i)
+      if (sleeps) __nanosleep(100);
     return wait(b, parity, site, p);
   }
 };
@@ -467,39 +471,42 @@ struct Ring {
 
 FA_DEV int units_of(int L) { return (L + kUnitKeys - 1) / kUnitKeys; }
 
-// Works out this thread block's units, every gridDim.x-th.
+// Works out this thread block's units, every gridDim.x-th, two at a time, half a warp
+// each.
 template <int D, bool kFp8>
 __device__ void unit_role(const Shared<D, kFp8>& sh, const WeighParams& p, long long units) {
-  const int lane = threadIdx.x % 32;
+  const int lane = threadIdx.x % 32, half = lane / 16, in = lane % 16;
   const int tt = kBN / p.group;
   const long long* pre = sh.pre();
   Ring<kUnits> r;
-  for (long long u = blockIdx.x;; u += gridDim.x) {
-    if (!sh.wait_long(sh.unit_empty(r.i), r.phase ^ 1, kSiteUnitEmpty, p)) return;
-    Unit* to = sh.unit(r.i);
-    if (u >= units) {
-      if (lane == 0) {
-        to->b = -1;
-        mbar_arrive(sh.unit_full(r.i));
+  for (long long u0 = blockIdx.x;; u0 += 2 * gridDim.x) {
+    Ring<kUnits> next = r;
+    next.next();
+    const int i = half ? next.i : r.i;
+    const long long u = u0 + half * gridDim.x;
+    const bool some = u < units;
+    int lo = 0;                      // last b with pre[b] <= u
+    if (some) {
+      int hi = p.s.B - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (pre[mid] <= u) lo = mid; else hi = mid - 1;
       }
-      return;
     }
-    int lo = 0, hi = p.s.B - 1;      // last b with pre[b] <= u
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (pre[mid] <= u) lo = mid; else hi = mid - 1;
-    }
+    __syncwarp();
     const paged::SeqRows q = paged::rows_of(p.s, lo);
-    const int block = (int)paged::div64(u - pre[lo], p.s.Hkv);      // the first keys, which most rows see, come first
-    const int head = (int)(u - pre[lo] - (long long)block * p.s.Hkv);
-    const int key = block * kUnitKeys + 16 * lane, past = q.L - q.n;
-    const bool some = lane < kUnitKeys / 16 && key < q.L;
-    const long long row = some ? slot_of(p, lo, head, key) : -1;
-    if (lane < kUnitKeys / 16) to->row[lane] = row;
-    const int copies = __popc(__ballot_sync(0xffffffffu, row >= 0));
+    const int block = some ? (int)paged::div64(u - pre[lo], p.s.Hkv) : 0;      // the first keys, which most rows see, come first
+    const int head = some ? (int)(u - pre[lo] - (long long)block * p.s.Hkv) : 0;
+    const int key = block * kUnitKeys + 16 * in, past = q.L - q.n;
+    const long long row = some && key < q.L ? slot_of(p, lo, head, key) : -1;
+    const uint32_t good = __ballot_sync(0xffffffffu, row >= 0);
+    if (!sh.wait_long(sh.unit_empty(r.i), r.phase ^ 1, kSiteUnitEmpty, p)) return;
+    if (!sh.wait_long(sh.unit_empty(next.i), next.phase ^ 1, kSiteUnitEmpty, p)) return;
+    Unit* to = sh.unit(i);
+    to->row[in] = row;
     __syncwarp();                    // the rows are written
-    if (lane == 0) {
-      to->b = lo;
+    if (in == 0) {
+      to->b = some ? lo : -1;
       to->head = head;
       to->key0 = block * kUnitKeys;
       to->n = q.n;
@@ -509,10 +516,12 @@ __device__ void unit_role(const Shared<D, kFp8>& sh, const WeighParams& p, long 
       const int tile0 = p.causal ? max(0, block * kUnitKeys - past) / tt : 0;      // (the last row at least sees the first key)
       to->tile0 = tile0;
       to->tiles = (q.n + tt - 1) / tt - tile0;
-      mbar_arrive_expect_tx(sh.unit_full(r.i), copies * 64);
+      mbar_arrive_expect_tx(sh.unit_full(i), __popc(good >> 16 * half & 0xFFFFu) * 64);
     }
     __syncwarp();
-    if (row >= 0) bulk_load(smem_u32(to->old + 16 * lane), p.sums + row, 64, sh.unit_full(r.i));
+    if (row >= 0) bulk_load(smem_u32(to->old + 16 * in), p.sums + row, 64, sh.unit_full(i));
+    if (u0 + gridDim.x >= units) return;      // one of them said that there are no more
+    r = next;
     r.next();
   }
 }
@@ -526,8 +535,8 @@ struct UnitReader {
   FA_DEV UnitReader(const Shared<D, kFp8>& s, const WeighParams& q) : sh(s), p(q) {}
   // The next one; nullptr at the end of the work or after a give-up.  The whole warp
   // calls it, and done() when it no longer needs the unit.
-  FA_DEV const Unit* next() {
-    if (!sh.wait_long(sh.unit_full(r.i), r.phase, kSiteUnitFull, p)) return nullptr;
+  FA_DEV const Unit* next(bool sleeps = true) {
+    if (!sh.wait_long(sh.unit_full(r.i), r.phase, kSiteUnitFull, p, sleeps)) return nullptr;
     const Unit* w = sh.unit(r.i);
     return w->b < 0 ? nullptr : w;
   }
@@ -584,93 +593,123 @@ __device__ void load_role(const Shared<D, kFp8>& sh, const CUtensorMap* tq, cons
   }
 }
 
-// The rows' LSE, negative, 128 floats a tile.
+// The rows' LSE, negative, 128 floats a tile.  They are loaded kAhead tiles before their
+// turn, also over the units' borders: one tile at a time, with the loads' latency
+// each time, this warp took 2300 cycles a tile and held up all others.
 template <int D, bool kFp8>
 __device__ void lse_role(const Shared<D, kFp8>& sh, const WeighParams& p) {
+  constexpr int kAhead = 2;
+  // With tile k on its way, and each unit a tile, this warp waits for unit k + kAhead.
+  // That comes together with one more, whose slot has to be that of a unit before k.
+  static_assert(kAhead + 1 - kUnits <= -1, "a tile waits for a unit that waits for it");
+  constexpr int kEach = kBN / 32;
   const int lane = threadIdx.x % 32;
   const int tt = kBN / p.group;
-  Ring<kLses> r;
-  int tok[kBN / 32], head[kBN / 32];
+  int tok[kEach], head[kEach];
 #pragma unroll
-  for (int i = 0; i < kBN / 32; ++i) {
+  for (int i = 0; i < kEach; ++i) {
     tok[i] = (lane + 32 * i) / p.group;
     head[i] = lane + 32 * i - tok[i] * p.group;
   }
   UnitReader<D, kFp8> in(sh, p);
-  while (const Unit* u = in.next()) {
-    const int b = u->b, q0 = u->q0, head0 = u->head * p.group, n = u->n, tiles = all_same(u->tiles);
-    int tok0 = u->tile0 * tt;
-    in.done();
-    for (int t = 0; t < tiles; ++t, tok0 += tt) {
-      float x[kBN / 32];
-#pragma unroll
-      for (int i = 0; i < kBN / 32; ++i) {
-        x[i] = 0.0f;
-        if (tok[i] < tt && tok0 + tok[i] < n) x[i] = lse_of(p.lse[lse_at(p, b, q0, head0 + head[i], tok0 + tok[i])]);
+  // the unit whose tiles are loaded, and the next tile's first token
+  int b = 0, q0 = 0, head0 = 0, n = 0, tok0 = 0;
+  bool two = false, more = true;
+  float x[kAhead + 1][kEach];
+  int kind[kAhead + 1];      // 0: no tile; 1: of a unit of up to 128 keys; 2: of more
+  auto load = [&](float (&y)[kEach]) -> int {
+    if (more && tok0 >= n) {
+      const Unit* u = in.next(false);
+      more = u != nullptr;
+      if (more) {
+        b = u->b;
+        q0 = u->q0;
+        head0 = u->head * p.group;
+        n = u->n;
+        two = u->two();
+        tok0 = u->tile0 * tt;
+        in.done();
       }
-      if (!sh.wait(sh.lse_empty(r.i), r.phase ^ 1, kSiteLseEmpty, p)) return;
+    }
+    if (!more) return 0;
 #pragma unroll
-      for (int i = 0; i < kBN / 32; ++i) sh.lse(r.i)[lane + 32 * i] = -x[i];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(sh.lse_full(r.i));
-      r.next();
+    for (int i = 0; i < kEach; ++i) {
+      y[i] = 0.0f;
+      if (tok[i] < tt && tok0 + tok[i] < n) y[i] = p.lse[lse_at(p, b, q0, head0 + head[i], tok0 + tok[i])];
+    }
+    tok0 += tt;
+    return two ? 2 : 1;
+  };
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) kind[k] = load(x[k]);
+  Ring<2> r;
+  for (;;) {
+    kind[kAhead] = load(x[kAhead]);
+    if (kind[0] == 0) return;
+    if (!sh.wait(sh.lse_empty(r.i), r.phase ^ 1, kSiteLseEmpty, p)) return;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) sh.lse(r.i)[lane + 32 * i] = -lse_of(x[0][i]);
+    __syncwarp();
+    if (lane < kind[0]) mbar_arrive(sh.s_full(lane, r.i));
+    r.next();
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      kind[k] = kind[k + 1];
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) x[k][i] = x[k + 1][i];
     }
   }
 }
 
-// E4M3 pages: four warps make the unit's keys BF16, which holds a code times its
+// E4M3 pages: eight warps make the unit's keys BF16, which holds a code times its
 // power of two exactly.  Rows behind the sequence's end are left as they were: each
 // is a lane of the product of its own.
 template <int D>
 __device__ void widen_role(const Shared<D, true>& sh, const WeighParams& p) {
   using L = Layout<D, true>;
   constexpr int kLanes = D / 16;                  // of a row
-  constexpr int kRows = 128 / kLanes;             // at a time
-  constexpr int kUnroll = 8;
-  const int thread = threadIdx.x - 384;
+  constexpr int kRows = 32 * L::kWideners / kLanes;         // at a time
+  constexpr int kUnroll = D == 128 ? 8 : 4;                 // a unit's 256
+  static_assert(kRows * kUnroll == kUnitKeys, "a unit at a time");
+  const int thread = threadIdx.x - 640;
   const int piece = thread % kLanes, row0 = thread / kLanes;
   Ring<2> r;
   UnitReader<D, true> in(sh, p);
   while (const Unit* w = in.next()) {
     const int keys = min(kUnitKeys, w->L - w->key0);
-    // the codes are on their way while the products still read what was there before
-    bool empty = false;
-#pragma unroll 1
-    for (int i0 = row0; i0 - row0 < keys; i0 += kRows * kUnroll) {
-      uint4 x[kUnroll];
-      uint32_t byte[kUnroll];
+    uint4 x[kUnroll];
+    uint32_t byte[kUnroll];
 #pragma unroll
-      for (int k = 0; k < kUnroll; ++k) {
-        const int i = i0 + k * kRows;
-        x[k] = make_uint4(0u, 0u, 0u, 0u);
-        byte[k] = 127u;
-        const long long row = i < keys ? w->row[i / 16] : -1;
-        if (row < 0) continue;
-        x[k] = static_cast<const uint4*>(p.k_pages)[(row + i % 16) * kLanes + piece];
-        byte[k] = p.k_scale[row + i % 16];
+    for (int k = 0; k < kUnroll; ++k) {
+      const int i = row0 + k * kRows;
+      x[k] = make_uint4(0u, 0u, 0u, 0u);
+      byte[k] = 127u;
+      const long long row = w->row[i / 16];
+      if (row < 0) continue;
+      x[k] = static_cast<const uint4*>(p.k_pages)[(row + i % 16) * kLanes + piece];
+      byte[k] = p.k_scale[row + i % 16];
+    }
+    // (the codes are on their way while the products still read what was there before)
+    if (!sh.wait_long(sh.k_empty(r.i), r.phase ^ 1, kSiteKEmpty, p, false)) return;
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      const int i = row0 + k * kRows;
+      if (i >= keys) continue;
+      const uint32_t f = byte[k] == 255u ? 0x7FC07FC0u : byte[k] << 7 | byte[k] << 23;
+      const uint32_t v[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+      uint32_t y[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t even = paged::mul_bf16x2(paged::e4m3_even(v[j]), f);
+        const uint32_t odd = paged::mul_bf16x2(paged::e4m3_odd(v[j]), f);
+        y[2 * j] = __byte_perm(even, odd, 0x5410);
+        y[2 * j + 1] = __byte_perm(even, odd, 0x7632);
       }
-      if (!empty && !sh.wait_long(sh.k_empty(r.i), r.phase ^ 1, kSiteKEmpty, p)) return;
-      empty = true;
-#pragma unroll
-      for (int k = 0; k < kUnroll; ++k) {
-        const int i = i0 + k * kRows;
-        if (i >= keys) continue;
-        const uint32_t f = byte[k] == 255u ? 0x7FC07FC0u : byte[k] << 7 | byte[k] << 23;
-        const uint32_t v[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-        uint32_t y[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t even = paged::mul_bf16x2(paged::e4m3_even(v[j]), f);
-          const uint32_t odd = paged::mul_bf16x2(paged::e4m3_odd(v[j]), f);
-          y[2 * j] = __byte_perm(even, odd, 0x5410);
-          y[2 * j + 1] = __byte_perm(even, odd, 0x7632);
-        }
-        const int m = i % kBM;
-        uint8_t* to = sh.base + L::kK + (2 * r.i + i / kBM) * L::kTileBytes + piece / 4 * L::kChunkBytes + m * 128;
-        const int c = piece % 4 * 2;
-        *reinterpret_cast<uint4*>(to + ((c ^ (m & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-        *reinterpret_cast<uint4*>(to + (((c + 1) ^ (m & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
-      }
+      const int m = i % kBM;
+      uint8_t* to = sh.base + L::kK + (2 * r.i + i / kBM) * L::kTileBytes + piece / 4 * L::kChunkBytes + m * 128;
+      const int c = piece % 4 * 2;
+      *reinterpret_cast<uint4*>(to + ((c ^ (m & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+      *reinterpret_cast<uint4*>(to + (((c + 1) ^ (m & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
     }
     fence_proxy_async_smem();
     __syncwarp();
@@ -680,43 +719,40 @@ __device__ void widen_role(const Shared<D, true>& sh, const WeighParams& p) {
   }
 }
 
-// MMA issue (a converged warp, one elected lane).
+// MMA issue (a converged warp, one elected lane).  Tiles are numbered through; tile i
+// takes score buffer i mod 2 of either 128 keys, which a unit with no more than 128
+// leaves out for the second.
 template <int D, bool kFp8>
 __device__ void mma_role(const Shared<D, kFp8>& sh, const uint32_t tmem, const WeighParams& p) {
   using L = Layout<D, kFp8>;
   constexpr uint32_t kId = idesc_bf16_f32(kBM, kBN, false, false);
-  Ring<2> kr, sr[2];
+  Ring<2> kr;
   Ring<L::kQStages> qr;
+  int j = 0;
+  uint32_t phase = 0;      // bit 2 m + j: of a score buffer
   UnitReader<D, kFp8> in(sh, p);
-  while (const Unit* w = in.next()) {
+  while (const Unit* w = in.next(false)) {
     const int tiles = all_same(w->tiles);
     const bool two = all_same((int)w->two()) != 0;
     in.done();
     if (!sh.wait(sh.k_full(kr.i), kr.phase, kSiteKFull, p)) return;
     tc_fence_after();
-    for (int t = 0; t < tiles; ++t) {
+    for (int t = 0; t < tiles; ++t, j ^= 1) {
       if (!sh.wait(sh.q_full(qr.i), qr.phase, kSiteQFull, p)) return;
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         if (m == 1 && !two) break;
-        if (!sh.wait(sh.s_empty(m, sr[m].i), sr[m].phase ^ 1, kSiteSEmpty, p)) return;
+        const int i = 2 * m + j;
+        if (!sh.wait(sh.s_empty(m, j), (phase >> i & 1) ^ 1, kSiteSEmpty, p)) return;
+        phase ^= 1u << i;
         tc_fence_after();
         const uint64_t da = sdesc_sw128(sh.sbase + L::kK + (2 * kr.i + m) * L::kTileBytes, 16, 1024);
         const uint64_t db = sdesc_sw128(sh.sbase + L::kQ + qr.i * L::kTileBytes, 16, 1024);
-        const uint32_t d = tmem + m * 256 + sr[m].i * 128;
-        mma_ss_w<0, 0>(d, desc_lo(da), desc_hi(da), desc_lo(db), desc_hi(db), kId, 0u);
-        mma_ss_w<2, 2>(d, desc_lo(da), desc_hi(da), desc_lo(db), desc_hi(db), kId, 1u);
-        mma_ss_w<4, 4>(d, desc_lo(da), desc_hi(da), desc_lo(db), desc_hi(db), kId, 1u);
-        mma_ss_w<6, 6>(d, desc_lo(da), desc_hi(da), desc_lo(db), desc_hi(db), kId, 1u);
-        if (D == 128) {
-          constexpr uint32_t kC = L::kChunkBytes / 16;
-          mma_ss_w<kC, kC>(d, desc_lo(da), desc_hi(da), desc_lo(db), desc_hi(db), kId, 1u);
-          mma_ss_w<kC + 2, kC + 2>(d, desc_lo(da), desc_hi(da), desc_lo(db), desc_hi(db), kId, 1u);
-          mma_ss_w<kC + 4, kC + 4>(d, desc_lo(da), desc_hi(da), desc_lo(db), desc_hi(db), kId, 1u);
-          mma_ss_w<kC + 6, kC + 6>(d, desc_lo(da), desc_hi(da), desc_lo(db), desc_hi(db), kId, 1u);
-        }
-        mma_commit_w(sh.s_full(m, sr[m].i));
-        sr[m].next();
+        const uint32_t d = tmem + i * 128;
+        paged::mma4_ss<0>(d, desc_lo(da), desc_hi(da), desc_lo(db), desc_hi(db), kId, 0u);
+        if (D == 128)
+          paged::mma4_ss<L::kChunkBytes / 16>(d, desc_lo(da), desc_hi(da), desc_lo(db), desc_hi(db), kId, 1u);
+        mma_commit_w(sh.s_full(m, j));
       }
       mma_commit_w(sh.q_empty(qr.i));
       qr.next();
@@ -726,21 +762,40 @@ __device__ void mma_role(const Shared<D, kFp8>& sh, const uint32_t tmem, const W
   }
 }
 
-// 32 scores of a key: their exponentials added to sum2; kMasked: those of columns
-// [lo, hi) alone.
-template <bool kMasked>
-FA_DEV void add_weights(const uint32_t (&x)[32], const float* nlse, float scale, int lo, int hi, uint64_t (&sum2)[2]) {
+// 32 lanes x 16 consecutive columns of tensor memory; the wait for them, which
+// what uses them is tied to.
+FA_DEV void load_scores(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+FA_DEV void scores_here(uint32_t (&r)[16]) {
+  tmem_ld_wait();
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+
+// Scores of a key: their exponentials added to sum2; kMasked: those of columns [lo, hi)
+// alone.
+template <bool kMasked, int kCols>
+FA_DEV void add_weights(const uint32_t (&x)[kCols], const float* nlse, float scale, int lo, int hi, uint64_t (&sum2)[2]) {
   const uint64_t scale2 = pk2(scale, scale), log2e2 = pk2(kLog2e, kLog2e);
 #pragma unroll
-  for (int i = 0; i < 32; i += 4) {
+  for (int i = 0; i < kCols; i += 4) {
     const float4 l = *reinterpret_cast<const float4*>(nlse + i);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       // taken from the LSE before it goes to log2 units: the difference is small where
       // the weight is large, and so is its rounding
       const uint64_t s2 = pk2(__uint_as_float(x[i + 2 * h]), __uint_as_float(x[i + 2 * h + 1]));
+      const uint64_t x2 = mul2(fma2(s2, scale2, h ? pk2(l.z, l.w) : pk2(l.x, l.y)), log2e2);
       float a, b;
-      up2(mul2(fma2(s2, scale2, h ? pk2(l.z, l.w) : pk2(l.x, l.y)), log2e2), a, b);
+      up2(x2, a, b);
       if (kMasked) {
         const int c = i + 2 * h;
         if (c < lo || c >= hi) a = -INFINITY;
@@ -751,74 +806,92 @@ FA_DEV void add_weights(const uint32_t (&x)[32], const float* nlse, float scale,
   }
 }
 
-// Exponentials and sums of 128 keys of each unit, a thread a key.
+// Exponentials and sums: 128 keys of each unit, a thread a key, over columns 64 j on of
+// each tile.
 template <int D, bool kFp8>
-__device__ void sum_role(const int m, const Shared<D, kFp8>& sh, const uint32_t tmem, const WeighParams& p) {
+__device__ void sum_role(const int m, const int j, const Shared<D, kFp8>& sh, const uint32_t tmem, const WeighParams& p) {
+  constexpr int kCols = 16;      // of scores in registers, twice
   const int lane = threadIdx.x % 32, wq = threadIdx.x / 32 % 4;
   const int tt = kBN / p.group;
   const int in_unit = m * kBM + wq * 32 + lane;
-  Ring<2> sr;
-  Ring<kLses> lr;
+  const uint32_t tm0 = tmem + (uint32_t(wq * 32) << 16) + m * 256 + j * 64;
+  uint32_t tile = 0;             // numbered through
+  uint32_t phase = 0;            // bit i: of score buffer i
   UnitReader<D, kFp8> in(sh, p);
-  while (const Unit* w = in.next()) {
+  while (const Unit* w = in.next(false)) {
     const int tiles = all_same(w->tiles);
     const bool active = m == 0 || all_same((int)w->two()) != 0;
     const int past_key = w->key0 + in_unit - w->past;      // the first token that sees the key
-    int tok0 = w->tile0 * tt;
     const int n = w->n;
+    int tok0 = w->tile0 * tt;
     uint64_t total2[2] = {0ull, 0ull};
-    for (int t = 0; t < tiles; ++t, tok0 += tt) {
-      const int hi = min(tt, n - tok0) * p.group;                             // columns with a row
-      const int lo = p.causal ? max(0, past_key - tok0) * p.group : 0;        // first one that sees the key
-      // (a half without keys is here long before the other is done with a unit)
-      if (!(active ? sh.wait(sh.lse_full(lr.i), lr.phase, kSiteLseFull, p)
-                   : sh.wait_long(sh.lse_full(lr.i), lr.phase, kSiteLseFull, p)))
-        return;
-      if (active) {
-        if (!sh.wait(sh.s_full(m, sr.i), sr.phase, kSiteSFull, p)) return;
-        tc_fence_after();
-        const uint32_t tm = tmem + (uint32_t(wq * 32) << 16) + m * 256 + sr.i * 128;
-        const float* nlse = sh.lse(lr.i);
-        const bool plain = __all_sync(0xffffffffu, lo == 0 && hi == kBN);
+    for (int t = 0; t < tiles; ++t, tok0 += tt, ++tile) {
+      const int i = tile & 1;
+      if (!active) {      // goes along with the first keys
+        if (!sh.wait_long(sh.s_full(0, i), tile >> 1 & 1, kSiteSFull, p)) return;
+      } else {
+        const int hi = min(tt, n - tok0) * p.group - 64 * j;                             // columns with a row
+        const int lo = p.causal ? max(0, past_key - tok0) * p.group - 64 * j : 0;        // first one that sees the key
+        const uint32_t tm = tm0 + i * 128;
+        const float* nlse = sh.lse(i) + 64 * j;
+        const bool plain = __all_sync(0xffffffffu, lo <= 0 && hi >= 64);
         uint64_t sum2[2] = {0ull, 0ull};
-        uint32_t xa[32], xb[32];
-        tmem_ld32(tm, xa);
-#pragma unroll 1
-        for (int c = 0; c < hi; c += 64) {
-          tmem_ld_wait();
-          tmem_ld_fence(xa);
-          tmem_ld32(tm + c + 32, xb);
-          if (plain)
+        uint32_t xa[kCols], xb[kCols];
+        if (!sh.wait(sh.s_full(m, i), phase >> i & 1, kSiteSFull, p)) return;
+        phase ^= 1u << i;
+        tc_fence_after();
+        // the buffer's last columns are here
+        auto release = [&]() {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sh.s_empty(m, i));
+        };
+        if (plain) {
+          load_scores(tm, xa);
+#pragma unroll
+          for (int c = 0; c < 64; c += 2 * kCols) {
+            scores_here(xa);
+            load_scores(tm + c + kCols, xb);
             add_weights<false>(xa, nlse + c, p.scale, 0, 0, sum2);
-          else
-            add_weights<true>(xa, nlse + c, p.scale, lo - c, hi - c, sum2);
-          tmem_ld_wait();
-          tmem_ld_fence(xb);
-          if (c + 64 < hi) {
-            tmem_ld32(tm + c + 64, xa);
-          } else {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(sh.s_empty(m, sr.i));
+            scores_here(xb);
+            if (c + 2 * kCols < 64) load_scores(tm + c + 2 * kCols, xa); else release();
+            add_weights<false>(xb, nlse + c + kCols, p.scale, 0, 0, sum2);
           }
-          if (plain)
-            add_weights<false>(xb, nlse + c + 32, p.scale, 0, 0, sum2);
-          else if (c + 32 < hi)
-            add_weights<true>(xb, nlse + c + 32, p.scale, lo - c - 32, hi - c - 32, sum2);
+        } else if (hi <= 0) {
+          release();
+        } else {
+          load_scores(tm, xa);
+#pragma unroll 1
+          for (int c = 0; c < 64; c += kCols) {
+            scores_here(xa);
+            add_weights<true>(xa, nlse + c, p.scale, lo - c, hi - c, sum2);
+            if (c + kCols < min(hi, 64)) {
+              load_scores(tm + c + kCols, xa);
+            } else {
+              release();
+              break;
+            }
+          }
         }
         total2[0] = add2(total2[0], sum2[0]);
         total2[1] = add2(total2[1], sum2[1]);
-        sr.next();
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(sh.lse_empty(lr.i));
-      lr.next();
+      if (lane == 0) mbar_arrive(sh.lse_empty(i));
     }
-    const long long row = w->row[in_unit / 16];
-    if (row >= 0 && w->key0 + in_unit < w->L) {
-      float a, b;
-      up2(add2(total2[0], total2[1]), a, b);
-      p.sums[row + in_unit % 16] = fmaf(p.decay, p.decay != 0.0f && past_key < 0 ? w->old[in_unit] : 0.0f, a + b);
+    float a, b;
+    up2(add2(total2[0], total2[1]), a, b);
+    const int slot = in.r.i;
+    if (j == 1) {
+      sh.unit(slot)->part[in_unit] = a + b;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sh.part_full(slot, m));
+    } else {
+      if (!sh.wait_long(sh.part_full(slot, m), in.r.phase, kSitePart, p, false)) return;
+      const long long row = w->row[in_unit / 16];
+      if (row >= 0 && w->key0 + in_unit < w->L)
+        p.sums[row + in_unit % 16] =
+            fmaf(p.decay, p.decay != 0.0f && past_key < 0 ? w->old[in_unit] : 0.0f, a + b + w->part[in_unit]);
     }
     in.done();
   }
@@ -836,31 +909,30 @@ __global__ void __launch_bounds__(Layout<D, kFp8>::kThreads, 1)
   sh.sbase = smem_u32(smem);
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(sh.k_full(i), kFp8 ? 4 : 1);      // one arrival per widening warp
+      mbar_init(sh.k_full(i), kFp8 ? L::kWideners : 1);      // one arrival per widening warp
       mbar_init(sh.k_empty(i), 1);
       for (int m = 0; m < 2; ++m) {
-        mbar_init(sh.s_full(m, i), 1);
-        mbar_init(sh.s_empty(m, i), 4);
+        mbar_init(sh.s_full(m, i), 2);
+        mbar_init(sh.s_empty(m, i), 8);
       }
     }
     for (int i = 0; i < L::kQStages; ++i) {
       mbar_init(sh.q_full(i), 1);
       mbar_init(sh.q_empty(i), 1);
     }
-    for (int i = 0; i < kLses; ++i) {
-      mbar_init(sh.lse_full(i), 1);
-      mbar_init(sh.lse_empty(i), 8);
-    }
+    for (int i = 0; i < 2; ++i) mbar_init(sh.lse_empty(i), 16);
     for (int i = 0; i < kUnits; ++i) {
       mbar_init(sh.unit_full(i), 1);
       mbar_init(sh.unit_empty(i), L::kReaders);
+      mbar_init(sh.part_full(i, 0), 4);
+      mbar_init(sh.part_full(i, 1), 4);
     }
     st_shared(sh.abort(), 0);
     fence_barrier_init();
     tma_prefetch_desc(&tm_q);
     if (!kFp8) tma_prefetch_desc(&tm_k);
   }
-  if (warp == 9) {
+  if (warp == 17) {
     tmem_alloc(sh.tmem_slot(), 512);
     tmem_relinquish();
   }
@@ -875,15 +947,15 @@ __global__ void __launch_bounds__(Layout<D, kFp8>::kThreads, 1)
   const uint32_t tmem = *sh.tmem_slot();
   const long long units = ok ? sh.pre()[p.s.B] : 0;
 
-  if (warp < 8) {
-    sum_role<D, kFp8>(warp / 4, sh, tmem, p);
-  } else if (warp == 8) {
+  if (warp < 16) {
+    sum_role<D, kFp8>(warp / 8, warp / 4 % 2, sh, tmem, p);
+  } else if (warp == 16) {
     load_role<D, kFp8>(sh, &tm_q, &tm_k, p);
-  } else if (warp == 9) {
+  } else if (warp == 17) {
     mma_role<D, kFp8>(sh, tmem, p);
-  } else if (warp == 10) {
+  } else if (warp == 18) {
     lse_role<D, kFp8>(sh, p);
-  } else if (warp == 11) {
+  } else if (warp == 19) {
     unit_role<D, kFp8>(sh, p, units);
   } else {
     if constexpr (kFp8) widen_role<D>(sh, p);
@@ -894,7 +966,7 @@ __global__ void __launch_bounds__(Layout<D, kFp8>::kThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 17) {
     tc_fence_after();
     if (ld_shared_volatile(sh.abort())) {
       const uint64_t t0 = globaltimer_ns();

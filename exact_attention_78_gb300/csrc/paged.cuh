@@ -186,6 +186,29 @@ struct Join {
 // start).  The slot of part k:
 FA_DEV int join_slot(int c, int k) { return k == 0 ? 2 * c - 1 : 2 * (c + k - 1); }
 
+// Four MMAs in one piece of PTX, issued by one elected lane of the (converged)
+// warp: one election instead of four, and only the operands' base words live
+// across it.  Offsets are in units of 16 bytes (descriptors) or TMEM columns.
+// The first MMA accumulates if acc != 0, the others always do.
+// D[tmem] (+)= A[smem] B[smem]: steps k at offset + 2 k in both operands.
+template <uint32_t OFF>
+FA_DEV void mma4_ss(uint32_t d, uint32_t alo, uint32_t ahi, uint32_t blo, uint32_t bhi, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred e, p;\n\t.reg .b32 al, bl;\n\t.reg .b64 ad, bd;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "add.u32 al, %1, %7;\n\tadd.u32 bl, %3, %7;\n\tmov.b64 ad, {al, %2};\n\tmov.b64 bd, {bl, %4};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %5, p;\n\t"
+      "add.u32 al, %1, %7 + 2;\n\tadd.u32 bl, %3, %7 + 2;\n\tmov.b64 ad, {al, %2};\n\tmov.b64 bd, {bl, %4};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %5, 1;\n\t"
+      "add.u32 al, %1, %7 + 4;\n\tadd.u32 bl, %3, %7 + 4;\n\tmov.b64 ad, {al, %2};\n\tmov.b64 bd, {bl, %4};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %5, 1;\n\t"
+      "add.u32 al, %1, %7 + 6;\n\tadd.u32 bl, %3, %7 + 6;\n\tmov.b64 ad, {al, %2};\n\tmov.b64 bd, {bl, %4};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %5, 1;\n\t}\n" ::"r"(d),
+      "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc), "r"(acc), "n"(OFF)
+      : "memory");
+}
+
 // 2^e of a scale byte; NaN for the byte of a row without a finite scale.
 FA_DEV float scale_value(uint32_t byte) {
   return byte == 255u ? __int_as_float(0x7FC00000) : __uint_as_float(byte << 23);

@@ -84,6 +84,14 @@ def test_long(fa, n, Hq, fp8):
     check(fa, c, [n, n // 2 + 1], Hq)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("L", [90, 600])
+def test_many_units(fa, L, fp8):
+    """A dozen units or more for every thread block, of one tile of rows each and of two."""
+    c = Cache([L] * (300 if L < 256 else 100), 8, 64, 64, fp8, seed=2)
+    check(fa, c, [9 + b % 2 * 5 for b in range(len(c.lens))], 32)
+
+
 @pytest.mark.parametrize("new", [1, 100])
 def test_far_scores(fa, new):
     """Large scores, far from the LSE and near it, and a scale of its own."""
