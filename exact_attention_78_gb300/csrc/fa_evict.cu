@@ -368,20 +368,49 @@ __global__ void __launch_bounds__(kMoveThreads, 4) keep_kernel(const KeepParams 
   uint8_t* scales = which ? p.v_scale : p.k_scale;
   float* sums = which ? nullptr : p.sums;
   const int tile = C * kRows, tiles = (count + tile - 1) / tile;
-  auto look_up = [&](int t) {
+  // Where a tile's rows lie, step by step, each with the loads of the step before
+  // behind it: the tokens, their old and new pages, the rows.
+  struct Tokens {
+    int from, to;            // the same: stays, or none
+  };
+  struct Pages {
+    int from, to;
+  };
+  auto tokens = [&](int t, Tokens (&x)[kEach]) {
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int r = e * kMoveThreads + tid;
+      const long long i = (long long)t * tile + rank * kRows + r;
+      x[e].from = x[e].to = -1;
+      if (r < kRows && i < count) {
+        x[e].to = start + (int)i;
+        x[e].from = index[i];
+      }
+    }
+  };
+  const int* table = p.s.block_table + (size_t)b * p.s.max_pages;
+  auto pages_of = [&](const Tokens (&x)[kEach], Pages (&y)[kEach]) {
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      if (x[e].from == x[e].to) continue;
+      y[e].from = table[x[e].from >> p.s.page_shift];
+      y[e].to = table[x[e].to >> p.s.page_shift];
+    }
+  };
+  auto row = [&](int page, int tok) -> long long {
+    return ((long long)page * p.s.Hkv + head << p.s.page_shift) + (tok & ((1 << p.s.page_shift) - 1));
+  };
+  auto place = [&](int t, const Tokens (&x)[kEach], const Pages (&y)[kEach]) {
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
       const int r = e * kMoveThreads + tid;
       if (r >= kRows) break;
-      const long long i = (long long)t * tile + rank * kRows + r;
       Move m{-1, -1};
-      if (i < count) {
-        const int from = index[i], to = start + (int)i;
-        if (from != to) {
-          m.from = row_of(p.s, b, head, from);
-          m.to = row_of(p.s, b, head, to);
-          if (m.to < 0) m.from = -1;
-        }
+      if (x[e].from != x[e].to) {
+        if ((unsigned)y[e].from < (unsigned)p.s.num_pages && (unsigned)y[e].to < (unsigned)p.s.num_pages)
+          m = Move{row(y[e].from, x[e].from), row(y[e].to, x[e].to)};
+        else
+          record_bad_input(&g_err, kSitePage);
       }
       moves[t % 3][r] = m;
     }
@@ -406,7 +435,16 @@ __global__ void __launch_bounds__(kMoveThreads, 4) keep_kernel(const KeepParams 
     }
   };
   if (tiles == 0) return;
-  look_up(0);
+  Tokens one[kEach], two[kEach];     // of the tiles one and two further on than the one that is read
+  Pages pages_one[kEach];
+  tokens(0, one);
+  tokens(1, two);
+  pages_of(one, pages_one);
+  place(0, one, pages_one);
+  pages_of(two, pages_one);
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) one[e] = two[e];
+  tokens(2, two);
   __syncthreads();
   read(0, x, scale, sum);
 #pragma unroll 1
@@ -414,7 +452,13 @@ __global__ void __launch_bounds__(kMoveThreads, 4) keep_kernel(const KeepParams 
     uint4 next[kUnroll];
     uint8_t next_scale[kEach];
     float next_sum[kEach];
-    if (t + 1 < tiles) look_up(t + 1);
+    if (t + 1 < tiles) {
+      place(t + 1, one, pages_one);
+      pages_of(two, pages_one);
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) one[e] = two[e];
+      tokens(t + 3, two);
+    }
     if (C > 1)
       cluster_sync();
     else
