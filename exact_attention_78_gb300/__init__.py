@@ -1,6 +1,7 @@
 """Exact scaled-dot-product attention (forward and backward) for one NVIDIA
 GB300, as hand-written sm_103a CUDA behind a C ABI (include/fa.h), with its
-serving path over a paged key/value cache (include/fa_paged.h).
+serving path over a paged key/value cache, speculative decoding and eviction
+among it (include/fa_paged.h).
 
 The Python surface is a thin ctypes binding: ``fwd``, ``bwd`` and helpers.
 The library is built in-tree by ``exact_attention_78_gb300.build.build()``.

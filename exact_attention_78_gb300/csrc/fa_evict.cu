@@ -485,6 +485,23 @@ __global__ void __launch_bounds__(kMoveThreads, 4) keep_kernel(const KeepParams 
   }
 }
 
+// How many clusters of C blocks the device holds at once.
+bool clusters_at_once(const void* kernel, int C, int threads, int smem, int* most) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(C);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = C;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(most, kernel, &cfg) == cudaSuccess) return true;
+  cudaGetLastError();
+  return false;
+}
+
 // Launches `units` clusters of C blocks; see launch_overlapped().
 template <class P>
 fa_status launch_clusters(void (*kernel)(P), int units, int C, int threads, int smem, cudaStream_t stream,
@@ -520,20 +537,29 @@ fa_status launch_cache_select(const SelectParams& in, int num_sms, cudaStream_t 
   SelectParams p = in;
   const int capacity = p.s.max_pages << p.s.page_shift;
   const long long units = (long long)p.s.B * p.s.Hkv;
+  const void* kernel = reinterpret_cast<const void*>(evict::select_kernel);
+  const fa_status st = prepare_kernel(kernel, (3 * evict::kBins + evict::kMostCached) * 4);
+  if (st != FA_OK) return st;
+  // A block of its own for each head where those fill the SMs, else a cluster, but no
+  // more blocks than have some thousand tokens each.  (24 x 8 heads, up to 12,000 tokens:
+  // 18 us, with two blocks 23; 4 heads of 200,001: 16 blocks 19 us, 8 blocks 26.)
   int C = 1;
   while (C < evict::kMaxSelect && units * C * 2 <= num_sms && 4096 * C < capacity) C *= 2;
-  const int each = ((capacity + C - 1) / C + 3) / 4 * 4;
-  p.cached = each < evict::kMostCached ? each : evict::kMostCached;
-  const int most = (3 * evict::kBins + evict::kMostCached) * 4;
-  const void* kernel = reinterpret_cast<const void*>(evict::select_kernel);
-  const fa_status st = prepare_kernel(kernel, most);
-  if (st != FA_OK) return st;
-  // clusters of more than 8 blocks have to be asked for (on each device)
+  // clusters of more than 8 blocks have to be asked for (on each device), and whether
+  // they are to be had depends on the chip's parts
   if (C > evict::kMaxCluster &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-    return FA_ERR_CUDA;
-  return evict::launch_clusters(evict::select_kernel, (int)units, C, evict::kThreads,
-                                (3 * evict::kBins + p.cached) * 4, stream, p);
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+    cudaGetLastError();
+    C = evict::kMaxCluster;
+  }
+  for (;; C /= 2) {
+    const int each = ((capacity + C - 1) / C + 3) / 4 * 4;
+    p.cached = each < evict::kMostCached ? each : evict::kMostCached;
+    const int smem = (3 * evict::kBins + p.cached) * 4;
+    int most = 1;
+    if (C > evict::kMaxCluster && evict::clusters_at_once(kernel, C, evict::kThreads, smem, &most) && most == 0) continue;
+    return evict::launch_clusters(evict::select_kernel, (int)units, C, evict::kThreads, smem, stream, p);
+  }
 }
 
 fa_status launch_cache_keep(const KeepParams& p, int num_sms, cudaStream_t stream) {

@@ -1,15 +1,21 @@
 /*
  * fa_paged.h -- attention over a paged key/value cache, the cache's writes
- * and reads, and rotary positions (same shared library as fa.h).
+ * and reads, rotary positions, trees of drafted tokens, and eviction (same shared
+ * library as fa.h).
  *
  * The serving path: fa_rope() turns the new queries and keys, fa_cache_write()
  * puts the new keys and values into the pages of a cache, fa_fwd_paged()
- * attends from the new queries to everything a sequence has in its pages
- * (fa_fwd_paged_tree() where the new tokens are a tree of drafts, whose masks
- * fa_tree_mask() makes), and
+ * attends from the new queries to everything a sequence has in its pages, and
  * fa_cache_read() copies pages back into packed rows (the layout of fa_fwd()
  * and fa_bwd() with cu_seqlens).  For training, fa_rope() with `inverse` is
  * the gradient of fa_rope().
+ *
+ * Speculative decoding: the new tokens are a tree of drafts, whose masks and
+ * depths fa_tree_mask() makes; fa_fwd_paged_tree() attends with them, and
+ * fa_cache_keep() moves the accepted ones together.  Eviction: after an attention
+ * call, fa_cache_weights() adds the weights that each key got to its sum,
+ * fa_cache_select() chooses by the sums which tokens each head keeps, and
+ * fa_cache_keep() moves those together.
  *
  * The rules of fa.h hold (BF16 element types, FP32 LSE, contiguous arrays with
  * D innermost, D 64 or 128, 16-byte aligned device pointers, asynchronous on
@@ -44,10 +50,10 @@
  *     zero codes and stands for NaN.  The two NaN codes, 0x7F and 0xFF, and
  *     bytes outside 17 ... 246 and 255 are made by no write and mean nothing.
  *   - Offsets, lengths and page numbers live on the device, so their rules are
- *     checked there.  Offsets or lengths that break them make fa_fwd_paged()
- *     compute nothing, and fa_cache_write() and fa_cache_read() skip all rows of
- *     the sequences they concern; a page number outside [0, num_pages) that is needed reads
- *     as zeros (fa_cache_write() skips the token).  fa_get_device_error()
+ *     checked there.  Offsets or lengths that break them make fa_fwd_paged(),
+ *     fa_fwd_paged_tree() and fa_cache_weights() compute nothing, and the others skip
+ *     all rows of the sequences they concern; a page number outside [0, num_pages) that is needed reads
+ *     as zeros (a token that would be written to it is skipped).  fa_get_device_error()
  *     reports each as FA_ERR_INVALID_ARG.
  */
 #ifndef FA_GB300_FA_PAGED_H
@@ -207,10 +213,10 @@ FA_API fa_status fa_fwd_paged_tree(const void* q, const void* k_pages, const voi
  *                slots that are no token's stay as they are
  *   scale        > 0, a normal FP32 number
  *   decay        >= 0, finite
- * Weights and sums are FP32.  Over E4M3 pages, with up to 16 rows of a sequence and
+ * Weights and sums are FP32.  Over E4M3 pages, with up to 32 rows of a sequence and
  * head, queries are FP16 as fa_fwd_paged() has them; else keys are BF16, exactly.  A
- * token in a bad page gets no sum.  Sequences that share pages must not share the slots
- * of tokens of theirs in one call.  Results are bitwise repeatable.
+ * token in a bad page gets no sum.  Every token's slot is read and written, so the
+ * sequences with new tokens must not share pages.  Results are bitwise repeatable.
  */
 FA_API fa_status fa_cache_weights(const void* q, const float* lse, const void* k_pages, const void* k_scale,
                                   float* sums, int B, int Hq, int Hkv, int Sn, int D, int num_pages, int page_size,
