@@ -61,6 +61,11 @@ constexpr int kMinStretch = 2 * kBN;  // keys: shorter stretches cost more to jo
 // sequences, 1 to 500 tokens over up to 9000 keys: as nothing 123 us, as one block
 // 119, 4 110, 8 115; others 138 -> 99, 119 -> 72.)
 constexpr int kUnitCost = 4 * kBN;
+// What a block takes on the line, of a tree's unit whose second tile has no tokens, which
+// is common with trees: a block of one tile takes 15% less time than one of two, whose
+// tiles wait for each other's products.  (48 ragged trees up to 61 tokens over up to 8192
+// E4M3 keys: as much as others 212 us, 116 206, 108 201, 96 210.)
+constexpr int kSingleBlock = 108;
 
 enum Site {
   kSiteSeqs = 1, kSitePage, kSiteSegFull, kSiteSegEmpty, kSiteQEmpty, kSiteKvEmpty, kSiteKvFull, kSiteQFull, kSiteS,
@@ -187,17 +192,22 @@ struct Shared {
 FA_DEV int tile_tokens(int group) { return kBM / group; }
 
 // A sequence's pairs of tiles and the keys that they see.
+template <bool kTree>
 struct Seq {
   int n, L, q0;
   int pairs, t2;      // pairs of tiles, tokens of a pair
   bool causal;
+  bool single;        // (kTree) the last pair has tokens in its first tile alone
   // Keys of a pair: at least one, so that rows without a key are written too.
   FA_DEV int keys(int pair) const { return max(1, causal ? min(L, L - n + (pair + 1) * t2) : L); }
   FA_DEV int blocks(int pair) const { return (keys(pair) + kBN - 1) / kBN; }
   // What the pairs [0, p) take on the line: their keys, and kUnitCost each.
   FA_DEV long long prefix(int p) const { return keys_before(p) + (long long)p * kUnitCost; }
   FA_DEV long long keys_before(int p) const {
-    if (!causal) return (long long)p * max(1, L);
+    if (!causal) {
+      const long long k = max(1, L);
+      return p * k - (kTree && single && p == pairs ? k - (k * kSingleBlock + kBN - 1) / kBN : 0);
+    }
     const long long last = p == pairs ? keys(pairs - 1) : 0;  // the one whose end the sequence's end cuts
     if (p == pairs) --p;
     const int e0 = L - n + t2;                                // of pair 0
@@ -206,21 +216,31 @@ struct Seq {
            ((long long)p * (p - 1) - (long long)none * (none - 1)) / 2 * t2;
   }
   FA_DEV long long total() const { return prefix(pairs); }
+  // A block's length on the line.
+  FA_DEV int step(int pair) const { return kTree && single && pair == pairs - 1 ? kSingleBlock : kBN; }
+  FA_DEV int longest() const {
+    return (kTree && single && pairs == 1 ? (int)keys_before(1) : keys(pairs - 1)) + kUnitCost;
+  }
   // Pairs run from the last (the longest under a mask) to the first: keys of
   // the i units before unit i of a head, all of which have `total`.
   FA_DEV long long before(int i, long long total) const { return total - prefix(pairs - i); }
 };
-FA_DEV Seq seq_from(const PagedAttnParams& p, const paged::SeqRows& rows) {
-  Seq r;
+template <bool kTree>
+FA_DEV Seq<kTree> seq_from(const PagedAttnParams& p, const paged::SeqRows& rows) {
+  Seq<kTree> r;
   r.L = rows.L;
   r.n = rows.n;
   r.q0 = rows.q0;
   r.t2 = 2 * tile_tokens(p.group);
   r.pairs = (r.n + r.t2 - 1) / r.t2;
-  r.causal = p.causal != 0;
+  r.causal = !kTree && p.causal != 0;
+  r.single = kTree && r.n - (r.pairs - 1) * r.t2 <= r.t2 / 2;
   return r;
 }
-FA_DEV Seq seq_of(const PagedAttnParams& p, int b) { return seq_from(p, paged::rows_of(p.s, b)); }
+template <bool kTree>
+FA_DEV Seq<kTree> seq_of(const PagedAttnParams& p, int b) {
+  return seq_from<kTree>(p, paged::rows_of(p.s, b));
+}
 
 // The work of a call: prefix tables over the sequences and where the whole
 // rounds end.
@@ -247,13 +267,14 @@ FA_DEV int last_at_most(const T* table, int B, T x) {
 
 // Builds the tables; all threads of the block.  No units when the sequences
 // break the rules.
+template <bool kTree>
 FA_DEV Line build_line(const PagedAttnParams& p, long long* kpre, int* upre, long long* sums, int ctas) {
   Line line{kpre, upre, 0, 0, 0, 0, 0};
   const bool ok = paged::prefix_sequences(
       p.s, p.max_q,
       [&](const paged::SeqRows& rows) {
-        const Seq s = seq_from(p, rows);
-        return paged::Work{s.total() * p.s.Hkv, s.pairs * p.s.Hkv, s.keys(s.pairs - 1) + kUnitCost};
+        const Seq<kTree> s = seq_from<kTree>(p, rows);
+        return paged::Work{s.total() * p.s.Hkv, s.pairs * p.s.Hkv, s.longest()};
       },
       kpre, upre, sums);
   if (!ok) {
@@ -274,7 +295,7 @@ FA_DEV Line build_line(const PagedAttnParams& p, long long* kpre, int* upre, lon
     line.t0 = 0;
   } else if (line.whole < carry_u) {
     const int b = last_at_most(upre, p.s.B, line.whole);
-    const Seq s = seq_of(p, b);
+    const Seq<kTree> s = seq_of<kTree>(p, b);
     const int r = line.whole - upre[b], head = r / s.pairs;
     const long long total = s.total();
     line.t0 = kpre[b] + head * total + s.before(r - head * s.pairs, total);
@@ -294,10 +315,11 @@ struct Place {
 };
 // The last one at or before position t < t1; kb may be the unit's blocks (t lies
 // in its cost: the unit stays whole).  One warp, converged.
+template <bool kTree>
 FA_DEV Place find_place(const PagedAttnParams& p, const Line& line, long long t) {
   Place w;
   w.b = last_at_most(line.kpre, p.s.B, t);
-  const Seq s = seq_of(p, w.b);
+  const Seq<kTree> s = seq_of<kTree>(p, w.b);
   const long long per_head = s.total();
   long long r = t - line.kpre[w.b];
   w.head = (int)paged::div64(r, per_head);
@@ -313,7 +335,7 @@ FA_DEV Place find_place(const PagedAttnParams& p, const Line& line, long long t)
   }
   w.i = lo;
   w.start = t - r + s.before(lo, per_head);
-  w.kb = min((int)((t - w.start) / kBN), s.blocks(s.pairs - 1 - lo));
+  w.kb = min((int)((t - w.start) / s.step(s.pairs - 1 - lo)), s.blocks(s.pairs - 1 - lo));
   return w;
 }
 
@@ -368,13 +390,13 @@ FA_DEV int tile_blocks(const Seg& w, int t, int tt, bool causal) {
   return min(w.count, max(0, (end + kBN - 1) / kBN - w.kb));
 }
 
-template <int D, bool kFp8>
+template <int D, bool kFp8, bool kTree>
 __device__ void scheduler_role(const Shared<D, kFp8>& sh, const PagedAttnParams& p, const Line& line) {
   const int lane = threadIdx.x % 32;
   const int G = gridDim.x, c = blockIdx.x;
   int slot_i = 0;
   uint32_t phase = 1;
-  auto put = [&](int b, int head, int pair, int kb, int count, const Seq& s, int slot) -> bool {
+  auto put = [&](int b, int head, int pair, int kb, int count, const Seq<kTree>& s, int slot) -> bool {
     if (!sh.wait_long(sh.seg_empty(slot_i), phase, kSiteSegEmpty, p)) return false;
     if (lane == 0) {
       volatile Seg& r = sh.segs()[slot_i];
@@ -398,22 +420,23 @@ __device__ void scheduler_role(const Shared<D, kFp8>& sh, const PagedAttnParams&
   };
   for (int u = c; u < line.whole; u += G) {
     const int b = last_at_most(line.upre, p.s.B, u);
-    const Seq s = seq_of(p, b);
+    const Seq<kTree> s = seq_of<kTree>(p, b);
     const int r = u - line.upre[b], head = r / s.pairs;
     const int pair = s.pairs - 1 - (r - head * s.pairs);
     if (!put(b, head, pair, 0, s.blocks(pair), s, -1)) return;
   }
   paged::Join join{};
   if (c < line.G) {
-    Place w = find_place(p, line, line.stretch(c));
+    Place w = find_place<kTree>(p, line, line.stretch(c));
     const bool to_end = c + 1 == line.G;
-    const Place z = to_end ? Place{} : find_place(p, line, line.stretch(c + 1));
-    Seq s = seq_of(p, w.b);
+    const Place z = to_end ? Place{} : find_place<kTree>(p, line, line.stretch(c + 1));
+    Seq<kTree> s = seq_of<kTree>(p, w.b);
     const int pair = s.pairs - 1 - w.i, nblk = s.blocks(pair);
     if (w.kb > 0 && w.kb < nblk) {
       // the unit is cut here: if for the first time, its parts are joined
-      if (line.stretch(c - 1) < w.start + kBN) {
-        const long long end = w.start + (long long)nblk * kBN;
+      const int step = s.step(pair);
+      if (line.stretch(c - 1) < w.start + step) {
+        const long long end = w.start + (long long)nblk * step;
         join = paged::Join{2, w.b, w.head, pair * s.t2, s.n, s.q0, {0, 0}};
         while (c + join.parts - 1 < line.G && line.stretch(c + join.parts - 1) < end) ++join.parts;
       }
@@ -435,7 +458,7 @@ __device__ void scheduler_role(const Shared<D, kFp8>& sh, const PagedAttnParams&
           w.head = 0;
           do {
             if (++w.b == p.s.B) break;
-            s = seq_of(p, w.b);
+            s = seq_of<kTree>(p, w.b);
           } while (s.n == 0);
           if (w.b == p.s.B) break;
         }
@@ -443,7 +466,7 @@ __device__ void scheduler_role(const Shared<D, kFp8>& sh, const PagedAttnParams&
     }
   }
   if (lane == 0) *Part<D>::join(p.part, c) = join;
-  Seq none{};
+  Seq<kTree> none{};
   put(-1, 0, 0, 0, 0, none, -1);
 }
 
@@ -1267,7 +1290,7 @@ __global__ void __launch_bounds__(Layout<D, kFp8>::kThreads, 1)
     tmem_alloc(sh.tmem_slot(), 512);
     tmem_relinquish();
   }
-  const Line line = build_line(p, reinterpret_cast<long long*>(smem + L::kKPre), reinterpret_cast<int*>(smem + L::kUPre),
+  const Line line = build_line<kTree>(p, reinterpret_cast<long long*>(smem + L::kKPre), reinterpret_cast<int*>(smem + L::kUPre),
                                reinterpret_cast<long long*>(smem + L::kSums), gridDim.x);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before();
@@ -1290,7 +1313,7 @@ __global__ void __launch_bounds__(Layout<D, kFp8>::kThreads, 1)
     } else if (warp == 14) {
       if constexpr (!kFp8) clean_role<D>(sh, p);
     } else {
-      scheduler_role<D, kFp8>(sh, p, line);
+      scheduler_role<D, kFp8, kTree>(sh, p, line);
     }
   } else {
     if constexpr (kFp8) {
