@@ -944,10 +944,12 @@ __global__ void __launch_bounds__(Layout<D, kFp8>::kThreads, 1)
     tmem_alloc(sh.tmem_slot(), 512);
     tmem_relinquish();
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");      // nothing global before this
   const bool ok = paged::prefix_sequences(
       p.s, p.max_q,
       [&](const paged::SeqRows& r) { return paged::Work{(long long)p.s.Hkv * units_of(r.L), 0, 0}; },
       reinterpret_cast<long long*>(smem + L::kPre), nullptr, reinterpret_cast<long long*>(smem + L::kSums));
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!ok && blockIdx.x == 0 && threadIdx.x == 0) paged::record_bad_input(&g_err, kSiteSeqs);
   tc_fence_before();
   __syncthreads();
@@ -998,8 +1000,7 @@ fa_status launch_blocks(const WeighParams& p, int num_sms, cudaStream_t stream) 
     return st;
   auto kernel = block_kernel<D, kFp8>;
   if ((st = prepare_kernel(reinterpret_cast<const void*>(kernel), L::kBytes)) != FA_OK) return st;
-  kernel<<<num_sms, L::kThreads, L::kBytes, stream>>>(tq, tk, p);
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  return launch_overlapped(kernel, dim3(num_sms), L::kThreads, L::kBytes, stream, tq, tk, p);
 }
 
 template <int D, bool kFp8>

@@ -154,3 +154,80 @@ def test_eviction(fa, n, fp8):
             one = f64(y[b:b + 1])
             plain.append(x, b, P.dequantise(*P.quantise(one)) if fp8 else one)
     check_rows(o, lse, q[rows], plain, new, [np.ones((m, L), dtype=bool) for m, L in zip(new, lens)], D ** -0.5)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_pages_far_from_the_first(fa, fp8):
+    """Pages whose elements lie behind the 2^31st: bit by bit what the same pages give at
+    the front."""
+    D, Hkv, Hq, page, far = 128, 8, 16, 64, 33000 * (2 if fp8 else 1)
+    lens, B = [300, 129, 700], 3
+    c = Cache(lens, Hkv, D, page, fp8, seed=6)
+    assert far * Hkv * page * D > 2 ** 31
+    big = {}
+    for name in ("k_pages", "v_pages", "k_scale", "v_scale"):
+        x = getattr(c, name)
+        if x is None:
+            big[name] = None
+            continue
+        big[name] = torch.empty((far + c.num_pages, *x.shape[1:]), dtype=x.dtype, device="cuda")
+        big[name].view(torch.uint8)[far:] = x.view(torch.uint8)
+    table = torch.where(c.block_table >= 0, c.block_table + far, c.block_table)
+    sums = torch.rand(c.k_pages.shape[:3], generator=torch.Generator().manual_seed(2)).cuda()
+    far_sums = torch.empty((far + c.num_pages, Hkv, page), device="cuda")
+    far_sums[far:] = sums
+
+    def steps(k, v, ks, vs, table, sums):
+        out = []
+        for n in (2, 40):
+            q = randn((B, n, Hq, D), n).cuda()
+            mask, _ = fa.tree_mask(ints([parents_of(n, b) for b in range(B)]))
+            out += fa.fwd_paged(q, k, v, table, c.seq_lens, tree=mask, k_scale=ks, v_scale=vs)
+            _, lse = fa.fwd_paged(q, k, v, table, c.seq_lens, k_scale=ks, v_scale=vs)
+            fa.cache_weights(q, lse, k, sums, table, c.seq_lens, k_scale=ks)
+        out += fa.cache_select(sums, table, c.seq_lens, 100, first=1, recent=9)
+        fa.cache_keep(k, v, table, out[-2], out[-1], k_scale=ks, v_scale=vs, sums=sums)
+        assert fa.get_device_error() == 0
+        return out
+
+    near = steps(c.k_pages, c.v_pages, c.k_scale, c.v_scale, c.block_table, sums)
+    there = steps(big["k_pages"], big["v_pages"], big["k_scale"], big["v_scale"], table, far_sums)
+    for a, b in zip(near, there):
+        assert torch.equal(a, b)
+    for name, x in list(big.items()) + [("sums", far_sums)]:
+        if x is not None:
+            small = sums if name == "sums" else getattr(c, name)
+            assert torch.equal(x[far:].contiguous().view(torch.uint8), small.view(torch.uint8)), name
+
+
+def test_streams_side_by_side(fa):
+    """Calls on two streams at once, each over its own cache, bit by bit as one after the other."""
+    def case(seed):
+        c = Cache([900, 333], 2, 64, 32, bool(seed % 2), seed=seed)
+        q = randn((2, 40, 8, 64), seed).cuda()
+        mask, _ = fa.tree_mask(ints([parents_of(40, seed), parents_of(40, seed + 9)]))
+        return c, q, mask, torch.zeros(c.k_pages.shape[:3], device="cuda")
+
+    def run(c, q, mask, sums):
+        out = list(fa.fwd_paged(q, c.k_pages, c.v_pages, c.block_table, c.seq_lens, tree=mask, **c.scales))
+        _, lse = fa.fwd_paged(q, c.k_pages, c.v_pages, c.block_table, c.seq_lens, **c.scales)
+        fa.cache_weights(q, lse, c.k_pages, sums, c.block_table, c.seq_lens, k_scale=c.k_scale)
+        fa.cache_weights(q[:, :1].contiguous(), lse[:, :, :1].contiguous(), c.k_pages, sums, c.block_table, c.seq_lens,
+                         k_scale=c.k_scale)
+        index, kept = fa.cache_select(sums, c.block_table, c.seq_lens, 64)
+        fa.cache_keep(c.k_pages, c.v_pages, c.block_table, index, kept, sums=sums, **c.scales)
+        return out + [index, kept, sums, c.k_pages.view(torch.uint8), c.v_pages.view(torch.uint8)]
+
+    want = [[x.clone() for x in run(*case(s))] for s in (1, 2)]
+    cases = [case(s) for s in (1, 2)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = []
+    for s, k in zip(streams, cases):
+        with torch.cuda.stream(s):
+            got.append(run(*k))
+    torch.cuda.synchronize()
+    assert fa.get_device_error() == 0
+    for a, b in zip(want, got):
+        for x, y in zip(a, b):
+            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
