@@ -59,13 +59,12 @@ FA_DEV long long row_of(const PagedSeqs& s, int b, int head, int tok) {
 // It reads four bytes a key, little: what takes the time is the chain of loads and
 // barriers, and the instructions for each token of the few SMs that take part.
 
-constexpr int kThreads = 1024;
-constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kGroups = kBins / 32;        // of bins that a warp adds up
 static_assert(kGroups == 64, "two groups a lane");
 FA_DEV int bits_of(int round) { return round == 2 ? 10 : 11; }
 FA_DEV int shift_of(int round) { return round == 0 ? 21 : round == 1 ? 10 : 0; }
+constexpr int kShort = 2048;               // tokens of a table whose heads take the smallest blocks
 constexpr int kMostCached = 49152;         // tokens of a block in shared memory; the others are read again
 
 // Floats in an order that unsigned integers have; a NaN is above all numbers.  Nothing
@@ -87,7 +86,9 @@ FA_DEV uint32_t scan(uint32_t v, int lane) {
   return v;
 }
 
+template <int kThreads>
 __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) {
+  constexpr int kWarps = kThreads / 32;
   extern __shared__ __align__(16) uint32_t smem[];
   uint32_t* hist = smem;                              // [3][kBins]
   uint32_t* cached = smem + 3 * kBins;
@@ -533,33 +534,48 @@ fa_status launch_keep(const KeepParams& p, int num_sms, cudaStream_t stream) {
 
 }  // namespace evict
 
-fa_status launch_cache_select(const SelectParams& in, int num_sms, cudaStream_t stream) {
+namespace evict {
+
+template <int kThreads>
+fa_status launch_select(const SelectParams& in, int C, cudaStream_t stream) {
   SelectParams p = in;
   const int capacity = p.s.max_pages << p.s.page_shift;
   const long long units = (long long)p.s.B * p.s.Hkv;
-  const void* kernel = reinterpret_cast<const void*>(evict::select_kernel);
-  const fa_status st = prepare_kernel(kernel, (3 * evict::kBins + evict::kMostCached) * 4);
+  auto kernel = select_kernel<kThreads>;
+  const void* func = reinterpret_cast<const void*>(kernel);
+  const fa_status st = prepare_kernel(func, (3 * kBins + kMostCached) * 4);
   if (st != FA_OK) return st;
-  // A block of its own for each head where those fill the SMs, else a cluster, but no
-  // more blocks than have some thousand tokens each.  (24 x 8 heads, up to 12,000 tokens:
-  // 18 us, with two blocks 23; 4 heads of 200,001: 16 blocks 19 us, 8 blocks 26.)
-  int C = 1;
-  while (C < evict::kMaxSelect && units * C * 2 <= num_sms && 4096 * C < capacity) C *= 2;
   // clusters of more than 8 blocks have to be asked for (on each device), and whether
   // they are to be had depends on the chip's parts
-  if (C > evict::kMaxCluster &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+  if (C > kMaxCluster && cudaFuncSetAttribute(func, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
     cudaGetLastError();
-    C = evict::kMaxCluster;
+    C = kMaxCluster;
   }
   for (;; C /= 2) {
     const int each = ((capacity + C - 1) / C + 3) / 4 * 4;
-    p.cached = each < evict::kMostCached ? each : evict::kMostCached;
-    const int smem = (3 * evict::kBins + p.cached) * 4;
+    p.cached = each < kMostCached ? each : kMostCached;
+    const int smem = (3 * kBins + p.cached) * 4;
     int most = 1;
-    if (C > evict::kMaxCluster && evict::clusters_at_once(kernel, C, evict::kThreads, smem, &most) && most == 0) continue;
-    return evict::launch_clusters(evict::select_kernel, (int)units, C, evict::kThreads, smem, stream, p);
+    if (C > kMaxCluster && clusters_at_once(func, C, kThreads, smem, &most) && most == 0) continue;
+    return launch_clusters(kernel, (int)units, C, kThreads, smem, stream, p);
   }
+}
+
+}  // namespace evict
+
+// A block of its own for each head where those fill the SMs, else a cluster, but no more
+// blocks than have some thousand tokens each.  (24 x 8 heads, up to 12,000 tokens: 18 us,
+// with two blocks 23; 4 heads of 200,001: 16 blocks 19 us, 8 blocks 26.)
+// More heads than two blocks an SM take smaller ones, of which an SM holds more: 800
+// heads of 1253 tokens 30 / 16.5 / 13 us with 1024 / 512 / 256 threads, 512 of 4000 24 /
+// 14.4 / 15.4; but 160 of 4000 8.3 / 11.6 / 12.5.
+fa_status launch_cache_select(const SelectParams& p, int num_sms, cudaStream_t stream) {
+  const int capacity = p.s.max_pages << p.s.page_shift;
+  const long long units = (long long)p.s.B * p.s.Hkv;
+  int C = 1;
+  while (C < evict::kMaxSelect && units * C * 2 <= num_sms && 4096 * C < capacity) C *= 2;
+  if (units <= 2ll * num_sms) return evict::launch_select<1024>(p, C, stream);
+  return capacity <= evict::kShort ? evict::launch_select<256>(p, 1, stream) : evict::launch_select<512>(p, 1, stream);
 }
 
 fa_status launch_cache_keep(const KeepParams& p, int num_sms, cudaStream_t stream) {
