@@ -186,8 +186,8 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
     }
     sync_all();
     // this block's share: bins [rank * share, + share), 32 a warp
-    const int share = kBins / C;
-    for (int g = warp; g < share / 32; g += kWarps) {
+    const int share = kBins / C, per = kGroups / C, shift_per = __ffs(per) - 1;      // (powers of two)
+    for (int g = warp; g < per; g += kWarps) {
       uint32_t sum = 0u;
       if (C == 1) {
         sum = h[g * 32 + lane];
@@ -199,15 +199,16 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
 #pragma unroll
         for (int r = 0; r < kMaxSelect; ++r) sum += x[r];
       }
-      total[g * 32 + lane] = sum;
+      if (C > 1) total[g * 32 + lane] = sum;
       sum = __reduce_add_sync(0xffffffffu, sum);
       if (lane == 0) group_total[g] = sum;
     }
     sync_all();
     if (warp == 0) {
       // the group, then the bin in it, from the top down
-      const int per = share / 32;
-      auto group_of = [&](int g) { return ld_cluster_u32(mapa_shared(smem_u32(group_total + g % per), g / per)); };
+      auto group_of = [&](int g) {
+        return C == 1 ? group_total[g] : ld_cluster_u32(mapa_shared(smem_u32(group_total + (g & (per - 1))), g >> shift_per));
+      };
       const uint32_t v0 = group_of(63 - 2 * lane), v1 = group_of(62 - 2 * lane);
       uint32_t above = scan(v0 + v1, lane) - v0 - v1;
       uint32_t mine = __ballot_sync(0xffffffffu, above < need && above + v0 + v1 >= need);
@@ -215,7 +216,9 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
       const bool second = above + v0 < need;
       const int group = __shfl_sync(0xffffffffu, second ? 62 - 2 * lane : 63 - 2 * lane, at);
       const uint32_t base = __shfl_sync(0xffffffffu, second ? above + v0 : above, at);
-      const uint32_t v = ld_cluster_u32(mapa_shared(smem_u32(total + group % per * 32 + 31 - lane), group / per));
+      const uint32_t v =
+          C == 1 ? h[group * 32 + 31 - lane]
+                 : ld_cluster_u32(mapa_shared(smem_u32(total + (group & (per - 1)) * 32 + 31 - lane), group >> shift_per));
       above = base + scan(v, lane) - v;
       mine = __ballot_sync(0xffffffffu, above < need && above + v >= need);
       at = mine ? __ffs(mine) - 1 : 0;

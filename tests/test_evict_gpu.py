@@ -81,9 +81,10 @@ def test_select_long(fa, L):
     s.check(fa, L - 1)
 
 
-def test_select_many(fa):
-    """As many heads as leave each one block."""
-    Sums([900] * 40, 32, 16, seed=1).check(fa, 100, 1, 30)
+@pytest.mark.parametrize("L,B", [(900, 40), (3000, 14)])
+def test_select_many(fa, L, B):
+    """More heads than two blocks an SM, of short sequences and of longer ones."""
+    Sums([L] * (B - 1) + [5], 32, 16, seed=1).check(fa, 100, 1, 30)
 
 
 def test_select_bad_input(fa):
