@@ -567,11 +567,11 @@ fa_status launch_select(const SelectParams& in, int C, cudaStream_t stream) {
 }  // namespace evict
 
 // A block of its own for each head where those fill the SMs, else a cluster, but no more
-// blocks than have some thousand tokens each.  (24 x 8 heads, up to 12,000 tokens: 18 us,
-// with two blocks 23; 4 heads of 200,001: 16 blocks 19 us, 8 blocks 26.)
+// blocks than have some thousand tokens each.  (24 x 8 heads, up to 12,000 tokens: 17 us,
+// with two blocks 5 more; 4 heads of 200,001: 16 blocks 18 us, 8 blocks 26.)
 // More heads than two blocks an SM take smaller ones, of which an SM holds more: 800
 // heads of 1253 tokens 30 / 16.5 / 13 us with 1024 / 512 / 256 threads, 512 of 4000 24 /
-// 14.4 / 15.4; but 160 of 4000 8.3 / 11.6 / 12.5.
+// 14.4 / 15.4; but 160 of 4000 8.3 / 11.6 / 12.5 (the smaller ones 1 to 2 us less by now).
 fa_status launch_cache_select(const SelectParams& p, int num_sms, cudaStream_t stream) {
   const int capacity = p.s.max_pages << p.s.page_shift;
   const long long units = (long long)p.s.B * p.s.Hkv;
