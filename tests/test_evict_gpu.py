@@ -280,3 +280,17 @@ def test_binding_refusals(fa):
     with pytest.raises(ValueError):
         fa.cache_select(sums.half(), c.block_table, c.seq_lens, 4)
     assert fa.get_device_error() == 0
+
+
+def test_long_selection_in_a_graph(fa):
+    """A selection by clusters of 16 blocks, first called while a graph is captured."""
+    s = Sums([150001], 1, 64, seed=6)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        index, kept = fa.cache_select(s.sums, s.block_table, s.seq_lens, 3000, 4, 500)
+    for _ in range(2):
+        index.fill_(-7)
+        graph.replay()
+        torch.cuda.synchronize()
+        np.testing.assert_array_equal(index[0, 0].cpu().numpy(), P.select(s.rows[0][0], 3000, 4, 500))
+    assert kept.tolist() == [3000] and fa.get_device_error() == 0
