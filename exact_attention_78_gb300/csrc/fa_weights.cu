@@ -374,8 +374,9 @@ fa_status launch_step(const WeighParams& p, int num_sms, cudaStream_t stream) {
 // no row statistics, no second product.  Both operands' tiles are read by all units
 // of a head (Q) or tiles of rows (K), from L2.
 //
-// 2048 tokens over 32,768 BF16 keys, 32/8 heads: 452 us, of which the products take 281 at
-// cuBLAS's rate and the exponentials 230; each set of warps waits for scores a tenth of
+// 2048 tokens over 32,768 BF16 keys, 32/8 heads: 433 us, of which the products take 281 at
+// cuBLAS's rate and the exponentials 230 (452 where a tile that is not full, or not seen
+// whole by all keys of a warp, was masked throughout); each set of warps waits for scores a tenth of
 // the time, the products' warp a third of it for room.  (One set of eight warps 597 us;
 // two that took tiles in turn 510; a share of the exponentials as polynomials on the
 // FMA pipe, 1 / 2 / 4 of 8 pairs, 549 / 594 / 728 instead.)  With few rows a unit's fixed
@@ -642,7 +643,7 @@ __device__ void lse_role(const Shared<D, kFp8>& sh, const WeighParams& p) {
     if (!more) return 0;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-      y[i] = 0.0f;
+      y[i] = INFINITY;      // (of a column without a row)
       if (tok[i] < tt && tok0 + tok[i] < n) y[i] = p.lse[lse_at(p, b, q0, head0 + head[i], tok0 + tok[i])];
     }
     tok0 += tt;
@@ -842,7 +843,9 @@ __device__ void sum_role(const int m, const int j, const Shared<D, kFp8>& sh, co
         const int lo = p.causal ? max(0, past_key - tok0) * p.group - 64 * j : 0;        // first one that sees the key
         const uint32_t tm = tm0 + i * 128;
         const float* nlse = sh.lse(i) + 64 * j;
-        const bool plain = __all_sync(0xffffffffu, lo <= 0 && hi >= 64);
+        // Columns that are no row's in any tile (the group does not divide 128) have queries
+        // of zero and an LSE of infinity; in a tile that is not full they are other rows'.
+        const bool seen = __all_sync(0xffffffffu, lo <= 0), plain = seen && hi >= min(64, tt * p.group - 64 * j);
         uint64_t sum2[2] = {0ull, 0ull};
         uint32_t xa[kCols], xb[kCols];
         if (!sh.wait(sh.s_full(m, i), phase >> i & 1, kSiteSFull, p)) return;
@@ -872,7 +875,10 @@ __device__ void sum_role(const int m, const int j, const Shared<D, kFp8>& sh, co
 #pragma unroll 1
           for (int c = 0; c < 64; c += kCols) {
             scores_here(xa);
-            add_weights<true>(xa, nlse + c, p.scale, lo - c, hi - c, sum2);
+            if (seen && c + kCols <= hi)
+              add_weights<false>(xa, nlse + c, p.scale, 0, 0, sum2);
+            else
+              add_weights<true>(xa, nlse + c, p.scale, lo - c, hi - c, sum2);
             if (c + kCols < min(hi, 64)) {
               load_scores(tm + c + kCols, xa);
             } else {
@@ -940,6 +946,13 @@ __global__ void __launch_bounds__(Layout<D, kFp8>::kThreads, 1)
     tma_prefetch_desc(&tm_q);
     if (!kFp8) tma_prefetch_desc(&tm_k);
   }
+  // rows of Q's tiles that no box fills
+  const int rows = kBN / p.group * p.group;
+  for (int i = threadIdx.x; i < (kBN - rows) * 8 * L::kChunks * L::kQStages; i += L::kThreads) {
+    const int chunk = i / ((kBN - rows) * 8), at = i - chunk * (kBN - rows) * 8;
+    *reinterpret_cast<uint4*>(smem + L::kQ + chunk * L::kChunkBytes + rows * 128 + at * 16) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();
   if (warp == 17) {
     tmem_alloc(sh.tmem_slot(), 512);
     tmem_relinquish();

@@ -215,7 +215,8 @@ FA_API fa_status fa_fwd_paged_tree(const void* q, const void* k_pages, const voi
  *   decay        >= 0, finite
  * Weights and sums are FP32.  Over E4M3 pages, with up to 32 rows of a sequence and
  * head, queries are FP16 as fa_fwd_paged() has them; else keys are BF16, exactly.  A
- * token in a bad page gets no sum.  Every token's slot is read and written, so the
+ * token in a bad page gets no sum.  What is not finite in a key reaches that key's own
+ * sum alone.  Every token's slot is read and written, so the
  * sequences with new tokens must not share pages.  Results are bitwise repeatable.
  */
 FA_API fa_status fa_cache_weights(const void* q, const float* lse, const void* k_pages, const void* k_scale,

@@ -121,6 +121,26 @@ def test_sums_of_an_attention_call(fa, n, fp8):
     np.testing.assert_allclose(sums.double().sum((0, 2)).cpu().numpy(), [2 * n * 4] * 2, rtol=1e-4)
 
 
+@pytest.mark.parametrize("n,Hq", [(1, 4), (9, 3), (30, 4), (60, 3)])
+def test_keys_that_are_not_finite(fa, n, Hq):
+    """They reach their own sums alone: also where the group leaves columns of a tile
+    without rows, and keys share a tile with them."""
+    c = Cache([300], 1, 128, 16, False, seed=6)
+    q, lse = randn((1, n, Hq, 128), 2).cuda(), torch.full((1, Hq, n), 5.0, device="cuda")
+    want = torch.zeros(c.k_pages.shape[:3], device="cuda")
+    fa.cache_weights(q, lse, c.k_pages, want, c.block_table, c.seq_lens)
+    for x in (float("nan"), float("inf"), -float("inf")):
+        c.upload()
+        got = torch.zeros_like(want)
+        for t in (7, 130):
+            c.k_pages[c.table[0, t // 16], 0, t % 16, 5] = x
+        fa.cache_weights(q, lse, c.k_pages, got, c.block_table, c.seq_lens)
+        for t in (7, 130):
+            got[c.table[0, t // 16], 0, t % 16] = want[c.table[0, t // 16], 0, t % 16]
+        assert torch.equal(got, want)
+    assert fa.get_device_error() == 0
+
+
 def test_bad_input(fa):
     for n in (1, 40):
         c = Cache([40, 60], 1, 64, 16, False, seed=1, junk=0.0)
