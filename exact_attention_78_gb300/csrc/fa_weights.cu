@@ -131,6 +131,12 @@ __global__ void __launch_bounds__(StepLayout<D, kFp8, kTiles>::kThreads, 1) step
   using Lay = StepLayout<D, kFp8, kTiles>;
   constexpr int kPieces = Lay::kPieces, kHalves = Lay::kHalves, kKeys = Lay::kKeys;
   constexpr int kWords = kFp8 ? 2 * kPieces : kPieces;        // of 16 bytes of a row of Q
+  // The tensor cores cut a running sum off where FP32 would round it, so a score is the
+  // sum of kParts shorter ones that are added, and rounded, outside them.  Error of
+  // the sums over 65,536 BF16 keys, D = 128, against 64 bits: one token, 8 heads
+  // 8.7e-7 as one sum, 5.2e-7 as two, 4.1e-7 as four; 32 rows 8.4e-7 and 3.7e-7.  Four cost
+  // nothing at 8 rows (51-52 us for 64 x 4096 keys); two cost 64 -> 70 us at 32, four spill.
+  constexpr int kParts = kTiles == 1 ? 4 : 2;
   extern __shared__ __align__(128) uint8_t ring_raw[];
   __shared__ long long pre[kMaxPackedSeqs + 1];
   __shared__ long long work_sums[2 * Lay::kWarps];
@@ -278,9 +284,12 @@ __global__ void __launch_bounds__(StepLayout<D, kFp8, kTiles>::kThreads, 1) step
       const uint8_t* from = ring + stage * Lay::kStage + half * Lay::kTile + g * Lay::kRowBytes + c * 16;
       const uint8_t* stats = ring + stage * Lay::kStage;
       const int key0 = at.k * kKeys + 16 * half;
-      float s[kTiles][4];                              // [2 h + e]: key g + 8 h, row 8 n + 2 c + e
+      // [2 h + e]: key g + 8 h, row 8 n + 2 c + e
+      float part[kTiles][kParts][4];
 #pragma unroll
-      for (int n = 0; n < kTiles; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+      for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) part[n][i][0] = part[n][i][1] = part[n][i][2] = part[n][i][3] = 0.0f;
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
         const uint4 x = *reinterpret_cast<const uint4*>(from + i * 64);
@@ -288,8 +297,8 @@ __global__ void __launch_bounds__(StepLayout<D, kFp8, kTiles>::kThreads, 1) step
         if (!kFp8) {
 #pragma unroll
           for (int n = 0; n < kTiles; ++n) {
-            mma16816(s[n], x.x, y.x, x.y, y.y, qf[n][i].x, qf[n][i].y);
-            mma16816(s[n], x.z, y.z, x.w, y.w, qf[n][i].z, qf[n][i].w);
+            mma16816(part[n][2 * i % kParts], x.x, y.x, x.y, y.y, qf[n][i].x, qf[n][i].y);
+            mma16816(part[n][(2 * i + 1) % kParts], x.z, y.z, x.w, y.w, qf[n][i].z, qf[n][i].w);
           }
         } else {
           const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
@@ -300,11 +309,20 @@ __global__ void __launch_bounds__(StepLayout<D, kFp8, kTiles>::kThreads, 1) step
 #pragma unroll
             for (int n = 0; n < kTiles; ++n) {
               const uint4 qw = qf[n][kFp8 ? 2 * i + j / 2 : 0];
-              mma16816_f16(s[n], a0, a1, a2, a3, j % 2 ? qw.z : qw.x, j % 2 ? qw.w : qw.y);
+              mma16816_f16(part[n][j % kParts], a0, a1, a2, a3, j % 2 ? qw.z : qw.x, j % 2 ? qw.w : qw.y);
             }
           }
         }
       }
+      float s[kTiles][4];
+#pragma unroll
+      for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[n][e] = part[n][0][e];
+#pragma unroll
+          for (int i = 1; i < kParts; ++i) s[n][e] += part[n][i][e];
+        }
       float w[2];                                      // of keys g, g + 8
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
