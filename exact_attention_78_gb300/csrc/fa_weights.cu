@@ -51,7 +51,11 @@ FA_DEV long long slot_of(const WeighParams& p, int b, int head, int key) {
 // E4M3 keys took 73 us; copying them to shared memory 60; so 57.)
 //
 // E4M3 codes become FP16, and the queries too, by a power of two of each row's own
-// (as in the decode kernel of the attention); keys' scales go to the scores in FP32.
+// (as in the decode kernel of the attention); keys' scales go to the scores in FP32.  A
+// product is brought back by its row's power of two, with that of `scale`, before it
+// meets the key's: that is where queries and keys far from one cancel, and the other
+// way round products of 2^30 pass FP32's range with keys from 2^98 on.  Powers of two
+// round nothing; the rest of `scale`, 1 to 2, goes along with the key's.
 
 constexpr int kStepRows = 32;        // most rows of a sequence and key/value head here
 
@@ -215,6 +219,8 @@ __global__ void __launch_bounds__(StepLayout<D, kFp8, kTiles>::kThreads, 1) step
   for (int i = 0; i < Lay::kDepth; ++i) copy(i);
 
   const int least_exp = 14 + max(0, 127 - (int)(__float_as_uint(p.scale) >> 23));
+  const float scale_pow = __uint_as_float(__float_as_uint(p.scale) & 0x7F800000u);
+  const uint32_t scale_rest = __float_as_uint(p.scale) & 0x007FFFFFu;      // (p.scale is a normal number)
   int stage = 0;
   uint32_t phase = 0;
   bool fresh = true;                                   // a unit begins
@@ -240,7 +246,7 @@ __global__ void __launch_bounds__(StepLayout<D, kFp8, kTiles>::kThreads, 1) step
       }
 #pragma unroll
       for (int n = 0; n < kTiles; ++n) {
-        float scale = p.scale;
+        float scale = kFp8 ? scale_pow : p.scale;
         if (kFp8) {
           uint32_t top = 0u;
 #pragma unroll
@@ -327,16 +333,18 @@ __global__ void __launch_bounds__(StepLayout<D, kFp8, kTiles>::kThreads, 1) step
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         // (a row that stands for NaN has codes of zero and the byte 255, which is
-        // infinity here: its scores are NaN)
-        const float fac = kFp8 ? __uint_as_float((uint32_t)stats[Lay::kScales + 16 * half + g + 8 * h] << 23) : 1.0f;
+        // infinity or NaN here: its scores are NaN)
+        const float fac =
+            kFp8 ? __uint_as_float((uint32_t)stats[Lay::kScales + 16 * half + g + 8 * h] << 23 | scale_rest) : 1.0f;
         uint64_t sum2 = 0ull;
 #pragma unroll
         for (int n = 0; n < kTiles; ++n) {
           // taken from the LSE before it goes to log2 units: the difference is small
           // where the weight is large, and so is its rounding
-          uint64_t x2 = pk2(s[n][2 * h], s[n][2 * h + 1]);
-          if (kFp8) x2 = mul2(x2, pk2(fac, fac));
-          x2 = mul2(fma2(x2, pk2(row_scale[n][0], row_scale[n][1]), pk2(nlse[n][0], nlse[n][1])), pk2(kLog2e, kLog2e));
+          const uint64_t s2 = pk2(s[n][2 * h], s[n][2 * h + 1]), row2 = pk2(row_scale[n][0], row_scale[n][1]);
+          const uint64_t nlse2 = pk2(nlse[n][0], nlse[n][1]);
+          const uint64_t x2 =
+              mul2(kFp8 ? fma2(mul2(s2, row2), pk2(fac, fac), nlse2) : fma2(s2, row2, nlse2), pk2(kLog2e, kLog2e));
           float x0, x1;
           up2(x2, x0, x1);
           const int key = key0 + g + 8 * h;
