@@ -696,6 +696,12 @@ __device__ void lse_role(const Shared<D, kFp8>& sh, const WeighParams& p) {
   }
 }
 
+// What keys of E4M3 pages are held times: 2^key_exp.  With a scale below 2^-110 products
+// pass FP32's range where scores are ordinary, so what the scale lies below that goes to
+// the keys.  All but those below 2^-110 stay exact, and what is cut off of these moves
+// no score by more than 2^-100: each element by 2^-134, times queries, times 2^-109 at most.
+FA_DEV int key_exp(float scale) { return min(0, (int)(__float_as_uint(scale) >> 23) - (127 - 110)); }
+
 // E4M3 pages: eight warps make the unit's keys BF16, which holds a code times its
 // power of two exactly.  Rows behind the sequence's end are left as they were: each
 // is a lane of the product of its own.
@@ -708,6 +714,7 @@ __device__ void widen_role(const Shared<D, true>& sh, const WeighParams& p) {
   static_assert(kRows * kUnroll == kUnitKeys, "a unit at a time");
   const int thread = threadIdx.x - 640;
   const int piece = thread % kLanes, row0 = thread / kLanes;
+  const uint32_t up = (127 + 120 + key_exp(p.scale)) * 0x00800080u;      // a code's exponent (see e4m3_even_raw), twice
   Ring<2> r;
   UnitReader<D, true> in(sh, p);
   while (const Unit* w = in.next()) {
@@ -735,8 +742,8 @@ __device__ void widen_role(const Shared<D, true>& sh, const WeighParams& p) {
       uint32_t y[8];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t even = paged::mul_bf16x2(paged::e4m3_even(v[j]), f);
-        const uint32_t odd = paged::mul_bf16x2(paged::e4m3_odd(v[j]), f);
+        const uint32_t even = paged::mul_bf16x2(paged::mul_bf16x2(paged::e4m3_even_raw(v[j]), up), f);
+        const uint32_t odd = paged::mul_bf16x2(paged::mul_bf16x2(paged::e4m3_odd_raw(v[j]), up), f);
         y[2 * j] = __byte_perm(even, odd, 0x5410);
         y[2 * j + 1] = __byte_perm(even, odd, 0x7632);
       }
@@ -849,6 +856,7 @@ __device__ void sum_role(const int m, const int j, const Shared<D, kFp8>& sh, co
   const int lane = threadIdx.x % 32, wq = threadIdx.x / 32 % 4;
   const int tt = kBN / p.group;
   const int in_unit = m * kBM + wq * 32 + lane;
+  const float scale = kFp8 ? p.scale * __uint_as_float((uint32_t)(127 - key_exp(p.scale)) << 23) : p.scale;
   const uint32_t tm0 = tmem + (uint32_t(wq * 32) << 16) + m * 256 + j * 64;
   uint32_t tile = 0;             // numbered through
   uint32_t phase = 0;            // bit i: of score buffer i
@@ -889,10 +897,10 @@ __device__ void sum_role(const int m, const int j, const Shared<D, kFp8>& sh, co
           for (int c = 0; c < 64; c += 2 * kCols) {
             scores_here(xa);
             load_scores(tm + c + kCols, xb);
-            add_weights<false>(xa, nlse + c, p.scale, 0, 0, sum2);
+            add_weights<false>(xa, nlse + c, scale, 0, 0, sum2);
             scores_here(xb);
             if (c + 2 * kCols < 64) load_scores(tm + c + 2 * kCols, xa); else release();
-            add_weights<false>(xb, nlse + c + kCols, p.scale, 0, 0, sum2);
+            add_weights<false>(xb, nlse + c + kCols, scale, 0, 0, sum2);
           }
         } else if (hi <= 0) {
           release();
@@ -902,9 +910,9 @@ __device__ void sum_role(const int m, const int j, const Shared<D, kFp8>& sh, co
           for (int c = 0; c < 64; c += kCols) {
             scores_here(xa);
             if (seen && c + kCols <= hi)
-              add_weights<false>(xa, nlse + c, p.scale, 0, 0, sum2);
+              add_weights<false>(xa, nlse + c, scale, 0, 0, sum2);
             else
-              add_weights<true>(xa, nlse + c, p.scale, lo - c, hi - c, sum2);
+              add_weights<true>(xa, nlse + c, scale, lo - c, hi - c, sum2);
             if (c + kCols < min(hi, 64)) {
               load_scores(tm + c + kCols, xa);
             } else {

@@ -214,7 +214,11 @@ FA_API fa_status fa_fwd_paged_tree(const void* q, const void* k_pages, const voi
  *   scale        > 0, a normal FP32 number
  *   decay        >= 0, finite
  * Weights and sums are FP32.  Over E4M3 pages, with up to 32 rows of a sequence and
- * head, queries are FP16 as fa_fwd_paged() has them; else keys are BF16, exactly.  A
+ * head, queries are FP16 as fa_fwd_paged() has them; else keys are BF16, exactly (with a
+ * scale below 2^-110 some are off, by what moves no score by 2^-100).  A score may
+ * overflow on its way where its size is above 2^18 (over BF16 pages: where the product of
+ * query and key does), or, over E4M3 pages with up to 32 rows, where `scale` times a query's
+ * largest element is above 2^100.  A
  * token in a bad page gets no sum.  What is not finite in a key reaches that key's own
  * sum alone.  Every token's slot is read and written, so the
  * sequences with new tokens must not share pages.  Results are bitwise repeatable.

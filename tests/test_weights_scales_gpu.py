@@ -60,3 +60,15 @@ def test_few_rows(fa, new, Hq, D, q_exp, k_exp):
 @pytest.mark.parametrize("new", [1, 4, 8])
 def test_few_rows_over_the_largest_keys(fa, new, D, scale, score):
     largest_keys(fa, D, new, scale, score)
+
+
+@pytest.mark.parametrize("q_exp,k_exp", FAR)
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_rows(fa, D, q_exp, k_exp):
+    weigh(fa, D, 50, 4, q_exp, k_exp)
+
+
+@pytest.mark.parametrize("D,scale,score", LARGEST)
+@pytest.mark.parametrize("new", [9, 50])
+def test_many_rows_over_the_largest_keys(fa, new, D, scale, score):
+    largest_keys(fa, D, new, scale, score)
