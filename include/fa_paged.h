@@ -208,7 +208,8 @@ FA_API fa_status fa_fwd_paged_tree(const void* q, const void* k_pages, const voi
  * decay 0, whatever it holds).
  *   q, causal, scale, block_table, seq_lens, cu_seqlens, max_q, and the pages
  *                as fa_fwd_paged() had them
- *   lse          as fa_fwd_paged() wrote it; a row with -inf gives no weight
+ *   lse          as fa_fwd_paged() wrote it; a row with -inf and finite queries gives
+ *                no weight
  *   sums         FP32 [num_pages, Hkv, page_size], laid out like the pages' scales;
  *                slots that are no token's stay as they are
  *   scale        > 0, a normal FP32 number
