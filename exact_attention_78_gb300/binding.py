@@ -615,7 +615,12 @@ def cache_weights(q, lse, k_pages, sums, block_table, seq_lens, causal=True, sca
     """Adds up the attention weights that the keys of the cache get from new tokens q,
     whose fwd_paged call gave `lse`: sums (float32 [num_pages, Hkv, page_size], a slot
     for each key) become decay * sums + the weights of the group's rows; those of the new
-    tokens start at zero.  q, lse and the other arguments as fwd_paged has them."""
+    tokens start at zero (a token that was new in no such call has what its slot held
+    before).  q, lse and the other arguments as fwd_paged has them; max_q chooses the
+    kernel here too, for all sequences of the call.  Not with a tree's q and lse as
+    they are, whose rows saw other keys than the causal mask gives: after cache_keep has
+    moved the accepted drafts together, with their rows of q and lse, packed, as new
+    tokens of sequences past + counts long."""
     lib = load_library()
     B, device = block_table.shape[0], q.device
     Sn = _new_tokens("q", q, B, cu_seqlens)

@@ -26,7 +26,7 @@ FA_DEV size_t lse_at(const WeighParams& p, int b, int q0, int head, int tok) {
   return p.s.cu ? (size_t)head * p.s.Sn + q0 + tok : ((size_t)b * p.Hq + head) * p.s.Sn + tok;
 }
 // A row that saw no key has an LSE of -inf, and gives no key a weight.  (With finite
-// queries: a score of NaN or infinity stays NaN.  fwd_paged gives no such row; a look at
+// queries: a score of NaN or infinity stays NaN.  fwd_paged gives no such row that sees a key; a look at
 // each row's LSE beside its score took 3% (2048 tokens over 32,768 keys) to 12% more time.)
 FA_DEV float lse_of(float x) { return x == -INFINITY ? INFINITY : x; }
 

@@ -13,7 +13,7 @@
  * Speculative decoding: the new tokens are a tree of drafts, whose masks and
  * depths fa_tree_mask() makes; fa_fwd_paged_tree() attends with them, and
  * fa_cache_keep() moves the accepted ones together.  Eviction: after an attention
- * call, fa_cache_weights() adds the weights that each key got to its sum,
+ * call (after a tree's, once the accepted tokens lie together), fa_cache_weights() adds the weights that each key got to its sum,
  * fa_cache_select() chooses by the sums which tokens each head keeps, and
  * fa_cache_keep() moves those together.
  *
@@ -205,11 +205,17 @@ FA_API fa_status fa_fwd_paged_tree(const void* q, const void* k_pages, const voi
  *   sums[t] = decay * sums[t] + sum over rows r that see t of exp(scale * q_r k_t - lse_r)
  * where the rows are the new tokens' query heads of the group, a token's slot in `sums`
  * is that of its key, and a new token's sum starts at zero (so does every sum with
- * decay 0, whatever it holds).
+ * decay 0, whatever it holds).  Only a call in which a token is new starts its sum; a
+ * token without one has the sum that its slot held before.
+ *   Not for a tree of drafts as new tokens: this call knows no tree's mask, and with
+ * another one the tree's LSE belongs to other keys.  Once fa_cache_keep() has moved the
+ * accepted drafts together, what each saw is what the causal mask gives: call this with
+ * their rows of the tree's q and LSE, packed, as the new tokens of sequences
+ * start[b] + counts[b] long.
  *   q, causal, scale, block_table, seq_lens, cu_seqlens, max_q, and the pages
  *                as fa_fwd_paged() had them
- *   lse          as fa_fwd_paged() wrote it; a row with -inf and finite queries gives
- *                no weight
+ *   lse          as fa_fwd_paged() wrote it for the same keys; a row with -inf and
+ *                finite queries gives no weight
  *   sums         FP32 [num_pages, Hkv, page_size], laid out like the pages' scales;
  *                slots that are no token's stay as they are
  *   scale        > 0, a normal FP32 number
@@ -219,10 +225,10 @@ FA_API fa_status fa_fwd_paged_tree(const void* q, const void* k_pages, const voi
  * scale below 2^-110 some are off, by what moves no score by 2^-100).  A score may
  * overflow on its way where its size is above 2^18 (over BF16 pages: where the product of
  * query and key does), or, over E4M3 pages with up to 32 rows, where `scale` times a query's
- * largest element is above 2^100.  A
- * token in a bad page gets no sum.  What is not finite in a key reaches that key's own
- * sum alone.  Every token's slot is read and written, so the
- * sequences with new tokens must not share pages.  Results are bitwise repeatable.
+ * largest element is above 2^100.  A token in a bad page gets no sum.  What is not
+ * finite in a key reaches that key's own sum alone.  Every token's slot is read and
+ * written, so the sequences with new tokens must not share pages.  Results are bitwise
+ * repeatable.
  */
 FA_API fa_status fa_cache_weights(const void* q, const float* lse, const void* k_pages, const void* k_scale,
                                   float* sums, int B, int Hq, int Hkv, int Sn, int D, int num_pages, int page_size,
