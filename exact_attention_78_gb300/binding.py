@@ -66,6 +66,7 @@ _SIGNATURES = {
     "fa_diag_exp2": (_i, [_vp, _vp, _vp, ctypes.c_longlong, _vp]),
     "fa_diag_wait_timeout": (_i, [ctypes.c_ulonglong, _vp]),
     "fa_diag_fwd_paged": (_i, [_vp] * 7 + [_i] * 9 + [_f] + [_vp] * 3 + [_i, _vp, _sz, ctypes.c_ulonglong, _vp]),
+    "fa_diag_cache_weights": (_i, [_vp] * 5 + [_i] * 9 + [_f] * 2 + [_vp] * 3 + [_i, ctypes.c_ulonglong, _i, _vp]),
 }
 
 

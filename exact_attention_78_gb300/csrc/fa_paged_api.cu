@@ -124,6 +124,44 @@ fa_status fwd_paged(const void* q, const void* k_pages, const void* v_pages, con
   }
 }
 
+fa_status cache_weights(const void* q, const float* lse, const void* k_pages, const void* k_scale, float* sums, int B,
+                        int Hq, int Hkv, int Sn, int D, int num_pages, int page_size, int max_pages, int causal,
+                        float scale, float decay, const int* block_table, const int* seq_lens, const int* cu_seqlens,
+                        int max_q, unsigned long long wait_limit_ns, int held, fa_stream_t stream) {
+  try {
+    WeighParams p{};
+    if (!q || !lse || !sums || !seq_lens || !aligned(q, 16) || !aligned(lse, 16) || !aligned(sums, 16))
+      return FA_ERR_INVALID_ARG;
+    if (causal != 0 && causal != 1) return FA_ERR_INVALID_ARG;
+    if (!(scale > 0.0f) || !std::isnormal(scale) || !(decay >= 0.0f) || !std::isfinite(decay)) return FA_ERR_INVALID_ARG;
+    fa_status st;
+    if (!attn_shape_ok(B, Hq, Hkv, Sn, D, cu_seqlens != nullptr, max_q, &st)) return st;
+    // (no values here: the keys stand in for their check)
+    st = check_cache(k_pages, k_pages, k_scale, k_scale, B, Hkv, Sn, D, num_pages, page_size, max_pages, block_table,
+                     seq_lens, cu_seqlens, &p.s);
+    if (st != FA_OK) return st;
+    int num_sms = 0;
+    if ((st = device_info(&num_sms)) != FA_OK) return st;
+    p.q = q;
+    p.lse = lse;
+    p.k_pages = k_pages;
+    p.k_scale = static_cast<const uint8_t*>(k_scale);
+    p.sums = sums;
+    p.Hq = Hq;
+    p.group = Hq / Hkv;
+    p.D = D;
+    p.causal = causal;
+    p.max_q = cu_seqlens ? max_q : Sn;
+    p.scale = scale;
+    p.decay = decay;
+    p.wait_limit_ns = wait_limit_ns;
+    p.held = held;
+    return launch_cache_weights(p, num_sms, reinterpret_cast<cudaStream_t>(stream));
+  } catch (...) {
+    return FA_ERR_CUDA;
+  }
+}
+
 }  // namespace
 }  // namespace fa
 
@@ -299,37 +337,8 @@ fa_status fa_cache_weights(const void* q, const float* lse, const void* k_pages,
                            int Hq, int Hkv, int Sn, int D, int num_pages, int page_size, int max_pages, int causal,
                            float scale, float decay, const int* block_table, const int* seq_lens, const int* cu_seqlens,
                            int max_q, fa_stream_t stream) {
-  try {
-    WeighParams p{};
-    if (!q || !lse || !sums || !seq_lens || !aligned(q, 16) || !aligned(lse, 16) || !aligned(sums, 16))
-      return FA_ERR_INVALID_ARG;
-    if (causal != 0 && causal != 1) return FA_ERR_INVALID_ARG;
-    if (!(scale > 0.0f) || !std::isnormal(scale) || !(decay >= 0.0f) || !std::isfinite(decay)) return FA_ERR_INVALID_ARG;
-    fa_status st;
-    if (!attn_shape_ok(B, Hq, Hkv, Sn, D, cu_seqlens != nullptr, max_q, &st)) return st;
-    // (no values here: the keys stand in for their check)
-    st = check_cache(k_pages, k_pages, k_scale, k_scale, B, Hkv, Sn, D, num_pages, page_size, max_pages, block_table,
-                     seq_lens, cu_seqlens, &p.s);
-    if (st != FA_OK) return st;
-    int num_sms = 0;
-    if ((st = device_info(&num_sms)) != FA_OK) return st;
-    p.q = q;
-    p.lse = lse;
-    p.k_pages = k_pages;
-    p.k_scale = static_cast<const uint8_t*>(k_scale);
-    p.sums = sums;
-    p.Hq = Hq;
-    p.group = Hq / Hkv;
-    p.D = D;
-    p.causal = causal;
-    p.max_q = cu_seqlens ? max_q : Sn;
-    p.scale = scale;
-    p.decay = decay;
-    p.wait_limit_ns = kDefaultWaitLimitNs;
-    return launch_cache_weights(p, num_sms, reinterpret_cast<cudaStream_t>(stream));
-  } catch (...) {
-    return FA_ERR_CUDA;
-  }
+  return cache_weights(q, lse, k_pages, k_scale, sums, B, Hq, Hkv, Sn, D, num_pages, page_size, max_pages, causal, scale,
+                       decay, block_table, seq_lens, cu_seqlens, max_q, kDefaultWaitLimitNs, -1, stream);
 }
 
 fa_status fa_cache_select(const float* sums, int* index, int* kept, int B, int Hkv, int num_pages, int page_size,
@@ -400,6 +409,17 @@ fa_status fa_diag_fwd_paged(const void* q, const void* k_pages, const void* v_pa
   return fwd_paged(q, k_pages, v_pages, k_scale, v_scale, o, lse, B, Hq, Hkv, Sn, D, num_pages, page_size, max_pages,
                    causal, nullptr, scale, block_table, seq_lens, cu_seqlens, max_q, workspace, workspace_bytes,
                    wait_limit_ns, stream);
+}
+
+fa_status fa_diag_cache_weights(const void* q, const float* lse, const void* k_pages, const void* k_scale, float* sums,
+                                int B, int Hq, int Hkv, int Sn, int D, int num_pages, int page_size, int max_pages,
+                                int causal, float scale, float decay, const int* block_table, const int* seq_lens,
+                                const int* cu_seqlens, int max_q, unsigned long long wait_limit_ns, int held,
+                                fa_stream_t stream) {
+  if (wait_limit_ns == 0 || wait_limit_ns > 10000000000ull) return FA_ERR_INVALID_ARG;
+  if (held < -1 || held >= weigh_barriers(D)) return FA_ERR_INVALID_ARG;
+  return cache_weights(q, lse, k_pages, k_scale, sums, B, Hq, Hkv, Sn, D, num_pages, page_size, max_pages, causal, scale,
+                       decay, block_table, seq_lens, cu_seqlens, max_q, wait_limit_ns, held, stream);
 }
 
 }  // extern "C"

@@ -30,6 +30,11 @@ FA_DEV size_t lse_at(const WeighParams& p, int b, int q0, int head, int tok) {
 // each row's LSE beside its score took 3% (2048 tokens over 32,768 keys) to 12% more time.)
 FA_DEV float lse_of(float x) { return x == -INFINITY ? INFINITY : x; }
 
+// The barrier's phase waits for bytes that nobody brings (fa_diag_cache_weights).
+FA_DEV void hold(uint32_t bar) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], 16;" ::"r"(bar) : "memory");
+}
+
 // The slot of the key's sum; -1 in a bad page.
 FA_DEV long long slot_of(const WeighParams& p, int b, int head, int key) {
   const int page = p.s.block_table[(size_t)b * p.s.max_pages + (key >> p.s.page_shift)];
@@ -150,6 +155,7 @@ __global__ void __launch_bounds__(StepLayout<D, kFp8, kTiles>::kThreads, 1) step
   const int c = lane % 4, g = lane / 4;
   const uint32_t bars = smem_u32(ring_raw) + Lay::kBars + warp * Lay::kDepth * 8, abort = smem_u32(ring_raw) + Lay::kMisc;
   if (lane < Lay::kDepth) mbar_init(bars + 8 * lane, 1);
+  if (lane < Lay::kDepth && lane == p.held) hold(bars + 8 * lane);
   if (threadIdx.x == 0) st_shared(abort, 0);
   fence_barrier_init();
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -452,7 +458,8 @@ struct Layout {
   static constexpr int kPre = kUnitRing + kUnits * (int)sizeof(Unit);      // prefix of units, [B + 1], 64 bits
   static constexpr int kSums = kPre + (kMaxPackedSeqs + 1) * 8;
   static constexpr int kBars = kSums + 32 * 16;
-  static constexpr int kNumBars = 4 + 2 * kQStages + 8 + 2 + 4 * kUnits;
+  static constexpr int kTileBars = 4 + 2 * kQStages + 8 + 2;      // somebody waits for each with a limit
+  static constexpr int kNumBars = kTileBars + 4 * kUnits;
   static constexpr int kMisc = kBars + kNumBars * 8;
   static constexpr int kBytes = kMisc + 64 + kSmemAlignSlack;
   static_assert(kBytes <= 232448, "dynamic shared memory above the 227 KB per-CTA limit");
@@ -971,6 +978,7 @@ __global__ void __launch_bounds__(Layout<D, kFp8>::kThreads, 1)
       mbar_init(sh.q_empty(i), 1);
     }
     for (int i = 0; i < 2; ++i) mbar_init(sh.lse_empty(i), 16);
+    if (p.held >= 0) hold(sh.bar(p.held));
     for (int i = 0; i < kUnits; ++i) {
       mbar_init(sh.unit_full(i), 1);
       mbar_init(sh.unit_empty(i), L::kReaders);
@@ -1064,6 +1072,10 @@ fa_status launch_cache_weights(const WeighParams& p, int num_sms, cudaStream_t s
   if (p.D == 128)
     return p.k_scale ? weigh::launch<128, true>(p, num_sms, stream) : weigh::launch<128, false>(p, num_sms, stream);
   return p.k_scale ? weigh::launch<64, true>(p, num_sms, stream) : weigh::launch<64, false>(p, num_sms, stream);
+}
+
+int weigh_barriers(int D) {
+  return D == 128 ? weigh::Layout<128, false>::kTileBars : weigh::Layout<64, false>::kTileBars;
 }
 
 fa_status weigh_take_device_error() {

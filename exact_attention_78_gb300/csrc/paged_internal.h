@@ -72,6 +72,7 @@ struct WeighParams {
   int causal;
   int max_q;
   float scale, decay;
+  int held;                 // a barrier that never completes (fa_diag_cache_weights), or -1
   unsigned long long wait_limit_ns;
 };
 
@@ -167,6 +168,8 @@ fa_status launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, int sm
 }
 
 fa_status launch_cache_weights(const WeighParams& p, int num_sms, cudaStream_t stream);
+// How many of its barriers WeighParams::held may name.
+int weigh_barriers(int D);
 fa_status launch_cache_select(const SelectParams& p, int num_sms, cudaStream_t stream);
 fa_status launch_cache_keep(const KeepParams& p, int num_sms, cudaStream_t stream);
 fa_status launch_tree_mask(const TreeParams& p, cudaStream_t stream);

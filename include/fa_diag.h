@@ -163,6 +163,19 @@ FA_API fa_status fa_diag_fwd_paged(const void* q, const void* k_pages, const voi
                                    void* workspace, size_t workspace_bytes, unsigned long long wait_limit_ns,
                                    fa_stream_t stream);
 
+/*
+ * fa_cache_weights() (fa_paged.h) with a limit of its kernels' waits, as above.
+ * held: -1, or the number of one of a thread block's barriers (with up to 32 rows,
+ * of each warp's), which then waits for bytes that nobody brings: whoever waits
+ * for it gives up after wait_limit_ns, and the next fa_get_device_error() returns
+ * FA_ERR_TIMEOUT.  Below 18 (D = 128) or 22 (D = 64).
+ */
+FA_API fa_status fa_diag_cache_weights(const void* q, const float* lse, const void* k_pages, const void* k_scale,
+                                       float* sums, int B, int Hq, int Hkv, int Sn, int D, int num_pages,
+                                       int page_size, int max_pages, int causal, float scale, float decay,
+                                       const int* block_table, const int* seq_lens, const int* cu_seqlens, int max_q,
+                                       unsigned long long wait_limit_ns, int held, fa_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
