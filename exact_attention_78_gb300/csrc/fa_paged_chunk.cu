@@ -64,7 +64,10 @@ constexpr int kUnitCost = 4 * kBN;
 // What a block takes on the line, of a tree's unit whose second tile has no tokens, which
 // is common with trees: a block of one tile takes 15% less time than one of two, whose
 // tiles wait for each other's products.  (48 ragged trees up to 61 tokens over up to 8192
-// E4M3 keys: as much as others 212 us, 116 206, 108 201, 96 210.)
+// E4M3 keys: as much as others 212 us, 116 206, 108 201, 96 210.  As much as others / 108:
+// the same over BF16 pages 184 / 178, at D = 64 E4M3 177 / 167, BF16 166 / 155; 48 up to 40
+// over up to 2000, D = 128, E4M3 89 / 84, BF16 73 / 69; 16 up to 30 over up to 16,000 123 / 124
+// and 109 / 112, D = 64 108 / 106 and 97 / 98.)
 constexpr int kSingleBlock = 108;
 
 enum Site {
